@@ -47,7 +47,10 @@ FFTMV_SCRATCH_BYTES = 128 << 20
 EXPORTS = ("fftmv_setup", "fftmv_apply", "fftmv_apply_adjoint", "fftmv_apply_scratch", "fftmv_destroy",
            "fftmv_status_string",
            "fftmv_query", "fftmv_set_mask", "fftmv_run_stages", "fftmv_buffer", "fftmv_model_defaults",
-           "fftmv_predict", "fftmv_pareto_front", "fftmv_select_precision", "fftmv_condition", "fftmv_version")
+           "fftmv_predict", "fftmv_pareto_front", "fftmv_select_precision", "fftmv_condition", "fftmv_version",
+           "fftmv_recurrence_workspace", "fftmv_recurrence_forward", "fftmv_recurrence_backward",
+           "fftmv_recurrence_step", "fftmv_group_norm_workspace", "fftmv_group_norm_forward",
+           "fftmv_group_norm_backward")
 
 
 def FFTMV_FP32(direction: int, stage: int) -> int:
@@ -365,3 +368,8 @@ def _hip_memcpy_d2d(dst: int, src: int, nbytes: int) -> None:
     rc = _hip.hipMemcpy(dst, src, nbytes, 3)  # hipMemcpyDeviceToDevice
     if rc != 0:
         raise RuntimeError(f"hipMemcpy failed with {rc}")
+
+
+# the sequence operators on torch tensors
+from .sequence import (group_norm, group_norm_backward, recurrence, recurrence_backward,  # noqa: E402,F401
+                       recurrence_step)

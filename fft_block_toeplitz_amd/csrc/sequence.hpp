@@ -1,0 +1,114 @@
+// Interface between the C entry points of the sequence operators
+// (sequence.cpp) and their kernels (recurrence*.hip, group_norm*.hip), and
+// the element arithmetic that the kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fftmv.h"
+
+namespace fftmv {
+
+hipError_t launch_recurrence_forward(const fftmv_recurrence_t &r, hipStream_t s);
+hipError_t launch_recurrence_backward(const fftmv_recurrence_t &r, hipStream_t s);
+hipError_t launch_recurrence_step(const fftmv_recurrence_step_t &r, hipStream_t s);
+hipError_t launch_group_norm_forward(const fftmv_group_norm_t &g, hipStream_t s);
+hipError_t launch_group_norm_backward(const fftmv_group_norm_t &g, hipStream_t s);
+
+using bf16 = __bf16;
+using f16 = _Float16;
+
+// ------------------------------------------------ terms of the recurrence
+// a = the decay, rest = 1 - a, slope = da/dg, each to a few ulp of FP32.
+// sigmoid: with t = exp(-|g|) <= 1 nothing overflows, 1 - a comes from t
+// without cancellation (a gate of 10 leaves 1 - a = 4.5e-5, which 1.0f - a
+// would hold to 3 digits only), and a NaN stays one.
+struct Terms {
+  float a, rest, slope;
+};
+
+// exp(v). FP32 elements take the library's (1 ulp); for 16-bit ones, whose
+// v is known to 2^-11 of itself at best, the hardware's exp2 of the once
+// rounded v log2(e), off by |v| 2^-24 relative, costs a quarter as much.
+template <typename T>
+__device__ __forceinline__ float exp_of(float v) {
+  if constexpr (sizeof(T) == 4) return expf(v);
+  return __builtin_amdgcn_exp2f(1.44269504088896341f * v);
+}
+
+template <typename T, int DECAY>
+__device__ __forceinline__ Terms decay_terms(float g) {
+  Terms r;
+  if constexpr (DECAY == FFTMV_DECAY_SIGMOID) {
+    const float t = exp_of<T>(-fabsf(g));
+    const float big = __builtin_amdgcn_rcpf(1.0f + t), small = t * big;
+    r.a = g >= 0.0f ? big : small;
+    r.rest = g >= 0.0f ? small : big;
+    r.slope = big * small;
+  } else if constexpr (DECAY == FFTMV_DECAY_EXP) {
+    r.a = exp_of<T>(g);
+    r.rest = -expm1f(g);
+    r.slope = r.a;
+  } else {
+    r.a = g;
+    r.rest = 1.0f - g;
+    r.slope = 1.0f;
+  }
+  return r;
+}
+
+// u, the drive of one step.
+template <int DRIVE>
+__device__ __forceinline__ float drive_of(const Terms &t, float x) {
+  return DRIVE == FFTMV_DRIVE_COMPLEMENT ? t.rest * x : x;
+}
+
+// ------------------------------------------------------------- activations
+// act(z) and act'(z).
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+  if constexpr (ACT == FFTMV_ACT_SILU) {
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+  } else if constexpr (ACT == FFTMV_ACT_GELU) {
+    return 0.5f * z * erfcf(-0.70710678118654752f * z);
+  } else {
+    return z;
+  }
+}
+template <int ACT>
+__device__ __forceinline__ float activate_slope(float z) {
+  if constexpr (ACT == FFTMV_ACT_SILU) {
+    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+    return p * (1.0f + z * (1.0f - p));
+  } else if constexpr (ACT == FFTMV_ACT_GELU) {
+    return 0.5f * erfcf(-0.70710678118654752f * z) +
+           0.39894228040143268f * z * __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
+  } else {
+    return 1.0f;
+  }
+}
+
+// ------------------------------------------------------------ type dispatch
+template <typename F>
+hipError_t by_dtype(int dtype, F f) {
+  if (dtype == FFTMV_BF16) return f(bf16{});
+  if (dtype == FFTMV_F16) return f(f16{});
+  return f(float{});
+}
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+template <typename F>
+hipError_t by_three(int v, F f) {
+  if (v == 0) return f(Const<0>{});
+  if (v == 1) return f(Const<1>{});
+  return f(Const<2>{});
+}
+template <typename F>
+hipError_t by_two(int v, F f) {
+  return v == 0 ? f(Const<0>{}) : f(Const<1>{});
+}
+
+}  // namespace fftmv

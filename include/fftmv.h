@@ -288,6 +288,184 @@ FFTMV_API int fftmv_select_precision(int64_t Nm, int64_t Nd, int64_t Nt, int dir
 FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, double *sigma_max, double *sigma_min,
                               hipStream_t stream);
 
+/* ------------------------------------------------- sequence operators
+ * Causal operators along time with learned, time-varying decays, for models
+ * that are trained on or streamed beside F: a gated linear recurrence and
+ * the group normalisation with activation that follows it. Fields are
+ * channels-last like m and d above: the channels of one time step are
+ * contiguous (channel stride 1); the strides of steps and sequences are
+ * arguments, in elements. Elements are FP32, BF16 or FP16; states,
+ * statistics, parameters and every sum are FP32.
+ *
+ * Structures are filled by the caller; unused pointers are NULL. Unless it
+ * says otherwise a call allocates nothing, never synchronises, runs on
+ * `stream`, and gives bitwise the same results for the same inputs. Outputs
+ * must not overlap inputs. Element pointers need their type's alignment;
+ * rows whose starts are multiples of 16 bytes (pointers and strides) and
+ * whose channel count is a multiple of 16 bytes' worth take wider loads. */
+#define FFTMV_F32 0
+#define FFTMV_BF16 1
+#define FFTMV_F16 2
+
+#define FFTMV_DECAY_SIGMOID 0 /* a = 1 / (1 + exp(-g)) */
+#define FFTMV_DECAY_EXP 1     /* a = exp(g)            */
+#define FFTMV_DECAY_VALUE 2   /* a = g                 */
+
+#define FFTMV_DRIVE_COMPLEMENT 0 /* u = (1 - a) x */
+#define FFTMV_DRIVE_PLAIN 1      /* u = x         */
+
+/* Gated linear recurrence: for every sequence and channel
+ *
+ *     h_t = a_t h_{t-1} + u_t,   t = 0..len-1,   h_{-1} = h0
+ *
+ * with the decay a_t = a(gate_t) and the drive u_t = u(a_t, x_t) above.
+ * Three forms:
+ *   batch    `batch` sequences of `steps` steps each; row (b, t) of a field
+ *            starts at b * batch_stride + t * step_stride
+ *   padded   the same with lengths[b] steps held in sequence b (values are
+ *            clamped to 0..steps); the others are not read, and are written
+ *            as zeros
+ *   packed   one axis of `steps` steps in all, sequence b being the steps
+ *            offsets[b]..offsets[b+1]-1 (ascending; equal neighbours: an
+ *            empty sequence); steps before offsets[0] or from
+ *            offsets[batch] on belong to none, are not read, and are
+ *            written as zeros; batch strides are ignored
+ * lengths / offsets are device arrays of int32. Neither their contents nor
+ * anything else on the device is read by the host.
+ *
+ * Forward writes h (rounded once to the element type), and where not NULL
+ *   h_last   [batch][channels] the state after each sequence's last step
+ *            (h0 for an empty one)
+ *   carries  [chunks][channels] the state that enters each run of
+ *            FFTMV_RECURRENCE_CHUNK steps, rows counted over all sequences
+ *            (chunks = ceil(rows / FFTMV_RECURRENCE_CHUNK), rows = batch *
+ *            steps, or steps when packed): what the backward pass starts from
+ *
+ * Backward takes x, gate, h0 and carries as the forward had and left them,
+ * dh (the gradient of h) and, where not NULL, dh_last (that of h_last), and
+ * writes with r_t = dh_t + a_{t+1} r_{t+1} (r_{len} a_{len} := dh_last)
+ *   dx_t     r_t (1 - a_t) or r_t
+ *   dgate_t  r_t (h_{t-1} - x_t) da/dg or r_t h_{t-1} da/dg
+ *   dh0      a_0 r_0 (dh_last for an empty sequence); may be NULL
+ * with h recomputed in FP32 from carries, not read back rounded.
+ *
+ * workspace: fftmv_recurrence_workspace bytes, 8-byte aligned, zero before
+ * the first call; each call leaves it zero again. Calls that share one must
+ * be ordered. h0 NULL stands for zeros. A state that is not finite stays
+ * not finite (infinity or NaN) until its sequence ends; it reaches no other
+ * sequence or channel.
+ * Errors: FFTMV_ERR_INVALID_ARG (a null or misaligned pointer, a size < 1
+ * -- steps may be 0 --, an unknown type/decay/drive, both lengths and
+ * offsets, a workspace that is too small); FFTMV_ERR_UNSUPPORTED_SIZE
+ * (more than 2^31 - 1 rows or channels, or a grid above 2^32 work-items). */
+#define FFTMV_RECURRENCE_CHUNK 256
+typedef struct fftmv_recurrence_s {
+  int64_t batch, steps, channels;
+  int32_t dtype, decay, drive, reserved; /* reserved: 0 */
+  const int32_t *lengths, *offsets;
+  const void *x;
+  int64_t x_batch, x_step;
+  const void *gate;
+  int64_t gate_batch, gate_step;
+  const float *h0;
+  float *carries;
+  void *workspace;
+  size_t workspace_bytes;
+  /* forward */
+  void *h;
+  int64_t h_batch, h_step;
+  float *h_last;
+  /* backward */
+  const void *dh;
+  int64_t dh_batch, dh_step;
+  const float *dh_last;
+  void *dx;
+  int64_t dx_batch, dx_step;
+  void *dgate;
+  int64_t dgate_batch, dgate_step;
+  float *dh0;
+} fftmv_recurrence_t;
+
+/* Workspace bytes of a forward or backward call over this many rows. */
+FFTMV_API int fftmv_recurrence_workspace(int64_t rows, int64_t channels, size_t *bytes);
+FFTMV_API int fftmv_recurrence_forward(const fftmv_recurrence_t *r, hipStream_t stream);
+FFTMV_API int fftmv_recurrence_backward(const fftmv_recurrence_t *r, hipStream_t stream);
+
+/* One time step of `batch` streams against a cache of states, in place:
+ * stream b takes row slots[b] of state ([places][channels] FP32, rows
+ * state_step apart) from h_{t-1} to h_t and gets h_t, rounded, in row b of h.
+ * A slot outside 0..places-1 marks an idle stream: its row of h is zero and
+ * no state changes. slots NULL: stream b uses row b (batch <= places). Two
+ * streams of one call must not name the same slot. */
+typedef struct fftmv_recurrence_step_s {
+  int64_t batch, channels, places;
+  int32_t dtype, decay, drive, reserved;
+  const void *x;
+  int64_t x_step;
+  const void *gate;
+  int64_t gate_step;
+  float *state;
+  int64_t state_step;
+  const int32_t *slots;
+  void *h;
+  int64_t h_step;
+} fftmv_recurrence_step_t;
+FFTMV_API int fftmv_recurrence_step(const fftmv_recurrence_step_t *r, hipStream_t stream);
+
+/* Group normalisation with an activation over channels-last fields: sample
+ * n holds `rows` rows (time steps, pixels; 1: single tokens) of `channels`
+ * channels in `groups` groups of channels/groups neighbours, and
+ *
+ *     xhat = (x - mean) rstd,   rstd = 1 / sqrt(var + eps)
+ *     y    = act(xhat weight + bias)
+ *
+ * with mean and (biased) variance over the sample's rows and one group.
+ * weight, bias: [channels] FP32, NULL for ones / zeros. lengths (device
+ * int32, clamped to 0..rows): sample n holds lengths[n] rows only; the
+ * others enter no sum, are not read, and are written as zeros; a sample
+ * that holds none has mean 0 and rstd 0.
+ *
+ * Forward writes y and, where not NULL, stats [samples][groups][2] (mean,
+ * rstd). Backward takes x, stats and the parameters as the forward had and
+ * left them and dy, and with z = xhat weight + bias, dz = dy act'(z) writes
+ *   dx       rstd (dz weight - mean(dz weight) - xhat mean(dz weight xhat))
+ *   dweight  [channels] FP32, sum of dz xhat over samples and rows (or NULL)
+ *   dbias    [channels] FP32, sum of dz (or NULL)
+ * workspace: fftmv_group_norm_workspace bytes, 16-byte aligned, any contents.
+ * Activations: none, SiLU z / (1 + exp(-z)), GELU z Phi(z) (exact, by erf).
+ * Errors as above, also when groups does not divide channels or eps is
+ * negative or NaN. */
+#define FFTMV_ACT_NONE 0
+#define FFTMV_ACT_SILU 1
+#define FFTMV_ACT_GELU 2
+typedef struct fftmv_group_norm_s {
+  int64_t samples, rows, channels, groups;
+  int32_t dtype, activation;
+  float eps;
+  int32_t reserved; /* 0 */
+  const int32_t *lengths;
+  const void *x;
+  int64_t x_sample, x_row;
+  const float *weight, *bias;
+  float *stats;
+  void *workspace;
+  size_t workspace_bytes;
+  /* forward */
+  void *y;
+  int64_t y_sample, y_row;
+  /* backward */
+  const void *dy;
+  int64_t dy_sample, dy_row;
+  void *dx;
+  int64_t dx_sample, dx_row;
+  float *dweight, *dbias;
+} fftmv_group_norm_t;
+
+FFTMV_API int fftmv_group_norm_workspace(int64_t samples, int64_t rows, int64_t channels, int64_t groups,
+                                         size_t *bytes);
+FFTMV_API int fftmv_group_norm_forward(const fftmv_group_norm_t *g, hipStream_t stream);
+FFTMV_API int fftmv_group_norm_backward(const fftmv_group_norm_t *g, hipStream_t stream);
+
 /* Library version, (major << 16) | (minor << 8) | patch. */
 FFTMV_API int fftmv_version(void);
 
