@@ -3,6 +3,7 @@
 #include "sequence.hpp"
 
 #include "internal.hpp"
+#include "recurrence.hpp"
 
 using namespace fftmv;
 
@@ -109,18 +110,24 @@ extern "C" {
 int fftmv_recurrence_workspace(int64_t rows, int64_t channels, size_t *bytes) {
   if (!bytes || rows < 0 || channels < 1) return FFTMV_ERR_INVALID_ARG;
   if (rows > INT32_MAX || channels > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
-  *bytes = 0;
+  *bytes = scan_workspace_bytes(rows, channels);
   return FFTMV_SUCCESS;
 }
 
 int fftmv_recurrence_forward(const fftmv_recurrence_t *r, hipStream_t stream) {
   const int st = check_recurrence(r, false);
-  return st != FFTMV_SUCCESS ? st : status_of(launch_recurrence_forward(*r, stream));
+  if (st != FFTMV_SUCCESS) return st;
+  return status_of(r->dtype == FFTMV_F32    ? launch_recurrence_forward_f32(*r, stream)
+                   : r->dtype == FFTMV_BF16 ? launch_recurrence_forward_bf16(*r, stream)
+                                            : launch_recurrence_forward_f16(*r, stream));
 }
 
 int fftmv_recurrence_backward(const fftmv_recurrence_t *r, hipStream_t stream) {
   const int st = check_recurrence(r, true);
-  return st != FFTMV_SUCCESS ? st : status_of(launch_recurrence_backward(*r, stream));
+  if (st != FFTMV_SUCCESS) return st;
+  return status_of(r->dtype == FFTMV_F32    ? launch_recurrence_backward_f32(*r, stream)
+                   : r->dtype == FFTMV_BF16 ? launch_recurrence_backward_bf16(*r, stream)
+                                            : launch_recurrence_backward_f16(*r, stream));
 }
 
 int fftmv_recurrence_step(const fftmv_recurrence_step_t *r, hipStream_t stream) {

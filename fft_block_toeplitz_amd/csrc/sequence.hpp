@@ -10,14 +10,58 @@
 
 namespace fftmv {
 
-hipError_t launch_recurrence_forward(const fftmv_recurrence_t &r, hipStream_t s);
-hipError_t launch_recurrence_backward(const fftmv_recurrence_t &r, hipStream_t s);
+// one translation unit per direction and element type
+hipError_t launch_recurrence_forward_f32(const fftmv_recurrence_t &r, hipStream_t s);
+hipError_t launch_recurrence_forward_bf16(const fftmv_recurrence_t &r, hipStream_t s);
+hipError_t launch_recurrence_forward_f16(const fftmv_recurrence_t &r, hipStream_t s);
+hipError_t launch_recurrence_backward_f32(const fftmv_recurrence_t &r, hipStream_t s);
+hipError_t launch_recurrence_backward_bf16(const fftmv_recurrence_t &r, hipStream_t s);
+hipError_t launch_recurrence_backward_f16(const fftmv_recurrence_t &r, hipStream_t s);
 hipError_t launch_recurrence_step(const fftmv_recurrence_step_t &r, hipStream_t s);
 hipError_t launch_group_norm_forward(const fftmv_group_norm_t &g, hipStream_t s);
 hipError_t launch_group_norm_backward(const fftmv_group_norm_t &g, hipStream_t s);
 
 using bf16 = __bf16;
 using f16 = _Float16;
+
+// --------------------------------------------------------- vectors of 16 bytes
+// VEC neighbouring channels of one row. A row starts at any element address;
+// gfx950 takes 16-byte global accesses at any alignment, so odd channel
+// counts and strides keep the wide loads.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <typename T, int VEC>
+struct Vec {
+  T v[VEC];
+  __device__ __forceinline__ float operator[](int e) const { return static_cast<float>(v[e]); }
+};
+
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);
+
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> load_vec(const T *p) {
+  if constexpr (VEC == kVec<T>) {
+    return __builtin_bit_cast(Vec<T, VEC>, *reinterpret_cast<const u32x4_any *>(p));
+  } else {
+    Vec<T, VEC> r;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) r.v[e] = p[e];
+    return r;
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
+  Vec<T, VEC> r;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) r.v[e] = static_cast<T>(f[e]);
+  if constexpr (VEC == kVec<T>) {
+    *reinterpret_cast<u32x4_any *>(p) = __builtin_bit_cast(u32x4_any, r);
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) p[e] = r.v[e];
+  }
+}
 
 // ------------------------------------------------ terms of the recurrence
 // a = the decay, rest = 1 - a, slope = da/dg, each to a few ulp of FP32.
