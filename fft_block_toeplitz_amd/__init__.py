@@ -48,7 +48,7 @@ EXPORTS = ("fftmv_setup", "fftmv_apply", "fftmv_apply_adjoint", "fftmv_apply_scr
            "fftmv_status_string",
            "fftmv_query", "fftmv_set_mask", "fftmv_run_stages", "fftmv_buffer", "fftmv_model_defaults",
            "fftmv_predict", "fftmv_pareto_front", "fftmv_select_precision", "fftmv_condition", "fftmv_version",
-           "fftmv_recurrence_workspace", "fftmv_recurrence_forward", "fftmv_recurrence_backward",
+           "fftmv_recurrence_sizes", "fftmv_recurrence_forward", "fftmv_recurrence_backward",
            "fftmv_recurrence_step", "fftmv_group_norm_workspace", "fftmv_group_norm_forward",
            "fftmv_group_norm_backward")
 

@@ -59,7 +59,7 @@ int check_recurrence(const fftmv_recurrence_t *r, bool backward) {
     if (!backward) {
       if (!field(r->h, es) || !strides_ok(B, r->h_batch, T, r->h_step, C)) return FFTMV_ERR_INVALID_ARG;
     } else {
-      if (!field(r->dh, es) || !field(r->dx, es) || !field(r->dgate, es) || !r->carries) return FFTMV_ERR_INVALID_ARG;
+      if (!field(r->dh, es) || !field(r->dx, es) || !field(r->dgate, es)) return FFTMV_ERR_INVALID_ARG;
       if (!strides_ok(B, r->dh_batch, T, r->dh_step, C) || !strides_ok(B, r->dx_batch, T, r->dx_step, C) ||
           !strides_ok(B, r->dgate_batch, T, r->dgate_step, C))
         return FFTMV_ERR_INVALID_ARG;
@@ -68,8 +68,10 @@ int check_recurrence(const fftmv_recurrence_t *r, bool backward) {
   if (!floats(r->h0) || !floats(r->h_last) || !floats(r->carries) || !floats(r->dh_last) || !floats(r->dh0))
     return FFTMV_ERR_INVALID_ARG;
   size_t need = 0;
-  const int st = fftmv_recurrence_workspace(rows, C, &need);
+  int64_t carries = 0;
+  const int st = fftmv_recurrence_sizes(r->batch, T, C, r->offsets != nullptr, &carries, &need);
   if (st != FFTMV_SUCCESS) return st;
+  if (backward && carries && !r->carries) return FFTMV_ERR_INVALID_ARG;
   if (need && (!r->workspace || !aligned(r->workspace, 8) || r->workspace_bytes < need)) return FFTMV_ERR_INVALID_ARG;
   return FFTMV_SUCCESS;
 }
@@ -107,10 +109,12 @@ int check_group_norm(const fftmv_group_norm_t *g, bool backward) {
 
 extern "C" {
 
-int fftmv_recurrence_workspace(int64_t rows, int64_t channels, size_t *bytes) {
-  if (!bytes || rows < 0 || channels < 1) return FFTMV_ERR_INVALID_ARG;
-  if (rows > INT32_MAX || channels > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
-  *bytes = scan_workspace_bytes(rows, channels);
+int fftmv_recurrence_sizes(int64_t batch, int64_t steps, int64_t channels, int packed, int64_t *carries,
+                           size_t *bytes) {
+  if (batch < 1 || steps < 0 || channels < 1) return FFTMV_ERR_INVALID_ARG;
+  if (rows_of(batch, steps, packed != 0) < 0 || channels > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
+  if (carries) *carries = scan_carries(batch, steps, packed != 0);
+  if (bytes) *bytes = scan_workspace_bytes(batch, steps, packed != 0, channels);
   return FFTMV_SUCCESS;
 }
 

@@ -56,7 +56,9 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
 #pragma unroll
   for (int e = 0; e < VEC; ++e) r.v[e] = static_cast<T>(f[e]);
   if constexpr (VEC == kVec<T>) {
-    *reinterpret_cast<u32x4_any *>(p) = __builtin_bit_cast(u32x4_any, r);
+    // streamed past the caches: no kernel here reads its own output, and the
+    // inputs' lines that two blocks of channels share stay longer
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_any, r), reinterpret_cast<u32x4_any *>(p));
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) p[e] = r.v[e];

@@ -18,11 +18,12 @@ forms. There is no fallback: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import FFTMV_SUCCESS, FftmvError, lib
 
 FFTMV_F32, FFTMV_BF16, FFTMV_F16 = 0, 1, 2
-FFTMV_RECURRENCE_CHUNK = 256
+FFTMV_RECURRENCE_CHUNK = 128
 DECAYS = {"sigmoid": 0, "exp": 1, "value": 2}
 DRIVES = {"complement": 0, "plain": 1}
 ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2}
@@ -72,7 +73,7 @@ def _lib():
     if _bound is None:
         L = lib()
         Z = ctypes.POINTER(_Z)
-        L.fftmv_recurrence_workspace.argtypes = [_I64, _I64, Z]
+        L.fftmv_recurrence_sizes.argtypes = [_I64, _I64, _I64, ctypes.c_int, ctypes.POINTER(_I64), Z]
         L.fftmv_group_norm_workspace.argtypes = [_I64, _I64, _I64, _I64, Z]
         for name, kind in (("recurrence_forward", _Recurrence), ("recurrence_backward", _Recurrence),
                            ("recurrence_step", _Step), ("group_norm_forward", _GroupNorm),
@@ -87,10 +88,12 @@ def _check(status, what):
         raise FftmvError(status, what)
 
 
-def fftmv_recurrence_workspace(rows: int, channels: int) -> int:
-    n = _Z()
-    _check(_lib().fftmv_recurrence_workspace(rows, channels, ctypes.byref(n)), "fftmv_recurrence_workspace")
-    return n.value
+def fftmv_recurrence_sizes(batch: int, steps: int, channels: int, packed: bool) -> tuple[int, int]:
+    """(rows of carries, bytes of workspace) of a forward or backward call."""
+    c, n = _I64(), _Z()
+    _check(_lib().fftmv_recurrence_sizes(batch, steps, channels, packed, ctypes.byref(c), ctypes.byref(n)),
+           "fftmv_recurrence_sizes")
+    return c.value, n.value
 
 
 def fftmv_recurrence_forward(r: _Recurrence, stream: int = 0) -> None:
@@ -236,6 +239,7 @@ class _On:
 
 # ---- the recurrence
 _workspaces = {}
+_sizes = functools.lru_cache(maxsize=1024)(fftmv_recurrence_sizes)  # a function of the shape alone
 
 
 def _workspace(nbytes, stream, like):
@@ -256,7 +260,7 @@ def _workspace(nbytes, stream, like):
 
 
 def _sequences(x, lengths, offsets):
-    """(batch, steps, channels, rows) of the three forms."""
+    """(batch, steps, channels) of the three forms."""
     if offsets is not None:
         if lengths is not None:
             raise ValueError("lengths belong to padded batches and offsets to packed ones: give one of them")
@@ -264,14 +268,14 @@ def _sequences(x, lengths, offsets):
             raise ValueError(f"a packed field is [steps, channels] with offsets [sequences + 1], got "
                              f"{tuple(x.shape)} and {tuple(offsets.shape)}")
         T, C = x.shape
-        return offsets.shape[0] - 1, T, C, T
+        return offsets.shape[0] - 1, T, C
     if x.dim() == 3:
         B, T, C = x.shape
     elif x.dim() == 2:
         (T, C), B = x.shape, 1
     else:
         raise ValueError(f"x must be [batch, steps, channels] or [steps, channels], got {tuple(x.shape)}")
-    return B, T, C, B * T
+    return B, T, C
 
 
 def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths=None, offsets=None, save=False,
@@ -295,7 +299,7 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     import torch
 
     dtype = _dtype_of(x, "x")
-    B, T, C, rows = _sequences(x, lengths, offsets)
+    B, T, C = _sequences(x, lengths, offsets)
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
     xf, gf = _field(x, x, "x"), _field(gate, x, "gate")
     h0p = _floats(h0, (B, C), x, "h0")
@@ -303,13 +307,12 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     with _On(stream, x, gate, h0, lengths, offsets, out) as s:
         h = _output(out, x, (x, gate), "out")
         last = torch.empty((B, C), dtype=torch.float32, device=x.device)
-        carries = torch.empty((-(-rows // FFTMV_RECURRENCE_CHUNK), C), dtype=torch.float32,
-                              device=x.device) if save else None
         if B == 0:
-            if rows:
+            if T:
                 h.zero_()
-            return (h, last, carries) if save else (h, last)
-        need = fftmv_recurrence_workspace(rows, C)
+            return (h, last, torch.empty((0, C), device=x.device)) if save else (h, last)
+        n, need = _sizes(B, T, C, offsets is not None)
+        carries = torch.empty((n, C), dtype=torch.float32, device=x.device) if save else None
         ws = _workspace(need, s, x)
         r = _Recurrence(B, T, C, dtype, *kinds, 0, lens, offs, *xf, *gf, h0p, carries.data_ptr() if save else None,
                         ws.data_ptr() if need else None, need, *_field(h, x, "out"), last.data_ptr())
@@ -326,23 +329,23 @@ def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="s
     import torch
 
     dtype = _dtype_of(x, "x")
-    B, T, C, rows = _sequences(x, lengths, offsets)
+    B, T, C = _sequences(x, lengths, offsets)
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
     xf, gf, df = _field(x, x, "x"), _field(gate, x, "gate"), _field(dh, x, "dh")
     h0p, lp = _floats(h0, (B, C), x, "h0"), _floats(dh_last, (B, C), x, "dh_last")
-    cp = _floats(carries, (-(-rows // FFTMV_RECURRENCE_CHUNK), C), x, "carries")
-    if cp is None:
+    n, need = _sizes(B, T, C, offsets is not None) if B else (0, 0)
+    if carries is None:
         raise ValueError("carries must be what recurrence(..., save=True) returned")
+    cp = _floats(carries, (n, C), x, "carries")
     lens, offs = _ints(lengths, B, x, "lengths"), _ints(offsets, B + 1, x, "offsets")
     with _On(stream, dh, x, gate, carries, h0, dh_last, lengths, offsets) as s:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dg = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         dh0 = torch.empty((B, C), dtype=torch.float32, device=x.device)
         if B == 0:
-            if rows:
+            if T:
                 dx.zero_(), dg.zero_()
             return dx, dg, dh0
-        need = fftmv_recurrence_workspace(rows, C)
         ws = _workspace(need, s, x)
         r = _Recurrence(B, T, C, dtype, *kinds, 0, lens, offs, *xf, *gf, h0p, cp, ws.data_ptr() if need else None, need,
                         None, 0, 0, None, *df, lp, *_field(dx, x, "dx"), *_field(dg, x, "dgate"), dh0.data_ptr())

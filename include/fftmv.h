@@ -336,10 +336,9 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  * Forward writes h (rounded once to the element type), and where not NULL
  *   h_last   [batch][channels] the state after each sequence's last step
  *            (h0 for an empty one)
- *   carries  [chunks][channels] the state that enters each run of
- *            FFTMV_RECURRENCE_CHUNK steps, rows counted over all sequences
- *            (chunks = ceil(rows / FFTMV_RECURRENCE_CHUNK), rows = batch *
- *            steps, or steps when packed): what the backward pass starts from
+ *   carries  [carries][channels] (their number: fftmv_recurrence_sizes) the
+ *            state that enters each run of FFTMV_RECURRENCE_CHUNK steps: what
+ *            the backward pass starts from
  *
  * Backward takes x, gate, h0 and carries as the forward had and left them,
  * dh (the gradient of h) and, where not NULL, dh_last (that of h_last), and
@@ -349,8 +348,8 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  *   dh0      a_0 r_0 (dh_last for an empty sequence); may be NULL
  * with h recomputed in FP32 from carries, not read back rounded.
  *
- * workspace: fftmv_recurrence_workspace bytes, 8-byte aligned, zero before
- * the first call; each call leaves it zero again. Calls that share one must
+ * workspace: as many bytes as fftmv_recurrence_sizes says, 8-byte aligned,
+ * zero before the first call; each call leaves it zero again. Calls that share one must
  * be ordered. h0 NULL stands for zeros. A state that is not finite stays
  * not finite (infinity or NaN) until its sequence ends; it reaches no other
  * sequence or channel.
@@ -358,7 +357,7 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  * -- steps may be 0 --, an unknown type/decay/drive, both lengths and
  * offsets, a workspace that is too small); FFTMV_ERR_UNSUPPORTED_SIZE
  * (more than 2^31 - 1 rows or channels, or a grid above 2^32 work-items). */
-#define FFTMV_RECURRENCE_CHUNK 256
+#define FFTMV_RECURRENCE_CHUNK 128
 typedef struct fftmv_recurrence_s {
   int64_t batch, steps, channels;
   int32_t dtype, decay, drive, reserved; /* reserved: 0 */
@@ -386,8 +385,11 @@ typedef struct fftmv_recurrence_s {
   float *dh0;
 } fftmv_recurrence_t;
 
-/* Workspace bytes of a forward or backward call over this many rows. */
-FFTMV_API int fftmv_recurrence_workspace(int64_t rows, int64_t channels, size_t *bytes);
+/* For a forward or backward call of this shape (packed: it has offsets): how
+ * many rows `carries` has (0: none are used) and how many bytes the workspace
+ * needs (0: none). Either output may be NULL. */
+FFTMV_API int fftmv_recurrence_sizes(int64_t batch, int64_t steps, int64_t channels, int packed, int64_t *carries,
+                                     size_t *workspace_bytes);
 FFTMV_API int fftmv_recurrence_forward(const fftmv_recurrence_t *r, hipStream_t stream);
 FFTMV_API int fftmv_recurrence_backward(const fftmv_recurrence_t *r, hipStream_t stream);
 
