@@ -48,30 +48,28 @@ static_assert(kSegs == 32 && kSegsPerWave == 4 && kWaves == 8, "one bit of a wor
 
 // How the rows are cut: chains of `places` chunks, `blocks` of channels.
 struct ScanAxis {
-  int64_t places;   // chunks of a chain
-  int64_t chains;   // chains over the batch (1 when packed)
-  int64_t blocks;   // blocks of W channels
-  int64_t per;      // sequences of one chunk, where whole ones fit (else 1)
+  int places;  // chunks of a chain
+  int chains;  // chains over the batch (1 when packed)
+  int blocks;  // blocks of W channels
+  int per;     // sequences of one chunk, where whole ones fit (else 1)
   __host__ __device__ bool joined() const { return places > 1; }
-  int64_t workgroups() const { return places * chains * blocks; }
+  int64_t pairs() const { return static_cast<int64_t>(chains) * blocks; }
+  int64_t workgroups() const { return pairs() * places; }
 };
 
 inline ScanAxis scan_axis(int64_t batch, int64_t steps, bool packed, int64_t channels, int64_t width) {
   ScanAxis a;
-  a.blocks = (channels + width - 1) / width;
+  a.blocks = static_cast<int>((channels + width - 1) / width);
   a.per = 1;
   if (steps == 0) {  // only first and last states, by one workgroup per block
     a.places = a.chains = 1;
-  } else if (packed) {
-    a.places = (steps + kChunk - 1) / kChunk;
-    a.chains = 1;
-  } else if (steps > kChunk / 2) {
-    a.places = (steps + kChunk - 1) / kChunk;
-    a.chains = batch;
+  } else if (packed || steps > kChunk / 2) {
+    a.places = static_cast<int>((steps + kChunk - 1) / kChunk);
+    a.chains = packed ? 1 : static_cast<int>(batch);
   } else {
     a.places = 1;
-    a.per = kChunk / steps;
-    a.chains = (batch + a.per - 1) / a.per;
+    a.per = static_cast<int>(kChunk / steps);
+    a.chains = static_cast<int>((batch + a.per - 1) / a.per);
   }
   return a;
 }
@@ -79,99 +77,111 @@ inline ScanAxis scan_axis(int64_t batch, int64_t steps, bool packed, int64_t cha
 // Rows of `carries`: one for every chunk, none where no chunk follows another.
 inline int64_t scan_carries(int64_t batch, int64_t steps, bool packed) {
   const ScanAxis a = scan_axis(batch, steps, packed, 1, 1);
-  return a.joined() ? a.places * a.chains : 0;
+  return a.joined() ? static_cast<int64_t>(a.places) * a.chains : 0;
 }
 
 // ------------------------------------------------------------- workspace
-// A counter line for every chain and block; then for every chunk and column
-// the map (A, H) as one 64-bit word and the state behind the chunk as one
-// 32-bit word. A word is written once, whole, and zero stands for "not there
-// yet" (the value +0 is written as -0), so no word needs a flag or a fence.
-struct ScanCounters {
-  uint32_t ticket, done;
-  uint32_t pad[30];  // 128 bytes
+// Counters, one for every chain and block of channels, in a buffer of their
+// own that every call leaves zero. And for every chunk and column three 64-bit
+// words: the two halves of its map (A, H) and the state behind it, each below
+// the number of the call in its upper half. A word is written once, whole,
+// and is there when it carries this call's number: no flag, no fence, and
+// nothing to clear for the next call, whatever its shape (the owner of the
+// workspace counts the calls). With 12 bytes a column, cleared by the last
+// workgroup of a chain, every workgroup had to wait for its words' arrival
+// before counting itself: 235 instead of 207 us backward at 4 x 4096 x 4096
+// bf16; cleared by a second launch, small calls took 3 us more.
+struct ScanCounter {
+  uint32_t ticket;
+  uint32_t pad[31];  // a line of its own
 };
 
 // Host: enough for every block width.
-inline size_t scan_workspace_bytes(int64_t batch, int64_t steps, bool packed, int64_t channels) {
+struct ScanWorkspace {
+  size_t counters = 0, words = 0;
+};
+inline ScanWorkspace scan_workspace_bytes(int64_t batch, int64_t steps, bool packed, int64_t channels) {
   const int64_t widest = 8 * kLanes;
   const ScanAxis a = scan_axis(batch, steps, packed, channels, widest);
-  if (!a.joined()) return 0;
-  const int64_t pairs = a.chains * a.blocks;  // blocks half as wide: twice as many counters
-  return static_cast<size_t>(2 * pairs) * sizeof(ScanCounters) + static_cast<size_t>(a.places * pairs) * widest * 12;
+  ScanWorkspace w;
+  if (!a.joined()) return w;
+  const int64_t pairs = a.pairs();  // blocks half as wide: twice as many chains
+  w.counters = static_cast<size_t>(2 * pairs) * sizeof(ScanCounter);
+  w.words = static_cast<size_t>(a.places * pairs) * widest * 24;
+  return w;
 }
 
 struct ScanChain {  // the workspace of one chain and block of channels
-  ScanCounters *count;
-  uint64_t *map;    // [places][W]
-  uint32_t *state;  // [places][W]
+  uint32_t *ticket;
+  uint64_t *words;  // [places][3][W]
+  uint32_t call;
+  bool deep;        // many chunks of the chain run at once
 };
 
 template <int W>
-__device__ __forceinline__ ScanChain scan_chain(void *ws, const ScanAxis &a, int64_t chain) {
+__device__ __forceinline__ ScanChain scan_chain(const fftmv_recurrence_t &r, const ScanAxis &a, int chain) {
   ScanChain s;
-  const int64_t all = a.chains * a.blocks;
-  unsigned char *p = static_cast<unsigned char *>(ws);
-  s.count = reinterpret_cast<ScanCounters *>(p) + chain;
-  p += all * static_cast<int64_t>(sizeof(ScanCounters));
-  s.map = reinterpret_cast<uint64_t *>(p) + chain * a.places * W;
-  s.state = reinterpret_cast<uint32_t *>(p + all * a.places * W * 8) + chain * a.places * W;
+  s.ticket = &(static_cast<ScanCounter *>(r.counters) + chain)->ticket;
+  s.words = static_cast<uint64_t *>(r.workspace) + static_cast<int64_t>(chain) * a.places * (3 * W);
+  s.call = r.call;
+  s.deep = a.chains * a.blocks <= 12;
   return s;
 }
 
-__device__ __forceinline__ float nonzero(float v) { return __builtin_bit_cast(uint32_t, v) == 0u ? -0.0f : v; }
-
-__device__ __forceinline__ void publish_map(const ScanChain &s, int64_t i, float A, float H) {
-  const uint64_t w = static_cast<uint64_t>(__builtin_bit_cast(uint32_t, nonzero(H))) << 32 |
-                     __builtin_bit_cast(uint32_t, A);
-  __hip_atomic_store(s.map + i, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void publish_state(const ScanChain &s, int64_t i, float h) {
-  __hip_atomic_store(s.state + i, __builtin_bit_cast(uint32_t, nonzero(h)), __ATOMIC_RELAXED,
+// Words of column c of a place: 0 and 1 its map (A, H), 2 the state behind it.
+template <int W>
+__device__ __forceinline__ void publish(const ScanChain &s, int place, int word, int c, float v) {
+  __hip_atomic_store(s.words + static_cast<int64_t>(place) * (3 * W) + (word * W + c),
+                     static_cast<uint64_t>(s.call) << 32 | __builtin_bit_cast(uint32_t, v), __ATOMIC_RELAXED,
                      __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ uint32_t peek_state(const ScanChain &s, int64_t i) {
-  return __hip_atomic_load(s.state + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+template <int W>
+__device__ __forceinline__ uint64_t peek(const ScanChain &s, int place, int word, int c) {
+  return __hip_atomic_load(s.words + static_cast<int64_t>(place) * (3 * W) + (word * W + c), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool is_there(const ScanChain &s, uint64_t word) {
+  return static_cast<uint32_t>(word >> 32) == s.call;
+}
+__device__ __forceinline__ float value_of(uint64_t word) {
+  return __builtin_bit_cast(float, static_cast<uint32_t>(word));
 }
 
-// The state behind place p - 1 in column c. Looks at the kWindow chunks in
-// front of p together; a state is there sooner or later, since each of them
+// The state behind place p - 1 in column c. Looks at the words of the two
+// chunks in front of p together, and of two more where a chain has over forty
+// chunks running at once (some 500 workgroups run together): every word that
+// is looked at delays all loads, every chunk less makes more of the chain wait
+// in a row. Measured forward, 2 | 4 | 8 chunks: 4 x 4096 x 4096 bf16 105 | 114 |
+// 125 us, 30011 x 2048 fp16 packed 117 | 125 | 241, one series of 65536 x 1024
+// bf16 170 | 137 | 148. A state is there sooner or later, since each chunk
 // publishes its own. The bound on the polls ends the wait if the workspace
-// was not what the call requires (not zero on entry): the result is NaN.
+// was not what the call requires: the result is NaN.
 template <int W>
-__device__ float state_before(const ScanChain &s, int64_t p, int c) {
-  constexpr int kWindow = 8;
+__device__ __forceinline__ float state_before(const ScanChain &s, int p, int c) {
+#pragma unroll 1
   for (int poll = 0; poll < (1 << 20); ++poll) {
-    uint32_t st[kWindow];
-    uint64_t mp[kWindow];
-#pragma unroll
-    for (int j = 0; j < kWindow; ++j) {
-      const int64_t i = p - 1 - j;
-      st[j] = 0;
-      mp[j] = 0;
-      if (i >= 0) {
-        st[j] = peek_state(s, i * W + c);
-        mp[j] = __hip_atomic_load(s.map + i * W + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int i0 = p - 1, i1 = p < 2 ? 0 : p - 2;
+    const uint64_t s0 = peek<W>(s, i0, 2, c), s1 = peek<W>(s, i1, 2, c);
+    const uint64_t A0 = peek<W>(s, i0, 0, c), H0 = peek<W>(s, i0, 1, c);
+    if (is_there(s, s0)) return value_of(s0);
+    if (is_there(s, A0) && is_there(s, H0)) {
+      if (is_there(s, s1)) return fmaf(value_of(A0), value_of(s1), value_of(H0));
+      if (s.deep) {
+        const int i2 = p < 3 ? 0 : p - 3, i3 = p < 4 ? 0 : p - 4;
+        const uint64_t s2 = peek<W>(s, i2, 2, c), s3 = peek<W>(s, i3, 2, c);
+        const uint64_t A1 = peek<W>(s, i1, 0, c), H1 = peek<W>(s, i1, 1, c);
+        const uint64_t A2 = peek<W>(s, i2, 0, c), H2 = peek<W>(s, i2, 1, c);
+        if (is_there(s, A1) && is_there(s, H1)) {
+          float h = 0.0f;
+          bool found = is_there(s, s2);
+          if (found) {
+            h = value_of(s2);
+          } else if (is_there(s, A2) && is_there(s, H2) && is_there(s, s3)) {
+            found = true;
+            h = fmaf(value_of(A2), value_of(s3), value_of(H2));
+          }
+          if (found) return fmaf(value_of(A0), fmaf(value_of(A1), h, value_of(H1)), value_of(H0));
+        }
       }
-    }
-    // the nearest state with every map behind it
-    int found = kWindow;
-    bool open = true;
-#pragma unroll
-    for (int j = 0; j < kWindow; ++j) {
-      if (open && st[j]) found = j, open = false;
-      if (open && !mp[j]) open = false;
-    }
-    if (found < kWindow) {
-      float h = 0.0f;
-#pragma unroll
-      for (int j = kWindow - 1; j >= 0; --j) {
-        if (j == found) h = __builtin_bit_cast(float, st[j]);
-        if (j < found)
-          h = nonzero(fmaf(__builtin_bit_cast(float, static_cast<uint32_t>(mp[j])), h,
-                           __builtin_bit_cast(float, static_cast<uint32_t>(mp[j] >> 32))));
-      }
-      return h;
     }
     __builtin_amdgcn_s_sleep(1);
   }
@@ -181,52 +191,58 @@ __device__ float state_before(const ScanChain &s, int64_t p, int c) {
 // What a chunk does with the states of its chain, by one thread per column:
 // publishes its map (A, H), or, when it is `closed` (nothing that enters it
 // leaves it), its state H; returns the state that enters it, where `needed`.
-// `early`: what peek_state saw in front some time ago, 0 for nothing. All its
-// words have arrived when it returns.
+// `early`: what peek saw as the state in front some time ago.
 template <int W>
-__device__ __forceinline__ float meet_chain(const ScanChain &s, int64_t p, int col, float A, float H, bool closed,
-                                            bool needed, uint32_t early) {
+__device__ __forceinline__ float meet_chain(const ScanChain &s, int p, int col, float A, float H, bool closed,
+                                            bool needed, uint64_t early) {
+  // the columns of a wave wait together
+  const bool ready = needed && __ballot(!is_there(s, early)) == 0;
   float in = 0.0f;
-  if (closed)
-    publish_state(s, p * W + col, H);
-  else if (!early)
-    publish_map(s, p * W + col, A, H);
-  if (needed) in = early ? __builtin_bit_cast(float, early) : state_before<W>(s, p, col);
-  if (!closed) publish_state(s, p * W + col, fmaf(A, in, nonzero(H)));
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if (closed) {
+    publish<W>(s, p, 2, col, H);
+  } else if (!ready) {
+    publish<W>(s, p, 0, col, A);
+    publish<W>(s, p, 1, col, H);
+  }
+  if (needed) in = ready ? value_of(early) : state_before<W>(s, p, col);
+  if (!closed) {
+    publish<W>(s, p, 2, col, fmaf(A, in, H));
+  }
   return in;
 }
 
-// Draws the next place of the chain, in the thread that gets the ticket.
+// The next place of a chain is the count before this call's addition; the
+// thread that drew the last one leaves the counter zero.
 __device__ __forceinline__ uint32_t draw_place(const ScanChain &s) {
-  return __hip_atomic_fetch_add(&s.count->ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __hip_atomic_fetch_add(s.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// Counts a workgroup that will not touch the chain's words again.
-__device__ __forceinline__ uint32_t leave_chain(const ScanChain &s) {
-  return __hip_atomic_fetch_add(&s.count->done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// Leaves the workspace of a chain zero: by the last workgroup that left it.
-template <int W>
-__device__ __forceinline__ void clear_chain(const ScanChain &s, int64_t places) {
-  for (int64_t i = threadIdx.x; i < places * W; i += kThreads) {
-    s.map[i] = 0;
-    s.state[i] = 0;
-  }
-  if (threadIdx.x == 0) s.count->ticket = s.count->done = 0;
+__device__ __forceinline__ uint32_t settle_ticket(const ScanChain &s, uint32_t ticket, int places) {
+  if (ticket == static_cast<uint32_t>(places - 1))
+    __hip_atomic_store(s.ticket, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return ticket;
 }
 
 // ------------------------------------------------------------------ rows
 // Which of a thread's rows start a sequence, end one, belong to none. In an
-// ordinary chunk (below) all that is known and only seq[0] and t[0] are set.
+// ordinary chunk (below) none does, and seq[0] alone is set.
 struct Rows {
-  uint32_t present, start, last, dead;  // a bit a row; dead: in no sequence, or not present
-  uint32_t empty;                       // dead, and stands for an empty sequence of a padded batch
-  uint32_t seq[kRows], t[kRows];        // sequence, and step within its strides (packed: the row)
+  uint32_t bits;   // kRows bits each, from bit 0: dead (in no sequence, or not present), start, last, and from
+                   // bit 16: not present, empty (a row that stands for an empty sequence of a padded batch)
+  int row0;        // step of row 0 in the sequence c.seq (packed: the row)
+  int seq[kRows];
+  __device__ __forceinline__ bool dead(int i) const { return bits >> i & 1u; }
+  __device__ __forceinline__ bool start(int i) const { return bits >> (4 + i) & 1u; }
+  __device__ __forceinline__ bool last(int i) const { return bits >> (8 + i) & 1u; }
+  __device__ __forceinline__ bool absent(int i) const { return bits >> (16 + i) & 1u; }
+  __device__ __forceinline__ bool empty(int i) const { return bits >> (20 + i) & 1u; }
+  __device__ __forceinline__ bool closed_front() const { return bits & 0x0FFu; }
+  __device__ __forceinline__ bool closed_back() const { return bits & 0xF0Fu; }
 };
+static_assert(kRows == 4, "nibbles");
 
 // The sequence that holds `row` when packed: the last one that starts at or
 // before it (-1: none does; batch: behind the last one's end).
-__device__ __forceinline__ int packed_sequence(const fftmv_recurrence_t &r, int64_t row) {
+__device__ __forceinline__ int packed_sequence(const fftmv_recurrence_t &r, int row) {
   int lo = 0, hi = static_cast<int>(r.batch) + 1;  // offsets[0..lo) <= row < offsets[hi..]
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;
@@ -236,107 +252,95 @@ __device__ __forceinline__ int packed_sequence(const fftmv_recurrence_t &r, int6
   return lo - 1;
 }
 
-__device__ __forceinline__ int64_t held_steps(const fftmv_recurrence_t &r, int64_t b) {
-  if (!r.lengths) return r.steps;
-  const int64_t l = r.lengths[b];
-  return l < 0 ? 0 : l > r.steps ? r.steps : l;
+__device__ __forceinline__ int held_steps(const fftmv_recurrence_t &r, int b) {
+  const int T = static_cast<int>(r.steps);
+  if (!r.lengths) return T;
+  const int l = r.lengths[b];
+  return l < 0 ? 0 : l > T ? T : l;
 }
 
 // One chunk, as the whole workgroup sees it.
 struct Chunk {
-  int64_t chain, place;  // over the batch; along the time axis
-  int64_t seq;           // sequence of the first row (of all rows if ordinary)
-  bool ordinary;         // all rows are steps of one sequence, none its last
-  bool head, tail;       // nothing enters from the chunk in front / from the one behind
+  int chain, place;  // over the batch; along the time axis
+  int seq;           // sequence of the first row (of all rows if ordinary)
+  bool ordinary;     // all rows are steps of one sequence, none its last
+  bool head, tail;   // nothing enters from the chunk in front / from the one behind
 };
 
-__device__ __forceinline__ Chunk chunk_at(const fftmv_recurrence_t &r, const ScanAxis &a, int64_t chain,
-                                          int64_t place) {
+__device__ __forceinline__ Chunk chunk_at(const fftmv_recurrence_t &r, const ScanAxis &a, int chain, int place) {
+  const int T = static_cast<int>(r.steps), S = static_cast<int>(r.batch);
+  const int t0 = place * kChunk, end = T - t0 > kChunk ? t0 + kChunk : T;  // behind the last row
   Chunk c;
   c.chain = chain;
   c.place = place;
-  const int64_t t0 = place * kChunk, end = t0 + kChunk;
+  int seq;
+  bool ordinary, head, tail;
   if (r.offsets) {
-    const int s = packed_sequence(r, t0);
-    const bool held = s >= 0 && s < r.batch && t0 < r.steps;
-    c.seq = s;
-    c.head = place == 0 || !held || r.offsets[s] == t0;
-    c.ordinary = held && end < r.offsets[s + 1] && end < r.steps;
-    const int64_t back = end < r.steps ? end : r.steps;  // behind the chunk's last row
-    const int e = packed_sequence(r, back - 1);
-    c.tail = back >= r.steps || e < 0 || e >= r.batch || r.offsets[e + 1] == back;
+    seq = packed_sequence(r, t0);
+    const bool held = seq >= 0 && seq < S && t0 < T;
+    head = place == 0 || !held || r.offsets[seq] == t0;
+    ordinary = held && T - t0 > kChunk && end < r.offsets[seq + 1];
+    const int e = ordinary ? seq : packed_sequence(r, end - 1);
+    tail = end >= T || e < 0 || e >= S || r.offsets[e + 1] == end;
   } else {
-    c.seq = chain * a.per;
-    const int64_t held = a.per > 1 || r.steps == 0 ? 0 : held_steps(r, c.seq);
-    c.ordinary = end < held;
-    c.head = place == 0 || t0 >= held;
-    c.tail = end >= held;
+    seq = chain * a.per;
+    const int held = a.per > 1 || T == 0 ? 0 : held_steps(r, seq);
+    ordinary = held - t0 > kChunk;
+    head = place == 0 || t0 >= held;
+    tail = held - t0 <= kChunk;
   }
+  // the same in every lane: kept in scalar registers
+  c.seq = __builtin_amdgcn_readfirstlane(seq);
+  const uint32_t bits = __builtin_amdgcn_readfirstlane((ordinary ? 1 : 0) | (head ? 2 : 0) | (tail ? 4 : 0));
+  c.ordinary = bits & 1u;
+  c.head = bits & 2u;
+  c.tail = bits & 4u;
   return c;
 }
 
-__device__ __forceinline__ Rows ordinary_rows(const fftmv_recurrence_t &r, const Chunk &c, int seg) {
+__device__ __forceinline__ Rows rows_of(const fftmv_recurrence_t &r, const ScanAxis &a, const Chunk &c, int seg) {
   Rows q;
-  q.start = q.last = q.dead = q.empty = 0;
-  q.present = (1u << kRows) - 1u;
-  q.seq[0] = static_cast<uint32_t>(c.seq);
-  q.t[0] = static_cast<uint32_t>(c.place * kChunk + seg * kRows);
-  return q;
-}
-
-__device__ __forceinline__ Rows special_rows(const fftmv_recurrence_t &r, const ScanAxis &a, const Chunk &c, int seg) {
-  Rows q;
-  q.present = q.start = q.last = q.empty = 0;
-  const int64_t row0 = c.place * kChunk + seg * kRows;
+  q.bits = 0;
+  q.seq[0] = c.seq;
+  q.row0 = c.place * kChunk + seg * kRows;
+  if (c.ordinary) return q;
+  const int T = static_cast<int>(r.steps), S = static_cast<int>(r.batch);
+  const int left = T - c.place * kChunk - seg * kRows;  // rows of the axis from here on, where one sequence has it
   if (r.offsets) {
-    int s = packed_sequence(r, row0);
-    const int S = static_cast<int>(r.batch);
-    int64_t from = s >= 0 ? r.offsets[s] : -1, to = s < S ? r.offsets[s + 1] : INT64_MAX;
+    int s = left > 0 ? packed_sequence(r, q.row0) : S;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int64_t row = row0 + i;
-      while (row >= to && s < S) {  // on to the next sequence that holds a row
-        ++s;
-        from = to;
-        to = s < S ? r.offsets[s + 1] : INT64_MAX;
-      }
-      q.seq[i] = static_cast<uint32_t>(s < 0 || s >= S ? 0 : s);
-      q.t[i] = static_cast<uint32_t>(row);
-      if (row < r.steps) {
-        q.present |= 1u << i;
-        if (s >= 0 && s < S) {
-          if (row == from) q.start |= 1u << i;
-          if (row + 1 == to) q.last |= 1u << i;
-        }
-      }
-      if (row >= r.steps || s < 0 || s >= S) q.empty |= 1u << i;  // for now: dead
+      const bool here = i < left;
+      const int row = q.row0 + i;
+      while (here && s < S && row >= r.offsets[s + 1]) ++s;  // on to the next sequence that holds a row
+      const bool held = here && s >= 0 && s < S;
+      q.seq[i] = held ? s : 0;
+      if (!here) q.bits |= 1u << (16 + i);
+      if (!held) q.bits |= 1u << i;
+      if (held && row == r.offsets[s]) q.bits |= 1u << (4 + i);
+      if (held && row + 1 == r.offsets[s + 1]) q.bits |= 1u << (8 + i);
     }
-    q.dead = q.empty;
-    q.empty = 0;
   } else {
-    q.dead = 0;
-    const uint32_t T = static_cast<uint32_t>(r.steps), local = static_cast<uint32_t>(seg * kRows);
-    uint32_t b = static_cast<uint32_t>(c.seq), t = static_cast<uint32_t>(row0);
-    if (a.per > 1) b += local / T, t = local % T;
-    const int64_t end = (c.chain + 1) * a.per < r.batch ? (c.chain + 1) * a.per : r.batch;  // first sequence not here
+    const bool many = a.per > 1;
+    const int end = a.per < S - c.seq ? c.seq + a.per : S;  // first sequence not here
+    int b = c.seq, t = q.row0;
+    if (many) b += t / T, t %= T;
+    else if (left <= 0) b = end;
+    int held = b < end ? held_steps(r, b) : 0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if (a.per > 1 && t == T) t = 0, ++b;
-      const bool here = t < T && b < end;
-      q.seq[i] = here ? b : 0;
-      q.t[i] = t;
-      int64_t held = 0;
-      if (here) {
-        held = held_steps(r, b);
-        q.present |= 1u << i;
-        if (held == 0 && t == 0) q.empty |= 1u << i;
+      if (many ? t == T : i == left) {
+        t = 0, ++b;
+        if (!many) b = end;
+        held = b < end ? held_steps(r, b) : 0;
       }
-      if (t >= held) {
-        q.dead |= 1u << i;
-      } else {
-        if (t == 0) q.start |= 1u << i;
-        if (t + 1 == held) q.last |= 1u << i;
-      }
+      const bool here = b < end;
+      q.seq[i] = here ? b : c.seq;
+      if (!here) q.bits |= 1u << (16 + i);
+      if (here && held == 0 && t == 0) q.bits |= 1u << (20 + i);
+      if (!here || t >= held) q.bits |= 1u << i;
+      else if (t == 0) q.bits |= 1u << (4 + i);
+      if (here && t + 1 == held) q.bits |= 1u << (8 + i);
       ++t;
     }
   }
@@ -344,37 +348,44 @@ __device__ __forceinline__ Rows special_rows(const fftmv_recurrence_t &r, const 
 }
 
 // Where row i of a thread starts in a field, in elements.
-__device__ __forceinline__ int64_t row_offset(const fftmv_recurrence_t &r, const Rows &q, int i, int64_t sb,
-                                              int64_t st) {
-  const int64_t t = static_cast<int64_t>(q.t[i]) * st;
-  return r.offsets ? t : static_cast<int64_t>(q.seq[i]) * sb + t;
+__device__ __forceinline__ int64_t row_offset(const fftmv_recurrence_t &r, const ScanAxis &a, const Chunk &c,
+                                              const Rows &q, int i, int64_t sb, int64_t st) {
+  const int seq = c.ordinary ? c.seq : q.seq[i];
+  int64_t t = static_cast<int64_t>(q.row0) + i;
+  if (a.per > 1) t -= static_cast<int64_t>(seq - c.seq) * r.steps;
+  return (r.offsets ? 0 : static_cast<int64_t>(seq) * sb) + t * st;
 }
 
-// One field's rows of this thread.
-template <bool ORDINARY, typename T, int VEC>
-__device__ __forceinline__ void load_rows(const fftmv_recurrence_t &r, const Rows &q, const void *field, int64_t sb,
-                                          int64_t st, int64_t ch, Vec<T, VEC> (&v)[kRows]) {
+// One field's rows of this thread. In the place of a dead row comes the first
+// row of the chunk's sequence (or of the axis): always there, in cache, and
+// not used.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_rows(const fftmv_recurrence_t &r, const ScanAxis &a, const Chunk &c,
+                                          const Rows &q, const void *field, int64_t sb, int64_t st, int64_t ch,
+                                          Vec<T, VEC> (&v)[kRows]) {
   const T *p = static_cast<const T *>(field) + ch;
-  if constexpr (ORDINARY) {
-    p += row_offset(r, q, 0, sb, st);
+  if (c.ordinary) {
+    p += row_offset(r, a, c, q, 0, sb, st);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) v[i] = load_vec<T, VEC>(p + i * st);
-  } else {
+  } else if (r.steps > 0) {
+    const int64_t instead = r.offsets ? 0 : c.seq * sb;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      v[i] = Vec<T, VEC>{};
-      if (!(q.dead >> i & 1u)) v[i] = load_vec<T, VEC>(p + row_offset(r, q, i, sb, st));
+      const int64_t at = row_offset(r, a, c, q, i, sb, st);
+      v[i] = load_vec<T, VEC>(p + (q.dead(i) ? instead : at));
     }
   }
 }
-template <bool ORDINARY, typename T, int VEC>
-__device__ __forceinline__ void store_row(const fftmv_recurrence_t &r, const Rows &q, int i, void *field, int64_t sb,
-                                          int64_t st, int64_t ch, const float (&f)[VEC]) {
+template <typename T, int VEC>
+__device__ __forceinline__ void store_row(const fftmv_recurrence_t &r, const ScanAxis &a, const Chunk &c,
+                                          const Rows &q, int i, void *field, int64_t sb, int64_t st, int64_t ch,
+                                          const float (&f)[VEC]) {
   T *p = static_cast<T *>(field) + ch;
-  if constexpr (ORDINARY)
-    store_vec<T, VEC>(p + row_offset(r, q, 0, sb, st) + i * st, f);
-  else if (q.present >> i & 1u)
-    store_vec<T, VEC>(p + row_offset(r, q, i, sb, st), f);
+  if (c.ordinary)
+    store_vec<T, VEC>(p + row_offset(r, a, c, q, 0, sb, st) + i * st, f);
+  else if (!q.absent(i))
+    store_vec<T, VEC>(p + row_offset(r, a, c, q, i, sb, st), f);
 }
 
 // Hides where a value came from, so that what was computed from it before is
@@ -384,8 +395,8 @@ template <typename T, int VEC>
 __device__ __forceinline__ void forget(Vec<T, VEC> (&v)[kRows]) {
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    if constexpr (VEC * sizeof(T) == 16) {
-      u32x4_any w = __builtin_bit_cast(u32x4_any, v[i]);
+    if constexpr (VEC * sizeof(T) >= 8) {
+      auto w = __builtin_bit_cast(typename Words<VEC * sizeof(T)>::type, v[i]);
       asm volatile("" : "+v"(w));
       v[i] = __builtin_bit_cast(Vec<T, VEC>, w);
     }
@@ -416,6 +427,7 @@ __device__ __forceinline__ void store_state(float *p, int64_t seq, int64_t chann
 template <int VEC>
 __device__ __forceinline__ void pass_empty(const fftmv_recurrence_t &r, int seg, int64_t ch, const float *from,
                                            float *to) {
+#pragma unroll 1
   for (int64_t b = seg; b < r.batch; b += kSegs)
     if (r.offsets ? r.offsets[b + 1] <= r.offsets[b] : true) {
       float v[VEC];

@@ -21,7 +21,7 @@ struct BackwardLds {
   float gA[G][W], gH[G][W], gS[G][W];  // maps of the groups
   float enter[W];                      // what the chunk behind hands over
   __align__(8) uint8_t front_bits[kWaves], back_bits[kWaves];
-  uint32_t ticket, order;
+  uint32_t ticket;
 };
 
 // The chunk's join: from the segments' maps (written, not yet synchronised)
@@ -29,7 +29,7 @@ struct BackwardLds {
 // gradient that enters it from behind, in lds.S.
 template <int W, int VEC>
 __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const ScanAxis &axis, const Chunk &c,
-                                              const ScanChain &s, int64_t order, float carry, uint32_t early,
+                                              const ScanChain &s, int order, float carry, uint64_t early,
                                               BackwardLds<W> &lds) {
   constexpr int G = BackwardLds<W>::G, SG = kSegs / G;
   constexpr uint32_t kGroup = ~0u >> (32 - SG);
@@ -38,17 +38,16 @@ __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const
   const uint32_t fronts = read_segment_bits(lds.front_bits), backs = read_segment_bits(lds.back_bits);
 
   // maps of groups of segments: one thread per column and group
-  float mA[SG], mH[SG], mS[SG], cA = 1.0f, cH = 0.0f, cS = 0.0f;
+  float cA = 1.0f, cH = 0.0f, cS = 0.0f;
 #pragma unroll
   for (int i = 0; i < SG; ++i) {
-    mA[i] = lds.A[grp * SG + i][col];
-    mH[i] = lds.H[grp * SG + i][col];
-    mS[i] = lds.S[grp * SG + i][col];
-    cH = through(fronts >> (grp * SG + i) & 1u, mA[i], mH[i], cH);
-    cA *= mA[i];
+    const float A = lds.A[grp * SG + i][col];
+    cH = through(fronts >> (grp * SG + i) & 1u, A, lds.H[grp * SG + i][col], cH);
+    cA *= A;
   }
 #pragma unroll
-  for (int i = SG - 1; i >= 0; --i) cS = through(backs >> (grp * SG + i) & 1u, mA[i], mS[i], cS);
+  for (int i = SG - 1; i >= 0; --i)
+    cS = through(backs >> (grp * SG + i) & 1u, lds.A[grp * SG + i][col], lds.S[grp * SG + i][col], cS);
   lds.gA[grp][col] = cA;
   lds.gH[grp][col] = cH;
   lds.gS[grp][col] = cS;
@@ -73,8 +72,10 @@ __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const
     for (int j = 0; j < grp; ++j) h = through(fronts >> (j * SG) & kGroup, lds.gA[j][col], lds.gH[j][col], h);
 #pragma unroll
     for (int i = 0; i < SG; ++i) {
-      lds.H[grp * SG + i][col] = h;
-      h = through(fronts >> (grp * SG + i) & 1u, mA[i], mH[i], h);
+      float &H = lds.H[grp * SG + i][col];
+      const float next = through(fronts >> (grp * SG + i) & 1u, lds.A[grp * SG + i][col], H, h);
+      H = h;
+      h = next;
     }
   }
   __syncthreads();
@@ -82,8 +83,10 @@ __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const
   for (int j = G - 1; j > grp; --j) v = through(backs >> (j * SG) & kGroup, lds.gA[j][col], lds.gS[j][col], v);
 #pragma unroll
   for (int i = SG - 1; i >= 0; --i) {
-    lds.S[grp * SG + i][col] = v;
-    v = through(backs >> (grp * SG + i) & 1u, mA[i], mS[i], v);
+    float &S = lds.S[grp * SG + i][col];
+    const float next = through(backs >> (grp * SG + i) & 1u, lds.A[grp * SG + i][col], S, v);
+    S = v;
+    v = next;
   }
   __syncthreads();
 }
@@ -93,167 +96,153 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_
   constexpr int W = kLanes * VEC;
   __shared__ BackwardLds<W> lds;
   const int tid = threadIdx.x, seg = tid / kLanes, lane = tid % kLanes;
-  const int64_t chains = axis.chains * axis.blocks, chain = blockIdx.x % chains;
-  const int64_t block = chain % axis.blocks;
-  const int64_t ch = column_channel<VEC>(r.channels, block * W + lane * VEC);
-  const ScanChain s = scan_chain<W>(r.workspace, axis, chain);
+  // chains of all blocks of channels: block by block of one sequence, then the next
+  const uint32_t chains = static_cast<uint32_t>(axis.chains) * axis.blocks, chain = blockIdx.x % chains;
+  const int block = chain % static_cast<uint32_t>(axis.blocks), over_batch = chain / static_cast<uint32_t>(axis.blocks);
+  const int64_t ch = column_channel<VEC>(r.channels, static_cast<int64_t>(block) * W + lane * VEC);
+  const ScanChain s = scan_chain<W>(r, axis, chain);
 
   // as in the forward kernel, but places count from the end of the time axis
-  int64_t order = blockIdx.x / chains;
-  Chunk c = chunk_at(r, axis, chain / axis.blocks, axis.places - 1 - order);
+  int order = blockIdx.x / chains;
   uint32_t ticket = 0;
-  if (axis.joined() && tid == 0) ticket = draw_place(s);
+  bool drawn = !axis.joined();
+  if (!drawn && tid == 0) ticket = draw_place(s);
+  Chunk c;
+  Rows q;
   Vec<T, VEC> x[kRows], g[kRows], d[kRows];
-  auto load = [&]() {
-    const Rows q = ordinary_rows(r, c, seg);
-    load_rows<true>(r, q, r.gate, r.gate_batch, r.gate_step, ch, g);
-    load_rows<true>(r, q, r.x, r.x_batch, r.x_step, ch, x);
-    load_rows<true>(r, q, r.dh, r.dh_batch, r.dh_step, ch, d);
-  };
-  if (c.ordinary) load();
-  uint32_t early = 0;
+  for (;;) {
+    c = chunk_at(r, axis, over_batch, axis.places - 1 - order);
+    q = rows_of(r, axis, c, seg);
+    load_rows(r, axis, c, q, r.gate, r.gate_batch, r.gate_step, ch, g);
+    load_rows(r, axis, c, q, r.x, r.x_batch, r.x_step, ch, x);
+    load_rows(r, axis, c, q, r.dh, r.dh_batch, r.dh_step, ch, d);
+    if (drawn) break;
+    drawn = true;
+    if (tid == 0) lds.ticket = settle_ticket(s, ticket, axis.places);
+    __syncthreads();
+    const uint32_t t = __builtin_amdgcn_readfirstlane(lds.ticket);
+    if (t >= static_cast<uint32_t>(axis.places)) return;  // a workspace or number that the call may not have
+    if (t == static_cast<uint32_t>(order)) break;
+    order = static_cast<int>(t);
+  }
+  uint64_t early = 0;
   float carry = 0.0f;
   if (axis.joined()) {
-    if (tid == 0) lds.ticket = ticket;
-    __syncthreads();
-    const int64_t drawn = __builtin_amdgcn_readfirstlane(lds.ticket);
-    if (drawn >= axis.places) return;  // a workspace that was not zero
-    if (drawn != order) {
-      order = drawn;
-      c = chunk_at(r, axis, c.chain, axis.places - 1 - order);
-      if (c.ordinary) load();
-    }
-    if (!c.tail && tid < W) early = peek_state(s, (order - 1) * W + tid);
+    if (!c.tail && tid < W) early = peek<W>(s, order - 1, 2, tid);
     // the state that enters the chunk (unused where a sequence starts)
-    const int64_t cc = column_channel<VEC>(r.channels, block * W + tid % W);
+    const int64_t cc = column_channel<VEC>(r.channels, static_cast<int64_t>(block) * W + tid % W);
     if (!c.head)
-      carry = r.carries[(c.chain * axis.places + c.place) * r.channels + cc];
+      carry = r.carries[(static_cast<int64_t>(c.chain) * axis.places + c.place) * r.channels + cc];
     else if (c.ordinary && r.h0)
       carry = r.h0[c.seq * r.channels + cc];
   }
 
-  float A[VEC], H[VEC], S[VEC], h[VEC], b[VEC], w[kRows][VEC];
+  float A[VEC], h[VEC], b[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) A[e] = 1.0f, H[e] = 0.0f, S[e] = 0.0f;
-  uint32_t left = 0;
-  auto join = [&](uint32_t front, uint32_t back) {
+  for (int e = 0; e < VEC; ++e) A[e] = 1.0f, h[e] = 0.0f, b[e] = 0.0f;
+  bool open = true;  // a later row's gradient reaches the segment's first
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      lds.A[seg][lane * VEC + e] = A[e];
-      lds.H[seg][lane * VEC + e] = H[e];
-      lds.S[seg][lane * VEC + e] = S[e];
+  for (int i = 0; i < kRows; ++i) {
+    float dl[VEC] = {};
+    if (!c.ordinary) {
+      open = open && !q.dead(i);
+      if (q.start(i)) load_state(r.h0, q.seq[i], r.channels, ch, h);
+      if (q.last(i)) load_state(r.dh_last, q.seq[i], r.channels, ch, dl);
     }
-    const uint64_t fb = __ballot(front != 0), bb = __ballot(back != 0);
-    if (tid % kWave == 0) lds.front_bits[tid / kWave] = segment_bits(fb), lds.back_bits[tid / kWave] = segment_bits(bb);
-    backward_join<W, VEC>(r, axis, c, s, order, carry, early, lds);
-    if (axis.joined() && tid == 0) left = leave_chain(s);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      h[e] = lds.H[seg][lane * VEC + e];
-      b[e] = lds.S[seg][lane * VEC + e];
-    }
-  };
-  // one step forward: w = h_{t-1} (- x_t), the factor of dgate
-  auto ahead = [&](int i) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const Terms t = decay_terms<T, DECAY>(g[i][e]);
-      w[i][e] = DRIVE == FFTMV_DRIVE_COMPLEMENT ? h[e] - x[i][e] : h[e];
       h[e] = fmaf(t.a, h[e], drive_of<DRIVE>(t, x[i][e]));
+      A[e] *= t.a;
+      if (open) b[e] = fmaf(A[e], d[i][e] + dl[e], b[e]);  // a_0 .. a_i dh_i
     }
-  };
-  // one step back: b becomes s_t
-  auto behind = [&](int i, bool dead, float (&du)[VEC], float (&dv)[VEC]) {
+    if (!c.ordinary) {
+      open = open && !q.last(i);
+      if (q.dead(i)) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) h[e] = 0.0f;
+      }
+    }
+    row_done();
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    lds.A[seg][lane * VEC + e] = A[e];
+    lds.H[seg][lane * VEC + e] = h[e];
+    lds.S[seg][lane * VEC + e] = b[e];
+  }
+  const uint64_t front = __ballot(q.closed_front()), back = __ballot(q.closed_back());
+  if (tid % kWave == 0) {
+    lds.front_bits[tid / kWave] = segment_bits(front);
+    lds.back_bits[tid / kWave] = segment_bits(back);
+  }
+  backward_join<W, VEC>(r, axis, c, s, order, carry, early, lds);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    h[e] = lds.H[seg][lane * VEC + e];
+    b[e] = lds.S[seg][lane * VEC + e];
+  }
+
+  // The rows behind first, two by two: forward to w = h_{t-1} (- x_t), the
+  // factor of dgate, and back over them; b becomes s_t. (All four rows' w at
+  // once would take 16 registers more, and a third of the workgroups.)
+  auto ahead = [&](int i, float (&v)[VEC], float (&w)[VEC]) {
+    if (!c.ordinary && q.start(i)) load_state(r.h0, q.seq[i], r.channels, ch, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const Terms t = decay_terms<T, DECAY>(g[i][e]);
-      const float rt = d[i][e] + b[e];
-      b[e] = dead ? 0.0f : t.a * rt;
-      du[e] = dead ? 0.0f : DRIVE == FFTMV_DRIVE_COMPLEMENT ? rt * t.rest : rt;
-      dv[e] = dead ? 0.0f : rt * w[i][e] * t.slope;
+      w[e] = DRIVE == FFTMV_DRIVE_COMPLEMENT ? v[e] - x[i][e] : v[e];
+      v[e] = fmaf(t.a, v[e], drive_of<DRIVE>(t, x[i][e]));
     }
+    row_done();
   };
-
-  if (c.ordinary) {
-    const Rows q = ordinary_rows(r, c, seg);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
+  for (int half = kRows - 2; half >= 0; half -= 2) {
+    float v[VEC], w[2][VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = h[e];
+    forget(g);
+    forget(x);
+#pragma unroll
+    for (int i = 0; i < half; ++i) ahead(i, v, w[0]);
+    ahead(half, v, w[0]);
+    ahead(half + 1, v, w[1]);
+    forget(g);
+    forget(d);
+#pragma unroll
+    for (int i = half + 1; i >= half; --i) {
+      if (!c.ordinary && q.last(i)) load_state(r.dh_last, q.seq[i], r.channels, ch, b);
+      const bool dead = !c.ordinary && q.dead(i);
+      float out[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const Terms t = decay_terms<T, DECAY>(g[i][e]);
-        H[e] = fmaf(t.a, H[e], drive_of<DRIVE>(t, x[i][e]));
-        A[e] *= t.a;
-        S[e] = fmaf(A[e], d[i][e], S[e]);  // a_0 .. a_i dh_i
+        const float rt = dead ? 0.0f : d[i][e] + b[e];
+        b[e] = rt;
+        out[e] = dead ? 0.0f : rt * w[i - half][e] * t.slope;
       }
-    join(0, 0);
-    forget(g);
-    forget(x);
-    forget(d);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) ahead(i);
-    forget(g);
-#pragma unroll
-    for (int i = kRows - 1; i >= 0; --i) {
-      float du[VEC], dv[VEC];
-      behind(i, false, du, dv);
-      store_row<true, T, VEC>(r, q, i, r.dx, r.dx_batch, r.dx_step, ch, du);
-      store_row<true, T, VEC>(r, q, i, r.dgate, r.dgate_batch, r.dgate_step, ch, dv);
-    }
-    if (c.head && seg == 0) store_state(r.dh0, c.seq, r.channels, ch, b);
-  } else {
-    const Rows q = special_rows(r, axis, c, seg);
-    load_rows<false>(r, q, r.gate, r.gate_batch, r.gate_step, ch, g);
-    load_rows<false>(r, q, r.x, r.x_batch, r.x_step, ch, x);
-    load_rows<false>(r, q, r.dh, r.dh_batch, r.dh_step, ch, d);
-    bool closed = false;  // a later row's gradient no longer reaches the segment's first
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const bool dead = q.dead >> i & 1u, start = q.start >> i & 1u, last = q.last >> i & 1u;
-      closed |= dead;
-      float h0[VEC] = {}, dl[VEC] = {};
-      if (start) load_state(r.h0, q.seq[i], r.channels, ch, h0);
-      if (last) load_state(r.dh_last, q.seq[i], r.channels, ch, dl);
+      store_row<T, VEC>(r, axis, c, q, i, r.dgate, r.dgate_batch, r.dgate_step, ch, out);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const Terms t = decay_terms<T, DECAY>(g[i][e]);
-        const float before = start ? h0[e] : H[e];
-        H[e] = dead ? 0.0f : fmaf(t.a, before, drive_of<DRIVE>(t, x[i][e]));
-        A[e] *= t.a;
-        if (!closed) S[e] = fmaf(A[e], d[i][e] + dl[e], S[e]);
+        out[e] = DRIVE == FFTMV_DRIVE_COMPLEMENT && !dead ? b[e] * t.rest : b[e];
+        b[e] = dead ? 0.0f : b[e] * t.a;
       }
-      closed |= last;
-    }
-    join(q.start | q.dead, q.last | q.dead);
-    forget(g);
-    forget(x);
-    forget(d);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (q.start >> i & 1u) load_state(r.h0, q.seq[i], r.channels, ch, h);
-      ahead(i);
-    }
-    forget(g);
-#pragma unroll
-    for (int i = kRows - 1; i >= 0; --i) {
-      if (q.last >> i & 1u) load_state(r.dh_last, q.seq[i], r.channels, ch, b);
-      float du[VEC], dv[VEC];
-      behind(i, q.dead >> i & 1u, du, dv);
-      store_row<false, T, VEC>(r, q, i, r.dx, r.dx_batch, r.dx_step, ch, du);
-      store_row<false, T, VEC>(r, q, i, r.dgate, r.dgate_batch, r.dgate_step, ch, dv);
-      if (q.start >> i & 1u) store_state(r.dh0, q.seq[i], r.channels, ch, b);
-      if (q.empty >> i & 1u) {
-        float dl[VEC];
-        load_state(r.dh_last, q.seq[i], r.channels, ch, dl);
-        store_state(r.dh0, q.seq[i], r.channels, ch, dl);
+      store_row<T, VEC>(r, axis, c, q, i, r.dx, r.dx_batch, r.dx_step, ch, out);
+      if (!c.ordinary) {
+        if (q.start(i)) store_state(r.dh0, q.seq[i], r.channels, ch, b);
+        if (q.empty(i)) {
+          float dl[VEC];
+          load_state(r.dh_last, q.seq[i], r.channels, ch, dl);
+          store_state(r.dh0, q.seq[i], r.channels, ch, dl);
+        }
       }
+      row_done();
     }
   }
+  // an ordinary chunk at the front of its sequence
+  if (c.ordinary && c.head && seg == 0) store_state(r.dh0, c.seq, r.channels, ch, b);
   if ((r.offsets || r.steps == 0) && c.place == 0) pass_empty<VEC>(r, seg, ch, r.dh_last, r.dh0);
-  if (axis.joined()) {
-    if (tid == 0) lds.order = left;
-    __syncthreads();
-    if (lds.order == static_cast<uint32_t>(axis.places - 1)) clear_chain<W>(s, axis.places);
-  }
 }
 
 template <typename T, int VEC>
@@ -267,11 +256,12 @@ hipError_t launch_recurrence_backward_vec(const fftmv_recurrence_t &r, hipStream
   });
 }
 
-// As the forward: rows shorter than one vector take one channel a lane.
+// Four channels a lane in every type: three inputs of eight 16-bit ones would
+// not fit the registers of two workgroups a CU. Rows shorter than that take
+// one channel a lane.
 template <typename T>
 hipError_t launch_recurrence_backward_as(const fftmv_recurrence_t &r, hipStream_t s) {
-  return r.channels >= kVec<T> ? launch_recurrence_backward_vec<T, kVec<T>>(r, s)
-                               : launch_recurrence_backward_vec<T, 1>(r, s);
+  return r.channels >= 4 ? launch_recurrence_backward_vec<T, 4>(r, s) : launch_recurrence_backward_vec<T, 1>(r, s);
 }
 
 }  // namespace fftmv

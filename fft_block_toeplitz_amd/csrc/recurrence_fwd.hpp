@@ -12,14 +12,14 @@ struct ForwardLds {
   float gA[G][W], gH[G][W];               // maps of the groups
   float enter[W];                         // the state that enters the chunk
   __align__(8) uint8_t bits[kWaves];
-  uint32_t ticket, order;
+  uint32_t ticket;
 };
 
 // The chunk's join: from the segments' maps in lds.A, lds.H (written, not yet
 // synchronised) to the state that enters each segment, in lds.H.
 template <int W, int VEC>
 __device__ __forceinline__ void forward_join(const fftmv_recurrence_t &r, const ScanAxis &axis, const Chunk &c,
-                                             const ScanChain &s, int64_t block, uint32_t early,
+                                             const ScanChain &s, int block, uint64_t early,
                                              ForwardLds<W> &lds) {
   constexpr int G = ForwardLds<W>::G, SG = kSegs / G;
   constexpr uint32_t kGroup = ~0u >> (32 - SG);
@@ -29,20 +29,19 @@ __device__ __forceinline__ void forward_join(const fftmv_recurrence_t &r, const 
   const uint32_t constants = read_segment_bits(lds.bits);
 
   // maps of groups of segments: one thread per column and group
-  float mA[SG], mH[SG], cA = 1.0f, cH = 0.0f;
+  float cA = 1.0f, cH = 0.0f;
 #pragma unroll
   for (int i = 0; i < SG; ++i) {
-    mA[i] = lds.A[grp * SG + i][col];
-    mH[i] = lds.H[grp * SG + i][col];
-    cH = through(constants >> (grp * SG + i) & 1u, mA[i], mH[i], cH);
-    cA *= mA[i];
+    const float A = lds.A[grp * SG + i][col];
+    cH = through(constants >> (grp * SG + i) & 1u, A, lds.H[grp * SG + i][col], cH);
+    cA *= A;
   }
   lds.gA[grp][col] = cA;
   lds.gH[grp][col] = cH;
   __syncthreads();
 
   if (tid < W) {  // the state that enters the chunk
-    const int64_t ch = column_channel<VEC>(r.channels, block * W + col);
+    const int64_t ch = column_channel<VEC>(r.channels, static_cast<int64_t>(block) * W + col);
     float in = 0.0f;
     // an ordinary chunk at the front of its sequence; a special one has it in a segment's map
     const bool first = c.ordinary && c.head;
@@ -57,7 +56,7 @@ __device__ __forceinline__ void forward_join(const fftmv_recurrence_t &r, const 
       if (first) H = fmaf(A, in, H);
       const float from = meet_chain<W>(s, c.place, col, A, H, first || constants, !c.head, early);
       if (!first) in = from;
-      if (r.carries) r.carries[(c.chain * axis.places + c.place) * r.channels + ch] = in;
+      if (r.carries) r.carries[(static_cast<int64_t>(c.chain) * axis.places + c.place) * r.channels + ch] = in;
     }
     lds.enter[col] = in;
   }
@@ -67,8 +66,10 @@ __device__ __forceinline__ void forward_join(const fftmv_recurrence_t &r, const 
   for (int j = 0; j < grp; ++j) h = through(constants >> (j * SG) & kGroup, lds.gA[j][col], lds.gH[j][col], h);
 #pragma unroll
   for (int i = 0; i < SG; ++i) {
-    lds.H[grp * SG + i][col] = h;
-    h = through(constants >> (grp * SG + i) & 1u, mA[i], mH[i], h);
+    float &H = lds.H[grp * SG + i][col];
+    const float next = through(constants >> (grp * SG + i) & 1u, lds.A[grp * SG + i][col], H, h);
+    H = h;
+    h = next;
   }
   __syncthreads();
 }
@@ -78,124 +79,92 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_forward_kernel(fftmv_r
   constexpr int W = kLanes * VEC;  // columns of the workgroup
   __shared__ ForwardLds<W> lds;
   const int tid = threadIdx.x, seg = tid / kLanes, lane = tid % kLanes;
-  const int64_t chains = axis.chains * axis.blocks, chain = blockIdx.x % chains;
-  const int64_t block = chain % axis.blocks;
-  const int64_t ch = column_channel<VEC>(r.channels, block * W + lane * VEC);
-  const ScanChain s = scan_chain<W>(r.workspace, axis, chain);
+  // chains of all blocks of channels: block by block of one sequence, then the next
+  const uint32_t chains = static_cast<uint32_t>(axis.chains) * axis.blocks, chain = blockIdx.x % chains;
+  const int block = chain % static_cast<uint32_t>(axis.blocks), over_batch = chain / static_cast<uint32_t>(axis.blocks);
+  const int64_t ch = column_channel<VEC>(r.channels, static_cast<int64_t>(block) * W + lane * VEC);
+  const ScanChain s = scan_chain<W>(r, axis, chain);
 
-  // Loads for the place that blockIdx suggests while the ticket is drawn;
-  // once more in the rare case that it says another.
-  Chunk c = chunk_at(r, axis, chain / axis.blocks, blockIdx.x / chains);
+  // Loads for the place that blockIdx suggests while the ticket is drawn; a
+  // second time in the rare case that it says another.
+  int place = blockIdx.x / chains;
   uint32_t ticket = 0;
-  if (axis.joined() && tid == 0) ticket = draw_place(s);
+  bool drawn = !axis.joined();
+  if (!drawn && tid == 0) ticket = draw_place(s);
+  Chunk c;
+  Rows q;
   Vec<T, VEC> x[kRows], g[kRows];
-  auto load = [&]() {
-    const Rows q = ordinary_rows(r, c, seg);
-    load_rows<true>(r, q, r.gate, r.gate_batch, r.gate_step, ch, g);
-    load_rows<true>(r, q, r.x, r.x_batch, r.x_step, ch, x);
-  };
-  if (c.ordinary) load();
-  uint32_t early = 0;
-  if (axis.joined()) {
-    if (tid == 0) lds.ticket = ticket;
+  for (;;) {
+    c = chunk_at(r, axis, over_batch, place);
+    q = rows_of(r, axis, c, seg);
+    load_rows(r, axis, c, q, r.gate, r.gate_batch, r.gate_step, ch, g);
+    load_rows(r, axis, c, q, r.x, r.x_batch, r.x_step, ch, x);
+    if (drawn) break;
+    drawn = true;
+    if (tid == 0) lds.ticket = settle_ticket(s, ticket, axis.places);
     __syncthreads();
-    const int64_t place = __builtin_amdgcn_readfirstlane(lds.ticket);
-    if (place >= axis.places) return;  // a workspace that was not zero
-    if (place != c.place) {
-      c = chunk_at(r, axis, c.chain, place);
-      if (c.ordinary) load();
-    }
-    if (!c.head && tid < W) early = peek_state(s, (place - 1) * W + tid);
+    const uint32_t t = __builtin_amdgcn_readfirstlane(lds.ticket);
+    if (t >= static_cast<uint32_t>(axis.places)) return;  // a workspace or number that the call may not have
+    if (t == static_cast<uint32_t>(place)) break;
+    place = static_cast<int>(t);
   }
+  uint64_t early = 0;
+  if (axis.joined() && !c.head && tid < W) early = peek<W>(s, place - 1, 2, tid);
 
-  float A[VEC], H[VEC], h[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) A[e] = 1.0f, H[e] = 0.0f;
-  uint32_t order = 0;
-  auto to_lds = [&](uint32_t reset) {
+  // one row: v becomes its state
+  auto step = [&](int i, float (&v)[VEC]) {
+    if (!c.ordinary && q.start(i)) load_state(r.h0, q.seq[i], r.channels, ch, v);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      lds.A[seg][lane * VEC + e] = A[e];
-      lds.H[seg][lane * VEC + e] = H[e];
+      const Terms t = decay_terms<T, DECAY>(g[i][e]);
+      v[e] = fmaf(t.a, v[e], drive_of<DRIVE>(t, x[i][e]));
     }
-    const uint64_t b = __ballot(reset != 0);
-    if (tid % kWave == 0) lds.bits[tid / kWave] = segment_bits(b);
-    forward_join<W, VEC>(r, axis, c, s, block, early, lds);
-    if (axis.joined() && tid == 0) order = leave_chain(s);
+    if (!c.ordinary && q.dead(i)) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) h[e] = lds.H[seg][lane * VEC + e];
-  };
-  // 16-bit inputs are held through the join as they are and their terms
-  // computed twice; FP32 ones as the terms, which take no more room.
-  constexpr bool kAgain = sizeof(T) == 2;
-  auto again = [&]() {
-    if constexpr (kAgain) {
-      forget(g);
-      forget(x);
+      for (int e = 0; e < VEC; ++e) v[e] = 0.0f;
     }
   };
-  auto step = [&](int i, int e, float before) {
-    const Terms t = decay_terms<T, DECAY>(g[i][e]);
-    return fmaf(t.a, before, drive_of<DRIVE>(t, x[i][e]));
-  };
-  if (c.ordinary) {
-    const Rows q = ordinary_rows(r, c, seg);
+
+  float A[VEC], h[VEC];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+  for (int e = 0; e < VEC; ++e) A[e] = 1.0f, h[e] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        H[e] = step(i, e, H[e]);
-        A[e] *= decay_terms<T, DECAY>(g[i][e]).a;
-      }
-      row_done();
-    }
-    to_lds(0);
-    again();
+  for (int i = 0; i < kRows; ++i) {
+    step(i, h);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
+    for (int e = 0; e < VEC; ++e) A[e] *= decay_terms<T, DECAY>(g[i][e]).a;
+    row_done();
+  }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) h[e] = step(i, e, h[e]);
-      store_row<true, T, VEC>(r, q, i, r.h, r.h_batch, r.h_step, ch, h);
-      row_done();
-    }
-  } else {
-    const Rows q = special_rows(r, axis, c, seg);
-    load_rows<false>(r, q, r.gate, r.gate_batch, r.gate_step, ch, g);
-    load_rows<false>(r, q, r.x, r.x_batch, r.x_step, ch, x);
-    auto special_step = [&](int i, float (&v)[VEC]) {
-      if (q.start >> i & 1u) load_state(r.h0, q.seq[i], r.channels, ch, v);
-      const bool dead = q.dead >> i & 1u;
+  for (int e = 0; e < VEC; ++e) {
+    lds.A[seg][lane * VEC + e] = A[e];
+    lds.H[seg][lane * VEC + e] = h[e];
+  }
+  const uint64_t front = __ballot(q.closed_front());
+  if (tid % kWave == 0) lds.bits[tid / kWave] = segment_bits(front);
+  forward_join<W, VEC>(r, axis, c, s, block, early, lds);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = dead ? 0.0f : step(i, e, v[e]);
-    };
+  for (int e = 0; e < VEC; ++e) h[e] = lds.H[seg][lane * VEC + e];
+
+  // The rows once more, now from the state that enters them: the inputs are
+  // held through the join as they came, and their terms computed again.
+  forget(g);
+  forget(x);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      special_step(i, H);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) A[e] *= decay_terms<T, DECAY>(g[i][e]).a;
-      row_done();
-    }
-    to_lds(q.start | q.dead);
-    again();
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      special_step(i, h);
-      store_row<false, T, VEC>(r, q, i, r.h, r.h_batch, r.h_step, ch, h);
-      if (q.last >> i & 1u) store_state(r.h_last, q.seq[i], r.channels, ch, h);
-      if (q.empty >> i & 1u) {
+  for (int i = 0; i < kRows; ++i) {
+    step(i, h);
+    store_row<T, VEC>(r, axis, c, q, i, r.h, r.h_batch, r.h_step, ch, h);
+    if (!c.ordinary) {
+      if (q.last(i)) store_state(r.h_last, q.seq[i], r.channels, ch, h);
+      if (q.empty(i)) {
         float h0[VEC];
         load_state(r.h0, q.seq[i], r.channels, ch, h0);
         store_state(r.h_last, q.seq[i], r.channels, ch, h0);
       }
-      row_done();
     }
+    row_done();
   }
   if ((r.offsets || r.steps == 0) && c.place == 0) pass_empty<VEC>(r, seg, ch, r.h0, r.h_last);
-  if (axis.joined()) {
-    if (tid == 0) lds.order = order;
-    __syncthreads();
-    if (lds.order == static_cast<uint32_t>(axis.places - 1)) clear_chain<W>(s, axis.places);
-  }
 }
 
 template <typename T, int VEC>

@@ -45,7 +45,7 @@ bool strides_ok(int64_t n, int64_t stride, int64_t m, int64_t step, int64_t chan
 
 int check_recurrence(const fftmv_recurrence_t *r, bool backward) {
   if (!r || r->batch < 1 || r->steps < 0 || r->channels < 1) return FFTMV_ERR_INVALID_ARG;
-  if (!types_ok(r->dtype, r->decay, r->drive, r->reserved)) return FFTMV_ERR_INVALID_ARG;
+  if (!types_ok(r->dtype, r->decay, r->drive, 0)) return FFTMV_ERR_INVALID_ARG;
   if (r->lengths && r->offsets) return FFTMV_ERR_INVALID_ARG;
   if (!aligned(r->lengths, 4) || !aligned(r->offsets, 4)) return FFTMV_ERR_INVALID_ARG;
   const int64_t rows = rows_of(r->batch, r->steps, r->offsets != nullptr);
@@ -67,12 +67,14 @@ int check_recurrence(const fftmv_recurrence_t *r, bool backward) {
   }
   if (!floats(r->h0) || !floats(r->h_last) || !floats(r->carries) || !floats(r->dh_last) || !floats(r->dh0))
     return FFTMV_ERR_INVALID_ARG;
-  size_t need = 0;
   int64_t carries = 0;
-  const int st = fftmv_recurrence_sizes(r->batch, T, C, r->offsets != nullptr, &carries, &need);
+  size_t counters = 0, words = 0;
+  const int st = fftmv_recurrence_sizes(r->batch, T, C, r->offsets != nullptr, &carries, &counters, &words);
   if (st != FFTMV_SUCCESS) return st;
   if (backward && carries && !r->carries) return FFTMV_ERR_INVALID_ARG;
-  if (need && (!r->workspace || !aligned(r->workspace, 8) || r->workspace_bytes < need)) return FFTMV_ERR_INVALID_ARG;
+  if (words && (!r->workspace || !r->counters || !aligned(r->workspace, 8) || !aligned(r->counters, 8) ||
+                r->workspace_bytes < words || r->counter_bytes < counters || r->call == 0))
+    return FFTMV_ERR_INVALID_ARG;
   return FFTMV_SUCCESS;
 }
 
@@ -110,11 +112,13 @@ int check_group_norm(const fftmv_group_norm_t *g, bool backward) {
 extern "C" {
 
 int fftmv_recurrence_sizes(int64_t batch, int64_t steps, int64_t channels, int packed, int64_t *carries,
-                           size_t *bytes) {
+                           size_t *counter_bytes, size_t *workspace_bytes) {
   if (batch < 1 || steps < 0 || channels < 1) return FFTMV_ERR_INVALID_ARG;
   if (rows_of(batch, steps, packed != 0) < 0 || channels > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
+  const ScanWorkspace w = scan_workspace_bytes(batch, steps, packed != 0, channels);
   if (carries) *carries = scan_carries(batch, steps, packed != 0);
-  if (bytes) *bytes = scan_workspace_bytes(batch, steps, packed != 0, channels);
+  if (counter_bytes) *counter_bytes = w.counters;
+  if (workspace_bytes) *workspace_bytes = w.words;
   return FFTMV_SUCCESS;
 }
 

@@ -29,6 +29,16 @@ using f16 = _Float16;
 // gfx950 takes 16-byte global accesses at any alignment, so odd channel
 // counts and strides keep the wide loads.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+// VEC elements as words, for the widths that one access moves whole
+template <int BYTES>
+struct Words {
+  using type = u32x4_any;
+};
+template <>
+struct Words<8> {
+  using type = u32x2_any;
+};
 
 template <typename T, int VEC>
 struct Vec {
@@ -41,8 +51,8 @@ constexpr int kVec = 16 / sizeof(T);
 
 template <typename T, int VEC>
 __device__ __forceinline__ Vec<T, VEC> load_vec(const T *p) {
-  if constexpr (VEC == kVec<T>) {
-    return __builtin_bit_cast(Vec<T, VEC>, *reinterpret_cast<const u32x4_any *>(p));
+  if constexpr (VEC * sizeof(T) >= 8) {
+    return __builtin_bit_cast(Vec<T, VEC>, *reinterpret_cast<const typename Words<VEC * sizeof(T)>::type *>(p));
   } else {
     Vec<T, VEC> r;
 #pragma unroll
@@ -55,10 +65,11 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
   Vec<T, VEC> r;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) r.v[e] = static_cast<T>(f[e]);
-  if constexpr (VEC == kVec<T>) {
+  if constexpr (VEC * sizeof(T) >= 8) {
     // streamed past the caches: no kernel here reads its own output, and the
     // inputs' lines that two blocks of channels share stay longer
-    __builtin_nontemporal_store(__builtin_bit_cast(u32x4_any, r), reinterpret_cast<u32x4_any *>(p));
+    using W = typename Words<VEC * sizeof(T)>::type;
+    __builtin_nontemporal_store(__builtin_bit_cast(W, r), reinterpret_cast<W *>(p));
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) p[e] = r.v[e];

@@ -36,11 +36,12 @@ def _fields(text, kind):
 
 
 class _Recurrence(ctypes.Structure):  # fftmv_recurrence_t
-    _fields_ = (_fields("batch steps channels", _I64) + _fields("dtype decay drive reserved", _I32)
-                + _fields("lengths offsets", _P)
+    _fields_ = (_fields("batch steps channels", _I64) + _fields("dtype decay drive", _I32)
+                + [("call", ctypes.c_uint32)] + _fields("lengths offsets", _P)
                 + [("x", _P), ("x_batch", _I64), ("x_step", _I64)]
                 + [("gate", _P), ("gate_batch", _I64), ("gate_step", _I64)]
-                + _fields("h0 carries workspace", _P) + [("workspace_bytes", _Z)]
+                + _fields("h0 carries", _P)
+                + [("counters", _P), ("counter_bytes", _Z), ("workspace", _P), ("workspace_bytes", _Z)]
                 + [("h", _P), ("h_batch", _I64), ("h_step", _I64), ("h_last", _P)]
                 + [("dh", _P), ("dh_batch", _I64), ("dh_step", _I64), ("dh_last", _P)]
                 + [("dx", _P), ("dx_batch", _I64), ("dx_step", _I64)]
@@ -73,7 +74,7 @@ def _lib():
     if _bound is None:
         L = lib()
         Z = ctypes.POINTER(_Z)
-        L.fftmv_recurrence_sizes.argtypes = [_I64, _I64, _I64, ctypes.c_int, ctypes.POINTER(_I64), Z]
+        L.fftmv_recurrence_sizes.argtypes = [_I64, _I64, _I64, ctypes.c_int, ctypes.POINTER(_I64), Z, Z]
         L.fftmv_group_norm_workspace.argtypes = [_I64, _I64, _I64, _I64, Z]
         for name, kind in (("recurrence_forward", _Recurrence), ("recurrence_backward", _Recurrence),
                            ("recurrence_step", _Step), ("group_norm_forward", _GroupNorm),
@@ -88,12 +89,12 @@ def _check(status, what):
         raise FftmvError(status, what)
 
 
-def fftmv_recurrence_sizes(batch: int, steps: int, channels: int, packed: bool) -> tuple[int, int]:
-    """(rows of carries, bytes of workspace) of a forward or backward call."""
-    c, n = _I64(), _Z()
-    _check(_lib().fftmv_recurrence_sizes(batch, steps, channels, packed, ctypes.byref(c), ctypes.byref(n)),
-           "fftmv_recurrence_sizes")
-    return c.value, n.value
+def fftmv_recurrence_sizes(batch: int, steps: int, channels: int, packed: bool) -> tuple[int, int, int]:
+    """(rows of carries, bytes of counters, bytes of workspace) of a forward or backward call."""
+    c, n, m = _I64(), _Z(), _Z()
+    _check(_lib().fftmv_recurrence_sizes(batch, steps, channels, packed, ctypes.byref(c), ctypes.byref(n),
+                                         ctypes.byref(m)), "fftmv_recurrence_sizes")
+    return c.value, n.value, m.value
 
 
 def fftmv_recurrence_forward(r: _Recurrence, stream: int = 0) -> None:
@@ -242,21 +243,30 @@ _workspaces = {}
 _sizes = functools.lru_cache(maxsize=1024)(fftmv_recurrence_sizes)  # a function of the shape alone
 
 
-def _workspace(nbytes, stream, like):
-    """Zeroed workspace of the recurrence. Every call leaves it zero, so one
-    per stream is kept and grown; a call under graph capture gets memory of
-    the graph's own, cleared inside the graph."""
+def _workspace(sizes, stream, like):
+    """(counters' address and bytes, workspace's address and bytes, number of
+    the call on it). Calls of one stream share a workspace, which is kept and
+    grown; a call under graph capture gets memory of the graph's own, cleared
+    inside the graph."""
     import torch
 
-    if nbytes == 0:
-        return None
+    _, few, many = sizes
+    if many == 0:
+        return None, 0, None, 0, 0
+    new = lambda n: torch.zeros(n, dtype=torch.uint8, device=like.device)  # noqa: E731
     if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=like.device)
-    key = (like.device.index, stream)
-    w = _workspaces.get(key)
-    if w is None or w.numel() < nbytes:
-        w = _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=like.device)
-    return w
+        w = [new(few), new(many), 0]
+    else:
+        w = _workspaces.get((like.get_device(), stream))
+        if w is None or w[0].numel() < few or w[1].numel() < many:
+            if w is not None:
+                few, many = max(few, w[0].numel()), max(many, w[1].numel())
+            w = _workspaces[like.get_device(), stream] = [new(few), new(many), 0]
+        elif w[2] == 2 ** 32 - 1:
+            w[1].zero_()
+            w[2] = 0
+    w[2] += 1
+    return w[0].data_ptr(), w[0].numel(), w[1].data_ptr(), w[1].numel(), w[2]
 
 
 def _sequences(x, lengths, offsets):
@@ -311,11 +321,11 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
             if T:
                 h.zero_()
             return (h, last, torch.empty((0, C), device=x.device)) if save else (h, last)
-        n, need = _sizes(B, T, C, offsets is not None)
-        carries = torch.empty((n, C), dtype=torch.float32, device=x.device) if save else None
-        ws = _workspace(need, s, x)
-        r = _Recurrence(B, T, C, dtype, *kinds, 0, lens, offs, *xf, *gf, h0p, carries.data_ptr() if save else None,
-                        ws.data_ptr() if need else None, need, *_field(h, x, "out"), last.data_ptr())
+        sizes = _sizes(B, T, C, offsets is not None)
+        carries = torch.empty((sizes[0], C), dtype=torch.float32, device=x.device) if save else None
+        *ws, call = _workspace(sizes, s, x)
+        r = _Recurrence(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, carries.data_ptr() if save else None,
+                        *ws, *_field(h, x, "out"), last.data_ptr())
         fftmv_recurrence_forward(r, s)
     return (h, last, carries) if save else (h, last)
 
@@ -333,10 +343,10 @@ def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="s
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
     xf, gf, df = _field(x, x, "x"), _field(gate, x, "gate"), _field(dh, x, "dh")
     h0p, lp = _floats(h0, (B, C), x, "h0"), _floats(dh_last, (B, C), x, "dh_last")
-    n, need = _sizes(B, T, C, offsets is not None) if B else (0, 0)
+    sizes = _sizes(B, T, C, offsets is not None) if B else (0, 0, 0)
     if carries is None:
         raise ValueError("carries must be what recurrence(..., save=True) returned")
-    cp = _floats(carries, (n, C), x, "carries")
+    cp = _floats(carries, (sizes[0], C), x, "carries")
     lens, offs = _ints(lengths, B, x, "lengths"), _ints(offsets, B + 1, x, "offsets")
     with _On(stream, dh, x, gate, carries, h0, dh_last, lengths, offsets) as s:
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -346,8 +356,8 @@ def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="s
             if T:
                 dx.zero_(), dg.zero_()
             return dx, dg, dh0
-        ws = _workspace(need, s, x)
-        r = _Recurrence(B, T, C, dtype, *kinds, 0, lens, offs, *xf, *gf, h0p, cp, ws.data_ptr() if need else None, need,
+        *ws, call = _workspace(sizes, s, x)
+        r = _Recurrence(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, cp, *ws,
                         None, 0, 0, None, *df, lp, *_field(dx, x, "dx"), *_field(dg, x, "dgate"), dh0.data_ptr())
         fftmv_recurrence_backward(r, s)
     return dx, dg, dh0

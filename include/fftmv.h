@@ -348,8 +348,13 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  *   dh0      a_0 r_0 (dh_last for an empty sequence); may be NULL
  * with h recomputed in FP32 from carries, not read back rounded.
  *
- * workspace: as many bytes as fftmv_recurrence_sizes says, 8-byte aligned,
- * zero before the first call; each call leaves it zero again. Calls that share one must
+ * counters, workspace: as many bytes as fftmv_recurrence_sizes says, 8-byte
+ * aligned, both zero before their first call and then left alone between
+ * calls of any shape. `call` numbers the calls that use one workspace: 1, 2,
+ * 3, ... (forward and backward alike; ascending, gaps are allowed); after
+ * 2^32 - 1 clear it and start again. What is captured in a graph clears its
+ * workspace in front of the captured calls, since replays repeat their
+ * numbers. Calls that share one must
  * be ordered. h0 NULL stands for zeros. A state that is not finite stays
  * not finite (infinity or NaN) until its sequence ends; it reaches no other
  * sequence or channel.
@@ -360,7 +365,8 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
 #define FFTMV_RECURRENCE_CHUNK 128
 typedef struct fftmv_recurrence_s {
   int64_t batch, steps, channels;
-  int32_t dtype, decay, drive, reserved; /* reserved: 0 */
+  int32_t dtype, decay, drive;
+  uint32_t call; /* number of the call on this workspace, from 1 */
   const int32_t *lengths, *offsets;
   const void *x;
   int64_t x_batch, x_step;
@@ -368,6 +374,8 @@ typedef struct fftmv_recurrence_s {
   int64_t gate_batch, gate_step;
   const float *h0;
   float *carries;
+  void *counters;
+  size_t counter_bytes;
   void *workspace;
   size_t workspace_bytes;
   /* forward */
@@ -386,10 +394,10 @@ typedef struct fftmv_recurrence_s {
 } fftmv_recurrence_t;
 
 /* For a forward or backward call of this shape (packed: it has offsets): how
- * many rows `carries` has (0: none are used) and how many bytes the workspace
- * needs (0: none). Either output may be NULL. */
+ * many rows `carries` has (0: none are used) and how many bytes the counters
+ * and the workspace need (0: none). Any output may be NULL. */
 FFTMV_API int fftmv_recurrence_sizes(int64_t batch, int64_t steps, int64_t channels, int packed, int64_t *carries,
-                                     size_t *workspace_bytes);
+                                     size_t *counter_bytes, size_t *workspace_bytes);
 FFTMV_API int fftmv_recurrence_forward(const fftmv_recurrence_t *r, hipStream_t stream);
 FFTMV_API int fftmv_recurrence_backward(const fftmv_recurrence_t *r, hipStream_t stream);
 

@@ -136,6 +136,25 @@ def test_recurrence_packed(fm, dtype, C, cuts, T):
                      spans=list(zip(cuts[:-1], cuts[1:])), packed=True)
 
 
+def test_recurrence_calls_of_all_shapes_share_a_workspace(fm):
+    """Calls whose counters lie where another shape's words were, in turn."""
+    shapes = [(1, 3000, 200), (9, 140, 64), (4, 300, 48), (1, 520, 1000), (40, 129, 8), (2, 5000, 16)]
+    want = {}
+    for turn in range(3):
+        for B, T, C in shapes if turn % 2 == 0 else shapes[::-1]:
+            for dtype in ("fp32", "bf16"):
+                x, g = fields(B + T, (B, T, C), dtype, "sigmoid")
+                h, last, carries = fm.recurrence(x, g, save=True)
+                grads = fm.recurrence_backward(x, x, g, carries)
+                got = [t.clone() for t in (h, last) + grads]
+                for a, b in zip(got, want.setdefault((B, T, C, dtype), got)):
+                    assert torch.equal(a, b)
+                if turn == 0:
+                    r = R.Recurrence(host(x)[0], host(g)[0], np.zeros(C), "sigmoid", "complement", dtype, host(x)[0])
+                    near(h[0], r.h, r.eh, "h")
+                    near(grads[0][0], r.dx, r.edx, "dx")
+
+
 def test_recurrence_no_steps(fm):
     h0 = torch.randn(3, 5, device="cuda")
     x = torch.empty(3, 0, 5, device="cuda")
