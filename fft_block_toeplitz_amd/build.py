@@ -14,7 +14,9 @@ SOURCES = [os.path.join(HERE, "csrc", f)
                      "fft_generic_inv_blue.hip", "fft_fixed_fwd.hip", "fft_fixed_inv.hip", "fft_setup.hip", "sbgemv.hip",
                      "padcast.hip", "condition.hip", "scratch.hip", "recurrence_fwd_f32.hip",
                      "recurrence_fwd_bf16.hip", "recurrence_fwd_f16.hip", "recurrence_bwd_f32.hip",
-                     "recurrence_bwd_bf16.hip", "recurrence_bwd_f16.hip", "recurrence_step.hip", "group_norm.hip",
+                     "recurrence_bwd_bf16.hip", "recurrence_bwd_f16.hip", "recurrence_step.hip",
+                     "group_norm_fwd_f32.hip", "group_norm_fwd_bf16.hip", "group_norm_fwd_f16.hip",
+                     "group_norm_bwd_f32.hip", "group_norm_bwd_bf16.hip", "group_norm_bwd_f16.hip", "group_norm.hip",
                      "plan.cpp", "precision.cpp", "sequence.cpp")]
 # measurement kernels of the benchmark (memory ceilings): a library of their own
 CEILING_SRC = os.path.join(HERE, "csrc", "ceiling.hip")
@@ -22,7 +24,7 @@ CEILING_LIB = os.path.join(HERE, "libfftmv_ceiling.so")
 HEADERS = [os.path.join(ROOT, "include", "fftmv.h")] + [
     os.path.join(HERE, "csrc", f) for f in ("common.hpp", "internal.hpp", "fft_device.hpp", "fft_fixed.hpp",
                                             "fft_generic.hpp", "sequence.hpp", "recurrence.hpp", "recurrence_fwd.hpp",
-                                            "recurrence_bwd.hpp")]
+                                            "recurrence_bwd.hpp", "group_norm.hpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,139 +1,141 @@
-// Group normalisation with an activation: one workgroup per sample and
-// group, three passes over its rows.
-#include "common.hpp"
-#include "internal.hpp"
-#include "sequence.hpp"
+// Group normalisation: which kernels a call takes, and the sums of the
+// parameters' gradients.
+#include "group_norm.hpp"
 
 namespace fftmv {
 namespace {
 
-// Sum over the workgroup, the same bits in every thread.
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float part[kBlock / kWave];
-  v = wave_sum(v);
-  __syncthreads();  // the last use of part is over
-  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
-  __syncthreads();
-  float s = part[0];
-  for (int i = 1; i < kBlock / kWave; ++i) s += part[i];
-  return s;
+__global__ __launch_bounds__(kBlock) void param_sums_kernel(fftmv_group_norm_t g, int64_t rows) {
+  __shared__ float lds[2 * kBlock];
+  param_sums(g, rows, blockIdx.x, lds);
 }
 
-__device__ __forceinline__ int64_t held_rows(const fftmv_group_norm_t &g, int64_t n) {
-  if (!g.lengths) return g.rows;
-  const int64_t l = g.lengths[n];
-  return l < 0 ? 0 : l > g.rows ? g.rows : l;
+int round64(int64_t n) { return static_cast<int>((n + 63) / 64 * 64); }
+
+// The widest slab of whole groups over at most `lanes` lanes of `vec`
+// channels, every slab at least one vector wide; 0 where there is none.
+int widest_slab(int D, int G, int vec, int lanes) {
+  constexpr int kMostGroups = 256;  // whose statistics lie in LDS
+  const int64_t fit = static_cast<int64_t>(lanes) * vec / D;
+  for (int gs = static_cast<int>(std::min<int64_t>({fit, G, kMostGroups})); gs >= 1; --gs)
+    if (static_cast<int64_t>(gs) * D >= vec && static_cast<int64_t>((G - 1) % gs + 1) * D >= vec) return gs;
+  return 0;
 }
 
-template <typename T, int ACT>
-__global__ __launch_bounds__(kBlock) void forward_kernel(fftmv_group_norm_t g) {
-  const int64_t n = blockIdx.x / g.groups, q = blockIdx.x % g.groups, D = g.channels / g.groups;
-  const int64_t held = held_rows(g, n), count = held * D;
-  const T *x = static_cast<const T *>(g.x) + n * g.x_sample + q * D;
-  T *y = static_cast<T *>(g.y) + n * g.y_sample + q * D;
-  float s = 0.0f;
-  for (int64_t i = threadIdx.x; i < count; i += kBlock) s += static_cast<float>(x[i / D * g.x_row + i % D]);
-  const float mean = count ? block_sum(s) / static_cast<float>(count) : 0.0f;
-  s = 0.0f;
-  for (int64_t i = threadIdx.x; i < count; i += kBlock) {
-    const float v = static_cast<float>(x[i / D * g.x_row + i % D]) - mean;
-    s += v * v;
-  }
-  const float rstd = count ? 1.0f / sqrtf(block_sum(s) / static_cast<float>(count) + g.eps) : 0.0f;
-  if (g.stats && threadIdx.x == 0) {
-    g.stats[2 * static_cast<int64_t>(blockIdx.x)] = mean;
-    g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1] = rstd;
-  }
-  for (int64_t i = threadIdx.x; i < g.rows * D; i += kBlock) {
-    float v = 0.0f;
-    if (i < count) {
-      const float w = g.weight ? g.weight[q * D + i % D] : 1.0f, b = g.bias ? g.bias[q * D + i % D] : 0.0f;
-      v = activate<ACT>((static_cast<float>(x[i / D * g.x_row + i % D]) - mean) * rstd * w + b);
-    }
-    y[i / D * g.y_row + i % D] = static_cast<T>(v);
-  }
+void take_slab(NormShape &s, int gs, int vec, int threads) {
+  s.gs = gs;
+  s.slabs = (s.G + gs - 1) / gs;
+  s.lx = (gs * s.D + vec - 1) / vec;
+  s.ty = threads / s.lx;
+  s.threads = threads;
 }
 
-template <typename T, int ACT>
-__global__ __launch_bounds__(kBlock) void backward_kernel(fftmv_group_norm_t g) {
-  const int64_t n = blockIdx.x / g.groups, q = blockIdx.x % g.groups, D = g.channels / g.groups;
-  const int64_t held = held_rows(g, n), count = held * D;
-  const T *x = static_cast<const T *>(g.x) + n * g.x_sample + q * D;
-  const T *dy = static_cast<const T *>(g.dy) + n * g.dy_sample + q * D;
-  T *dx = static_cast<T *>(g.dx) + n * g.dx_sample + q * D;
-  float *sums = static_cast<float *>(g.workspace) + 2 * (n * g.channels + q * D);
-  const float mean = g.stats[2 * static_cast<int64_t>(blockIdx.x)];
-  const float rstd = g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1];
-  float m1 = 0.0f, m2 = 0.0f;
-  for (int64_t c = 0; c < D; ++c) {
-    const float w = g.weight ? g.weight[q * D + c] : 1.0f, b = g.bias ? g.bias[q * D + c] : 0.0f;
-    float sb = 0.0f, sw = 0.0f;
-    for (int64_t t = threadIdx.x; t < held; t += kBlock) {
-      const float xh = (static_cast<float>(x[t * g.x_row + c]) - mean) * rstd;
-      const float dz = static_cast<float>(dy[t * g.dy_row + c]) * activate_slope<ACT>(xh * w + b);
-      sb += dz;
-      sw += dz * xh;
-    }
-    sb = block_sum(sb);
-    sw = block_sum(sw);
-    if (threadIdx.x == 0) sums[2 * c] = sb, sums[2 * c + 1] = sw;
-    m1 += sb * w;
-    m2 += sw * w;
-  }
-  m1 = count ? m1 / static_cast<float>(count) : 0.0f;
-  m2 = count ? m2 / static_cast<float>(count) : 0.0f;
-  for (int64_t i = threadIdx.x; i < g.rows * D; i += kBlock) {
-    float v = 0.0f;
-    const int64_t t = i / D, c = i % D;
-    if (t < held) {
-      const float w = g.weight ? g.weight[q * D + c] : 1.0f, b = g.bias ? g.bias[q * D + c] : 0.0f;
-      const float xh = (static_cast<float>(x[t * g.x_row + c]) - mean) * rstd;
-      const float dz = static_cast<float>(dy[t * g.dy_row + c]) * activate_slope<ACT>(xh * w + b);
-      v = rstd * (dz * w - m1 - xh * m2);
-    }
-    dx[t * g.dx_row + c] = static_cast<T>(v);
-  }
-}
-
-__global__ __launch_bounds__(kBlock) void parameter_sums_kernel(fftmv_group_norm_t g) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kBlock + threadIdx.x;
-  if (c >= g.channels) return;
-  const float *sums = static_cast<const float *>(g.workspace);
-  float sb = 0.0f, sw = 0.0f;
-  for (int64_t n = 0; n < g.samples; ++n) {
-    sb += sums[2 * (n * g.channels + c)];
-    sw += sums[2 * (n * g.channels + c) + 1];
-  }
-  if (g.dbias) g.dbias[c] = sb;
-  if (g.dweight) g.dweight[c] = sw;
-}
-
-template <typename F>
-hipError_t by_kind(const fftmv_group_norm_t &g, F f) {
-  return by_dtype(g.dtype, [&](auto t) { return by_three(g.activation, [&](auto a) { return f(t, a); }); });
+void take_team(NormShape &s, int sums) {
+  s.team = 64;
+  while (s.team > 1 && s.team * sums > s.threads) s.team /= 2;
 }
 
 }  // namespace
 
-hipError_t launch_group_norm_forward(const fftmv_group_norm_t &g, hipStream_t s) {
-  if (!grid_fits(g.samples * g.groups, kBlock)) return hipErrorInvalidConfiguration;
-  return by_kind(g, [&](auto t, auto a) {
-    forward_kernel<decltype(t), decltype(a)::value>
-        <<<static_cast<unsigned>(g.samples * g.groups), kBlock, 0, s>>>(g);
-    return hipGetLastError();
-  });
+hipError_t launch_param_sums(const fftmv_group_norm_t &g, int64_t rows, hipStream_t s) {
+  param_sums_kernel<<<static_cast<unsigned>((g.channels + kWave - 1) / kWave), kBlock, 0, s>>>(g, rows);
+  return hipGetLastError();
 }
 
-hipError_t launch_group_norm_backward(const fftmv_group_norm_t &g, hipStream_t s) {
-  if (!grid_fits(g.samples * g.groups, kBlock)) return hipErrorInvalidConfiguration;
-  hipError_t e = by_kind(g, [&](auto t, auto a) {
-    backward_kernel<decltype(t), decltype(a)::value>
-        <<<static_cast<unsigned>(g.samples * g.groups), kBlock, 0, s>>>(g);
-    return hipGetLastError();
-  });
-  if (e != hipSuccess) return e;
-  parameter_sums_kernel<<<static_cast<unsigned>((g.channels + kBlock - 1) / kBlock), kBlock, 0, s>>>(g);
-  return hipGetLastError();
+NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t groups, int dtype, bool backward) {
+  NormPlan p;
+  NormShape &s = p.s;
+  s.N = samples;
+  s.S = static_cast<int>(rows);
+  s.G = static_cast<int>(groups);
+  s.D = static_cast<int>(channels / groups);
+  const int es = dtype == FFTMV_F32 ? 4 : 2;
+  const int most = backward ? 512 : 1024;  // threads of a resident workgroup (backward: twice the sums in LDS)
+  p.vec = 16 / es;
+  if (widest_slab(s.D, s.G, p.vec, 1024) == 0) p.vec = 1;
+  const int v = p.vec, alone = static_cast<int>((static_cast<int64_t>(s.D) + v - 1) / v);  // lanes of one group
+  if (alone > 1024 || widest_slab(s.D, s.G, v, 1024) == 0) {
+    p.rows = samples;
+    p.workspace = backward ? static_cast<size_t>(samples * channels) * 8 : 0;
+    return p;
+  }
+  p.whole = s.D % v == 0;
+  const int64_t bytes = samples * std::max<int64_t>(rows, 1) * channels * es;
+  const int Q = backward ? 2 : 4;
+
+  // Single rows, or a few: Q samples at a time, side by side in a thread's
+  // registers, so that a barrier serves all of them; where that leaves too
+  // few workgroups for the CUs, the resident form below takes them one by one.
+  if (rows <= 8) {
+    const int R = std::max(1, s.S);
+    const int threads = alone * R <= 256 ? 256 : round64(static_cast<int64_t>(alone) * R);
+    if (threads <= (p.whole ? 512 : 256)) {
+      const int gs = widest_slab(s.D, s.G, v, threads / R);
+      if (gs > 0) {
+        take_slab(s, gs, v, threads);
+        s.threads = std::min(threads, round64(static_cast<int64_t>(s.lx) * R));
+        s.ty = std::min(s.threads / s.lx, R);
+        const int64_t turns = (samples + Q - 1) / Q;
+        if (s.ty >= R && turns * s.slabs >= 256) {
+          p.kind = NormPlan::kTokens;
+          s.across = static_cast<int>(std::min<int64_t>(turns, std::max(1, (backward ? 1024 : 2048) / s.slabs)));
+        }
+      }
+    }
+  }
+  // A sample's slab in registers, up to eight rows a thread.
+  if (p.kind == NormPlan::kWide) {
+    for (int threads = 256; threads <= most && p.kind == NormPlan::kWide; threads *= 2) {
+      for (int lanes = std::min(threads, 256); lanes >= 1; lanes /= 2) {
+        const int gs = widest_slab(s.D, s.G, v, std::max(lanes, alone));
+        if (gs == 0) continue;
+        take_slab(s, gs, v, threads);
+        if (s.lx > threads || s.S > 8 * s.ty) continue;
+        // rows of less than 64 bytes waste the lines that they touch
+        if (s.lx * v * es < 64 && s.slabs > 1) break;
+        // narrower while workgroups are few, down to 128 bytes a row
+        while (samples * s.slabs < 512 && s.gs > 1) {
+          const int half = widest_slab(s.D, s.G, v, s.lx / 2);
+          if (half == 0 || half * s.D * es < 128) break;
+          take_slab(s, half, v, threads);
+        }
+        s.ty = std::min(s.ty, std::max(1, s.S));
+        s.threads = std::min(threads, round64(static_cast<int64_t>(s.lx) * s.ty));
+        if (samples * s.slabs < 64 && bytes > (int64_t(2) << 20)) break;  // too few to fill the card: split
+        p.kind = NormPlan::kResident;
+        s.across = static_cast<int>(std::min<int64_t>(samples, std::max(1, (backward ? 1024 : 8192) / s.slabs)));
+        break;
+      }
+    }
+  }
+  if (p.kind != NormPlan::kWide) {
+    const int q = p.kind == NormPlan::kTokens ? Q : 1, sets = backward ? 2 * q : q;
+    take_team(s, sets * s.gs);
+    const size_t slots = static_cast<size_t>(s.ty) * s.lx * (p.whole ? 1 : v);
+    size_t floats = sets * slots + (backward ? 4 : 2) * static_cast<size_t>(q) * s.gs;
+    if (backward) floats = std::max(floats, static_cast<size_t>(s.ty) * s.lx * v);
+    p.lds = floats * 4;
+    p.rows = s.across;
+    p.workspace = backward && s.across > 1 ? static_cast<size_t>(s.across) * channels * 8 : 0;
+    return p;
+  }
+  // Split: ranges of rows over many workgroups.
+  p.kind = NormPlan::kSplit;
+  int gs = widest_slab(s.D, s.G, v, std::max(alone, 32));  // 512 bytes of a row, or one group
+  if (gs == 0) gs = widest_slab(s.D, s.G, v, 1024);
+  take_slab(s, gs, v, 256);
+  if (s.lx > 256) take_slab(s, s.gs, v, round64(s.lx));
+  take_team(s, s.gs);
+  const int64_t tile = 8 * static_cast<int64_t>(s.ty);
+  const int64_t want = std::max<int64_t>(1, 2048 / std::max<int64_t>(1, samples * s.slabs));
+  const int64_t tiles = std::max<int64_t>(1, (rows + tile - 1) / tile);
+  const int64_t per = (tiles + want - 1) / want;  // tiles of a range
+  s.range = static_cast<int>(std::min<int64_t>(per * tile, INT32_MAX));
+  s.across = static_cast<int>(std::max<int64_t>(1, (rows + s.range - 1) / s.range));
+  p.lds = (static_cast<size_t>(s.ty) * s.lx * v + s.gs) * 4;
+  p.rows = samples * s.across;
+  p.workspace = static_cast<size_t>(p.rows) * (backward ? channels + groups : groups) * 8;
+  return p;
 }
 
 }  // namespace fftmv

@@ -1,0 +1,899 @@
+// Group normalisation with an activation over channels-last fields.
+//
+// A workgroup takes a slab of whole groups, neighbouring channels that its
+// lanes read in 16-byte vectors, and spreads its rows over the rest of its
+// threads. What fits a workgroup's registers is read once ("resident": short
+// samples, single tokens); longer samples are read twice, once for the sums
+// and once to be written ("split": rows shared out over many workgroups).
+// The bound is memory traffic in all of them.
+//
+// A vector may cover channels of two groups (their width need not divide by
+// eight): then sums go through LDS per channel, otherwise per thread (WHOLE).
+// Variances are sums of squared deviations from the mean: deviations of
+// registers from the sample's mean (resident), or per tile from the tile's own
+// mean, joined by the pairwise formula (split); no difference of large sums.
+// Every sum runs in a fixed order.
+#pragma once
+
+#include <algorithm>
+
+#include "common.hpp"
+#include "internal.hpp"
+#include "sequence.hpp"
+
+namespace fftmv {
+
+constexpr int kNormThreads = 1024;  // at most
+
+// How a field is cut into slabs and workgroups.
+struct NormShape {
+  int64_t N;
+  int S, D, G;
+  int threads;      // of a workgroup
+  int gs, slabs;    // groups of a slab, slabs of a row
+  int lx, ty;       // lanes across a slab, rows side by side
+  int team;         // threads that sum one group (a power of two, at most a wave)
+  int across;       // workgroups over the samples of one slab (resident), or row ranges of a sample (split)
+  int range;        // split: rows of a range
+};
+
+__device__ __forceinline__ int held_rows(const fftmv_group_norm_t &g, int64_t n) {
+  const int S = static_cast<int>(g.rows);
+  if (!g.lengths) return S;
+  const int l = g.lengths[n];
+  return l < 0 ? 0 : l > S ? S : l;
+}
+
+// This thread's place in a slab.
+template <int VEC>
+struct SlabLane {
+  int ng, wd;     // groups and channels of this slab
+  int lane, row;  // row: first of its rows, ty apart
+  int c;          // first of its VEC channels, within the slab. The last lane steps back to end with the slab: the
+                  // channels that it repeats go to the same places with the same values
+  int64_t ch0;    // the slab's first channel
+  bool in;
+  __device__ SlabLane(const NormShape &s, int slab) {
+    ng = s.gs < s.G - slab * s.gs ? s.gs : s.G - slab * s.gs;
+    wd = ng * s.D;
+    ch0 = static_cast<int64_t>(slab) * s.gs * s.D;
+    lane = threadIdx.x % s.lx;
+    row = threadIdx.x / s.lx;
+    c = lane * VEC;
+    in = row < s.ty && c < wd;
+    if (c + VEC > wd) c = wd - VEC;
+  }
+};
+
+template <int VEC>
+__device__ __forceinline__ void load_params(const float *p, int64_t ch, float none, float (&v)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] = p ? p[ch + e] : none;
+}
+
+// Group of each of a thread's channels.
+template <int VEC, bool WHOLE>
+struct GroupOf {
+  int g[WHOLE ? 1 : VEC];
+  __device__ GroupOf(int c, int D) {
+    if constexpr (WHOLE) {
+      g[0] = c / D;
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[e] = (c + e) / D;
+    }
+  }
+  __device__ __forceinline__ int operator[](int e) const { return g[WHOLE ? 0 : e]; }
+};
+
+// A thread's contribution to the sums of its groups, in `part` (one row of
+// slots for each of the ty rows): one slot a thread, or one a channel.
+template <int VEC, bool WHOLE>
+__device__ __forceinline__ void put_part(float *part, const NormShape &s, const SlabLane<VEC> &l, const float (&v)[VEC]) {
+  if (!l.in) return;
+  if constexpr (WHOLE) {
+    float sum = v[0];
+#pragma unroll
+    for (int e = 1; e < VEC; ++e) sum += v[e];
+    part[l.row * s.lx + l.lane] = sum;
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) part[l.row * (s.lx * VEC) + l.c + e] = v[e];
+  }
+}
+template <int VEC, bool WHOLE>
+__device__ __forceinline__ int part_slots(const NormShape &s) {
+  return s.ty * s.lx * (WHOLE ? 1 : VEC);
+}
+
+// Sums of `sets` x ng groups: f(set * ng + group, sum) by one thread each. The
+// slots of set k start at part + k * slots. All of a workgroup's threads call it.
+template <int VEC, bool WHOLE, typename F>
+__device__ __forceinline__ void team_sums(const float *part, const NormShape &s, int ng, int sets, F f) {
+  const int gw = WHOLE ? s.D / VEC : s.D, lw = WHOLE ? s.lx : s.lx * VEC;
+  const int slots = s.ty * lw, items = s.ty * gw;
+  const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
+  for (int pair = threadIdx.x / s.team; pair < sets * ng; pair += teams) {
+    const int set = pair / ng, g = pair - set * ng;
+    const float *base = part + set * slots + g * gw;
+    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    int t = me / gw, j = me - t * gw, k = 0;
+    for (int i = me; i < items; i += s.team) {
+      const float v = base[t * lw + j];
+      sum[0] += k == 0 ? v : 0.0f;
+      sum[1] += k == 1 ? v : 0.0f;
+      sum[2] += k == 2 ? v : 0.0f;
+      sum[3] += k == 3 ? v : 0.0f;
+      k = (k + 1) & 3;
+      j += s.team;
+      while (j >= gw) j -= gw, ++t;
+    }
+    float v = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    for (int m = s.team / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
+    if (me == 0) f(pair, v);
+  }
+}
+
+// ------------------------------------------------------------ resident
+// Q samples at a time, up to P rows of each in a thread's registers.
+template <typename T, int VEC, bool WHOLE, int ACT, int Q, int P>
+__global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(fftmv_group_norm_t g, NormShape s) {
+  extern __shared__ float lds[];
+  const int slots = part_slots<VEC, WHOLE>(s);
+  float *part = lds, *mean = lds + Q * slots, *rstd = mean + Q * s.gs;
+  const int slab = blockIdx.x % s.slabs;
+  const SlabLane<VEC> l(s, slab);
+  const GroupOf<VEC, WHOLE> group(l.c, s.D);
+  float w[VEC], b[VEC];
+  if (l.in) {
+    load_params(g.weight, l.ch0 + l.c, 1.0f, w);
+    load_params(g.bias, l.ch0 + l.c, 0.0f, b);
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * Q;
+  for (int64_t n0 = static_cast<int64_t>(blockIdx.x / s.slabs) * Q; n0 < s.N; n0 += step) {
+    Vec<T, VEC> v[Q][P];
+    int held[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      held[q] = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
+      const T *x = static_cast<const T *>(g.x) + (n0 + q) * g.x_sample + l.ch0 + l.c;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        v[q][p] = Vec<T, VEC>{};
+        if (l.in && l.row + p * s.ty < held[q])
+          v[q][p] = load_vec<T, VEC>(x + static_cast<int64_t>(l.row + p * s.ty) * g.x_row);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float sum[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        sum[e] = v[q][0][e];
+#pragma unroll
+        for (int p = 1; p < P; ++p) sum[e] += v[q][p][e];
+      }
+      put_part<VEC, WHOLE>(part + q * slots, s, l, sum);
+    }
+    __syncthreads();
+    team_sums<VEC, WHOLE>(part, s, l.ng, Q, [&](int pair, float sum) {
+      const int q = pair / l.ng;
+      const int h = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
+      mean[pair] = h ? sum / (static_cast<float>(h) * s.D) : 0.0f;
+    });
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float sq[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float m = l.in ? mean[q * l.ng + group[e]] : 0.0f;
+        sq[e] = 0.0f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const float d = l.row + p * s.ty < held[q] ? v[q][p][e] - m : 0.0f;
+          sq[e] = fmaf(d, d, sq[e]);
+        }
+      }
+      put_part<VEC, WHOLE>(part + q * slots, s, l, sq);
+    }
+    __syncthreads();
+    team_sums<VEC, WHOLE>(part, s, l.ng, Q, [&](int pair, float sum) {
+      const int q = pair / l.ng;
+      const int h = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
+      const float r = h ? 1.0f / sqrtf(sum / (static_cast<float>(h) * s.D) + g.eps) : 0.0f;
+      rstd[pair] = r;
+      if (g.stats && n0 + q < s.N) {
+        float *to = g.stats + 2 * ((n0 + q) * s.G + static_cast<int64_t>(slab) * s.gs + (pair - q * l.ng));
+        to[0] = mean[pair];
+        to[1] = r;
+      }
+    });
+    __syncthreads();
+    if (l.in) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        if (n0 + q >= s.N) break;
+        T *y = static_cast<T *>(g.y) + (n0 + q) * g.y_sample + l.ch0 + l.c;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int row = l.row + p * s.ty;
+          if (row >= s.S) break;
+          float o[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const int k = q * l.ng + group[e];
+            o[e] = row < held[q] ? activate<ACT>(fmaf((v[q][p][e] - mean[k]) * rstd[k], w[e], b[e])) : 0.0f;
+          }
+          store_vec<T, VEC>(y + static_cast<int64_t>(row) * g.y_row, o);
+        }
+      }
+    }
+  }
+}
+
+// Sums of dz and dz xhat over the rows of all samples of this workgroup: row
+// `first` of the workspace, or the results themselves where there is one.
+template <int VEC>
+__device__ __forceinline__ void put_param_sums(const fftmv_group_norm_t &g, const NormShape &s,
+                                               const SlabLane<VEC> &l, float *lds, int first, bool alone,
+                                               const float (&db)[VEC], const float (&dw)[VEC]) {
+  const int lw = s.lx * VEC;
+  const int64_t C = static_cast<int64_t>(s.G) * s.D;
+  float2 *to = static_cast<float2 *>(g.workspace) + first * C + l.ch0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    __syncthreads();
+    put_part<VEC, false>(lds, s, l, k ? dw : db);
+    __syncthreads();
+    for (int c = threadIdx.x; c < l.wd; c += blockDim.x) {
+      float sum = 0.0f;
+      for (int t0 = 0; t0 < s.ty; t0 += 16) {
+        float some = 0.0f;
+        for (int t = t0; t < s.ty && t < t0 + 16; ++t) some += lds[t * lw + c];
+        sum += some;
+      }
+      if (!alone) {
+        (k ? to[c].y : to[c].x) = sum;
+      } else {
+        float *out = k ? g.dweight : g.dbias;
+        if (out) out[l.ch0 + c] = sum;
+      }
+    }
+  }
+}
+
+template <typename T, int VEC, bool WHOLE, int ACT, int Q, int P>
+__global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(fftmv_group_norm_t g, NormShape s) {
+  extern __shared__ float lds[];
+  const int slots = part_slots<VEC, WHOLE>(s);
+  float *part = lds, *stat = lds + 2 * Q * slots, *m = stat + 2 * Q * s.gs;
+  const int slab = blockIdx.x % s.slabs, first = blockIdx.x / s.slabs;
+  const SlabLane<VEC> l(s, slab);
+  const GroupOf<VEC, WHOLE> group(l.c, s.D);
+  float w[VEC], b[VEC], db[VEC], dw[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) db[e] = dw[e] = 0.0f;
+  if (l.in) {
+    load_params(g.weight, l.ch0 + l.c, 1.0f, w);
+    load_params(g.bias, l.ch0 + l.c, 0.0f, b);
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * Q;
+  for (int64_t n0 = static_cast<int64_t>(first) * Q; n0 < s.N; n0 += step) {
+    Vec<T, VEC> v[Q][P], d[Q][P];
+    int held[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      held[q] = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
+      const T *x = static_cast<const T *>(g.x) + (n0 + q) * g.x_sample + l.ch0 + l.c;
+      const T *dy = static_cast<const T *>(g.dy) + (n0 + q) * g.dy_sample + l.ch0 + l.c;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        v[q][p] = d[q][p] = Vec<T, VEC>{};
+        const int64_t row = l.row + p * s.ty;
+        if (l.in && row < held[q]) {
+          v[q][p] = load_vec<T, VEC>(x + row * g.x_row);
+          d[q][p] = load_vec<T, VEC>(dy + row * g.dy_row);
+        }
+      }
+    }
+    for (int i = threadIdx.x; i < Q * l.ng; i += blockDim.x) {
+      const int q = i / l.ng;
+      if (n0 + q < s.N) {
+        const float *from = g.stats + 2 * ((n0 + q) * s.G + static_cast<int64_t>(slab) * s.gs + (i - q * l.ng));
+        stat[2 * i] = from[0];
+        stat[2 * i + 1] = from[1];
+      } else {
+        stat[2 * i] = stat[2 * i + 1] = 0.0f;
+      }
+    }
+    __syncthreads();
+    // dz and xhat of one element, both 0 where no row is held
+    auto terms = [&](int q, int p, int e, float &xh, float &dz) {
+      const int k = 2 * (q * l.ng + group[e]);
+      const bool on = l.row + p * s.ty < held[q];
+      xh = on ? (v[q][p][e] - stat[k]) * stat[k + 1] : 0.0f;
+      dz = on ? d[q][p][e] * activate_slope<ACT>(fmaf(xh, w[e], b[e])) : 0.0f;
+    };
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      float t1[VEC], t2[VEC];
+      if (l.in) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          float sb = 0.0f, sw = 0.0f;
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            float xh, dz;
+            terms(q, p, e, xh, dz);
+            sb += dz;
+            sw = fmaf(dz, xh, sw);
+          }
+          db[e] += sb;
+          dw[e] += sw;
+          t1[e] = sb * w[e];
+          t2[e] = sw * w[e];
+        }
+      }
+      put_part<VEC, WHOLE>(part + q * slots, s, l, t1);
+      put_part<VEC, WHOLE>(part + (Q + q) * slots, s, l, t2);
+    }
+    __syncthreads();
+    team_sums<VEC, WHOLE>(part, s, l.ng, 2 * Q, [&](int pair, float sum) {
+      const int q = pair / l.ng % Q;
+      const int h = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
+      m[pair] = h ? sum / (static_cast<float>(h) * s.D) : 0.0f;
+    });
+    __syncthreads();
+    if (l.in) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        if (n0 + q >= s.N) break;
+        T *dx = static_cast<T *>(g.dx) + (n0 + q) * g.dx_sample + l.ch0 + l.c;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const int row = l.row + p * s.ty;
+          if (row >= s.S) break;
+          float o[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            float xh, dz;
+            terms(q, p, e, xh, dz);
+            const int k = q * l.ng + group[e];
+            o[e] = row < held[q] ? stat[2 * k + 1] * (fmaf(dz, w[e], -m[k]) - xh * m[Q * l.ng + k]) : 0.0f;
+          }
+          store_vec<T, VEC>(dx + static_cast<int64_t>(row) * g.dx_row, o);
+        }
+      }
+    }
+    __syncthreads();  // stat is written again
+  }
+  put_param_sums<VEC>(g, s, l, lds, first, gridDim.x == static_cast<unsigned>(s.slabs), db, dw);
+}
+
+// --------------------------------------------------------------- split
+// One range of rows of one sample and slab.
+struct Range {
+  int64_t n;
+  int slab, part, from, to;  // to: behind the last held row
+  __device__ Range(const fftmv_group_norm_t &g, const NormShape &s) {
+    slab = blockIdx.x % s.slabs;
+    const int64_t rest = blockIdx.x / s.slabs;
+    part = static_cast<int>(rest % s.across);
+    n = rest / s.across;
+    from = part * s.range;
+    const int held = held_rows(g, n);
+    to = held - from < s.range ? held : from + s.range;
+  }
+};
+
+constexpr int kTile = 8;  // rows of a thread in one tile
+
+// (mean, sum of squared deviations) of each group over one range, from
+// tiles of kTile rows a thread, each about its own mean and joined pairwise.
+template <typename T, int VEC>
+__global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_norm_t g, NormShape s) {
+  extern __shared__ float lds[];
+  float *part = lds, *mean = lds + s.ty * s.lx * VEC;
+  const Range r(g, s);
+  const SlabLane<VEC> l(s, r.slab);
+  const GroupOf<VEC, false> group(l.c, s.D);
+  const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
+  float mu[VEC], m2[VEC], count = 0.0f;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) mu[e] = m2[e] = 0.0f;
+  if (l.in) {
+    for (int t = r.from + l.row; t < r.to; t += kTile * s.ty) {
+      Vec<T, VEC> v[kTile];
+      int rows = (r.to - t + s.ty - 1) / s.ty;
+      rows = rows < kTile ? rows : kTile;
+#pragma unroll
+      for (int p = 0; p < kTile; ++p) {
+        v[p] = Vec<T, VEC>{};
+        if (p < rows) v[p] = load_vec<T, VEC>(x + static_cast<int64_t>(t + p * s.ty) * g.x_row);
+      }
+      const float k = static_cast<float>(rows), all = count + k, share = k / all, weight = count * share;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float sum = 0.0f, sq = 0.0f;
+#pragma unroll
+        for (int p = 0; p < kTile; ++p) sum += v[p][e];
+        const float m = sum / k;
+#pragma unroll
+        for (int p = 0; p < kTile; ++p) {
+          const float d = p < rows ? v[p][e] - m : 0.0f;
+          sq = fmaf(d, d, sq);
+        }
+        const float d = m - mu[e];
+        mu[e] = fmaf(d, share, mu[e]);
+        m2[e] += fmaf(d * d, weight, sq);
+      }
+      count = all;
+    }
+  }
+  const int rows = r.to - r.from;
+  float v[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) v[e] = count * mu[e];
+  put_part<VEC, false>(part, s, l, v);
+  __syncthreads();
+  team_sums<VEC, false>(part, s, l.ng, 1, [&](int k, float sum) {
+    mean[k] = rows > 0 ? sum / (static_cast<float>(rows) * s.D) : 0.0f;
+  });
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const float d = l.in ? mu[e] - mean[group[e]] : 0.0f;
+    v[e] = fmaf(d * d, count, m2[e]);
+  }
+  put_part<VEC, false>(part, s, l, v);
+  __syncthreads();
+  float2 *to = static_cast<float2 *>(g.workspace) + (r.n * s.across + r.part) * s.G + static_cast<int64_t>(r.slab) * s.gs;
+  team_sums<VEC, false>(part, s, l.ng, 1, [&](int k, float sum) { to[k] = make_float2(mean[k], sum); });
+}
+
+// Joins the ranges' sums, then normalises one range.
+template <typename T, int VEC, int ACT>
+__global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_norm_t g, NormShape s) {
+  extern __shared__ float lds[];
+  float *mean = lds, *rstd = lds + s.gs;
+  const Range r(g, s);
+  const SlabLane<VEC> l(s, r.slab);
+  const GroupOf<VEC, false> group(l.c, s.D);
+  const int held = held_rows(g, r.n);
+  const float2 *from = static_cast<const float2 *>(g.workspace) + r.n * s.across * s.G + static_cast<int64_t>(r.slab) * s.gs;
+  // one team of threads a group, one range a thread at a time
+  const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
+  for (int k = threadIdx.x / s.team; k < l.ng; k += teams) {
+    float sum = 0.0f;
+    for (int i = me; i < s.across; i += s.team) {
+      const int rows = held - i * s.range;
+      if (rows > 0) sum += static_cast<float>(rows < s.range ? rows : s.range) * from[static_cast<int64_t>(i) * s.G + k].x;
+    }
+    for (int m = s.team / 2; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+    const float mu = held ? sum / static_cast<float>(held) : 0.0f;
+    float sq = 0.0f;
+    for (int i = me; i < s.across; i += s.team) {
+      const int rows = held - i * s.range;
+      if (rows > 0) {
+        const float2 v = from[static_cast<int64_t>(i) * s.G + k];
+        const float d = v.x - mu;
+        sq += fmaf(d * d, static_cast<float>(rows < s.range ? rows : s.range) * s.D, v.y);
+      }
+    }
+    for (int m = s.team / 2; m > 0; m >>= 1) sq += __shfl_xor(sq, m);
+    if (me == 0) {
+      mean[k] = mu;
+      rstd[k] = held ? 1.0f / sqrtf(sq / (static_cast<float>(held) * s.D) + g.eps) : 0.0f;
+      if (g.stats && r.part == 0) {
+        float *to = g.stats + 2 * (r.n * s.G + static_cast<int64_t>(r.slab) * s.gs + k);
+        to[0] = mu;
+        to[1] = rstd[k];
+      }
+    }
+  }
+  __syncthreads();
+  if (!l.in) return;
+  // y = act(x scale + (bias - mean scale)) would cancel for large means
+  float w[VEC], b[VEC], mu[VEC], rs[VEC];
+  load_params(g.weight, l.ch0 + l.c, 1.0f, w);
+  load_params(g.bias, l.ch0 + l.c, 0.0f, b);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) mu[e] = mean[group[e]], rs[e] = rstd[group[e]];
+  const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
+  T *y = static_cast<T *>(g.y) + r.n * g.y_sample + l.ch0 + l.c;
+  const int end = s.S - r.from < s.range ? s.S : r.from + s.range;
+  for (int t = r.from + l.row; t < end; t += 4 * s.ty) {
+    Vec<T, VEC> v[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      v[p] = Vec<T, VEC>{};
+      if (t + p * s.ty < r.to) v[p] = load_vec<T, VEC>(x + static_cast<int64_t>(t + p * s.ty) * g.x_row);
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const int row = t + p * s.ty;
+      if (row >= end) break;
+      float o[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        o[e] = row < r.to ? activate<ACT>(fmaf((v[p][e] - mu[e]) * rs[e], w[e], b[e])) : 0.0f;
+      store_vec<T, VEC>(y + static_cast<int64_t>(row) * g.y_row, o);
+    }
+  }
+}
+
+// Sums of dz and dz xhat over one range: of each channel, in row (n, range) of
+// the workspace, and, times the weight, of each group, behind those rows.
+template <typename T, int VEC, int ACT>
+__global__ __launch_bounds__(kNormThreads) void norm_sums_kernel(fftmv_group_norm_t g, NormShape s) {
+  extern __shared__ float lds[];
+  const Range r(g, s);
+  const SlabLane<VEC> l(s, r.slab);
+  float w[VEC], db[VEC], dw[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) w[e] = db[e] = dw[e] = 0.0f;
+  if (l.in) {
+    const GroupOf<VEC, false> group(l.c, s.D);
+    float b[VEC], mu[VEC], rs[VEC];
+    load_params(g.weight, l.ch0 + l.c, 1.0f, w);
+    load_params(g.bias, l.ch0 + l.c, 0.0f, b);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float *from = g.stats + 2 * (r.n * s.G + static_cast<int64_t>(r.slab) * s.gs + group[e]);
+      mu[e] = from[0];
+      rs[e] = from[1];
+    }
+    const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
+    const T *dy = static_cast<const T *>(g.dy) + r.n * g.dy_sample + l.ch0 + l.c;
+    for (int t = r.from + l.row; t < r.to; t += 4 * s.ty) {
+      Vec<T, VEC> v[4], d[4];
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        v[p] = d[p] = Vec<T, VEC>{};
+        const int64_t row = t + p * s.ty;
+        if (row < r.to) {
+          v[p] = load_vec<T, VEC>(x + row * g.x_row);
+          d[p] = load_vec<T, VEC>(dy + row * g.dy_row);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float sb = 0.0f, sw = 0.0f;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {  // rows that are not there have dy = 0
+          const float xh = (v[p][e] - mu[e]) * rs[e], dz = d[p][e] * activate_slope<ACT>(fmaf(xh, w[e], b[e]));
+          sb += dz;
+          sw = fmaf(dz, xh, sw);
+        }
+        db[e] += sb;
+        dw[e] += sw;
+      }
+    }
+  }
+  const int64_t row = r.n * s.across + r.part, C = static_cast<int64_t>(s.G) * s.D;
+  put_param_sums<VEC>(g, s, l, lds, static_cast<int>(row), false, db, dw);
+  float2 *to = static_cast<float2 *>(g.workspace) + s.N * s.across * C + row * s.G + static_cast<int64_t>(r.slab) * s.gs;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float t[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) t[e] = (k ? dw[e] : db[e]) * w[e];
+    __syncthreads();
+    put_part<VEC, false>(lds, s, l, t);
+    __syncthreads();
+    team_sums<VEC, false>(lds, s, l.ng, 1, [&](int i, float sum) { (k ? to[i].y : to[i].x) = sum; });
+  }
+}
+
+// dweight and dbias of 64 channels from `rows` rows of the workspace: four
+// threads a channel, each some of the rows.
+__device__ __forceinline__ void param_sums(const fftmv_group_norm_t &g, int64_t rows, int64_t block, float *lds) {
+  const int c = threadIdx.x % kWave, part = threadIdx.x / kWave, parts = blockDim.x / kWave;
+  const int64_t ch = block * kWave + c;
+  const float2 *from = static_cast<const float2 *>(g.workspace);
+  float sb = 0.0f, sw = 0.0f;
+  if (ch < g.channels)
+    for (int64_t i0 = part; i0 < rows; i0 += 16 * parts) {
+      float b = 0.0f, w = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int64_t i = i0 + k * parts;
+        if (i < rows) {
+          const float2 v = from[i * g.channels + ch];
+          b += v.x;
+          w += v.y;
+        }
+      }
+      sb += b;
+      sw += w;
+    }
+  lds[threadIdx.x] = sb;
+  lds[blockDim.x + threadIdx.x] = sw;
+  __syncthreads();
+  if (part == 0 && ch < g.channels) {
+    for (int k = 1; k < parts; ++k) {
+      sb += lds[k * kWave + c];
+      sw += lds[blockDim.x + k * kWave + c];
+    }
+    if (g.dbias) g.dbias[ch] = sb;
+    if (g.dweight) g.dweight[ch] = sw;
+  }
+}
+
+// dx of one range, the means of dz w and dz w xhat joined from all ranges; and,
+// in the workgroups behind the first `main`, the parameters' sums.
+template <typename T, int VEC, int ACT>
+__global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_norm_t g, NormShape s, int64_t main) {
+  extern __shared__ float lds[];
+  if (blockIdx.x >= main) {
+    param_sums(g, s.N * s.across, blockIdx.x - main, lds);
+    return;
+  }
+  float *m1 = lds, *m2 = lds + s.gs;
+  const Range r(g, s);
+  const SlabLane<VEC> l(s, r.slab);
+  const GroupOf<VEC, false> group(l.c, s.D);
+  const int held = held_rows(g, r.n);
+  const int64_t C = static_cast<int64_t>(s.G) * s.D;
+  const float2 *from = static_cast<const float2 *>(g.workspace) + s.N * s.across * C + r.n * s.across * s.G +
+                       static_cast<int64_t>(r.slab) * s.gs;
+  const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
+  for (int k = threadIdx.x / s.team; k < l.ng; k += teams) {
+    float a = 0.0f, b = 0.0f;
+    for (int i = me; i < s.across; i += s.team) {
+      const float2 v = from[static_cast<int64_t>(i) * s.G + k];
+      a += v.x;
+      b += v.y;
+    }
+    for (int m = s.team / 2; m > 0; m >>= 1) {
+      a += __shfl_xor(a, m);
+      b += __shfl_xor(b, m);
+    }
+    if (me == 0) {
+      const float n = static_cast<float>(held) * s.D;
+      m1[k] = held ? a / n : 0.0f;
+      m2[k] = held ? b / n : 0.0f;
+    }
+  }
+  __syncthreads();
+  if (!l.in) return;
+  float w[VEC], b[VEC], mu[VEC], rs[VEC], k1[VEC], k2[VEC];
+  load_params(g.weight, l.ch0 + l.c, 1.0f, w);
+  load_params(g.bias, l.ch0 + l.c, 0.0f, b);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const float *st = g.stats + 2 * (r.n * s.G + static_cast<int64_t>(r.slab) * s.gs + group[e]);
+    mu[e] = st[0];
+    rs[e] = st[1];
+    k1[e] = m1[group[e]];
+    k2[e] = m2[group[e]];
+  }
+  const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
+  const T *dy = static_cast<const T *>(g.dy) + r.n * g.dy_sample + l.ch0 + l.c;
+  T *dx = static_cast<T *>(g.dx) + r.n * g.dx_sample + l.ch0 + l.c;
+  const int end = s.S - r.from < s.range ? s.S : r.from + s.range;
+  for (int t = r.from + l.row; t < end; t += 2 * s.ty) {
+    Vec<T, VEC> v[2], d[2];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      v[p] = d[p] = Vec<T, VEC>{};
+      const int64_t row = t + p * s.ty;
+      if (row < r.to) {
+        v[p] = load_vec<T, VEC>(x + row * g.x_row);
+        d[p] = load_vec<T, VEC>(dy + row * g.dy_row);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int row = t + p * s.ty;
+      if (row >= end) break;
+      float o[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float xh = (v[p][e] - mu[e]) * rs[e], dz = d[p][e] * activate_slope<ACT>(fmaf(xh, w[e], b[e]));
+        o[e] = row < r.to ? rs[e] * (fmaf(dz, w[e], -k1[e]) - xh * k2[e]) : 0.0f;
+      }
+      store_vec<T, VEC>(dx + static_cast<int64_t>(row) * g.dx_row, o);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- wide
+// Groups wider than a workgroup's lanes: one workgroup per sample and group,
+// its threads along the channels, the rows in turn, read again for each pass.
+__device__ __forceinline__ float block_sum(float v) {
+  __shared__ float part[kBlock / kWave];
+  v = wave_sum(v);
+  __syncthreads();  // the last use of part is over
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = v;
+  __syncthreads();
+  float s = part[0];
+#pragma unroll
+  for (int i = 1; i < kBlock / kWave; ++i) s += part[i];
+  return s;
+}
+
+template <typename T, int ACT>
+__global__ __launch_bounds__(kBlock) void norm_wide_forward_kernel(fftmv_group_norm_t g) {
+  const int64_t n = blockIdx.x / g.groups, q = blockIdx.x % g.groups, D = g.channels / g.groups;
+  const int held = held_rows(g, n);
+  const float count = static_cast<float>(held) * D;
+  const T *x = static_cast<const T *>(g.x) + n * g.x_sample + q * D;
+  T *y = static_cast<T *>(g.y) + n * g.y_sample + q * D;
+  float sum = 0.0f;
+  for (int t = 0; t < held; ++t) {
+    float s = 0.0f;
+    for (int64_t c = threadIdx.x; c < D; c += kBlock) s += static_cast<float>(x[t * g.x_row + c]);
+    sum += s;
+  }
+  const float mean = block_sum(sum) / fmaxf(count, 1.0f);
+  sum = 0.0f;
+  for (int t = 0; t < held; ++t) {
+    float s = 0.0f;
+    for (int64_t c = threadIdx.x; c < D; c += kBlock) {
+      const float d = static_cast<float>(x[t * g.x_row + c]) - mean;
+      s = fmaf(d, d, s);
+    }
+    sum += s;
+  }
+  sum = block_sum(sum);
+  const float rstd = held ? 1.0f / sqrtf(sum / count + g.eps) : 0.0f;
+  if (g.stats && threadIdx.x == 0) {
+    g.stats[2 * static_cast<int64_t>(blockIdx.x)] = mean;
+    g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1] = rstd;
+  }
+  for (int t = 0; t < static_cast<int>(g.rows); ++t)
+    for (int64_t c = threadIdx.x; c < D; c += kBlock) {
+      float v = 0.0f;
+      if (t < held) {
+        const float w = g.weight ? g.weight[q * D + c] : 1.0f, b = g.bias ? g.bias[q * D + c] : 0.0f;
+        v = activate<ACT>(fmaf((static_cast<float>(x[t * g.x_row + c]) - mean) * rstd, w, b));
+      }
+      y[t * g.y_row + c] = static_cast<T>(v);
+    }
+}
+
+// Writes its sums of each channel in row n of the workspace.
+template <typename T, int ACT>
+__global__ __launch_bounds__(kBlock) void norm_wide_backward_kernel(fftmv_group_norm_t g) {
+  const int64_t n = blockIdx.x / g.groups, q = blockIdx.x % g.groups, D = g.channels / g.groups;
+  const int held = held_rows(g, n);
+  const float count = fmaxf(static_cast<float>(held) * D, 1.0f);
+  const T *x = static_cast<const T *>(g.x) + n * g.x_sample + q * D;
+  const T *dy = static_cast<const T *>(g.dy) + n * g.dy_sample + q * D;
+  T *dx = static_cast<T *>(g.dx) + n * g.dx_sample + q * D;
+  float2 *sums = static_cast<float2 *>(g.workspace) + n * g.channels + q * D;
+  const float mean = g.stats[2 * static_cast<int64_t>(blockIdx.x)];
+  const float rstd = g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1];
+  float m1 = 0.0f, m2 = 0.0f;
+  for (int64_t c = threadIdx.x; c < D; c += kBlock) {
+    const float w = g.weight ? g.weight[q * D + c] : 1.0f, b = g.bias ? g.bias[q * D + c] : 0.0f;
+    float sb = 0.0f, sw = 0.0f;
+    for (int t0 = 0; t0 < held; t0 += 32) {
+      float pb = 0.0f, pw = 0.0f;
+      for (int t = t0; t < held && t < t0 + 32; ++t) {
+        const float xh = (static_cast<float>(x[t * g.x_row + c]) - mean) * rstd;
+        const float dz = static_cast<float>(dy[t * g.dy_row + c]) * activate_slope<ACT>(fmaf(xh, w, b));
+        pb += dz;
+        pw = fmaf(dz, xh, pw);
+      }
+      sb += pb;
+      sw += pw;
+    }
+    sums[c] = make_float2(sb, sw);
+    m1 = fmaf(sb, w, m1);
+    m2 = fmaf(sw, w, m2);
+  }
+  m1 = block_sum(m1) / count;
+  m2 = block_sum(m2) / count;
+  for (int t = 0; t < static_cast<int>(g.rows); ++t)
+    for (int64_t c = threadIdx.x; c < D; c += kBlock) {
+      float v = 0.0f;
+      if (t < held) {
+        const float w = g.weight ? g.weight[q * D + c] : 1.0f, b = g.bias ? g.bias[q * D + c] : 0.0f;
+        const float xh = (static_cast<float>(x[t * g.x_row + c]) - mean) * rstd;
+        const float dz = static_cast<float>(dy[t * g.dy_row + c]) * activate_slope<ACT>(fmaf(xh, w, b));
+        v = rstd * (fmaf(dz, w, -m1) - xh * m2);
+      }
+      dx[t * g.dx_row + c] = static_cast<T>(v);
+    }
+}
+
+// ---------------------------------------------------------------- plans
+// What a call launches; decided by sizes alone.
+struct NormPlan {
+  enum Kind { kWide, kTokens, kResident, kSplit } kind = kWide;
+  bool whole = false;
+  int vec = 1;
+  NormShape s{};
+  int64_t rows = 0;      // rows of sums that backward leaves in the workspace
+  size_t lds = 0, workspace = 0;
+};
+
+NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t groups, int dtype, bool backward);
+
+hipError_t launch_param_sums(const fftmv_group_norm_t &g, int64_t rows, hipStream_t s);
+
+template <typename T, int ACT, int VEC>
+hipError_t launch_norm_forward_vec(const fftmv_group_norm_t &g, const NormPlan &p, hipStream_t s) {
+  const NormShape &h = p.s;
+  const unsigned threads = static_cast<unsigned>(h.threads);
+  if (p.kind == NormPlan::kSplit) {
+    const int64_t blocks = h.N * h.slabs * h.across;
+    if (!grid_fits(blocks, h.threads)) return hipErrorInvalidConfiguration;
+    norm_ranges_kernel<T, VEC><<<static_cast<unsigned>(blocks), threads, p.lds, s>>>(g, h);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    norm_apply_kernel<T, VEC, ACT><<<static_cast<unsigned>(blocks), threads, 2 * h.gs * sizeof(float), s>>>(g, h);
+    return hipGetLastError();
+  }
+  const unsigned blocks = static_cast<unsigned>(h.slabs * h.across);
+  if (p.kind == NormPlan::kTokens) {
+    if (p.whole) norm_forward_kernel<T, VEC, true, ACT, 4, 1><<<blocks, threads, p.lds, s>>>(g, h);
+    else norm_forward_kernel<T, VEC, false, ACT, 4, 1><<<blocks, threads, p.lds, s>>>(g, h);
+  } else {
+    if (p.whole) norm_forward_kernel<T, VEC, true, ACT, 1, 8><<<blocks, threads, p.lds, s>>>(g, h);
+    else norm_forward_kernel<T, VEC, false, ACT, 1, 8><<<blocks, threads, p.lds, s>>>(g, h);
+  }
+  return hipGetLastError();
+}
+
+template <typename T, int ACT, int VEC>
+hipError_t launch_norm_backward_vec(const fftmv_group_norm_t &g, const NormPlan &p, hipStream_t s) {
+  const NormShape &h = p.s;
+  const unsigned threads = static_cast<unsigned>(h.threads);
+  if (p.kind == NormPlan::kSplit) {
+    const int64_t blocks = h.N * h.slabs * h.across, more = (g.channels + kWave - 1) / kWave;
+    if (!grid_fits(blocks + more, h.threads)) return hipErrorInvalidConfiguration;
+    norm_sums_kernel<T, VEC, ACT><<<static_cast<unsigned>(blocks), threads, p.lds, s>>>(g, h);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const size_t lds = std::max<size_t>(2 * h.gs, 2 * h.threads) * sizeof(float);
+    norm_grad_kernel<T, VEC, ACT><<<static_cast<unsigned>(blocks + more), threads, lds, s>>>(g, h, blocks);
+    return hipGetLastError();
+  }
+  const unsigned blocks = static_cast<unsigned>(h.slabs * h.across);
+  if (p.kind == NormPlan::kTokens) {
+    if (p.whole) norm_backward_kernel<T, VEC, true, ACT, 2, 1><<<blocks, threads, p.lds, s>>>(g, h);
+    else norm_backward_kernel<T, VEC, false, ACT, 2, 1><<<blocks, threads, p.lds, s>>>(g, h);
+  } else {
+    if (p.whole) norm_backward_kernel<T, VEC, true, ACT, 1, 8><<<blocks, threads, p.lds, s>>>(g, h);
+    else norm_backward_kernel<T, VEC, false, ACT, 1, 8><<<blocks, threads, p.lds, s>>>(g, h);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || h.across == 1) return e;
+  return launch_param_sums(g, h.across, s);
+}
+
+template <typename T>
+hipError_t launch_group_norm_forward_as(const fftmv_group_norm_t &g, hipStream_t s) {
+  const NormPlan p = norm_plan(g.samples, g.rows, g.channels, g.groups, g.dtype, false);
+  return by_three(g.activation, [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+    if (p.kind == NormPlan::kWide) {
+      if (!grid_fits(g.samples * g.groups, kBlock)) return hipErrorInvalidConfiguration;
+      norm_wide_forward_kernel<T, ACT><<<static_cast<unsigned>(g.samples * g.groups), kBlock, 0, s>>>(g);
+      return hipGetLastError();
+    }
+    return p.vec > 1 ? launch_norm_forward_vec<T, ACT, kVec<T>>(g, p, s) : launch_norm_forward_vec<T, ACT, 1>(g, p, s);
+  });
+}
+
+template <typename T>
+hipError_t launch_group_norm_backward_as(const fftmv_group_norm_t &g, hipStream_t s) {
+  const NormPlan p = norm_plan(g.samples, g.rows, g.channels, g.groups, g.dtype, true);
+  return by_three(g.activation, [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+    if (p.kind == NormPlan::kWide) {
+      if (!grid_fits(g.samples * g.groups, kBlock)) return hipErrorInvalidConfiguration;
+      norm_wide_backward_kernel<T, ACT><<<static_cast<unsigned>(g.samples * g.groups), kBlock, 0, s>>>(g);
+      const hipError_t e = hipGetLastError();
+      return e != hipSuccess ? e : launch_param_sums(g, g.samples, s);
+    }
+    return p.vec > 1 ? launch_norm_backward_vec<T, ACT, kVec<T>>(g, p, s)
+                     : launch_norm_backward_vec<T, ACT, 1>(g, p, s);
+  });
+}
+
+}  // namespace fftmv

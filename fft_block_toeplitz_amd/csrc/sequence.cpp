@@ -2,6 +2,7 @@
 // kernels' launches. Nothing here reads device memory or throws.
 #include "sequence.hpp"
 
+#include "group_norm.hpp"
 #include "internal.hpp"
 #include "recurrence.hpp"
 
@@ -27,11 +28,11 @@ bool types_ok(int dtype, int decay, int drive, int reserved) {
          (drive == FFTMV_DRIVE_COMPLEMENT || drive == FFTMV_DRIVE_PLAIN) && reserved == 0;
 }
 
-// rows of the flattened time axis, or -1 where they pass 32 bits
-int64_t rows_of(int64_t batch, int64_t steps, bool packed) {
-  if (batch > INT32_MAX || steps > INT32_MAX) return -1;
-  const int64_t rows = packed ? steps : batch * steps;
-  return rows > INT32_MAX ? -1 : rows;
+// The kernels count samples, rows of a sample and channels in 32 bits, and run
+// up to a few thousand rows past the last one.
+constexpr int64_t kMost = INT32_MAX - (1 << 16);
+bool sizes_fit(int64_t batch, int64_t rows, int64_t channels) {
+  return batch <= kMost && rows <= kMost && channels <= kMost;
 }
 
 // Rows r * step apart, the last of them `channels` long, stay inside 63 bits.
@@ -48,11 +49,10 @@ int check_recurrence(const fftmv_recurrence_t *r, bool backward) {
   if (!types_ok(r->dtype, r->decay, r->drive, 0)) return FFTMV_ERR_INVALID_ARG;
   if (r->lengths && r->offsets) return FFTMV_ERR_INVALID_ARG;
   if (!aligned(r->lengths, 4) || !aligned(r->offsets, 4)) return FFTMV_ERR_INVALID_ARG;
-  const int64_t rows = rows_of(r->batch, r->steps, r->offsets != nullptr);
-  if (rows < 0 || r->channels > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
+  if (!sizes_fit(r->batch, r->steps, r->channels)) return FFTMV_ERR_UNSUPPORTED_SIZE;
   const size_t es = elem_bytes(r->dtype);
   const int64_t B = r->offsets ? 1 : r->batch, T = r->steps, C = r->channels;
-  if (rows > 0) {
+  if (r->steps > 0) {
     if (!field(r->x, es) || !field(r->gate, es)) return FFTMV_ERR_INVALID_ARG;
     if (!strides_ok(B, r->x_batch, T, r->x_step, C) || !strides_ok(B, r->gate_batch, T, r->gate_step, C))
       return FFTMV_ERR_INVALID_ARG;
@@ -84,7 +84,7 @@ int check_group_norm(const fftmv_group_norm_t *g, bool backward) {
   if (g->dtype < FFTMV_F32 || g->dtype > FFTMV_F16 || g->activation < FFTMV_ACT_NONE ||
       g->activation > FFTMV_ACT_GELU || g->reserved != 0 || !(g->eps >= 0.0f))
     return FFTMV_ERR_INVALID_ARG;
-  if (rows_of(g->samples, g->rows, false) < 0 || g->channels > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
+  if (!sizes_fit(g->samples, g->rows, g->channels)) return FFTMV_ERR_UNSUPPORTED_SIZE;
   const size_t es = elem_bytes(g->dtype);
   const int64_t N = g->samples, S = g->rows, C = g->channels;
   if (S > 0) {
@@ -101,7 +101,7 @@ int check_group_norm(const fftmv_group_norm_t *g, bool backward) {
       !floats(g->dweight) || !floats(g->dbias))
     return FFTMV_ERR_INVALID_ARG;
   size_t need = 0;
-  const int st = fftmv_group_norm_workspace(N, S, C, g->groups, &need);
+  const int st = fftmv_group_norm_workspace(N, S, C, g->groups, g->dtype, backward, &need);
   if (st != FFTMV_SUCCESS) return st;
   if (need && (!g->workspace || !aligned(g->workspace, 16) || g->workspace_bytes < need)) return FFTMV_ERR_INVALID_ARG;
   return FFTMV_SUCCESS;
@@ -114,7 +114,7 @@ extern "C" {
 int fftmv_recurrence_sizes(int64_t batch, int64_t steps, int64_t channels, int packed, int64_t *carries,
                            size_t *counter_bytes, size_t *workspace_bytes) {
   if (batch < 1 || steps < 0 || channels < 1) return FFTMV_ERR_INVALID_ARG;
-  if (rows_of(batch, steps, packed != 0) < 0 || channels > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
+  if (!sizes_fit(batch, steps, channels)) return FFTMV_ERR_UNSUPPORTED_SIZE;
   const ScanWorkspace w = scan_workspace_bytes(batch, steps, packed != 0, channels);
   if (carries) *carries = scan_carries(batch, steps, packed != 0);
   if (counter_bytes) *counter_bytes = w.counters;
@@ -142,7 +142,7 @@ int fftmv_recurrence_step(const fftmv_recurrence_step_t *r, hipStream_t stream) 
   if (!r || r->batch < 1 || r->channels < 1 || r->places < 1 || (!r->slots && r->batch > r->places))
     return FFTMV_ERR_INVALID_ARG;
   if (!types_ok(r->dtype, r->decay, r->drive, r->reserved)) return FFTMV_ERR_INVALID_ARG;
-  if (r->batch > INT32_MAX || r->channels > INT32_MAX || r->places > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
+  if (!sizes_fit(r->batch, r->places, r->channels)) return FFTMV_ERR_UNSUPPORTED_SIZE;
   const size_t es = elem_bytes(r->dtype);
   if (!field(r->x, es) || !field(r->gate, es) || !field(r->h, es) || !r->state || !floats(r->state) ||
       !aligned(r->slots, 4))
@@ -154,22 +154,30 @@ int fftmv_recurrence_step(const fftmv_recurrence_step_t *r, hipStream_t stream) 
   return status_of(launch_recurrence_step(*r, stream));
 }
 
-int fftmv_group_norm_workspace(int64_t samples, int64_t rows, int64_t channels, int64_t groups, size_t *bytes) {
-  if (!bytes || samples < 1 || rows < 0 || channels < 1 || groups < 1 || channels % groups)
+int fftmv_group_norm_workspace(int64_t samples, int64_t rows, int64_t channels, int64_t groups, int dtype,
+                               int backward, size_t *bytes) {
+  if (!bytes || samples < 1 || rows < 0 || channels < 1 || groups < 1 || channels % groups || dtype < FFTMV_F32 ||
+      dtype > FFTMV_F16)
     return FFTMV_ERR_INVALID_ARG;
-  if (rows_of(samples, rows, false) < 0 || channels > INT32_MAX) return FFTMV_ERR_UNSUPPORTED_SIZE;
-  *bytes = static_cast<size_t>(samples) * channels * 8;
+  if (!sizes_fit(samples, rows, channels)) return FFTMV_ERR_UNSUPPORTED_SIZE;
+  *bytes = norm_plan(samples, rows, channels, groups, dtype, backward != 0).workspace;
   return FFTMV_SUCCESS;
 }
 
 int fftmv_group_norm_forward(const fftmv_group_norm_t *g, hipStream_t stream) {
   const int st = check_group_norm(g, false);
-  return st != FFTMV_SUCCESS ? st : status_of(launch_group_norm_forward(*g, stream));
+  if (st != FFTMV_SUCCESS) return st;
+  return status_of(g->dtype == FFTMV_F32    ? launch_group_norm_forward_f32(*g, stream)
+                   : g->dtype == FFTMV_BF16 ? launch_group_norm_forward_bf16(*g, stream)
+                                            : launch_group_norm_forward_f16(*g, stream));
 }
 
 int fftmv_group_norm_backward(const fftmv_group_norm_t *g, hipStream_t stream) {
   const int st = check_group_norm(g, true);
-  return st != FFTMV_SUCCESS ? st : status_of(launch_group_norm_backward(*g, stream));
+  if (st != FFTMV_SUCCESS) return st;
+  return status_of(g->dtype == FFTMV_F32    ? launch_group_norm_backward_f32(*g, stream)
+                   : g->dtype == FFTMV_BF16 ? launch_group_norm_backward_bf16(*g, stream)
+                                            : launch_group_norm_backward_f16(*g, stream));
 }
 
 }  // extern "C"

@@ -18,8 +18,12 @@ hipError_t launch_recurrence_backward_f32(const fftmv_recurrence_t &r, hipStream
 hipError_t launch_recurrence_backward_bf16(const fftmv_recurrence_t &r, hipStream_t s);
 hipError_t launch_recurrence_backward_f16(const fftmv_recurrence_t &r, hipStream_t s);
 hipError_t launch_recurrence_step(const fftmv_recurrence_step_t &r, hipStream_t s);
-hipError_t launch_group_norm_forward(const fftmv_group_norm_t &g, hipStream_t s);
-hipError_t launch_group_norm_backward(const fftmv_group_norm_t &g, hipStream_t s);
+hipError_t launch_group_norm_forward_f32(const fftmv_group_norm_t &g, hipStream_t s);
+hipError_t launch_group_norm_forward_bf16(const fftmv_group_norm_t &g, hipStream_t s);
+hipError_t launch_group_norm_forward_f16(const fftmv_group_norm_t &g, hipStream_t s);
+hipError_t launch_group_norm_backward_f32(const fftmv_group_norm_t &g, hipStream_t s);
+hipError_t launch_group_norm_backward_bf16(const fftmv_group_norm_t &g, hipStream_t s);
+hipError_t launch_group_norm_backward_f16(const fftmv_group_norm_t &g, hipStream_t s);
 
 using bf16 = __bf16;
 using f16 = _Float16;

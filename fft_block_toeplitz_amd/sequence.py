@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 
 from . import FFTMV_SUCCESS, FftmvError, lib
 
@@ -28,44 +29,17 @@ DECAYS = {"sigmoid": 0, "exp": 1, "value": 2}
 DRIVES = {"complement": 0, "plain": 1}
 ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2}
 
-_I64, _I32, _F32, _P, _Z = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+# The structures of include/fftmv.h as packed bytes, fields in their order (q:
+# int64, i / I: int32, f: float, P: pointer, N: size_t; native alignment). A
+# bytes object is a quarter of the cost of a ctypes structure, and these calls
+# answer single time steps.
+_RECURRENCE = struct.Struct("@3q3iI2P PqqPqq2P PNPN PqqP PqqP PqqPqqP")  # fftmv_recurrence_t
+_STEP = struct.Struct("@3q4i PqPq PqP Pq")  # fftmv_recurrence_step_t
+_GROUP_NORM = struct.Struct("@4q2ifiP Pqq 4PN Pqq PqqPqq2P")  # fftmv_group_norm_t
+_I64, _P, _Z = ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
 
-def _fields(text, kind):
-    return [(name, kind) for name in text.split()]
-
-
-class _Recurrence(ctypes.Structure):  # fftmv_recurrence_t
-    _fields_ = (_fields("batch steps channels", _I64) + _fields("dtype decay drive", _I32)
-                + [("call", ctypes.c_uint32)] + _fields("lengths offsets", _P)
-                + [("x", _P), ("x_batch", _I64), ("x_step", _I64)]
-                + [("gate", _P), ("gate_batch", _I64), ("gate_step", _I64)]
-                + _fields("h0 carries", _P)
-                + [("counters", _P), ("counter_bytes", _Z), ("workspace", _P), ("workspace_bytes", _Z)]
-                + [("h", _P), ("h_batch", _I64), ("h_step", _I64), ("h_last", _P)]
-                + [("dh", _P), ("dh_batch", _I64), ("dh_step", _I64), ("dh_last", _P)]
-                + [("dx", _P), ("dx_batch", _I64), ("dx_step", _I64)]
-                + [("dgate", _P), ("dgate_batch", _I64), ("dgate_step", _I64), ("dh0", _P)])
-
-
-class _Step(ctypes.Structure):  # fftmv_recurrence_step_t
-    _fields_ = (_fields("batch channels places", _I64) + _fields("dtype decay drive reserved", _I32)
-                + [("x", _P), ("x_step", _I64), ("gate", _P), ("gate_step", _I64)]
-                + [("state", _P), ("state_step", _I64), ("slots", _P), ("h", _P), ("h_step", _I64)])
-
-
-class _GroupNorm(ctypes.Structure):  # fftmv_group_norm_t
-    _fields_ = (_fields("samples rows channels groups", _I64) + _fields("dtype activation", _I32)
-                + [("eps", _F32), ("reserved", _I32), ("lengths", _P)]
-                + [("x", _P), ("x_sample", _I64), ("x_row", _I64)]
-                + _fields("weight bias stats workspace", _P) + [("workspace_bytes", _Z)]
-                + [("y", _P), ("y_sample", _I64), ("y_row", _I64)]
-                + [("dy", _P), ("dy_sample", _I64), ("dy_row", _I64)]
-                + [("dx", _P), ("dx_sample", _I64), ("dx_row", _I64)]
-                + _fields("dweight dbias", _P))
-
-
-# ---- same-name wrappers of the C entry points (structures, streams as ints)
+# ---- same-name wrappers of the C entry points (structures as bytes, streams as ints)
 _bound = None
 
 
@@ -75,11 +49,10 @@ def _lib():
         L = lib()
         Z = ctypes.POINTER(_Z)
         L.fftmv_recurrence_sizes.argtypes = [_I64, _I64, _I64, ctypes.c_int, ctypes.POINTER(_I64), Z, Z]
-        L.fftmv_group_norm_workspace.argtypes = [_I64, _I64, _I64, _I64, Z]
-        for name, kind in (("recurrence_forward", _Recurrence), ("recurrence_backward", _Recurrence),
-                           ("recurrence_step", _Step), ("group_norm_forward", _GroupNorm),
-                           ("group_norm_backward", _GroupNorm)):
-            getattr(L, "fftmv_" + name).argtypes = [ctypes.POINTER(kind), _P]
+        L.fftmv_group_norm_workspace.argtypes = [_I64, _I64, _I64, _I64, ctypes.c_int, ctypes.c_int, Z]
+        for name in ("recurrence_forward", "recurrence_backward", "recurrence_step", "group_norm_forward",
+                     "group_norm_backward"):
+            getattr(L, "fftmv_" + name).argtypes = [ctypes.c_char_p, _P]
         _bound = L
     return _bound
 
@@ -97,51 +70,55 @@ def fftmv_recurrence_sizes(batch: int, steps: int, channels: int, packed: bool) 
     return c.value, n.value, m.value
 
 
-def fftmv_recurrence_forward(r: _Recurrence, stream: int = 0) -> None:
+def fftmv_recurrence_forward(r: bytes, stream: int = 0) -> None:
     _check(_lib().fftmv_recurrence_forward(r, stream), "fftmv_recurrence_forward")
 
 
-def fftmv_recurrence_backward(r: _Recurrence, stream: int = 0) -> None:
+def fftmv_recurrence_backward(r: bytes, stream: int = 0) -> None:
     _check(_lib().fftmv_recurrence_backward(r, stream), "fftmv_recurrence_backward")
 
 
-def fftmv_recurrence_step(r: _Step, stream: int = 0) -> None:
+def fftmv_recurrence_step(r: bytes, stream: int = 0) -> None:
     _check(_lib().fftmv_recurrence_step(r, stream), "fftmv_recurrence_step")
 
 
-def fftmv_group_norm_workspace(samples: int, rows: int, channels: int, groups: int) -> int:
+def fftmv_group_norm_workspace(samples: int, rows: int, channels: int, groups: int, dtype: int,
+                               backward: bool) -> int:
     n = _Z()
-    _check(_lib().fftmv_group_norm_workspace(samples, rows, channels, groups, ctypes.byref(n)),
+    _check(_lib().fftmv_group_norm_workspace(samples, rows, channels, groups, dtype, backward, ctypes.byref(n)),
            "fftmv_group_norm_workspace")
     return n.value
 
 
-def fftmv_group_norm_forward(g: _GroupNorm, stream: int = 0) -> None:
+def fftmv_group_norm_forward(g: bytes, stream: int = 0) -> None:
     _check(_lib().fftmv_group_norm_forward(g, stream), "fftmv_group_norm_forward")
 
 
-def fftmv_group_norm_backward(g: _GroupNorm, stream: int = 0) -> None:
+def fftmv_group_norm_backward(g: bytes, stream: int = 0) -> None:
     _check(_lib().fftmv_group_norm_backward(g, stream), "fftmv_group_norm_backward")
 
 
 # ---- argument checks shared by the torch layer
-_types = None
+_torch = None
+_types = {}
 
 
-def _torch_types():
-    global _types
-    import torch
+def _torch_module():
+    """torch, imported by the first call."""
+    global _torch
+    if _torch is None:
+        import torch
 
-    _types = {torch.float32: FFTMV_F32, torch.bfloat16: FFTMV_BF16, torch.float16: FFTMV_F16}
-    return _types
+        _types.update({torch.float32: FFTMV_F32, torch.bfloat16: FFTMV_BF16, torch.float16: FFTMV_F16})
+        _torch = torch
+    return _torch
 
 
 def _dtype_of(x, name):
-    import torch
-
+    torch = _torch or _torch_module()
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    code = (_types or _torch_types()).get(x.dtype)
+    code = _types.get(x.dtype)
     if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
     if x.get_device() != torch.cuda.current_device():
@@ -149,13 +126,17 @@ def _dtype_of(x, name):
     return code
 
 
-def _field(t, like, name):
-    """(pointer, batch stride, step stride) of a channels-last field of the shape, type and device of ``like``."""
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{name} must have the shape, type and device of its counterpart: got {tuple(t.shape)} "
-                         f"{t.dtype} on {t.device}, expected {tuple(like.shape)} {like.dtype} on {like.device}")
+def _differs(t, shape, like, name):
+    return ValueError(f"{name} must have the shape, type and device of its counterpart: got {tuple(t.shape)} "
+                      f"{t.dtype} on {t.device}, expected {tuple(shape)} {like.dtype} on {like.device}")
+
+
+def _field(t, shape, like, name):
+    """(pointer, batch stride, step stride) of a channels-last field of this shape, of ``like``'s type and device."""
+    if t is not like and (t.shape != shape or t.dtype != like.dtype or t.get_device() != like.get_device()):
+        raise _differs(t, shape, like, name)
     st = t.stride()
-    if st[-1] != 1 and t.shape[-1] != 1 and t.numel():
+    if st[-1] != 1 and shape[-1] != 1 and t.numel():
         raise ValueError(f"{name}: channels must be contiguous (stride 1), got strides {st}")
     return (t.data_ptr(), st[0] if len(st) == 3 else 0, st[-2])
 
@@ -163,10 +144,8 @@ def _field(t, like, name):
 def _floats(t, shape, like, name):
     """Pointer of an optional contiguous float32 tensor."""
     if t is None:
-        return None
-    import torch
-
-    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != like.device:
+        return 0
+    if t.dtype != _torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be a contiguous float32 tensor {shape} on {like.device}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
@@ -174,10 +153,8 @@ def _floats(t, shape, like, name):
 
 def _ints(t, n, like, name):
     if t is None:
-        return None
-    import torch
-
-    if t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous() or t.device != like.device:
+        return 0
+    if t.dtype != _torch.int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be a contiguous int32 tensor ({n},) on {like.device}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
@@ -196,51 +173,59 @@ def _span(t):
     return t.data_ptr(), t.data_ptr() + n * t.element_size()
 
 
-def _output(out, like, inputs, name):
+def _output(out, like, inputs):
     """A new contiguous tensor like ``like``, or ``out`` after its checks."""
-    import torch
-
     if out is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return _torch.empty(like.shape, dtype=like.dtype, device=like.device)
     if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {like.dtype} tensor {tuple(like.shape)} on {like.device}")
+        raise ValueError(f"out must be a contiguous {like.dtype} tensor {tuple(like.shape)} on {like.device}")
     lo, hi = _span(out)
     for t in inputs:
         if t is not None:
             a, b = _span(t)
             if a < hi and lo < b:
-                raise ValueError(f"{name} must not overlap an input")
+                raise ValueError("out must not overlap an input")
     return out
 
 
 class _On:
-    """The stream that a call runs on: allocations inside belong to it, and
-    tensors that came from another stream are kept for it."""
+    """A stream that is not the current one: allocations inside belong to it,
+    and tensors that came from another stream are kept for it."""
 
     def __init__(self, stream, *tensors):
-        self.stream, self.tensors, self.inside = stream, tensors, None
+        self.inside, self.stream, self.tensors = _torch.cuda.stream(stream), stream, tensors
 
     def __enter__(self):
-        import torch
-
-        if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
-        if self.stream != torch.cuda.current_stream():
-            self.inside = torch.cuda.stream(self.stream)
-            self.inside.__enter__()
-            for t in self.tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
-        return self.stream.cuda_stream
+        self.inside.__enter__()
+        for t in self.tensors:
+            if t is not None:
+                t.record_stream(self.stream)
 
     def __exit__(self, *what):
-        if self.inside is not None:
-            self.inside.__exit__(*what)
+        self.inside.__exit__(*what)
+
+
+def _current_stream():
+    return _torch.cuda.current_stream().cuda_stream
+
+
+def _on_stream(call):
+    """Gives a public function its ``stream`` argument: the call runs with that stream current."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        _torch_module()
+        tensors = [t for t in (*args, *kwargs.values()) if isinstance(t, _torch.Tensor) and t.is_cuda]
+        with _On(stream, *tensors):
+            return call(*args, **kwargs)
+    return wrapped
 
 
 # ---- the recurrence
 _workspaces = {}
-_sizes = functools.lru_cache(maxsize=1024)(fftmv_recurrence_sizes)  # a function of the shape alone
+_sizes = functools.lru_cache(maxsize=1024)(fftmv_recurrence_sizes)  # functions of the shape alone
+_norm_sizes = functools.lru_cache(maxsize=1024)(fftmv_group_norm_workspace)
 
 
 def _workspace(sizes, stream, like):
@@ -248,25 +233,24 @@ def _workspace(sizes, stream, like):
     the call on it). Calls of one stream share a workspace, which is kept and
     grown; a call under graph capture gets memory of the graph's own, cleared
     inside the graph."""
-    import torch
-
     _, few, many = sizes
     if many == 0:
-        return None, 0, None, 0, 0
-    new = lambda n: torch.zeros(n, dtype=torch.uint8, device=like.device)  # noqa: E731
-    if torch.cuda.is_current_stream_capturing():
-        w = [new(few), new(many), 0]
-    else:
-        w = _workspaces.get((like.get_device(), stream))
-        if w is None or w[0].numel() < few or w[1].numel() < many:
-            if w is not None:
-                few, many = max(few, w[0].numel()), max(many, w[1].numel())
-            w = _workspaces[like.get_device(), stream] = [new(few), new(many), 0]
-        elif w[2] == 2 ** 32 - 1:
-            w[1].zero_()
-            w[2] = 0
-    w[2] += 1
-    return w[0].data_ptr(), w[0].numel(), w[1].data_ptr(), w[1].numel(), w[2]
+        return 0, 0, 0, 0, 0
+    new = lambda n: _torch.zeros(n, dtype=_torch.uint8, device=like.device)  # noqa: E731
+    if _torch.cuda.is_current_stream_capturing():
+        a, b = new(few), new(many)
+        return a.data_ptr(), few, b.data_ptr(), many, 1
+    w = _workspaces.get((like.get_device(), stream))
+    if w is None or w[1] < few or w[3] < many:
+        if w is not None:
+            few, many = max(few, w[1]), max(many, w[3])
+        a, b = new(few), new(many)
+        w = _workspaces[like.get_device(), stream] = [a.data_ptr(), few, b.data_ptr(), many, 0, a, b]
+    elif w[4] == 2 ** 32 - 1:
+        w[6].zero_()
+        w[4] = 0
+    w[4] += 1
+    return w[:5]
 
 
 def _sequences(x, lengths, offsets):
@@ -288,8 +272,9 @@ def _sequences(x, lengths, offsets):
     return B, T, C
 
 
+@_on_stream
 def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths=None, offsets=None, save=False,
-               out=None, stream=None):
+               out=None):
     """Gated linear recurrence along time, per sequence and channel:
 
         h_t = a_t h_{t-1} + u_t,   h_{-1} = h0 (zeros when None)
@@ -306,98 +291,99 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     Returns h (x's type) and the last states, float32 [batch, channels];
     with ``save`` also the carries that ``recurrence_backward`` needs. Runs
     on ``stream`` (default: the current one), without synchronising."""
-    import torch
-
     dtype = _dtype_of(x, "x")
     B, T, C = _sequences(x, lengths, offsets)
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
-    xf, gf = _field(x, x, "x"), _field(gate, x, "gate")
+    shape, packed = x.shape, offsets is not None
+    xf, gf = _field(x, shape, x, "x"), _field(gate, shape, x, "gate")
     h0p = _floats(h0, (B, C), x, "h0")
     lens, offs = _ints(lengths, B, x, "lengths"), _ints(offsets, B + 1, x, "offsets")
-    with _On(stream, x, gate, h0, lengths, offsets, out) as s:
-        h = _output(out, x, (x, gate), "out")
-        last = torch.empty((B, C), dtype=torch.float32, device=x.device)
-        if B == 0:
-            if T:
-                h.zero_()
-            return (h, last, torch.empty((0, C), device=x.device)) if save else (h, last)
-        sizes = _sizes(B, T, C, offsets is not None)
-        carries = torch.empty((sizes[0], C), dtype=torch.float32, device=x.device) if save else None
-        *ws, call = _workspace(sizes, s, x)
-        r = _Recurrence(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, carries.data_ptr() if save else None,
-                        *ws, *_field(h, x, "out"), last.data_ptr())
-        fftmv_recurrence_forward(r, s)
+    h = _output(out, x, (x, gate))
+    last = _torch.empty((B, C), dtype=_torch.float32, device=x.device)
+    if B == 0:
+        h.zero_()
+        return (h, last, last) if save else (h, last)
+    sizes = _sizes(B, T, C, packed)
+    carries = _torch.empty((sizes[0], C), dtype=_torch.float32, device=x.device) if save else None
+    stream = _current_stream()
+    *ws, call = _workspace(sizes, stream, x)
+    r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, carries.data_ptr() if save else 0,
+                         *ws, h.data_ptr(), T * C, C, last.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    fftmv_recurrence_forward(r, stream)
     return (h, last, carries) if save else (h, last)
 
 
+@_on_stream
 def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="sigmoid", drive="complement",
-                        lengths=None, offsets=None, stream=None):
+                        lengths=None, offsets=None):
     """Gradients of ``recurrence``: (dx, dgate, dh0) from dh, the gradient of
     h, and dh_last, that of the last states (zeros when None). x, gate, h0
     and the keywords are the forward call's, ``carries`` what it saved; h is
     recomputed from them in float32."""
-    import torch
-
     dtype = _dtype_of(x, "x")
     B, T, C = _sequences(x, lengths, offsets)
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
-    xf, gf, df = _field(x, x, "x"), _field(gate, x, "gate"), _field(dh, x, "dh")
+    shape = x.shape
+    xf, gf, df = _field(x, shape, x, "x"), _field(gate, shape, x, "gate"), _field(dh, shape, x, "dh")
     h0p, lp = _floats(h0, (B, C), x, "h0"), _floats(dh_last, (B, C), x, "dh_last")
     sizes = _sizes(B, T, C, offsets is not None) if B else (0, 0, 0)
     if carries is None:
         raise ValueError("carries must be what recurrence(..., save=True) returned")
     cp = _floats(carries, (sizes[0], C), x, "carries")
     lens, offs = _ints(lengths, B, x, "lengths"), _ints(offsets, B + 1, x, "offsets")
-    with _On(stream, dh, x, gate, carries, h0, dh_last, lengths, offsets) as s:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dg = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dh0 = torch.empty((B, C), dtype=torch.float32, device=x.device)
-        if B == 0:
-            if T:
-                dx.zero_(), dg.zero_()
-            return dx, dg, dh0
-        *ws, call = _workspace(sizes, s, x)
-        r = _Recurrence(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, cp, *ws,
-                        None, 0, 0, None, *df, lp, *_field(dx, x, "dx"), *_field(dg, x, "dgate"), dh0.data_ptr())
-        fftmv_recurrence_backward(r, s)
+    dx = _torch.empty(shape, dtype=x.dtype, device=x.device)
+    dg = _torch.empty(shape, dtype=x.dtype, device=x.device)
+    dh0 = _torch.empty((B, C), dtype=_torch.float32, device=x.device)
+    if B == 0:
+        return dx.zero_(), dg.zero_(), dh0
+    stream = _current_stream()
+    *ws, call = _workspace(sizes, stream, x)
+    r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, cp, *ws, 0, 0, 0, 0, *df, lp,
+                         dx.data_ptr(), T * C, C, dg.data_ptr(), T * C, C, dh0.data_ptr())
+    fftmv_recurrence_backward(r, stream)
     return dx, dg, dh0
 
 
-def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="complement", out=None, stream=None):
+@_on_stream
+def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="complement", out=None):
     """One time step of many streams against a cache of states, in place.
     x, gate: [batch, channels]; state: float32 [places, channels]; slots:
     int32 [batch], the place of each stream (None: stream b has place b). A
     slot outside the cache, -1 say, marks an idle stream: zeros come back
     and no state changes. Slots of one call must differ. Returns h [batch,
     channels]."""
-    import torch
-
     dtype = _dtype_of(x, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must be [batch, channels], got {tuple(x.shape)}")
-    B, C = x.shape
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [batch, channels], got {tuple(shape)}")
+    B, C = shape
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
-    xf, gf = _field(x, x, "x"), _field(gate, x, "gate")
-    if state.dtype != torch.float32 or state.dim() != 2 or state.shape[1] != C or state.device != x.device or (
-            state.stride(1) != 1 and C != 1) or (state.stride(0) < C and state.shape[0] > 1):
+    xp, _, xs = _field(x, shape, x, "x")
+    gp, _, gs = _field(gate, shape, x, "gate")
+    places = state.shape[0] if state.dim() == 2 else -1
+    ss = state.stride()
+    if (places < 0 or state.dtype != _torch.float32 or state.shape[1] != C or state.get_device() != x.get_device()
+            or (ss[1] != 1 and C != 1) or (ss[0] < C and places > 1)):
         raise ValueError(f"state must be a float32 tensor [places, {C}] on {x.device} with contiguous channels, got "
-                         f"{tuple(state.shape)} {state.dtype}, strides {state.stride()}, on {state.device}")
-    if slots is None and B > state.shape[0]:
-        raise ValueError(f"{B} streams without slots need as many places, the state has {state.shape[0]}")
+                         f"{tuple(state.shape)} {state.dtype}, strides {ss}, on {state.device}")
+    if slots is None and B > places:
+        raise ValueError(f"{B} streams without slots need as many places, the state has {places}")
     sp = _ints(slots, B, x, "slots")
-    with _On(stream, x, gate, state, slots, out) as s:
-        h = _output(out, x, (x, gate, state), "out")
-        if B == 0:
-            return h
-        if state.shape[0] == 0:
-            return h.zero_()
-        r = _Step(B, C, state.shape[0], dtype, *kinds, 0, xf[0], xf[2], gf[0], gf[2], state.data_ptr(),
-                  max(state.stride(0), C), sp, h.data_ptr(), C)
-        fftmv_recurrence_step(r, s)
+    h = _output(out, x, (x, gate, state))
+    if B == 0 or places == 0:
+        return h.zero_()
+    fftmv_recurrence_step(_STEP.pack(B, C, places, dtype, *kinds, 0, xp, xs, gp, gs, state.data_ptr(),
+                                     max(ss[0], C), sp, h.data_ptr(), C), _current_stream())
     return h
 
 
 # ---- group normalisation
+def _scratch(samples, rows, channels, groups, backward, like):
+    """(scratch memory or None, its bytes) of a call of this shape."""
+    need = _norm_sizes(samples, rows, channels, groups, _types[like.dtype], backward)
+    return (_torch.empty(need, dtype=_torch.uint8, device=like.device), need) if need else (None, 0)
+
+
 def _samples(x):
     """x as [samples, rows, channels], without a copy."""
     if x.dim() == 3:
@@ -413,8 +399,8 @@ def _samples(x):
                          "make it contiguous") from None
 
 
-def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, lengths=None, save=False, out=None,
-               stream=None):
+@_on_stream
+def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, lengths=None, save=False, out=None):
     """Group normalisation with an activation, channels last:
 
         y = act((x - mean) rstd weight + bias),   rstd = 1 / sqrt(var + eps)
@@ -428,61 +414,55 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
 
     Returns y (x's type); with ``save`` also the statistics, float32
     [samples, groups, 2] (mean, rstd), that ``group_norm_backward`` needs."""
-    import torch
-
     dtype = _dtype_of(x, "x")
     v = _samples(x)
-    N, S, C = v.shape
+    N, S, C = shape = v.shape
     if not isinstance(groups, int) or groups < 1 or C < 1 or C % groups:
         raise ValueError(f"groups must divide the channels: got {groups!r} for {C}")
     act = _choice(activation, ACTIVATIONS, "activation")
     if not eps >= 0.0:
         raise ValueError(f"eps must be >= 0, got {eps}")
-    xf = _field(v, v, "x")
+    xf = _field(v, shape, v, "x")
     wp, bp = _floats(weight, (C,), x, "weight"), _floats(bias, (C,), x, "bias")
     lens = _ints(lengths, N, x, "lengths")
-    with _On(stream, x, weight, bias, lengths, out) as s:
-        y = _output(out, x, (x,), "out")
-        stats = torch.empty((N, groups, 2), dtype=torch.float32, device=x.device) if save else None
-        if N == 0:
-            return (y, stats) if save else y
-        need = fftmv_group_norm_workspace(N, S, C, groups)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        g = _GroupNorm(N, S, C, groups, dtype, act, eps, 0, lens, *xf, wp, bp, stats.data_ptr() if save else None,
-                       ws.data_ptr() if need else None, need, y.data_ptr(), S * C, C)
-        fftmv_group_norm_forward(g, s)
+    y = _output(out, x, (x,))
+    stats = _torch.empty((N, groups, 2), dtype=_torch.float32, device=x.device) if save else None
+    if N == 0:
+        return (y, stats) if save else y
+    ws, need = _scratch(N, S, C, groups, False, x)
+    g = _GROUP_NORM.pack(N, S, C, groups, dtype, act, eps, 0, lens, *xf, wp, bp, stats.data_ptr() if save else 0,
+                         ws.data_ptr() if need else 0, need, y.data_ptr(), S * C, C, 0, 0, 0, 0, 0, 0, 0, 0)
+    fftmv_group_norm_forward(g, _current_stream())
     return (y, stats) if save else y
 
 
-def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, *, activation=None, lengths=None, stream=None):
+@_on_stream
+def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, *, activation=None, lengths=None):
     """Gradients of ``group_norm``: (dx, dweight, dbias), the last two float32
     [channels], from dy, the gradient of y. x, the parameters and the
     keywords are the forward call's, ``stats`` what it saved."""
-    import torch
-
     dtype = _dtype_of(x, "x")
     v = _samples(x)
-    N, S, C = v.shape
+    N, S, C = shape = v.shape
     if not isinstance(groups, int) or groups < 1 or C < 1 or C % groups:
         raise ValueError(f"groups must divide the channels: got {groups!r} for {C}")
     act = _choice(activation, ACTIVATIONS, "activation")
     if dy.shape != x.shape:
         raise ValueError(f"dy must have x's shape {tuple(x.shape)}, got {tuple(dy.shape)}")
-    xf, df = _field(v, v, "x"), _field(_samples(dy), v, "dy")
+    xf, df = _field(v, shape, v, "x"), _field(_samples(dy), shape, v, "dy")
     wp, bp = _floats(weight, (C,), x, "weight"), _floats(bias, (C,), x, "bias")
-    sp = _floats(stats, (N, groups, 2), x, "stats")
-    if sp is None:
+    if stats is None:
         raise ValueError("stats must be what group_norm(..., save=True) returned")
+    sp = _floats(stats, (N, groups, 2), x, "stats")
     lens = _ints(lengths, N, x, "lengths")
-    with _On(stream, dy, x, stats, weight, bias, lengths) as s:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        if N == 0:
-            return dx, torch.zeros(C, device=x.device), torch.zeros(C, device=x.device)
-        dw = torch.empty(C, dtype=torch.float32, device=x.device)
-        db = torch.empty(C, dtype=torch.float32, device=x.device)
-        need = fftmv_group_norm_workspace(N, S, C, groups)
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-        g = _GroupNorm(N, S, C, groups, dtype, act, 0.0, 0, lens, *xf, wp, bp, sp, ws.data_ptr() if need else None,
-                       need, None, 0, 0, *df, dx.data_ptr(), S * C, C, dw.data_ptr(), db.data_ptr())
-        fftmv_group_norm_backward(g, s)
+    dx = _torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    both = _torch.empty((2, C), dtype=_torch.float32, device=x.device)
+    dw, db = both[0], both[1]
+    if N == 0:
+        both.zero_()
+        return dx, dw, db
+    ws, need = _scratch(N, S, C, groups, True, x)
+    g = _GROUP_NORM.pack(N, S, C, groups, dtype, act, 0.0, 0, lens, *xf, wp, bp, sp, ws.data_ptr() if need else 0, need,
+                         0, 0, 0, *df, dx.data_ptr(), S * C, C, dw.data_ptr(), db.data_ptr())
+    fftmv_group_norm_backward(g, _current_stream())
     return dx, dw, db

@@ -361,7 +361,8 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  * Errors: FFTMV_ERR_INVALID_ARG (a null or misaligned pointer, a size < 1
  * -- steps may be 0 --, an unknown type/decay/drive, both lengths and
  * offsets, a workspace that is too small); FFTMV_ERR_UNSUPPORTED_SIZE
- * (more than 2^31 - 1 rows or channels, or a grid above 2^32 work-items). */
+ * (more than 2^31 - 2^16 sequences, steps or channels, or a grid above 2^32
+ * work-items). */
 #define FFTMV_RECURRENCE_CHUNK 128
 typedef struct fftmv_recurrence_s {
   int64_t batch, steps, channels;
@@ -471,8 +472,9 @@ typedef struct fftmv_group_norm_s {
   float *dweight, *dbias;
 } fftmv_group_norm_t;
 
-FFTMV_API int fftmv_group_norm_workspace(int64_t samples, int64_t rows, int64_t channels, int64_t groups,
-                                         size_t *bytes);
+/* Workspace bytes of a forward (backward: 0) or backward (1) call. */
+FFTMV_API int fftmv_group_norm_workspace(int64_t samples, int64_t rows, int64_t channels, int64_t groups, int dtype,
+                                         int backward, size_t *bytes);
 FFTMV_API int fftmv_group_norm_forward(const fftmv_group_norm_t *g, hipStream_t stream);
 FFTMV_API int fftmv_group_norm_backward(const fftmv_group_norm_t *g, hipStream_t stream);
 
