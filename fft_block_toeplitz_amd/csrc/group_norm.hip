@@ -50,7 +50,6 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   s.G = static_cast<int>(groups);
   s.D = static_cast<int>(channels / groups);
   const int es = dtype == FFTMV_F32 ? 4 : 2;
-  const int most = backward ? 512 : 1024;  // threads of a resident workgroup (backward: twice the sums in LDS)
   p.vec = 16 / es;
   if (widest_slab(s.D, s.G, p.vec, 1024) == 0) p.vec = 1;
   const int v = p.vec, alone = static_cast<int>((static_cast<int64_t>(s.D) + v - 1) / v);  // lanes of one group
@@ -83,14 +82,17 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
       }
     }
   }
-  // A sample's slab in registers, up to eight rows a thread.
-  if (p.kind == NormPlan::kWide) {
+  // A sample's slab in registers: one row a thread, or up to eight (backward,
+  // with twice the inputs: four).
+  const int several = backward ? 4 : 8;
+  for (int P = 1; P <= several && p.kind == NormPlan::kWide; P *= several) {
+    const int most = P == 1 ? kNormThreads : kHeldThreads;
     for (int threads = 256; threads <= most && p.kind == NormPlan::kWide; threads *= 2) {
       for (int lanes = std::min(threads, 256); lanes >= 1; lanes /= 2) {
         const int gs = widest_slab(s.D, s.G, v, std::max(lanes, alone));
         if (gs == 0) continue;
         take_slab(s, gs, v, threads);
-        if (s.lx > threads || s.S > 8 * s.ty) continue;
+        if (s.lx > threads || s.S > P * s.ty) continue;
         // rows of less than 64 bytes waste the lines that they touch
         if (s.lx * v * es < 64 && s.slabs > 1) break;
         // narrower while workgroups are few, down to 128 bytes a row
@@ -102,7 +104,7 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
         s.ty = std::min(s.ty, std::max(1, s.S));
         s.threads = std::min(threads, round64(static_cast<int64_t>(s.lx) * s.ty));
         if (samples * s.slabs < 64 && bytes > (int64_t(2) << 20)) break;  // too few to fill the card: split
-        p.kind = NormPlan::kResident;
+        p.kind = P == 1 ? NormPlan::kRow : NormPlan::kResident;
         s.across = static_cast<int>(std::min<int64_t>(samples, std::max(1, (backward ? 1024 : 8192) / s.slabs)));
         break;
       }

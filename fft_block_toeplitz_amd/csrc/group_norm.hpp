@@ -24,6 +24,10 @@
 namespace fftmv {
 
 constexpr int kNormThreads = 1024;  // at most
+// of a resident workgroup that holds several rows a thread (256 registers each)
+constexpr int kHeldThreads = 512;
+template <int Q, int P>
+constexpr int kResidentThreads = Q * P > 1 ? kHeldThreads : kNormThreads;
 
 // How a field is cut into slabs and workgroups.
 struct NormShape {
@@ -137,7 +141,7 @@ __device__ __forceinline__ void team_sums(const float *part, const NormShape &s,
 // ------------------------------------------------------------ resident
 // Q samples at a time, up to P rows of each in a thread's registers.
 template <typename T, int VEC, bool WHOLE, int ACT, int Q, int P>
-__global__ __launch_bounds__(kNormThreads) void norm_forward_kernel(fftmv_group_norm_t g, NormShape s) {
+__global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(fftmv_group_norm_t g, NormShape s) {
   extern __shared__ float lds[];
   const int slots = part_slots<VEC, WHOLE>(s);
   float *part = lds, *mean = lds + Q * slots, *rstd = mean + Q * s.gs;
@@ -264,7 +268,7 @@ __device__ __forceinline__ void put_param_sums(const fftmv_group_norm_t &g, cons
 }
 
 template <typename T, int VEC, bool WHOLE, int ACT, int Q, int P>
-__global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(fftmv_group_norm_t g, NormShape s) {
+__global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel(fftmv_group_norm_t g, NormShape s) {
   extern __shared__ float lds[];
   const int slots = part_slots<VEC, WHOLE>(s);
   float *part = lds, *stat = lds + 2 * Q * slots, *m = stat + 2 * Q * s.gs;
@@ -339,6 +343,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(fftmv_group
       put_part<VEC, WHOLE>(part + (Q + q) * slots, s, l, t2);
     }
     __syncthreads();
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      forget(v[q]);
+      forget(d[q]);
+    }
     team_sums<VEC, WHOLE>(part, s, l.ng, 2 * Q, [&](int pair, float sum) {
       const int q = pair / l.ng % Q;
       const int h = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
@@ -363,6 +372,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_backward_kernel(fftmv_group
             o[e] = row < held[q] ? stat[2 * k + 1] * (fmaf(dz, w[e], -m[k]) - xh * m[Q * l.ng + k]) : 0.0f;
           }
           store_vec<T, VEC>(dx + static_cast<int64_t>(row) * g.dx_row, o);
+          row_done();
         }
       }
     }
@@ -803,7 +813,7 @@ __global__ __launch_bounds__(kBlock) void norm_wide_backward_kernel(fftmv_group_
 // ---------------------------------------------------------------- plans
 // What a call launches; decided by sizes alone.
 struct NormPlan {
-  enum Kind { kWide, kTokens, kResident, kSplit } kind = kWide;
+  enum Kind { kWide, kTokens, kRow, kResident, kSplit } kind = kWide;
   bool whole = false;
   int vec = 1;
   NormShape s{};
@@ -832,6 +842,9 @@ hipError_t launch_norm_forward_vec(const fftmv_group_norm_t &g, const NormPlan &
   if (p.kind == NormPlan::kTokens) {
     if (p.whole) norm_forward_kernel<T, VEC, true, ACT, 4, 1><<<blocks, threads, p.lds, s>>>(g, h);
     else norm_forward_kernel<T, VEC, false, ACT, 4, 1><<<blocks, threads, p.lds, s>>>(g, h);
+  } else if (p.kind == NormPlan::kRow) {
+    if (p.whole) norm_forward_kernel<T, VEC, true, ACT, 1, 1><<<blocks, threads, p.lds, s>>>(g, h);
+    else norm_forward_kernel<T, VEC, false, ACT, 1, 1><<<blocks, threads, p.lds, s>>>(g, h);
   } else {
     if (p.whole) norm_forward_kernel<T, VEC, true, ACT, 1, 8><<<blocks, threads, p.lds, s>>>(g, h);
     else norm_forward_kernel<T, VEC, false, ACT, 1, 8><<<blocks, threads, p.lds, s>>>(g, h);
@@ -857,9 +870,12 @@ hipError_t launch_norm_backward_vec(const fftmv_group_norm_t &g, const NormPlan 
   if (p.kind == NormPlan::kTokens) {
     if (p.whole) norm_backward_kernel<T, VEC, true, ACT, 2, 1><<<blocks, threads, p.lds, s>>>(g, h);
     else norm_backward_kernel<T, VEC, false, ACT, 2, 1><<<blocks, threads, p.lds, s>>>(g, h);
+  } else if (p.kind == NormPlan::kRow) {
+    if (p.whole) norm_backward_kernel<T, VEC, true, ACT, 1, 1><<<blocks, threads, p.lds, s>>>(g, h);
+    else norm_backward_kernel<T, VEC, false, ACT, 1, 1><<<blocks, threads, p.lds, s>>>(g, h);
   } else {
-    if (p.whole) norm_backward_kernel<T, VEC, true, ACT, 1, 8><<<blocks, threads, p.lds, s>>>(g, h);
-    else norm_backward_kernel<T, VEC, false, ACT, 1, 8><<<blocks, threads, p.lds, s>>>(g, h);
+    if (p.whole) norm_backward_kernel<T, VEC, true, ACT, 1, 4><<<blocks, threads, p.lds, s>>>(g, h);
+    else norm_backward_kernel<T, VEC, false, ACT, 1, 4><<<blocks, threads, p.lds, s>>>(g, h);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || h.across == 1) return e;

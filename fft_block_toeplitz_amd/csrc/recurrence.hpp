@@ -388,25 +388,6 @@ __device__ __forceinline__ void store_row(const fftmv_recurrence_t &r, const Sca
     store_vec<T, VEC>(p + row_offset(r, a, c, q, i, sb, st), f);
 }
 
-// Hides where a value came from, so that what was computed from it before is
-// computed again instead of kept: the decays of a thread's elements take 32
-// registers each time they are kept, an exponential when they are not.
-template <typename T, int VEC>
-__device__ __forceinline__ void forget(Vec<T, VEC> (&v)[kRows]) {
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if constexpr (VEC * sizeof(T) >= 8) {
-      auto w = __builtin_bit_cast(typename Words<VEC * sizeof(T)>::type, v[i]);
-      asm volatile("" : "+v"(w));
-      v[i] = __builtin_bit_cast(Vec<T, VEC>, w);
-    }
-  }
-}
-
-// Keeps the compiler from starting on further rows' exponentials before a row
-// is done: it would hold them all, and spill.
-__device__ __forceinline__ void row_done() { __builtin_amdgcn_sched_barrier(0); }
-
 // VEC channels of a [batch][channels] state, zeros where there is none.
 template <int VEC>
 __device__ __forceinline__ void load_state(const float *p, int64_t seq, int64_t channels, int64_t ch,

@@ -80,6 +80,25 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
   }
 }
 
+// Hides where a value came from, so that what was computed from it before is
+// computed again instead of kept: what a thread's 32 elements became takes 32
+// registers, an exponential more where it is computed again.
+template <typename T, int VEC, int N>
+__device__ __forceinline__ void forget(Vec<T, VEC> (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (VEC * sizeof(T) >= 8) {
+      auto w = __builtin_bit_cast(typename Words<VEC * sizeof(T)>::type, v[i]);
+      asm volatile("" : "+v"(w));
+      v[i] = __builtin_bit_cast(Vec<T, VEC>, w);
+    }
+  }
+}
+
+// Keeps the compiler from starting on further rows' exponentials before a row
+// is done: it would hold them all, and spill.
+__device__ __forceinline__ void row_done() { __builtin_amdgcn_sched_barrier(0); }
+
 // ------------------------------------------------ terms of the recurrence
 // a = the decay, rest = 1 - a, slope = da/dg, each to a few ulp of FP32.
 // sigmoid: with t = exp(-|g|) <= 1 nothing overflows, 1 - a comes from t
