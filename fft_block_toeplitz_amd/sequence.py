@@ -133,7 +133,7 @@ def _differs(t, shape, like, name):
 
 def _field(t, shape, like, name):
     """(pointer, batch stride, step stride) of a channels-last field of this shape, of ``like``'s type and device."""
-    if t is not like and (t.shape != shape or t.dtype != like.dtype or t.get_device() != like.get_device()):
+    if t is not like and (t.shape != shape or t.dtype is not like.dtype or t.get_device() != like.get_device()):
         raise _differs(t, shape, like, name)
     st = t.stride()
     if st[-1] != 1 and shape[-1] != 1 and t.numel():
@@ -176,7 +176,7 @@ def _span(t):
 def _output(out, like, inputs):
     """A new contiguous tensor like ``like``, or ``out`` after its checks."""
     if out is None:
-        return _torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return _torch.empty_like(like, memory_format=_torch.contiguous_format)
     if out.shape != like.shape or out.dtype != like.dtype or out.device != like.device or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {like.dtype} tensor {tuple(like.shape)} on {like.device}")
     lo, hi = _span(out)
@@ -205,21 +205,17 @@ class _On:
         self.inside.__exit__(*what)
 
 
-def _current_stream():
-    return _torch.cuda.current_stream().cuda_stream
+def _elsewhere(stream, call, *args, **kwargs):
+    """The call with another stream current."""
+    _torch_module()
+    tensors = [t for t in (*args, *kwargs.values()) if isinstance(t, _torch.Tensor) and t.is_cuda]
+    with _On(stream, *tensors):
+        return call(*args, **kwargs)
 
 
-def _on_stream(call):
-    """Gives a public function its ``stream`` argument: the call runs with that stream current."""
-    @functools.wraps(call)
-    def wrapped(*args, stream=None, **kwargs):
-        if stream is None:
-            return call(*args, **kwargs)
-        _torch_module()
-        tensors = [t for t in (*args, *kwargs.values()) if isinstance(t, _torch.Tensor) and t.is_cuda]
-        with _On(stream, *tensors):
-            return call(*args, **kwargs)
-    return wrapped
+def _current_stream(device):
+    """Handle of the device's current stream (torch.cuda.current_stream builds an object first: 3 us)."""
+    return _torch._C._cuda_getCurrentRawStream(device)
 
 
 # ---- the recurrence
@@ -228,7 +224,7 @@ _sizes = functools.lru_cache(maxsize=1024)(fftmv_recurrence_sizes)  # functions 
 _norm_sizes = functools.lru_cache(maxsize=1024)(fftmv_group_norm_workspace)
 
 
-def _workspace(sizes, stream, like):
+def _workspace(sizes, device, stream, like):
     """(counters' address and bytes, workspace's address and bytes, number of
     the call on it). Calls of one stream share a workspace, which is kept and
     grown; a call under graph capture gets memory of the graph's own, cleared
@@ -240,12 +236,12 @@ def _workspace(sizes, stream, like):
     if _torch.cuda.is_current_stream_capturing():
         a, b = new(few), new(many)
         return a.data_ptr(), few, b.data_ptr(), many, 1
-    w = _workspaces.get((like.get_device(), stream))
+    w = _workspaces.get((device, stream))
     if w is None or w[1] < few or w[3] < many:
         if w is not None:
             few, many = max(few, w[1]), max(many, w[3])
         a, b = new(few), new(many)
-        w = _workspaces[like.get_device(), stream] = [a.data_ptr(), few, b.data_ptr(), many, 0, a, b]
+        w = _workspaces[device, stream] = [a.data_ptr(), few, b.data_ptr(), many, 0, a, b]
     elif w[4] == 2 ** 32 - 1:
         w[6].zero_()
         w[4] = 0
@@ -272,9 +268,8 @@ def _sequences(x, lengths, offsets):
     return B, T, C
 
 
-@_on_stream
 def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths=None, offsets=None, save=False,
-               out=None):
+               out=None, stream=None):
     """Gated linear recurrence along time, per sequence and channel:
 
         h_t = a_t h_{t-1} + u_t,   h_{-1} = h0 (zeros when None)
@@ -291,6 +286,9 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     Returns h (x's type) and the last states, float32 [batch, channels];
     with ``save`` also the carries that ``recurrence_backward`` needs. Runs
     on ``stream`` (default: the current one), without synchronising."""
+    if stream is not None:
+        return _elsewhere(stream, recurrence, x, gate, h0, decay=decay, drive=drive, lengths=lengths, offsets=offsets,
+                          save=save, out=out)
     dtype = _dtype_of(x, "x")
     B, T, C = _sequences(x, lengths, offsets)
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
@@ -299,27 +297,30 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     h0p = _floats(h0, (B, C), x, "h0")
     lens, offs = _ints(lengths, B, x, "lengths"), _ints(offsets, B + 1, x, "offsets")
     h = _output(out, x, (x, gate))
-    last = _torch.empty((B, C), dtype=_torch.float32, device=x.device)
+    last = x.new_empty((B, C), dtype=_torch.float32)
     if B == 0:
         h.zero_()
         return (h, last, last) if save else (h, last)
     sizes = _sizes(B, T, C, packed)
-    carries = _torch.empty((sizes[0], C), dtype=_torch.float32, device=x.device) if save else None
-    stream = _current_stream()
-    *ws, call = _workspace(sizes, stream, x)
+    carries = x.new_empty((sizes[0], C), dtype=_torch.float32) if save else None
+    device = x.get_device()
+    stream = _current_stream(device)
+    *ws, call = _workspace(sizes, device, stream, x)
     r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, carries.data_ptr() if save else 0,
                          *ws, h.data_ptr(), T * C, C, last.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     fftmv_recurrence_forward(r, stream)
     return (h, last, carries) if save else (h, last)
 
 
-@_on_stream
 def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="sigmoid", drive="complement",
-                        lengths=None, offsets=None):
+                        lengths=None, offsets=None, stream=None):
     """Gradients of ``recurrence``: (dx, dgate, dh0) from dh, the gradient of
     h, and dh_last, that of the last states (zeros when None). x, gate, h0
     and the keywords are the forward call's, ``carries`` what it saved; h is
     recomputed from them in float32."""
+    if stream is not None:
+        return _elsewhere(stream, recurrence_backward, dh, x, gate, carries, h0, dh_last, decay=decay, drive=drive,
+                          lengths=lengths, offsets=offsets)
     dtype = _dtype_of(x, "x")
     B, T, C = _sequences(x, lengths, offsets)
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
@@ -331,27 +332,30 @@ def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="s
         raise ValueError("carries must be what recurrence(..., save=True) returned")
     cp = _floats(carries, (sizes[0], C), x, "carries")
     lens, offs = _ints(lengths, B, x, "lengths"), _ints(offsets, B + 1, x, "offsets")
-    dx = _torch.empty(shape, dtype=x.dtype, device=x.device)
-    dg = _torch.empty(shape, dtype=x.dtype, device=x.device)
-    dh0 = _torch.empty((B, C), dtype=_torch.float32, device=x.device)
+    dx = _torch.empty_like(x, memory_format=_torch.contiguous_format)
+    dg = _torch.empty_like(dx)
+    dh0 = x.new_empty((B, C), dtype=_torch.float32)
     if B == 0:
         return dx.zero_(), dg.zero_(), dh0
-    stream = _current_stream()
-    *ws, call = _workspace(sizes, stream, x)
+    device = x.get_device()
+    stream = _current_stream(device)
+    *ws, call = _workspace(sizes, device, stream, x)
     r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, cp, *ws, 0, 0, 0, 0, *df, lp,
                          dx.data_ptr(), T * C, C, dg.data_ptr(), T * C, C, dh0.data_ptr())
     fftmv_recurrence_backward(r, stream)
     return dx, dg, dh0
 
 
-@_on_stream
-def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="complement", out=None):
+def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="complement", out=None,
+                    stream=None):
     """One time step of many streams against a cache of states, in place.
     x, gate: [batch, channels]; state: float32 [places, channels]; slots:
     int32 [batch], the place of each stream (None: stream b has place b). A
     slot outside the cache, -1 say, marks an idle stream: zeros come back
     and no state changes. Slots of one call must differ. Returns h [batch,
     channels]."""
+    if stream is not None:
+        return _elsewhere(stream, recurrence_step, x, gate, state, slots, decay=decay, drive=drive, out=out)
     dtype = _dtype_of(x, "x")
     shape = x.shape
     if len(shape) != 2:
@@ -373,7 +377,7 @@ def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="compl
     if B == 0 or places == 0:
         return h.zero_()
     fftmv_recurrence_step(_STEP.pack(B, C, places, dtype, *kinds, 0, xp, xs, gp, gs, state.data_ptr(),
-                                     max(ss[0], C), sp, h.data_ptr(), C), _current_stream())
+                                     max(ss[0], C), sp, h.data_ptr(), C), _current_stream(x.get_device()))
     return h
 
 
@@ -381,7 +385,7 @@ def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="compl
 def _scratch(samples, rows, channels, groups, backward, like):
     """(scratch memory or None, its bytes) of a call of this shape."""
     need = _norm_sizes(samples, rows, channels, groups, _types[like.dtype], backward)
-    return (_torch.empty(need, dtype=_torch.uint8, device=like.device), need) if need else (None, 0)
+    return (like.new_empty(need, dtype=_torch.uint8), need) if need else (None, 0)
 
 
 def _samples(x):
@@ -399,8 +403,8 @@ def _samples(x):
                          "make it contiguous") from None
 
 
-@_on_stream
-def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, lengths=None, save=False, out=None):
+def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, lengths=None, save=False, out=None,
+               stream=None):
     """Group normalisation with an activation, channels last:
 
         y = act((x - mean) rstd weight + bias),   rstd = 1 / sqrt(var + eps)
@@ -414,6 +418,9 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
 
     Returns y (x's type); with ``save`` also the statistics, float32
     [samples, groups, 2] (mean, rstd), that ``group_norm_backward`` needs."""
+    if stream is not None:
+        return _elsewhere(stream, group_norm, x, groups, weight, bias, eps=eps, activation=activation, lengths=lengths,
+                          save=save, out=out)
     dtype = _dtype_of(x, "x")
     v = _samples(x)
     N, S, C = shape = v.shape
@@ -426,21 +433,23 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
     wp, bp = _floats(weight, (C,), x, "weight"), _floats(bias, (C,), x, "bias")
     lens = _ints(lengths, N, x, "lengths")
     y = _output(out, x, (x,))
-    stats = _torch.empty((N, groups, 2), dtype=_torch.float32, device=x.device) if save else None
+    stats = x.new_empty((N, groups, 2), dtype=_torch.float32) if save else None
     if N == 0:
         return (y, stats) if save else y
     ws, need = _scratch(N, S, C, groups, False, x)
     g = _GROUP_NORM.pack(N, S, C, groups, dtype, act, eps, 0, lens, *xf, wp, bp, stats.data_ptr() if save else 0,
                          ws.data_ptr() if need else 0, need, y.data_ptr(), S * C, C, 0, 0, 0, 0, 0, 0, 0, 0)
-    fftmv_group_norm_forward(g, _current_stream())
+    fftmv_group_norm_forward(g, _current_stream(x.get_device()))
     return (y, stats) if save else y
 
 
-@_on_stream
-def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, *, activation=None, lengths=None):
+def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, *, activation=None, lengths=None, stream=None):
     """Gradients of ``group_norm``: (dx, dweight, dbias), the last two float32
     [channels], from dy, the gradient of y. x, the parameters and the
     keywords are the forward call's, ``stats`` what it saved."""
+    if stream is not None:
+        return _elsewhere(stream, group_norm_backward, dy, x, stats, groups, weight, bias, activation=activation,
+                          lengths=lengths)
     dtype = _dtype_of(x, "x")
     v = _samples(x)
     N, S, C = shape = v.shape
@@ -455,8 +464,8 @@ def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, *, activat
         raise ValueError("stats must be what group_norm(..., save=True) returned")
     sp = _floats(stats, (N, groups, 2), x, "stats")
     lens = _ints(lengths, N, x, "lengths")
-    dx = _torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    both = _torch.empty((2, C), dtype=_torch.float32, device=x.device)
+    dx = _torch.empty_like(x, memory_format=_torch.contiguous_format)
+    both = x.new_empty((2, C), dtype=_torch.float32)
     dw, db = both[0], both[1]
     if N == 0:
         both.zero_()
@@ -464,5 +473,5 @@ def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, *, activat
     ws, need = _scratch(N, S, C, groups, True, x)
     g = _GROUP_NORM.pack(N, S, C, groups, dtype, act, 0.0, 0, lens, *xf, wp, bp, sp, ws.data_ptr() if need else 0, need,
                          0, 0, 0, *df, dx.data_ptr(), S * C, C, dw.data_ptr(), db.data_ptr())
-    fftmv_group_norm_backward(g, _current_stream())
+    fftmv_group_norm_backward(g, _current_stream(x.get_device()))
     return dx, dw, db
