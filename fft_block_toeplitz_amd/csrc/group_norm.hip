@@ -27,6 +27,7 @@ void take_slab(NormShape &s, int gs, int vec, int threads) {
   s.slabs = (s.G + gs - 1) / gs;
   s.lx = (gs * s.D + vec - 1) / vec;
   s.ty = threads / s.lx;
+  s.sub = 1;
   s.threads = threads;
 }
 
@@ -38,7 +39,8 @@ void take_team(NormShape &s, int sums) {
 }  // namespace
 
 hipError_t launch_param_sums(const fftmv_group_norm_t &g, int64_t rows, hipStream_t s) {
-  param_sums_kernel<<<static_cast<unsigned>((g.channels + kWave - 1) / kWave), kBlock, 0, s>>>(g, rows);
+  param_sums_kernel<<<static_cast<unsigned>((g.channels + kSumChannels - 1) / kSumChannels), kBlock, 0,
+                      s>>>(g, rows);
   return hipGetLastError();
 }
 
@@ -62,23 +64,27 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   const int64_t bytes = samples * std::max<int64_t>(rows, 1) * channels * es;
   const int Q = backward ? 2 : 4;
 
-  // Single rows, or a few: Q samples at a time, side by side in a thread's
-  // registers, so that a barrier serves all of them; where that leaves too
-  // few workgroups for the CUs, the resident form below takes them one by one.
+  // Single rows, or a few: Q samples at a time in a thread's registers, so
+  // that a barrier serves all of them, and narrow ones side by side; where
+  // that leaves too few workgroups for the CUs, the form below takes them one
+  // by one.
   if (rows <= 8) {
     const int R = std::max(1, s.S);
-    const int threads = alone * R <= 256 ? 256 : round64(static_cast<int64_t>(alone) * R);
-    if (threads <= (p.whole ? 512 : 256)) {
-      const int gs = widest_slab(s.D, s.G, v, threads / R);
-      if (gs > 0) {
-        take_slab(s, gs, v, threads);
-        s.threads = std::min(threads, round64(static_cast<int64_t>(s.lx) * R));
-        s.ty = std::min(s.threads / s.lx, R);
-        const int64_t turns = (samples + Q - 1) / Q;
-        if (s.ty >= R && turns * s.slabs >= 256) {
-          p.kind = NormPlan::kTokens;
-          s.across = static_cast<int>(std::min<int64_t>(turns, std::max(1, (backward ? 1024 : 2048) / s.slabs)));
-        }
+    const int64_t least = static_cast<int64_t>(alone) * R;
+    const int threads = least <= 256 ? 256 : least <= 512 ? 512 : 0;
+    const int gs = threads ? widest_slab(s.D, s.G, v, threads / R) : 0;
+    if (gs > 0 && (threads == 256 || p.whole)) {
+      take_slab(s, gs, v, threads);
+      constexpr int kMostSums = 512;  // of a thread's sample, whose statistics lie in LDS
+      s.sub = std::min(s.ty / R, std::max(1, kMostSums / s.gs));
+      s.ty = R;
+      s.threads = round64(static_cast<int64_t>(s.lx) * s.ty * s.sub);
+      while (s.sub > 1 && (samples + Q * s.sub - 1) / (Q * s.sub) * s.slabs < 512) s.sub /= 2;
+      s.threads = round64(static_cast<int64_t>(s.lx) * s.ty * s.sub);
+      const int64_t turns = (samples + Q * s.sub - 1) / (Q * s.sub);
+      if (turns * s.slabs >= 256) {
+        p.kind = NormPlan::kTokens;
+        s.across = static_cast<int>(std::min<int64_t>(turns, std::max(1, (backward ? 1024 : 2048) / s.slabs)));
       }
     }
   }
@@ -93,6 +99,8 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
         if (gs == 0) continue;
         take_slab(s, gs, v, threads);
         if (s.lx > threads || s.S > P * s.ty) continue;
+        // one row a thread: for few rows, or where one takes most of the threads
+        if (P == 1 && s.lx * s.S > 256 && alone <= 256) continue;
         // rows of less than 64 bytes waste the lines that they touch
         if (s.lx * v * es < 64 && s.slabs > 1) break;
         // narrower while workgroups are few, down to 128 bytes a row
@@ -112,10 +120,10 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   }
   if (p.kind != NormPlan::kWide) {
     const int q = p.kind == NormPlan::kTokens ? Q : 1, sets = backward ? 2 * q : q;
-    take_team(s, sets * s.gs);
-    const size_t slots = static_cast<size_t>(s.ty) * s.lx * (p.whole ? 1 : v);
-    size_t floats = sets * slots + (backward ? 4 : 2) * static_cast<size_t>(q) * s.gs;
-    if (backward) floats = std::max(floats, static_cast<size_t>(s.ty) * s.lx * v);
+    take_team(s, sets * s.sub * s.gs);
+    const size_t flat = static_cast<size_t>(s.sub) * s.ty * s.lx;
+    size_t floats = sets * flat * (p.whole ? 1 : v) + (backward ? 4 : 2) * static_cast<size_t>(q) * s.sub * s.gs;
+    if (backward) floats = std::max(floats, flat * v);
     p.lds = floats * 4;
     p.rows = s.across;
     p.workspace = backward && s.across > 1 ? static_cast<size_t>(s.across) * channels * 8 : 0;

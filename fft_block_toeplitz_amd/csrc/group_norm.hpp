@@ -35,7 +35,8 @@ struct NormShape {
   int S, D, G;
   int threads;      // of a workgroup
   int gs, slabs;    // groups of a slab, slabs of a row
-  int lx, ty;       // lanes across a slab, rows side by side
+  int lx, ty;       // lanes across a slab, rows of a sample side by side
+  int sub;          // samples side by side (1 but for short samples)
   int team;         // threads that sum one group (a power of two, at most a wave)
   int across;       // workgroups over the samples of one slab (resident), or row ranges of a sample (split)
   int range;        // split: rows of a range
@@ -51,20 +52,23 @@ __device__ __forceinline__ int held_rows(const fftmv_group_norm_t &g, int64_t n)
 // This thread's place in a slab.
 template <int VEC>
 struct SlabLane {
-  int ng, wd;     // groups and channels of this slab
-  int lane, row;  // row: first of its rows, ty apart
-  int c;          // first of its VEC channels, within the slab. The last lane steps back to end with the slab: the
-                  // channels that it repeats go to the same places with the same values
-  int64_t ch0;    // the slab's first channel
+  int ng, wd;           // groups and channels of this slab
+  int lane, flat;       // flat: its row of lanes
+  int sub, row;         // which of the samples side by side, and the first of its rows there (ty apart)
+  int c;                // first of its VEC channels, within the slab. The last lane steps back to end with the slab:
+                        // the channels that it repeats go to the same places with the same values
+  int64_t ch0;          // the slab's first channel
   bool in;
   __device__ SlabLane(const NormShape &s, int slab) {
     ng = s.gs < s.G - slab * s.gs ? s.gs : s.G - slab * s.gs;
     wd = ng * s.D;
     ch0 = static_cast<int64_t>(slab) * s.gs * s.D;
     lane = threadIdx.x % s.lx;
-    row = threadIdx.x / s.lx;
+    flat = threadIdx.x / s.lx;
+    sub = s.sub > 1 ? flat / s.ty : 0;
+    row = flat - sub * s.ty;
     c = lane * VEC;
-    in = row < s.ty && c < wd;
+    in = flat < s.ty * s.sub && c < wd;
     if (c + VEC > wd) c = wd - VEC;
   }
 };
@@ -90,8 +94,8 @@ struct GroupOf {
   __device__ __forceinline__ int operator[](int e) const { return g[WHOLE ? 0 : e]; }
 };
 
-// A thread's contribution to the sums of its groups, in `part` (one row of
-// slots for each of the ty rows): one slot a thread, or one a channel.
+// A thread's contribution to the sums of its groups, in `part` (a row of slots
+// for each row of lanes): one slot a thread, or one a channel.
 template <int VEC, bool WHOLE>
 __device__ __forceinline__ void put_part(float *part, const NormShape &s, const SlabLane<VEC> &l, const float (&v)[VEC]) {
   if (!l.in) return;
@@ -99,42 +103,45 @@ __device__ __forceinline__ void put_part(float *part, const NormShape &s, const 
     float sum = v[0];
 #pragma unroll
     for (int e = 1; e < VEC; ++e) sum += v[e];
-    part[l.row * s.lx + l.lane] = sum;
+    part[l.flat * s.lx + l.lane] = sum;
   } else {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) part[l.row * (s.lx * VEC) + l.c + e] = v[e];
+    for (int e = 0; e < VEC; ++e) part[l.flat * (s.lx * VEC) + l.c + e] = v[e];
   }
 }
 template <int VEC, bool WHOLE>
 __device__ __forceinline__ int part_slots(const NormShape &s) {
-  return s.ty * s.lx * (WHOLE ? 1 : VEC);
+  return s.sub * s.ty * s.lx * (WHOLE ? 1 : VEC);
 }
 
-// Sums of `sets` x ng groups: f(set * ng + group, sum) by one thread each. The
-// slots of set k start at part + k * slots. All of a workgroup's threads call it.
+// Sums of `sets` x ng groups, a set being the ty rows of slots of one sample:
+// f(set * ng + group, sum) by one thread each. All threads call it.
 template <int VEC, bool WHOLE, typename F>
 __device__ __forceinline__ void team_sums(const float *part, const NormShape &s, int ng, int sets, F f) {
-  const int gw = WHOLE ? s.D / VEC : s.D, lw = WHOLE ? s.lx : s.lx * VEC;
-  const int slots = s.ty * lw, items = s.ty * gw;
-  const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
-  for (int pair = threadIdx.x / s.team; pair < sets * ng; pair += teams) {
+  const int gw = WHOLE ? s.D / VEC : s.D, lw = WHOLE ? s.lx : s.lx * VEC, slots = s.ty * lw;
+  // the team as `across` threads along a row of slots, its rest over the rows
+  int across = 1;
+  while (across < gw && across < s.team) across *= 2;
+  const int me = threadIdx.x & (s.team - 1), first = me & (across - 1), row = me / across, rows = s.team / across;
+  for (int pair = threadIdx.x / s.team; pair < sets * ng; pair += blockDim.x / s.team) {
     const int set = pair / ng, g = pair - set * ng;
     const float *base = part + set * slots + g * gw;
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int t = me / gw, j = me - t * gw, k = 0;
-    for (int i = me; i < items; i += s.team) {
-      const float v = base[t * lw + j];
-      sum[0] += k == 0 ? v : 0.0f;
-      sum[1] += k == 1 ? v : 0.0f;
-      sum[2] += k == 2 ? v : 0.0f;
-      sum[3] += k == 3 ? v : 0.0f;
-      k = (k + 1) & 3;
-      j += s.team;
-      while (j >= gw) j -= gw, ++t;
+    float sum = 0.0f;
+    for (int t = row; t < s.ty; t += rows) {
+      const float *p = base + t * lw;
+      float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+      int j = first;
+      for (; j + 3 * across < gw; j += 4 * across) {
+        s0 += p[j];
+        s1 += p[j + across];
+        s2 += p[j + 2 * across];
+        s3 += p[j + 3 * across];
+      }
+      for (; j < gw; j += across) s0 += p[j];
+      sum += (s0 + s1) + (s2 + s3);
     }
-    float v = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-    for (int m = s.team / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
-    if (me == 0) f(pair, v);
+    for (int m = s.team / 2; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
+    if (me == 0) f(pair, sum);
   }
 }
 
@@ -144,7 +151,7 @@ template <typename T, int VEC, bool WHOLE, int ACT, int Q, int P>
 __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(fftmv_group_norm_t g, NormShape s) {
   extern __shared__ float lds[];
   const int slots = part_slots<VEC, WHOLE>(s);
-  float *part = lds, *mean = lds + Q * slots, *rstd = mean + Q * s.gs;
+  float *part = lds, *mean = lds + Q * slots, *rstd = mean + Q * s.sub * s.gs;
   const int slab = blockIdx.x % s.slabs;
   const SlabLane<VEC> l(s, slab);
   const GroupOf<VEC, WHOLE> group(l.c, s.D);
@@ -153,18 +160,19 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
     load_params(g.weight, l.ch0 + l.c, 1.0f, w);
     load_params(g.bias, l.ch0 + l.c, 0.0f, b);
   }
-  const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * Q;
-  for (int64_t n0 = static_cast<int64_t>(blockIdx.x / s.slabs) * Q; n0 < s.N; n0 += step) {
+  const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * (Q * s.sub);
+  for (int64_t n0 = static_cast<int64_t>(blockIdx.x / s.slabs) * (Q * s.sub); n0 < s.N; n0 += step) {
     Vec<T, VEC> v[Q][P];
     int held[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      held[q] = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
-      const T *x = static_cast<const T *>(g.x) + (n0 + q) * g.x_sample + l.ch0 + l.c;
+      const int64_t n = n0 + q * s.sub + l.sub;
+      held[q] = l.in && n < s.N ? held_rows(g, n) : 0;
+      const T *x = static_cast<const T *>(g.x) + n * g.x_sample + l.ch0 + l.c;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         v[q][p] = Vec<T, VEC>{};
-        if (l.in && l.row + p * s.ty < held[q])
+        if (l.row + p * s.ty < held[q])
           v[q][p] = load_vec<T, VEC>(x + static_cast<int64_t>(l.row + p * s.ty) * g.x_row);
       }
     }
@@ -180,9 +188,9 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
       put_part<VEC, WHOLE>(part + q * slots, s, l, sum);
     }
     __syncthreads();
-    team_sums<VEC, WHOLE>(part, s, l.ng, Q, [&](int pair, float sum) {
-      const int q = pair / l.ng;
-      const int h = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
+    team_sums<VEC, WHOLE>(part, s, l.ng, Q * s.sub, [&](int pair, float sum) {
+      const int64_t n = n0 + pair / l.ng;
+      const int h = n < s.N ? held_rows(g, n) : 0;
       mean[pair] = h ? sum / (static_cast<float>(h) * s.D) : 0.0f;
     });
     __syncthreads();
@@ -191,7 +199,7 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
       float sq[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const float m = l.in ? mean[q * l.ng + group[e]] : 0.0f;
+        const float m = l.in ? mean[(q * s.sub + l.sub) * l.ng + group[e]] : 0.0f;
         sq[e] = 0.0f;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
@@ -202,13 +210,13 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
       put_part<VEC, WHOLE>(part + q * slots, s, l, sq);
     }
     __syncthreads();
-    team_sums<VEC, WHOLE>(part, s, l.ng, Q, [&](int pair, float sum) {
-      const int q = pair / l.ng;
-      const int h = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
+    team_sums<VEC, WHOLE>(part, s, l.ng, Q * s.sub, [&](int pair, float sum) {
+      const int64_t n = n0 + pair / l.ng;
+      const int h = n < s.N ? held_rows(g, n) : 0;
       const float r = h ? 1.0f / sqrtf(sum / (static_cast<float>(h) * s.D) + g.eps) : 0.0f;
       rstd[pair] = r;
-      if (g.stats && n0 + q < s.N) {
-        float *to = g.stats + 2 * ((n0 + q) * s.G + static_cast<int64_t>(slab) * s.gs + (pair - q * l.ng));
+      if (g.stats && n < s.N) {
+        float *to = g.stats + 2 * (n * s.G + static_cast<int64_t>(slab) * s.gs + pair % l.ng);
         to[0] = mean[pair];
         to[1] = r;
       }
@@ -217,8 +225,9 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
     if (l.in) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        if (n0 + q >= s.N) break;
-        T *y = static_cast<T *>(g.y) + (n0 + q) * g.y_sample + l.ch0 + l.c;
+        const int64_t n = n0 + q * s.sub + l.sub;
+        if (n >= s.N) break;
+        T *y = static_cast<T *>(g.y) + n * g.y_sample + l.ch0 + l.c;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           const int row = l.row + p * s.ty;
@@ -226,7 +235,7 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
           float o[VEC];
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            const int k = q * l.ng + group[e];
+            const int k = (q * s.sub + l.sub) * l.ng + group[e];
             o[e] = row < held[q] ? activate<ACT>(fmaf((v[q][p][e] - mean[k]) * rstd[k], w[e], b[e])) : 0.0f;
           }
           store_vec<T, VEC>(y + static_cast<int64_t>(row) * g.y_row, o);
@@ -252,9 +261,10 @@ __device__ __forceinline__ void put_param_sums(const fftmv_group_norm_t &g, cons
     __syncthreads();
     for (int c = threadIdx.x; c < l.wd; c += blockDim.x) {
       float sum = 0.0f;
-      for (int t0 = 0; t0 < s.ty; t0 += 16) {
+      const int rows = s.sub * s.ty;
+      for (int t0 = 0; t0 < rows; t0 += 16) {
         float some = 0.0f;
-        for (int t = t0; t < s.ty && t < t0 + 16; ++t) some += lds[t * lw + c];
+        for (int t = t0; t < rows && t < t0 + 16; ++t) some += lds[t * lw + c];
         sum += some;
       }
       if (!alone) {
@@ -271,7 +281,7 @@ template <typename T, int VEC, bool WHOLE, int ACT, int Q, int P>
 __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel(fftmv_group_norm_t g, NormShape s) {
   extern __shared__ float lds[];
   const int slots = part_slots<VEC, WHOLE>(s);
-  float *part = lds, *stat = lds + 2 * Q * slots, *m = stat + 2 * Q * s.gs;
+  float *part = lds, *stat = lds + 2 * Q * slots, *m = stat + 2 * Q * s.sub * s.gs;
   const int slab = blockIdx.x % s.slabs, first = blockIdx.x / s.slabs;
   const SlabLane<VEC> l(s, slab);
   const GroupOf<VEC, WHOLE> group(l.c, s.D);
@@ -282,29 +292,30 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel
     load_params(g.weight, l.ch0 + l.c, 1.0f, w);
     load_params(g.bias, l.ch0 + l.c, 0.0f, b);
   }
-  const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * Q;
-  for (int64_t n0 = static_cast<int64_t>(first) * Q; n0 < s.N; n0 += step) {
+  const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * (Q * s.sub);
+  for (int64_t n0 = static_cast<int64_t>(first) * (Q * s.sub); n0 < s.N; n0 += step) {
     Vec<T, VEC> v[Q][P], d[Q][P];
     int held[Q];
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      held[q] = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
-      const T *x = static_cast<const T *>(g.x) + (n0 + q) * g.x_sample + l.ch0 + l.c;
-      const T *dy = static_cast<const T *>(g.dy) + (n0 + q) * g.dy_sample + l.ch0 + l.c;
+      const int64_t n = n0 + q * s.sub + l.sub;
+      held[q] = l.in && n < s.N ? held_rows(g, n) : 0;
+      const T *x = static_cast<const T *>(g.x) + n * g.x_sample + l.ch0 + l.c;
+      const T *dy = static_cast<const T *>(g.dy) + n * g.dy_sample + l.ch0 + l.c;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
         v[q][p] = d[q][p] = Vec<T, VEC>{};
         const int64_t row = l.row + p * s.ty;
-        if (l.in && row < held[q]) {
+        if (row < held[q]) {
           v[q][p] = load_vec<T, VEC>(x + row * g.x_row);
           d[q][p] = load_vec<T, VEC>(dy + row * g.dy_row);
         }
       }
     }
-    for (int i = threadIdx.x; i < Q * l.ng; i += blockDim.x) {
-      const int q = i / l.ng;
-      if (n0 + q < s.N) {
-        const float *from = g.stats + 2 * ((n0 + q) * s.G + static_cast<int64_t>(slab) * s.gs + (i - q * l.ng));
+    for (int i = threadIdx.x; i < Q * s.sub * l.ng; i += blockDim.x) {
+      const int64_t n = n0 + i / l.ng;
+      if (n < s.N) {
+        const float *from = g.stats + 2 * (n * s.G + static_cast<int64_t>(slab) * s.gs + i % l.ng);
         stat[2 * i] = from[0];
         stat[2 * i + 1] = from[1];
       } else {
@@ -314,7 +325,7 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel
     __syncthreads();
     // dz and xhat of one element, both 0 where no row is held
     auto terms = [&](int q, int p, int e, float &xh, float &dz) {
-      const int k = 2 * (q * l.ng + group[e]);
+      const int k = 2 * ((q * s.sub + l.sub) * l.ng + group[e]);
       const bool on = l.row + p * s.ty < held[q];
       xh = on ? (v[q][p][e] - stat[k]) * stat[k + 1] : 0.0f;
       dz = on ? d[q][p][e] * activate_slope<ACT>(fmaf(xh, w[e], b[e])) : 0.0f;
@@ -348,17 +359,18 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel
       forget(v[q]);
       forget(d[q]);
     }
-    team_sums<VEC, WHOLE>(part, s, l.ng, 2 * Q, [&](int pair, float sum) {
-      const int q = pair / l.ng % Q;
-      const int h = n0 + q < s.N ? held_rows(g, n0 + q) : 0;
+    team_sums<VEC, WHOLE>(part, s, l.ng, 2 * Q * s.sub, [&](int pair, float sum) {
+      const int64_t n = n0 + pair / l.ng % (Q * s.sub);
+      const int h = n < s.N ? held_rows(g, n) : 0;
       m[pair] = h ? sum / (static_cast<float>(h) * s.D) : 0.0f;
     });
     __syncthreads();
     if (l.in) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        if (n0 + q >= s.N) break;
-        T *dx = static_cast<T *>(g.dx) + (n0 + q) * g.dx_sample + l.ch0 + l.c;
+        const int64_t n = n0 + q * s.sub + l.sub;
+        if (n >= s.N) break;
+        T *dx = static_cast<T *>(g.dx) + n * g.dx_sample + l.ch0 + l.c;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           const int row = l.row + p * s.ty;
@@ -368,8 +380,8 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel
           for (int e = 0; e < VEC; ++e) {
             float xh, dz;
             terms(q, p, e, xh, dz);
-            const int k = q * l.ng + group[e];
-            o[e] = row < held[q] ? stat[2 * k + 1] * (fmaf(dz, w[e], -m[k]) - xh * m[Q * l.ng + k]) : 0.0f;
+            const int k = (q * s.sub + l.sub) * l.ng + group[e];
+            o[e] = row < held[q] ? stat[2 * k + 1] * (fmaf(dz, w[e], -m[k]) - xh * m[Q * s.sub * l.ng + k]) : 0.0f;
           }
           store_vec<T, VEC>(dx + static_cast<int64_t>(row) * g.dx_row, o);
           row_done();
@@ -596,11 +608,12 @@ __global__ __launch_bounds__(kNormThreads) void norm_sums_kernel(fftmv_group_nor
   }
 }
 
-// dweight and dbias of 64 channels from `rows` rows of the workspace: four
-// threads a channel, each some of the rows.
+// dweight and dbias of kSumChannels channels (a line of the workspace) from its
+// `rows` rows, shared out over the rest of the threads.
+constexpr int kSumChannels = 16;
 __device__ __forceinline__ void param_sums(const fftmv_group_norm_t &g, int64_t rows, int64_t block, float *lds) {
-  const int c = threadIdx.x % kWave, part = threadIdx.x / kWave, parts = blockDim.x / kWave;
-  const int64_t ch = block * kWave + c;
+  const int c = threadIdx.x % kSumChannels, part = threadIdx.x / kSumChannels, parts = blockDim.x / kSumChannels;
+  const int64_t ch = block * kSumChannels + c;
   const float2 *from = static_cast<const float2 *>(g.workspace);
   float sb = 0.0f, sw = 0.0f;
   if (ch < g.channels)
@@ -623,8 +636,8 @@ __device__ __forceinline__ void param_sums(const fftmv_group_norm_t &g, int64_t 
   __syncthreads();
   if (part == 0 && ch < g.channels) {
     for (int k = 1; k < parts; ++k) {
-      sb += lds[k * kWave + c];
-      sw += lds[blockDim.x + k * kWave + c];
+      sb += lds[k * kSumChannels + c];
+      sw += lds[blockDim.x + k * kSumChannels + c];
     }
     if (g.dbias) g.dbias[ch] = sb;
     if (g.dweight) g.dweight[ch] = sw;
@@ -857,7 +870,7 @@ hipError_t launch_norm_backward_vec(const fftmv_group_norm_t &g, const NormPlan 
   const NormShape &h = p.s;
   const unsigned threads = static_cast<unsigned>(h.threads);
   if (p.kind == NormPlan::kSplit) {
-    const int64_t blocks = h.N * h.slabs * h.across, more = (g.channels + kWave - 1) / kWave;
+    const int64_t blocks = h.N * h.slabs * h.across, more = (g.channels + kSumChannels - 1) / kSumChannels;
     if (!grid_fits(blocks + more, h.threads)) return hipErrorInvalidConfiguration;
     norm_sums_kernel<T, VEC, ACT><<<static_cast<unsigned>(blocks), threads, p.lds, s>>>(g, h);
     hipError_t e = hipGetLastError();
