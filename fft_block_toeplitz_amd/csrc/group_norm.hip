@@ -12,13 +12,22 @@ __global__ __launch_bounds__(kBlock) void param_sums_kernel(fftmv_group_norm_t g
 
 int round64(int64_t n) { return static_cast<int>((n + 63) / 64 * 64); }
 
-// The widest slab of whole groups over at most `lanes` lanes of `vec`
-// channels, every slab at least one vector wide; 0 where there is none.
+// Groups of the widest slabs over at most `lanes` lanes of `vec` channels,
+// every slab at least one vector wide; 0 where there are none. As few slabs as
+// that gives, of about the same width.
 int widest_slab(int D, int G, int vec, int lanes) {
   constexpr int kMostGroups = 256;  // whose statistics lie in LDS
   const int64_t fit = static_cast<int64_t>(lanes) * vec / D;
-  for (int gs = static_cast<int>(std::min<int64_t>({fit, G, kMostGroups})); gs >= 1; --gs)
-    if (static_cast<int64_t>(gs) * D >= vec && static_cast<int64_t>((G - 1) % gs + 1) * D >= vec) return gs;
+  const int most = static_cast<int>(std::min<int64_t>({fit, G, kMostGroups}));
+  auto wide = [&](int gs) {
+    return static_cast<int64_t>(gs) * D >= vec && static_cast<int64_t>((G - 1) % gs + 1) * D >= vec;
+  };
+  if (most > 0) {
+    const int slabs = (G + most - 1) / most, even = (G + slabs - 1) / slabs;
+    if (wide(even)) return even;
+  }
+  for (int gs = most; gs >= 1; --gs)
+    if (wide(gs)) return gs;
   return 0;
 }
 

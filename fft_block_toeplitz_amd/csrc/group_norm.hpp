@@ -409,7 +409,7 @@ struct Range {
   }
 };
 
-constexpr int kTile = 8;  // rows of a thread in one tile
+constexpr int kTile = 4;  // rows of a thread in one tile (eight measured the same, and spilled)
 
 // (mean, sum of squared deviations) of each group over one range, from
 // tiles of kTile rows a thread, each about its own mean and joined pairwise.

@@ -79,8 +79,10 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_forward_kernel(fftmv_r
   constexpr int W = kLanes * VEC;  // columns of the workgroup
   __shared__ ForwardLds<W> lds;
   const int tid = threadIdx.x, seg = tid / kLanes, lane = tid % kLanes;
-  // chains of all blocks of channels: block by block of one sequence, then the next
-  const uint32_t chains = static_cast<uint32_t>(axis.chains) * axis.blocks, chain = blockIdx.x % chains;
+  // chains of all blocks of channels: block by block of one sequence, then the
+  // next. Neighbours share the lines at their edges, and so an XCD.
+  const uint32_t chains = static_cast<uint32_t>(axis.chains) * axis.blocks;
+  const uint32_t chain = static_cast<uint32_t>(xcd_contiguous_block(blockIdx.x % chains, chains));
   const int block = chain % static_cast<uint32_t>(axis.blocks), over_batch = chain / static_cast<uint32_t>(axis.blocks);
   const int64_t ch = column_channel<VEC>(r.channels, static_cast<int64_t>(block) * W + lane * VEC);
   const ScanChain s = scan_chain<W>(r, axis, chain);
