@@ -64,7 +64,7 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   p.vec = 16 / es;
   if (widest_slab(s.D, s.G, p.vec, 1024) == 0) p.vec = 1;
   const int v = p.vec, alone = static_cast<int>((static_cast<int64_t>(s.D) + v - 1) / v);  // lanes of one group
-  if (alone > 1024 || widest_slab(s.D, s.G, v, 1024) == 0) {
+  if (rows == 0 || alone > 1024 || widest_slab(s.D, s.G, v, 1024) == 0) {
     p.rows = samples;
     p.workspace = backward ? static_cast<size_t>(samples * channels) * 8 : 0;
     return p;

@@ -49,6 +49,21 @@ __device__ __forceinline__ int held_rows(const fftmv_group_norm_t &g, int64_t n)
   return l < 0 ? 0 : l > S ? S : l;
 }
 
+// Row `row` of a sample, zeros where row >= held. The load is unconditional (of
+// row 0 in that case, which is there): loads behind branches wait one for
+// another, and took three times as long.
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> load_held(const T *sample, int row, int held, int64_t stride) {
+  const bool on = row < held;
+  const Vec<T, VEC> v = load_vec<T, VEC>(sample + static_cast<int64_t>(on ? row : 0) * stride);
+  if constexpr (VEC * sizeof(T) == 16) {
+    const u32x4_any w = __builtin_bit_cast(u32x4_any, v), none = {0, 0, 0, 0};
+    return __builtin_bit_cast(Vec<T, VEC>, on ? w : none);
+  } else {
+    return on ? v : Vec<T, VEC>{};
+  }
+}
+
 // This thread's place in a slab.
 template <int VEC>
 struct SlabLane {
@@ -71,7 +86,29 @@ struct SlabLane {
     in = flat < s.ty * s.sub && c < wd;
     if (c + VEC > wd) c = wd - VEC;
   }
+  // sample q of this thread, kept inside the batch
+  __device__ __forceinline__ int64_t sample(const NormShape &s, int64_t n0, int q) const {
+    const int64_t n = n0 + q * s.sub + sub;
+    return n < s.N ? n : s.N - 1;
+  }
 };
+
+// Rows that each of a thread's samples holds (0 behind the last sample).
+template <int VEC, int Q>
+__device__ __forceinline__ void held_of(const fftmv_group_norm_t &g, const NormShape &s, const SlabLane<VEC> &l,
+                                        int64_t n0, int (&held)[Q]) {
+#pragma unroll
+  for (int q = 0; q < Q; ++q) held[q] = s.S;
+  if (g.lengths) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) held[q] = g.lengths[l.sample(s, n0, q)];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) held[q] = held[q] < 0 ? 0 : held[q] > s.S ? s.S : held[q];
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (!l.in || n0 + q * s.sub + l.sub >= s.N) held[q] = 0;
+}
 
 template <int VEC>
 __device__ __forceinline__ void load_params(const float *p, int64_t ch, float none, float (&v)[VEC]) {
@@ -156,25 +193,18 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
   const SlabLane<VEC> l(s, slab);
   const GroupOf<VEC, WHOLE> group(l.c, s.D);
   float w[VEC], b[VEC];
-  if (l.in) {
-    load_params(g.weight, l.ch0 + l.c, 1.0f, w);
-    load_params(g.bias, l.ch0 + l.c, 0.0f, b);
-  }
+  load_params(g.weight, l.ch0 + l.c, 1.0f, w);
+  load_params(g.bias, l.ch0 + l.c, 0.0f, b);
   const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * (Q * s.sub);
   for (int64_t n0 = static_cast<int64_t>(blockIdx.x / s.slabs) * (Q * s.sub); n0 < s.N; n0 += step) {
     Vec<T, VEC> v[Q][P];
     int held[Q];
+    held_of<VEC, Q>(g, s, l, n0, held);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const int64_t n = n0 + q * s.sub + l.sub;
-      held[q] = l.in && n < s.N ? held_rows(g, n) : 0;
-      const T *x = static_cast<const T *>(g.x) + n * g.x_sample + l.ch0 + l.c;
+      const T *x = static_cast<const T *>(g.x) + l.sample(s, n0, q) * g.x_sample + l.ch0 + l.c;
 #pragma unroll
-      for (int p = 0; p < P; ++p) {
-        v[q][p] = Vec<T, VEC>{};
-        if (l.row + p * s.ty < held[q])
-          v[q][p] = load_vec<T, VEC>(x + static_cast<int64_t>(l.row + p * s.ty) * g.x_row);
-      }
+      for (int p = 0; p < P; ++p) v[q][p] = load_held<T, VEC>(x, l.row + p * s.ty, held[q], g.x_row);
     }
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -288,28 +318,22 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel
   float w[VEC], b[VEC], db[VEC], dw[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) db[e] = dw[e] = 0.0f;
-  if (l.in) {
-    load_params(g.weight, l.ch0 + l.c, 1.0f, w);
-    load_params(g.bias, l.ch0 + l.c, 0.0f, b);
-  }
+  load_params(g.weight, l.ch0 + l.c, 1.0f, w);
+  load_params(g.bias, l.ch0 + l.c, 0.0f, b);
   const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * (Q * s.sub);
   for (int64_t n0 = static_cast<int64_t>(first) * (Q * s.sub); n0 < s.N; n0 += step) {
     Vec<T, VEC> v[Q][P], d[Q][P];
     int held[Q];
+    held_of<VEC, Q>(g, s, l, n0, held);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const int64_t n = n0 + q * s.sub + l.sub;
-      held[q] = l.in && n < s.N ? held_rows(g, n) : 0;
+      const int64_t n = l.sample(s, n0, q);
       const T *x = static_cast<const T *>(g.x) + n * g.x_sample + l.ch0 + l.c;
       const T *dy = static_cast<const T *>(g.dy) + n * g.dy_sample + l.ch0 + l.c;
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        v[q][p] = d[q][p] = Vec<T, VEC>{};
-        const int64_t row = l.row + p * s.ty;
-        if (row < held[q]) {
-          v[q][p] = load_vec<T, VEC>(x + row * g.x_row);
-          d[q][p] = load_vec<T, VEC>(dy + row * g.dy_row);
-        }
+        v[q][p] = load_held<T, VEC>(x, l.row + p * s.ty, held[q], g.x_row);
+        d[q][p] = load_held<T, VEC>(dy, l.row + p * s.ty, held[q], g.dy_row);
       }
     }
     for (int i = threadIdx.x; i < Q * s.sub * l.ng; i += blockDim.x) {
@@ -430,10 +454,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_n
       int rows = (r.to - t + s.ty - 1) / s.ty;
       rows = rows < kTile ? rows : kTile;
 #pragma unroll
-      for (int p = 0; p < kTile; ++p) {
-        v[p] = Vec<T, VEC>{};
-        if (p < rows) v[p] = load_vec<T, VEC>(x + static_cast<int64_t>(t + p * s.ty) * g.x_row);
-      }
+      for (int p = 0; p < kTile; ++p) v[p] = load_held<T, VEC>(x, t + p * s.ty, r.to, g.x_row);
       const float k = static_cast<float>(rows), all = count + k, share = k / all, weight = count * share;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -484,26 +505,35 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
   const GroupOf<VEC, false> group(l.c, s.D);
   const int held = held_rows(g, r.n);
   const float2 *from = static_cast<const float2 *>(g.workspace) + r.n * s.across * s.G + static_cast<int64_t>(r.slab) * s.gs;
-  // one team of threads a group, one range a thread at a time
+  // one team of threads a group, four ranges of a thread at a time, joined
+  // pairwise: (count, mean, sum of squared deviations)
   const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
   for (int k = threadIdx.x / s.team; k < l.ng; k += teams) {
-    float sum = 0.0f;
-    for (int i = me; i < s.across; i += s.team) {
-      const int rows = held - i * s.range;
-      if (rows > 0) sum += static_cast<float>(rows < s.range ? rows : s.range) * from[static_cast<int64_t>(i) * s.G + k].x;
-    }
-    for (int m = s.team / 2; m > 0; m >>= 1) sum += __shfl_xor(sum, m);
-    const float mu = held ? sum / static_cast<float>(held) : 0.0f;
-    float sq = 0.0f;
-    for (int i = me; i < s.across; i += s.team) {
-      const int rows = held - i * s.range;
-      if (rows > 0) {
-        const float2 v = from[static_cast<int64_t>(i) * s.G + k];
-        const float d = v.x - mu;
-        sq += fmaf(d * d, static_cast<float>(rows < s.range ? rows : s.range) * s.D, v.y);
+    float count = 0.0f, mu = 0.0f, sq = 0.0f;
+    auto join = [&](float n, float m, float q) {
+      const float all = count + n, share = all > 0.0f ? n / all : 0.0f, d = m - mu;
+      sq += q + d * d * count * share;
+      mu = fmaf(d, share, mu);
+      count = all;
+    };
+    for (int i0 = me; i0 < s.across; i0 += 4 * s.team) {
+      float2 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * s.team;
+        v[j] = from[static_cast<int64_t>(i < s.across ? i : 0) * s.G + k];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int rows = held - (i0 + j * s.team) * s.range;
+        if (i0 + j * s.team < s.across && rows > 0)
+          join(static_cast<float>(rows < s.range ? rows : s.range) * s.D, v[j].x, v[j].y);
       }
     }
-    for (int m = s.team / 2; m > 0; m >>= 1) sq += __shfl_xor(sq, m);
+    for (int m = 1; m < s.team; m <<= 1) {
+      const float n = __shfl_xor(count, m), mm = __shfl_xor(mu, m), qq = __shfl_xor(sq, m);
+      join(n, mm, qq);  // lane 0's order is the one that counts
+    }
     if (me == 0) {
       mean[k] = mu;
       rstd[k] = held ? 1.0f / sqrtf(sq / (static_cast<float>(held) * s.D) + g.eps) : 0.0f;
@@ -528,10 +558,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
   for (int t = r.from + l.row; t < end; t += 4 * s.ty) {
     Vec<T, VEC> v[4];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      v[p] = Vec<T, VEC>{};
-      if (t + p * s.ty < r.to) v[p] = load_vec<T, VEC>(x + static_cast<int64_t>(t + p * s.ty) * g.x_row);
-    }
+    for (int p = 0; p < 4; ++p) v[p] = load_held<T, VEC>(x, t + p * s.ty, r.to, g.x_row);
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const int row = t + p * s.ty;
@@ -572,12 +599,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_sums_kernel(fftmv_group_nor
       Vec<T, VEC> v[4], d[4];
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        v[p] = d[p] = Vec<T, VEC>{};
-        const int64_t row = t + p * s.ty;
-        if (row < r.to) {
-          v[p] = load_vec<T, VEC>(x + row * g.x_row);
-          d[p] = load_vec<T, VEC>(dy + row * g.dy_row);
-        }
+        v[p] = load_held<T, VEC>(x, t + p * s.ty, r.to, g.x_row);
+        d[p] = load_held<T, VEC>(dy, t + p * s.ty, r.to, g.dy_row);
       }
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -622,11 +645,9 @@ __device__ __forceinline__ void param_sums(const fftmv_group_norm_t &g, int64_t 
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
         const int64_t i = i0 + k * parts;
-        if (i < rows) {
-          const float2 v = from[i * g.channels + ch];
-          b += v.x;
-          w += v.y;
-        }
+        const float2 v = from[(i < rows ? i : i0) * g.channels + ch];
+        b += i < rows ? v.x : 0.0f;
+        w += i < rows ? v.y : 0.0f;
       }
       sb += b;
       sw += w;
@@ -664,10 +685,16 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_nor
   const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
   for (int k = threadIdx.x / s.team; k < l.ng; k += teams) {
     float a = 0.0f, b = 0.0f;
-    for (int i = me; i < s.across; i += s.team) {
-      const float2 v = from[static_cast<int64_t>(i) * s.G + k];
-      a += v.x;
-      b += v.y;
+    for (int i0 = me; i0 < s.across; i0 += 4 * s.team) {
+      float2 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * s.team;
+        v[j] = from[static_cast<int64_t>(i < s.across ? i : 0) * s.G + k];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i0 + j * s.team < s.across) a += v[j].x, b += v[j].y;
     }
     for (int m = s.team / 2; m > 0; m >>= 1) {
       a += __shfl_xor(a, m);
@@ -700,12 +727,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_nor
     Vec<T, VEC> v[2], d[2];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      v[p] = d[p] = Vec<T, VEC>{};
-      const int64_t row = t + p * s.ty;
-      if (row < r.to) {
-        v[p] = load_vec<T, VEC>(x + row * g.x_row);
-        d[p] = load_vec<T, VEC>(dy + row * g.dy_row);
-      }
+      v[p] = load_held<T, VEC>(x, t + p * s.ty, r.to, g.x_row);
+      d[p] = load_held<T, VEC>(dy, t + p * s.ty, r.to, g.dy_row);
     }
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
