@@ -262,11 +262,13 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
         for (int p = 0; p < P; ++p) {
           const int row = l.row + p * s.ty;
           if (row >= s.S) break;
-          float o[VEC];
+          float o[VEC] = {};
+          if (row < held[q]) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const int k = (q * s.sub + l.sub) * l.ng + group[e];
-            o[e] = row < held[q] ? activate<ACT>(fmaf((v[q][p][e] - mean[k]) * rstd[k], w[e], b[e])) : 0.0f;
+            for (int e = 0; e < VEC; ++e) {
+              const int k = (q * s.sub + l.sub) * l.ng + group[e];
+              o[e] = activate<ACT>(fmaf((v[q][p][e] - mean[k]) * rstd[k], w[e], b[e]));
+            }
           }
           store_vec<T, VEC>(y + static_cast<int64_t>(row) * g.y_row, o);
         }
@@ -347,12 +349,11 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel
       }
     }
     __syncthreads();
-    // dz and xhat of one element, both 0 where no row is held
+    // dz and xhat of one element; where no row is held, dy and dz are 0
     auto terms = [&](int q, int p, int e, float &xh, float &dz) {
       const int k = 2 * ((q * s.sub + l.sub) * l.ng + group[e]);
-      const bool on = l.row + p * s.ty < held[q];
-      xh = on ? (v[q][p][e] - stat[k]) * stat[k + 1] : 0.0f;
-      dz = on ? d[q][p][e] * activate_slope<ACT>(fmaf(xh, w[e], b[e])) : 0.0f;
+      xh = (v[q][p][e] - stat[k]) * stat[k + 1];
+      dz = d[q][p][e] * activate_slope<ACT>(fmaf(xh, w[e], b[e]));
     };
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -399,13 +400,15 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel
         for (int p = 0; p < P; ++p) {
           const int row = l.row + p * s.ty;
           if (row >= s.S) break;
-          float o[VEC];
+          float o[VEC] = {};
+          if (row < held[q]) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            float xh, dz;
-            terms(q, p, e, xh, dz);
-            const int k = (q * s.sub + l.sub) * l.ng + group[e];
-            o[e] = row < held[q] ? stat[2 * k + 1] * (fmaf(dz, w[e], -m[k]) - xh * m[Q * s.sub * l.ng + k]) : 0.0f;
+            for (int e = 0; e < VEC; ++e) {
+              float xh, dz;
+              terms(q, p, e, xh, dz);
+              const int k = (q * s.sub + l.sub) * l.ng + group[e];
+              o[e] = stat[2 * k + 1] * (fmaf(dz, w[e], -m[k]) - xh * m[Q * s.sub * l.ng + k]);
+            }
           }
           store_vec<T, VEC>(dx + static_cast<int64_t>(row) * g.dx_row, o);
           row_done();
@@ -563,10 +566,11 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
     for (int p = 0; p < 4; ++p) {
       const int row = t + p * s.ty;
       if (row >= end) break;
-      float o[VEC];
+      float o[VEC] = {};
+      if (row < r.to) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        o[e] = row < r.to ? activate<ACT>(fmaf((v[p][e] - mu[e]) * rs[e], w[e], b[e])) : 0.0f;
+        for (int e = 0; e < VEC; ++e) o[e] = activate<ACT>(fmaf((v[p][e] - mu[e]) * rs[e], w[e], b[e]));
+      }
       store_vec<T, VEC>(y + static_cast<int64_t>(row) * g.y_row, o);
     }
   }
@@ -734,11 +738,13 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_nor
     for (int p = 0; p < 2; ++p) {
       const int row = t + p * s.ty;
       if (row >= end) break;
-      float o[VEC];
+      float o[VEC] = {};
+      if (row < r.to) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float xh = (v[p][e] - mu[e]) * rs[e], dz = d[p][e] * activate_slope<ACT>(fmaf(xh, w[e], b[e]));
-        o[e] = row < r.to ? rs[e] * (fmaf(dz, w[e], -k1[e]) - xh * k2[e]) : 0.0f;
+        for (int e = 0; e < VEC; ++e) {
+          const float xh = (v[p][e] - mu[e]) * rs[e], dz = d[p][e] * activate_slope<ACT>(fmaf(xh, w[e], b[e]));
+          o[e] = rs[e] * (fmaf(dz, w[e], -k1[e]) - xh * k2[e]);
+        }
       }
       store_vec<T, VEC>(dx + static_cast<int64_t>(row) * g.dx_row, o);
     }
