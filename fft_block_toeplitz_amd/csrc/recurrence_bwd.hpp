@@ -127,19 +127,13 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_
     if (t == static_cast<uint32_t>(order)) break;
     order = static_cast<int>(t);
   }
-  uint64_t early = 0;
-  float carry = 0.0f;
-  if (axis.joined()) {
-    if (!c.tail && tid < W) early = peek<W>(s, order - 1, 2, tid);
-    // the state that enters the chunk (unused where a sequence starts)
-    const int64_t cc = column_channel<VEC>(r.channels, static_cast<int64_t>(block) * W + tid % W);
-    if (!c.head)
-      carry = r.carries[(static_cast<int64_t>(c.chain) * axis.places + c.place) * r.channels + cc];
-    else if (c.ordinary && r.h0)
-      carry = r.h0[c.seq * r.channels + cc];
-  }
-
-  float A[VEC], h[VEC], b[VEC];
+  // The maps' terms are held through the join; what the gradients need besides
+  // is evaluated again behind it. (Holding that too would pass 128 registers;
+  // evaluating everything in each of the three passes took 202 instead of 194
+  // us at 8 x 1000 x 5000 FP32. FP32 inputs beside both a and u would, too:
+  // there the complement's terms are evaluated in all three.)
+  constexpr bool kHold = sizeof(T) == 2 || DRIVE == FFTMV_DRIVE_PLAIN;
+  float A[VEC], h[VEC], b[VEC], a[kRows][VEC], u[kRows][VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) A[e] = 1.0f, h[e] = 0.0f, b[e] = 0.0f;
   bool open = true;  // a later row's gradient reaches the segment's first
@@ -154,9 +148,11 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const Terms t = decay_terms<T, DECAY>(g[i][e]);
-      h[e] = fmaf(t.a, h[e], drive_of<DRIVE>(t, x[i][e]));
+      a[i][e] = t.a;
+      u[i][e] = drive_of<DRIVE>(t, x[i][e]);
+      h[e] = fmaf(t.a, h[e], u[i][e]);
       A[e] *= t.a;
-      if (open) b[e] = fmaf(A[e], d[i][e] + dl[e], b[e]);  // a_0 .. a_i dh_i
+      b[e] = open ? fmaf(A[e], d[i][e] + dl[e], b[e]) : b[e];  // a_0 .. a_i dh_i
     }
     if (!c.ordinary) {
       open = open && !q.last(i);
@@ -167,6 +163,18 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_
     }
     row_done();
   }
+  uint64_t early = 0;
+  float carry = 0.0f;
+  if (axis.joined()) {
+    if (!c.tail && tid < W) early = peek<W>(s, order - 1, 2, tid);
+    // the state that enters the chunk (unused where a sequence starts)
+    const int64_t cc = column_channel<VEC>(r.channels, static_cast<int64_t>(block) * W + tid % W);
+    if (!c.head)
+      carry = r.carries[(static_cast<int64_t>(c.chain) * axis.places + c.place) * r.channels + cc];
+    else if (c.ordinary && r.h0)
+      carry = r.h0[c.seq * r.channels + cc];
+  }
+
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
     lds.A[seg][lane * VEC + e] = A[e];
@@ -185,62 +193,52 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_
     b[e] = lds.S[seg][lane * VEC + e];
   }
 
-  // The rows behind first, two by two: forward to w = h_{t-1} (- x_t), the
-  // factor of dgate, and back over them; b becomes s_t. (All four rows' w at
-  // once would take 16 registers more, and a third of the workgroups.)
-  auto ahead = [&](int i, float (&v)[VEC], float (&w)[VEC]) {
-    if (!c.ordinary && q.start(i)) load_state(r.h0, q.seq[i], r.channels, ch, v);
+  // forward to w = h_{t-1} (- x_t), the factor of dgate
+  if constexpr (!kHold) forget(g);
+  float w[kRows][VEC];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (!c.ordinary && q.start(i)) load_state(r.h0, q.seq[i], r.channels, ch, h);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      w[i][e] = DRIVE == FFTMV_DRIVE_COMPLEMENT ? h[e] - x[i][e] : h[e];
+      if constexpr (kHold) {
+        h[e] = fmaf(a[i][e], h[e], u[i][e]);
+      } else {
+        const Terms t = decay_terms<T, DECAY>(g[i][e]);
+        h[e] = fmaf(t.a, h[e], drive_of<DRIVE>(t, x[i][e]));
+      }
+    }
+  }
+  // and back: b becomes s_t
+  forget(g);
+#pragma unroll
+  for (int i = kRows - 1; i >= 0; --i) {
+    if (!c.ordinary && q.last(i)) load_state(r.dh_last, q.seq[i], r.channels, ch, b);
+    float du[VEC], dv[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const Terms t = decay_terms<T, DECAY>(g[i][e]);
-      w[e] = DRIVE == FFTMV_DRIVE_COMPLEMENT ? v[e] - x[i][e] : v[e];
-      v[e] = fmaf(t.a, v[e], drive_of<DRIVE>(t, x[i][e]));
+      const float rt = d[i][e] + b[e];
+      b[e] = t.a * rt;
+      du[e] = DRIVE == FFTMV_DRIVE_COMPLEMENT ? rt * t.rest : rt;
+      dv[e] = rt * w[i][e] * t.slope;
+    }
+    if (!c.ordinary && q.dead(i)) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) b[e] = du[e] = dv[e] = 0.0f;
+    }
+    store_row<T, VEC>(r, axis, c, q, i, r.dx, r.dx_batch, r.dx_step, ch, du);
+    store_row<T, VEC>(r, axis, c, q, i, r.dgate, r.dgate_batch, r.dgate_step, ch, dv);
+    if (!c.ordinary) {
+      if (q.start(i)) store_state(r.dh0, q.seq[i], r.channels, ch, b);
+      if (q.empty(i)) {
+        float dl[VEC];
+        load_state(r.dh_last, q.seq[i], r.channels, ch, dl);
+        store_state(r.dh0, q.seq[i], r.channels, ch, dl);
+      }
     }
     row_done();
-  };
-#pragma unroll
-  for (int half = kRows - 2; half >= 0; half -= 2) {
-    float v[VEC], w[2][VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) v[e] = h[e];
-    forget(g);
-    forget(x);
-#pragma unroll
-    for (int i = 0; i < half; ++i) ahead(i, v, w[0]);
-    ahead(half, v, w[0]);
-    ahead(half + 1, v, w[1]);
-    forget(g);
-    forget(d);
-#pragma unroll
-    for (int i = half + 1; i >= half; --i) {
-      if (!c.ordinary && q.last(i)) load_state(r.dh_last, q.seq[i], r.channels, ch, b);
-      const bool dead = !c.ordinary && q.dead(i);
-      float out[VEC];
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const Terms t = decay_terms<T, DECAY>(g[i][e]);
-        const float rt = dead ? 0.0f : d[i][e] + b[e];
-        b[e] = rt;
-        out[e] = dead ? 0.0f : rt * w[i - half][e] * t.slope;
-      }
-      store_row<T, VEC>(r, axis, c, q, i, r.dgate, r.dgate_batch, r.dgate_step, ch, out);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const Terms t = decay_terms<T, DECAY>(g[i][e]);
-        out[e] = DRIVE == FFTMV_DRIVE_COMPLEMENT && !dead ? b[e] * t.rest : b[e];
-        b[e] = dead ? 0.0f : b[e] * t.a;
-      }
-      store_row<T, VEC>(r, axis, c, q, i, r.dx, r.dx_batch, r.dx_step, ch, out);
-      if (!c.ordinary) {
-        if (q.start(i)) store_state(r.dh0, q.seq[i], r.channels, ch, b);
-        if (q.empty(i)) {
-          float dl[VEC];
-          load_state(r.dh_last, q.seq[i], r.channels, ch, dl);
-          store_state(r.dh0, q.seq[i], r.channels, ch, dl);
-        }
-      }
-      row_done();
-    }
   }
   // an ordinary chunk at the front of its sequence
   if (c.ordinary && c.head && seg == 0) store_state(r.dh0, c.seq, r.channels, ch, b);
