@@ -277,6 +277,18 @@ def test_step_against_the_definition(fm, dtype, B, C):
     assert torch.equal(state[untouched], old[untouched])
 
 
+@pytest.mark.parametrize("B,C", [(70001, 3), (70001, 5)])
+def test_step_of_many_narrow_streams(fm, B, C):
+    """More streams than one grid dimension counts; rows that end inside a vector."""
+    x, g = fields(16, (B, C), "fp32", "value")
+    state = fields(17, (B, C), "fp32", "value")[0].clone()
+    want = host(g) * host(state) + host(x)
+    bound = 4 * R.U * (np.abs(host(g) * host(state)) + np.abs(host(x)))
+    h = fm.recurrence_step(x, g, state, decay="value", drive="plain")
+    near(h, want, bound, "h")
+    near(state, want, bound, "state")
+
+
 @pytest.mark.parametrize("decay,drive", [("sigmoid", "complement"), ("exp", "complement"), ("value", "plain")])
 def test_steps_follow_the_whole_series(fm, decay, drive):
     """Step after step gives the series' states, to the reordering of FP32 sums."""
