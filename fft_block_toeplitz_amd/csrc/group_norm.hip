@@ -74,9 +74,11 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   const int Q = backward ? 2 : 4;
 
   // Single rows, or a few: Q samples at a time in a thread's registers, so
-  // that a barrier serves all of them, and narrow ones side by side; where
-  // that leaves too few workgroups for the CUs, the form below takes them one
-  // by one.
+  // that a barrier serves all of them, and narrow ones side by side (forward
+  // and backward, bf16: 16000 x 5000 in 25 groups 86 and 177 us against 134 and
+  // 206 one by one, 20522 x 246 in 2 groups 16 and 32 against 26 and 78);
+  // where that leaves too few workgroups for the CUs, the form below takes
+  // them one by one.
   if (rows <= 8) {
     const int R = std::max(1, s.S);
     const int64_t least = static_cast<int64_t>(alone) * R;
@@ -98,7 +100,8 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
     }
   }
   // A sample's slab in registers: one row a thread, or up to eight (backward,
-  // with twice the inputs: four).
+  // with twice the inputs: four). 400 samples of 100 rows of 8 x 64 bf16 take
+  // 31 and 56 us, split 42 and 64.
   const int several = backward ? 4 : 8;
   for (int P = 1; P <= several && p.kind == NormPlan::kWide; P *= several) {
     const int most = P == 1 ? kNormThreads : kHeldThreads;
@@ -110,17 +113,29 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
         if (s.lx > threads || s.S > P * s.ty) continue;
         // one row a thread: for few rows, or where one takes most of the threads
         if (P == 1 && s.lx * s.S > 256 && alone <= 256) continue;
-        // rows of less than 64 bytes waste the lines that they touch
+        // rows of less than 64 bytes waste the lines that they touch (200
+        // samples of 256 rows of 64 x 8 bf16: 112 and 197 us instead of 32 and 75)
         if (s.lx * v * es < 64 && s.slabs > 1) break;
-        // narrower while workgroups are few, down to 128 bytes a row
-        while (samples * s.slabs < 512 && s.gs > 1) {
+        // narrower while workgroups are fewer than CUs, down to 128 bytes a row:
+        // 4 samples of 64 rows of 16 x 64 bf16 6.6 us forward, whole slabs 7.6;
+        // going on to twice the CUs, 16 of 64 rows of 32 x 64 15.0 instead of
+        // 11.9 backward
+        while (samples * s.slabs < 256 && s.gs > 1) {
           const int half = widest_slab(s.D, s.G, v, s.lx / 2);
           if (half == 0 || half * s.D * es < 128) break;
           take_slab(s, half, v, threads);
         }
         s.ty = std::min(s.ty, std::max(1, s.S));
         s.threads = std::min(threads, round64(static_cast<int64_t>(s.lx) * s.ty));
-        if (samples * s.slabs < 64 && bytes > (int64_t(2) << 20)) break;  // too few to fill the card: split
+        // One row a thread is the quickest to answer, and cuts large inputs
+        // into rows of little more than a line: 400 samples of 16 rows of 8 x 64
+        // bf16 take 9.8 and 16 us, 13 and 20 with several rows a thread; 1000
+        // of 12 rows of 16 x 64, 25 and 38 against 17 and 34.
+        if (P == 1 && alone <= 256 && samples * s.slabs > 4096) continue;
+        // Sums by channel (groups that cut vectors) on too few CUs take longer
+        // than a second launch: 1 x 256 rows of 50 x 100 bf16 22 us forward,
+        // split 16; with whole vectors, 40 x 128, 10.5 against 15.
+        if (!p.whole && samples * s.slabs < 64 && bytes > (int64_t(1) << 20)) break;
         p.kind = P == 1 ? NormPlan::kRow : NormPlan::kResident;
         s.across = static_cast<int>(std::min<int64_t>(samples, std::max(1, (backward ? 1024 : 8192) / s.slabs)));
         break;

@@ -6,6 +6,11 @@
 // in FP32 from the state that entered the chunk (the forward's carries), so
 // that x, gate and dh are read once each, dx and dgate written once, and no
 // rounded h is read at all.
+//
+// Memory traffic bounds it, and at this many workgroups the chunks' joins: 4 x
+// 4096 x 4096 bf16 take 205 us (3.3 TB/s of five fields; 145 with the joins left
+// out, which gives wrong values), 8 x 2000 x 5000 280 us, 8 x 1000 x 5000 FP32
+// 199 us (4.0 TB/s).
 #pragma once
 
 #include "recurrence.hpp"

@@ -278,8 +278,8 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     ("value"); ``drive``: u = (1 - a) x ("complement") or x ("plain").
     x and gate are [batch, steps, channels] (or one sequence [steps,
     channels]) with contiguous channels and any strides otherwise.
-    ``lengths`` (int32 [batch]): padded batch, steps from lengths[b] on are
-    not read and come back zero. ``offsets`` (int32 [sequences + 1]): x is
+    ``lengths`` (int32 [batch]): padded batch, steps from lengths[b] on do
+    not matter and come back zero. ``offsets`` (int32 [sequences + 1]): x is
     [steps, channels], sequence b its rows offsets[b]..offsets[b+1]-1; rows
     of no sequence come back zero.
 
@@ -414,7 +414,7 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
     of ``groups`` runs of neighbouring channels. weight, bias: float32
     [channels] or None. ``activation``: None, "silu" or "gelu" (exact).
     ``lengths`` (int32 [samples]): sample n holds its first lengths[n] rows;
-    the others enter no sum, are not read, and come back zero.
+    the others enter no sum whatever they hold, and come back zero.
 
     Returns y (x's type); with ``save`` also the statistics, float32
     [samples, groups, 2] (mean, rstd), that ``group_norm_backward`` needs."""

@@ -323,12 +323,12 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  *   batch    `batch` sequences of `steps` steps each; row (b, t) of a field
  *            starts at b * batch_stride + t * step_stride
  *   padded   the same with lengths[b] steps held in sequence b (values are
- *            clamped to 0..steps); the others are not read, and are written
+ *            clamped to 0..steps); the others do not matter, and are written
  *            as zeros
  *   packed   one axis of `steps` steps in all, sequence b being the steps
  *            offsets[b]..offsets[b+1]-1 (ascending; equal neighbours: an
  *            empty sequence); steps before offsets[0] or from
- *            offsets[batch] on belong to none, are not read, and are
+ *            offsets[batch] on belong to none, do not matter, and are
  *            written as zeros; batch strides are ignored
  * lengths / offsets are device arrays of int32. Neither their contents nor
  * anything else on the device is read by the host.
@@ -433,7 +433,7 @@ FFTMV_API int fftmv_recurrence_step(const fftmv_recurrence_step_t *r, hipStream_
  * with mean and (biased) variance over the sample's rows and one group.
  * weight, bias: [channels] FP32, NULL for ones / zeros. lengths (device
  * int32, clamped to 0..rows): sample n holds lengths[n] rows only; the
- * others enter no sum, are not read, and are written as zeros; a sample
+ * others enter no sum whatever they hold, and are written as zeros; a sample
  * that holds none has mean 0 and rstd 0.
  *
  * Forward writes y and, where not NULL, stats [samples][groups][2] (mean,
