@@ -380,12 +380,12 @@ __device__ __forceinline__ void load_rows(const fftmv_recurrence_t &r, const Sca
 template <typename T, int VEC>
 __device__ __forceinline__ void store_row(const fftmv_recurrence_t &r, const ScanAxis &a, const Chunk &c,
                                           const Rows &q, int i, void *field, int64_t sb, int64_t st, int64_t ch,
-                                          const float (&f)[VEC]) {
+                                          const float (&f)[VEC], bool streamed = true) {
   T *p = static_cast<T *>(field) + ch;
   if (c.ordinary)
-    store_vec<T, VEC>(p + row_offset(r, a, c, q, 0, sb, st) + i * st, f);
+    store_vec<T, VEC>(p + row_offset(r, a, c, q, 0, sb, st) + i * st, f, streamed);
   else if (!q.absent(i))
-    store_vec<T, VEC>(p + row_offset(r, a, c, q, i, sb, st), f);
+    store_vec<T, VEC>(p + row_offset(r, a, c, q, i, sb, st), f, streamed);
 }
 
 // VEC channels of a [batch][channels] state, zeros where there is none.

@@ -9,8 +9,8 @@
 //
 // Memory traffic bounds it, and at this many workgroups the chunks' joins: 4 x
 // 4096 x 4096 bf16 take 205 us (3.3 TB/s of five fields; 145 with the joins left
-// out, which gives wrong values), 8 x 2000 x 5000 280 us, 8 x 1000 x 5000 FP32
-// 199 us (4.0 TB/s).
+// out, which gives wrong values), 8 x 2000 x 5000 260 us, 8 x 1000 x 5000 FP32
+// 182 us (4.4 TB/s).
 #pragma once
 
 #include "recurrence.hpp"
@@ -97,7 +97,8 @@ __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const
 }
 
 template <typename T, int VEC, int DECAY, int DRIVE>
-__global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_recurrence_t r, ScanAxis axis) {
+__global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_recurrence_t r, ScanAxis axis,
+                                                                          bool streamed) {
   constexpr int W = kLanes * VEC;
   __shared__ BackwardLds<W> lds;
   const int tid = threadIdx.x, seg = tid / kLanes, lane = tid % kLanes;
@@ -233,8 +234,8 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_
 #pragma unroll
       for (int e = 0; e < VEC; ++e) b[e] = du[e] = dv[e] = 0.0f;
     }
-    store_row<T, VEC>(r, axis, c, q, i, r.dx, r.dx_batch, r.dx_step, ch, du);
-    store_row<T, VEC>(r, axis, c, q, i, r.dgate, r.dgate_batch, r.dgate_step, ch, dv);
+    store_row<T, VEC>(r, axis, c, q, i, r.dx, r.dx_batch, r.dx_step, ch, du, streamed);
+    store_row<T, VEC>(r, axis, c, q, i, r.dgate, r.dgate_batch, r.dgate_step, ch, dv, streamed);
     if (!c.ordinary) {
       if (q.start(i)) store_state(r.dh0, q.seq[i], r.channels, ch, b);
       if (q.empty(i)) {
@@ -250,13 +251,25 @@ __global__ __launch_bounds__(kThreads, 4) void recurrence_backward_kernel(fftmv_
   if ((r.offsets || r.steps == 0) && c.place == 0) pass_empty<VEC>(r, seg, ch, r.dh_last, r.dh0);
 }
 
+// All rows of a field start on a line of memory.
+template <typename T>
+bool on_lines(const fftmv_recurrence_t &r, const void *p, int64_t batch, int64_t step) {
+  const int64_t strides = (r.offsets ? 0 : batch) | step;
+  return (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(strides * static_cast<int64_t>(sizeof(T)))) % 128 == 0;
+}
+
 template <typename T, int VEC>
 hipError_t launch_recurrence_backward_vec(const fftmv_recurrence_t &r, hipStream_t s) {
+  // Where rows start inside a line, two blocks of channels write parts of one:
+  // through the caches these leave as one write (8 x 2000 x 5000 bf16 260 us,
+  // streamed 280; 4 x 4096 x 4096, on lines, 211 and 206).
+  const bool streamed = on_lines<T>(r, r.dx, r.dx_batch, r.dx_step) &&
+                        on_lines<T>(r, r.dgate, r.dgate_batch, r.dgate_step);
   const ScanAxis axis = scan_axis(r.batch, r.steps, r.offsets != nullptr, r.channels, kLanes * VEC);
   if (!grid_fits(axis.workgroups(), kThreads)) return hipErrorInvalidConfiguration;
   return by_recurrence_kind(r.decay, r.drive, [&](auto d, auto u) {
     recurrence_backward_kernel<T, VEC, decltype(d)::value, decltype(u)::value>
-        <<<static_cast<unsigned>(axis.workgroups()), kThreads, 0, s>>>(r, axis);
+        <<<static_cast<unsigned>(axis.workgroups()), kThreads, 0, s>>>(r, axis, streamed);
     return hipGetLastError();
   });
 }

@@ -65,7 +65,7 @@ __device__ __forceinline__ Vec<T, VEC> load_vec(const T *p) {
   }
 }
 template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
+__device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC], bool streamed = true) {
   Vec<T, VEC> r;
 #pragma unroll
   for (int e = 0; e < VEC; ++e) r.v[e] = static_cast<T>(f[e]);
@@ -74,7 +74,10 @@ __device__ __forceinline__ void store_vec(T *p, const float (&f)[VEC]) {
     // inputs' lines that two blocks of channels share stay longer (8192 x 4096
     // bf16 normalised in 36 us, through the caches 39)
     using W = typename Words<VEC * sizeof(T)>::type;
-    __builtin_nontemporal_store(__builtin_bit_cast(W, r), reinterpret_cast<W *>(p));
+    if (streamed)
+      __builtin_nontemporal_store(__builtin_bit_cast(W, r), reinterpret_cast<W *>(p));
+    else
+      *reinterpret_cast<W *>(p) = __builtin_bit_cast(W, r);
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) p[e] = r.v[e];
