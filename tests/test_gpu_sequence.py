@@ -251,6 +251,40 @@ def test_recurrence_gradient_against_differences(fm, decay, drive):
         assert abs(got - want) <= 100 * 1e-6 * 3 / (2 * e) + 10 * e * e * size
 
 
+# ------------------------------------------------------------ far offsets
+def test_offsets_beyond_32_bits(fm):
+    """Rows 2^23 elements apart, the last ones more than 2^31 elements from the first: same bits as side by side."""
+    C, far = 20, 1 << 23
+    x, g = fields(18, (2, 150, C), "bf16", "sigmoid")
+    buffer = torch.empty(300 * far, dtype=torch.bfloat16, device="cuda")
+    xs, gs = (buffer[k * 64:].as_strided((2, 150, C), (150 * far, far, 1)) for k in range(2))
+    xs.copy_(x)
+    gs.copy_(g)
+    close, last, carries = fm.recurrence(x, g, save=True)
+    h, end, carries_far = fm.recurrence(xs, gs, save=True)
+    assert torch.equal(h, close) and torch.equal(end, last) and torch.equal(carries_far, carries)
+    want = fm.recurrence_backward(x, x, g, carries)
+    assert all(torch.equal(a, b) for a, b in zip(fm.recurrence_backward(xs, xs, gs, carries), want))
+    flat = xs.as_strided((300, C), (far, 1))
+    assert torch.equal(fm.recurrence_step(flat, gs.as_strided((300, C), (far, 1)), torch.zeros(300, C, device="cuda")),
+                       fm.recurrence_step(x.reshape(300, C), g.reshape(300, C), torch.zeros(300, C, device="cuda")))
+    w = torch.linspace(0.5, 1.5, C, device="cuda")
+    for a, b in ((xs, x), (flat, x.reshape(300, C))):
+        y, stats = fm.group_norm(a, 5, w, w, activation="gelu", save=True)
+        z, stats_near = fm.group_norm(b, 5, w, w, activation="gelu", save=True)
+        assert torch.equal(y, z) and torch.equal(stats, stats_near)
+        got = fm.group_norm_backward(a, a, stats, 5, w, w, activation="gelu")
+        assert all(torch.equal(p, q) for p, q in zip(got, fm.group_norm_backward(b, b, stats, 5, w, w, activation="gelu")))
+    del buffer, xs, gs, flat
+    states = torch.empty((1 << 31) + 64, dtype=torch.float32, device="cuda")
+    cache = states.as_strided((2, C), (1 << 31, 1))
+    cache.zero_()
+    out = fm.recurrence_step(x[:, 0], g[:, 0], cache, torch.tensor([1, 0], dtype=torch.int32, device="cuda"))
+    zero = torch.zeros(2, C, device="cuda")
+    assert torch.equal(out, fm.recurrence_step(x[:, 0], g[:, 0], zero))
+    assert torch.equal(cache, zero.flip(0))
+
+
 # ------------------------------------------------------------------- step
 @pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("B,C", [(1, 1), (3, 65), (4, 500), (33, 264)])
