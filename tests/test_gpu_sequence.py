@@ -403,6 +403,20 @@ def test_norm_sizes(fm, N, S, G, D, dtype):
     check_norm(fm, N + S + G + D, N, S, G, D, dtype, "silu")
 
 
+@pytest.mark.parametrize("N,S,G,D", [
+    (2100, 1, 3, 40), (1300, 2, 5, 24), (1205, 1, 2, 25), (1100, 3, 64, 2), (2100, 9, 4, 64), (1, 250, 41, 100),
+    (1, 200, 20, 128), (16, 64, 9, 64), (1100, 1, 1, 2056)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_norm_many_samples_and_wide_rows(fm, N, S, G, D, dtype):
+    """Sizes that fill the card: several samples a workgroup, whole slabs, and ranges of one sample."""
+    check_norm(fm, N + S + G + D, N, S, G, D, dtype, "silu")
+
+
+def test_norm_many_padded(fm):
+    rng = np.random.default_rng(29)
+    check_norm(fm, 29, 1500, 4, 3, 40, "bf16", "gelu", lengths=rng.integers(0, 5, 1500).tolist())
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_norm_large_mean(fm, dtype):
     """Means of a thousand deviations: the variance is not a difference of squares."""
