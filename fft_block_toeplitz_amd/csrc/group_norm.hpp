@@ -820,8 +820,9 @@ __global__ __launch_bounds__(kBlock) void norm_wide_backward_kernel(fftmv_group_
   const T *dy = static_cast<const T *>(g.dy) + n * g.dy_sample + q * D;
   T *dx = static_cast<T *>(g.dx) + n * g.dx_sample + q * D;
   float2 *sums = static_cast<float2 *>(g.workspace) + n * g.channels + q * D;
-  const float mean = g.stats[2 * static_cast<int64_t>(blockIdx.x)];
-  const float rstd = g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1];
+  // where no row is held nothing needs them, and a call without rows may have none
+  const float mean = held ? g.stats[2 * static_cast<int64_t>(blockIdx.x)] : 0.0f;
+  const float rstd = held ? g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1] : 0.0f;
   float m1 = 0.0f, m2 = 0.0f;
   for (int64_t c = threadIdx.x; c < D; c += kBlock) {
     const float w = g.weight ? g.weight[q * D + c] : 1.0f, b = g.bias ? g.bias[q * D + c] : 0.0f;
