@@ -20,6 +20,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import struct
+import threading
 
 from . import FFTMV_SUCCESS, FftmvError, lib
 
@@ -224,29 +225,52 @@ _sizes = functools.lru_cache(maxsize=1024)(fftmv_recurrence_sizes)  # functions 
 _norm_sizes = functools.lru_cache(maxsize=1024)(fftmv_group_norm_workspace)
 
 
-def _workspace(sizes, device, stream, like):
-    """(counters' address and bytes, workspace's address and bytes, number of
-    the call on it). Calls of one stream share a workspace, which is kept and
-    grown; a call under graph capture gets memory of the graph's own, cleared
-    inside the graph."""
-    _, few, many = sizes
-    if many == 0:
-        return 0, 0, 0, 0, 0
-    new = lambda n: _torch.zeros(n, dtype=_torch.uint8, device=like.device)  # noqa: E731
-    if _torch.cuda.is_current_stream_capturing():
-        a, b = new(few), new(many)
-        return a.data_ptr(), few, b.data_ptr(), many, 1
-    w = _workspaces.get((device, stream))
-    if w is None or w[1] < few or w[3] < many:
-        if w is not None:
-            few, many = max(few, w[1]), max(many, w[3])
-        a, b = new(few), new(many)
-        w = _workspaces[device, stream] = [a.data_ptr(), few, b.data_ptr(), many, 0, a, b]
-    elif w[4] == 2 ** 32 - 1:
-        w[6].zero_()
-        w[4] = 0
-    w[4] += 1
-    return w[:5]
+class _workspace:
+    """The memory of one call, to be entered around its launch: (counters'
+    address and bytes, workspace's address and bytes, number of the call on
+    it). Calls of one stream share a workspace, which is kept and grown; a call
+    under graph capture gets memory of the graph's own, cleared inside the
+    graph. Threads may share a stream: a workspace is held until the call has
+    been launched on it, so that none is replaced in front of a launch and
+    numbers ascend in the order of the launches."""
+
+    __slots__ = ("sizes", "device", "stream", "like", "held")
+    lock = threading.Lock()
+
+    def __init__(self, sizes, device, stream, like):
+        self.sizes, self.device, self.stream, self.like = sizes, device, stream, like
+        self.held = None
+
+    def __enter__(self):
+        _, few, many = self.sizes
+        if many == 0:
+            return 0, 0, 0, 0, 0
+        new = lambda n: _torch.zeros(n, dtype=_torch.uint8, device=self.like.device)  # noqa: E731
+        if _torch.cuda.is_current_stream_capturing():
+            a, b = self.held = new(few), new(many)
+            return a.data_ptr(), few, b.data_ptr(), many, 1
+        self.lock.acquire()
+        try:
+            w = _workspaces.get((self.device, self.stream))
+            if w is None or w[1] < few or w[3] < many:
+                if w is not None:
+                    few, many = max(few, w[1]), max(many, w[3])
+                a, b = new(few), new(many)
+                w = _workspaces[self.device, self.stream] = [a.data_ptr(), few, b.data_ptr(), many, 0, a, b]
+            elif w[4] == 2 ** 32 - 1:
+                w[6].zero_()
+                w[4] = 0
+            w[4] += 1
+        except BaseException:
+            self.lock.release()
+            raise
+        self.held = self.lock
+        return w[:5]
+
+    def __exit__(self, *what):
+        if self.held is self.lock:
+            self.lock.release()
+        self.held = None
 
 
 def _sequences(x, lengths, offsets):
@@ -305,10 +329,11 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     carries = x.new_empty((sizes[0], C), dtype=_torch.float32) if save else None
     device = x.get_device()
     stream = _current_stream(device)
-    *ws, call = _workspace(sizes, device, stream, x)
-    r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, carries.data_ptr() if save else 0,
-                         *ws, h.data_ptr(), T * C, C, last.data_ptr(), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    fftmv_recurrence_forward(r, stream)
+    with _workspace(sizes, device, stream, x) as (*ws, call):
+        r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p,
+                             carries.data_ptr() if save else 0, *ws, h.data_ptr(), T * C, C, last.data_ptr(), 0, 0, 0,
+                             0, 0, 0, 0, 0, 0, 0, 0)
+        fftmv_recurrence_forward(r, stream)
     return (h, last, carries) if save else (h, last)
 
 
@@ -339,10 +364,10 @@ def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="s
         return dx.zero_(), dg.zero_(), dh0
     device = x.get_device()
     stream = _current_stream(device)
-    *ws, call = _workspace(sizes, device, stream, x)
-    r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, cp, *ws, 0, 0, 0, 0, *df, lp,
-                         dx.data_ptr(), T * C, C, dg.data_ptr(), T * C, C, dh0.data_ptr())
-    fftmv_recurrence_backward(r, stream)
+    with _workspace(sizes, device, stream, x) as (*ws, call):
+        r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, cp, *ws, 0, 0, 0, 0, *df, lp,
+                             dx.data_ptr(), T * C, C, dg.data_ptr(), T * C, C, dh0.data_ptr())
+        fftmv_recurrence_backward(r, stream)
     return dx, dg, dh0
 
 

@@ -1,0 +1,99 @@
+"""The torch layer of the sequence operators on the host: workspaces shared by
+threads, and the checks that need no device. CPU only."""
+import gc
+import threading
+import time
+import weakref
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from fft_block_toeplitz_amd import sequence as sq  # noqa: E402
+
+
+@pytest.fixture
+def shared(monkeypatch):
+    """The stream's workspace made on the CPU, slowly enough that threads meet in it."""
+    monkeypatch.setattr(sq, "_workspaces", {})
+    monkeypatch.setattr(sq._torch_module().cuda, "is_current_stream_capturing", lambda: False)
+    zeros = torch.zeros
+
+    def slow(*args, **kwargs):
+        time.sleep(0.002)
+        return zeros(*args, **kwargs)
+
+    monkeypatch.setattr(torch, "zeros", slow)
+    return torch.empty(0)
+
+
+def test_threads_of_one_stream_share_a_workspace_safely(shared):
+    """Calls of growing and changing sizes from eight threads: every call has
+    a number of its own, in the order of the launches, and its counters and
+    words are alive and as large as it asked for when it is launched, and still
+    the stream's own: no other thread has replaced them."""
+    launched, errors = [], []
+    start = threading.Barrier(8)
+
+    def launch(few, many, counters, counter_bytes, words, word_bytes, call):
+        kept = {t.data_ptr(): t.numel() for t in gc.get_objects() if type(t) is torch.Tensor and t.dtype is torch.uint8}
+        if kept.get(counters, 0) < few or kept.get(words, 0) < many or counter_bytes < few or word_bytes < many:
+            errors.append("memory of a call that is about to be launched was freed")
+        if not any(w[0] == counters and w[2] == words for w in sq._workspaces.values()):
+            errors.append("a call uses a workspace that is not the stream's any more")
+        launched.append((words, call))
+        time.sleep(0.0005)
+
+    def work(k):
+        start.wait()
+        for i in range(12):
+            few, many = 256 * (1 + (k + i) % 3), 4096 * (1 + (3 * k + 5 * i) % 11)
+            with sq._workspace((1, few, many), 0, 0, shared) as w:
+                launch(few, many, *w)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors[0]
+    by_memory = {}
+    for words, call in launched:
+        by_memory.setdefault(words, []).append(call)
+    for calls in by_memory.values():
+        assert calls == sorted(set(calls)), "numbers repeat or run backwards"
+
+
+def test_a_call_without_a_workspace_takes_none(shared):
+    with sq._workspace((0, 0, 0), 0, 0, shared) as w:
+        assert tuple(w) == (0, 0, 0, 0, 0)
+    assert not sq._workspaces
+
+
+def test_captured_calls_hold_memory_of_their_own(shared, monkeypatch):
+    """Two captured calls: not the stream's workspace, alive until launched."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    made = []
+    zeros = torch.zeros
+
+    def watched(*args, **kwargs):
+        t = zeros(*args, **kwargs)
+        made.append(weakref.ref(t))
+        return t
+
+    monkeypatch.setattr(torch, "zeros", watched)
+    for _ in range(2):
+        with sq._workspace((1, 256, 512), 0, 0, shared) as w:
+            assert [r().data_ptr() for r in made] == [w[0], w[2]] and w[4] == 1
+        made.clear()
+    assert not sq._workspaces
+
+
+def test_numbers_start_again_on_a_cleared_workspace(shared):
+    with sq._workspace((1, 256, 512), 0, 0, shared) as w:
+        assert w[4] == 1
+    entry = next(iter(sq._workspaces.values()))
+    entry[4] = 2 ** 32 - 1
+    entry[6].fill_(255)
+    with sq._workspace((1, 256, 512), 0, 0, shared) as w:
+        assert w[4] == 1 and not entry[6].any()
