@@ -3,7 +3,7 @@ import threading
 
 import pytest
 
-from test_gpu_sequence import fields
+from test_gpu_sequence import check_norm, fields
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -61,3 +61,10 @@ def test_threads_on_one_stream(fm):
     assert sum(map(len, got)) == 120
     for j, outs in sum(got, []):
         assert all(torch.equal(a, b) for a, b in zip(outs, want[j]))
+
+
+@pytest.mark.parametrize("D", [8185, 8190])
+def test_norm_backward_of_the_widest_groups(fm, D):
+    """16-bit groups that cut vectors and take all of a workgroup's lanes: the
+    backward pass asks for more than 64 KiB of LDS."""
+    check_norm(fm, D, 5, 1, 2, D, "bf16", "silu")
