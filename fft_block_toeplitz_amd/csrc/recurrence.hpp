@@ -240,6 +240,12 @@ struct Rows {
 };
 static_assert(kRows == 4, "nibbles");
 
+// Where packed sequence i starts, clamped to the axis as lengths are.
+__device__ __forceinline__ int packed_start(const fftmv_recurrence_t &r, int i) {
+  const int T = static_cast<int>(r.steps), o = r.offsets[i];
+  return o < 0 ? 0 : o > T ? T : o;
+}
+
 // The sequence that holds `row` when packed: the last one that starts at or
 // before it (-1: none does; batch: behind the last one's end).
 __device__ __forceinline__ int packed_sequence(const fftmv_recurrence_t &r, int row) {
@@ -278,10 +284,10 @@ __device__ __forceinline__ Chunk chunk_at(const fftmv_recurrence_t &r, const Sca
   if (r.offsets) {
     seq = packed_sequence(r, t0);
     const bool held = seq >= 0 && seq < S && t0 < T;
-    head = place == 0 || !held || r.offsets[seq] == t0;
-    ordinary = held && T - t0 > kChunk && end < r.offsets[seq + 1];
+    head = place == 0 || !held || packed_start(r, seq) == t0;
+    ordinary = held && T - t0 > kChunk && end < packed_start(r, seq + 1);
     const int e = ordinary ? seq : packed_sequence(r, end - 1);
-    tail = end >= T || e < 0 || e >= S || r.offsets[e + 1] == end;
+    tail = end >= T || e < 0 || e >= S || packed_start(r, e + 1) == end;
   } else {
     seq = chain * a.per;
     const int held = a.per > 1 || T == 0 ? 0 : held_steps(r, seq);
@@ -312,13 +318,13 @@ __device__ __forceinline__ Rows rows_of(const fftmv_recurrence_t &r, const ScanA
     for (int i = 0; i < kRows; ++i) {
       const bool here = i < left;
       const int row = q.row0 + i;
-      while (here && s < S && row >= r.offsets[s + 1]) ++s;  // on to the next sequence that holds a row
+      while (here && s < S && row >= packed_start(r, s + 1)) ++s;  // on to the next sequence that holds a row
       const bool held = here && s >= 0 && s < S;
       q.seq[i] = held ? s : 0;
       if (!here) q.bits |= 1u << (16 + i);
       if (!held) q.bits |= 1u << i;
-      if (held && row == r.offsets[s]) q.bits |= 1u << (4 + i);
-      if (held && row + 1 == r.offsets[s + 1]) q.bits |= 1u << (8 + i);
+      if (held && row == packed_start(r, s)) q.bits |= 1u << (4 + i);
+      if (held && row + 1 == packed_start(r, s + 1)) q.bits |= 1u << (8 + i);
     }
   } else {
     const bool many = a.per > 1;
@@ -410,7 +416,7 @@ __device__ __forceinline__ void pass_empty(const fftmv_recurrence_t &r, int seg,
                                            float *to) {
 #pragma unroll 1
   for (int64_t b = seg; b < r.batch; b += kSegs)
-    if (r.offsets ? r.offsets[b + 1] <= r.offsets[b] : true) {
+    if (!r.offsets || packed_start(r, static_cast<int>(b) + 1) <= packed_start(r, static_cast<int>(b))) {
       float v[VEC];
       load_state(from, b, r.channels, ch, v);
       store_state(to, b, r.channels, ch, v);

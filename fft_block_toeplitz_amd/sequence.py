@@ -305,7 +305,7 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     ``lengths`` (int32 [batch]): padded batch, steps from lengths[b] on do
     not matter and come back zero. ``offsets`` (int32 [sequences + 1]): x is
     [steps, channels], sequence b its rows offsets[b]..offsets[b+1]-1; rows
-    of no sequence come back zero.
+    of no sequence come back zero. Both are clamped to 0..steps.
 
     Returns h (x's type) and the last states, float32 [batch, channels];
     with ``save`` also the carries that ``recurrence_backward`` needs. Runs

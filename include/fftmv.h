@@ -327,9 +327,9 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  *            as zeros
  *   packed   one axis of `steps` steps in all, sequence b being the steps
  *            offsets[b]..offsets[b+1]-1 (ascending; equal neighbours: an
- *            empty sequence); steps before offsets[0] or from
- *            offsets[batch] on belong to none, do not matter, and are
- *            written as zeros; batch strides are ignored
+ *            empty sequence; values are clamped to 0..steps); steps before
+ *            offsets[0] or from offsets[batch] on belong to none, do not
+ *            matter, and are written as zeros; batch strides are ignored
  * lengths / offsets are device arrays of int32. Neither their contents nor
  * anything else on the device is read by the host.
  *

@@ -68,3 +68,25 @@ def test_norm_backward_of_the_widest_groups(fm, D):
     """16-bit groups that cut vectors and take all of a workgroup's lanes: the
     backward pass asks for more than 64 KiB of LDS."""
     check_norm(fm, D, 5, 1, 2, D, "bf16", "silu")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T,cuts", [(300, [-5, 0, 120, 290, 400, 500]), (300, [-9, -9, 300, 301]), (100, [0, 128, 200]),
+                                    (256, [0, 257, 999]), (0, [0, 3, 9])])
+def test_recurrence_offsets_are_clamped_as_lengths_are(fm, dtype, T, cuts):
+    """Offsets below 0 and above the steps stand for 0 and the steps: sequences
+    that end behind the axis end with it, those that start there are empty."""
+    C, B = 40, len(cuts) - 1
+    x, g = fields(41, (T, C), dtype, "sigmoid")
+    h0, dl = torch.randn(2, B, C, device="cuda")
+    dh = torch.randn(T, C, device="cuda").to(x.dtype)
+    got = []
+    for c in (cuts, [min(max(v, 0), T) for v in cuts]):
+        # what an output that is not written would be found to hold
+        del_me = [torch.full((B, C), float("nan"), device="cuda") for _ in range(4)]
+        del del_me
+        offs = torch.tensor(c, dtype=torch.int32, device="cuda")
+        h, last, carries = fm.recurrence(x, g, h0, offsets=offs, save=True)
+        got.append((h, last) + fm.recurrence_backward(dh, x, g, carries, h0, dl, offsets=offs))
+    for a, b in zip(*got):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
