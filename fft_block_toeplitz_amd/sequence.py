@@ -170,6 +170,8 @@ def _choice(value, table, name):
 
 def _span(t):
     """First byte and the byte after the last of a strided tensor."""
+    if t.is_contiguous():
+        return t.data_ptr(), t.data_ptr() + t.nbytes
     n = sum((s - 1) * st for s, st in zip(t.shape, t.stride())) + 1 if t.numel() else 0
     return t.data_ptr(), t.data_ptr() + n * t.element_size()
 
@@ -320,7 +322,7 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     xf, gf = _field(x, shape, x, "x"), _field(gate, shape, x, "gate")
     h0p = _floats(h0, (B, C), x, "h0")
     lens, offs = _ints(lengths, B, x, "lengths"), _ints(offsets, B + 1, x, "offsets")
-    h = _output(out, x, (x, gate))
+    h = _output(out, x, (x, gate, h0, lengths, offsets))
     last = x.new_empty((B, C), dtype=_torch.float32)
     if B == 0:
         h.zero_()
@@ -398,7 +400,7 @@ def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="compl
     if slots is None and B > places:
         raise ValueError(f"{B} streams without slots need as many places, the state has {places}")
     sp = _ints(slots, B, x, "slots")
-    h = _output(out, x, (x, gate, state))
+    h = _output(out, x, (x, gate, state, slots))
     if B == 0 or places == 0:
         return h.zero_()
     fftmv_recurrence_step(_STEP.pack(B, C, places, dtype, *kinds, 0, xp, xs, gp, gs, state.data_ptr(),
@@ -457,7 +459,7 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
     xf = _field(v, shape, v, "x")
     wp, bp = _floats(weight, (C,), x, "weight"), _floats(bias, (C,), x, "bias")
     lens = _ints(lengths, N, x, "lengths")
-    y = _output(out, x, (x,))
+    y = _output(out, x, (x, weight, bias, lengths))
     stats = x.new_empty((N, groups, 2), dtype=_torch.float32) if save else None
     if N == 0:
         return (y, stats) if save else y

@@ -90,3 +90,28 @@ def test_recurrence_offsets_are_clamped_as_lengths_are(fm, dtype, T, cuts):
         got.append((h, last) + fm.recurrence_backward(dh, x, g, carries, h0, dl, offsets=offs))
     for a, b in zip(*got):
         assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+def test_outputs_that_overlap_any_input_are_refused(fm):
+    """Not only x and gate: an `out` over states, parameters or index arrays is refused as well."""
+    flat = torch.zeros(4096, device="cuda")
+    x = torch.zeros(2, 1, 66, device="cuda")
+    state, out = flat[:132].view(2, 66), flat[:132].view(2, 1, 66)
+    ints = flat.view(torch.int32)
+    tokens = torch.zeros(2, 66, device="cuda")
+    bad = [
+        lambda: fm.recurrence(x, x, state, out=out),
+        lambda: fm.recurrence(x, x, out=out, lengths=ints[100:102]),
+        lambda: fm.recurrence(x[:, 0], x[:, 0], out=out[:, 0], offsets=ints[:4]),
+        lambda: fm.recurrence_step(tokens, tokens, torch.zeros(2, 66, device="cuda"), ints[4:6], out=out[:, 0]),
+        lambda: fm.recurrence_step(tokens, tokens, state, out=out[:, 0]),
+        lambda: fm.group_norm(tokens, 2, weight=flat[:66], out=out[:, 0]),
+        lambda: fm.group_norm(tokens, 2, bias=flat[66:132], out=out[:, 0]),
+        lambda: fm.group_norm(x, 2, lengths=ints[131:133], out=out),
+    ]
+    for k, call in enumerate(bad):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+            pytest.fail(f"refusal {k} did not raise")
+    # side by side is no overlap
+    assert fm.recurrence(x, x, flat[132:264].view(2, 66), out=out)[0] is out

@@ -97,3 +97,15 @@ def test_numbers_start_again_on_a_cleared_workspace(shared):
     entry[6].fill_(255)
     with sq._workspace((1, 256, 512), 0, 0, shared) as w:
         assert w[4] == 1 and not entry[6].any()
+
+
+def test_overlap_of_an_output(monkeypatch):
+    """Bytes shared with any input: contiguous, strided or a view of another type; neighbours are none."""
+    flat = torch.zeros(100)
+    out, like = flat[20:60].view(4, 10), torch.zeros(4, 10)
+    assert sq._output(out, like, (flat[:20], None, flat[60:], flat.view(torch.int32)[60:70])) is out
+    strided = flat[:60].view(6, 10)[:3, :5]  # its last element is flat[24]
+    for other in (out, flat[59:], flat[:21], strided, flat[15:].as_strided((2,), (10,)), flat.view(torch.int32)[30:31]):
+        with pytest.raises(ValueError, match="overlap"):
+            sq._output(out, like, (like, None, other))
+    assert sq._output(out, like, (flat[:50].view(5, 10)[:2, :5], flat[40:40])) is out  # ends at flat[14]; nothing at all
