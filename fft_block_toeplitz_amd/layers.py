@@ -16,6 +16,17 @@ def _rows(t):
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
+def _field_rows(t):
+    """The same for a field, whose rows have to be evenly spaced as well: a sum over an axis hands back a gradient
+    expanded over it, a transpose one with its axes in another order."""
+    t = _rows(t)
+    try:
+        sequence._samples(t)
+    except ValueError:
+        return t.contiguous()
+    return t
+
+
 class _Recurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate, h0, decay, drive, lengths, offsets):
@@ -52,7 +63,7 @@ class _GroupNorm(torch.autograd.Function):
     def backward(ctx, dy):
         x, stats, weight, bias, lengths = ctx.saved_tensors
         groups, activation = ctx.how
-        dx, dw, db = sequence.group_norm_backward(_rows(dy), x, stats, groups, weight, bias, activation=activation,
+        dx, dw, db = sequence.group_norm_backward(_field_rows(dy), x, stats, groups, weight, bias, activation=activation,
                                                   lengths=lengths)
         return dx, None, dw if weight is not None else None, db if bias is not None else None, None, None, None
 

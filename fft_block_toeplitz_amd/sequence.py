@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import struct
 import threading
 
@@ -424,7 +425,7 @@ def _samples(x):
     if x.dim() < 2:
         raise ValueError(f"x must be [samples, ..., channels], got {tuple(x.shape)}")
     try:
-        return x.view(x.shape[0], -1, x.shape[-1]) if x.numel() else x.reshape(x.shape[0], -1, x.shape[-1])
+        return x.view(x.shape[0], math.prod(x.shape[1:-1]), x.shape[-1])
     except RuntimeError:
         raise ValueError(f"the rows of x {tuple(x.shape)} with strides {x.stride()} are not evenly spaced: "
                          "make it contiguous") from None

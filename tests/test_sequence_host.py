@@ -109,3 +109,15 @@ def test_overlap_of_an_output(monkeypatch):
         with pytest.raises(ValueError, match="overlap"):
             sq._output(out, like, (like, None, other))
     assert sq._output(out, like, (flat[:50].view(5, 10)[:2, :5], flat[40:40])) is out  # ends at flat[14]; nothing at all
+
+
+def test_rows_of_fields():
+    """[samples, rows, channels] of every number of axes, empty ones too; rows that are not evenly spaced are refused."""
+    for shape in ((3, 8), (3, 4, 8), (3, 4, 5, 8), (2, 3, 4, 5, 8), (0, 4, 5, 8), (3, 0, 5, 8), (3, 4, 0, 8), (3, 4, 5, 0)):
+        v = sq._samples(torch.zeros(shape))
+        assert v.shape == (shape[0], torch.Size(shape[1:-1]).numel(), shape[-1])
+    x = torch.zeros(2, 4, 5, 8)
+    assert sq._samples(x[:, :, :, :3]).stride() == (160, 8, 1)
+    for uneven in (x.transpose(1, 2), x[:, :, :3], x.sum(1, keepdim=True).expand(2, 4, 5, 8)):
+        with pytest.raises(ValueError, match="evenly"):
+            sq._samples(uneven)
