@@ -192,6 +192,14 @@ def _output(out, like, inputs):
     return out
 
 
+def _wrote(*tensors):
+    """What a kernel has written in place, through its address, counts as written for autograd too: a graph that has
+    saved it raises in its backward pass instead of going on with other values."""
+    for t in tensors:
+        if t is not None:
+            _torch.autograd.graph.increment_version(t)
+
+
 class _On:
     """A stream that is not the current one: allocations inside belong to it,
     and tensors that came from another stream are kept for it."""
@@ -337,6 +345,7 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
                              carries.data_ptr() if save else 0, *ws, h.data_ptr(), T * C, C, last.data_ptr(), 0, 0, 0,
                              0, 0, 0, 0, 0, 0, 0, 0)
         fftmv_recurrence_forward(r, stream)
+    _wrote(out)
     return (h, last, carries) if save else (h, last)
 
 
@@ -406,6 +415,7 @@ def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="compl
         return h.zero_()
     fftmv_recurrence_step(_STEP.pack(B, C, places, dtype, *kinds, 0, xp, xs, gp, gs, state.data_ptr(),
                                      max(ss[0], C), sp, h.data_ptr(), C), _current_stream(x.get_device()))
+    _wrote(state, out)
     return h
 
 
@@ -468,6 +478,7 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
     g = _GROUP_NORM.pack(N, S, C, groups, dtype, act, eps, 0, lens, *xf, wp, bp, stats.data_ptr() if save else 0,
                          ws.data_ptr() if need else 0, need, y.data_ptr(), S * C, C, 0, 0, 0, 0, 0, 0, 0, 0)
     fftmv_group_norm_forward(g, _current_stream(x.get_device()))
+    _wrote(out)
     return (y, stats) if save else y
 
 

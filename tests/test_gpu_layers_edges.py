@@ -49,3 +49,36 @@ def test_norm_of_empty_fields(fm, shape):
     y = layers.group_norm(x, 2, w, activation="gelu")
     y.sum().backward()
     assert y.shape == shape and x.grad.shape == shape and not w.grad.any()
+
+
+def test_what_is_written_in_place_is_known_to_autograd(fm):
+    """A state that a graph has saved, stepped on or written as `out` before
+    the backward pass: an error, as for torch's own in-place operations, and
+    not the gradient of other values."""
+    from fft_block_toeplitz_amd import layers
+
+    x = torch.randn(2, 30, 16, device="cuda", requires_grad=True)
+    tokens = torch.randn(2, 16, device="cuda")
+
+    def recurrence():
+        state = torch.randn(2, 16, device="cuda")
+        return layers.recurrence(x, x.detach() + 1.0, state)[0].sum(), state
+
+    def product():
+        kept = torch.randn(2, 30, 16, device="cuda")
+        return (x * kept).sum(), kept
+
+    for graph, write in (
+            (recurrence, lambda t: fm.recurrence_step(tokens, tokens, t)),
+            (recurrence, lambda t: fm.recurrence_step(tokens, tokens, t.clone(), out=t)),
+            (product, lambda t: fm.recurrence(x.detach(), x.detach(), out=t)),
+            (product, lambda t: fm.group_norm(x.detach(), 4, out=t))):
+        loss, saved = graph()
+        write(saved)
+        with pytest.raises(RuntimeError, match="inplace|in-place"):
+            loss.backward()
+    # inference tensors have no versions; nothing to raise
+    with torch.inference_mode():
+        state = torch.zeros(2, 16, device="cuda")
+        out = torch.empty(2, 16, device="cuda")
+        assert fm.recurrence_step(tokens, tokens, state, out=out) is out and state.any()
