@@ -11,12 +11,16 @@ F_k = diag(a^k).
 Thin wrappers of the C entry points declared in ``include/fftmv.h``: they
 check arguments, allocate outputs and pass pointers; torch supplies device
 memory and streams. Elements are float32, bfloat16 or float16; states,
-statistics and parameters are float32. ``layers`` holds the differentiable
-forms. There is no fallback: without the built library every call raises.
+statistics and parameters are float32. ``recurrence`` and ``group_norm`` of
+tensors that require a gradient go through the differentiable forms in
+``layers``; with ``save=True`` they are the first half of a gradient taken by
+hand, and their results carry none. There is no fallback: without the built
+library every call raises.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -73,15 +77,21 @@ def fftmv_recurrence_sizes(batch: int, steps: int, channels: int, packed: bool) 
 
 
 def fftmv_recurrence_forward(r: bytes, stream: int = 0) -> None:
-    _check(_lib().fftmv_recurrence_forward(r, stream), "fftmv_recurrence_forward")
+    status = (_bound or _lib()).fftmv_recurrence_forward(r, stream)
+    if status:
+        _check(status, "fftmv_recurrence_forward")
 
 
 def fftmv_recurrence_backward(r: bytes, stream: int = 0) -> None:
-    _check(_lib().fftmv_recurrence_backward(r, stream), "fftmv_recurrence_backward")
+    status = (_bound or _lib()).fftmv_recurrence_backward(r, stream)
+    if status:
+        _check(status, "fftmv_recurrence_backward")
 
 
 def fftmv_recurrence_step(r: bytes, stream: int = 0) -> None:
-    _check(_lib().fftmv_recurrence_step(r, stream), "fftmv_recurrence_step")
+    status = (_bound or _lib()).fftmv_recurrence_step(r, stream)
+    if status:
+        _check(status, "fftmv_recurrence_step")
 
 
 def fftmv_group_norm_workspace(samples: int, rows: int, channels: int, groups: int, dtype: int,
@@ -93,11 +103,15 @@ def fftmv_group_norm_workspace(samples: int, rows: int, channels: int, groups: i
 
 
 def fftmv_group_norm_forward(g: bytes, stream: int = 0) -> None:
-    _check(_lib().fftmv_group_norm_forward(g, stream), "fftmv_group_norm_forward")
+    status = (_bound or _lib()).fftmv_group_norm_forward(g, stream)
+    if status:
+        _check(status, "fftmv_group_norm_forward")
 
 
 def fftmv_group_norm_backward(g: bytes, stream: int = 0) -> None:
-    _check(_lib().fftmv_group_norm_backward(g, stream), "fftmv_group_norm_backward")
+    status = (_bound or _lib()).fftmv_group_norm_backward(g, stream)
+    if status:
+        _check(status, "fftmv_group_norm_backward")
 
 
 # ---- argument checks shared by the torch layer
@@ -123,7 +137,7 @@ def _dtype_of(x, name):
     code = _types.get(x.dtype)
     if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
-    if x.get_device() != torch.cuda.current_device():
+    if x.get_device() != torch._C._cuda_getDevice():  # torch.cuda.current_device() without its check: x is there
         raise ValueError(f"{name} is on {x.device}, not on the current device")
     return code
 
@@ -192,12 +206,24 @@ def _output(out, like, inputs):
     return out
 
 
+def _wants_grad(*tensors):
+    """Autograd is on and one of these requires a gradient."""
+    if _torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
+def _no_out(out):
+    if out is not None:
+        raise ValueError("out= takes results without a gradient: call under torch.no_grad() or detach the inputs")
+
+
 def _wrote(*tensors):
     """What a kernel has written in place, through its address, counts as written for autograd too: a graph that has
     saved it raises in its backward pass instead of going on with other values."""
-    for t in tensors:
-        if t is not None:
-            _torch.autograd.graph.increment_version(t)
+    _torch.autograd.graph.increment_version([t for t in tensors if t is not None])
 
 
 class _On:
@@ -284,6 +310,9 @@ class _workspace:
         self.held = None
 
 
+_NO_WORKSPACE = contextlib.nullcontext((0, 0, 0, 0, 0))
+
+
 def _sequences(x, lengths, offsets):
     """(batch, steps, channels) of the three forms."""
     if offsets is not None:
@@ -318,13 +347,19 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     [steps, channels], sequence b its rows offsets[b]..offsets[b+1]-1; rows
     of no sequence come back zero. Both are clamped to 0..steps.
 
-    Returns h (x's type) and the last states, float32 [batch, channels];
-    with ``save`` also the carries that ``recurrence_backward`` needs. Runs
-    on ``stream`` (default: the current one), without synchronising."""
+    Returns h (x's type) and the last states, float32 [batch, channels],
+    differentiable where x, gate or h0 requires a gradient; with ``save``
+    without, but also the carries that ``recurrence_backward`` needs.
+    Runs on ``stream`` (default: the current one), without synchronising."""
     if stream is not None:
         return _elsewhere(stream, recurrence, x, gate, h0, decay=decay, drive=drive, lengths=lengths, offsets=offsets,
                           save=save, out=out)
     dtype = _dtype_of(x, "x")
+    if not save and _wants_grad(x, gate, h0, out):
+        from . import layers
+
+        _no_out(out)
+        return layers.recurrence(x, gate, h0, decay=decay, drive=drive, lengths=lengths, offsets=offsets)
     B, T, C = _sequences(x, lengths, offsets)
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
     shape, packed = x.shape, offsets is not None
@@ -340,12 +375,13 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
     carries = x.new_empty((sizes[0], C), dtype=_torch.float32) if save else None
     device = x.get_device()
     stream = _current_stream(device)
-    with _workspace(sizes, device, stream, x) as (*ws, call):
+    with _workspace(sizes, device, stream, x) if sizes[2] else _NO_WORKSPACE as (*ws, call):
         r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p,
                              carries.data_ptr() if save else 0, *ws, h.data_ptr(), T * C, C, last.data_ptr(), 0, 0, 0,
                              0, 0, 0, 0, 0, 0, 0, 0)
         fftmv_recurrence_forward(r, stream)
-    _wrote(out)
+    if out is not None:
+        _wrote(out)
     return (h, last, carries) if save else (h, last)
 
 
@@ -376,7 +412,7 @@ def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="s
         return dx.zero_(), dg.zero_(), dh0
     device = x.get_device()
     stream = _current_stream(device)
-    with _workspace(sizes, device, stream, x) as (*ws, call):
+    with _workspace(sizes, device, stream, x) if sizes[2] else _NO_WORKSPACE as (*ws, call):
         r = _RECURRENCE.pack(B, T, C, dtype, *kinds, call, lens, offs, *xf, *gf, h0p, cp, *ws, 0, 0, 0, 0, *df, lp,
                              dx.data_ptr(), T * C, C, dg.data_ptr(), T * C, C, dh0.data_ptr())
         fftmv_recurrence_backward(r, stream)
@@ -390,10 +426,13 @@ def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="compl
     int32 [batch], the place of each stream (None: stream b has place b). A
     slot outside the cache, -1 say, marks an idle stream: zeros come back
     and no state changes. Slots of one call must differ. Returns h [batch,
-    channels]."""
+    channels], which has no gradient: inputs that require one are refused
+    unless autograd is off."""
     if stream is not None:
         return _elsewhere(stream, recurrence_step, x, gate, state, slots, decay=decay, drive=drive, out=out)
     dtype = _dtype_of(x, "x")
+    if _wants_grad(x, gate, state, out):
+        raise ValueError("a step in place has no gradient: call it under torch.no_grad(), or recurrence on whole series")
     shape = x.shape
     if len(shape) != 2:
         raise ValueError(f"x must be [batch, channels], got {tuple(shape)}")
@@ -454,12 +493,18 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
     ``lengths`` (int32 [samples]): sample n holds its first lengths[n] rows;
     the others enter no sum whatever they hold, and come back zero.
 
-    Returns y (x's type); with ``save`` also the statistics, float32
+    Returns y (x's type), differentiable where x, weight or bias requires a
+    gradient; with ``save`` without, but also the statistics, float32
     [samples, groups, 2] (mean, rstd), that ``group_norm_backward`` needs."""
     if stream is not None:
         return _elsewhere(stream, group_norm, x, groups, weight, bias, eps=eps, activation=activation, lengths=lengths,
                           save=save, out=out)
     dtype = _dtype_of(x, "x")
+    if not save and _wants_grad(x, weight, bias, out):
+        from . import layers
+
+        _no_out(out)
+        return layers.group_norm(x, groups, weight, bias, eps=eps, activation=activation, lengths=lengths)
     v = _samples(x)
     N, S, C = shape = v.shape
     if not isinstance(groups, int) or groups < 1 or C < 1 or C % groups:
@@ -478,7 +523,8 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
     g = _GROUP_NORM.pack(N, S, C, groups, dtype, act, eps, 0, lens, *xf, wp, bp, stats.data_ptr() if save else 0,
                          ws.data_ptr() if need else 0, need, y.data_ptr(), S * C, C, 0, 0, 0, 0, 0, 0, 0, 0)
     fftmv_group_norm_forward(g, _current_stream(x.get_device()))
-    _wrote(out)
+    if out is not None:
+        _wrote(out)
     return (y, stats) if save else y
 
 

@@ -82,3 +82,45 @@ def test_what_is_written_in_place_is_known_to_autograd(fm):
         state = torch.zeros(2, 16, device="cuda")
         out = torch.empty(2, 16, device="cuda")
         assert fm.recurrence_step(tokens, tokens, state, out=out) is out and state.any()
+
+
+def test_public_names_keep_gradients(fm):
+    """fm.recurrence and fm.group_norm of tensors that require a gradient give
+    results that have one; where there is none to give, they say so."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    x, g, h0, w, b = leaf(gen, 2, 40, 16), leaf(gen, 2, 40, 16), leaf(gen, 2, 16), leaf(gen, 16), leaf(gen, 16)
+    leaves = (x, g, h0, w, b)
+
+    def grads(m):
+        h, last = m.recurrence(x, g, h0, decay="sigmoid", drive="plain")
+        y = m.group_norm(h, 4, w, b, eps=1e-3, activation="gelu")
+        return torch.autograd.grad(y.square().sum() + last.sum(), leaves)
+
+    from fft_block_toeplitz_amd import layers
+
+    for a, c in zip(grads(fm), grads(layers)):
+        assert torch.equal(a, c)
+    # one of the inputs is enough
+    assert fm.recurrence(x.detach(), g.detach(), h0)[1].requires_grad
+    assert fm.group_norm(x.detach(), 4, w).requires_grad and fm.group_norm(x.detach(), 4, bias=b).requires_grad
+    # on another stream as well
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    assert fm.recurrence(x, g, stream=side)[0].requires_grad
+    torch.cuda.current_stream().wait_stream(side)
+    # without gradients nothing changes
+    with torch.no_grad():
+        assert not fm.recurrence(x, g)[0].requires_grad and not fm.group_norm(x, 4, w).requires_grad
+        out = torch.empty_like(x)
+        assert fm.recurrence(x, g, out=out)[0] is out
+        fm.recurrence_step(x[:, 0], g[:, 0], torch.zeros(2, 16, device="cuda"))
+    # save=True is the first half of a gradient by hand
+    assert not any(t.requires_grad for t in fm.recurrence(x, g, save=True))
+    assert not any(t.requires_grad for t in fm.group_norm(x, 4, w, save=True))
+    state = torch.zeros(2, 16, device="cuda")
+    for call in (lambda: fm.recurrence(x, g, out=torch.empty_like(x)), lambda: fm.group_norm(x, 4, out=torch.empty_like(x)),
+                 lambda: fm.recurrence_step(x[:, 0], g[:, 0].detach(), state),
+                 lambda: fm.recurrence_step(x[:, 0].detach(), g[:, 0].detach(), h0)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
