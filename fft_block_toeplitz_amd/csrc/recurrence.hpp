@@ -19,7 +19,8 @@
 //     for anything, then folds the maps in front of it onto the nearest
 //     published state: the same sequence of operations whatever state it
 //     found, since the state behind a chunk is itself defined as
-//     fma(A, state before, H).
+//     fma(A, state before, H). (A chunk whose A is out of FP32's range publishes
+//     no map, only its state, which went through its segments one by one.)
 // A chunk's place in its chain is drawn from a counter, not taken from
 // blockIdx: every chunk in front has then been started by a running
 // workgroup, which publishes without waiting, so all waits end in whatever
@@ -189,24 +190,25 @@ __device__ __forceinline__ float state_before(const ScanChain &s, int p, int c) 
 }
 
 // What a chunk does with the states of its chain, by one thread per column:
-// publishes its map (A, H), or, when it is `closed` (nothing that enters it
-// leaves it), its state H; returns the state that enters it, where `needed`.
+// publishes its map (A, H), where it has one, or, when it is `closed` (nothing
+// that enters it leaves it), its state H; returns the state that enters it,
+// where `needed`. behind(h): the state behind the chunk for h in front.
 // `early`: what peek saw as the state in front some time ago.
-template <int W>
+template <int W, typename F>
 __device__ __forceinline__ float meet_chain(const ScanChain &s, int p, int col, float A, float H, bool closed,
-                                            bool needed, uint64_t early) {
+                                            bool mapped, bool needed, uint64_t early, F behind) {
   // the columns of a wave wait together
   const bool ready = needed && __ballot(!is_there(s, early)) == 0;
   float in = 0.0f;
   if (closed) {
     publish<W>(s, p, 2, col, H);
-  } else if (!ready) {
+  } else if (!ready && mapped) {
     publish<W>(s, p, 0, col, A);
     publish<W>(s, p, 1, col, H);
   }
   if (needed) in = ready ? value_of(early) : state_before<W>(s, p, col);
   if (!closed) {
-    publish<W>(s, p, 2, col, fmaf(A, in, H));
+    publish<W>(s, p, 2, col, behind(in));
   }
   return in;
 }
@@ -454,6 +456,29 @@ __device__ __forceinline__ uint32_t read_segment_bits(const uint8_t *bits) {
 // from the last): h becomes the state behind them.
 __device__ __forceinline__ float through(bool constant, float A, float H, float h) {
   return constant ? H : fmaf(A, h, H);
+}
+
+// A product of decays that FP32 holds. Decays above one can pass its range
+// within a chunk while the states that they act on are zero or tiny: such a
+// product is used nowhere, and the states go through the single segments (of
+// kRows decays each) instead.
+__device__ __forceinline__ bool in_range(float A) { return fabsf(A) <= 3.402823466e38f; }
+
+// The same through group j of SG segments, whose maps are A, H and whose joined
+// map is gA, gH; BACK from the last segment.
+template <bool BACK, int SG, int W>
+__device__ __forceinline__ float through_group(const float (*A)[W], const float (*H)[W], const float (*gA)[W],
+                                               const float (*gH)[W], uint32_t constants, int j, int col, float h) {
+  constexpr uint32_t kGroup = ~0u >> (32 - SG);
+  if (constants >> (j * SG) & kGroup) return gH[j][col];
+  const float a = gA[j][col];
+  if (in_range(a)) return fmaf(a, h, gH[j][col]);
+#pragma unroll 1
+  for (int i = 0; i < SG; ++i) {
+    const int seg = j * SG + (BACK ? SG - 1 - i : i);
+    h = fmaf(A[seg][col], h, H[seg][col]);
+  }
+  return h;
 }
 
 template <typename F>

@@ -27,6 +27,7 @@ struct BackwardLds {
   float enter[W];                      // what the chunk behind hands over
   __align__(8) uint8_t front_bits[kWaves], back_bits[kWaves];
   uint32_t ticket;
+  uint32_t over;  // a group's product of decays is out of range
 };
 
 // The chunk's join: from the segments' maps (written, not yet synchronised)
@@ -39,6 +40,7 @@ __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const
   constexpr int G = BackwardLds<W>::G, SG = kSegs / G;
   constexpr uint32_t kGroup = ~0u >> (32 - SG);
   const int tid = threadIdx.x, col = tid % W, grp = tid / W;
+  if (tid == 0) lds.over = 0;
   __syncthreads();
   const uint32_t fronts = read_segment_bits(lds.front_bits), backs = read_segment_bits(lds.back_bits);
 
@@ -56,7 +58,13 @@ __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const
   lds.gA[grp][col] = cA;
   lds.gH[grp][col] = cH;
   lds.gS[grp][col] = cS;
+  if (!in_range(cA)) lds.over = 1;
   __syncthreads();
+  auto walk_back = [&](float v, int from) {  // through the groups behind `from`, the last one first
+#pragma unroll 1
+    for (int j = G - 1; j > from; --j) v = through_group<true, SG, W>(lds.A, lds.S, lds.gA, lds.gS, backs, j, col, v);
+    return v;
+  };
 
   if (tid < W) {  // what the chunk behind hands over
     float in = 0.0f;
@@ -67,14 +75,27 @@ __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const
         S = through(backs >> (j * SG) & kGroup, lds.gA[j][col], lds.gS[j][col], S);
         A *= lds.gA[j][col];
       }
-      in = meet_chain<W>(s, order, col, A, S, backs, !c.tail, early);
+      const bool mapped = in_range(A), all = __ballot(!mapped) == 0;
+      if (!all && !mapped) S = walk_back(0.0f, -1);  // (a group's product out of range makes A infinite or NaN)
+      in = meet_chain<W>(s, order, col, A, S, backs, mapped, !c.tail, early, [&](float v) {
+        float u = fmaf(A, v, S);
+        if (!all && !mapped) u = walk_back(v, -1);
+        return u;
+      });
     }
     lds.enter[col] = in;
   }
   // meanwhile, the state that enters each segment
+  const bool over = __builtin_amdgcn_readfirstlane(lds.over);
   {
     float h = carry;
-    for (int j = 0; j < grp; ++j) h = through(fronts >> (j * SG) & kGroup, lds.gA[j][col], lds.gH[j][col], h);
+    if (over) {
+#pragma unroll 1
+      for (int j = 0; j < grp; ++j) h = through_group<false, SG, W>(lds.A, lds.H, lds.gA, lds.gH, fronts, j, col, h);
+      __syncthreads();  // the segments' maps are overwritten below
+    } else {
+      for (int j = 0; j < grp; ++j) h = through(fronts >> (j * SG) & kGroup, lds.gA[j][col], lds.gH[j][col], h);
+    }
 #pragma unroll
     for (int i = 0; i < SG; ++i) {
       float &H = lds.H[grp * SG + i][col];
@@ -85,7 +106,12 @@ __device__ __forceinline__ void backward_join(const fftmv_recurrence_t &r, const
   }
   __syncthreads();
   float v = lds.enter[col];
-  for (int j = G - 1; j > grp; --j) v = through(backs >> (j * SG) & kGroup, lds.gA[j][col], lds.gS[j][col], v);
+  if (over) {
+    v = walk_back(v, grp);
+    __syncthreads();
+  } else {
+    for (int j = G - 1; j > grp; --j) v = through(backs >> (j * SG) & kGroup, lds.gA[j][col], lds.gS[j][col], v);
+  }
 #pragma unroll
   for (int i = SG - 1; i >= 0; --i) {
     float &S = lds.S[grp * SG + i][col];

@@ -19,6 +19,7 @@ struct ForwardLds {
   float enter[W];                         // the state that enters the chunk
   __align__(8) uint8_t bits[kWaves];
   uint32_t ticket;
+  uint32_t over;  // a group's product of decays is out of range
 };
 
 // The chunk's join: from the segments' maps in lds.A, lds.H (written, not yet
@@ -31,6 +32,7 @@ __device__ __forceinline__ void forward_join(const fftmv_recurrence_t &r, const 
   constexpr uint32_t kGroup = ~0u >> (32 - SG);
   static_assert(G * SG == kSegs, "whole groups");
   const int tid = threadIdx.x, col = tid % W, grp = tid / W;
+  if (tid == 0) lds.over = 0;
   __syncthreads();
   const uint32_t constants = read_segment_bits(lds.bits);
 
@@ -44,7 +46,13 @@ __device__ __forceinline__ void forward_join(const fftmv_recurrence_t &r, const 
   }
   lds.gA[grp][col] = cA;
   lds.gH[grp][col] = cH;
+  if (!in_range(cA)) lds.over = 1;
   __syncthreads();
+  auto walk = [&](float h, int groups) {
+#pragma unroll 1
+    for (int j = 0; j < groups; ++j) h = through_group<false, SG, W>(lds.A, lds.H, lds.gA, lds.gH, constants, j, col, h);
+    return h;
+  };
 
   if (tid < W) {  // the state that enters the chunk
     const int64_t ch = column_channel<VEC>(r.channels, static_cast<int64_t>(block) * W + col);
@@ -59,8 +67,15 @@ __device__ __forceinline__ void forward_join(const fftmv_recurrence_t &r, const 
         H = through(constants >> (j * SG) & kGroup, lds.gA[j][col], lds.gH[j][col], H);
         A *= lds.gA[j][col];
       }
-      if (first) H = fmaf(A, in, H);
-      const float from = meet_chain<W>(s, c.place, col, A, H, first || constants, !c.head, early);
+      const bool mapped = in_range(A), all = __ballot(!mapped) == 0;
+      if (!all && !mapped) H = walk(0.0f, G);  // (a group's product out of range makes A infinite or NaN)
+      auto behind = [&](float h) {
+        float v = fmaf(A, h, H);
+        if (!all && !mapped) v = walk(h, G);
+        return v;
+      };
+      if (first) H = behind(in);
+      const float from = meet_chain<W>(s, c.place, col, A, H, first || constants, mapped, !c.head, early, behind);
       if (!first) in = from;
       if (r.carries) r.carries[(static_cast<int64_t>(c.chain) * axis.places + c.place) * r.channels + ch] = in;
     }
@@ -69,7 +84,12 @@ __device__ __forceinline__ void forward_join(const fftmv_recurrence_t &r, const 
   __syncthreads();
 
   float h = lds.enter[col];
-  for (int j = 0; j < grp; ++j) h = through(constants >> (j * SG) & kGroup, lds.gA[j][col], lds.gH[j][col], h);
+  if (__builtin_amdgcn_readfirstlane(lds.over)) {
+    h = walk(h, grp);
+    __syncthreads();  // the segments' maps are overwritten below
+  } else {
+    for (int j = 0; j < grp; ++j) h = through(constants >> (j * SG) & kGroup, lds.gA[j][col], lds.gH[j][col], h);
+  }
 #pragma unroll
   for (int i = 0; i < SG; ++i) {
     float &H = lds.H[grp * SG + i][col];

@@ -357,7 +357,9 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  * numbers. Calls that share one must
  * be ordered. h0 NULL stands for zeros. A state that is not finite stays
  * not finite (infinity or NaN) until its sequence ends; it reaches no other
- * sequence or channel.
+ * sequence or channel. Decays may be above one, and their product over a
+ * sequence beyond FP32's range, as long as the states and gradients are not;
+ * only the product of four neighbouring decays has to stay below 3.4e38.
  * Errors: FFTMV_ERR_INVALID_ARG (a null or misaligned pointer, a size < 1
  * -- steps may be 0 --, an unknown type/decay/drive, both lengths and
  * offsets, a workspace that is too small); FFTMV_ERR_UNSUPPORTED_SIZE

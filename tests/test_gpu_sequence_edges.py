@@ -1,9 +1,11 @@
 """The sequence operators at the edges of what their entry points accept."""
 import threading
 
+import numpy as np
 import pytest
 
-from test_gpu_sequence import check_norm, fields
+import sequence_reference as R
+from test_gpu_sequence import check_norm, fields, host, near
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -115,3 +117,41 @@ def test_outputs_that_overlap_any_input_are_refused(fm):
             pytest.fail(f"refusal {k} did not raise")
     # side by side is no overlap
     assert fm.recurrence(x, x, flat[132:264].view(2, 66), out=out)[0] is out
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("decay,drive", [("value", "plain"), ("exp", "plain"), ("value", "complement")])
+@pytest.mark.parametrize("bits,steps", [(2, 100), (10, 20)])
+def test_recurrence_of_decays_above_one(fm, dtype, decay, drive, bits, steps):
+    """Growth by 2^200 in a window of some steps, which no FP32 product of
+    decays holds, over states and gradients that are zero or 2^-110: what the
+    definition gives is in range, and so is what the kernels give."""
+    B, T, C = 3, 700, 72
+    x, g = fields(42, (B, T, C), dtype, decay)
+    dh, dl = torch.randn(B, T, C, device="cuda").to(x.dtype), torch.randn(B, C, device="cuda")
+    of = (lambda a: a) if decay == "value" else lambda a: float(np.log(a))  # noqa: E731
+    small = 2.0 ** -110
+    for b, t in enumerate((60, 128, 301)):  # over a chunk's edge, inside one, over a later edge
+        end = t + steps
+        x[b, :end] = 0.0
+        g[b, :t], g[b, t:end], g[b, end:] = of(1.0), of(2.0 ** bits), of(0.5)
+        dh[b, t:end] = 0.0
+        dh[b, end:] *= small
+    dl *= small
+    dh[..., 1::3] = 0.0
+    dl[:, 1::3] = 0.0
+    h0 = torch.zeros(B, C, device="cuda")
+    h0[:, ::3] = small
+    for lengths in (None, [700, 500, 300]):
+        lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        how = {"decay": decay, "drive": drive, "lengths": lens}
+        h, last, carries = fm.recurrence(x, g, h0, save=True, **how)
+        dx, dg, dh0 = fm.recurrence_backward(dh, x, g, carries, h0, dl, **how)
+        for b in range(B):
+            n = T if lengths is None else lengths[b]
+            r = R.Recurrence(host(x)[b, :n], host(g)[b, :n], host(h0)[b], decay, drive, dtype, host(dh)[b, :n], host(dl)[b])
+            assert max(np.abs(v).max() for v in (r.h, r.dx, r.dg, r.dh0)) < 1e38  # the definition is in range
+            for got, want, bound, what in ((h[b, :n], r.h, r.eh, "h"), (last[b], r.last, r.elast, "last state"),
+                                           (dx[b, :n], r.dx, r.edx, "dx"), (dg[b, :n], r.dg, r.edg, "dgate"),
+                                           (dh0[b], r.dh0, r.edh0, "dh0")):
+                near(got, want, bound + 2.0 ** -126, what)  # the smallest normal number
