@@ -121,12 +121,25 @@ __device__ __forceinline__ float exp_of(float v) {
   return __builtin_amdgcn_exp2f(1.44269504088896341f * v);
 }
 
+// 1 / v, v in [1, 2]. For 16-bit elements the hardware's reciprocal (1 ulp). FP32
+// ones take a step of Newton's iteration behind it, which leaves half an ulp,
+// the quotient's own rounding: a decay's error enters once a step, and with the
+// bare reciprocal the gradient of h0 over 1000 steps was off by 3.2e-7 instead
+// of 2.4e-7. (8 x 1000 x 5000 FP32 forward: 119 us bare, 122 so, 135 with the
+// division.)
+template <typename T>
+__device__ __forceinline__ float inverse_of(float v) {
+  const float r = __builtin_amdgcn_rcpf(v);
+  if constexpr (sizeof(T) == 4) return fmaf(r, fmaf(-v, r, 1.0f), r);
+  return r;
+}
+
 template <typename T, int DECAY>
 __device__ __forceinline__ Terms decay_terms(float g) {
   Terms r;
   if constexpr (DECAY == FFTMV_DECAY_SIGMOID) {
     const float t = exp_of<T>(-fabsf(g));
-    const float big = __builtin_amdgcn_rcpf(1.0f + t), small = t * big;
+    const float big = inverse_of<T>(1.0f + t), small = t * big;
     r.a = g >= 0.0f ? big : small;
     r.rest = g >= 0.0f ? small : big;
     r.slope = big * small;

@@ -155,3 +155,35 @@ def test_recurrence_of_decays_above_one(fm, dtype, decay, drive, bits, steps):
                                            (dx[b, :n], r.dx, r.edx, "dx"), (dg[b, :n], r.dg, r.edg, "dgate"),
                                            (dh0[b], r.dh0, r.edh0, "dh0")):
                 near(got, want, bound + 2.0 ** -126, what)  # the smallest normal number
+
+
+def _candidates(g):
+    """(a, 1 - a, da/dg) of a sigmoid in FP32, correctly rounded but for the
+    exponential, which may be one unit in the last place off: all that can come out."""
+    f = np.float32
+    true = np.exp(-np.abs(g.astype(np.float64)))
+    t = true.astype(f)
+    for t in (t, np.nextafter(t, f(0)), np.nextafter(t, f(np.inf))):
+        big = f(1) / (f(1) + t)
+        small = t * big
+        yield np.where(g >= 0, big, small), np.where(g >= 0, small, big), big * small
+
+
+def test_fp32_decays_are_rounded_once_an_operation(fm):
+    """One step from a state of one (the decay), with a drive of one (its
+    complement), and their gradient by the gate (the slope)."""
+    rng = np.random.default_rng(43)
+    C = 20000
+    gv = rng.uniform(-12, 12, C).astype(np.float32)
+    g = torch.from_numpy(gv).cuda().view(1, 1, C)
+    zero, one = torch.zeros(1, 1, C, device="cuda"), torch.ones(1, 1, C, device="cuda")
+    a, _, carries = fm.recurrence(zero, g, one[0], drive="plain", save=True)
+    _, slope, _ = fm.recurrence_backward(one, zero, g, carries, one[0], drive="plain")
+    rest, _ = fm.recurrence(one, g)
+    step_a = fm.recurrence_step(zero[0], g[0], torch.ones(1, C, device="cuda"), drive="plain")
+    step_rest = fm.recurrence_step(one[0], g[0], torch.zeros(1, C, device="cuda"))
+    may = list(_candidates(gv))
+    for got, k, what in ((a, 0, "a"), (rest, 1, "1 - a"), (slope, 2, "slope"), (step_a, 0, "step's a"),
+                         (step_rest, 1, "step's 1 - a")):
+        got = got.flatten().cpu().numpy()
+        assert np.any([got == m[k] for m in may], axis=0).all(), what
