@@ -121,7 +121,7 @@ __device__ __forceinline__ float exp_of(float v) {
   return __builtin_amdgcn_exp2f(1.44269504088896341f * v);
 }
 
-// 1 / v, v in [1, 2]. For 16-bit elements the hardware's reciprocal (1 ulp). FP32
+// 1 / v, v in [1, 1e38]. For 16-bit elements the hardware's reciprocal (1 ulp). FP32
 // ones take a step of Newton's iteration behind it, which leaves half an ulp,
 // the quotient's own rounding: a decay's error enters once a step, and with the
 // bare reciprocal the gradient of h0 over 1000 steps was off by 3.2e-7 instead
@@ -188,22 +188,54 @@ __device__ __forceinline__ Normal normal_of(float z) {
   return r;
 }
 
-// act(z) and act'(z).
-template <int ACT>
+// exp(v) for |v| <= 87 to an ulp and a half: the hardware's exp2 of the rounded
+// v log2(e), made good for what that rounding left off. (16000 tokens of
+// 5000 channels FP32 with SiLU: 138 us forward, 144 with the library's expf.)
+__device__ __forceinline__ float exp_near(float v) {
+  constexpr float kLog2e = 1.44269502162933349609375f, kRest = 1.92596298909109e-8f;  // their sum is log2(e)
+  const float w = kLog2e * v, off = fmaf(kRest, v, fmaf(kLog2e, v, -w));
+  const float e = __builtin_amdgcn_exp2f(w);
+  return fmaf(e, 0.693147180559945309f * off, e);
+}
+
+// The logistic function of z and its complement. 16-bit elements take the
+// hardware's exp2 of the once rounded argument, |z| 2^-24 off relative. For FP32
+// ones e = exp(-z) is right to 3 2^-24, and p = 1 / (1 + e), e p to a few: no
+// cancellation, and no error that grows with |z|. (Beyond |z| = 87, where FP32
+// ends, p stays what it is there: 1, or 1.6e-38.)
+struct Logistic {
+  float p, rest;
+};
+template <typename T>
+__device__ __forceinline__ Logistic logistic(float z) {
+  Logistic r;
+  if constexpr (sizeof(T) == 4) {
+    const float e = exp_near(-__builtin_amdgcn_fmed3f(z, -87.0f, 87.0f));
+    r.p = inverse_of<T>(1.0f + e);
+    r.rest = e * r.p;
+  } else {
+    r.p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+    r.rest = 1.0f - r.p;
+  }
+  return r;
+}
+
+// act(z) and act'(z), z of elements of type T.
+template <typename T, int ACT>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == FFTMV_ACT_SILU) {
-    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
+    return z * logistic<T>(z).p;
   } else if constexpr (ACT == FFTMV_ACT_GELU) {
     return z * normal_of(z).phi;
   } else {
     return z;
   }
 }
-template <int ACT>
+template <typename T, int ACT>
 __device__ __forceinline__ float activate_slope(float z) {
   if constexpr (ACT == FFTMV_ACT_SILU) {
-    const float p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
-    return p * (1.0f + z * (1.0f - p));
+    const Logistic l = logistic<T>(z);
+    return l.p * (1.0f + z * l.rest);
   } else if constexpr (ACT == FFTMV_ACT_GELU) {
     const Normal n = normal_of(z);
     return fmaf(0.39894228040143268f * z, n.bell, n.phi);

@@ -187,3 +187,36 @@ def test_fp32_decays_are_rounded_once_an_operation(fm):
                          (step_rest, 1, "step's 1 - a")):
         got = got.flatten().cpu().numpy()
         assert np.any([got == m[k] for m in may], axis=0).all(), what
+
+
+def _values_and_slopes(fm, activation, z):
+    """act(z) and act'(z) by themselves: groups of (1, -1) have mean 0 and
+    deviation 1, a weight of zero leaves z to the bias."""
+    C = z.size
+    x = torch.tensor([1.0, -1.0], device="cuda").repeat(C // 2).view(1, C)
+    b, w = torch.from_numpy(z).cuda(), torch.zeros(C, device="cuda")
+    y, stats = fm.group_norm(x, C // 2, w, b, eps=0.0, activation=activation, save=True)
+    assert torch.equal(stats, torch.tensor([0.0, 1.0], device="cuda").expand_as(stats))
+    _, _, db = fm.group_norm_backward(torch.ones_like(x), x, stats, C // 2, w, b, activation=activation)
+    return host(y)[0], host(db)
+
+
+def _points(far):
+    rng = np.random.default_rng(44)
+    z = np.concatenate([rng.standard_normal(8000), rng.uniform(-far, far, 8000), [0.0, -0.0, 1e-30, -1e-30]])
+    return z.astype(np.float32)
+
+
+def test_fp32_silu_to_a_few_roundings(fm):
+    """With e = exp(-z) (3 U: an ulp and a rounding), 1 + e (U, and e's share of
+    its error), the quotient (U) the sigmoid p is off by 5 U, y by 6 U. q = 1 - p =
+    e p: 3 U of e, of which 1 + e takes back what it grows by, and three
+    roundings, 6 U. The slope p (1 + z q): 12 U of p |z| q and 7 U of itself."""
+    z = _points(80.0)
+    y, s = _values_and_slopes(fm, "silu", z)
+    v = z.astype(np.float64)
+    p, q = 1.0 / (1.0 + np.exp(-v)), 1.0 / (1.0 + np.exp(v))
+    want, slope = v * p, p * (1.0 + v * q)
+    assert (np.abs(y - want) <= 6 * R.U * np.abs(want)).all(), np.nanmax(np.abs(y - want) / np.abs(want)) / R.U
+    bound = R.U * (12 * p * np.abs(v) * q + 7 * np.abs(slope))
+    assert (np.abs(s - slope) <= bound).all(), (np.abs(s - slope) / bound).max()
