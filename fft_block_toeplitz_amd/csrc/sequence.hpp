@@ -200,9 +200,9 @@ __device__ __forceinline__ float exp_near(float v) {
 
 // The logistic function of z and its complement. 16-bit elements take the
 // hardware's exp2 of the once rounded argument, |z| 2^-24 off relative. For FP32
-// ones e = exp(-z) is right to 3 2^-24, and p = 1 / (1 + e), e p to a few: no
-// cancellation, and no error that grows with |z|. (Beyond |z| = 87, where FP32
-// ends, p stays what it is there: 1, or 1.6e-38.)
+// ones e = exp(-z) is right to 3 2^-24, and p = 1 / (1 + e) to 5, whatever z. The
+// complement is 1 - p, exact as far as p is, or, where that cancels, e p. (Beyond
+// |z| = 87, where FP32 ends, p stays what it is there: 1, or 1.6e-38.)
 struct Logistic {
   float p, rest;
 };
@@ -212,7 +212,7 @@ __device__ __forceinline__ Logistic logistic(float z) {
   if constexpr (sizeof(T) == 4) {
     const float e = exp_near(-__builtin_amdgcn_fmed3f(z, -87.0f, 87.0f));
     r.p = inverse_of<T>(1.0f + e);
-    r.rest = e * r.p;
+    r.rest = z > 2.0f ? e * r.p : 1.0f - r.p;
   } else {
     r.p = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * z));
     r.rest = 1.0f - r.p;
@@ -235,7 +235,7 @@ template <typename T, int ACT>
 __device__ __forceinline__ float activate_slope(float z) {
   if constexpr (ACT == FFTMV_ACT_SILU) {
     const Logistic l = logistic<T>(z);
-    return l.p * (1.0f + z * l.rest);
+    return fmaf(l.p * z, l.rest, l.p);
   } else if constexpr (ACT == FFTMV_ACT_GELU) {
     const Normal n = normal_of(z);
     return fmaf(0.39894228040143268f * z, n.bell, n.phi);

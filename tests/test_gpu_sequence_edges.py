@@ -209,9 +209,12 @@ def _points(far):
 
 def test_fp32_silu_to_a_few_roundings(fm):
     """With e = exp(-z) (3 U: an ulp and a rounding), 1 + e (U, and e's share of
-    its error), the quotient (U) the sigmoid p is off by 5 U, y by 6 U. q = 1 - p =
-    e p: 3 U of e, of which 1 + e takes back what it grows by, and three
-    roundings, 6 U. The slope p (1 + z q): 12 U of p |z| q and 7 U of itself."""
+    its error), the quotient (U) the sigmoid p is off by 5 U, y by 6 U. The slope
+    is p + (p z) q: where z > 2 q = e p is off by its factors' 8 U and a rounding,
+    of which 1 + e takes back what it grows by, else q = 1 - p by p's error, which
+    so enters the slope by its derivative 1 + z (1 - 2 p) alone, under 1 for z > -1
+    and under |z| below. Products and sum 3 U: together 12 U of p |z| q and 7 U of
+    the slope."""
     z = _points(80.0)
     y, s = _values_and_slopes(fm, "silu", z)
     v = z.astype(np.float64)
