@@ -162,33 +162,7 @@ __device__ __forceinline__ float drive_of(const Terms &t, float x) {
 }
 
 // ------------------------------------------------------------- activations
-// Phi(z), the normal distribution's integral, and exp(-z^2 / 2) beside it:
-//   Phi(-|z|) = erfc(x) / 2, x = |z| / sqrt(2), erfc(x) = exp(-x^2) R(1 / (1 + 0.33 x)),
-// R a polynomial without constant term fitted to exp(x^2) erfc(x) on [0, 10]
-// (relative error 9e-8; 5e-7 in FP32 arithmetic). The library's erfc costs
-// three times as much: a GELU forward of 32768 x 320 fp16 was bound by it.
-struct Normal {
-  float phi, bell;
-};
-__device__ __forceinline__ Normal normal_of(float z) {
-  Normal r;
-  const float x = 0.70710678118654752f * fabsf(z);
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.33f, x, 1.0f));
-  r.bell = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
-  float p = -0.13534443080425262f;
-  p = fmaf(p, t, 0.46023201942443848f);
-  p = fmaf(p, t, -0.35114115476608276f);
-  p = fmaf(p, t, 0.40849229693412781f);
-  p = fmaf(p, t, 0.047224629670381546f);
-  p = fmaf(p, t, 0.20122270286083221f);
-  p = fmaf(p, t, 0.18295612931251526f);
-  p = fmaf(p, t, 0.18635779619216919f);
-  const float half = 0.5f * r.bell * p * t;
-  r.phi = z < 0.0f ? half : 1.0f - half;
-  return r;
-}
-
-// exp(v) for |v| <= 87 to an ulp and a half: the hardware's exp2 of the rounded
+// exp(v), -128 <= v <= 87, to an ulp and a half (0 below -87): the hardware's exp2 of the rounded
 // v log2(e), made good for what that rounding left off. (16000 tokens of
 // 5000 channels FP32 with SiLU: 138 us forward, 144 with the library's expf.)
 __device__ __forceinline__ float exp_near(float v) {
@@ -196,6 +170,54 @@ __device__ __forceinline__ float exp_near(float v) {
   const float w = kLog2e * v, off = fmaf(kRest, v, fmaf(kLog2e, v, -w));
   const float e = __builtin_amdgcn_exp2f(w);
   return fmaf(e, 0.693147180559945309f * off, e);
+}
+
+// Phi(z), the normal distribution's integral, and exp(-z^2 / 2) beside it:
+//   Phi(-|z|) = erfc(x) / 2,  x = |z| / sqrt(2),  erfc(x) = exp(-x^2) t R(t),  t = 1 / (1 + k x),
+// R a polynomial fitted to exp(x^2) erfc(x) / t with the least relative error.
+// 16-bit elements: k = 0.33, x in [0, 10], 1.2e-7; in FP32 arithmetic 6e-7 up to
+// |z| = 3, and beyond it -z^2 / 2, rounded before exp2, makes that grow as z^2, to
+// 8e-6 at 12.5, all far below their type's rounding. (The library's erfc costs
+// three times as much: a GELU forward of 32768 x 320 fp16 was bound by it.)
+// FP32 elements: up to |z| = 1 Phi = 1/2 + z P(z^2), 5.3e-8, which loses nothing
+// to 1 - Phi(-|z|); from there k = 0.4, 1.3e-7, with the rounding of z^2 made good
+// in the exponential. (2 x 16384 x 320: 43 us forward, 61 backward; with the library's
+// erfc 48 and 71; by the 16-bit elements' way 41 and 58, dx 1.05e-7 off, not 8.3e-8.)
+constexpr float kTail16[] = {0.18635779619216919f,  0.18295612931251526f, 0.20122270286083221f,  0.047224629670381546f,
+                             0.40849229693412781f, -0.35114115476608276f, 0.46023201942443848f, -0.13534443080425262f};
+constexpr float kTail32[] = {0.2256411910057068f,   0.22646473348140717f, 0.2002403885126114f,  0.2082897424697876f,
+                             0.01665278896689415f, 0.23601338267326355f, -0.11349567770957947f};
+constexpr float kCentre32[] = {0.3989422619342804f, -0.06648958474397659f, 0.009967196732759476f,
+                               -0.001169353723526001f, 9.423524170415476e-05f};
+template <int N>
+__device__ __forceinline__ float polynomial(const float (&c)[N], float t) {
+  float p = c[N - 1];
+#pragma unroll
+  for (int i = N - 2; i >= 0; --i) p = fmaf(p, t, c[i]);
+  return p;
+}
+
+struct Normal {
+  float phi, bell;
+};
+template <typename T>
+__device__ __forceinline__ Normal normal_of(float z) {
+  Normal r;
+  if constexpr (sizeof(T) == 4) {
+    const float a = fminf(fabsf(z), 16.0f);  // Phi has reached its ends before
+    const float w = a * a, e = exp_near(-0.5f * w);
+    r.bell = fmaf(e, -0.5f * fmaf(a, a, -w), e);
+    const float t = inverse_of<T>(fmaf(0.28284271247461901f, a, 1.0f));
+    const float half = 0.5f * r.bell * (polynomial(kTail32, t) * t);
+    r.phi = a < 1.0f ? fmaf(z, polynomial(kCentre32, w), 0.5f) : z < 0.0f ? half : 1.0f - half;
+  } else {
+    const float x = 0.70710678118654752f * fabsf(z);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.33f, x, 1.0f));
+    r.bell = __builtin_amdgcn_exp2f(-0.72134752044448170f * z * z);
+    const float half = 0.5f * r.bell * polynomial(kTail16, t) * t;
+    r.phi = z < 0.0f ? half : 1.0f - half;
+  }
+  return r;
 }
 
 // The logistic function of z and its complement. 16-bit elements take the
@@ -226,7 +248,7 @@ __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == FFTMV_ACT_SILU) {
     return z * logistic<T>(z).p;
   } else if constexpr (ACT == FFTMV_ACT_GELU) {
-    return z * normal_of(z).phi;
+    return z * normal_of<T>(z).phi;
   } else {
     return z;
   }
@@ -237,7 +259,7 @@ __device__ __forceinline__ float activate_slope(float z) {
     const Logistic l = logistic<T>(z);
     return fmaf(l.p * z, l.rest, l.p);
   } else if constexpr (ACT == FFTMV_ACT_GELU) {
-    const Normal n = normal_of(z);
+    const Normal n = normal_of<T>(z);
     return fmaf(0.39894228040143268f * z, n.bell, n.phi);
   } else {
     return 1.0f;

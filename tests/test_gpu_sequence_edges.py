@@ -1,4 +1,5 @@
 """The sequence operators at the edges of what their entry points accept."""
+import math
 import threading
 
 import numpy as np
@@ -223,3 +224,20 @@ def test_fp32_silu_to_a_few_roundings(fm):
     assert (np.abs(y - want) <= 6 * R.U * np.abs(want)).all(), np.nanmax(np.abs(y - want) / np.abs(want)) / R.U
     bound = R.U * (12 * p * np.abs(v) * q + 7 * np.abs(slope))
     assert (np.abs(s - slope) <= bound).all(), (np.abs(s - slope) / bound).max()
+
+
+def test_fp32_gelu_to_a_few_roundings(fm):
+    """Phi = exp(-z^2/2) t R(t) / 2: the exponential 3 U, its exponent's remainder
+    and what takes it in 2 U; t from its argument and the quotient 2 U, by which t
+    R(t) changes 2.4 times as much; R's fit 2 U, coefficients and sums 3 U; three
+    products: 17 U of Phi. Near zero 1/2 + z P less than that. y = z Phi: 18 U. The
+    slope Phi + z phi(z): 17 U of Phi, and of the second term the bell's 5 U,
+    constant and products 3 U, the sum's rounding of either U."""
+    z = _points(12.0)
+    y, s = _values_and_slopes(fm, "gelu", z)
+    v = z.astype(np.float64)
+    phi = 0.5 * np.vectorize(math.erfc)(-v / math.sqrt(2.0))
+    second = v * np.exp(-0.5 * v * v) / math.sqrt(2.0 * math.pi)
+    assert (np.abs(y - v * phi) <= 18 * R.U * np.abs(v * phi)).all(), np.nanmax(np.abs(y / (v * phi) - 1)) / R.U
+    bound = R.U * (18 * phi + 9 * np.abs(second))
+    assert (np.abs(s - phi - second) <= bound).all(), (np.abs(s - phi - second) / bound).max()
