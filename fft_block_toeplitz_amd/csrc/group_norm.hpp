@@ -15,7 +15,8 @@
 // Variances are sums of squared deviations from the mean: deviations of
 // registers from the sample's mean (resident), or per tile from the tile's own
 // mean, joined by the pairwise formula (split); no difference of large sums.
-// Every sum runs in a fixed order.
+// Every sum runs in a fixed order, and at most kInTurn terms or so one after the
+// other: longer ones in blocks whose sums are added up in turn.
 #pragma once
 
 #include <algorithm>
@@ -29,6 +30,7 @@ namespace fftmv {
 constexpr int kNormThreads = 1024;  // at most
 // of a resident workgroup that holds several rows a thread (256 registers each)
 constexpr int kHeldThreads = 512;
+constexpr int kInTurn = 32;
 template <int Q, int P>
 constexpr int kResidentThreads = Q * P > 1 ? kHeldThreads : kNormThreads;
 
@@ -281,11 +283,12 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
 }
 
 // Sums of dz and dz xhat over the rows of all samples of this workgroup: row
-// `first` of the workspace, or the results themselves where there is one.
+// `first` of the workspace, or the results themselves where there is one; `more`:
+// added to what an earlier call left there.
 template <int VEC>
 __device__ __forceinline__ void put_param_sums(const fftmv_group_norm_t &g, const NormShape &s,
                                                const SlabLane<VEC> &l, float *lds, int first, bool alone,
-                                               const float (&db)[VEC], const float (&dw)[VEC]) {
+                                               const float (&db)[VEC], const float (&dw)[VEC], bool more = false) {
   const int lw = s.lx * VEC;
   const int64_t C = static_cast<int64_t>(s.G) * s.D;
   float2 *to = static_cast<float2 *>(g.workspace) + first * C + l.ch0;
@@ -302,12 +305,10 @@ __device__ __forceinline__ void put_param_sums(const fftmv_group_norm_t &g, cons
         for (int t = t0; t < rows && t < t0 + 16; ++t) some += lds[t * lw + c];
         sum += some;
       }
-      if (!alone) {
-        (k ? to[c].y : to[c].x) = sum;
-      } else {
-        float *out = k ? g.dweight : g.dbias;
-        if (out) out[l.ch0 + c] = sum;
-      }
+      float *out = k ? g.dweight : g.dbias;
+      if (!alone) out = k ? &to[c].y : &to[c].x;
+      else if (out) out += l.ch0 + c;
+      if (out) *out = more ? *out + sum : sum;
     }
   }
 }
@@ -321,112 +322,121 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_backward_kernel
   const SlabLane<VEC> l(s, slab);
   const GroupOf<VEC, WHOLE> group(l.c, s.D);
   float w[VEC], b[VEC], db[VEC], dw[VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) db[e] = dw[e] = 0.0f;
   load_params(g.weight, l.ch0 + l.c, 1.0f, w);
   load_params(g.bias, l.ch0 + l.c, 0.0f, b);
+  constexpr int kTurns = 3 * kInTurn;  // under the hundred roundings that the sums are held to
   const int64_t step = static_cast<int64_t>(gridDim.x / s.slabs) * (Q * s.sub);
-  for (int64_t n0 = static_cast<int64_t>(first) * (Q * s.sub); n0 < s.N; n0 += step) {
-    Vec<T, VEC> v[Q][P], d[Q][P];
-    int held[Q];
-    held_of<VEC, Q>(g, s, l, n0, held);
+  const bool alone = gridDim.x == static_cast<unsigned>(s.slabs);
+  int64_t n0 = static_cast<int64_t>(first) * (Q * s.sub);
+  bool more = false;
+  do {  // kTurns samples of each thread, whose sums go out in front of the next
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int64_t n = l.sample(s, n0, q);
-      const T *x = static_cast<const T *>(g.x) + n * g.x_sample + l.ch0 + l.c;
-      const T *dy = static_cast<const T *>(g.dy) + n * g.dy_sample + l.ch0 + l.c;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        v[q][p] = load_held<T, VEC>(x, l.row + p * s.ty, held[q], g.x_row);
-        d[q][p] = load_held<T, VEC>(dy, l.row + p * s.ty, held[q], g.dy_row);
-      }
-    }
-    for (int i = threadIdx.x; i < Q * s.sub * l.ng; i += blockDim.x) {
-      const int64_t n = n0 + i / l.ng;
-      if (n < s.N) {
-        const float *from = g.stats + 2 * (n * s.G + static_cast<int64_t>(slab) * s.gs + i % l.ng);
-        stat[2 * i] = from[0];
-        stat[2 * i + 1] = from[1];
-      } else {
-        stat[2 * i] = stat[2 * i + 1] = 0.0f;
-      }
-    }
-    __syncthreads();
-    // dz and xhat of one element; where no row is held, dy and dz are 0. In FP32
-    // dz takes dy's place, so that no slope is evaluated again behind the sums
-    // (16000 x 5000 tokens with SiLU 199 us, evaluated twice 220); the place of a
-    // 16-bit element cannot hold it
-    constexpr bool kKeep = sizeof(T) == 4;
-    auto terms = [&](int q, int p, int e, bool kept, float &xh, float &dz) {
-      const int k = 2 * ((q * s.sub + l.sub) * l.ng + group[e]);
-      xh = (v[q][p][e] - stat[k]) * stat[k + 1];
-      dz = d[q][p][e];
-      if (!kept) dz *= activate_slope<T, ACT>(fmaf(xh, w[e], b[e]));
-    };
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      float t1[VEC], t2[VEC];
-      if (l.in) {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          float sb = 0.0f, sw = 0.0f;
-#pragma unroll
-          for (int p = 0; p < P; ++p) {
-            float xh, dz;
-            terms(q, p, e, false, xh, dz);
-            if constexpr (kKeep) d[q][p].v[e] = dz;
-            sb += dz;
-            sw = fmaf(dz, xh, sw);
-          }
-          db[e] += sb;
-          dw[e] += sw;
-          t1[e] = sb * w[e];
-          t2[e] = sw * w[e];
-        }
-      }
-      put_part<VEC, WHOLE>(part + q * slots, s, l, t1);
-      put_part<VEC, WHOLE>(part + (Q + q) * slots, s, l, t2);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      forget(v[q]);
-      forget(d[q]);
-    }
-    team_sums<VEC, WHOLE>(part, s, l.ng, 2 * Q * s.sub, [&](int pair, float sum) {
-      const int64_t n = n0 + pair / l.ng % (Q * s.sub);
-      const int h = n < s.N ? held_rows(g, n) : 0;
-      m[pair] = h ? sum / (static_cast<float>(h) * s.D) : 0.0f;
-    });
-    __syncthreads();
-    if (l.in) {
+    for (int e = 0; e < VEC; ++e) db[e] = dw[e] = 0.0f;
+    const int64_t end = s.N - n0 > kTurns / Q * step ? n0 + kTurns / Q * step : s.N;
+    for (; n0 < end; n0 += step) {
+      Vec<T, VEC> v[Q][P], d[Q][P];
+      int held[Q];
+      held_of<VEC, Q>(g, s, l, n0, held);
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        const int64_t n = n0 + q * s.sub + l.sub;
-        if (n >= s.N) break;
-        T *dx = static_cast<T *>(g.dx) + n * g.dx_sample + l.ch0 + l.c;
+        const int64_t n = l.sample(s, n0, q);
+        const T *x = static_cast<const T *>(g.x) + n * g.x_sample + l.ch0 + l.c;
+        const T *dy = static_cast<const T *>(g.dy) + n * g.dy_sample + l.ch0 + l.c;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-          const int row = l.row + p * s.ty;
-          if (row >= s.S) break;
-          float o[VEC] = {};
-          if (row < held[q]) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              float xh, dz;
-              terms(q, p, e, kKeep, xh, dz);
-              const int k = (q * s.sub + l.sub) * l.ng + group[e];
-              o[e] = stat[2 * k + 1] * (fmaf(dz, w[e], -m[k]) - xh * m[Q * s.sub * l.ng + k]);
-            }
-          }
-          store_vec<T, VEC>(dx + static_cast<int64_t>(row) * g.dx_row, o);
-          row_done();
+          v[q][p] = load_held<T, VEC>(x, l.row + p * s.ty, held[q], g.x_row);
+          d[q][p] = load_held<T, VEC>(dy, l.row + p * s.ty, held[q], g.dy_row);
         }
       }
+      for (int i = threadIdx.x; i < Q * s.sub * l.ng; i += blockDim.x) {
+        const int64_t n = n0 + i / l.ng;
+        if (n < s.N) {
+          const float *from = g.stats + 2 * (n * s.G + static_cast<int64_t>(slab) * s.gs + i % l.ng);
+          stat[2 * i] = from[0];
+          stat[2 * i + 1] = from[1];
+        } else {
+          stat[2 * i] = stat[2 * i + 1] = 0.0f;
+        }
+      }
+      __syncthreads();
+      // dz and xhat of one element; where no row is held, dy and dz are 0. In FP32
+      // dz takes dy's place, so that no slope is evaluated again behind the sums
+      // (16000 x 5000 tokens with SiLU 199 us, evaluated twice 220); the place of a
+      // 16-bit element cannot hold it
+      constexpr bool kKeep = sizeof(T) == 4;
+      auto terms = [&](int q, int p, int e, bool kept, float &xh, float &dz) {
+        const int k = 2 * ((q * s.sub + l.sub) * l.ng + group[e]);
+        xh = (v[q][p][e] - stat[k]) * stat[k + 1];
+        dz = d[q][p][e];
+        if (!kept) dz *= activate_slope<T, ACT>(fmaf(xh, w[e], b[e]));
+      };
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        float t1[VEC], t2[VEC];
+        if (l.in) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            float sb = 0.0f, sw = 0.0f;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              float xh, dz;
+              terms(q, p, e, false, xh, dz);
+              if constexpr (kKeep) d[q][p].v[e] = dz;
+              sb += dz;
+              sw = fmaf(dz, xh, sw);
+            }
+            db[e] += sb;
+            dw[e] += sw;
+            t1[e] = sb * w[e];
+            t2[e] = sw * w[e];
+          }
+        }
+        put_part<VEC, WHOLE>(part + q * slots, s, l, t1);
+        put_part<VEC, WHOLE>(part + (Q + q) * slots, s, l, t2);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        forget(v[q]);
+        forget(d[q]);
+      }
+      team_sums<VEC, WHOLE>(part, s, l.ng, 2 * Q * s.sub, [&](int pair, float sum) {
+        const int64_t n = n0 + pair / l.ng % (Q * s.sub);
+        const int h = n < s.N ? held_rows(g, n) : 0;
+        m[pair] = h ? sum / (static_cast<float>(h) * s.D) : 0.0f;
+      });
+      __syncthreads();
+      if (l.in) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          const int64_t n = n0 + q * s.sub + l.sub;
+          if (n >= s.N) break;
+          T *dx = static_cast<T *>(g.dx) + n * g.dx_sample + l.ch0 + l.c;
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            const int row = l.row + p * s.ty;
+            if (row >= s.S) break;
+            float o[VEC] = {};
+            if (row < held[q]) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                float xh, dz;
+                terms(q, p, e, kKeep, xh, dz);
+                const int k = (q * s.sub + l.sub) * l.ng + group[e];
+                o[e] = stat[2 * k + 1] * (fmaf(dz, w[e], -m[k]) - xh * m[Q * s.sub * l.ng + k]);
+              }
+            }
+            store_vec<T, VEC>(dx + static_cast<int64_t>(row) * g.dx_row, o);
+            row_done();
+          }
+        }
+      }
+      __syncthreads();  // stat is written again
     }
-    __syncthreads();  // stat is written again
-  }
-  put_param_sums<VEC>(g, s, l, lds, first, gridDim.x == static_cast<unsigned>(s.slabs), db, dw);
+    put_param_sums<VEC>(g, s, l, lds, first, alone, db, dw, more);
+    __syncthreads();
+    more = true;
+  } while (n0 < s.N);
 }
 
 // --------------------------------------------------------------- split
@@ -457,17 +467,30 @@ __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_n
   const SlabLane<VEC> l(s, r.slab);
   const GroupOf<VEC, false> group(l.c, s.D);
   const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
-  float mu[VEC], m2[VEC], count = 0.0f;
+  float mu[VEC], m2[VEC], count = 0.0f, bmu[VEC], bm2[VEC], bcount = 0.0f;  // of all tiles, of a block of them
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) mu[e] = m2[e] = 0.0f;
+  for (int e = 0; e < VEC; ++e) mu[e] = m2[e] = bmu[e] = bm2[e] = 0.0f;
+  auto take_block = [&] {
+    const float all = count + bcount, share = all > 0.0f ? bcount / all : 0.0f, weight = count * share;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float d = bmu[e] - mu[e];
+      mu[e] = fmaf(d, share, mu[e]);
+      m2[e] += fmaf(d * d, weight, bm2[e]);
+      bmu[e] = bm2[e] = 0.0f;
+    }
+    count = all;
+    bcount = 0.0f;
+  };
   if (l.in) {
+    int turn = 0;
     for (int t = r.from + l.row; t < r.to; t += kTile * s.ty) {
       Vec<T, VEC> v[kTile];
       int rows = (r.to - t + s.ty - 1) / s.ty;
       rows = rows < kTile ? rows : kTile;
 #pragma unroll
       for (int p = 0; p < kTile; ++p) v[p] = load_held<T, VEC>(x, t + p * s.ty, r.to, g.x_row);
-      const float k = static_cast<float>(rows), all = count + k, share = k / all, weight = count * share;
+      const float k = static_cast<float>(rows), all = bcount + k, share = k / all, weight = bcount * share;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         float sum = 0.0f, sq = 0.0f;
@@ -479,12 +502,17 @@ __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_n
           const float d = p < rows ? v[p][e] - m : 0.0f;
           sq = fmaf(d, d, sq);
         }
-        const float d = m - mu[e];
-        mu[e] = fmaf(d, share, mu[e]);
-        m2[e] += fmaf(d * d, weight, sq);
+        const float d = m - bmu[e];
+        bmu[e] = fmaf(d, share, bmu[e]);
+        bm2[e] += fmaf(d * d, weight, sq);
       }
-      count = all;
+      bcount = all;
+      if (++turn == kInTurn) {
+        take_block();
+        turn = 0;
+      }
     }
+    take_block();
   }
   const int rows = r.to - r.from;
   float v[VEC];
@@ -522,29 +550,33 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
   const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
   for (int k = threadIdx.x / s.team; k < l.ng; k += teams) {
     float count = 0.0f, mu = 0.0f, sq = 0.0f;
-    auto join = [&](float n, float m, float q) {
+    auto join = [](float &count, float &mu, float &sq, float n, float m, float q) {
       const float all = count + n, share = all > 0.0f ? n / all : 0.0f, d = m - mu;
       sq += q + d * d * count * share;
       mu = fmaf(d, share, mu);
       count = all;
     };
-    for (int i0 = me; i0 < s.across; i0 += 4 * s.team) {
-      float2 v[4];
+    for (int b0 = me; b0 < s.across; b0 += kInTurn * s.team) {
+      float bcount = 0.0f, bmu = 0.0f, bsq = 0.0f;  // of a block of ranges
+      for (int i0 = b0; i0 < s.across && i0 < b0 + kInTurn * s.team; i0 += 4 * s.team) {
+        float2 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * s.team;
-        v[j] = from[static_cast<int64_t>(i < s.across ? i : 0) * s.G + k];
-      }
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + j * s.team;
+          v[j] = from[static_cast<int64_t>(i < s.across ? i : 0) * s.G + k];
+        }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int rows = held - (i0 + j * s.team) * s.range;
-        if (i0 + j * s.team < s.across && rows > 0)
-          join(static_cast<float>(rows < s.range ? rows : s.range) * s.D, v[j].x, v[j].y);
+        for (int j = 0; j < 4; ++j) {
+          const int rows = held - (i0 + j * s.team) * s.range;
+          if (i0 + j * s.team < s.across && rows > 0)
+            join(bcount, bmu, bsq, static_cast<float>(rows < s.range ? rows : s.range) * s.D, v[j].x, v[j].y);
+        }
       }
+      join(count, mu, sq, bcount, bmu, bsq);
     }
     for (int m = 1; m < s.team; m <<= 1) {
       const float n = __shfl_xor(count, m), mm = __shfl_xor(mu, m), qq = __shfl_xor(sq, m);
-      join(n, mm, qq);  // lane 0's order is the one that counts
+      join(count, mu, sq, n, mm, qq);  // lane 0's order is the one that counts
     }
     if (me == 0) {
       mean[k] = mu;
@@ -608,6 +640,10 @@ __global__ __launch_bounds__(kNormThreads) void norm_sums_kernel(fftmv_group_nor
     }
     const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
     const T *dy = static_cast<const T *>(g.dy) + r.n * g.dy_sample + l.ch0 + l.c;
+    float pb[VEC], pw[VEC];  // of a block of tiles
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) pb[e] = pw[e] = 0.0f;
+    int turn = 0;
     for (int t = r.from + l.row; t < r.to; t += 4 * s.ty) {
       Vec<T, VEC> v[4], d[4];
 #pragma unroll
@@ -624,9 +660,23 @@ __global__ __launch_bounds__(kNormThreads) void norm_sums_kernel(fftmv_group_nor
           sb += dz;
           sw = fmaf(dz, xh, sw);
         }
-        db[e] += sb;
-        dw[e] += sw;
+        pb[e] += sb;
+        pw[e] += sw;
       }
+      if (++turn == kInTurn) {
+        turn = 0;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          db[e] += pb[e];
+          dw[e] += pw[e];
+          pb[e] = pw[e] = 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      db[e] += pb[e];
+      dw[e] += pw[e];
     }
   }
   const int64_t row = r.n * s.across + r.part, C = static_cast<int64_t>(s.G) * s.D;
@@ -653,17 +703,22 @@ __device__ __forceinline__ void param_sums(const fftmv_group_norm_t &g, int64_t 
   const float2 *from = static_cast<const float2 *>(g.workspace);
   float sb = 0.0f, sw = 0.0f;
   if (ch < g.channels)
-    for (int64_t i0 = part; i0 < rows; i0 += 16 * parts) {
-      float b = 0.0f, w = 0.0f;
+    for (int64_t b0 = part; b0 < rows; b0 += kInTurn * 16 * parts) {
+      float tb = 0.0f, tw = 0.0f;
+      for (int64_t i0 = b0; i0 < rows && i0 < b0 + kInTurn * 16 * parts; i0 += 16 * parts) {
+        float b = 0.0f, w = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int64_t i = i0 + k * parts;
-        const float2 v = from[(i < rows ? i : i0) * g.channels + ch];
-        b += i < rows ? v.x : 0.0f;
-        w += i < rows ? v.y : 0.0f;
+        for (int k = 0; k < 16; ++k) {
+          const int64_t i = i0 + k * parts;
+          const float2 v = from[(i < rows ? i : i0) * g.channels + ch];
+          b += i < rows ? v.x : 0.0f;
+          w += i < rows ? v.y : 0.0f;
+        }
+        tb += b;
+        tw += w;
       }
-      sb += b;
-      sw += w;
+      sb += tb;
+      sw += tw;
     }
   lds[threadIdx.x] = sb;
   lds[blockDim.x + threadIdx.x] = sw;
@@ -698,16 +753,21 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_nor
   const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
   for (int k = threadIdx.x / s.team; k < l.ng; k += teams) {
     float a = 0.0f, b = 0.0f;
-    for (int i0 = me; i0 < s.across; i0 += 4 * s.team) {
-      float2 v[4];
+    for (int b0 = me; b0 < s.across; b0 += kInTurn * s.team) {
+      float pa = 0.0f, pb = 0.0f;
+      for (int i0 = b0; i0 < s.across && i0 < b0 + kInTurn * s.team; i0 += 4 * s.team) {
+        float2 v[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * s.team;
-        v[j] = from[static_cast<int64_t>(i < s.across ? i : 0) * s.G + k];
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + j * s.team;
+          v[j] = from[static_cast<int64_t>(i < s.across ? i : 0) * s.G + k];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i0 + j * s.team < s.across) pa += v[j].x, pb += v[j].y;
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (i0 + j * s.team < s.across) a += v[j].x, b += v[j].y;
+      a += pa;
+      b += pb;
     }
     for (int m = s.team / 2; m > 0; m >>= 1) {
       a += __shfl_xor(a, m);
@@ -776,6 +836,31 @@ __device__ __forceinline__ float block_sum(float v) {
   return s;
 }
 
+// The sum of f(t, c) over a sample's held rows and this thread's channels, in
+// blocks of kInTurn channels and rows.
+template <typename F>
+__device__ __forceinline__ float wide_sum(int held, int64_t D, F f) {
+  float sum = 0.0f;
+  for (int t0 = 0; t0 < held; t0 += kInTurn * kInTurn) {
+    float far = 0.0f;
+    for (int t1 = t0; t1 < held && t1 < t0 + kInTurn * kInTurn; t1 += kInTurn) {
+      float near = 0.0f;
+      for (int t = t1; t < held && t < t1 + kInTurn; ++t) {
+        float row = 0.0f;
+        for (int64_t c0 = threadIdx.x; c0 < D; c0 += kInTurn * kBlock) {
+          float part = 0.0f;
+          for (int64_t c = c0; c < D && c < c0 + kInTurn * kBlock; c += kBlock) part += f(t, c);
+          row += part;
+        }
+        near += row;
+      }
+      far += near;
+    }
+    sum += far;
+  }
+  return sum;
+}
+
 template <typename T, int ACT>
 __global__ __launch_bounds__(kBlock) void norm_wide_forward_kernel(fftmv_group_norm_t g) {
   const int64_t n = blockIdx.x / g.groups, q = blockIdx.x % g.groups, D = g.channels / g.groups;
@@ -783,23 +868,13 @@ __global__ __launch_bounds__(kBlock) void norm_wide_forward_kernel(fftmv_group_n
   const float count = static_cast<float>(held) * D;
   const T *x = static_cast<const T *>(g.x) + n * g.x_sample + q * D;
   T *y = static_cast<T *>(g.y) + n * g.y_sample + q * D;
-  float sum = 0.0f;
-  for (int t = 0; t < held; ++t) {
-    float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < D; c += kBlock) s += static_cast<float>(x[t * g.x_row + c]);
-    sum += s;
-  }
-  const float mean = block_sum(sum) / fmaxf(count, 1.0f);
-  sum = 0.0f;
-  for (int t = 0; t < held; ++t) {
-    float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < D; c += kBlock) {
-      const float d = static_cast<float>(x[t * g.x_row + c]) - mean;
-      s = fmaf(d, d, s);
-    }
-    sum += s;
-  }
-  sum = block_sum(sum);
+  const float mean =
+      block_sum(wide_sum(held, D, [&](int t, int64_t c) { return static_cast<float>(x[t * g.x_row + c]); })) /
+      fmaxf(count, 1.0f);
+  const float sum = block_sum(wide_sum(held, D, [&](int t, int64_t c) {
+    const float d = static_cast<float>(x[t * g.x_row + c]) - mean;
+    return d * d;
+  }));
   const float rstd = held ? 1.0f / sqrtf(sum / count + g.eps) : 0.0f;
   if (g.stats && threadIdx.x == 0) {
     g.stats[2 * static_cast<int64_t>(blockIdx.x)] = mean;
@@ -829,25 +904,39 @@ __global__ __launch_bounds__(kBlock) void norm_wide_backward_kernel(fftmv_group_
   // where no row is held nothing needs them, and a call without rows may have none
   const float mean = held ? g.stats[2 * static_cast<int64_t>(blockIdx.x)] : 0.0f;
   const float rstd = held ? g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1] : 0.0f;
-  float m1 = 0.0f, m2 = 0.0f;
+  float m1 = 0.0f, m2 = 0.0f, n1 = 0.0f, n2 = 0.0f;
+  int turn = 0;
   for (int64_t c = threadIdx.x; c < D; c += kBlock) {
     const float w = g.weight ? g.weight[q * D + c] : 1.0f, b = g.bias ? g.bias[q * D + c] : 0.0f;
     float sb = 0.0f, sw = 0.0f;
-    for (int t0 = 0; t0 < held; t0 += 32) {
-      float pb = 0.0f, pw = 0.0f;
-      for (int t = t0; t < held && t < t0 + 32; ++t) {
-        const float xh = (static_cast<float>(x[t * g.x_row + c]) - mean) * rstd;
-        const float dz = static_cast<float>(dy[t * g.dy_row + c]) * activate_slope<T, ACT>(fmaf(xh, w, b));
-        pb += dz;
-        pw = fmaf(dz, xh, pw);
+    for (int t0 = 0; t0 < held; t0 += kInTurn * kInTurn) {
+      float fb = 0.0f, fw = 0.0f;
+      for (int t1 = t0; t1 < held && t1 < t0 + kInTurn * kInTurn; t1 += kInTurn) {
+        float pb = 0.0f, pw = 0.0f;
+        for (int t = t1; t < held && t < t1 + kInTurn; ++t) {
+          const float xh = (static_cast<float>(x[t * g.x_row + c]) - mean) * rstd;
+          const float dz = static_cast<float>(dy[t * g.dy_row + c]) * activate_slope<T, ACT>(fmaf(xh, w, b));
+          pb += dz;
+          pw = fmaf(dz, xh, pw);
+        }
+        fb += pb;
+        fw += pw;
       }
-      sb += pb;
-      sw += pw;
+      sb += fb;
+      sw += fw;
     }
     sums[c] = make_float2(sb, sw);
-    m1 = fmaf(sb, w, m1);
-    m2 = fmaf(sw, w, m2);
+    n1 = fmaf(sb, w, n1);
+    n2 = fmaf(sw, w, n2);
+    if (++turn == kInTurn) {
+      m1 += n1;
+      m2 += n2;
+      n1 = n2 = 0.0f;
+      turn = 0;
+    }
   }
+  m1 += n1;
+  m2 += n2;
   m1 = block_sum(m1) / count;
   m2 = block_sum(m2) / count;
   for (int t = 0; t < static_cast<int>(g.rows); ++t)

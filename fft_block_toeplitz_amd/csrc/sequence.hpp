@@ -209,7 +209,9 @@ __device__ __forceinline__ Normal normal_of(float z) {
     r.bell = fmaf(e, -0.5f * fmaf(a, a, -w), e);
     const float t = inverse_of<T>(fmaf(0.28284271247461901f, a, 1.0f));
     const float half = 0.5f * r.bell * (polynomial(kTail32, t) * t);
-    r.phi = a < 1.0f ? fmaf(z, polynomial(kCentre32, w), 0.5f) : z < 0.0f ? half : 1.0f - half;
+    float centre = fmaf(z, polynomial(kCentre32, w), 0.5f), side = z < 0.0f ? half : 1.0f - half;
+    asm volatile("" : "+v"(centre), "+v"(side));  // both and no branch: a wave has lanes on either side
+    r.phi = a < 1.0f ? centre : side;
   } else {
     const float x = 0.70710678118654752f * fabsf(z);
     const float t = __builtin_amdgcn_rcpf(fmaf(0.33f, x, 1.0f));

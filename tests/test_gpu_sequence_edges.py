@@ -241,3 +241,83 @@ def test_fp32_gelu_to_a_few_roundings(fm):
     assert (np.abs(y - v * phi) <= 18 * R.U * np.abs(v * phi)).all(), np.nanmax(np.abs(y / (v * phi) - 1)) / R.U
     bound = R.U * (18 * phi + 9 * np.abs(second))
     assert (np.abs(s - phi - second) <= bound).all(), (np.abs(s - phi - second) / bound).max()
+
+
+# FP32 numbers whose sum, one after the other, drifts: each addition rounds the same way over a whole binade. Their
+# sum over 512, 1024 terms is off by 128 and 256 U.
+DRIFTS = {512: 1.0118866, 1024: 1.9810181, 4096: 1.9963379, 16384: 1.9794922}
+
+
+def test_norm_parameter_gradients_of_many_tokens(fm):
+    """65536 tokens whose dy is the same drifting number: dbias is a product."""
+    N, G, D = 65536, 16, 1028
+    x = torch.randn(1, G * D, device="cuda")
+    y, stats = fm.group_norm(x, G, save=True)
+    dy = torch.full((1, G * D), DRIFTS[1024], device="cuda")
+    _, _, db = fm.group_norm_backward(dy.expand(N, -1), x.expand(N, -1), stats.expand(N, -1, -1).contiguous(), G)
+    want = np.full(G * D, N * float(np.float32(DRIFTS[1024])))
+    near(db, want, R.U * R.DEPTH * want, "dbias")
+
+
+def check_constant_gradient(fm, N, S, C, G):
+    """x at its mean and dy one drifting number c: dbias is a product, and dx what the mean of dy is off from c."""
+    x = torch.ones(1, 1, C, device="cuda").expand(N, S, C)
+    dy = torch.full((1, 1, C), DRIFTS[512], device="cuda").expand(N, S, C)
+    dx, dw, db = fm.group_norm_backward(dy, x, torch.ones(N, G, 2, device="cuda"), G)
+    c = float(np.float32(DRIFTS[512]))
+    near(db, np.full(C, N * S * c), np.full(C, R.U * R.DEPTH * N * S * c), "dbias")
+    assert not dw.any()
+    near(dx[::512], np.zeros(dx[::512].shape), np.full((1, 1, 1), (R.DEPTH + 4.0) * R.U * c), "dx")
+
+
+def test_norm_sums_of_many_rows_by_few_threads(fm):
+    """As many samples as fill the card, each 16384 rows in one range: their
+    variance, and the sums of the backward pass, from rows that all add the same
+    drifting number."""
+    N, S, C = 1025, 16384, 128
+    sign = 1.0 - 2.0 * (torch.arange(S, device="cuda") // 8 % 2)
+    v = float(np.sqrt(np.float32(DRIFTS[512])))
+    x = (sign[:, None] * v).expand(S, C).contiguous()[None]
+    y, stats = fm.group_norm(x.expand(N, -1, -1), 1, save=True, eps=0.0)
+    vf = float(np.float32(v))
+    near(stats[::64, 0, 0], np.zeros(17), np.full(17, R.U * R.DEPTH * vf), "mean")
+    # the variance's own sum is off by DEPTH U at most, its root by half of that
+    near(stats[::64, 0, 1], np.full(17, 1.0 / vf), np.full(17, (0.5 * R.DEPTH + 4.0) * R.U / vf), "rstd")
+    del y
+    check_constant_gradient(fm, N, S, C, 1)
+
+
+def test_norm_joins_many_ranges(fm):
+    """One sample of 65536 rows in a thousand ranges, 256 groups of one
+    channel: few threads a group to join them."""
+    S, C = 65536, 256
+    sign = 1.0 - 2.0 * (torch.arange(S, device="cuda") // 8 % 2)
+    v = float(np.sqrt(np.float32(DRIFTS[512])))
+    x = (sign[:, None] * v).expand(S, C).contiguous()[None]
+    _, stats = fm.group_norm(x, C, save=True, eps=0.0)
+    vf = float(np.float32(v))
+    near(stats[0, :, 1], np.full(C, 1.0 / vf), np.full(C, (0.5 * R.DEPTH + 4.0) * R.U / vf), "rstd")
+    check_constant_gradient(fm, 1, S, C, C)
+
+
+def test_norm_wide_groups_of_many_rows(fm):
+    """Groups wider than a workgroup, 4096 rows of one drifting number."""
+    S, D = 4096, 4100
+    x = torch.full((1, 1, D), DRIFTS[4096], device="cuda").expand(1, S, D)
+    c = float(np.float32(DRIFTS[4096]))
+    _, stats = fm.group_norm(x, 1, save=True)
+    near(stats[0, 0, :1], np.full(1, c), np.full(1, R.U * R.DEPTH * c), "mean")
+    S = 16384
+    x = torch.randn(1, 1, D, device="cuda")
+    _, stats = fm.group_norm(x, 1, save=True)
+    dy = torch.full((1, 1, D), DRIFTS[512], device="cuda").expand(1, S, D)
+    _, _, db = fm.group_norm_backward(dy, x.expand(1, S, D), stats, 1)
+    want = np.full(D, S * float(np.float32(DRIFTS[512])))
+    near(db, want, R.U * R.DEPTH * want, "dbias")
+
+
+@pytest.mark.parametrize("N,S,G,D,dtype,lengths", [
+    (3, 5, 2, 4100, "fp32", [5, 0, 3]), (2, 70, 1, 4099, "fp32", None), (2, 40, 3, 8200, "bf16", [40, 33]),
+    (5, 1, 1, 9001, "fp16", None), (1, 65, 2, 8193, "bf16", None)])
+def test_norm_wide_groups(fm, N, S, G, D, dtype, lengths):
+    check_norm(fm, 45, N, S, G, D, dtype, "silu", lengths=lengths)
