@@ -81,7 +81,9 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
 class RecurrentLayer(nn.Module):
     """y = out(silu(norm(h))) + skip(h), h the recurrence of (x', gate) = in(x)
     over time; each time step is normalised by itself. Inputs [batch, steps,
-    inputs], outputs [batch, steps, outputs]."""
+    inputs], outputs [batch, steps, outputs]. Moved to a 16-bit type
+    (``layer.bfloat16()``) or under autocast the fields are of that type; states
+    and the normalisation's arithmetic stay float32."""
 
     def __init__(self, inputs: int, channels: int, outputs: int, groups: int = 8, device="cuda"):
         super().__init__()
@@ -96,11 +98,14 @@ class RecurrentLayer(nn.Module):
         with torch.no_grad():  # memories from one step to a few hundred
             self.into.bias[channels:] = torch.linspace(-2.0, 6.0, channels, device=device)
 
+    def _norm(self, h):
+        return sequence.group_norm(h, self.groups, self.weight.float(), self.bias.float(), activation="silu")
+
     def forward(self, x, state=None, lengths=None):
         """(y, last states); ``state``: float32 [batch, channels] or None."""
         p = self.into(x)
         h, last = recurrence(p[..., :self.channels], p[..., self.channels:], state, lengths=lengths)
-        z = group_norm(h.flatten(0, 1), self.groups, self.weight, self.bias, activation="silu")
+        z = self._norm(h.flatten(0, 1))
         return self.out(z.view_as(h)) + self.skip(h), last
 
     @torch.no_grad()
@@ -109,5 +114,4 @@ class RecurrentLayer(nn.Module):
         channels], moves on in place. Returns y [batch, outputs]."""
         p = self.into(x)
         h = sequence.recurrence_step(p[:, :self.channels], p[:, self.channels:], state, slots)
-        z = sequence.group_norm(h, self.groups, self.weight, self.bias, activation="silu")
-        return self.out(z) + self.skip(h)
+        return self.out(self._norm(h)) + self.skip(h)

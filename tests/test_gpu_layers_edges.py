@@ -124,3 +124,31 @@ def test_public_names_keep_gradients(fm):
                  lambda: fm.recurrence_step(x[:, 0].detach(), g[:, 0].detach(), h0)):
         with pytest.raises(ValueError, match="gradient"):
             call()
+
+
+@pytest.mark.parametrize("how", ["bfloat16", "half", "autocast"])
+def test_layer_in_16_bits(fm, how):
+    """The layer moved to a 16-bit type, or under autocast: trains and streams
+    as in FP32, to that type's rounding."""
+    from fft_block_toeplitz_amd.layers import RecurrentLayer
+
+    torch.manual_seed(5)
+    layer = RecurrentLayer(5, 40, 3, groups=4)
+    x = torch.randn(3, 150, 5, device="cuda")
+    want, want_last = layer(x)
+    want.square().mean().backward()
+    ref = [p.grad.clone() for p in layer.parameters()]
+    layer.zero_grad()
+    # a unit of bfloat16 is 2^-8; a few operations one after the other
+    with torch.autocast("cuda", torch.bfloat16, enabled=how == "autocast"):
+        if how != "autocast":
+            layer, x = getattr(layer, how)(), getattr(x, how)()
+        y, last = layer(x)
+        y.square().mean().backward()
+        state = torch.zeros(3, 40, device="cuda")
+        steps = torch.stack([layer.step(x[:, t], state) for t in range(150)], 1)
+    assert y.dtype == (torch.float16 if how == "half" else torch.bfloat16) and last.dtype == torch.float32
+    assert off(y, want.detach().double()) < 16 * 2 ** -8 and off(steps, y.detach().double()) < 16 * 2 ** -8
+    assert off(state, last.detach().double()) < 16 * 2 ** -8
+    for p, r in zip(layer.parameters(), ref):
+        assert p.grad.dtype == p.dtype and off(p.grad, r.double()) < 32 * 2 ** -8
