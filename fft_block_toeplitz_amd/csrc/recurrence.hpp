@@ -125,7 +125,7 @@ __device__ __forceinline__ ScanChain scan_chain(const fftmv_recurrence_t &r, con
   s.ticket = &(static_cast<ScanCounter *>(r.counters) + chain)->ticket;
   s.words = static_cast<uint64_t *>(r.workspace) + static_cast<int64_t>(chain) * a.places * (3 * W);
   s.call = r.call;
-  s.deep = a.chains * a.blocks <= 12;
+  s.deep = a.chains * a.blocks < 24;
   return s;
 }
 
@@ -148,13 +148,19 @@ __device__ __forceinline__ float value_of(uint64_t word) {
 }
 
 // The state behind place p - 1 in column c. Looks at the words of the two
-// chunks in front of p together, and of two more where a chain has over forty
+// chunks in front of p together, and of two more where a chain has over twenty
 // chunks running at once (some 500 workgroups run together): every word that
 // is looked at delays all loads, every chunk less makes more of the chain wait
-// in a row. Measured forward, 2 | 4 | 8 chunks: 4 x 4096 x 4096 bf16 105 | 114 |
-// 125 us, 30011 x 2048 fp16 packed 117 | 125 | 241, one series of 65536 x 1024
-// bf16 170 | 137 | 148. A state is there sooner or later, since each chunk
-// publishes its own. The bound on the polls ends the wait if the workspace
+// in a row. Two | four chunks, us, one series of 61e6 bf16 or 31e6 FP32 elements
+// in so many chains (blocks of channels):
+//                    8           12          16          20          24          32
+//   bf16 forward     157 | 112   130 | 117   109 | 106   115 | 114   102 | 102   101.6 | 102.0
+//   bf16 backward    228 | 217   211 | 206   201 | 201   196 | 196   193 | 193   189.1 | 189.4
+//   FP32 forward     150 | 102   123 |  99    90 |  85    99 |  97    83 |  82    79.9 |  80.8
+//   FP32 backward    197 | 158   173 | 156   153 | 148   156 | 152   143 | 141   141.1 | 141.7
+//   fp16, 45 packed  172 | 167   179 | 176   161 | 159   175 | 174   161 | 161   155   | 155
+// A state is there sooner or later, since each chunk publishes its own. The
+// bound on the polls ends the wait if the workspace
 // was not what the call requires: the result is NaN.
 template <int W>
 __device__ __forceinline__ float state_before(const ScanChain &s, int p, int c) {
