@@ -31,6 +31,23 @@ int widest_slab(int D, int G, int vec, int lanes) {
   return 0;
 }
 
+// Pieces of one group wider than the lanes of a workgroup: as few as 256 lanes
+// allow, of about the same width, in whole vectors; the last one at least one
+// vector wide.
+void cut_group(NormShape &s, int vec) {
+  const int64_t D = s.D, most = 256 * static_cast<int64_t>(vec), pieces = (D + most - 1) / most;
+  int64_t width = ((D + pieces - 1) / pieces + vec - 1) / vec * vec;
+  while ((D - 1) % width + 1 < vec) width -= vec;
+  s.width = static_cast<int>(width);
+  s.cut = static_cast<int>((D + width - 1) / width);
+  s.gs = 1;
+  s.slabs = s.G * s.cut;
+  s.lx = s.width / vec;
+  s.threads = 256;
+  s.ty = s.threads / s.lx;
+  s.sub = 1;
+}
+
 void take_slab(NormShape &s, int gs, int vec, int threads) {
   s.gs = gs;
   s.slabs = (s.G + gs - 1) / gs;
@@ -62,9 +79,18 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   s.D = static_cast<int>(channels / groups);
   const int es = dtype == FFTMV_F32 ? 4 : 2;
   p.vec = 16 / es;
-  if (widest_slab(s.D, s.G, p.vec, 1024) == 0) p.vec = 1;
+  s.cut = 1;
+  const bool wide = s.D > 1024 * p.vec;  // one group is more than a workgroup's lanes
+  if (!wide && widest_slab(s.D, s.G, p.vec, 1024) == 0) p.vec = 1;
   const int v = p.vec, alone = static_cast<int>((static_cast<int64_t>(s.D) + v - 1) / v);  // lanes of one group
-  if (rows == 0 || alone > 1024 || widest_slab(s.D, s.G, v, 1024) == 0) {
+  const bool split = wide || rows == 0;
+  // A row or two of many samples: one workgroup for each group. Us forward and
+  // backward, so | cut and split as below: 2000 tokens of 9000 bf16 channels 43
+  // and 99 | 104 and 186, 300 of them 19 and 39 | 23 and 43, 64 of them 16.5 and 28
+  // | 14.7 and 20; 2000 samples of two rows 81 and 173 | 110 and 193, 300 of them 34
+  // and 63 | 24 and 43; 2000 of three 118 and 258 | 114 and 203.
+  if (wide && rows > 0 && rows <= 2 && samples * groups >= 256 * rows * rows) {
+    p.kind = NormPlan::kWide;
     p.rows = samples;
     p.workspace = backward ? static_cast<size_t>(samples * channels) * 8 : 0;
     return p;
@@ -79,7 +105,7 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   // 206 one by one, 20522 x 246 in 2 groups 16 and 32 against 26 and 78);
   // where that leaves too few workgroups for the CUs, the form below takes
   // them one by one.
-  if (rows <= 8) {
+  if (!split && rows <= 8) {
     const int R = std::max(1, s.S);
     const int64_t least = static_cast<int64_t>(alone) * R;
     const int threads = least <= 256 ? 256 : least <= 512 ? 512 : 0;
@@ -103,9 +129,9 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   // with twice the inputs: four). 400 samples of 100 rows of 8 x 64 bf16 take
   // 31 and 56 us, split 42 and 64.
   const int several = backward ? 4 : 8;
-  for (int P = 1; P <= several && p.kind == NormPlan::kWide; P *= several) {
+  for (int P = 1; !split && P <= several && p.kind == NormPlan::kSplit; P *= several) {
     const int most = P == 1 ? kNormThreads : kHeldThreads;
-    for (int threads = 256; threads <= most && p.kind == NormPlan::kWide; threads *= 2) {
+    for (int threads = 256; threads <= most && p.kind == NormPlan::kSplit; threads *= 2) {
       for (int lanes = std::min(threads, 256); lanes >= 1; lanes /= 2) {
         const int gs = widest_slab(s.D, s.G, v, std::max(lanes, alone));
         if (gs == 0) continue;
@@ -142,7 +168,7 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
       }
     }
   }
-  if (p.kind != NormPlan::kWide) {
+  if (p.kind != NormPlan::kSplit) {
     const int q = p.kind == NormPlan::kTokens ? Q : 1, sets = backward ? 2 * q : q;
     take_team(s, sets * s.sub * s.gs);
     const size_t flat = static_cast<size_t>(s.sub) * s.ty * s.lx;
@@ -153,12 +179,17 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
     p.workspace = backward && s.across > 1 ? static_cast<size_t>(s.across) * channels * 8 : 0;
     return p;
   }
-  // Split: ranges of rows over many workgroups.
-  p.kind = NormPlan::kSplit;
-  int gs = widest_slab(s.D, s.G, v, std::max(alone, 32));  // 512 bytes of a row, or one group
-  if (gs == 0) gs = widest_slab(s.D, s.G, v, 1024);
-  take_slab(s, gs, v, 256);
-  if (s.lx > 256) take_slab(s, s.gs, v, round64(s.lx));
+  // Split: ranges of rows over many workgroups. Groups wider than a workgroup's
+  // lanes as well, cut into pieces: 4000 rows of 5000 FP32 channels in one group
+  // take 52 us forward and 62 backward, 70 and 51 thousand by one workgroup.
+  if (wide) {
+    cut_group(s, v);
+  } else {
+    int gs = widest_slab(s.D, s.G, v, std::max(alone, 32));  // 512 bytes of a row, or one group
+    if (gs == 0) gs = widest_slab(s.D, s.G, v, 1024);
+    take_slab(s, gs, v, 256);
+    if (s.lx > 256) take_slab(s, s.gs, v, round64(s.lx));
+  }
   take_team(s, s.gs);
   const int64_t tile = 8 * static_cast<int64_t>(s.ty);
   const int64_t want = std::max<int64_t>(1, 2048 / std::max<int64_t>(1, samples * s.slabs));
@@ -168,7 +199,7 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   s.across = static_cast<int>(std::max<int64_t>(1, (rows + s.range - 1) / s.range));
   p.lds = (static_cast<size_t>(s.ty) * s.lx * v + s.gs) * 4;
   p.rows = samples * s.across;
-  p.workspace = static_cast<size_t>(p.rows) * (backward ? channels + groups : groups) * 8;
+  p.workspace = static_cast<size_t>(p.rows) * ((backward ? channels : 0) + (wide ? s.slabs : groups)) * 8;
   return p;
 }
 

@@ -45,6 +45,7 @@ struct NormShape {
   int team;         // threads that sum one group (a power of two, at most a wave)
   int across;       // workgroups over the samples of one slab (resident), or row ranges of a sample (split)
   int range;        // split: rows of a range
+  int cut, width;   // split: slabs that one group is cut into where it is wider than the lanes (else 1), their channels
 };
 
 __device__ __forceinline__ int held_rows(const fftmv_group_norm_t &g, int64_t n) {
@@ -69,10 +70,11 @@ __device__ __forceinline__ Vec<T, VEC> load_held(const T *sample, int row, int h
   }
 }
 
-// This thread's place in a slab.
-template <int VEC>
+// This thread's place in a slab. CUT: slabs are pieces of one group.
+template <int VEC, bool CUT = false>
 struct SlabLane {
   int ng, wd;           // groups and channels of this slab
+  int g0;               // the slab's first group
   int lane, flat;       // flat: its row of lanes
   int sub, row;         // which of the samples side by side, and the first of its rows there (ty apart)
   int c;                // first of its VEC channels, within the slab. The last lane steps back to end with the slab:
@@ -80,9 +82,18 @@ struct SlabLane {
   int64_t ch0;          // the slab's first channel
   bool in;
   __device__ SlabLane(const NormShape &s, int slab) {
-    ng = s.gs < s.G - slab * s.gs ? s.gs : s.G - slab * s.gs;
-    wd = ng * s.D;
-    ch0 = static_cast<int64_t>(slab) * s.gs * s.D;
+    if constexpr (CUT) {
+      g0 = slab / s.cut;
+      const int from = (slab - g0 * s.cut) * s.width;
+      ng = 1;
+      wd = s.D - from < s.width ? s.D - from : s.width;
+      ch0 = static_cast<int64_t>(g0) * s.D + from;
+    } else {
+      g0 = slab * s.gs;
+      ng = s.gs < s.G - g0 ? s.gs : s.G - g0;
+      wd = ng * s.D;
+      ch0 = static_cast<int64_t>(g0) * s.D;
+    }
     lane = threadIdx.x % s.lx;
     flat = threadIdx.x / s.lx;
     sub = s.sub > 1 ? flat / s.ty : 0;
@@ -138,8 +149,8 @@ struct GroupOf {
 
 // A thread's contribution to the sums of its groups, in `part` (a row of slots
 // for each row of lanes): one slot a thread, or one a channel.
-template <int VEC, bool WHOLE>
-__device__ __forceinline__ void put_part(float *part, const NormShape &s, const SlabLane<VEC> &l, const float (&v)[VEC]) {
+template <int VEC, bool WHOLE, typename Lane>
+__device__ __forceinline__ void put_part(float *part, const NormShape &s, const Lane &l, const float (&v)[VEC]) {
   if (!l.in) return;
   if constexpr (WHOLE) {
     float sum = v[0];
@@ -285,9 +296,9 @@ __global__ __launch_bounds__((kResidentThreads<Q, P>)) void norm_forward_kernel(
 // Sums of dz and dz xhat over the rows of all samples of this workgroup: row
 // `first` of the workspace, or the results themselves where there is one; `more`:
 // added to what an earlier call left there.
-template <int VEC>
+template <int VEC, typename Lane>
 __device__ __forceinline__ void put_param_sums(const fftmv_group_norm_t &g, const NormShape &s,
-                                               const SlabLane<VEC> &l, float *lds, int first, bool alone,
+                                               const Lane &l, float *lds, int first, bool alone,
                                                const float (&db)[VEC], const float (&dw)[VEC], bool more = false) {
   const int lw = s.lx * VEC;
   const int64_t C = static_cast<int64_t>(s.G) * s.D;
@@ -455,16 +466,38 @@ struct Range {
   }
 };
 
+// What the ranges leave for each of their slab's groups (CUT: for the slab, a
+// piece of one group): one pair of numbers; a row of pairs for each range.
+template <bool CUT>
+__device__ __forceinline__ int64_t pairs_of_range(const NormShape &s) {
+  return CUT ? s.slabs : s.G;
+}
+// Where part i of a group stands behind its first: range i, or piece i % cut of range i / cut.
+template <bool CUT>
+__device__ __forceinline__ int64_t range_pair(const NormShape &s, int64_t pairs, int i) {
+  if constexpr (!CUT) return i * pairs;
+  const int part = i / s.cut;
+  return part * pairs + (i - part * s.cut);
+}
+// The shape as team_sums takes it: a slab of one group as wide as the slab.
+template <bool CUT, typename Lane>
+__device__ __forceinline__ NormShape summed(const NormShape &s, const Lane &l) {
+  NormShape t = s;
+  if constexpr (CUT) t.D = l.wd;
+  return t;
+}
+
 constexpr int kTile = 4;  // rows of a thread in one tile (eight measured the same, and spilled)
 
 // (mean, sum of squared deviations) of each group over one range, from
 // tiles of kTile rows a thread, each about its own mean and joined pairwise.
-template <typename T, int VEC>
+template <typename T, int VEC, bool CUT>
 __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_norm_t g, NormShape s) {
   extern __shared__ float lds[];
   float *part = lds, *mean = lds + s.ty * s.lx * VEC;
   const Range r(g, s);
-  const SlabLane<VEC> l(s, r.slab);
+  const SlabLane<VEC, CUT> l(s, r.slab);
+  const NormShape sum_of = summed<CUT>(s, l);
   const GroupOf<VEC, false> group(l.c, s.D);
   const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
   float mu[VEC], m2[VEC], count = 0.0f, bmu[VEC], bm2[VEC], bcount = 0.0f;  // of all tiles, of a block of them
@@ -520,8 +553,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_n
   for (int e = 0; e < VEC; ++e) v[e] = count * mu[e];
   put_part<VEC, false>(part, s, l, v);
   __syncthreads();
-  team_sums<VEC, false>(part, s, l.ng, 1, [&](int k, float sum) {
-    mean[k] = rows > 0 ? sum / (static_cast<float>(rows) * s.D) : 0.0f;
+  team_sums<VEC, false>(part, sum_of, l.ng, 1, [&](int k, float sum) {
+    mean[k] = rows > 0 ? sum / (static_cast<float>(rows) * sum_of.D) : 0.0f;
   });
   __syncthreads();
 #pragma unroll
@@ -531,20 +564,23 @@ __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_n
   }
   put_part<VEC, false>(part, s, l, v);
   __syncthreads();
-  float2 *to = static_cast<float2 *>(g.workspace) + (r.n * s.across + r.part) * s.G + static_cast<int64_t>(r.slab) * s.gs;
-  team_sums<VEC, false>(part, s, l.ng, 1, [&](int k, float sum) { to[k] = make_float2(mean[k], sum); });
+  float2 *to = static_cast<float2 *>(g.workspace) + (r.n * s.across + r.part) * pairs_of_range<CUT>(s) +
+               (CUT ? r.slab : l.g0);
+  team_sums<VEC, false>(part, sum_of, l.ng, 1, [&](int k, float sum) { to[k] = make_float2(mean[k], sum); });
 }
 
 // Joins the ranges' sums, then normalises one range.
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool CUT>
 __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_norm_t g, NormShape s) {
   extern __shared__ float lds[];
   float *mean = lds, *rstd = lds + s.gs;
   const Range r(g, s);
-  const SlabLane<VEC> l(s, r.slab);
+  const SlabLane<VEC, CUT> l(s, r.slab);
   const GroupOf<VEC, false> group(l.c, s.D);
   const int held = held_rows(g, r.n);
-  const float2 *from = static_cast<const float2 *>(g.workspace) + r.n * s.across * s.G + static_cast<int64_t>(r.slab) * s.gs;
+  const int64_t pairs = pairs_of_range<CUT>(s);
+  const float2 *from = static_cast<const float2 *>(g.workspace) + r.n * s.across * pairs + l.g0 * s.cut;
+  const int parts = s.across * s.cut;  // of a group: the pieces of one range, then of the next
   // one team of threads a group, four ranges of a thread at a time, joined
   // pairwise: (count, mean, sum of squared deviations)
   const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
@@ -556,20 +592,22 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
       mu = fmaf(d, share, mu);
       count = all;
     };
-    for (int b0 = me; b0 < s.across; b0 += kInTurn * s.team) {
+    for (int b0 = me; b0 < parts; b0 += kInTurn * s.team) {
       float bcount = 0.0f, bmu = 0.0f, bsq = 0.0f;  // of a block of ranges
-      for (int i0 = b0; i0 < s.across && i0 < b0 + kInTurn * s.team; i0 += 4 * s.team) {
+      for (int i0 = b0; i0 < parts && i0 < b0 + kInTurn * s.team; i0 += 4 * s.team) {
         float2 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = i0 + j * s.team;
-          v[j] = from[static_cast<int64_t>(i < s.across ? i : 0) * s.G + k];
+          v[j] = from[range_pair<CUT>(s, pairs, i < parts ? i : 0) + k];
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int rows = held - (i0 + j * s.team) * s.range;
-          if (i0 + j * s.team < s.across && rows > 0)
-            join(bcount, bmu, bsq, static_cast<float>(rows < s.range ? rows : s.range) * s.D, v[j].x, v[j].y);
+          const int i = i0 + j * s.team, part = CUT ? i / s.cut : i, piece = CUT ? i - part * s.cut : 0;
+          const int rows = held - part * s.range, rest = s.D - piece * s.width;
+          if (i < parts && rows > 0)
+            join(bcount, bmu, bsq, static_cast<float>(rows < s.range ? rows : s.range) * (CUT && rest > s.width ? s.width : rest),
+                 v[j].x, v[j].y);
         }
       }
       join(count, mu, sq, bcount, bmu, bsq);
@@ -581,8 +619,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
     if (me == 0) {
       mean[k] = mu;
       rstd[k] = held ? 1.0f / sqrtf(sq / (static_cast<float>(held) * s.D) + g.eps) : 0.0f;
-      if (g.stats && r.part == 0) {
-        float *to = g.stats + 2 * (r.n * s.G + static_cast<int64_t>(r.slab) * s.gs + k);
+      if (g.stats && r.part == 0) {  // (CUT: every piece the same)
+        float *to = g.stats + 2 * (r.n * s.G + l.g0 + k);
         to[0] = mu;
         to[1] = rstd[k];
       }
@@ -619,22 +657,23 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
 
 // Sums of dz and dz xhat over one range: of each channel, in row (n, range) of
 // the workspace, and, times the weight, of each group, behind those rows.
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool CUT>
 __global__ __launch_bounds__(kNormThreads) void norm_sums_kernel(fftmv_group_norm_t g, NormShape s) {
   extern __shared__ float lds[];
   const Range r(g, s);
-  const SlabLane<VEC> l(s, r.slab);
+  const SlabLane<VEC, CUT> l(s, r.slab);
+  const NormShape sum_of = summed<CUT>(s, l);
   float w[VEC], db[VEC], dw[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) w[e] = db[e] = dw[e] = 0.0f;
-  if (l.in) {
+  if (l.in && r.to > r.from) {  // (without rows there may be no statistics)
     const GroupOf<VEC, false> group(l.c, s.D);
     float b[VEC], mu[VEC], rs[VEC];
     load_params(g.weight, l.ch0 + l.c, 1.0f, w);
     load_params(g.bias, l.ch0 + l.c, 0.0f, b);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float *from = g.stats + 2 * (r.n * s.G + static_cast<int64_t>(r.slab) * s.gs + group[e]);
+      const float *from = g.stats + 2 * (r.n * s.G + l.g0 + group[e]);
       mu[e] = from[0];
       rs[e] = from[1];
     }
@@ -681,7 +720,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_sums_kernel(fftmv_group_nor
   }
   const int64_t row = r.n * s.across + r.part, C = static_cast<int64_t>(s.G) * s.D;
   put_param_sums<VEC>(g, s, l, lds, static_cast<int>(row), false, db, dw);
-  float2 *to = static_cast<float2 *>(g.workspace) + s.N * s.across * C + row * s.G + static_cast<int64_t>(r.slab) * s.gs;
+  float2 *to = static_cast<float2 *>(g.workspace) + s.N * s.across * C + row * pairs_of_range<CUT>(s) +
+               (CUT ? r.slab : l.g0);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     float t[VEC];
@@ -690,7 +730,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_sums_kernel(fftmv_group_nor
     __syncthreads();
     put_part<VEC, false>(lds, s, l, t);
     __syncthreads();
-    team_sums<VEC, false>(lds, s, l.ng, 1, [&](int i, float sum) { (k ? to[i].y : to[i].x) = sum; });
+    team_sums<VEC, false>(lds, sum_of, l.ng, 1, [&](int i, float sum) { (k ? to[i].y : to[i].x) = sum; });
   }
 }
 
@@ -735,7 +775,7 @@ __device__ __forceinline__ void param_sums(const fftmv_group_norm_t &g, int64_t 
 
 // dx of one range, the means of dz w and dz w xhat joined from all ranges; and,
 // in the workgroups behind the first `main`, the parameters' sums.
-template <typename T, int VEC, int ACT>
+template <typename T, int VEC, int ACT, bool CUT>
 __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_norm_t g, NormShape s, int64_t main) {
   extern __shared__ float lds[];
   if (blockIdx.x >= main) {
@@ -744,27 +784,28 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_nor
   }
   float *m1 = lds, *m2 = lds + s.gs;
   const Range r(g, s);
-  const SlabLane<VEC> l(s, r.slab);
+  const SlabLane<VEC, CUT> l(s, r.slab);
   const GroupOf<VEC, false> group(l.c, s.D);
   const int held = held_rows(g, r.n);
   const int64_t C = static_cast<int64_t>(s.G) * s.D;
-  const float2 *from = static_cast<const float2 *>(g.workspace) + s.N * s.across * C + r.n * s.across * s.G +
-                       static_cast<int64_t>(r.slab) * s.gs;
+  const int64_t pairs = pairs_of_range<CUT>(s);
+  const float2 *from = static_cast<const float2 *>(g.workspace) + s.N * s.across * C + r.n * s.across * pairs + l.g0 * s.cut;
+  const int parts = s.across * s.cut;
   const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
   for (int k = threadIdx.x / s.team; k < l.ng; k += teams) {
     float a = 0.0f, b = 0.0f;
-    for (int b0 = me; b0 < s.across; b0 += kInTurn * s.team) {
+    for (int b0 = me; b0 < parts; b0 += kInTurn * s.team) {
       float pa = 0.0f, pb = 0.0f;
-      for (int i0 = b0; i0 < s.across && i0 < b0 + kInTurn * s.team; i0 += 4 * s.team) {
+      for (int i0 = b0; i0 < parts && i0 < b0 + kInTurn * s.team; i0 += 4 * s.team) {
         float2 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int i = i0 + j * s.team;
-          v[j] = from[static_cast<int64_t>(i < s.across ? i : 0) * s.G + k];
+          v[j] = from[range_pair<CUT>(s, pairs, i < parts ? i : 0) + k];
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (i0 + j * s.team < s.across) pa += v[j].x, pb += v[j].y;
+          if (i0 + j * s.team < parts) pa += v[j].x, pb += v[j].y;
       }
       a += pa;
       b += pb;
@@ -780,13 +821,14 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_nor
     }
   }
   __syncthreads();
-  if (!l.in) return;
+  const int end = s.S - r.from < s.range ? s.S : r.from + s.range;
+  if (!l.in || r.from >= end) return;
   float w[VEC], b[VEC], mu[VEC], rs[VEC], k1[VEC], k2[VEC];
   load_params(g.weight, l.ch0 + l.c, 1.0f, w);
   load_params(g.bias, l.ch0 + l.c, 0.0f, b);
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    const float *st = g.stats + 2 * (r.n * s.G + static_cast<int64_t>(r.slab) * s.gs + group[e]);
+    const float *st = g.stats + 2 * (r.n * s.G + l.g0 + group[e]);
     mu[e] = st[0];
     rs[e] = st[1];
     k1[e] = m1[group[e]];
@@ -795,7 +837,6 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_nor
   const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
   const T *dy = static_cast<const T *>(g.dy) + r.n * g.dy_sample + l.ch0 + l.c;
   T *dx = static_cast<T *>(g.dx) + r.n * g.dx_sample + l.ch0 + l.c;
-  const int end = s.S - r.from < s.range ? s.S : r.from + s.range;
   for (int t = r.from + l.row; t < end; t += 2 * s.ty) {
     Vec<T, VEC> v[2], d[2];
 #pragma unroll
@@ -821,9 +862,9 @@ __global__ __launch_bounds__(kNormThreads) void norm_grad_kernel(fftmv_group_nor
 }
 
 // ---------------------------------------------------------------- wide
-// Groups wider than a workgroup's lanes (8192 channels at 16 bits): one
-// workgroup per sample and group, its threads along the channels, the rows in
-// turn, read again for each pass.
+// A row or two of groups wider than a workgroup's lanes (8192 channels at 16
+// bits, 4096 in FP32): one workgroup per sample and group, its threads along the
+// channels, the rows in turn, read again from the caches for each pass.
 __device__ __forceinline__ float block_sum(float v) {
   __shared__ float part[kBlock / kWave];
   v = wave_sum(v);
@@ -837,27 +878,16 @@ __device__ __forceinline__ float block_sum(float v) {
 }
 
 // The sum of f(t, c) over a sample's held rows and this thread's channels, in
-// blocks of kInTurn channels and rows.
+// blocks of kInTurn channels.
 template <typename F>
 __device__ __forceinline__ float wide_sum(int held, int64_t D, F f) {
   float sum = 0.0f;
-  for (int t0 = 0; t0 < held; t0 += kInTurn * kInTurn) {
-    float far = 0.0f;
-    for (int t1 = t0; t1 < held && t1 < t0 + kInTurn * kInTurn; t1 += kInTurn) {
-      float near = 0.0f;
-      for (int t = t1; t < held && t < t1 + kInTurn; ++t) {
-        float row = 0.0f;
-        for (int64_t c0 = threadIdx.x; c0 < D; c0 += kInTurn * kBlock) {
-          float part = 0.0f;
-          for (int64_t c = c0; c < D && c < c0 + kInTurn * kBlock; c += kBlock) part += f(t, c);
-          row += part;
-        }
-        near += row;
-      }
-      far += near;
+  for (int t = 0; t < held; ++t)
+    for (int64_t c0 = threadIdx.x; c0 < D; c0 += kInTurn * kBlock) {
+      float part = 0.0f;
+      for (int64_t c = c0; c < D && c < c0 + kInTurn * kBlock; c += kBlock) part += f(t, c);
+      sum += part;
     }
-    sum += far;
-  }
   return sum;
 }
 
@@ -901,29 +931,18 @@ __global__ __launch_bounds__(kBlock) void norm_wide_backward_kernel(fftmv_group_
   const T *dy = static_cast<const T *>(g.dy) + n * g.dy_sample + q * D;
   T *dx = static_cast<T *>(g.dx) + n * g.dx_sample + q * D;
   float2 *sums = static_cast<float2 *>(g.workspace) + n * g.channels + q * D;
-  // where no row is held nothing needs them, and a call without rows may have none
-  const float mean = held ? g.stats[2 * static_cast<int64_t>(blockIdx.x)] : 0.0f;
-  const float rstd = held ? g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1] : 0.0f;
+  const float mean = g.stats[2 * static_cast<int64_t>(blockIdx.x)];
+  const float rstd = g.stats[2 * static_cast<int64_t>(blockIdx.x) + 1];
   float m1 = 0.0f, m2 = 0.0f, n1 = 0.0f, n2 = 0.0f;
   int turn = 0;
   for (int64_t c = threadIdx.x; c < D; c += kBlock) {
     const float w = g.weight ? g.weight[q * D + c] : 1.0f, b = g.bias ? g.bias[q * D + c] : 0.0f;
     float sb = 0.0f, sw = 0.0f;
-    for (int t0 = 0; t0 < held; t0 += kInTurn * kInTurn) {
-      float fb = 0.0f, fw = 0.0f;
-      for (int t1 = t0; t1 < held && t1 < t0 + kInTurn * kInTurn; t1 += kInTurn) {
-        float pb = 0.0f, pw = 0.0f;
-        for (int t = t1; t < held && t < t1 + kInTurn; ++t) {
-          const float xh = (static_cast<float>(x[t * g.x_row + c]) - mean) * rstd;
-          const float dz = static_cast<float>(dy[t * g.dy_row + c]) * activate_slope<T, ACT>(fmaf(xh, w, b));
-          pb += dz;
-          pw = fmaf(dz, xh, pw);
-        }
-        fb += pb;
-        fw += pw;
-      }
-      sb += fb;
-      sw += fw;
+    for (int t = 0; t < held; ++t) {
+      const float xh = (static_cast<float>(x[t * g.x_row + c]) - mean) * rstd;
+      const float dz = static_cast<float>(dy[t * g.dy_row + c]) * activate_slope<T, ACT>(fmaf(xh, w, b));
+      sb += dz;
+      sw = fmaf(dz, xh, sw);
     }
     sums[c] = make_float2(sb, sw);
     n1 = fmaf(sb, w, n1);
@@ -955,7 +974,7 @@ __global__ __launch_bounds__(kBlock) void norm_wide_backward_kernel(fftmv_group_
 // ---------------------------------------------------------------- plans
 // What a call launches; decided by sizes alone.
 struct NormPlan {
-  enum Kind { kWide, kTokens, kRow, kResident, kSplit } kind = kWide;
+  enum Kind { kSplit, kTokens, kRow, kResident, kWide } kind = kSplit;
   bool whole = false;
   int vec = 1;
   NormShape s{};
@@ -967,6 +986,14 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
 
 hipError_t launch_param_sums(const fftmv_group_norm_t &g, int64_t rows, hipStream_t s);
 
+// Groups are cut only where they are wider than the lanes, so into whole vectors.
+template <int VEC, typename F>
+hipError_t by_cut(const NormShape &h, F f) {
+  if constexpr (VEC > 1)
+    if (h.cut > 1) return f(Const<true>{});
+  return f(Const<false>{});
+}
+
 template <typename T, int ACT, int VEC>
 hipError_t launch_norm_forward_vec(const fftmv_group_norm_t &g, const NormPlan &p, hipStream_t s) {
   const NormShape &h = p.s;
@@ -974,11 +1001,14 @@ hipError_t launch_norm_forward_vec(const fftmv_group_norm_t &g, const NormPlan &
   if (p.kind == NormPlan::kSplit) {
     const int64_t blocks = h.N * h.slabs * h.across;
     if (!grid_fits(blocks, h.threads)) return hipErrorInvalidConfiguration;
-    norm_ranges_kernel<T, VEC><<<static_cast<unsigned>(blocks), threads, p.lds, s>>>(g, h);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    norm_apply_kernel<T, VEC, ACT><<<static_cast<unsigned>(blocks), threads, 2 * h.gs * sizeof(float), s>>>(g, h);
-    return hipGetLastError();
+    return by_cut<VEC>(h, [&](auto cut) {
+      constexpr bool CUT = decltype(cut)::value;
+      norm_ranges_kernel<T, VEC, CUT><<<static_cast<unsigned>(blocks), threads, p.lds, s>>>(g, h);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      norm_apply_kernel<T, VEC, ACT, CUT><<<static_cast<unsigned>(blocks), threads, 2 * h.gs * sizeof(float), s>>>(g, h);
+      return hipGetLastError();
+    });
   }
   const unsigned blocks = static_cast<unsigned>(h.slabs * h.across);
   if (p.kind == NormPlan::kTokens) {
@@ -1001,12 +1031,15 @@ hipError_t launch_norm_backward_vec(const fftmv_group_norm_t &g, const NormPlan 
   if (p.kind == NormPlan::kSplit) {
     const int64_t blocks = h.N * h.slabs * h.across, more = (g.channels + kSumChannels - 1) / kSumChannels;
     if (!grid_fits(blocks + more, h.threads)) return hipErrorInvalidConfiguration;
-    norm_sums_kernel<T, VEC, ACT><<<static_cast<unsigned>(blocks), threads, p.lds, s>>>(g, h);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const size_t lds = std::max<size_t>(2 * h.gs, 2 * h.threads) * sizeof(float);
-    norm_grad_kernel<T, VEC, ACT><<<static_cast<unsigned>(blocks + more), threads, lds, s>>>(g, h, blocks);
-    return hipGetLastError();
+    return by_cut<VEC>(h, [&](auto cut) {
+      constexpr bool CUT = decltype(cut)::value;
+      norm_sums_kernel<T, VEC, ACT, CUT><<<static_cast<unsigned>(blocks), threads, p.lds, s>>>(g, h);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      const size_t lds = std::max<size_t>(2 * h.gs, 2 * h.threads) * sizeof(float);
+      norm_grad_kernel<T, VEC, ACT, CUT><<<static_cast<unsigned>(blocks + more), threads, lds, s>>>(g, h, blocks);
+      return hipGetLastError();
+    });
   }
   const unsigned blocks = static_cast<unsigned>(h.slabs * h.across);
   if (p.kind == NormPlan::kTokens) {

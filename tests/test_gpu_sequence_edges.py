@@ -321,3 +321,43 @@ def test_norm_wide_groups_of_many_rows(fm):
     (5, 1, 1, 9001, "fp16", None), (1, 65, 2, 8193, "bf16", None)])
 def test_norm_wide_groups(fm, N, S, G, D, dtype, lengths):
     check_norm(fm, 45, N, S, G, D, dtype, "silu", lengths=lengths)
+
+
+@pytest.mark.parametrize("N,S,G,D,dtype,lengths", [
+    (300, 1, 1, 8200, "bf16", None), (100, 1, 3, 4100, "fp32", None), (520, 2, 2, 4097, "fp32", None),
+    (2, 300, 1, 16389, "bf16", [300, 11]), (1, 33, 2, 12290, "fp32", None), (3, 3, 1, 5121, "fp32", [0, 3, 1]),
+    (1, 1, 1, 40001, "fp16", None), (1, 700, 2, 8193, "fp16", None)])
+def test_norm_wide_groups_in_pieces_and_whole(fm, N, S, G, D, dtype, lengths):
+    """Groups wider than a workgroup's lanes: one workgroup each for a row or
+    two of many samples, else cut into pieces; last pieces of few channels and
+    of whole ones, several groups, padded samples."""
+    check_norm(fm, 46, N, S, G, D, dtype, "gelu", lengths=lengths)
+
+
+def test_norm_wide_groups_without_rows(fm):
+    x = torch.empty(3, 0, 9000, device="cuda")
+    y, stats = fm.group_norm(x, 1, save=True)
+    assert y.shape == x.shape and not stats.any()
+    _, dw, db = fm.group_norm_backward(x, x, stats, 1)
+    assert not dw.any() and not db.any()
+
+
+def test_norm_wide_groups_take_no_longer_than_others(fm):
+    """4000 rows of 5000 FP32 channels, as one group and as five: within ten
+    times of one another (one workgroup for all rows took a thousand times)."""
+    x = torch.randn(1, 4000, 5000, device="cuda")
+    times = []
+    for groups in (5, 1):
+        def work():
+            _, stats = fm.group_norm(x, groups, save=True)
+            fm.group_norm_backward(x, x, stats, groups)
+
+        work()
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(3):
+            work()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    assert times[1] < 10 * times[0]
