@@ -500,20 +500,20 @@ __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_n
   const NormShape sum_of = summed<CUT>(s, l);
   const GroupOf<VEC, false> group(l.c, s.D);
   const T *x = static_cast<const T *>(g.x) + r.n * g.x_sample + l.ch0 + l.c;
-  float mu[VEC], m2[VEC], count = 0.0f, bmu[VEC], bm2[VEC], bcount = 0.0f;  // of all tiles, of a block of them
+  float mu[VEC], m2[VEC], count = 0.0f;        // of a block of tiles
+  float fmu[VEC], fm2[VEC], fcount = 0.0f;     // of the blocks in front of it
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) mu[e] = m2[e] = bmu[e] = bm2[e] = 0.0f;
-  auto take_block = [&] {
-    const float all = count + bcount, share = all > 0.0f ? bcount / all : 0.0f, weight = count * share;
+  for (int e = 0; e < VEC; ++e) mu[e] = m2[e] = fmu[e] = fm2[e] = 0.0f;
+  // the block joined to those in front
+  auto join_front = [&] {
+    const float all = fcount + count, share = all > 0.0f ? count / all : 0.0f, weight = fcount * share;
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float d = bmu[e] - mu[e];
-      mu[e] = fmaf(d, share, mu[e]);
-      m2[e] += fmaf(d * d, weight, bm2[e]);
-      bmu[e] = bm2[e] = 0.0f;
+      const float d = mu[e] - fmu[e];
+      mu[e] = fmaf(d, share, fmu[e]);
+      m2[e] = fm2[e] + fmaf(d * d, weight, m2[e]);
     }
     count = all;
-    bcount = 0.0f;
   };
   if (l.in) {
     int turn = 0;
@@ -523,7 +523,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_n
       rows = rows < kTile ? rows : kTile;
 #pragma unroll
       for (int p = 0; p < kTile; ++p) v[p] = load_held<T, VEC>(x, t + p * s.ty, r.to, g.x_row);
-      const float k = static_cast<float>(rows), all = bcount + k, share = k / all, weight = bcount * share;
+      const float k = static_cast<float>(rows), all = count + k, share = k / all, weight = count * share;
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         float sum = 0.0f, sq = 0.0f;
@@ -535,17 +535,25 @@ __global__ __launch_bounds__(kNormThreads) void norm_ranges_kernel(fftmv_group_n
           const float d = p < rows ? v[p][e] - m : 0.0f;
           sq = fmaf(d, d, sq);
         }
-        const float d = m - bmu[e];
-        bmu[e] = fmaf(d, share, bmu[e]);
-        bm2[e] += fmaf(d * d, weight, sq);
+        const float d = m - mu[e];
+        mu[e] = fmaf(d, share, mu[e]);
+        m2[e] += fmaf(d * d, weight, sq);
       }
-      bcount = all;
+      count = all;
       if (++turn == kInTurn) {
-        take_block();
+        join_front();
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          fmu[e] = mu[e];
+          fm2[e] = m2[e];
+          mu[e] = m2[e] = 0.0f;
+        }
+        fcount = count;
+        count = 0.0f;
         turn = 0;
       }
     }
-    take_block();
+    if (fcount > 0.0f) join_front();
   }
   const int rows = r.to - r.from;
   float v[VEC];
@@ -585,7 +593,7 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
   // pairwise: (count, mean, sum of squared deviations)
   const int me = threadIdx.x % s.team, teams = blockDim.x / s.team;
   for (int k = threadIdx.x / s.team; k < l.ng; k += teams) {
-    float count = 0.0f, mu = 0.0f, sq = 0.0f;
+    float count = 0.0f, mu = 0.0f, sq = 0.0f;  // of the blocks of ranges so far
     auto join = [](float &count, float &mu, float &sq, float n, float m, float q) {
       const float all = count + n, share = all > 0.0f ? n / all : 0.0f, d = m - mu;
       sq += q + d * d * count * share;
@@ -610,7 +618,8 @@ __global__ __launch_bounds__(kNormThreads) void norm_apply_kernel(fftmv_group_no
                  v[j].x, v[j].y);
         }
       }
-      join(count, mu, sq, bcount, bmu, bsq);
+      if (b0 == me) count = bcount, mu = bmu, sq = bsq;
+      else join(count, mu, sq, bcount, bmu, bsq);
     }
     for (int m = 1; m < s.team; m <<= 1) {
       const float n = __shfl_xor(count, m), mm = __shfl_xor(mu, m), qq = __shfl_xor(sq, m);
