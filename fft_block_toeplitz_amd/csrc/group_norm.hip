@@ -101,8 +101,8 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
 
   // Single rows, or a few: Q samples at a time in a thread's registers, so
   // that a barrier serves all of them, and narrow ones side by side (forward
-  // and backward, bf16: 16000 x 5000 in 25 groups 86 and 177 us against 134 and
-  // 206 one by one, 20522 x 246 in 2 groups 16 and 32 against 26 and 78);
+  // and backward, bf16: 16000 x 5000 in 25 groups 82 and 180 us against 134 and
+  // 206 one by one, 20522 x 246 in 2 groups 15 and 29 against 26 and 78);
   // where that leaves too few workgroups for the CUs, the form below takes
   // them one by one.
   if (!split && rows <= 8) {
@@ -127,7 +127,7 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
   }
   // A sample's slab in registers: one row a thread, or up to eight (backward,
   // with twice the inputs: four). 400 samples of 100 rows of 8 x 64 bf16 take
-  // 31 and 56 us, split 42 and 64.
+  // 30 and 56 us, split 42 and 64.
   const int several = backward ? 4 : 8;
   for (int P = 1; !split && P <= several && p.kind == NormPlan::kSplit; P *= several) {
     const int most = P == 1 ? kNormThreads : kHeldThreads;
@@ -140,12 +140,12 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
         // one row a thread: for few rows, or where one takes most of the threads
         if (P == 1 && s.lx * s.S > 256 && alone <= 256) continue;
         // rows of less than 64 bytes waste the lines that they touch (200
-        // samples of 256 rows of 64 x 8 bf16: 112 and 197 us instead of 32 and 75)
+        // samples of 256 rows of 64 x 8 bf16: 112 and 197 us instead of 31 and 67)
         if (s.lx * v * es < 64 && s.slabs > 1) break;
         // narrower while workgroups are fewer than CUs, down to 128 bytes a row:
         // 4 samples of 64 rows of 16 x 64 bf16 6.6 us forward, whole slabs 7.6;
         // going on to twice the CUs, 16 of 64 rows of 32 x 64 15.0 instead of
-        // 11.9 backward
+        // 12.5 backward
         while (samples * s.slabs < 256 && s.gs > 1) {
           const int half = widest_slab(s.D, s.G, v, s.lx / 2);
           if (half == 0 || half * s.D * es < 128) break;
@@ -155,8 +155,8 @@ NormPlan norm_plan(int64_t samples, int64_t rows, int64_t channels, int64_t grou
         s.threads = std::min(threads, round64(static_cast<int64_t>(s.lx) * s.ty));
         // One row a thread is the quickest to answer, and cuts large inputs
         // into rows of little more than a line: 400 samples of 16 rows of 8 x 64
-        // bf16 take 9.8 and 16 us, 13 and 20 with several rows a thread; 1000
-        // of 12 rows of 16 x 64, 25 and 38 against 17 and 34.
+        // bf16 take 9.7 and 16 us, 13 and 20 with several rows a thread; 1000
+        // of 12 rows of 16 x 64, 25 and 38 against 17 and 35.
         if (P == 1 && alone <= 256 && samples * s.slabs > 4096) continue;
         // Sums by channel (groups that cut vectors) on too few CUs take longer
         // than a second launch: 1 x 256 rows of 50 x 100 bf16 22 us forward,

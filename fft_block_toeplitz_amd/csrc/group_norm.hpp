@@ -6,9 +6,10 @@
 // samples, single tokens); longer samples are read twice, once for the sums
 // and once to be written ("split": rows shared out over many workgroups).
 // The bound is memory traffic in all of them: 16000 tokens of 5000 channels in
-// bf16 take 86 us forward (3.7 TB/s) and 177 us backward (2.7 TB/s), 8 x 4096 x
-// 1024 fields 49 and 83 us (the split form's second reading, of 2 and 4 fields,
-// comes from the last cache: 2.7 and 2.4 TB/s of the bytes that must move).
+// bf16 take 85 us forward (3.8 TB/s) and 182 us backward (2.6 TB/s; FP32 136 and
+// 206, 4.7 TB/s), 8 x 4096 x 1024 fields 50 and 78 us (the split form's second
+// reading, of 2 and 4 fields, comes from the last cache: 2.7 and 2.6 TB/s of the
+// bytes that must move; FP32 86 and 133, 3.1 and 3.0 TB/s).
 //
 // A vector may cover channels of two groups (their width need not divide by
 // eight): then sums go through LDS per channel, otherwise per thread (WHOLE).

@@ -2,11 +2,12 @@
 // its forward and backward kernels.
 //
 // A workgroup takes one chunk of kChunk rows (time steps) of kLanes * VEC
-// channels: kSegs segments of kRows rows, by kLanes lanes of 16 bytes, so a
-// row of the chunk is 256 bytes and a thread keeps its kRows x VEC elements
-// in registers: each input is read once. (128-byte rows, half a wave each,
-// measured 10-25% slower: the memory system serves whole lines, and rows
-// rarely start on one.)
+// channels: kSegs segments of kRows rows, by kLanes lanes, and a thread keeps
+// its kRows x VEC elements in registers: each input is read once. A lane has 16
+// bytes of a row, so that a chunk's row is 256 bytes (128-byte rows measured
+// 10-25% slower: the memory system serves whole lines, and rows rarely start
+// on one); in the 16-bit backward pass, whose three inputs would not fit the
+// registers at that width, 8 bytes, and the row 128.
 //
 // A run of steps maps the state that enters it, h, to A h + H with A the
 // product of its decays. Three levels join these maps, each in a fixed order

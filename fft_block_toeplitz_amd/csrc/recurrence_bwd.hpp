@@ -8,9 +8,9 @@
 // rounded h is read at all.
 //
 // Memory traffic bounds it, and at this many workgroups the chunks' joins: 4 x
-// 4096 x 4096 bf16 take 205 us (3.3 TB/s of five fields; 145 with the joins left
-// out, which gives wrong values), 8 x 2000 x 5000 260 us, 8 x 1000 x 5000 FP32
-// 182 us (4.4 TB/s).
+// 4096 x 4096 bf16 take 212 us (3.2 TB/s of five fields; 145 with the joins left
+// out, which gives wrong values), 8 x 2000 x 5000 261 us, 8 x 1000 x 5000 FP32
+// 183 us (4.4 TB/s).
 #pragma once
 
 #include "recurrence.hpp"

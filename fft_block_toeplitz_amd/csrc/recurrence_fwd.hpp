@@ -1,9 +1,9 @@
 // Forward kernel of the gated linear recurrence.
 //
 // x and gate are read once, h written once, and memory traffic bounds it as far
-// as the chunks' joins let it: 4 x 4096 x 4096 bf16 take 115 us (3.5 TB/s of
+// as the chunks' joins let it: 4 x 4096 x 4096 bf16 take 116 us (3.5 TB/s of
 // three fields; 86 with the joins left out, which gives wrong values), 8 x 2000
-// x 5000 140 us, 8 x 1000 x 5000 FP32 118 us (4.1 TB/s). A series of one
+// x 5000 143 us, 8 x 1000 x 5000 FP32 122 us (3.9 TB/s). A series of one
 // chunk joins nothing.
 #pragma once
 

@@ -300,9 +300,8 @@ FFTMV_API int fftmv_condition(fftmv_plan_t plan, int iters, double *kappa, doubl
  * Structures are filled by the caller; unused pointers are NULL. Unless it
  * says otherwise a call allocates nothing, never synchronises, runs on
  * `stream`, and gives bitwise the same results for the same inputs. Outputs
- * must not overlap inputs. Element pointers need their type's alignment;
- * rows whose starts are multiples of 16 bytes (pointers and strides) and
- * whose channel count is a multiple of 16 bytes' worth take wider loads. */
+ * must not overlap inputs. Element pointers need their type's alignment, no
+ * more: rows may start at any element. */
 #define FFTMV_F32 0
 #define FFTMV_BF16 1
 #define FFTMV_F16 2
@@ -436,7 +435,8 @@ FFTMV_API int fftmv_recurrence_step(const fftmv_recurrence_step_t *r, hipStream_
  * weight, bias: [channels] FP32, NULL for ones / zeros. lengths (device
  * int32, clamped to 0..rows): sample n holds lengths[n] rows only; the
  * others enter no sum whatever they hold, and are written as zeros; a sample
- * that holds none has mean 0 and rstd 0.
+ * that holds none has mean 0 and rstd 0. Without rows (rows = 0) there are no
+ * fields and stats may be NULL in backward; dweight and dbias are zeros.
  *
  * Forward writes y and, where not NULL, stats [samples][groups][2] (mean,
  * rstd). Backward takes x, stats and the parameters as the forward had and
