@@ -208,10 +208,9 @@ def _output(out, like, inputs):
 
 def _wants_grad(*tensors):
     """Autograd is on and one of these requires a gradient."""
-    if _torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                return True
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return _torch.is_grad_enabled()
     return False
 
 
@@ -223,7 +222,7 @@ def _no_out(out):
 def _wrote(*tensors):
     """What a kernel has written in place, through its address, counts as written for autograd too: a graph that has
     saved it raises in its backward pass instead of going on with other values."""
-    _torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+    _torch._C._increment_version(tensors)  # torch.autograd.graph.increment_version without its type check
 
 
 class _On:
@@ -454,7 +453,10 @@ def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="compl
         return h.zero_()
     fftmv_recurrence_step(_STEP.pack(B, C, places, dtype, *kinds, 0, xp, xs, gp, gs, state.data_ptr(),
                                      max(ss[0], C), sp, h.data_ptr(), C), _current_stream(x.get_device()))
-    _wrote(state, out)
+    if out is None:
+        _wrote(state)
+    else:
+        _wrote(state, out)
     return h
 
 
