@@ -279,8 +279,6 @@ class _workspace:
 
     def __enter__(self):
         _, few, many = self.sizes
-        if many == 0:
-            return 0, 0, 0, 0, 0
         new = lambda n: _torch.zeros(n, dtype=_torch.uint8, device=self.like.device)  # noqa: E731
         if _torch.cuda.is_current_stream_capturing():
             a, b = self.held = new(few), new(many)
@@ -309,7 +307,7 @@ class _workspace:
         self.held = None
 
 
-_NO_WORKSPACE = contextlib.nullcontext((0, 0, 0, 0, 0))
+_NO_WORKSPACE = contextlib.nullcontext((0, 0, 0, 0, 0))  # of a call whose sizes ask for none
 
 
 def _sequences(x, lengths, offsets):

@@ -65,8 +65,9 @@ def test_threads_of_one_stream_share_a_workspace_safely(shared):
 
 
 def test_a_call_without_a_workspace_takes_none(shared):
-    with sq._workspace((0, 0, 0), 0, 0, shared) as w:
-        assert tuple(w) == (0, 0, 0, 0, 0)
+    for _ in range(2):
+        with sq._NO_WORKSPACE as (*memory, call):
+            assert memory == [0, 0, 0, 0] and call == 0
     assert not sq._workspaces
 
 
