@@ -50,7 +50,9 @@ EXPORTS = ("fftmv_setup", "fftmv_apply", "fftmv_apply_adjoint", "fftmv_apply_scr
            "fftmv_predict", "fftmv_pareto_front", "fftmv_select_precision", "fftmv_condition", "fftmv_version",
            "fftmv_recurrence_sizes", "fftmv_recurrence_forward", "fftmv_recurrence_backward",
            "fftmv_recurrence_step", "fftmv_group_norm_workspace", "fftmv_group_norm_forward",
-           "fftmv_group_norm_backward")
+           "fftmv_group_norm_backward",
+           "fftmv_delta_rule_sizes", "fftmv_delta_rule_forward", "fftmv_delta_rule_backward", "fftmv_delta_rule_step",
+           "fftmv_qk_norm_workspace", "fftmv_qk_norm_forward", "fftmv_qk_norm_backward")
 
 
 def FFTMV_FP32(direction: int, stage: int) -> int:
@@ -373,3 +375,4 @@ def _hip_memcpy_d2d(dst: int, src: int, nbytes: int) -> None:
 # the sequence operators on torch tensors
 from .sequence import (group_norm, group_norm_backward, recurrence, recurrence_backward,  # noqa: E402,F401
                        recurrence_step)
+from .delta import delta_rule, delta_rule_backward, delta_rule_step, qk_norm, qk_norm_backward  # noqa: E402,F401

@@ -17,14 +17,17 @@ SOURCES = [os.path.join(HERE, "csrc", f)
                      "recurrence_bwd_bf16.hip", "recurrence_bwd_f16.hip", "recurrence_step.hip",
                      "group_norm_fwd_f32.hip", "group_norm_fwd_bf16.hip", "group_norm_fwd_f16.hip",
                      "group_norm_bwd_f32.hip", "group_norm_bwd_bf16.hip", "group_norm_bwd_f16.hip", "group_norm.hip",
-                     "plan.cpp", "precision.cpp", "sequence.cpp")]
+                     "delta_rule_fwd_f32.hip", "delta_rule_fwd_bf16.hip", "delta_rule_fwd_f16.hip",
+                     "delta_rule_bwd_f32.hip", "delta_rule_bwd_bf16.hip", "delta_rule_bwd_f16.hip",
+                     "delta_rule_step.hip", "qk_norm.hip", "plan.cpp", "precision.cpp", "sequence.cpp", "delta.cpp")]
 # measurement kernels of the benchmark (memory ceilings): a library of their own
 CEILING_SRC = os.path.join(HERE, "csrc", "ceiling.hip")
 CEILING_LIB = os.path.join(HERE, "libfftmv_ceiling.so")
 HEADERS = [os.path.join(ROOT, "include", "fftmv.h")] + [
     os.path.join(HERE, "csrc", f) for f in ("common.hpp", "internal.hpp", "fft_device.hpp", "fft_fixed.hpp",
                                             "fft_generic.hpp", "sequence.hpp", "recurrence.hpp", "recurrence_fwd.hpp",
-                                            "recurrence_bwd.hpp", "group_norm.hpp")]
+                                            "recurrence_bwd.hpp", "group_norm.hpp", "checks.hpp", "delta_rule.hpp",
+                                            "delta_rule_fwd.hpp", "delta_rule_bwd.hpp", "qk_norm.hpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

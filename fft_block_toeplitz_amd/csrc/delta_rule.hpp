@@ -1,0 +1,695 @@
+// The gated delta rule in runs of kRun = 64 steps: what its kernels share.
+//
+// Within a run that the state S enters, with G_i the sum of log a up to step i,
+// E_ij = exp(G_i - G_j) and
+//   B_ij = E_ij k_i.k_j  (j < i),      P_ij = scale E_ij q_i.k_j  (j <= i),
+//   T    = (1 + diag(b) B)^-1          (unit lower triangular),
+// the corrections U (row i is what step i writes under its key) are
+//   U  = T diag(b) (V - diag(e^G) K S)
+//   Y  = scale diag(e^G) Q S + P U
+//   S' = e^{G_last} S + (diag(e^{G_last - G}) K)^T U
+// so that a run is products of matrices, and only K S, T (..) and K^T U wait for
+// the run before. T, P and the factors need no state: a kernel of their own
+// computes them for all runs at once.
+//
+// Products go to the bf16 matrix instructions with FP32 sums. An FP32 operand
+// is cut into bf16 parts, the leading 8 bits, the next 8, the last 8: three parts
+// hold all 24 bits. bf16 inputs are one part, fp16 inputs two, both exact. What
+// becomes an FP32 output (the states, gradients of h0) takes all products of
+// parts down to 2^-24; what becomes a 16-bit output, products down to 2^-16,
+// far under that rounding. (An FP32 matrix instruction has a sixteenth of the rate:
+// three parts against one exact operand are 5.3 times as fast, six products 2.7.)
+//
+// Layouts of a 16x16x32 product in a wave: operands have index lane % 16 and 8
+// slots of the contracted axis, the result column lane % 16 and rows 4 (lane /
+// 16) + 0..3. Which rows of the contracted axis the slots stand for is free as
+// long as both operands agree, so a result is the next product's operand as it
+// lies in the registers: slots 0..3 from one 16-row tile, 4..7 from the next.
+#pragma once
+
+#include "common.hpp"
+#include "internal.hpp"
+#include "sequence.hpp"
+
+namespace fftmv {
+
+hipError_t launch_delta_forward_f32(const fftmv_delta_rule_t &r, hipStream_t s);
+hipError_t launch_delta_forward_bf16(const fftmv_delta_rule_t &r, hipStream_t s);
+hipError_t launch_delta_forward_f16(const fftmv_delta_rule_t &r, hipStream_t s);
+hipError_t launch_delta_backward_f32(const fftmv_delta_rule_t &r, hipStream_t s);
+hipError_t launch_delta_backward_bf16(const fftmv_delta_rule_t &r, hipStream_t s);
+hipError_t launch_delta_backward_f16(const fftmv_delta_rule_t &r, hipStream_t s);
+hipError_t launch_delta_step(const fftmv_delta_rule_step_t &r, hipStream_t s);
+
+constexpr int kRun = FFTMV_DELTA_RUN;
+constexpr int kTiles = kRun / 16;
+static_assert(kRun == 64, "one lane for each step of a run");
+constexpr int kFrags = 6;  // operands of 16 rows x 32 slots that a triangle of kRun holds something in
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// bf16 parts of an element, exact; and of an FP32 value next to it: kept down
+// to 2^-24 (kFull) or, for results of 16 bits, 2^-16
+template <typename T>
+constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
+template <>
+inline constexpr int kParts<f16> = 2;
+constexpr int kFull = 3;
+template <typename T>
+constexpr int kOut = sizeof(T) == 4 ? 3 : 2;
+
+// ------------------------------------------------------------------ operands
+template <int N>
+struct Cut {
+  u32x4 p[N];  // 8 slots of each part
+};
+
+__device__ __forceinline__ uint32_t high_halves(uint32_t lo, uint32_t hi) {
+  return __builtin_amdgcn_perm(hi, lo, 0x07060302);
+}
+
+// Eight values as N parts. All but the last are cut off, which leaves the rest
+// exact; the last is rounded (exact where the bits end there).
+template <int N>
+__device__ __forceinline__ Cut<N> cut(const float (&x)[8]) {
+  Cut<N> c;
+  float r[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = x[e];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (n == N - 1) {
+      bf16x8 b;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e] = static_cast<__bf16>(r[e]);
+      c.p[n] = __builtin_bit_cast(u32x4, b);
+    } else {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t lo = __float_as_uint(r[2 * w]), hi = __float_as_uint(r[2 * w + 1]);
+        c.p[n][w] = high_halves(lo, hi);
+        r[2 * w] -= __uint_as_float(lo & 0xffff0000u);
+        r[2 * w + 1] -= __uint_as_float(hi & 0xffff0000u);
+      }
+    }
+  }
+  return c;
+}
+
+// Two result tiles of 16 rows as the next product's operand.
+template <int N>
+__device__ __forceinline__ Cut<N> cut_tiles(f32x4 first, f32x4 second) {
+  const float x[8] = {first[0], first[1], first[2], first[3], second[0], second[1], second[2], second[3]};
+  return cut<N>(x);
+}
+
+// c += a b over the parts' products down to 2^(-8 LIMIT), the small ones first.
+template <int LIMIT, int NA, int NB>
+__device__ __forceinline__ void multiply(f32x4 &c, const Cut<NA> &a, const Cut<NB> &b) {
+#pragma unroll
+  for (int s = LIMIT - 1; s >= 0; --s) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int j = s - i;
+      if (j >= 0 && j < NB)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.p[i]),
+                                                    __builtin_bit_cast(bf16x8, b.p[j]), c, 0, 0, 0);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- fields
+template <typename T>
+__device__ __forceinline__ T *head_row(const fftmv_heads_t &f, int64_t b, int64_t t, int64_t n) {
+  return static_cast<T *>(f.data) + b * f.batch + t * f.step + n * f.head;
+}
+
+// Elements c..c+7 of a row of n, those behind it as zeros. Exact.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int c, int n, float (&x)[8]) {
+  if (c + 8 <= n) {
+    constexpr int V = kVec<T>;
+#pragma unroll
+    for (int h = 0; h < 8 / V; ++h) {
+      const Vec<T, V> v = load_vec<T, V>(p + c + h * V);
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[h * V + e] = v[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = c + e < n ? static_cast<float>(p[c + e]) : 0.0f;
+  }
+}
+// The same as an operand; bf16 needs no conversion.
+template <typename T>
+__device__ __forceinline__ Cut<kParts<T>> load_cut(const T *p, int c, int n, bool held) {
+  if constexpr (kParts<T> == 1) {
+    Cut<1> r;
+    r.p[0] = u32x4{0, 0, 0, 0};
+    if (held) {
+      if (c + 8 <= n) {
+        const u32x4_any w = *reinterpret_cast<const u32x4_any *>(p + c);
+        r.p[0] = u32x4{w[0], w[1], w[2], w[3]};
+      } else {
+        float x[8];
+        load8(p, c, n, x);
+        r = cut<1>(x);
+      }
+    }
+    return r;
+  } else {
+    float x[8] = {};
+    if (held) load8(p, c, n, x);
+    return cut<kParts<T>>(x);
+  }
+}
+
+// Eight FP32 values as N parts.
+template <int N>
+__device__ __forceinline__ Cut<N> load_wide(const float *p, int c, int n, bool held) {
+  float x[8] = {};
+  if (held) load8(p, c, n, x);
+  return cut<N>(x);
+}
+
+// The steps of sequence b: flat rows (packed) or rows of its own, and the
+// number of its first run.
+struct Span {
+  int64_t batch, row, run;
+  int len;
+};
+inline __host__ __device__ int64_t runs_of(int64_t steps) { return (steps + kRun - 1) / kRun; }
+inline __host__ __device__ int64_t delta_runs(int64_t batch, int64_t steps, bool packed) {
+  return steps == 0 ? 0 : packed ? steps / kRun + batch : batch * runs_of(steps);
+}
+template <typename I>
+__device__ __forceinline__ I clamp_to(I v, I most) {
+  return v < 0 ? 0 : v > most ? most : v;
+}
+__device__ __forceinline__ Span span_of(const fftmv_delta_rule_t &r, int64_t b) {
+  const int steps = static_cast<int>(r.steps);
+  if (r.offsets) {
+    const int lo = clamp_to(r.offsets[b], steps), hi = clamp_to(r.offsets[b + 1], steps);
+    return {0, lo, lo / kRun + b, hi > lo ? hi - lo : 0};
+  }
+  return {b, 0, b * runs_of(steps), r.lengths ? clamp_to(r.lengths[b], steps) : steps};
+}
+// The sequence of run slot i and the run's first step in it, -1 where the slot
+// holds no run. Packed: sequences begin at slots offsets[b] / kRun + b, which
+// ascend; slots between one's last run and the next one's first stay empty.
+struct Slot {
+  int64_t b;
+  int first;
+};
+__device__ __forceinline__ Slot slot_of(const fftmv_delta_rule_t &r, int64_t i) {
+  const int steps = static_cast<int>(r.steps);
+  if (!r.offsets) {
+    const int64_t n = runs_of(steps), b = i / n;
+    return {b, static_cast<int>(i - b * n) * kRun};
+  }
+  int64_t lo = 0, hi = r.batch - 1;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) / 2;
+    if (clamp_to(r.offsets[mid], steps) / kRun + mid <= i)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int64_t place = i - (clamp_to(r.offsets[lo], steps) / kRun + lo);
+  return {lo, place < 0 || place * kRun > INT32_MAX ? -1 : static_cast<int>(place) * kRun};
+}
+
+// ---------------------------------------------------------------- workspace
+// What the first kernel leaves for each run slot and head.
+struct Factors {
+  double sum[kRun];  // G_i
+  float into[kRun], out[kRun], rate[kRun];  // e^{G_i}, e^{G_last - G_i}, b_i; into[kRun - 1] is the whole run's decay
+};
+// Fragments (one part of an operand, 64 lanes x 16 bytes) of: T diag(b) and P
+// forward; T diag(b), T^T and P^T backward.
+template <typename T, bool BACK>
+struct Triangles {
+  static constexpr int kT = 0, kTParts = BACK ? kOut<T> : kFull;
+  static constexpr int kP = kT + kFrags * kTParts, kPParts = BACK ? kFull : kOut<T>;
+  static constexpr int kTt = kP + kFrags * kPParts, kTtParts = BACK ? kFull : 0;
+  static constexpr int kAll = kTt + kFrags * kTtParts;
+  static constexpr size_t kBytes = size_t{kAll} * kWave * sizeof(u32x4);
+};
+// Fragment of rows tile m and slots 32 s.. of a lower or upper triangle.
+__host__ __device__ constexpr int lower_frag(int m, int s) { return m < 2 ? m : 2 * m - 2 + s; }
+__host__ __device__ constexpr int upper_frag(int m, int s) { return m < 2 ? 2 * m + s : m + 2; }
+__host__ __device__ constexpr bool in_lower(int m, int s) { return s == 0 || m >= 2; }
+__host__ __device__ constexpr bool in_upper(int m, int s) { return s == 1 || m < 2; }
+
+template <int N>
+__device__ __forceinline__ Cut<N> load_frag(const u32x4 *f, int frag, int parts, int lane) {
+  Cut<N> c;
+#pragma unroll
+  for (int n = 0; n < N; ++n) c.p[n] = f[(frag * parts + n) * kWave + lane];
+  return c;
+}
+
+// The workspace of a call in its parts.
+struct DeltaWorkspace {
+  Factors *factors;
+  u32x4 *triangles;
+  float *grads;  // backward: the gradients of the states behind each run, [runs][heads][keys][values]
+};
+inline size_t delta_triangle_bytes(int dtype, bool back) {
+  const size_t per_part = size_t{kFrags} * kWave * sizeof(u32x4);
+  const size_t out = dtype == FFTMV_F32 ? 3 : 2;
+  return per_part * (back ? out + 2 * kFull : kFull + out);
+}
+inline size_t delta_workspace(int64_t runs, int64_t heads, int64_t keys, int64_t values, int dtype, bool back,
+                              void *at = nullptr, DeltaWorkspace *w = nullptr) {
+  const size_t n = static_cast<size_t>(runs) * heads;
+  const size_t factors = n * sizeof(Factors), triangles = n * delta_triangle_bytes(dtype, back);
+  const size_t grads = back ? n * keys * values * sizeof(float) : 0;
+  static_assert(sizeof(Factors) % 16 == 0, "fragments are 16-byte aligned");
+  if (w) {
+    char *p = static_cast<char *>(at);
+    w->factors = reinterpret_cast<Factors *>(p);
+    w->triangles = reinterpret_cast<u32x4 *>(p + factors);
+    w->grads = reinterpret_cast<float *>(p + factors + triangles);
+  }
+  return factors + triangles + grads;
+}
+
+// ------------------------------------------------------ gates of 64 steps
+// log a, bounded below: e^-1e5 is zero, and a sum with it still tells the others
+// apart in 64 bits.
+template <int DUMMY = 0>
+__device__ __forceinline__ float log_decay(int decay, float g) {
+  float l = g;
+  if (decay == FFTMV_DECAY_SIGMOID) l = fminf(g, 0.0f) - log1pf(expf(-fabsf(g)));
+  if (g != g) l = g;
+  return l < -1e5f ? -1e5f : l;
+}
+__device__ __forceinline__ float rate_of(int rate, float v) {
+  return rate == FFTMV_RATE_SIGMOID ? 1.0f / (1.0f + expf(-v)) : v;
+}
+__device__ __forceinline__ double lane_sums(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const double o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// ------------------------------------------------------ T, P and the factors
+// One wave for each run slot and head. The inverse goes by blocks: a lane
+// solves one column of a diagonal block of 16 by substitution (products of
+// powers would lose what cancels where keys are alike), and the blocks below
+// are joined in FP32 products, T_21 = -T_22 A_21 T_11.
+constexpr int kTri = kRun + 4;  // floats between rows of the triangle in LDS
+
+template <bool TRANSPOSED>
+__device__ __forceinline__ f32x4 load4(const float *a, int row, int col) {
+  if constexpr (TRANSPOSED) return f32x4{a[col * kTri + row], a[(col + 1) * kTri + row], a[(col + 2) * kTri + row], a[(col + 3) * kTri + row]};
+  const float4 v = *reinterpret_cast<const float4 *>(a + row * kTri + col);
+  return f32x4{v.x, v.y, v.z, v.w};
+}
+
+// c += L X for a 16x16 block of LDS (rows at r, contracted columns at k) and X in a result's layout.
+__device__ __forceinline__ void block_multiply(f32x4 &c, const float *a, int r, int k, f32x4 x, int lane) {
+  const f32x4 l = load4<false>(a, r + lane % 16, k + 4 * (lane / 16));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(l[i], x[i], c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 block_load(const float *a, int r, int c, int lane) {
+  return load4<true>(a, c + lane % 16, r + 4 * (lane / 16));
+}
+__device__ __forceinline__ void block_store(float *a, int r, int c, f32x4 v, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[(r + 4 * (lane / 16) + i) * kTri + c + lane % 16] = v[i];
+}
+
+// Turns the strictly lower A in LDS into (1 + A)^-1 (its upper blocks are not written).
+__device__ __forceinline__ void invert(float *a, int lane) {
+  {  // the diagonal blocks: block lane / 16, column lane % 16
+    const int b = lane / 16 * 16, col = lane % 16;
+    float x[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float s = r == col ? 1.0f : 0.0f;
+#pragma unroll
+      for (int k = 0; k < (r + 3) / 4; ++k) {
+        const f32x4 v = load4<false>(a, b + r, b + 4 * k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * k + i < r) s = fmaf(-v[i], x[4 * k + i], s);
+      }
+      x[r] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) a[(b + r) * kTri + b + col] = x[r];
+    __syncthreads();
+  }
+#pragma unroll
+  for (int b = 0; b < kRun; b += 32) {
+    f32x4 y = {0, 0, 0, 0}, t = {0, 0, 0, 0};
+    block_multiply(y, a, b + 16, b, block_load(a, b, b, lane), lane);
+    block_multiply(t, a, b + 16, b + 16, -y, lane);
+    __syncthreads();
+    block_store(a, b + 16, b, t, lane);
+    __syncthreads();
+  }
+  f32x4 y[2][2], t[2][2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      y[r][c] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = c; k < 2; ++k) block_multiply(y[r][c], a, 32 + 16 * r, 16 * k, block_load(a, 16 * k, 16 * c, lane), lane);
+    }
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      t[r][c] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k <= r; ++k) block_multiply(t[r][c], a, 32 + 16 * r, 32 + 16 * k, -y[k][c], lane);
+    }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) block_store(a, 32 + 16 * r, 16 * c, t[r][c], lane);
+  __syncthreads();
+}
+
+// Zeros in the rows of `n` elements that belong to no sequence: those of a
+// padded run behind its length; of the packed axis, rows 64 i.. outside all.
+template <typename T>
+__device__ __forceinline__ void clear_rows(const fftmv_delta_rule_t &r, const fftmv_heads_t &f, int64_t slot,
+                                           int64_t b, int first, int64_t head, int n, int lane) {
+  if (!f.data) return;
+  const int steps = static_cast<int>(r.steps);
+  if (r.offsets) {
+    const int lo = clamp_to(r.offsets[0], steps), hi = clamp_to(r.offsets[r.batch], steps);
+    const int64_t at = slot * kRun;
+    for (int64_t t = at; t < at + kRun && t < steps; ++t) {
+      if (t >= lo && t < hi) continue;
+      T *row = head_row<T>(f, 0, t, head);
+      for (int c = lane; c < n; c += kWave) row[c] = static_cast<T>(0.0f);
+    }
+  } else if (r.lengths) {
+    const int len = clamp_to(r.lengths[b], steps);
+    for (int t = max(first, len); t < min(first + kRun, steps); ++t) {
+      T *row = head_row<T>(f, b, t, head);
+      for (int c = lane; c < n; c += kWave) row[c] = static_cast<T>(0.0f);
+    }
+  }
+}
+
+template <typename T, int KEYS, bool BACK>
+__global__ __launch_bounds__(kWave) void delta_factors_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
+  __shared__ __align__(16) float tri[kRun * kTri];
+  __shared__ double total[kRun];
+  __shared__ float rates[kRun];
+  using Tri = Triangles<T, BACK>;
+  const int lane = threadIdx.x, x = lane % 16, g = lane / 16;
+  const int64_t slot = blockIdx.x / r.heads, head = blockIdx.x % r.heads, at = slot * r.heads + head;
+  const int64_t key_head = head / (r.heads / r.key_heads);
+  const Slot where = slot_of(r, slot);
+  if constexpr (BACK) {
+    clear_rows<T>(r, r.dv, slot, where.b, where.first, head, static_cast<int>(r.values), lane);
+    clear_rows<T>(r, r.dgate, slot, where.b, where.first, head, 1, lane);
+    clear_rows<T>(r, r.dbeta, slot, where.b, where.first, head, 1, lane);
+    if (head % (r.heads / r.key_heads) == 0) {
+      clear_rows<T>(r, r.dq, slot, where.b, where.first, key_head, static_cast<int>(r.keys), lane);
+      clear_rows<T>(r, r.dk, slot, where.b, where.first, key_head, static_cast<int>(r.keys), lane);
+    }
+  } else {
+    clear_rows<T>(r, r.y, slot, where.b, where.first, head, static_cast<int>(r.values), lane);
+  }
+  if (where.first < 0) return;
+  const Span span = span_of(r, where.b);
+  const int n = min(kRun, span.len - where.first);  // steps of this run
+  if (n <= 0) return;
+  const int64_t row = span.row + where.first;
+
+  // gates: lane i has step i; steps behind the last leave the state as it is
+  {
+    const bool held = lane < n;
+    const float gate = held ? static_cast<float>(*head_row<T>(r.gate, span.batch, row + lane, head)) : 0.0f;
+    const float beta = held ? static_cast<float>(*head_row<T>(r.beta, span.batch, row + lane, head)) : 0.0f;
+    const double sum = lane_sums(held ? static_cast<double>(log_decay(r.decay, gate)) : 0.0, lane);
+    const double last = __shfl(sum, kRun - 1);
+    Factors &f = w.factors[at];
+    f.into[lane] = expf(static_cast<float>(sum));
+    f.out[lane] = expf(static_cast<float>(last - sum));
+    f.sum[lane] = sum;
+    f.rate[lane] = rates[lane] = held ? rate_of(r.rate, beta) : 0.0f;
+    total[lane] = sum;
+  }
+
+  // rows of keys, as both operands of K K^T and K Q^T
+  constexpr int S = KEYS / 32, NP = kParts<T>;
+  const int keys = static_cast<int>(r.keys);
+  Cut<NP> k[kTiles][S];
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      k[m][s] = load_cut(head_row<T>(r.k, span.batch, row + min(16 * m + x, n - 1), key_head), 32 * s + 8 * g, keys,
+                         16 * m + x < n);
+  __syncthreads();
+  auto decay = [&](int i, int j) { return expf(static_cast<float>(total[i] - total[j])); };
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int c = 0; c <= m; ++c) {
+      f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < S; ++s) multiply<kFull>(p, k[m][s], k[c][s]);
+      const int j = 16 * c + x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * m + 4 * g + i;
+        tri[t * kTri + j] = j < t ? rates[t] * decay(t, j) * p[i] : 0.0f;
+      }
+    }
+  __syncthreads();
+  invert(tri, lane);
+
+  u32x4 *out = w.triangles + at * Tri::kAll * kWave;
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (in_lower(m, s)) {  // T diag(b): row 16 m + x, slots of the columns
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int i = 16 * m + x, j = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
+          v[e] = j <= i ? tri[i * kTri + j] * rates[j] : 0.0f;
+        }
+        const auto c = cut<Tri::kTParts>(v);
+#pragma unroll
+        for (int q = 0; q < Tri::kTParts; ++q) out[(Tri::kT + lower_frag(m, s) * Tri::kTParts + q) * kWave + lane] = c.p[q];
+      }
+      if constexpr (BACK) {
+        if (in_upper(m, s)) {  // T^T
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int j = 16 * m + x, i = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
+            v[e] = j <= i ? tri[i * kTri + j] : 0.0f;
+          }
+          const auto c = cut<Tri::kTtParts>(v);
+#pragma unroll
+          for (int q = 0; q < Tri::kTtParts; ++q) out[(Tri::kTt + upper_frag(m, s) * Tri::kTtParts + q) * kWave + lane] = c.p[q];
+        }
+      }
+    }
+
+  // P as the operand that it becomes: forward its rows at lane % 16 and columns
+  // as slots, so the tile is computed as K Q^T; backward P^T, as Q K^T
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m) {
+    Cut<NP> q[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      q[s] = load_cut(head_row<T>(r.q, span.batch, row + min(16 * m + x, n - 1), key_head), 32 * s + 8 * g, keys,
+                      16 * m + x < n);
+    if constexpr (!BACK) {
+      f32x4 p[kTiles];
+#pragma unroll
+      for (int c = 0; c < kTiles; ++c) {
+        p[c] = f32x4{0, 0, 0, 0};
+        if (c > m) continue;
+#pragma unroll
+        for (int s = 0; s < S; ++s) multiply<kOut<T>>(p[c], k[c][s], q[s]);
+        const int i = 16 * m + x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = 16 * c + 4 * g + e;
+          p[c][e] = j <= i ? r.scale * decay(i, j) * p[c][e] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (in_lower(m, s)) {
+          const auto c = cut_tiles<Tri::kPParts>(p[2 * s], p[2 * s + 1]);
+#pragma unroll
+          for (int a = 0; a < Tri::kPParts; ++a) out[(Tri::kP + lower_frag(m, s) * Tri::kPParts + a) * kWave + lane] = c.p[a];
+        }
+    } else {
+      // row tile m of Q gives slots tile m of P^T for all columns c <= m: kept in LDS until both tiles of a slot are there
+#pragma unroll
+      for (int c = 0; c <= m; ++c) {
+        f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < S; ++s) multiply<kFull>(p, q[s], k[c][s]);
+        const int j = 16 * c + x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 16 * m + 4 * g + e;
+          p[e] = j <= i ? r.scale * decay(i, j) * p[e] : 0.0f;
+        }
+        if (c == 0 && m == 0) __syncthreads();
+        block_store(tri, 16 * m, 16 * c, p, lane);
+      }
+    }
+  }
+  if constexpr (BACK) {
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (in_upper(m, s)) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int j = 16 * m + x, i = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
+            v[e] = j <= i ? tri[i * kTri + j] : 0.0f;
+          }
+          const auto c = cut<Tri::kPParts>(v);
+#pragma unroll
+          for (int q = 0; q < Tri::kPParts; ++q) out[(Tri::kP + upper_frag(m, s) * Tri::kPParts + q) * kWave + lane] = c.p[q];
+        }
+  }
+}
+
+// ------------------------------------------------------ tiles of keys in LDS
+// Rows of kRun steps, KEYS elements from `from` on (zeros behind the last), parts
+// one behind the other; 16 bytes between rows keep them off each other's banks.
+template <int KEYS>
+constexpr int kTileRow = KEYS + 8;
+
+template <typename T, int KEYS, int THREADS>
+__device__ __forceinline__ void fill_tile(uint16_t *tile, const fftmv_heads_t &f, int64_t b, int64_t row, int n,
+                                          int64_t head, int width, int from = 0) {
+  constexpr int G = KEYS / 8, NP = kParts<T>;
+#pragma unroll
+  for (int u = threadIdx.x; u < kRun * G; u += THREADS) {
+    const int t = u / G, c = u % G * 8;
+    const Cut<NP> v = load_cut(head_row<T>(f, b, row + min(t, n - 1), head), from + c, width, t < n);
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+      *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * kTileRow<KEYS> + c) = v.p[p];
+  }
+}
+// Operand with index row 16 m + lane % 16 and slots of elements 32 s + 8 g ...
+template <int KEYS, int NP>
+__device__ __forceinline__ Cut<NP> tile_rows(const uint16_t *tile, int m, int s, int lane) {
+  Cut<NP> c;
+#pragma unroll
+  for (int p = 0; p < NP; ++p)
+    c.p[p] = *reinterpret_cast<const u32x4 *>(tile + (p * kRun + 16 * m + lane % 16) * kTileRow<KEYS> + 32 * s + 8 * (lane / 16));
+  return c;
+}
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+// Four rows of one column for each lane: within 16 lanes, lane l reads 4
+// elements of row l / 4 and receives column l of the 4 x 16 that they read.
+__device__ __forceinline__ s16x4 transposed4(const uint16_t *p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p));
+}
+__device__ __forceinline__ u32x4 join8(s16x4 a, s16x4 b) {
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return __builtin_bit_cast(u32x4, v);
+}
+// Key that row (lane group g, i) of the state's tile t stands for: eight
+// neighbouring keys of a lane then lie in the tiles 2 s and 2 s + 1, the slots
+// of tile_rows.
+__host__ __device__ constexpr int key_of(int t, int g, int i) { return 32 * (t / 2) + 8 * g + 4 * (t % 2) + i; }
+// Operand with index the keys of state tile t and slots of the steps as results hold them.
+template <int KEYS, int NP>
+__device__ __forceinline__ Cut<NP> tile_columns(const uint16_t *tile, int t, int s, int lane) {
+  Cut<NP> c;
+  const int l = lane % 16, row = 32 * s + 4 * (lane / 16) + l / 4, col = key_of(t, l % 4, 0);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const uint16_t *q = tile + (p * kRun + row) * kTileRow<KEYS> + col;
+    c.p[p] = join8(transposed4(q), transposed4(q + 16 * kTileRow<KEYS>));
+  }
+  return c;
+}
+
+// Operand with index columns col.. (lane % 16) and slots of rows row + 8 g + 0..7 (GAP 4), or as results hold them (GAP 16).
+template <int ROW, int NP, int GAP>
+__device__ __forceinline__ Cut<NP> plain_columns(const uint16_t *tile, int row, int col, int lane) {
+  Cut<NP> c;
+  const int l = lane % 16;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const uint16_t *q = tile + (p * kRun + row + (GAP == 4 ? 8 : 4) * (lane / 16) + l / 4) * ROW + col + 4 * (l % 4);
+    c.p[p] = join8(transposed4(q), transposed4(q + GAP * ROW));
+  }
+  return c;
+}
+
+// Rows 16 m + 4 g + 0..3 of column col + lane % 16, as results hold them.
+template <int ROW, int NP>
+__device__ __forceinline__ f32x4 tile_values(const uint16_t *tile, int m, int col, int lane) {
+  f32x4 v = {0, 0, 0, 0};
+  const int l = lane % 16;
+#pragma unroll
+  for (int p = NP - 1; p >= 0; --p) {
+    const s16x4 q = transposed4(tile + (p * kRun + 16 * m + 4 * (lane / 16) + l / 4) * ROW + col + 4 * (l % 4));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(q[i])) << 16);
+  }
+  return v;
+}
+// Keeps the scheduler from moving work across: it would start on later loads and products and spill.
+__device__ __forceinline__ void part_done() { __builtin_amdgcn_sched_barrier(0); }
+
+// The same number, of unknown origin: addresses and conditions made from it are
+// computed where they are used. The compiler would else compute those of a whole
+// loop's body in front of the loop, hundreds of them, and spill.
+__device__ __forceinline__ int afresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Steps 16 m + 4 g + 0..3 of one value column, zeros where nothing is held.
+template <typename T>
+__device__ __forceinline__ f32x4 load_column(const fftmv_heads_t &f, int64_t b, int64_t row, int n, int64_t head,
+                                             int m, int g, int col, bool inside) {
+  f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 16 * m + 4 * g + i;
+    if (inside && t < n) v[i] = static_cast<float>(head_row<T>(f, b, row + t, head)[col]);
+  }
+  return v;
+}
+
+template <typename F>
+hipError_t by_keys(int64_t keys, F f) {
+  if (keys <= 32) return f(Const<32>{});
+  if (keys <= 64) return f(Const<64>{});
+  return f(Const<128>{});
+}
+
+}  // namespace fftmv

@@ -1,0 +1,6 @@
+// The delta rule's backward pass for bf16 elements.
+#include "delta_rule_bwd.hpp"
+
+namespace fftmv {
+hipError_t launch_delta_backward_bf16(const fftmv_delta_rule_t &r, hipStream_t s) { return launch_delta_backward<bf16>(r, s); }
+}  // namespace fftmv

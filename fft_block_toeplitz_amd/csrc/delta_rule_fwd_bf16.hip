@@ -1,0 +1,6 @@
+// The delta rule's forward pass for bf16 elements.
+#include "delta_rule_fwd.hpp"
+
+namespace fftmv {
+hipError_t launch_delta_forward_bf16(const fftmv_delta_rule_t &r, hipStream_t s) { return launch_delta_forward<bf16>(r, s); }
+}  // namespace fftmv

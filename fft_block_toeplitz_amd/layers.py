@@ -1,6 +1,7 @@
-"""Differentiable forms of the sequence operators, and a recurrent layer made
-of them: projection, gated linear recurrence, group normalisation with SiLU,
-projection. The layer runs over whole series (training, prompts) and one time
+"""Differentiable forms of the sequence operators, and two layers made of them:
+projection, gated linear recurrence (``RecurrentLayer``) or queries' and keys'
+norms and gated delta rule (``DeltaLayer``), group normalisation with SiLU,
+projection. The layers run over whole series (training, prompts) and one time
 step at a time against a cache of states (streams)."""
 
 from __future__ import annotations
@@ -8,7 +9,7 @@ from __future__ import annotations
 import torch
 from torch import nn
 
-from . import sequence
+from . import delta, sequence
 
 
 def _rows(t):
@@ -68,6 +69,48 @@ class _GroupNorm(torch.autograd.Function):
         return dx, None, dw if weight is not None else None, db if bias is not None else None, None, None, None
 
 
+class _DeltaRule(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, gate, beta, h0, decay, rate, scale, lengths, offsets):
+        ctx.kinds = {"decay": decay, "rate": rate, "scale": scale}
+        y, last, carries = delta.delta_rule(q, k, v, gate, beta, h0, lengths=lengths, offsets=offsets, save=True,
+                                            **ctx.kinds)
+        ctx.save_for_backward(q, k, v, gate, beta, h0, carries, lengths, offsets)
+        ctx.set_materialize_grads(False)
+        return y, last
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dlast):
+        q, k, v, gate, beta, h0, carries, lengths, offsets = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros_like(v, memory_format=torch.contiguous_format)
+        *grads, dh0 = delta.delta_rule_backward(
+            _rows(dy), q, k, v, gate, beta, carries, h0, None if dlast is None else dlast.contiguous(),
+            lengths=lengths, offsets=offsets, **ctx.kinds)
+        return *grads, dh0 if h0 is not None else None, None, None, None, None, None
+
+
+class _QKNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, frequencies, positions, lengths, how):
+        ctx.save_for_backward(q, k, q_weight, k_weight, frequencies, positions, lengths)
+        ctx.how = how
+        ctx.set_materialize_grads(False)
+        return delta.qk_norm(q, k, q_weight, k_weight, frequencies=frequencies, positions=positions, lengths=lengths,
+                             **how)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dqy, dky):
+        q, k, q_weight, k_weight, frequencies, positions, lengths = ctx.saved_tensors
+        dqy, dky = (None if x is None else torch.zeros_like(x, memory_format=torch.contiguous_format) if d is None
+                    else _rows(d) for d, x in ((dqy, q), (dky, k)))
+        grads = delta.qk_norm_backward(dqy, dky, q, k, q_weight, k_weight, frequencies=frequencies,
+                                       positions=positions, lengths=lengths, **ctx.how)
+        return *grads, None, None, None, None
+
+
 def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths=None, offsets=None):
     """``sequence.recurrence`` with gradients for x, gate and h0; returns (h, last states)."""
     return _Recurrence.apply(x, gate, h0, decay, drive, lengths, offsets)
@@ -76,6 +119,19 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
 def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, lengths=None):
     """``sequence.group_norm`` with gradients for x, weight and bias."""
     return _GroupNorm.apply(x, groups, weight, bias, eps, activation, lengths)
+
+
+def delta_rule(q, k, v, gate, beta, h0=None, *, decay="sigmoid", rate="sigmoid", scale=None, lengths=None,
+               offsets=None):
+    """``delta.delta_rule`` with gradients for q, k, v, gate, beta and h0; returns (y, last states)."""
+    return _DeltaRule.apply(q, k, v, gate, beta, h0, decay, rate, scale, lengths, offsets)
+
+
+def qk_norm(q, k=None, q_weight=None, k_weight=None, *, norm="rms", eps=1e-6, frequencies=None, positions=None,
+            pairs="halves", lengths=None):
+    """``delta.qk_norm`` with gradients for q, k and the weights."""
+    return _QKNorm.apply(q, k, q_weight, k_weight, frequencies, positions, lengths,
+                         {"norm": norm, "eps": eps, "pairs": pairs})
 
 
 class RecurrentLayer(nn.Module):
@@ -115,3 +171,59 @@ class RecurrentLayer(nn.Module):
         p = self.into(x)
         h = sequence.recurrence_step(p[:, :self.channels], p[:, self.channels:], state, slots)
         return self.out(self._norm(h)) + self.skip(h)
+
+
+class DeltaLayer(nn.Module):
+    """y = out(silu(norm(o))) + skip(x), o the delta rule of (q, k, v, gate,
+    beta) = in(x) over time with unit queries and keys, each head of o
+    normalised by itself. ``base``: queries and keys are turned by position,
+    pair p at base ** (-2 p / keys) radians a step (None: not at all).
+    Inputs [batch, steps, inputs], outputs [batch, steps, outputs]. Moved to a
+    16-bit type or under autocast the fields are of that type; states and
+    the normalisation's arithmetic stay float32."""
+
+    def __init__(self, inputs: int, heads: int, keys: int, values: int, outputs: int, key_heads: int | None = None,
+                 base: float | None = None, device="cuda"):
+        super().__init__()
+        key_heads = heads if key_heads is None else key_heads
+        if key_heads < 1 or heads % key_heads:
+            raise ValueError(f"key_heads must divide the heads: got {key_heads} for {heads}")
+        self.heads, self.key_heads, self.keys, self.values = heads, key_heads, keys, values
+        self.parts = [key_heads * keys, key_heads * keys, heads * values, heads, heads]
+        self.into = nn.Linear(inputs, sum(self.parts), device=device)
+        self.out = nn.Linear(heads * values, outputs, device=device)
+        self.skip = nn.Linear(inputs, outputs, bias=False, device=device)
+        self.weight = nn.Parameter(torch.ones(heads * values, device=device))
+        self.bias = nn.Parameter(torch.zeros(heads * values, device=device))
+        # a plain attribute: moving the layer to another type leaves the frequencies as they are
+        self.frequencies = None if base is None else base ** (
+            -2.0 / keys * torch.arange(keys // 2, dtype=torch.float64, device=device))
+        with torch.no_grad():  # memories from a few steps to a few hundred
+            self.into.bias[sum(self.parts[:3]):sum(self.parts[:4])] = torch.linspace(1.0, 6.0, heads, device=device)
+
+    def _fields(self, x, positions, lengths=None):
+        q, k, v, gate, beta = self.into(x).split(self.parts, -1)
+        q, k = (t.unflatten(-1, (self.key_heads, self.keys)) for t in (q, k))
+        q, k = delta.qk_norm(q, k, norm="l2", frequencies=self.frequencies, positions=positions, lengths=lengths)
+        return q, k, v.unflatten(-1, (self.heads, self.values)), gate, beta
+
+    def _norm(self, y):
+        return sequence.group_norm(y.reshape(-1, self.heads * self.values), self.heads,
+                                   self.weight.float(), self.bias.float(), activation="silu")
+
+    def forward(self, x, state=None, lengths=None, positions=None):
+        """(y, last states); ``state``: float32 [batch, heads, keys, values]
+        or None; ``positions``: int32 [batch, steps], None for 0, 1, 2, ..."""
+        fields = self._fields(x, positions, lengths)
+        y, last = delta.delta_rule(*fields, state, lengths=lengths)
+        return self.out(self._norm(y).view(*y.shape[:-2], -1)) + self.skip(x), last
+
+    @torch.no_grad()
+    def step(self, x, state, slots=None, positions=None):
+        """One time step: x [batch, inputs]; ``state``, float32 [places, heads,
+        keys, values], moves on in place; ``positions``: int32 [batch], needed
+        where the layer turns by position. Returns y [batch, outputs]."""
+        if self.frequencies is not None and positions is None:
+            raise ValueError("a layer that turns by position needs the positions of a step")
+        y = delta.delta_rule_step(*self._fields(x, positions), state, slots)
+        return self.out(self._norm(y)) + self.skip(x)

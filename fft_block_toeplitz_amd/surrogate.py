@@ -5,9 +5,10 @@ F applies to whole series: v = F m needs all of m. A recurrent layer that has
 learned F's impulse responses gives each v_t as m_t arrives. This example
 draws an operator of decaying modes, F_k = C diag(a^k) B, takes its training
 pairs from ``Plan.apply`` on random series, fits a ``layers.RecurrentLayer``
-to them, and then streams a fresh series through the layer step by step.
+(or, with ``--layer delta``, a ``layers.DeltaLayer``) to them, and then streams
+a fresh series through the layer step by step.
 
-    python -m fft_block_toeplitz_amd.surrogate [--iterations 400] [--steps 200]
+    python -m fft_block_toeplitz_amd.surrogate [--layer delta] [--iterations 400] [--steps 200]
 """
 
 from __future__ import annotations
@@ -31,12 +32,17 @@ def modes_operator(Nm: int, Nd: int, Nt: int, modes: int, generator, device="cud
 
 
 def run(iterations: int = 400, Nm: int = 24, Nd: int = 6, Nt: int = 200, batch: int = 16, channels: int = 128,
-        seed: int = 0, report=print) -> dict:
-    """Fits the layer and streams with it; returns the errors, relative L2."""
+        seed: int = 0, report=print, layer: str = "recurrent") -> dict:
+    """Fits the layer and streams with it; returns the errors, relative L2.
+    ``channels``: those of a recurrent layer's state, or the values of all heads
+    of a delta layer, 16 a head."""
     import torch
 
     import fft_block_toeplitz_amd as fm
-    from fft_block_toeplitz_amd.layers import RecurrentLayer
+    from fft_block_toeplitz_amd.layers import DeltaLayer, RecurrentLayer
+
+    if layer not in ("recurrent", "delta"):
+        raise ValueError(f"layer must be 'recurrent' or 'delta', got {layer!r}")
 
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)
@@ -49,12 +55,15 @@ def run(iterations: int = 400, Nm: int = 24, Nd: int = 6, Nt: int = 200, batch: 
         return m.float(), v.float()
 
     m, v = series(4 * batch)
-    layer = RecurrentLayer(Nm, channels, Nd)
-    optimizer = torch.optim.Adam(layer.parameters(), lr=5e-3)
+    if layer == "delta":
+        model, places = DeltaLayer(Nm, max(1, channels // 16), 16, 16, Nd), (9, max(1, channels // 16), 16, 16)
+    else:
+        model, places = RecurrentLayer(Nm, channels, Nd), (9, channels)
+    optimizer = torch.optim.Adam(model.parameters(), lr=5e-3)
     schedule = torch.optim.lr_scheduler.CosineAnnealingLR(optimizer, iterations)
     for i in range(iterations):
         pick = slice(i % 4 * batch, (i % 4 + 1) * batch)
-        loss = torch.nn.functional.mse_loss(layer(m[pick])[0], v[pick]) / v.square().mean()
+        loss = torch.nn.functional.mse_loss(model(m[pick])[0], v[pick]) / v.square().mean()
         optimizer.zero_grad()
         loss.backward()
         optimizer.step()
@@ -65,10 +74,10 @@ def run(iterations: int = 400, Nm: int = 24, Nd: int = 6, Nt: int = 200, batch: 
     # fresh series, step by step in a cache with more places than streams
     m, v = series(4)
     with torch.no_grad():
-        whole, last = layer(m)
-    state = torch.zeros((9, channels), device="cuda")
+        whole, last = model(m)
+    state = torch.zeros(places, device="cuda")
     slots = torch.tensor([7, 0, 3, 5], dtype=torch.int32, device="cuda")
-    streamed = torch.stack([layer.step(m[:, t], state, slots) for t in range(Nt)], 1)
+    streamed = torch.stack([model.step(m[:, t], state, slots) for t in range(Nt)], 1)
     plan.close()
 
     def off(x, ref):
@@ -86,5 +95,6 @@ if __name__ == "__main__":
     ap = argparse.ArgumentParser(description="fit a recurrent layer to a block Toeplitz operator and stream with it")
     ap.add_argument("--iterations", type=int, default=400)
     ap.add_argument("--steps", type=int, default=200, help="time steps of a series (Nt)")
+    ap.add_argument("--layer", choices=["recurrent", "delta"], default="recurrent")
     a = ap.parse_args()
-    run(iterations=a.iterations, Nt=a.steps)
+    run(iterations=a.iterations, Nt=a.steps, layer=a.layer)

@@ -480,6 +480,155 @@ FFTMV_API int fftmv_group_norm_workspace(int64_t samples, int64_t rows, int64_t 
 FFTMV_API int fftmv_group_norm_forward(const fftmv_group_norm_t *g, hipStream_t stream);
 FFTMV_API int fftmv_group_norm_backward(const fftmv_group_norm_t *g, hipStream_t stream);
 
+/* Fields of the operators below have heads: element c of head n in row (b, t)
+ * of a field lies at data[b * batch + t * step + n * head + c]; strides are in
+ * elements, and the elements of one head are contiguous. A field without rows
+ * may be NULL. */
+typedef struct fftmv_heads_s {
+  void *data;
+  int64_t batch, step, head;
+} fftmv_heads_t;
+
+/* Gated delta rule: a causal linear operator along time whose state is a
+ * matrix [keys][values] for every sequence and head,
+ *
+ *     S_t = a_t S_{t-1} + b_t k_t (v_t - a_t S_{t-1}^T k_t)^T,   S_{-1} = h0
+ *     y_t = scale S_t^T q_t
+ *
+ * The state is asked for what it holds under k_t and corrected towards v_t.
+ * a = 1 / (1 + exp(-gate)) or exp(gate) (FFTMV_DECAY_SIGMOID, _EXP; a gate of
+ * minus infinity clears the state), b = 1 / (1 + exp(-beta)) or beta
+ * (FFTMV_RATE_*). Head n takes the queries and keys of head n / (heads /
+ * key_heads); key_heads divides heads. Keys are meant to have norms near or
+ * below one (fftmv_qk_norm_forward).
+ *
+ * q, k: [keys] elements a head; v, y: [values]; gate, beta: one (their `head`
+ * is the stride between heads). Batch, padded and packed forms, lengths and
+ * offsets are those of fftmv_recurrence_t; rows that no sequence holds do not
+ * matter, and are written as zeros (y, dq, dk, dv, dgate, dbeta).
+ *
+ * Steps are taken in runs of FFTMV_DELTA_RUN of one sequence. Forward writes y
+ * (rounded once to the element type) and, where not NULL,
+ *   h_last   [batch][heads][keys][values] the states after the last steps (h0
+ *            of an empty sequence)
+ *   carries  [runs][heads][keys][values] (runs: fftmv_delta_rule_sizes) the
+ *            states that enter the runs: what the backward pass starts from
+ * Backward takes the inputs, h0 and carries as the forward had and left them,
+ * dy (the gradient of y) and, where not NULL, dh_last (that of h_last), and
+ * writes the gradients dq, dk (summed over the heads that share them), dv,
+ * dgate, dbeta and, where not NULL, dh0.
+ *
+ * workspace: fftmv_delta_rule_sizes bytes, 16-byte aligned, any contents; calls
+ * that may run at the same time need their own. States and sums are FP32. A
+ * value that is not finite makes results of its head not finite from the first
+ * step of its run on until the sequence ends; it reaches no other sequence and no
+ * head with other queries and keys.
+ * Errors: FFTMV_ERR_INVALID_ARG (a null or misaligned pointer, a size < 1 --
+ * steps may be 0 --, an unknown type/decay/rate, key_heads that do not divide
+ * heads, both lengths and offsets, a workspace that is too small);
+ * FFTMV_ERR_UNSUPPORTED_SIZE (keys > FFTMV_DELTA_KEYS, values >
+ * FFTMV_DELTA_VALUES, more than 2^31 - 2^16 sequences, steps or heads, or a
+ * grid above 2^32 work-items). */
+#define FFTMV_RATE_SIGMOID 0 /* b = 1 / (1 + exp(-beta)) */
+#define FFTMV_RATE_VALUE 1   /* b = beta                 */
+#define FFTMV_DELTA_RUN 64
+#define FFTMV_DELTA_KEYS 128
+#define FFTMV_DELTA_VALUES 1024
+typedef struct fftmv_delta_rule_s {
+  int64_t batch, steps, key_heads, heads, keys, values;
+  int32_t dtype, decay, rate;
+  float scale;
+  const int32_t *lengths, *offsets;
+  fftmv_heads_t q, k, v, gate, beta;
+  const float *h0;
+  float *carries;
+  void *workspace;
+  size_t workspace_bytes;
+  /* forward */
+  fftmv_heads_t y;
+  float *h_last;
+  /* backward */
+  fftmv_heads_t dy;
+  const float *dh_last;
+  fftmv_heads_t dq, dk, dv, dgate, dbeta;
+  float *dh0;
+} fftmv_delta_rule_t;
+
+/* For a forward (backward: 0) or backward (1) call of this shape (packed: it
+ * has offsets): how many runs `carries` has and how many bytes the workspace
+ * needs. Any output may be NULL. */
+FFTMV_API int fftmv_delta_rule_sizes(int64_t batch, int64_t steps, int64_t key_heads, int64_t heads, int64_t keys,
+                                     int64_t values, int dtype, int packed, int backward, int64_t *runs,
+                                     size_t *workspace_bytes);
+FFTMV_API int fftmv_delta_rule_forward(const fftmv_delta_rule_t *r, hipStream_t stream);
+FFTMV_API int fftmv_delta_rule_backward(const fftmv_delta_rule_t *r, hipStream_t stream);
+
+/* One step of `batch` streams against a cache of states, in place: stream b
+ * takes state[slots[b]] ([places][heads][keys][values] FP32, places
+ * state_place elements apart) one step on and gets its row of y. Rows are
+ * addressed by b * step (batch strides are ignored). Slots as in
+ * fftmv_recurrence_step. */
+typedef struct fftmv_delta_rule_step_s {
+  int64_t batch, key_heads, heads, keys, values, places;
+  int32_t dtype, decay, rate;
+  float scale;
+  fftmv_heads_t q, k, v, gate, beta;
+  float *state;
+  int64_t state_place;
+  const int32_t *slots;
+  fftmv_heads_t y;
+} fftmv_delta_rule_step_t;
+FFTMV_API int fftmv_delta_rule_step(const fftmv_delta_rule_step_t *r, hipStream_t stream);
+
+/* Norms of queries and keys for each head, with a rotation by position in the
+ * same pass: for each row and head of `dim` elements
+ *
+ *     z = x w / n,   n = sqrt(mean(x^2) + eps)  or  sqrt(sum(x^2) + eps)
+ *     y = z, its first 2 * frequencies elements turned in pairs:
+ *         (z_i, z_j) -> (z_i cos f - z_j sin f, z_j cos f + z_i sin f),
+ *         f = position * frequency[p], j = i + frequencies (FFTMV_PAIRS_HALVES,
+ *         i = p) or j = i + 1 (FFTMV_PAIRS_NEIGHBOURS, i = 2 p)
+ *
+ * q and k (key_heads may be 0: no keys) are taken in one call. q_weight,
+ * k_weight: [dim] FP32, NULL for ones. frequency: FP64 [frequencies], radians
+ * a position; positions: int32, row (b, t) at positions[b * position_batch +
+ * t], NULL for t. Angles are taken in FP64. lengths (device int32 [batch],
+ * clamped to 0..steps): rows from lengths[b] on enter no sum whatever they
+ * hold, and are written as zeros.
+ *
+ * Forward writes qy and ky. Backward takes the inputs and dqy, dky (the
+ * gradients of qy and ky) and writes dq, dk and, where not NULL, dq_weight,
+ * dk_weight ([dim] FP32). workspace: fftmv_qk_norm_workspace bytes, 16-byte
+ * aligned, any contents (backward only).
+ * Errors as above; FFTMV_ERR_UNSUPPORTED_SIZE also for dim > FFTMV_QK_NORM_DIM. */
+#define FFTMV_NORM_RMS 0
+#define FFTMV_NORM_L2 1
+#define FFTMV_PAIRS_HALVES 0
+#define FFTMV_PAIRS_NEIGHBOURS 1
+#define FFTMV_QK_NORM_DIM 512
+typedef struct fftmv_qk_norm_s {
+  int64_t batch, steps, query_heads, key_heads, dim, frequencies;
+  int32_t dtype, norm, pairs;
+  float eps;
+  const int32_t *lengths;
+  const double *frequency;
+  const int32_t *positions;
+  int64_t position_batch;
+  fftmv_heads_t q, k;
+  const float *q_weight, *k_weight;
+  /* forward */
+  fftmv_heads_t qy, ky;
+  /* backward */
+  fftmv_heads_t dqy, dky, dq, dk;
+  float *dq_weight, *dk_weight;
+  void *workspace;
+  size_t workspace_bytes;
+} fftmv_qk_norm_t;
+FFTMV_API int fftmv_qk_norm_workspace(int64_t batch, int64_t steps, int64_t query_heads, int64_t key_heads,
+                                      int64_t dim, size_t *bytes);
+FFTMV_API int fftmv_qk_norm_forward(const fftmv_qk_norm_t *n, hipStream_t stream);
+FFTMV_API int fftmv_qk_norm_backward(const fftmv_qk_norm_t *n, hipStream_t stream);
+
 /* Library version, (major << 16) | (minor << 8) | patch. */
 FFTMV_API int fftmv_version(void);
 
