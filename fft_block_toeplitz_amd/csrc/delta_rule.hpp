@@ -61,6 +61,15 @@ constexpr int kFull = 3;
 template <typename T>
 constexpr int kOut = sizeof(T) == 4 ? 3 : 2;
 
+// f(Const<0>), ..., f(Const<N - 1>): loops whose numbers choose registers.
+template <int I, int N, typename F>
+__device__ __forceinline__ void unrolled(F &&f) {
+  if constexpr (I < N) {
+    f(Const<I>{});
+    unrolled<I + 1, N>(f);
+  }
+}
+
 // ------------------------------------------------------------------ operands
 template <int N>
 struct Cut {
@@ -121,7 +130,45 @@ __device__ __forceinline__ void multiply(f32x4 &c, const Cut<NA> &a, const Cut<N
   }
 }
 
+// The same for several results: neighbouring instructions add to different ones, which need not wait for each other.
+template <int LIMIT, int M, int NA, int NB>
+__device__ __forceinline__ void multiply_rows(f32x4 *c, const Cut<NA> (&a)[M], const Cut<NB> &b) {
+#pragma unroll
+  for (int s = LIMIT - 1; s >= 0; --s) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int j = s - i;
+      if (j < 0 || j >= NB) continue;
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[m].p[i]),
+                                                       __builtin_bit_cast(bf16x8, b.p[j]), c[m], 0, 0, 0);
+    }
+  }
+}
+
+// The transposed results: b's index in rows 4 (lane / 16) + 0..3, a's in column lane % 16.
+template <int LIMIT, int M, int NA, int NB>
+__device__ __forceinline__ void multiply_rows_t(f32x4 *c, const Cut<NA> (&a)[M], const Cut<NB> &b) {
+#pragma unroll
+  for (int s = LIMIT - 1; s >= 0; --s) {
+#pragma unroll
+    for (int i = 0; i < NA; ++i) {
+      const int j = s - i;
+      if (j < 0 || j >= NB) continue;
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b.p[j]),
+                                                       __builtin_bit_cast(bf16x8, a[m].p[i]), c[m], 0, 0, 0);
+    }
+  }
+}
+
 // ------------------------------------------------------------------- fields
+template <typename I>
+__device__ __forceinline__ I clamp_to(I v, I most) {
+  return v < 0 ? 0 : v > most ? most : v;
+}
 template <typename T>
 __device__ __forceinline__ T *head_row(const fftmv_heads_t &f, int64_t b, int64_t t, int64_t n) {
   return static_cast<T *>(f.data) + b * f.batch + t * f.step + n * f.head;
@@ -167,6 +214,106 @@ __device__ __forceinline__ Cut<kParts<T>> load_cut(const T *p, int c, int n, boo
   }
 }
 
+// Eight elements c.. of row t of n elements as they lie in memory: loaded now,
+// settled (what is behind the row's end, or in rows that are not there, cleared)
+// when they are needed. A run's rows are loaded a run ahead, so nothing here may
+// wait for them.
+//   WHOLE  rows are multiples of eight elements, words, and not far apart
+//          (delta_whole): a chunk is in a row or behind it, and the hardware's
+//          bounds check on the run's bytes gives zeros for rows behind the last.
+//          Addresses take one instruction, and no branch stands between loads
+//   else   where the row ends inside, the load is moved back to end with the row,
+//          and shifted afterwards
+template <typename T>
+struct Raw8 {
+  u32x4 w[sizeof(T) / 2];
+};
+constexpr int kBufferFlags = 0x00027000;  // plain words
+template <typename T, bool WHOLE>
+struct Rows {
+  const T *first;
+  int64_t step;
+  int n, width;
+  __amdgpu_buffer_rsrc_t buffer;
+  __device__ __forceinline__ Rows(const fftmv_heads_t &f, int64_t b, int64_t row, int64_t head, int n, int width)
+      : first(head_row<const T>(f, b, row, head)), step(f.step), n(n), width(width) {
+    if constexpr (WHOLE)
+      buffer = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<T *>(first), 0, static_cast<int>(((n - 1) * step + width) * static_cast<int64_t>(sizeof(T))), kBufferFlags);
+  }
+  __device__ __forceinline__ Raw8<T> load(int t, int c) const {
+    Raw8<T> r;
+    if constexpr (WHOLE) {
+      const int at = (t * static_cast<int>(step) + c) * static_cast<int>(sizeof(T));
+#pragma unroll
+      for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+        r.w[h] = __builtin_amdgcn_raw_buffer_load_b128(buffer, at + 16 * h, 0, 0);
+    } else {
+      const T *p = first + min(t, n - 1) * step;
+      if (width >= 8) {
+        p += min(c, width - 8);
+#pragma unroll
+        for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h) {
+          const u32x4_any v = reinterpret_cast<const u32x4_any *>(p)[h];
+          r.w[h] = u32x4{v[0], v[1], v[2], v[3]};
+        }
+      } else {
+        T e[8] = {};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c == 0 && i < width) e[i] = p[i];
+        __builtin_memcpy(&r, e, sizeof(e));
+      }
+    }
+    return r;
+  }
+};
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void settle(Raw8<T> &r, int c, int n, bool held) {
+  if constexpr (WHOLE) {
+    const bool in = c < n;
+#pragma unroll
+    for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[h][i] = in ? r.w[h][i] : 0u;
+    return;
+  }
+  const int drop = !held ? 8 : n >= 8 ? clamp_to(c + 8 - n, 8) : 0;  // elements at the front that are not the chunk's
+  if constexpr (sizeof(T) == 2) {
+    uint64_t lo = r.w[0][0] | static_cast<uint64_t>(r.w[0][1]) << 32, hi = r.w[0][2] | static_cast<uint64_t>(r.w[0][3]) << 32;
+    if (drop >= 4) lo = hi, hi = 0;
+    const int bits = drop % 4 * 16;
+    if (drop == 8) lo = 0;
+    lo = bits ? lo >> bits | hi << (64 - bits) : lo;
+    hi >>= bits;
+    r.w[0] = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+  } else {
+#pragma unroll
+    for (int step = 4; step >= 1; step /= 2) {
+      const bool by = drop & step;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t moved = i + step < 8 ? r.w[(i + step) / 4 % 2][(i + step) % 4] : 0u;
+        r.w[i / 4][i % 4] = by ? moved : r.w[i / 4][i % 4];
+      }
+    }
+    if (drop == 8) r.w[0] = r.w[1] = u32x4{0, 0, 0, 0};
+  }
+}
+template <typename T>
+__device__ __forceinline__ Cut<kParts<T>> cut_raw(const Raw8<T> &r) {
+  if constexpr (kParts<T> == 1) {
+    return Cut<1>{{r.w[0]}};
+  } else {
+    T e[8];
+    __builtin_memcpy(e, &r, sizeof(e));
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(e[i]);
+    return cut<kParts<T>>(x);
+  }
+}
+
 // Eight FP32 values as N parts.
 template <int N>
 __device__ __forceinline__ Cut<N> load_wide(const float *p, int c, int n, bool held) {
@@ -184,10 +331,6 @@ struct Span {
 inline __host__ __device__ int64_t runs_of(int64_t steps) { return (steps + kRun - 1) / kRun; }
 inline __host__ __device__ int64_t delta_runs(int64_t batch, int64_t steps, bool packed) {
   return steps == 0 ? 0 : packed ? steps / kRun + batch : batch * runs_of(steps);
-}
-template <typename I>
-__device__ __forceinline__ I clamp_to(I v, I most) {
-  return v < 0 ? 0 : v > most ? most : v;
 }
 __device__ __forceinline__ Span span_of(const fftmv_delta_rule_t &r, int64_t b) {
   const int steps = static_cast<int>(r.steps);
@@ -244,12 +387,52 @@ __host__ __device__ constexpr int upper_frag(int m, int s) { return m < 2 ? 2 * 
 __host__ __device__ constexpr bool in_lower(int m, int s) { return s == 0 || m >= 2; }
 __host__ __device__ constexpr bool in_upper(int m, int s) { return s == 1 || m < 2; }
 
+// p[i] with an offset of 32 bits beside an address that all lanes share.
+template <typename T>
+__device__ __forceinline__ const T &at_lane(const T *p, uint32_t i) {
+  return *reinterpret_cast<const T *>(reinterpret_cast<const char *>(p) + i * static_cast<uint32_t>(sizeof(T)));
+}
+template <typename T>
+__device__ __forceinline__ T &at_lane_of(T *p, uint32_t i) {
+  return *reinterpret_cast<T *>(reinterpret_cast<char *>(p) + i * static_cast<uint32_t>(sizeof(T)));
+}
 template <int N>
 __device__ __forceinline__ Cut<N> load_frag(const u32x4 *f, int frag, int parts, int lane) {
   Cut<N> c;
 #pragma unroll
-  for (int n = 0; n < N; ++n) c.p[n] = f[(frag * parts + n) * kWave + lane];
+  for (int n = 0; n < N; ++n) c.p[n] = at_lane(f + (frag * parts + n) * kWave, lane);
   return c;
+}
+
+template <int LIMIT, bool UPPER, bool TRANSPOSED, int N, int NB>
+__device__ __forceinline__ void multiply_triangle(f32x4 (&c)[kTiles], const Cut<N> (&a)[kFrags], const Cut<NB> &lo,
+                                                  const Cut<NB> &hi) {
+#pragma unroll
+  for (int s = LIMIT - 1; s >= 0; --s) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int j = s - i;
+      if (j < 0 || j >= NB) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          if (!(UPPER ? in_upper(m, h) : in_lower(m, h))) continue;
+          const bf16x8 f = __builtin_bit_cast(bf16x8, a[UPPER ? upper_frag(m, h) : lower_frag(m, h)].p[i]);
+          const bf16x8 x = __builtin_bit_cast(bf16x8, (h ? hi : lo).p[j]);
+          c[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(TRANSPOSED ? x : f, TRANSPOSED ? f : x, c[m], 0, 0, 0);
+        }
+    }
+  }
+}
+// c += the lower (upper) triangle in f, PARTS parts of a fragment, times the operands of steps 0..31 and 32..63.
+template <int LIMIT, int N, int PARTS, bool UPPER, int NB>
+__device__ __forceinline__ void multiply_triangle(f32x4 (&c)[kTiles], const u32x4 *f, const Cut<NB> &lo, const Cut<NB> &hi,
+                                                  int lane) {
+  Cut<N> a[kFrags];
+#pragma unroll
+  for (int i = 0; i < kFrags; ++i) a[i] = load_frag<N>(f, i, PARTS, lane);
+  multiply_triangle<LIMIT, UPPER, false>(c, a, lo, hi);
 }
 
 // The workspace of a call in its parts.
@@ -607,6 +790,11 @@ __device__ __forceinline__ Cut<NP> tile_rows(const uint16_t *tile, int m, int s,
     c.p[p] = *reinterpret_cast<const u32x4 *>(tile + (p * kRun + 16 * m + lane % 16) * kTileRow<KEYS> + 32 * s + 8 * (lane / 16));
   return c;
 }
+template <int KEYS, int NP>
+__device__ __forceinline__ void tile_rows(Cut<NP> (&c)[kTiles], const uint16_t *tile, int s, int lane) {
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m) c[m] = tile_rows<KEYS, NP>(tile, m, s, lane);
+}
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 // Four rows of one column for each lane: within 16 lanes, lane l reads 4
 // elements of row l / 4 and receives column l of the 4 x 16 that they read.
@@ -635,6 +823,23 @@ __device__ __forceinline__ Cut<NP> tile_columns(const uint16_t *tile, int t, int
   return c;
 }
 
+// state += (columns of the tile)^T times the operands of steps 0..31 and 32..63, four tiles of keys at a time.
+template <int KEYS, int NP>
+__device__ __forceinline__ void multiply_columns(f32x4 (&state)[KEYS / 16], const uint16_t *tile, const Cut<kFull> &lo,
+                                                 const Cut<kFull> &hi, int lane) {
+  constexpr int M = KEYS / 16 < 4 ? KEYS / 16 : 4;
+#pragma unroll
+  for (int t = 0; t < KEYS / 16; t += M) {
+    Cut<NP> k[2][M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      k[0][i] = tile_columns<KEYS, NP>(tile, t + i, 0, lane);
+      k[1][i] = tile_columns<KEYS, NP>(tile, t + i, 1, lane);
+    }
+    multiply_rows<kFull>(state + t, k[0], lo);
+    multiply_rows<kFull>(state + t, k[1], hi);
+  }
+}
 // Operand with index columns col.. (lane % 16) and slots of rows row + 8 g + 0..7 (GAP 4), or as results hold them (GAP 16).
 template <int ROW, int NP, int GAP>
 __device__ __forceinline__ Cut<NP> plain_columns(const uint16_t *tile, int row, int col, int lane) {
@@ -685,6 +890,154 @@ __device__ __forceinline__ f32x4 load_column(const fftmv_heads_t &f, int64_t b, 
   return v;
 }
 
+// ------------------------------------------------------- runs one after another
+// The chains (of states, and of their gradients) go through a sequence's runs.
+// Only K S, T (..) and K^T U of a run wait for the run before: four waves, the
+// front, do those, 16 value columns each with the state in registers; four more,
+// one on each SIMD beside a front wave, do all else: they bring the next run's
+// rows and triangles from memory to LDS and make the outputs from what the front
+// leaves there, operands of the state at a run's start and of U in its middle. A
+// run has two halves between barriers:
+//   front  R = V - e^G K S, U = T R     | S' = e^{G_last} S + K^T (..) U
+//   back   Q S; the next run's loads    | Y = .. + P U; the next run into LDS
+// (8 x 2048 x 16 heads of 128 x 128 in bf16 took 235 us with all of it in one
+// wave a SIMD.)
+constexpr int kFrontWaves = 4;
+constexpr int kFrontThreads = kFrontWaves * kWave;
+constexpr int kChainThreads = 2 * kFrontThreads;
+constexpr int kValues = 16 * kFrontWaves;  // value columns of a workgroup
+constexpr int kLdsBytes = 160 << 10;
+
+template <typename T>
+constexpr int kValueRow = kValues + 16 / sizeof(T);
+
+template <typename T, int KEYS, int FRAGS, int BUFFERS>
+struct ChainLds {
+  static constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32;
+  alignas(16) uint16_t k[BUFFERS][NP * kRun * kTileRow<KEYS>];
+  alignas(16) T v[kRun * kValueRow<T>];
+  alignas(16) u32x4 frags[FRAGS * kWave];
+  alignas(16) float into[kRun], out[kRun], rate[kRun];
+};
+
+// A thread's part of a run's rows of keys on their way to LDS.
+template <typename T, int KEYS, bool WHOLE>
+__device__ __forceinline__ void fetch_rows(Raw8<T> (&k)[KEYS / 32], int thread, const fftmv_heads_t &f, int keys,
+                                           int64_t b, int64_t row, int n, int64_t head) {
+  const Rows<T, WHOLE> rows(f, b, row, head, n, keys);
+#pragma unroll
+  for (int i = 0; i < KEYS / 32; ++i) k[i] = rows.load(thread / (KEYS / 8) + i * (kFrontThreads * 8 / KEYS), thread % (KEYS / 8) * 8);
+}
+template <typename T, int KEYS, bool WHOLE>
+__device__ __forceinline__ void put_rows(Raw8<T> (&k)[KEYS / 32], int thread, uint16_t *tile, int keys, int n) {
+#pragma unroll
+  for (int i = 0; i < KEYS / 32; ++i) {
+    const int u = thread + i * kFrontThreads, t = u / (KEYS / 8), c = u % (KEYS / 8) * 8;
+    if (!WHOLE || keys < KEYS) settle<WHOLE>(k[i], c, keys, t < n);
+    const auto parts = cut_raw<T>(k[i]);
+#pragma unroll
+    for (int p = 0; p < kParts<T>; ++p)
+      *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * kTileRow<KEYS> + c) = parts.p[p];
+  }
+}
+
+// The same for all that a run needs: keys, values, a triangle's fragments, factors.
+template <typename T, int KEYS, int FRAGS, bool WHOLE>
+struct Fetched {
+  static constexpr int NV = kValues / 32, NF = (FRAGS * kWave + kFrontThreads - 1) / kFrontThreads;
+  Raw8<T> k[KEYS / 32], v[NV];
+  u32x4 frags[NF], factors;
+
+  __device__ __forceinline__ void fetch_keys(int thread, const fftmv_heads_t &f, int keys, int64_t b, int64_t row, int n,
+                                             int64_t head) {
+    fetch_rows<T, KEYS, WHOLE>(k, thread, f, keys, b, row, n, head);
+  }
+  __device__ __forceinline__ void put_keys(int thread, uint16_t *tile, int keys, int n) {
+    put_rows<T, KEYS, WHOLE>(k, thread, tile, keys, n);
+  }
+  __device__ __forceinline__ void fetch_values(int thread, const fftmv_heads_t &f, int values, int64_t b, int64_t row,
+                                               int n, int64_t head, int first_col) {
+    const Rows<T, WHOLE> rows(f, b, row, head, n, values);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      v[i] = rows.load(thread / (kValues / 8) + i * (kFrontThreads * 8 / kValues), first_col + thread % (kValues / 8) * 8);
+  }
+  template <typename L>
+  __device__ __forceinline__ void put_values(int thread, L &lds, int values, int n, int first_col) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int u = thread + i * kFrontThreads, t = u / (kValues / 8), c = u % (kValues / 8) * 8;
+      if (!WHOLE || first_col + kValues > values) settle<WHOLE>(v[i], first_col + c, values, t < n);
+#pragma unroll
+      for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+        reinterpret_cast<u32x4 *>(lds.v + t * kValueRow<T> + c)[h] = v[i].w[h];
+    }
+  }
+  __device__ __forceinline__ void fetch_factors(int thread, const u32x4 *from, const Factors &f) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i) frags[i] = at_lane(from, min(thread + i * kFrontThreads, FRAGS * kWave - 1));
+    factors = at_lane(reinterpret_cast<const u32x4 *>(f.into), min(thread, 3 * kRun / 4 - 1));
+  }
+  template <typename L>
+  __device__ __forceinline__ void put_factors(int thread, L &lds) {
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      const int u = thread + i * kFrontThreads;
+      if (FRAGS * kWave % kFrontThreads == 0 || u < FRAGS * kWave) lds.frags[u] = frags[i];
+    }
+    if (thread < 3 * kRun / 4) reinterpret_cast<u32x4 *>(lds.into)[thread] = factors;
+  }
+};
+
+// Rows of queries as operands straight from memory, HOLD of their S parts of 32 keys at a time.
+template <typename T, int KEYS, bool WHOLE>
+struct QueryRows {
+  static constexpr int S = KEYS / 32, HOLD = sizeof(T) == 2 ? S : 1;
+  Raw8<T> q[HOLD][kTiles];
+  template <int s>
+  __device__ __forceinline__ void fetch(const fftmv_heads_t &f, int keys, int64_t b, int64_t row, int n,
+                                        int64_t head, int lane) {
+    const Rows<T, WHOLE> rows(f, b, row, head, n, keys);
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) q[s % HOLD][m] = rows.load(16 * m + lane % 16, 32 * s + 8 * (lane / 16));
+  }
+  template <int s>
+  __device__ __forceinline__ Cut<kParts<T>> operand(int m, int keys, int n, int lane) {
+    if (!WHOLE || keys < KEYS)
+      settle<WHOLE>(q[s % HOLD][m], 32 * s + 8 * (lane / 16), keys, 16 * m + lane % 16 < n);
+    return cut_raw<T>(q[s % HOLD][m]);
+  }
+};
+
+// Steps 16 m + 4 g + 0..3 of column col + lane % 16 of the values in LDS.
+template <typename T>
+__device__ __forceinline__ f32x4 value_column(const T *v, int m, int col, int lane) {
+  const int l = lane % 16, row = 16 * m + 4 * (lane / 16);
+  f32x4 r;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = v[(row + i) * kValueRow<T> + col + l];
+  } else {
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(v) + (row + l / 4) * kValueRow<T> + col + 4 * (l % 4);
+    const T4 q = __builtin_bit_cast(T4, transposed4(p));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = static_cast<float>(q[i]);
+  }
+  return r;
+}
+
+// Rows that are multiples of eight elements, begin at words, do not overlap, and
+// whose run of 64 is addressed in 31 bits.
+inline bool delta_whole(const fftmv_heads_t &f, int64_t width, int dtype) {
+  const int64_t es = dtype == FFTMV_F32 ? 4 : 2;
+  return width % 8 == 0 && f.step >= width && f.step <= (1 << 22) && f.batch * es % 4 == 0 && f.step * es % 4 == 0 &&
+         f.head * es % 4 == 0 && reinterpret_cast<uintptr_t>(f.data) % 4 == 0;
+}
+inline bool delta_whole(const fftmv_delta_rule_t &r, const fftmv_heads_t &valued, const fftmv_heads_t &other) {
+  return delta_whole(r.q, r.keys, r.dtype) && delta_whole(r.k, r.keys, r.dtype) && delta_whole(valued, r.values, r.dtype) &&
+         delta_whole(other, r.values, r.dtype);
+}
 template <typename F>
 hipError_t by_keys(int64_t keys, F f) {
   if (keys <= 32) return f(Const<32>{});

@@ -20,123 +20,235 @@
 
 namespace fftmv {
 
-constexpr int kBackWaves = 4;
-constexpr int kBackThreads = kBackWaves * kWave;
+// The chain of the states' gradients. P^T dY and (scale diag(e^G) Q)^T dY wait
+// for no other run: the back waves compute them a run ahead of the front, which
+// does K D, T^T (..) and K^T Z.
+template <typename T, int KEYS, int BUFFERS, bool TILE>
+struct BackwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
+  alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS> : 8];  // queries of the back waves' run
+  alignas(16) f32x4 z[kFrontWaves][kTiles][kWave];                       // P^T dY of the front's
+  alignas(16) f32x4 d[kFrontWaves][KEYS / 16][kWave];                    // Q^T (..) dY
+};
 
-template <typename T, int KEYS>
-__global__ __launch_bounds__(kBackThreads) void delta_back_chain_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
+template <typename T, int KEYS, bool WHOLE>
+__global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Tri = Triangles<T, true>;
-  constexpr int NP = kParts<T>, S = KEYS / 32;
-  __shared__ __align__(16) uint16_t ktile[NP * kRun * kTileRow<KEYS>], qtile[NP * kRun * kTileRow<KEYS>];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, x = lane % 16, g = lane / 16;
+  constexpr int FRAGS = kFrags * kFull, NP = kParts<T>, S = KEYS / 32;
+  constexpr bool TILE = sizeof(BackwardLds<T, KEYS, 1, true>) <= kLdsBytes;
+  constexpr int BUFFERS = sizeof(BackwardLds<T, KEYS, 2, TILE>) <= kLdsBytes ? 2 : 1;
+  using Lds = BackwardLds<T, KEYS, BUFFERS, TILE>;
+  __shared__ Lds lds;
+  const int side = __builtin_amdgcn_readfirstlane(threadIdx.x / kFrontThreads);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % kFrontWaves;
+  int thread = threadIdx.x % kFrontThreads, lane = threadIdx.x % kWave, x = lane % 16, g = lane / 16;
+  auto again = [&]() __attribute__((always_inline)) {
+    thread = afresh(thread), lane = thread % kWave, x = lane % 16, g = lane / 16;
+  };
   const int64_t head = blockIdx.x % r.heads, b = blockIdx.x / r.heads;
   const int64_t key_head = head / (r.heads / r.key_heads);
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
-  const int col = (blockIdx.y * kBackWaves + wave) * 16 + x;
+  const int first_col = blockIdx.y * kValues, col = first_col + wave * 16 + x;
   const bool inside = col < values;
   const Span span = span_of(r, b);
   const int64_t states = r.keys * r.values;
+  const int last = span.len > 0 ? (span.len - 1) / kRun * kRun : -kRun;
+  auto at = [&](int first) __attribute__((always_inline)) { return (span.run + first / kRun) * r.heads + head; };
 
-  f32x4 grad[KEYS / 16];
-#pragma unroll
-  for (int t = 0; t < KEYS / 16; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = key_of(t, g, i);
-      grad[t][i] = r.dh_last && inside && key < keys
-                       ? r.dh_last[(b * r.heads + head) * states + static_cast<int64_t>(key) * values + col]
-                       : 0.0f;
-    }
-  auto keep = [&](float *to) {
+  if (side == 0) {
+    f32x4 grad[KEYS / 16];
 #pragma unroll
     for (int t = 0; t < KEYS / 16; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = key_of(t, g, i);
-        if (inside && key < keys) to[static_cast<int64_t>(key) * values + col] = grad[t][i];
+        grad[t][i] = r.dh_last && inside && key < keys
+                         ? r.dh_last[(b * r.heads + head) * states + static_cast<int64_t>(key) * values + col]
+                         : 0.0f;
       }
-  };
-
-  for (int first = (span.len - 1) / kRun * kRun; first >= 0 && span.len > 0; first -= kRun) {
-    const int n = min(kRun, span.len - first);
-    const int64_t row = span.row + first, at = (span.run + first / kRun) * r.heads + head;
-    const Factors &f = w.factors[at];
-    const u32x4 *tri = w.triangles + at * Tri::kAll * kWave;
-    keep(w.grads + at * states);
+    auto keep = [&](float *to) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < KEYS / 16; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = key_of(t, g, i);
+          if (inside && key < keys) to[static_cast<int64_t>(key) * values + col] = grad[t][i];
+        }
+    };
     __syncthreads();
-    fill_tile<T, KEYS, kBackThreads>(ktile, r.k, span.batch, row, n, key_head, keys);
-    fill_tile<T, KEYS, kBackThreads>(qtile, r.q, span.batch, row, n, key_head, keys);
-    f32x4 dy[kTiles];
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) dy[m] = load_column<T>(r.dy, span.batch, row, n, head, m, g, col, inside);
     __syncthreads();
-
-    f32x4 z[kTiles];
+    __syncthreads();
+    for (int first = last, buffer = 0; first >= 0; first -= kRun, buffer = (buffer + 1) % BUFFERS) {
+      again();
+      const uint16_t *k = lds.k[buffer];
+      keep(w.grads + at(first) * states);
+      const float whole = lds.into[kRun - 1];
+      f32x4 z[kTiles];
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) z[m] = f32x4{0, 0, 0, 0};
+      for (int m = 0; m < kTiles; ++m) z[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const Cut<kFull> part = cut_tiles<kFull>(grad[2 * s], grad[2 * s + 1]);
+      for (int s = 0; s < S; ++s) {
+        const Cut<kFull> part = cut_tiles<kFull>(grad[2 * s], grad[2 * s + 1]);
+        Cut<NP> rows[kTiles];
+        tile_rows<KEYS>(rows, k, s, lane);
+        multiply_rows<kFull>(z, rows, part);
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) multiply<kFull>(z[m], tile_rows<KEYS, NP>(ktile, m, s, lane), part);
-    }
-    {
-      const Cut<NP> a = cut_tiles<NP>(dy[0], dy[1]), c = cut_tiles<NP>(dy[2], dy[3]);
-      const u32x4 *p = tri + Tri::kP * kWave;
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        z[m] *= *reinterpret_cast<const f32x4 *>(f.out + 16 * m + 4 * g);
-        if (m < 2) multiply<kFull>(z[m], load_frag<kFull>(p, upper_frag(m, 0), Tri::kPParts, lane), a);
-        multiply<kFull>(z[m], load_frag<kFull>(p, upper_frag(m, 1), Tri::kPParts, lane), c);
+        for (int t = 2 * s; t < 2 * s + 2; ++t) grad[t] = grad[t] * whole + lds.d[wave][t][lane];
       }
-    }
-    {
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) z[m] = z[m] * *reinterpret_cast<const f32x4 *>(lds.out + 16 * m + 4 * g) + lds.z[wave][m][lane];
+      {
+        const Cut<kFull> a = cut_tiles<kFull>(z[0], z[1]), c = cut_tiles<kFull>(z[2], z[3]);
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) z[m] = f32x4{0, 0, 0, 0};
+        multiply_triangle<kFull, kFull, kFull, true>(z, lds.frags, a, c, lane);
+      }
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m)
+        z[m] *= -(*reinterpret_cast<const f32x4 *>(lds.rate + 16 * m + 4 * g) * *reinterpret_cast<const f32x4 *>(lds.into + 16 * m + 4 * g));
+      __syncthreads();
       const Cut<kFull> a = cut_tiles<kFull>(z[0], z[1]), c = cut_tiles<kFull>(z[2], z[3]);
-      const u32x4 *p = tri + Tri::kTt * kWave;
+      multiply_columns<KEYS, NP>(grad, k, a, c, lane);
+      if constexpr (BUFFERS == 1) __syncthreads();
+      __syncthreads();
+    }
+    if (r.dh0) keep(r.dh0 + (b * r.heads + head) * states);
+  } else {
+    Fetched<T, KEYS, FRAGS, WHOLE> next;  // keys and T^T of the front's next run, dY of the run behind it
+    Raw8<T> q[TILE ? KEYS / 32 : 1];
+    auto steps = [&](int first) __attribute__((always_inline)) { return min(kRun, span.len - first); };
+    auto fetch_front = [&](int first) __attribute__((always_inline)) {
+      next.fetch_keys(thread, r.k, keys, span.batch, span.row + first, steps(first), key_head);
+      next.fetch_factors(thread, w.triangles + (at(first) * Tri::kAll + Tri::kTt) * kWave, w.factors[at(first)]);
+    };
+    auto put_front = [&](int first, int buffer) __attribute__((always_inline)) {
+      next.put_factors(thread, lds);
+      next.put_keys(thread, lds.k[buffer], keys, steps(first));
+    };
+    auto fetch_back = [&](int first) __attribute__((always_inline)) {
+      next.fetch_values(thread, r.dy, values, span.batch, span.row + first, steps(first), head, first_col);
+      if constexpr (TILE)
+        fetch_rows<T, KEYS, WHOLE>(q, thread, r.q, keys, span.batch, span.row + first, steps(first), key_head);
+    };
+    auto put_back = [&](int first) __attribute__((always_inline)) {
+      next.put_values(thread, lds, values, steps(first), first_col);
+      if constexpr (TILE) put_rows<T, KEYS, WHOLE>(q, thread, lds.q, keys, steps(first));
+    };
+    f32x4 z[kTiles], d[KEYS / 16], into[kTiles];
+    Cut<kFull> p[kFrags];  // P^T
+    auto fetch_own = [&](int first) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i)
+        p[i] = load_frag<kFull>(w.triangles + (at(first) * Tri::kAll + Tri::kP) * kWave, i, Tri::kPParts, lane);
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) into[m] = *reinterpret_cast<const f32x4 *>(w.factors[at(first)].into + 16 * m + 4 * g);
+    };
+    auto compute = [&](int first) __attribute__((always_inline)) {
+      f32x4 dy[kTiles];
 #pragma unroll
       for (int m = 0; m < kTiles; ++m) {
+        dy[m] = value_column(lds.v, m, 16 * wave, lane);
         z[m] = f32x4{0, 0, 0, 0};
-        if (m < 2) multiply<kFull>(z[m], load_frag<kFull>(p, upper_frag(m, 0), Tri::kTtParts, lane), a);
-        multiply<kFull>(z[m], load_frag<kFull>(p, upper_frag(m, 1), Tri::kTtParts, lane), c);
       }
-    }
+      {
+        const Cut<NP> a = cut_tiles<NP>(dy[0], dy[1]), c = cut_tiles<NP>(dy[2], dy[3]);
+        multiply_triangle<kFull, true, false>(z, p, a, c);
+      }
+      part_done();
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      const f32x4 into = *reinterpret_cast<const f32x4 *>(f.into + 16 * m + 4 * g);
-      const f32x4 rate = *reinterpret_cast<const f32x4 *>(f.rate + 16 * m + 4 * g);
-      z[m] *= -(rate * into);
-      dy[m] *= into * r.scale;
-    }
-    const float whole = f.into[kRun - 1];
-    const Cut<kFull> za = cut_tiles<kFull>(z[0], z[1]), zc = cut_tiles<kFull>(z[2], z[3]);
-    const Cut<kFull> ya = cut_tiles<kFull>(dy[0], dy[1]), yc = cut_tiles<kFull>(dy[2], dy[3]);
+      for (int m = 0; m < kTiles; ++m) dy[m] *= r.scale * into[m];
+      const Cut<kFull> a = cut_tiles<kFull>(dy[0], dy[1]), c = cut_tiles<kFull>(dy[2], dy[3]);
 #pragma unroll
-    for (int t = 0; t < KEYS / 16; ++t) {
-      grad[t] *= whole;
-      multiply<kFull>(grad[t], tile_columns<KEYS, NP>(ktile, t, 0, lane), za);
-      multiply<kFull>(grad[t], tile_columns<KEYS, NP>(ktile, t, 1, lane), zc);
-      multiply<kFull>(grad[t], tile_columns<KEYS, NP>(qtile, t, 0, lane), ya);
-      multiply<kFull>(grad[t], tile_columns<KEYS, NP>(qtile, t, 1, lane), yc);
+      for (int t = 0; t < KEYS / 16; ++t) d[t] = f32x4{0, 0, 0, 0};
+      if constexpr (TILE) {
+        multiply_columns<KEYS, NP>(d, lds.q, a, c, lane);
+      } else {
+#pragma unroll
+        for (int t = 0; t < KEYS / 16; ++t) {  // straight from memory, as results hold the steps
+          const int key = key_of(t, x / 4, x % 4), n = steps(first);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const f32x4 lo = load_column<T>(r.q, span.batch, span.row + first, n, key_head, 2 * s, g, key, key < keys);
+            const f32x4 hi = load_column<T>(r.q, span.batch, span.row + first, n, key_head, 2 * s + 1, g, key, key < keys);
+            multiply<kFull>(d[t], cut_tiles<NP>(lo, hi), s ? c : a);
+          }
+          part_done();
+        }
+      }
+    };
+    auto leave = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) lds.z[wave][m][lane] = z[m];
+#pragma unroll
+      for (int t = 0; t < KEYS / 16; ++t) lds.d[wave][t][lane] = d[t];
+    };
+    if (last >= 0) {
+      fetch_own(last);
+      fetch_front(last);
+      fetch_back(last);
+      put_front(last, 0);
+      put_back(last);
+    }
+    __syncthreads();
+    // the first run's products by themselves; then always one run ahead
+    if (last >= 0) {
+      compute(last);
+      const int then = max(last - kRun, 0);
+      fetch_back(then);
+      fetch_own(then);
+      leave();
+    }
+    __syncthreads();
+    if (last >= 0) put_back(max(last - kRun, 0));
+    __syncthreads();
+    for (int first = last, buffer = 0; first >= 0; first -= kRun, buffer = (buffer + 1) % BUFFERS) {
+      again();
+      // in front of the first run that one again: loads stand in no branch
+      const int then = max(first - kRun, 0), later = max(then - kRun, 0);
+      fetch_front(then);
+      fetch_back(later);
+      compute(then);
+      __syncthreads();
+      again();
+      leave();
+      if constexpr (BUFFERS == 2) put_front(then, 1 - buffer);
+      put_back(later);
+      fetch_own(later);
+      if constexpr (BUFFERS == 1) {
+        __syncthreads();
+        put_front(then, 0);
+      }
+      __syncthreads();
     }
   }
-  if (r.dh0) keep(r.dh0 + (b * r.heads + head) * states);
 }
 
 // ------------------------------------------------------------ one run's gradients
 // A workgroup has one run of one head of queries and keys, and goes through the
 // heads that share it, so that their gradients add up in registers. Values are
-// taken 64 columns at a time: 16 for a wave while U and Z are computed, then all
-// of them for a wave's own keys.
-constexpr int kValues = 64;
+// taken kValues columns at a time: four waves compute U, 16 columns each, four
+// others Z; then all of them take products over the values, each for keys (and
+// steps) of its own, transposed, so that a lane has four neighbouring keys.
+constexpr int kGradWaves = 8;
+constexpr int kGradThreads = kGradWaves * kWave;
 constexpr int kGrams = 10;  // 16x16 tiles of a lower triangle of kRun
+constexpr int kGradJobs = (2 * kGrams + kGradWaves - 1) / kGradWaves;
 
 __host__ __device__ constexpr int gram_row(int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; }
 __host__ __device__ constexpr int gram_col(int t) { return t - gram_row(t) * (gram_row(t) + 1) / 2; }
 
+// The sum over 16 neighbouring lanes, in each of them.
 __device__ __forceinline__ float across16(float v) {
-#pragma unroll
-  for (int d = 1; d < 16; d *= 2) v += __shfl_xor(v, d);
-  return v;
+  auto turned = [](float f, auto by) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(f), 0x120 + decltype(by)::value, 0xf, 0xf, true));
+  };
+  v += turned(v, Const<8>{});
+  v += turned(v, Const<4>{});
+  v += turned(v, Const<2>{});
+  return v + turned(v, Const<1>{});
+}
+__device__ __forceinline__ float across_groups(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
 }
 
 template <typename T, int KEYS>
@@ -144,28 +256,57 @@ struct GradsLds {
   static constexpr int NP = kParts<T>, NO = kOut<T>, VR = kTileRow<kValues>;
   alignas(16) uint16_t k[NP * kRun * kTileRow<KEYS>];  // keys, and at the end queries
   union {
+    // U and Z first as they are, then with dY as they stand in the gradients' rows; u holds V's rows before U's
     struct {
-      alignas(16) uint16_t u[NO * kRun * VR], z[NO * kRun * VR], dy[NP * kRun * VR];
+      alignas(16) uint16_t u[NO * kRun * VR], z[NO * kRun * VR], dy[NO * kRun * VR];
     } one;
     struct {
       alignas(16) uint16_t f[NO * kRun * VR], h[NO * kRun * VR];
     } two;
   };
-  float rows[kBackWaves][kRun];   // dG by row, of each wave's keys
-  float lasts[kBackWaves];        // what the last step's G has beside
-  float rates[kBackWaves][kRun];  // z . x by row, of each wave's values
+  alignas(16) Factors f;
+  float sums[kFrontWaves][kRun];   // what of dG goes through the states by the keys, of each wave's values
+  float rates[kFrontWaves][kRun];  // z . x, of each wave's values
+  float turns[KEYS / 16][kRun];    // q . dq, of each 16 keys
+  float lasts[kGradWaves];         // what the last step's G has beside
   float gram_rows[2 * kGrams][16], gram_cols[2 * kGrams][16], gram_rates[kGrams][16];
 };
 
-template <typename T, int KEYS>
-__global__ __launch_bounds__(kBackThreads) void delta_grads_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
+// One column of four result tiles as parts, for all waves to read by rows.
+template <int N, int ROW>
+__device__ __forceinline__ void put_column(uint16_t *tile, const f32x4 (&v)[kTiles], int col, int lane) {
+#pragma unroll
+  for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float rest = v[m][i];
+#pragma unroll
+      for (int p = 0; p < N; ++p) {
+        const __bf16 part = static_cast<__bf16>(rest);
+        tile[(p * kRun + 16 * m + 4 * (lane / 16) + i) * ROW + col + lane % 16] = __builtin_bit_cast(uint16_t, part);
+        rest -= static_cast<float>(part);
+      }
+    }
+}
+__device__ __forceinline__ f32x4 factor4(const float *f, int m, int lane) {
+  return *reinterpret_cast<const f32x4 *>(f + 16 * m + 4 * (lane / 16));
+}
+
+template <typename T, int KEYS, bool WHOLE>
+__global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
+    fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Tri = Triangles<T, true>;
   using Lds = GradsLds<T, KEYS>;
-  constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32, VR = Lds::VR;
-  constexpr int KT = KEYS / 16 > kBackWaves ? KEYS / 16 / kBackWaves : 1;  // tiles of keys a wave
-  constexpr int JOBS = 2 * kGrams / kBackWaves;
+  constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32, VR = Lds::VR, KR = kTileRow<KEYS>;
+  constexpr int KT = KEYS / 16, MT = kTiles * KT / kGradWaves;  // tiles of keys, and of steps for one of them a wave
   __shared__ Lds lds;
-  const int wave = threadIdx.x / kWave, lane0 = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), column = wave % kFrontWaves;
+  const bool first_side = wave < kFrontWaves;
+  const int tile_k = wave % KT, tile_m = wave / KT * MT;  // this wave's keys and steps
+  int thread = threadIdx.x, lane = thread % kWave, x = lane % 16, g = lane / 16;
+  auto again = [&]() __attribute__((always_inline)) {
+    thread = afresh(thread), lane = thread % kWave, x = lane % 16, g = lane / 16;
+  };
   const int64_t slot = blockIdx.x / r.key_heads, key_head = blockIdx.x % r.key_heads;
   const Slot where = slot_of(r, slot);
   if (where.first < 0) return;
@@ -175,240 +316,277 @@ __global__ __launch_bounds__(kBackThreads) void delta_grads_kernel(fftmv_delta_r
   const int64_t row = span.row + where.first, states = r.keys * r.values;
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
   const int share = static_cast<int>(r.heads / r.key_heads);
-  const bool mine = wave * KT < KEYS / 16;  // this wave has keys
 
-  f32x4 dq[kTiles][KT], dk[kTiles][KT];
+  // rows of 8 * CHUNKS elements into a tile
+  auto fill = [&](uint16_t *tile, auto chunks, const Rows<T, WHOLE> &rows, int from) __attribute__((always_inline)) {
+    constexpr int C = decltype(chunks)::value;
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
+    for (int i = 0; i < (kRun * C + kGradThreads - 1) / kGradThreads; ++i) {
+      const int u = thread + i * kGradThreads, t = u / C, c = u % C * 8;
+      if (kRun * C % kGradThreads && u >= kRun * C) break;
+      Raw8<T> v = rows.load(t, from + c);
+      if (!WHOLE || from + 8 * C > rows.width) settle<WHOLE>(v, from + c, rows.width, t < n);
+      const auto parts = cut_raw<T>(v);
 #pragma unroll
-    for (int c = 0; c < KT; ++c) dq[m][c] = dk[m][c] = f32x4{0, 0, 0, 0};
+      for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * (8 * C + 8) + c) = parts.p[p];
+    }
+  };
+
+  f32x4 dq[MT], dk[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) dq[m] = dk[m] = f32x4{0, 0, 0, 0};
+  double turned = 0.0;  // wave 0, lane i: q_i . dq_i over the heads so far
 
   for (int64_t head = key_head * share; head < (key_head + 1) * share; ++head) {
+    again();
     const int64_t at = slot * r.heads + head;
-    const Factors &f = w.factors[at];
     const u32x4 *tri = w.triangles + at * Tri::kAll * kWave;
-    const float *state = r.carries + at * states, *grad = w.grads + at * states;
-    f32x4 aq[kTiles][KT], az[kTiles][KT], au[kTiles][KT], gram[JOBS], zx[kTiles];
+    // states and their gradients: rows behind the last read as zeros
+    const auto state = __builtin_amdgcn_make_buffer_rsrc(r.carries + at * states, 0, static_cast<int>(states * 4), kBufferFlags);
+    const auto grad = __builtin_amdgcn_make_buffer_rsrc(w.grads + at * states, 0, static_cast<int>(states * 4), kBufferFlags);
+    f32x4 gram[kGradJobs];
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      zx[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int c = 0; c < KT; ++c) aq[m][c] = az[m][c] = au[m][c] = f32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int q = 0; q < JOBS; ++q) gram[q] = f32x4{0, 0, 0, 0};
-    int lane = afresh(lane0), x = lane % 16, g = lane / 16;
-    auto again = [&] { lane = afresh(lane0), x = lane % 16, g = lane / 16; };
-    float dot = 0.0f;  // <state, its gradient>, of this wave's values
+    for (int q = 0; q < kGradJobs; ++q) gram[q] = f32x4{0, 0, 0, 0};
+    float last = 0.0f;  // of this wave's values: e^{G_last} <state, its gradient> and the sum of k . o
     __syncthreads();
-    fill_tile<T, KEYS, kBackThreads>(lds.k, r.k, span.batch, row, n, key_head, keys);
+    fill(lds.k, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.k, span.batch, row, key_head, n, keys), 0);
+    if (thread < static_cast<int>(sizeof(Factors) / 16))
+      reinterpret_cast<u32x4 *>(&lds.f)[thread] = at_lane(reinterpret_cast<const u32x4 *>(w.factors + at), thread);
+    if (thread < kFrontWaves * kRun) lds.sums[0][thread] = lds.rates[0][thread] = 0.0f;
 
     for (int from = 0; from < values; from += kValues) {
-      __syncthreads();
-      fill_tile<T, kValues, kBackThreads>(lds.one.dy, r.dy, span.batch, row, n, head, values, from);
+      if (from) __syncthreads();
       again();
-      const int col = from + 16 * wave + x;
+      const int col = from + 16 * column + x;
       const bool inside = col < values;
-      // U and Z of 16 columns
-      f32x4 u[kTiles], z[kTiles];
+      // one side's columns of the state, the other's of its gradient
+      float a[S][8];
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) u[m] = z[m] = f32x4{0, 0, 0, 0};
+      for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          a[s][e] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(first_side ? state : grad, ((32 * s + e + 8 * g) * values + col) * 4, 0, 0));
+      fill(lds.one.dy, Const<kValues / 8>{}, Rows<T, WHOLE>(r.dy, span.batch, row, head, n, values), from);
+      if constexpr (sizeof(T) == 2) {
+        const int t = thread / (kValues / 8), c = thread % (kValues / 8) * 8;
+        Raw8<T> v = Rows<T, WHOLE>(r.v, span.batch, row, head, n, values).load(t, from + c);
+        if (!WHOLE || from + kValues > values) settle<WHOLE>(v, from + c, values, t < n);
+        *reinterpret_cast<u32x4 *>(lds.one.u + t * VR + c) = v.w[0];
+      }
       __syncthreads();
+      if (from + kValues > values) {
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a[s][e] = inside ? a[s][e] : 0.0f;
+      }
+      f32x4 o[kTiles], p[kTiles], in[kTiles];  // U's side: U, K S and X; Z's: Z, its part through K
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) p[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        float a[8], d[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int key = 32 * s + 8 * g + e;
-          const bool there = inside && key < keys;
-          a[e] = there ? state[static_cast<int64_t>(key) * values + col] : 0.0f;
-          d[e] = there ? grad[static_cast<int64_t>(key) * values + col] : 0.0f;
-          dot = fmaf(a[e], d[e], dot);
-        }
-        const Cut<NO> sp = cut<NO>(a), dp = cut<NO>(d);
+        Cut<NP> k[kTiles];
+        tile_rows<KEYS>(k, lds.k, s, lane);
+        multiply_rows<NO>(p, k, cut<NO>(a[s]));
+      }
+      part_done();
+      if (first_side) {
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
-          const Cut<NP> k = tile_rows<KEYS, NP>(lds.k, m, s, lane);
-          multiply<NO>(u[m], k, sp);
-          multiply<NO>(z[m], k, dp);
+          f32x4 v;
+          if constexpr (sizeof(T) == 2)
+            v = value_column(reinterpret_cast<const T *>(lds.one.u), m, 16 * column, lane);
+          else
+            v = load_column<T>(r.v, span.batch, row, n, head, m, g, col, inside);
+          p[m] *= factor4(lds.f.into, m, lane);
+          in[m] = v - p[m];
+          o[m] = f32x4{0, 0, 0, 0};
         }
+        multiply_triangle<NO, NO, Tri::kTParts, false>(o, tri, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]), lane);
+        put_column<NO, VR>(lds.one.u, o, 16 * column, lane);
+      } else {
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          p[m] *= factor4(lds.f.out, m, lane);
+          in[m] = p[m];
+          o[m] = f32x4{0, 0, 0, 0};
+        }
+        multiply_triangle<NO, NO, Tri::kPParts, true>(in, tri + Tri::kP * kWave, plain_columns<VR, NP, 16>(lds.one.dy, 0, 16 * column, lane),
+                                                      plain_columns<VR, NP, 16>(lds.one.dy, 32, 16 * column, lane), lane);
         part_done();
+        multiply_triangle<NO, NO, Tri::kTtParts, true>(o, tri + Tri::kTt * kWave, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]), lane);
+        put_column<NO, VR>(lds.one.z, o, 16 * column, lane);
       }
+      __syncthreads();
+      again();
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        again();
-        const f32x4 v = load_column<T>(r.v, span.batch, row, n, head, m, g, col, inside);
-        const f32x4 into = *reinterpret_cast<const f32x4 *>(f.into + 16 * m + 4 * g);
-        u[m] = v - into * u[m];
-        z[m] *= *reinterpret_cast<const f32x4 *>(f.out + 16 * m + 4 * g);
-      }
-      f32x4 xs[kTiles];
+      for (int q = 0; q < kGradJobs; ++q) {
+        const int job = wave + kGradWaves * q, tile = job < kGrams ? job : job - kGrams;
+        if (job >= 2 * kGrams) break;
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) xs[m] = u[m];
-      {
-        const Cut<NO> a = cut_tiles<NO>(u[0], u[1]), c = cut_tiles<NO>(u[2], u[3]);
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          u[m] = f32x4{0, 0, 0, 0};
-          multiply<NO>(u[m], load_frag<NO>(tri, lower_frag(m, 0), Tri::kTParts, lane), a);
-          if (m >= 2) multiply<NO>(u[m], load_frag<NO>(tri, lower_frag(m, 1), Tri::kTParts, lane), c);
+        for (int s = 0; s < kValues / 32; ++s) {
+          const Cut<NO> u = tile_rows<kValues, NO>(lds.one.u, gram_col(tile), s, lane);
+          if (job < kGrams)
+            multiply<NO>(gram[q], tile_rows<kValues, NP>(lds.one.dy, gram_row(tile), s, lane), u);
+          else
+            multiply<NO>(gram[q], tile_rows<kValues, NO>(lds.one.z, gram_row(tile), s, lane), u);
         }
       }
       part_done();
-      {
-        const u32x4 *p = tri + Tri::kP * kWave;
-        const Cut<NP> a = plain_columns<VR, NP, 16>(lds.one.dy, 0, 16 * wave, lane);
-        const Cut<NP> c = plain_columns<VR, NP, 16>(lds.one.dy, 32, 16 * wave, lane);
+      {  // dV by rows, eight columns a thread
+        const int t = thread / (kValues / 8), c = from + thread % (kValues / 8) * 8;
+        float v[8] = {};
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          if (m < 2) multiply<NO>(z[m], load_frag<NO>(p, upper_frag(m, 0), Tri::kPParts, lane), a);
-          multiply<NO>(z[m], load_frag<NO>(p, upper_frag(m, 1), Tri::kPParts, lane), c);
+        for (int part = NO - 1; part >= 0; --part) {
+          const bf16x8 b = *reinterpret_cast<const bf16x8 *>(lds.one.z + (part * kRun + t) * VR + c - from);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += static_cast<float>(b[e]);
         }
-      }
-      part_done();
-      {
-        const Cut<NO> a = cut_tiles<NO>(z[0], z[1]), c = cut_tiles<NO>(z[2], z[3]);
-        const u32x4 *p = tri + Tri::kTt * kWave;
+        const float rate = lds.f.rate[t];
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          z[m] = f32x4{0, 0, 0, 0};
-          if (m < 2) multiply<NO>(z[m], load_frag<NO>(p, upper_frag(m, 0), Tri::kTtParts, lane), a);
-          multiply<NO>(z[m], load_frag<NO>(p, upper_frag(m, 1), Tri::kTtParts, lane), c);
-        }
-      }
+        for (int e = 0; e < 8; ++e) v[e] *= rate;
+        if (t < n) {
+          T *to = head_row<T>(r.dv, span.batch, row + t, head) + c;
+          if (c + 8 <= values) {
+            if constexpr (sizeof(T) == 2) {
+              store_vec(to, v, false);
+            } else {
+              const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+              store_vec(to, lo, false);
+              store_vec(to + 4, hi, false);
+            }
+          } else {
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        again();
-        const f32x4 rate = *reinterpret_cast<const f32x4 *>(f.rate + 16 * m + 4 * g);
-        zx[m] += z[m] * xs[m];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 16 * m + 4 * g + i;
-          if (inside && t < n) head_row<T>(r.dv, span.batch, row + t, head)[col] = static_cast<T>(rate[i] * z[m][i]);
-          float ur = u[m][i], zr = z[m][i];
-#pragma unroll
-          for (int p = 0; p < NO; ++p) {
-            const __bf16 ub = static_cast<__bf16>(ur), zb = static_cast<__bf16>(zr);
-            lds.one.u[(p * kRun + t) * VR + 16 * wave + x] = __builtin_bit_cast(uint16_t, ub);
-            lds.one.z[(p * kRun + t) * VR + 16 * wave + x] = __builtin_bit_cast(uint16_t, zb);
-            ur -= static_cast<float>(ub);
-            zr -= static_cast<float>(zb);
+            for (int e = 0; e < 8; ++e)
+              if (c + e < values) to[e] = static_cast<T>(v[e]);
           }
         }
       }
+      part_done();
+      again();
+      if (first_side) {
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const f32x4 z = tile_values<VR, NO>(lds.one.z, m, 16 * column, lane);
+          const f32x4 rate = factor4(lds.f.rate, m, lane) * z;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float zk = across16(rate[i] * p[m][i]), zx = across16(z[i] * in[m][i]);
+            if (x == 0) {
+              lds.sums[column][16 * m + 4 * g + i] += zk;
+              lds.rates[column][16 * m + 4 * g + i] += zx;
+            }
+          }
+          in[m] = tile_values<VR, NP>(lds.one.dy, m, 16 * column, lane) * (factor4(lds.f.into, m, lane) * r.scale);
+          o[m] *= factor4(lds.f.out, m, lane);
+        }
+      }
       __syncthreads();
-      // products over the values: this wave's keys, and its tiles of the triangles
+      if (first_side) {
+        put_column<NO, VR>(lds.one.dy, in, 16 * column, lane);
+      } else {  // lds.sums is the other side's up to here
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const f32x4 uk = tile_values<VR, NO>(lds.one.u, m, 16 * column, lane) * p[m];
+          last += (uk[0] + uk[1]) + (uk[2] + uk[3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float sum = across16(uk[i]);
+            if (x == 0) lds.sums[column][16 * m + 4 * g + i] += sum;
+          }
+          o[m] *= -(factor4(lds.f.rate, m, lane) * factor4(lds.f.into, m, lane));
+        }
+        put_column<NO, VR>(lds.one.z, o, 16 * column, lane);
+      }
+      // rows of the state and its gradient
+      Cut<NO> sp[kValues / 32], dp[kValues / 32];
+      again();
 #pragma unroll
       for (int s = 0; s < kValues / 32; ++s) {
-        again();
-        const int c0 = from + 32 * s + 8 * g;
-        if (mine) {
-          Cut<NO> sp[KT], dp[KT];
+        const int c = from + 32 * s + 8 * g, byte = ((16 * tile_k + x) * values + c) * 4;
+        float b[2][8];
 #pragma unroll
-          for (int c = 0; c < KT; ++c) {
-            const int key = 16 * (wave * KT + c) + x;
-            sp[c] = load_wide<NO>(state + static_cast<int64_t>(min(key, keys - 1)) * values, c0, values, key < keys);
-            dp[c] = load_wide<NO>(grad + static_cast<int64_t>(min(key, keys - 1)) * values, c0, values, key < keys);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(state, byte + 16 * h, 0, 0);
+          const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(grad, byte + 16 * h, 0, 0);
 #pragma unroll
-          for (int m = 0; m < kTiles; ++m) {
-            const Cut<NP> y = tile_rows<kValues, NP>(lds.one.dy, m, s, lane);
-            const Cut<NO> zz = tile_rows<kValues, NO>(lds.one.z, m, s, lane), uu = tile_rows<kValues, NO>(lds.one.u, m, s, lane);
-#pragma unroll
-            for (int c = 0; c < KT; ++c) {
-              multiply<NO>(aq[m][c], y, sp[c]);
-              multiply<NO>(az[m][c], zz, sp[c]);
-              multiply<NO>(au[m][c], uu, dp[c]);
-            }
-            part_done();
+          for (int e = 0; e < 4; ++e) {
+            b[0][4 * h + e] = __uint_as_float(lo[e]);
+            b[1][4 * h + e] = __uint_as_float(hi[e]);
           }
         }
+        if (from + kValues > values) {
 #pragma unroll
-        for (int q = 0; q < JOBS; ++q) {
-          const int job = wave + kBackWaves * q, tile = job < kGrams ? job : job - kGrams;
-          const Cut<NO> uu = tile_rows<kValues, NO>(lds.one.u, gram_col(tile), s, lane);
-          if (job < kGrams)
-            multiply<NO>(gram[q], tile_rows<kValues, NP>(lds.one.dy, gram_row(tile), s, lane), uu);
-          else
-            multiply<NO>(gram[q], tile_rows<kValues, NO>(lds.one.z, gram_row(tile), s, lane), uu);
-          part_done();
+          for (int e = 0; e < 8; ++e) {
+            b[0][e] = c + e < values ? b[0][e] : 0.0f;
+            b[1][e] = c + e < values ? b[1][e] : 0.0f;
+          }
         }
+        if (wave / KT == 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) last = fmaf(b[0][e] * lds.f.into[kRun - 1], b[1][e], last);
+        }
+        sp[s] = cut<NO>(b[0]);
+        dp[s] = cut<NO>(b[1]);
       }
+      __syncthreads();
+      if (first_side) put_column<NO, VR>(lds.one.u, o, 16 * column, lane);
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < kValues / 32; ++s)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          multiply<NO>(dq[m], sp[s], tile_rows<kValues, NO>(lds.one.dy, tile_m + m, s, lane));
+          multiply<NO>(dk[m], sp[s], tile_rows<kValues, NO>(lds.one.z, tile_m + m, s, lane));
+          multiply<NO>(dk[m], dp[s], tile_rows<kValues, NO>(lds.one.u, tile_m + m, s, lane));
+        }
     }
-    again();
+    last = across_groups(across16(last));
+    if (lane == 0) lds.lasts[wave] = last;
     __syncthreads();  // u, z and dy are done with
-    // what goes through the states
-    f32x4 sums[kTiles];
-    {
-      float last = 0.0f;
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        const f32x4 into = *reinterpret_cast<const f32x4 *>(f.into + 16 * m + 4 * g);
-        const f32x4 out = *reinterpret_cast<const f32x4 *>(f.out + 16 * m + 4 * g);
-        const f32x4 rate = *reinterpret_cast<const f32x4 *>(f.rate + 16 * m + 4 * g);
-        sums[m] = f32x4{0, 0, 0, 0};
-        f32x4 behind = {0, 0, 0, 0};
-#pragma unroll
-        for (int c = 0; c < KT; ++c) {
-          const f32x4 d = az[m][c] * (into * rate), o = au[m][c] * out;
-          aq[m][c] *= into * r.scale;
-          dq[m][c] += aq[m][c];
-          dk[m][c] += o - d;
-          if (mine) {
-            const f32x4 k = tile_values<kTileRow<KEYS>, NP>(lds.k, m, 16 * (wave * KT + c), lane);
-            sums[m] -= k * d;
-            behind += k * o;
-          }
-        }
-        sums[m] -= behind;
-        last += behind[0] + behind[1] + behind[2] + behind[3];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float zr = across16(zx[m][i]);
-          if (x == 0) lds.rates[wave][16 * m + 4 * g + i] = zr;
-        }
-      }
-      last = fmaf(f.into[kRun - 1], dot, last);
-      last = across16(last);
-      last += __shfl_xor(last, 16);
-      last += __shfl_xor(last, 32);
-      if (lane == 0) lds.lasts[wave] = last;
-    }
-    part_done();
+
     // what goes through the triangles
 #pragma unroll
-    for (int q = 0; q < JOBS; ++q) {
+    for (int q = 0; q < kGradJobs; ++q) {
       again();
-      const int job = wave + kBackWaves * q, tile = job < kGrams ? job : job - kGrams;
+      const int job = wave + kGradWaves * q, tile = job < kGrams ? job : job - kGrams;
+      if (job >= 2 * kGrams) break;
       const int m = gram_row(tile), c = gram_col(tile), j = 16 * c + x;
       f32x4 raw = {0, 0, 0, 0};
+      if (job < kGrams) {
+        const Rows<T, WHOLE> rows(r.q, span.batch, row, key_head, n, keys);
+        Raw8<T> own[S];
 #pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const Cut<NP> kc = tile_rows<KEYS, NP>(lds.k, c, s, lane);
-        if (job < kGrams)
-          multiply<NO>(raw,
-                       load_cut(head_row<T>(r.q, span.batch, row + min(16 * m + x, n - 1), key_head), 32 * s + 8 * g,
-                                keys, 16 * m + x < n),
-                       kc);
-        else
-          multiply<NO>(raw, tile_rows<KEYS, NP>(lds.k, m, s, lane), kc);
+        for (int s = 0; s < S; ++s) own[s] = rows.load(16 * m + x, 32 * s + 8 * g);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          if (!WHOLE || keys < KEYS) settle<WHOLE>(own[s], 32 * s + 8 * g, keys, 16 * m + x < n);
+          multiply<NO>(raw, cut_raw<T>(own[s]), tile_rows<KEYS, NP>(lds.k, c, s, lane));
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < S; ++s) multiply<NO>(raw, tile_rows<KEYS, NP>(lds.k, m, s, lane), tile_rows<KEYS, NP>(lds.k, c, s, lane));
       }
       uint16_t *to = job < kGrams ? lds.two.f : lds.two.h;
+      const double sum_j = lds.f.sum[j];
       float down = 0.0f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 16 * m + 4 * g + i;
         const bool in = job < kGrams ? j <= t : j < t;
-        const float e = in ? expf(static_cast<float>(f.sum[t] - f.sum[j])) : 0.0f;
-        float v, rate = 0.0f;
+        const float e = in ? expf(static_cast<float>(lds.f.sum[t] - sum_j)) : 0.0f;
+        // dG_t: q . dq holds this row of P but for its diagonal, which e^{G_t - G_t} is no factor of
+        float v = (job < kGrams ? r.scale : -lds.f.rate[t]) * e * gram[q][i], line, rate = 0.0f;
+        if (!in) v = 0.0f;
+        const float p = in ? v * raw[i] : 0.0f;
         if (job < kGrams) {
-          v = in ? r.scale * e * gram[q][i] : 0.0f;
+          line = across16(j == t ? -p : 0.0f);
+          down += j < t ? p : 0.0f;
         } else {
-          v = in ? -f.rate[t] * e * gram[q][i] : 0.0f;
+          line = across16(p);
           rate = across16(in ? -e * raw[i] * gram[q][i] : 0.0f);
+          down += p;
         }
-        const float p = j < t ? v * raw[i] : 0.0f, line = across16(p);
-        down += p;
         if (x == 0) {
           lds.gram_rows[job][4 * g + i] = line;
           if (job >= kGrams) lds.gram_rates[tile][4 * g + i] = rate;
@@ -421,79 +599,62 @@ __global__ __launch_bounds__(kBackThreads) void delta_grads_kernel(fftmv_delta_r
           v -= static_cast<float>(vb);
         }
       }
-      down += __shfl_xor(down, 16);
-      down += __shfl_xor(down, 32);
+      down = across_groups(down);
       if (g == 0) lds.gram_cols[job][x] = down;
       part_done();
     }
     __syncthreads();
 
-    if (mine) {
+    again();
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        Cut<NP> kc[KT];
-        again();
+    for (int s = 0; s < 2; ++s) {
+      const Cut<NP> k = plain_columns<KR, NP, 4>(lds.k, 32 * s, 16 * tile_k, lane);
 #pragma unroll
-        for (int c = 0; c < KT; ++c) kc[c] = plain_columns<kTileRow<KEYS>, NP, 4>(lds.k, 32 * s, 16 * (wave * KT + c), lane);
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          if (in_lower(m, s)) {
-            const Cut<NO> f = tile_rows<kValues, NO>(lds.two.f, m, s, lane), h = tile_rows<kValues, NO>(lds.two.h, m, s, lane);
-#pragma unroll
-            for (int c = 0; c < KT; ++c) {
-              multiply<NO>(dq[m][c], f, kc[c]);
-              multiply<NO>(dk[m][c], h, kc[c]);
-            }
-          }
-          if (in_upper(m, s)) {
-            const Cut<NO> h = plain_columns<VR, NO, 4>(lds.two.h, 32 * s, 16 * m, lane);
-#pragma unroll
-            for (int c = 0; c < KT; ++c) multiply<NO>(dk[m][c], h, kc[c]);
-          }
-          part_done();
+      for (int m = 0; m < MT; ++m) {
+        if (in_lower(tile_m + m, s)) {
+          multiply<NO>(dq[m], k, tile_rows<kValues, NO>(lds.two.f, tile_m + m, s, lane));
+          multiply<NO>(dk[m], k, tile_rows<kValues, NO>(lds.two.h, tile_m + m, s, lane));
         }
+        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], k, plain_columns<VR, NO, 4>(lds.two.h, 32 * s, 16 * (tile_m + m), lane));
       }
     }
     __syncthreads();
-    fill_tile<T, KEYS, kBackThreads>(lds.k, r.q, span.batch, row, n, key_head, keys);
+    fill(lds.k, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.q, span.batch, row, key_head, n, keys), 0);
     __syncthreads();
-    if (mine) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        Cut<NP> qc[KT];
-        again();
+    for (int s = 0; s < 2; ++s) {
+      const Cut<NP> q = plain_columns<KR, NP, 4>(lds.k, 32 * s, 16 * tile_k, lane);
 #pragma unroll
-        for (int c = 0; c < KT; ++c) qc[c] = plain_columns<kTileRow<KEYS>, NP, 4>(lds.k, 32 * s, 16 * (wave * KT + c), lane);
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m)
-          if (in_upper(m, s)) {
-            const Cut<NO> f = plain_columns<VR, NO, 4>(lds.two.f, 32 * s, 16 * m, lane);
-#pragma unroll
-            for (int c = 0; c < KT; ++c) multiply<NO>(dk[m][c], f, qc[c]);
-            part_done();
-          }
-      }
+      for (int m = 0; m < MT; ++m)
+        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], q, plain_columns<VR, NO, 4>(lds.two.f, 32 * s, 16 * (tile_m + m), lane));
     }
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
+    for (int m = 0; m < MT; ++m) {  // q . dq: step 16 m + x, four keys
+      float sum = 0.0f;
+      const int t = 16 * (tile_m + m) + x;
 #pragma unroll
-      for (int c = 0; c < KT; ++c)
-        if (mine) sums[m] += aq[m][c] * tile_values<kTileRow<KEYS>, NP>(lds.k, m, 16 * (wave * KT + c), lane);
+      for (int part = 0; part < NP; ++part) {
+        const uint16_t *q = lds.k + (part * kRun + t) * KR + 16 * tile_k + 4 * g;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float s = across16(sums[m][i]);
-        if (x == 0) lds.rows[wave][16 * m + 4 * g + i] = s;
+        for (int i = 0; i < 4; ++i) sum = fmaf(dq[m][i], __uint_as_float(static_cast<uint32_t>(q[i]) << 16), sum);
       }
+      sum = across_groups(sum);
+      if (g == 0) lds.turns[tile_k][t] = sum;
     }
     __syncthreads();
     if (wave == 0) {  // the gates: lane i has step i
-      double own = 0.0, rate = 0.0, last = 0.0;
+      double own = -turned, rate = 0.0, end = 0.0;
+      turned = 0.0;
 #pragma unroll
-      for (int v = 0; v < kBackWaves; ++v) {
-        own += lds.rows[v][lane];
+      for (int v = 0; v < KT; ++v) turned += lds.turns[v][lane];
+#pragma unroll
+      for (int v = 0; v < kFrontWaves; ++v) {
+        own -= lds.sums[v][lane];
         rate += lds.rates[v][lane];
-        last += lds.lasts[v];
       }
+#pragma unroll
+      for (int v = 0; v < kGradWaves; ++v) end += lds.lasts[v];
+      own += turned;
 #pragma unroll
       for (int job = 0; job < 2 * kGrams; ++job) {
         const int tile = job % kGrams;
@@ -505,7 +666,7 @@ __global__ __launch_bounds__(kBackThreads) void delta_grads_kernel(fftmv_delta_r
       }
       // sum over this step and those behind it
       const double all = lane_sums(own, lane);
-      const double grad_log = __shfl(all, kWave - 1) - all + own + last;
+      const double grad_log = __shfl(all, kWave - 1) - all + own + end;
       if (lane < n) {
         const float gate = static_cast<float>(*head_row<T>(r.gate, span.batch, row + lane, head));
         const float beta = static_cast<float>(*head_row<T>(r.beta, span.batch, row + lane, head));
@@ -517,20 +678,24 @@ __global__ __launch_bounds__(kBackThreads) void delta_grads_kernel(fftmv_delta_r
       }
     }
   }
-  if (mine) {
-    const int lane = afresh(lane0), x = lane % 16, g = lane / 16;
+  again();
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m)
+  for (int m = 0; m < MT; ++m) {
+    const int t = 16 * (tile_m + m) + x, key = 16 * tile_k + 4 * g;
+    if (t >= n) continue;
+    T *q = head_row<T>(r.dq, span.batch, row + t, key_head) + key, *k = head_row<T>(r.dk, span.batch, row + t, key_head) + key;
+    if (key + 4 <= keys) {
+      const float a[4] = {dq[m][0], dq[m][1], dq[m][2], dq[m][3]}, b[4] = {dk[m][0], dk[m][1], dk[m][2], dk[m][3]};
+      store_vec(q, a, false);
+      store_vec(k, b, false);
+    } else {
 #pragma unroll
-      for (int c = 0; c < KT; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 16 * m + 4 * g + i, key = 16 * (wave * KT + c) + x;
-          if (t < n && key < keys) {
-            head_row<T>(r.dq, span.batch, row + t, key_head)[key] = static_cast<T>(dq[m][c][i]);
-            head_row<T>(r.dk, span.batch, row + t, key_head)[key] = static_cast<T>(dk[m][c][i]);
-          }
+      for (int i = 0; i < 4; ++i)
+        if (key + i < keys) {
+          q[i] = static_cast<T>(dq[m][i]);
+          k[i] = static_cast<T>(dk[m][i]);
         }
+    }
   }
 }
 
@@ -539,9 +704,9 @@ hipError_t launch_delta_backward(const fftmv_delta_rule_t &r, hipStream_t s) {
   const int64_t runs = delta_runs(r.batch, r.steps, r.offsets != nullptr);
   DeltaWorkspace w;
   delta_workspace(runs, r.heads, r.keys, r.values, r.dtype, true, r.workspace, &w);
-  const int64_t waves = (r.values + 15) / 16, blocks = (waves + kBackWaves - 1) / kBackWaves;
-  if (!grid_fits(runs * r.heads, kWave) || !grid_fits(runs * r.key_heads, kBackThreads) ||
-      !grid_fits(r.batch * r.heads * blocks, kBackThreads))
+  const int64_t blocks = (r.values + kValues - 1) / kValues;
+  if (!grid_fits(runs * r.heads, kWave) || !grid_fits(runs * r.key_heads, kChainThreads) ||
+      !grid_fits(r.batch * r.heads * blocks, kChainThreads))
     return hipErrorInvalidConfiguration;
   return by_keys(r.keys, [&](auto k) {
     constexpr int KEYS = decltype(k)::value;
@@ -550,10 +715,17 @@ hipError_t launch_delta_backward(const fftmv_delta_rule_t &r, hipStream_t s) {
       if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     const dim3 grid(static_cast<unsigned>(r.batch * r.heads), static_cast<unsigned>(blocks));
-    delta_back_chain_kernel<T, KEYS><<<grid, kBackThreads, 0, s>>>(r, w);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    if (runs > 0) delta_grads_kernel<T, KEYS><<<static_cast<unsigned>(runs * r.key_heads), kBackThreads, 0, s>>>(r, w);
-    return hipGetLastError();
+    const hipError_t e = by_two(delta_whole(r, r.dy, r.dy), [&](auto whole) {
+      delta_back_chain_kernel<T, KEYS, decltype(whole)::value != 0><<<grid, kChainThreads, 0, s>>>(r, w);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    if (runs == 0) return hipSuccess;
+    return by_two(delta_whole(r, r.dy, r.v), [&](auto whole) {
+      delta_grads_kernel<T, KEYS, decltype(whole)::value != 0>
+          <<<static_cast<unsigned>(runs * r.key_heads), kGradThreads, 0, s>>>(r, w);
+      return hipGetLastError();
+    });
   });
 }
 

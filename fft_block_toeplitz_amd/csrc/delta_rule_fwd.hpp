@@ -8,117 +8,204 @@
 
 namespace fftmv {
 
-constexpr int kChainWaves = 4;
-constexpr int kChainThreads = kChainWaves * kWave;
+template <typename T, int KEYS, int BUFFERS, bool TILE>
+struct ForwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
+  alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS> : 8];
+  static constexpr int NO = kOut<T>, S = KEYS / 32;
+  alignas(16) u32x4 s[kFrontWaves][S][NO][kWave];  // the state at the run's start, cut
+  alignas(16) f32x4 u[kFrontWaves][kTiles][kWave];  // U
+};
 
-template <typename T, int KEYS, bool SAVE>
+template <typename T, int KEYS, bool WHOLE, bool SAVE>
 __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Tri = Triangles<T, false>;
-  constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32;
-  __shared__ __align__(16) uint16_t ktile[NP * kRun * kTileRow<KEYS>], qtile[NP * kRun * kTileRow<KEYS>];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, x = lane % 16, g = lane / 16;
+  constexpr int FRAGS = kFrags * kFull, S = KEYS / 32;
+  constexpr bool TILE = sizeof(ForwardLds<T, KEYS, 1, true>) <= kLdsBytes;  // else queries go from memory to registers
+  constexpr int BUFFERS = sizeof(ForwardLds<T, KEYS, 2, TILE>) <= kLdsBytes ? 2 : 1;
+  using Lds = ForwardLds<T, KEYS, BUFFERS, TILE>;
+  constexpr int NP = kParts<T>, NO = kOut<T>;
+  __shared__ Lds lds;
+  const int side = __builtin_amdgcn_readfirstlane(threadIdx.x / kFrontThreads);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % kFrontWaves;
+  int thread = threadIdx.x % kFrontThreads, lane = threadIdx.x % kWave, x = lane % 16, g = lane / 16;
+  auto again = [&]() __attribute__((always_inline)) {
+    thread = afresh(thread), lane = thread % kWave, x = lane % 16, g = lane / 16;
+  };
   const int64_t head = blockIdx.x % r.heads, b = blockIdx.x / r.heads;
   const int64_t key_head = head / (r.heads / r.key_heads);
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
-  const int col = (blockIdx.y * kChainWaves + wave) * 16 + x;
+  const int first_col = blockIdx.y * kValues, col = first_col + wave * 16 + x;
   const bool inside = col < values;
   const Span span = span_of(r, b);
   const int64_t states = r.keys * r.values;
 
-  f32x4 state[KEYS / 16];
-#pragma unroll
-  for (int t = 0; t < KEYS / 16; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = key_of(t, g, i);
-      state[t][i] = r.h0 && inside && key < keys
-                        ? r.h0[(b * r.heads + head) * states + static_cast<int64_t>(key) * values + col]
-                        : 0.0f;
-    }
-
-  auto keep = [&](float *to) {
+  if (side == 0) {
+    f32x4 state[KEYS / 16];
 #pragma unroll
     for (int t = 0; t < KEYS / 16; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = key_of(t, g, i);
-        if (inside && key < keys) to[static_cast<int64_t>(key) * values + col] = state[t][i];
+        state[t][i] = r.h0 && inside && key < keys
+                          ? r.h0[(b * r.heads + head) * states + static_cast<int64_t>(key) * values + col]
+                          : 0.0f;
       }
-  };
-
-  for (int first = 0; first < span.len; first += kRun) {
-    const int n = min(kRun, span.len - first);
-    const int64_t row = span.row + first, at = (span.run + first / kRun) * r.heads + head;
-    const Factors &f = w.factors[at];
-    const u32x4 *tri = w.triangles + at * Tri::kAll * kWave;
-    if constexpr (SAVE) keep(r.carries + at * states);
+    auto keep = [&](float *to) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < KEYS / 16; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int key = key_of(t, g, i);
+          if (inside && key < keys) to[static_cast<int64_t>(key) * values + col] = state[t][i];
+        }
+    };
+    Cut<kFull> part[S];
+    auto leave_state = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        part[s] = cut_tiles<kFull>(state[2 * s], state[2 * s + 1]);
+#pragma unroll
+        for (int p = 0; p < NO; ++p) lds.s[wave][s][p][lane] = part[s].p[p];
+      }
+    };
+    leave_state();
     __syncthreads();
-    fill_tile<T, KEYS, kChainThreads>(ktile, r.k, span.batch, row, n, key_head, keys);
-    fill_tile<T, KEYS, kChainThreads>(qtile, r.q, span.batch, row, n, key_head, keys);
-    f32x4 v[kTiles];
+    for (int first = 0, buffer = 0; first < span.len; first += kRun, buffer = (buffer + 1) % BUFFERS) {
+      const uint16_t *k = lds.k[buffer];
+      again();
+      f32x4 u[kTiles];
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) v[m] = load_column<T>(r.v, span.batch, row, n, head, m, g, col, inside);
-    __syncthreads();
-
-    f32x4 u[kTiles], y[kTiles];
+      for (int m = 0; m < kTiles; ++m) u[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) u[m] = y[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int s = 0; s < S; ++s) {
-      const Cut<kFull> part = cut_tiles<kFull>(state[2 * s], state[2 * s + 1]);
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        multiply<kFull>(u[m], tile_rows<KEYS, NP>(ktile, m, s, lane), part);
-        multiply<NO>(y[m], tile_rows<KEYS, NP>(qtile, m, s, lane), part);
+      for (int s = 0; s < S; ++s) {
+        Cut<NP> rows[kTiles];
+        tile_rows<KEYS>(rows, k, s, lane);
+        multiply_rows<kFull>(u, rows, part[s]);
       }
-    }
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      const f32x4 into = *reinterpret_cast<const f32x4 *>(f.into + 16 * m + 4 * g);
+      for (int m = 0; m < kTiles; ++m)
+        u[m] = value_column(lds.v, m, 16 * wave, lane) - *reinterpret_cast<const f32x4 *>(lds.into + 16 * m + 4 * g) * u[m];
+      {
+        const Cut<kFull> a = cut_tiles<kFull>(u[0], u[1]), c = cut_tiles<kFull>(u[2], u[3]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        u[m][i] = fmaf(-into[i], u[m][i], v[m][i]);
-        y[m][i] *= r.scale * into[i];
+        for (int m = 0; m < kTiles; ++m) u[m] = f32x4{0, 0, 0, 0};
+        multiply_triangle<kFull, kFull, kFull, false>(u, lds.frags, a, c, lane);
       }
-    }
-    {
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) lds.u[wave][m][lane] = u[m];
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) u[m] *= *reinterpret_cast<const f32x4 *>(lds.out + 16 * m + 4 * g);
+      const float whole = lds.into[kRun - 1];
+      if constexpr (SAVE) keep(r.carries + ((span.run + first / kRun) * r.heads + head) * states);
+      __syncthreads();
       const Cut<kFull> a = cut_tiles<kFull>(u[0], u[1]), c = cut_tiles<kFull>(u[2], u[3]);
 #pragma unroll
+      for (int t = 0; t < KEYS / 16; ++t) state[t] *= whole;
+      multiply_columns<KEYS, NP>(state, k, a, c, lane);
+      if constexpr (BUFFERS == 1) __syncthreads();
+      leave_state();
+      __syncthreads();
+    }
+    if (r.h_last) keep(r.h_last + (b * r.heads + head) * states);
+  } else {
+    Fetched<T, KEYS, FRAGS, WHOLE> next;
+    Raw8<T> own[KEYS / 32];       // queries, with a tile
+    QueryRows<T, KEYS, WHOLE> q;  // without a tile
+    Cut<NO> p[kFrags];
+    constexpr int HOLD = QueryRows<T, KEYS, WHOLE>::HOLD;
+    auto at = [&](int first) __attribute__((always_inline)) { return (span.run + first / kRun) * r.heads + head; };
+    auto steps = [&](int first) __attribute__((always_inline)) { return min(kRun, span.len - first); };
+    // behind the last run that one again: loads stand in no branch
+    const int last = (span.len - 1) / kRun * kRun;
+    auto fetch = [&](int first) __attribute__((always_inline)) {
+      next.fetch_keys(thread, r.k, keys, span.batch, span.row + first, steps(first), key_head);
+      next.fetch_values(thread, r.v, values, span.batch, span.row + first, steps(first), head, first_col);
+      next.fetch_factors(thread, w.triangles + at(first) * Tri::kAll * kWave, w.factors[at(first)]);
+      if constexpr (TILE)
+        fetch_rows<T, KEYS, WHOLE>(own, thread, r.q, keys, span.batch, span.row + first, steps(first), key_head);
+    };
+    auto put = [&](int first) __attribute__((always_inline)) {
+      next.put_values(thread, lds, values, steps(first), first_col);
+      next.put_factors(thread, lds);
+      if constexpr (TILE) put_rows<T, KEYS, WHOLE>(own, thread, lds.q, keys, steps(first));
+    };
+    auto fetch_triangle = [&](int first) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i)
+        p[i] = load_frag<NO>(w.triangles + (at(first) * Tri::kAll + Tri::kP) * kWave, i, Tri::kPParts, lane);
+    };
+    auto fetch_queries = [&](int first, auto s) __attribute__((always_inline)) {
+      q.template fetch<decltype(s)::value>(r.q, keys, span.batch, span.row + first, steps(first), key_head, lane);
+    };
+    auto fetch_first_queries = [&](int first) __attribute__((always_inline)) { unrolled<0, HOLD>([&](auto s) __attribute__((always_inline)) { fetch_queries(first, s); }); };
+    if (span.len > 0) {
+      fetch(0);
+      if constexpr (sizeof(T) == 2) fetch_triangle(0);
+      if constexpr (!TILE) fetch_first_queries(0);
+      next.put_keys(thread, lds.k[0], keys, steps(0));
+      put(0);
+    }
+    __syncthreads();
+    for (int first = 0, buffer = 0; first < span.len; first += kRun, buffer = (buffer + 1) % BUFFERS) {
+      again();
+      const int n = steps(first), then = min(first + kRun, last);
+      fetch(then);
+      f32x4 y[kTiles];
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) y[m] = f32x4{0, 0, 0, 0};
+      unrolled<0, S>([&](auto i) __attribute__((always_inline)) {
+        constexpr int s = decltype(i)::value;
+        Cut<NO> part;
+#pragma unroll
+        for (int p = 0; p < NO; ++p) part.p[p] = lds.s[wave][s][p][lane];
+        Cut<NP> rows[kTiles];
+        if constexpr (TILE) {
+          tile_rows<KEYS>(rows, lds.q, s, lane);
+        } else {
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m) rows[m] = q.template operand<s>(m, keys, n, lane);
+          if constexpr (s + HOLD < S) fetch_queries(first, Const<s + HOLD>{});
+        }
+        multiply_rows_t<NO>(y, rows, part);  // steps along the lanes
+        if constexpr (!TILE) part_done();
+      });
+      if constexpr (sizeof(T) == 4) fetch_triangle(first);  // only now: registers
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) y[m] *= r.scale * lds.into[16 * m + x];
+      __syncthreads();
+      f32x4 u[kTiles];
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m) u[m] = lds.u[wave][m][lane];
+      multiply_triangle<NO, false, true>(y, p, cut_tiles<NO>(u[0], u[1]), cut_tiles<NO>(u[2], u[3]));
+      if constexpr (sizeof(T) == 2) fetch_triangle(then);
+      if constexpr (!TILE) fetch_first_queries(then);
+      const int c = first_col + 16 * wave + 4 * g;
+      T *to = head_row<T>(r.y, span.batch, span.row + first, head);
+#pragma unroll
       for (int m = 0; m < kTiles; ++m) {
-        u[m] = f32x4{0, 0, 0, 0};
-        multiply<kFull>(u[m], load_frag<kFull>(tri, lower_frag(m, 0), Tri::kTParts, lane), a);
-        if (m >= 2) multiply<kFull>(u[m], load_frag<kFull>(tri, lower_frag(m, 1), Tri::kTParts, lane), c);
+        const int t = 16 * m + x;
+        if constexpr (WHOLE) {
+          if (t < n && c < values) {
+            const float e[4] = {y[m][0], y[m][1], y[m][2], y[m][3]};
+            store_vec(&at_lane_of(to, t * static_cast<uint32_t>(r.y.step) + c), e, false);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (t < n && c + i < values) to[t * r.y.step + c + i] = static_cast<T>(y[m][i]);
+        }
       }
-    }
-    {
-      const Cut<NO> a = cut_tiles<NO>(u[0], u[1]), c = cut_tiles<NO>(u[2], u[3]);
-      const u32x4 *p = tri + Tri::kP * kWave;
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        multiply<NO>(y[m], load_frag<NO>(p, lower_frag(m, 0), Tri::kPParts, lane), a);
-        if (m >= 2) multiply<NO>(y[m], load_frag<NO>(p, lower_frag(m, 1), Tri::kPParts, lane), c);
+      again();
+      put(then);
+      if constexpr (BUFFERS == 2) {
+        next.put_keys(thread, lds.k[1 - buffer], keys, steps(then));
+      } else {
+        __syncthreads();
+        next.put_keys(thread, lds.k[0], keys, steps(then));
       }
-    }
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      const f32x4 out = *reinterpret_cast<const f32x4 *>(f.out + 16 * m + 4 * g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * m + 4 * g + i;
-        if (inside && t < n) head_row<T>(r.y, span.batch, row + t, head)[col] = static_cast<T>(y[m][i]);
-      }
-      u[m] *= out;
-    }
-    const float whole = f.into[kRun - 1];
-    const Cut<kFull> a = cut_tiles<kFull>(u[0], u[1]), c = cut_tiles<kFull>(u[2], u[3]);
-#pragma unroll
-    for (int t = 0; t < KEYS / 16; ++t) {
-      state[t] *= whole;
-      multiply<kFull>(state[t], tile_columns<KEYS, NP>(ktile, t, 0, lane), a);
-      multiply<kFull>(state[t], tile_columns<KEYS, NP>(ktile, t, 1, lane), c);
+      __syncthreads();
     }
   }
-  if (r.h_last) keep(r.h_last + (b * r.heads + head) * states);
 }
 
 template <typename T>
@@ -126,7 +213,7 @@ hipError_t launch_delta_forward(const fftmv_delta_rule_t &r, hipStream_t s) {
   const int64_t runs = delta_runs(r.batch, r.steps, r.offsets != nullptr);
   DeltaWorkspace w;
   delta_workspace(runs, r.heads, r.keys, r.values, r.dtype, false, r.workspace, &w);
-  const int64_t waves = (r.values + 15) / 16, blocks = (waves + kChainWaves - 1) / kChainWaves;
+  const int64_t blocks = (r.values + kValues - 1) / kValues;
   if (!grid_fits(runs * r.heads, kWave) || !grid_fits(r.batch * r.heads * blocks, kChainThreads))
     return hipErrorInvalidConfiguration;
   return by_keys(r.keys, [&](auto k) {
@@ -136,11 +223,11 @@ hipError_t launch_delta_forward(const fftmv_delta_rule_t &r, hipStream_t s) {
       if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
     const dim3 grid(static_cast<unsigned>(r.batch * r.heads), static_cast<unsigned>(blocks));
-    if (r.carries)
-      delta_chain_kernel<T, KEYS, true><<<grid, kChainThreads, 0, s>>>(r, w);
-    else
-      delta_chain_kernel<T, KEYS, false><<<grid, kChainThreads, 0, s>>>(r, w);
-    return hipGetLastError();
+    auto launch = [&](auto whole, auto save) {
+      delta_chain_kernel<T, KEYS, decltype(whole)::value != 0, decltype(save)::value != 0><<<grid, kChainThreads, 0, s>>>(r, w);
+      return hipGetLastError();
+    };
+    return by_two(delta_whole(r, r.v, r.y), [&](auto whole) { return by_two(r.carries != nullptr, [&](auto save) { return launch(whole, save); }); });
   });
 }
 
