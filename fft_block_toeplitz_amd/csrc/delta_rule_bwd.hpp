@@ -251,10 +251,13 @@ __device__ __forceinline__ float across_groups(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-template <typename T, int KEYS>
+// QUERIES, FRAGS: tiles of their own for the queries and the triangles, where they fit.
+template <typename T, int KEYS, bool QUERIES, bool FRAGS>
 struct GradsLds {
   static constexpr int NP = kParts<T>, NO = kOut<T>, VR = kTileRow<kValues>;
-  alignas(16) uint16_t k[NP * kRun * kTileRow<KEYS>];  // keys, and at the end queries
+  alignas(16) uint16_t k[NP * kRun * kTileRow<KEYS>];  // keys, and without a tile of their own at the end queries
+  alignas(16) uint16_t q[QUERIES ? NP * kRun * kTileRow<KEYS> : 8];
+  alignas(16) u32x4 frags[FRAGS ? 3 * kFrags * NO * kWave : 1];
   union {
     // U and Z first as they are, then with dY as they stand in the gradients' rows; u holds V's rows before U's
     struct {
@@ -265,7 +268,7 @@ struct GradsLds {
     } two;
   };
   alignas(16) Factors f;
-  float sums[kFrontWaves][kRun];   // what of dG goes through the states by the keys, of each wave's values
+  float sums[kGradWaves][kRun];    // what of dG goes through the states by the keys, of each wave's values
   float rates[kFrontWaves][kRun];  // z . x, of each wave's values
   float turns[KEYS / 16][kRun];    // q . dq, of each 16 keys
   float lasts[kGradWaves];         // what the last step's G has beside
@@ -296,7 +299,9 @@ template <typename T, int KEYS, bool WHOLE>
 __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Tri = Triangles<T, true>;
-  using Lds = GradsLds<T, KEYS>;
+  constexpr bool QUERIES = sizeof(GradsLds<T, KEYS, true, false>) <= kLdsBytes;
+  constexpr bool FRAGS = sizeof(GradsLds<T, KEYS, QUERIES, true>) <= kLdsBytes;
+  using Lds = GradsLds<T, KEYS, QUERIES, FRAGS>;
   constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32, VR = Lds::VR, KR = kTileRow<KEYS>;
   constexpr int KT = KEYS / 16, MT = kTiles * KT / kGradWaves;  // tiles of keys, and of steps for one of them a wave
   __shared__ Lds lds;
@@ -349,10 +354,31 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     for (int q = 0; q < kGradJobs; ++q) gram[q] = f32x4{0, 0, 0, 0};
     float last = 0.0f;  // of this wave's values: e^{G_last} <state, its gradient> and the sum of k . o
     __syncthreads();
-    fill(lds.k, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.k, span.batch, row, key_head, n, keys), 0);
+    if (!QUERIES || head % share == 0) fill(lds.k, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.k, span.batch, row, key_head, n, keys), 0);
     if (thread < static_cast<int>(sizeof(Factors) / 16))
       reinterpret_cast<u32x4 *>(&lds.f)[thread] = at_lane(reinterpret_cast<const u32x4 *>(w.factors + at), thread);
-    if (thread < kFrontWaves * kRun) lds.sums[0][thread] = lds.rates[0][thread] = 0.0f;
+    if (QUERIES && head % share == 0) fill(lds.q, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.q, span.batch, row, key_head, n, keys), 0);
+    if constexpr (FRAGS) {  // T diag(b), P^T and T^T, NO parts of each
+      constexpr int N = kFrags * NO * kWave;
+#pragma unroll
+      for (int i = 0; i < (3 * N + kGradThreads - 1) / kGradThreads; ++i) {
+        const int u = thread + i * kGradThreads, which = u / N, frag = u % N / kWave;
+        if (u >= 3 * N) break;
+        const int parts = which == 0 ? Tri::kTParts : kFull, start = which == 0 ? Tri::kT : which == 1 ? Tri::kP : Tri::kTt;
+        lds.frags[u] = at_lane(tri, (start + frag / NO * parts + frag % NO) * kWave + u % kWave);
+      }
+    }
+    f32x4 by_row[2][kTiles];  // over this wave's values: z . x and b z . K S on U's side, u . K D on Z's
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) by_row[0][m] = by_row[1][m] = f32x4{0, 0, 0, 0};
+    auto triangle = [&](f32x4 (&c)[kTiles], auto which, const auto &lo, const auto &hi) __attribute__((always_inline)) {
+      constexpr int W = decltype(which)::value;
+      if constexpr (FRAGS)
+        multiply_triangle<NO, NO, NO, W != 0>(c, lds.frags + W * kFrags * NO * kWave, lo, hi, lane);
+      else
+        multiply_triangle<NO, NO, W == 0 ? Tri::kTParts : kFull, W != 0>(
+            c, tri + (W == 0 ? Tri::kT : W == 1 ? Tri::kP : Tri::kTt) * kWave, lo, hi, lane);
+    };
 
     for (int from = 0; from < values; from += kValues) {
       if (from) __syncthreads();
@@ -389,6 +415,19 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         tile_rows<KEYS>(k, lds.k, s, lane);
         multiply_rows<NO>(p, k, cut<NO>(a[s]));
       }
+      // rows of the state and its gradient, for the products at the end
+      u32x4 rows[kValues / 32][2][2];
+      auto fetch_rows_of_states = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < kValues / 32; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int byte = ((16 * tile_k + x) * values + from + 32 * s + 8 * g + 4 * h) * 4;
+            rows[s][0][h] = __builtin_amdgcn_raw_buffer_load_b128(state, byte, 0, 0);
+            rows[s][1][h] = __builtin_amdgcn_raw_buffer_load_b128(grad, byte, 0, 0);
+          }
+      };
+      if constexpr (sizeof(T) == 2) fetch_rows_of_states();  // FP32 has no registers for them
       part_done();
       if (first_side) {
 #pragma unroll
@@ -402,7 +441,8 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
           in[m] = v - p[m];
           o[m] = f32x4{0, 0, 0, 0};
         }
-        multiply_triangle<NO, NO, Tri::kTParts, false>(o, tri, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]), lane);
+        part_done();
+        triangle(o, Const<0>{}, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]));
         put_column<NO, VR>(lds.one.u, o, 16 * column, lane);
       } else {
 #pragma unroll
@@ -411,10 +451,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
           in[m] = p[m];
           o[m] = f32x4{0, 0, 0, 0};
         }
-        multiply_triangle<NO, NO, Tri::kPParts, true>(in, tri + Tri::kP * kWave, plain_columns<VR, NP, 16>(lds.one.dy, 0, 16 * column, lane),
-                                                      plain_columns<VR, NP, 16>(lds.one.dy, 32, 16 * column, lane), lane);
         part_done();
-        multiply_triangle<NO, NO, Tri::kTtParts, true>(o, tri + Tri::kTt * kWave, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]), lane);
+        triangle(in, Const<1>{}, plain_columns<VR, NP, 16>(lds.one.dy, 0, 16 * column, lane),
+                 plain_columns<VR, NP, 16>(lds.one.dy, 32, 16 * column, lane));
+        part_done();
+        triangle(o, Const<2>{}, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]));
         put_column<NO, VR>(lds.one.z, o, 16 * column, lane);
       }
       __syncthreads();
@@ -468,53 +509,39 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
           const f32x4 z = tile_values<VR, NO>(lds.one.z, m, 16 * column, lane);
-          const f32x4 rate = factor4(lds.f.rate, m, lane) * z;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float zk = across16(rate[i] * p[m][i]), zx = across16(z[i] * in[m][i]);
-            if (x == 0) {
-              lds.sums[column][16 * m + 4 * g + i] += zk;
-              lds.rates[column][16 * m + 4 * g + i] += zx;
-            }
-          }
+          by_row[0][m] += z * in[m];
+          by_row[1][m] += factor4(lds.f.rate, m, lane) * z * p[m];
           in[m] = tile_values<VR, NP>(lds.one.dy, m, 16 * column, lane) * (factor4(lds.f.into, m, lane) * r.scale);
           o[m] *= factor4(lds.f.out, m, lane);
+          part_done();
         }
       }
       __syncthreads();
       if (first_side) {
         put_column<NO, VR>(lds.one.dy, in, 16 * column, lane);
-      } else {  // lds.sums is the other side's up to here
+      } else {
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
-          const f32x4 uk = tile_values<VR, NO>(lds.one.u, m, 16 * column, lane) * p[m];
-          last += (uk[0] + uk[1]) + (uk[2] + uk[3]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float sum = across16(uk[i]);
-            if (x == 0) lds.sums[column][16 * m + 4 * g + i] += sum;
-          }
+          by_row[1][m] += tile_values<VR, NO>(lds.one.u, m, 16 * column, lane) * p[m];
           o[m] *= -(factor4(lds.f.rate, m, lane) * factor4(lds.f.into, m, lane));
+          part_done();
         }
         put_column<NO, VR>(lds.one.z, o, 16 * column, lane);
       }
-      // rows of the state and its gradient
       Cut<NO> sp[kValues / 32], dp[kValues / 32];
       again();
+      if constexpr (sizeof(T) == 4) fetch_rows_of_states();
 #pragma unroll
       for (int s = 0; s < kValues / 32; ++s) {
-        const int c = from + 32 * s + 8 * g, byte = ((16 * tile_k + x) * values + c) * 4;
+        const int c = from + 32 * s + 8 * g;
         float b[2][8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(state, byte + 16 * h, 0, 0);
-          const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(grad, byte + 16 * h, 0, 0);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            b[0][4 * h + e] = __uint_as_float(lo[e]);
-            b[1][4 * h + e] = __uint_as_float(hi[e]);
+            b[0][4 * h + e] = __uint_as_float(rows[s][0][h][e]);
+            b[1][4 * h + e] = __uint_as_float(rows[s][1][h][e]);
           }
-        }
         if (from + kValues > values) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -541,6 +568,23 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
           multiply<NO>(dk[m], dp[s], tile_rows<kValues, NO>(lds.one.u, tile_m + m, s, lane));
         }
     }
+#pragma unroll
+    for (int m = 0; m < kTiles; ++m) {
+      float sums[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sums[0][i] = across16(by_row[0][m][i]);
+        sums[1][i] = across16(by_row[1][m][i]);
+        if (!first_side && x == 0) last += sums[1][i];  // k . o
+      }
+      if (x < 4) {
+        const auto of = [&](const float (&v)[4]) __attribute__((always_inline)) {
+          return x == 0 ? v[0] : x == 1 ? v[1] : x == 2 ? v[2] : v[3];
+        };
+        lds.sums[wave][16 * m + 4 * g + x] = of(sums[1]);
+        if (first_side) lds.rates[wave][16 * m + 4 * g + x] = of(sums[0]);
+      }
+    }
     last = across_groups(across16(last));
     if (lane == 0) lds.lasts[wave] = last;
     __syncthreads();  // u, z and dy are done with
@@ -554,14 +598,19 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
       const int m = gram_row(tile), c = gram_col(tile), j = 16 * c + x;
       f32x4 raw = {0, 0, 0, 0};
       if (job < kGrams) {
-        const Rows<T, WHOLE> rows(r.q, span.batch, row, key_head, n, keys);
-        Raw8<T> own[S];
+        if constexpr (QUERIES) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) own[s] = rows.load(16 * m + x, 32 * s + 8 * g);
+          for (int s = 0; s < S; ++s) multiply<NO>(raw, tile_rows<KEYS, NP>(lds.q, m, s, lane), tile_rows<KEYS, NP>(lds.k, c, s, lane));
+        } else {
+          const Rows<T, WHOLE> rows(r.q, span.batch, row, key_head, n, keys);
+          Raw8<T> own[S];
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-          if (!WHOLE || keys < KEYS) settle<WHOLE>(own[s], 32 * s + 8 * g, keys, 16 * m + x < n);
-          multiply<NO>(raw, cut_raw<T>(own[s]), tile_rows<KEYS, NP>(lds.k, c, s, lane));
+          for (int s = 0; s < S; ++s) own[s] = rows.load(16 * m + x, 32 * s + 8 * g);
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+            if (!WHOLE || keys < KEYS) settle<WHOLE>(own[s], 32 * s + 8 * g, keys, 16 * m + x < n);
+            multiply<NO>(raw, cut_raw<T>(own[s]), tile_rows<KEYS, NP>(lds.k, c, s, lane));
+          }
         }
       } else {
 #pragma unroll
@@ -618,12 +667,15 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], k, plain_columns<VR, NO, 4>(lds.two.h, 32 * s, 16 * (tile_m + m), lane));
       }
     }
-    __syncthreads();
-    fill(lds.k, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.q, span.batch, row, key_head, n, keys), 0);
-    __syncthreads();
+    if constexpr (!QUERIES) {
+      __syncthreads();
+      fill(lds.k, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.q, span.batch, row, key_head, n, keys), 0);
+      __syncthreads();
+    }
+    const uint16_t *queries = QUERIES ? lds.q : lds.k;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const Cut<NP> q = plain_columns<KR, NP, 4>(lds.k, 32 * s, 16 * tile_k, lane);
+      const Cut<NP> q = plain_columns<KR, NP, 4>(queries, 32 * s, 16 * tile_k, lane);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
         if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], q, plain_columns<VR, NO, 4>(lds.two.f, 32 * s, 16 * (tile_m + m), lane));
@@ -634,7 +686,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
       const int t = 16 * (tile_m + m) + x;
 #pragma unroll
       for (int part = 0; part < NP; ++part) {
-        const uint16_t *q = lds.k + (part * kRun + t) * KR + 16 * tile_k + 4 * g;
+        const uint16_t *q = queries + (part * kRun + t) * KR + 16 * tile_k + 4 * g;
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum = fmaf(dq[m][i], __uint_as_float(static_cast<uint32_t>(q[i]) << 16), sum);
       }
@@ -648,12 +700,11 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 #pragma unroll
       for (int v = 0; v < KT; ++v) turned += lds.turns[v][lane];
 #pragma unroll
-      for (int v = 0; v < kFrontWaves; ++v) {
+      for (int v = 0; v < kGradWaves; ++v) {
         own -= lds.sums[v][lane];
-        rate += lds.rates[v][lane];
+        if (v < kFrontWaves) rate += lds.rates[v][lane];
+        end += lds.lasts[v];
       }
-#pragma unroll
-      for (int v = 0; v < kGradWaves; ++v) end += lds.lasts[v];
       own += turned;
 #pragma unroll
       for (int job = 0; job < 2 * kGrams; ++job) {
