@@ -435,30 +435,71 @@ __device__ __forceinline__ void multiply_triangle(f32x4 (&c)[kTiles], const u32x
   multiply_triangle<LIMIT, UPPER, false>(c, a, lo, hi);
 }
 
+// Long sequences with few heads leave most of the card without work: they are
+// cut into parts. The state behind a part is M S + N of the state S in front of
+// it; M and N of all parts but the last are computed at once (the same chain, from
+// no state and from each unit state without values), joined one after another, and
+// then every part goes through its runs from its own state: two and a half times
+// the work, by as many times the workgroups. The gradients' chain is cut likewise.
+struct DeltaCuts {
+  int parts;  // of a sequence, at most
+  int runs;   // of a part
+};
+// Times in tenths of a run of the chain, on 256 CUs: a map's run takes 0.8 of one, a joint 1.2, the
+// two more launches 4. (One sequence of 65536 steps, 8 heads of 128 x 128: whole
+// 3430 us, in 16 parts 560.) Packed sequences' lengths are on the device: they stay whole.
+inline DeltaCuts delta_cuts(int64_t batch, int64_t steps, int64_t heads, int64_t keys, int64_t values, bool packed) {
+  const int64_t runs = (steps + kRun - 1) / kRun, chains = batch * heads;
+  DeltaCuts best = {1, static_cast<int>(runs > 0 ? runs : 1)};
+  if (packed || runs < 8 || chains >= 256) return best;
+  const int64_t vb = (values + 63) / 64, kb = (keys + 63) / 64;
+  int64_t least = (chains * vb + 255) / 256 * runs * 10;
+  for (int64_t n = 2; n <= 64 && n <= runs / 4; ++n) {
+    const int64_t per = (runs + n - 1) / n, parts = (runs + per - 1) / per;
+    const int64_t time = (chains * vb * parts + 255) / 256 * per * 10 +
+                         (chains * (parts - 1) * (vb + kb) + 255) / 256 * per * 8 + (parts - 1) * 12 + 40;
+    if (time < least) {
+      least = time;
+      best = {static_cast<int>(parts), static_cast<int>(per)};
+    }
+  }
+  return best;
+}
+
 // The workspace of a call in its parts.
 struct DeltaWorkspace {
   Factors *factors;
   u32x4 *triangles;
   float *grads;  // backward: the gradients of the states behind each run, [runs][heads][keys][values]
+  // of each part of a sequence: (N, M) [keys][values + keys], and the state in front of it (backward: behind it)
+  float *maps, *starts;
+  DeltaCuts cuts;
 };
 inline size_t delta_triangle_bytes(int dtype, bool back) {
   const size_t per_part = size_t{kFrags} * kWave * sizeof(u32x4);
   const size_t out = dtype == FFTMV_F32 ? 3 : 2;
   return per_part * (back ? out + 2 * kFull : kFull + out);
 }
-inline size_t delta_workspace(int64_t runs, int64_t heads, int64_t keys, int64_t values, int dtype, bool back,
-                              void *at = nullptr, DeltaWorkspace *w = nullptr) {
-  const size_t n = static_cast<size_t>(runs) * heads;
+inline size_t delta_workspace(int64_t batch, int64_t steps, int64_t heads, int64_t keys, int64_t values, int dtype,
+                              bool packed, bool back, void *at = nullptr, DeltaWorkspace *w = nullptr) {
+  const size_t n = static_cast<size_t>(delta_runs(batch, steps, packed)) * heads;
+  const DeltaCuts cuts = delta_cuts(batch, steps, heads, keys, values, packed);
+  const size_t parts = cuts.parts > 1 ? static_cast<size_t>(batch) * heads * cuts.parts : 0;
   const size_t factors = n * sizeof(Factors), triangles = n * delta_triangle_bytes(dtype, back);
-  const size_t grads = back ? n * keys * values * sizeof(float) : 0;
+  const size_t grads = (back ? n * keys * values * sizeof(float) + 15 : 0) & ~size_t{15};
+  const size_t maps = (parts * keys * (keys + values) * sizeof(float) + 15) & ~size_t{15};
+  const size_t starts = parts * keys * values * sizeof(float);
   static_assert(sizeof(Factors) % 16 == 0, "fragments are 16-byte aligned");
   if (w) {
     char *p = static_cast<char *>(at);
     w->factors = reinterpret_cast<Factors *>(p);
     w->triangles = reinterpret_cast<u32x4 *>(p + factors);
     w->grads = reinterpret_cast<float *>(p + factors + triangles);
+    w->maps = reinterpret_cast<float *>(p + factors + triangles + grads);
+    w->starts = reinterpret_cast<float *>(p + factors + triangles + grads + maps);
+    w->cuts = cuts;
   }
-  return factors + triangles + grads;
+  return factors + triangles + grads + maps + starts;
 }
 
 // ------------------------------------------------------ gates of 64 steps
@@ -1038,6 +1079,86 @@ inline bool delta_whole(const fftmv_delta_rule_t &r, const fftmv_heads_t &valued
   return delta_whole(r.q, r.keys, r.dtype) && delta_whole(r.k, r.keys, r.dtype) && delta_whole(valued, r.values, r.dtype) &&
          delta_whole(other, r.values, r.dtype);
 }
+// A part of a sequence, in its steps.
+struct Part {
+  int64_t sequence;  // sequence and head
+  int part, begin, end;
+  __device__ __forceinline__ Part(const DeltaCuts &cuts, int64_t index, int len)
+      : sequence(index / cuts.parts), part(static_cast<int>(index % cuts.parts)) {
+    const int64_t each = static_cast<int64_t>(cuts.runs) * kRun;
+    begin = static_cast<int>(min(part * each, static_cast<int64_t>(len)));
+    end = static_cast<int>(part == cuts.parts - 1 ? len : min((part + 1) * each, static_cast<int64_t>(len)));
+  }
+};
+
+// The states in front of the parts (backward: the gradients of those behind
+// them) one after another. A workgroup has 16 value columns and a wave 16 keys of
+// them; the waves pass each other the state through LDS, and load the next map
+// while they wait. (One wave for all keys took 18 us a joint at 128 x 128.)
+// (T keeps the instances of one element type's source apart from the others'.)
+template <typename T, int KEYS, bool BACK>
+__global__ __launch_bounds__(KEYS / 16 * kWave) void delta_join_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
+  constexpr int S = KEYS / 32, TILES = KEYS / 16;
+  __shared__ f32x4 shared[2][TILES][kWave];
+  const int t = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave, x = lane % 16, g = lane / 16;
+  const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values), width = keys + values;
+  const int col = blockIdx.y * 16 + x, row = key_of(t, x / 4, x % 4);
+  const bool inside = col < values;
+  const int64_t sequence = blockIdx.x, states = r.keys * r.values;
+  const Span span = span_of(r, sequence / r.heads);
+  const int64_t each = static_cast<int64_t>(w.cuts.runs) * kRun;
+  const int joints = static_cast<int>((span.len + each - 1) / each) - 1;
+  auto part_of = [&](int i) { return BACK ? joints - i : i; };
+  struct Map {
+    float m[S][8];
+    f32x4 n;
+  };
+  auto fetch = [&](Map &to, int i) __attribute__((always_inline)) {
+    const float *map = w.maps + (sequence * w.cuts.parts + part_of(i)) * keys * width;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) to.m[s][e] = 0.0f;
+      if (row < keys) load8(map + static_cast<int64_t>(row) * width + values, 32 * s + 8 * g, keys, to.m[s]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = key_of(t, g, e);
+      to.n[e] = inside && key < keys ? map[static_cast<int64_t>(key) * width + col] : 0.0f;
+    }
+  };
+  const float *from = BACK ? r.dh_last : r.h0;
+  f32x4 state;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int key = key_of(t, g, i);
+    state[i] = from && inside && key < keys ? from[sequence * states + static_cast<int64_t>(key) * values + col] : 0.0f;
+  }
+  auto join = [&](const Map &map, int i) __attribute__((always_inline)) {
+    shared[i % 2][t][lane] = state;
+    __syncthreads();
+    state = map.n;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      multiply<kFull>(state, cut<kFull>(map.m[s]), cut_tiles<kFull>(shared[i % 2][2 * s][lane], shared[i % 2][2 * s + 1][lane]));
+    float *to = w.starts + (sequence * w.cuts.parts + part_of(i) + (BACK ? -1 : 1)) * states;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = key_of(t, g, e);
+      if (inside && key < keys) to[static_cast<int64_t>(key) * values + col] = state[e];
+    }
+  };
+  Map even, odd;
+  if (joints > 0) fetch(even, 0);
+  for (int i = 0; i < joints; i += 2) {
+    if (i + 1 < joints) fetch(odd, i + 1);
+    join(even, i);
+    if (i + 1 >= joints) break;
+    if (i + 2 < joints) fetch(even, i + 2);
+    join(odd, i + 1);
+  }
+}
+
 template <typename F>
 hipError_t by_keys(int64_t keys, F f) {
   if (keys <= 32) return f(Const<32>{});

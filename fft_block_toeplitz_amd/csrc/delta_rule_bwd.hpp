@@ -30,7 +30,7 @@ struct BackwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
   alignas(16) f32x4 d[kFrontWaves][KEYS / 16][kWave];                    // Q^T (..) dY
 };
 
-template <typename T, int KEYS, bool WHOLE>
+template <typename T, int KEYS, bool WHOLE, bool MAPS>
 __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Tri = Triangles<T, true>;
   constexpr int FRAGS = kFrags * kFull, NP = kParts<T>, S = KEYS / 32;
@@ -44,14 +44,19 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
   auto again = [&]() __attribute__((always_inline)) {
     thread = afresh(thread), lane = thread % kWave, x = lane % 16, g = lane / 16;
   };
-  const int64_t head = blockIdx.x % r.heads, b = blockIdx.x / r.heads;
+  const int64_t sequence = blockIdx.x / w.cuts.parts, head = sequence % r.heads, b = sequence / r.heads;
   const int64_t key_head = head / (r.heads / r.key_heads);
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
-  const int first_col = blockIdx.y * kValues, col = first_col + wave * 16 + x;
-  const bool inside = col < values;
+  // maps: blocks of value columns, then blocks of unit gradients without dY
+  const int value_blocks = (values + kValues - 1) / kValues;
+  const bool units = MAPS && static_cast<int>(blockIdx.y) >= value_blocks;
+  const int first_col = (blockIdx.y - (units ? value_blocks : 0)) * kValues, col = first_col + wave * 16 + x;
+  const bool inside = col < (units ? keys : values);
   const Span span = span_of(r, b);
+  const Part part(w.cuts, blockIdx.x, span.len);
+  if (MAPS ? part.part == 0 || part.begin >= span.len : part.part > 0 && part.begin >= span.len) return;
   const int64_t states = r.keys * r.values;
-  const int last = span.len > 0 ? (span.len - 1) / kRun * kRun : -kRun;
+  const int last = part.end > part.begin ? (part.end - 1) / kRun * kRun : part.begin - kRun;
   auto at = [&](int first) __attribute__((always_inline)) { return (span.run + first / kRun) * r.heads + head; };
 
   if (side == 0) {
@@ -61,26 +66,30 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = key_of(t, g, i);
-        grad[t][i] = r.dh_last && inside && key < keys
-                         ? r.dh_last[(b * r.heads + head) * states + static_cast<int64_t>(key) * values + col]
-                         : 0.0f;
+        grad[t][i] = 0.0f;
+        if constexpr (MAPS) {
+          grad[t][i] = units && key == col ? 1.0f : 0.0f;
+        } else {
+          const float *from = part.end < span.len ? w.starts + blockIdx.x * states : r.dh_last ? r.dh_last + sequence * states : nullptr;
+          if (from && inside && key < keys) grad[t][i] = from[static_cast<int64_t>(key) * values + col];
+        }
       }
-    auto keep = [&](float *to) __attribute__((always_inline)) {
+    auto keep = [&](float *to, int width) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < KEYS / 16; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = key_of(t, g, i);
-          if (inside && key < keys) to[static_cast<int64_t>(key) * values + col] = grad[t][i];
+          if (inside && key < keys) to[static_cast<int64_t>(key) * width + col] = grad[t][i];
         }
     };
     __syncthreads();
     __syncthreads();
     __syncthreads();
-    for (int first = last, buffer = 0; first >= 0; first -= kRun, buffer = (buffer + 1) % BUFFERS) {
+    for (int first = last, buffer = 0; first >= part.begin; first -= kRun, buffer = (buffer + 1) % BUFFERS) {
       again();
       const uint16_t *k = lds.k[buffer];
-      keep(w.grads + at(first) * states);
+      if constexpr (!MAPS) keep(w.grads + at(first) * states, values);
       const float whole = lds.into[kRun - 1];
       f32x4 z[kTiles];
 #pragma unroll
@@ -111,7 +120,10 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
       if constexpr (BUFFERS == 1) __syncthreads();
       __syncthreads();
     }
-    if (r.dh0) keep(r.dh0 + (b * r.heads + head) * states);
+    if constexpr (MAPS)
+      keep(w.maps + static_cast<int64_t>(blockIdx.x) * keys * (keys + values) + (units ? values : 0), keys + values);
+    else if (r.dh0 && part.part == 0)
+      keep(r.dh0 + sequence * states, values);
   } else {
     Fetched<T, KEYS, FRAGS, WHOLE> next;  // keys and T^T of the front's next run, dY of the run behind it
     Raw8<T> q[TILE ? KEYS / 32 : 1];
@@ -130,6 +142,12 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
         fetch_rows<T, KEYS, WHOLE>(q, thread, r.q, keys, span.batch, span.row + first, steps(first), key_head);
     };
     auto put_back = [&](int first) __attribute__((always_inline)) {
+      if (units) {
+#pragma unroll
+        for (auto &v : next.v)
+#pragma unroll
+          for (auto &word : v.w) word = u32x4{0, 0, 0, 0};
+      }
       next.put_values(thread, lds, values, steps(first), first_col);
       if constexpr (TILE) put_rows<T, KEYS, WHOLE>(q, thread, lds.q, keys, steps(first));
     };
@@ -181,7 +199,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
 #pragma unroll
       for (int t = 0; t < KEYS / 16; ++t) lds.d[wave][t][lane] = d[t];
     };
-    if (last >= 0) {
+    if (last >= part.begin) {
       fetch_own(last);
       fetch_front(last);
       fetch_back(last);
@@ -190,20 +208,20 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
     }
     __syncthreads();
     // the first run's products by themselves; then always one run ahead
-    if (last >= 0) {
+    if (last >= part.begin) {
       compute(last);
-      const int then = max(last - kRun, 0);
+      const int then = max(last - kRun, part.begin);
       fetch_back(then);
       fetch_own(then);
       leave();
     }
     __syncthreads();
-    if (last >= 0) put_back(max(last - kRun, 0));
+    if (last >= part.begin) put_back(max(last - kRun, part.begin));
     __syncthreads();
-    for (int first = last, buffer = 0; first >= 0; first -= kRun, buffer = (buffer + 1) % BUFFERS) {
+    for (int first = last, buffer = 0; first >= part.begin; first -= kRun, buffer = (buffer + 1) % BUFFERS) {
       again();
       // in front of the first run that one again: loads stand in no branch
-      const int then = max(first - kRun, 0), later = max(then - kRun, 0);
+      const int then = max(first - kRun, part.begin), later = max(then - kRun, part.begin);
       fetch_front(then);
       fetch_back(later);
       compute(then);
@@ -752,12 +770,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 
 template <typename T>
 hipError_t launch_delta_backward(const fftmv_delta_rule_t &r, hipStream_t s) {
-  const int64_t runs = delta_runs(r.batch, r.steps, r.offsets != nullptr);
+  const int64_t runs = delta_runs(r.batch, r.steps, r.offsets != nullptr), sequences = r.batch * r.heads;
   DeltaWorkspace w;
-  delta_workspace(runs, r.heads, r.keys, r.values, r.dtype, true, r.workspace, &w);
-  const int64_t blocks = (r.values + kValues - 1) / kValues;
-  if (!grid_fits(runs * r.heads, kWave) || !grid_fits(runs * r.key_heads, kChainThreads) ||
-      !grid_fits(r.batch * r.heads * blocks, kChainThreads))
+  delta_workspace(r.batch, r.steps, r.heads, r.keys, r.values, r.dtype, r.offsets != nullptr, true, r.workspace, &w);
+  const int64_t blocks = (r.values + kValues - 1) / kValues, units = (r.keys + kValues - 1) / kValues;
+  if (!grid_fits(runs * r.heads, kWave) || !grid_fits(sequences * ((r.values + 15) / 16), 512) || !grid_fits(runs * r.key_heads, kGradThreads) ||
+      !grid_fits(sequences * w.cuts.parts * (blocks + units), kChainThreads))
     return hipErrorInvalidConfiguration;
   return by_keys(r.keys, [&](auto k) {
     constexpr int KEYS = decltype(k)::value;
@@ -765,9 +783,18 @@ hipError_t launch_delta_backward(const fftmv_delta_rule_t &r, hipStream_t s) {
       delta_factors_kernel<T, KEYS, true><<<static_cast<unsigned>(runs * r.heads), kWave, 0, s>>>(r, w);
       if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    const dim3 grid(static_cast<unsigned>(r.batch * r.heads), static_cast<unsigned>(blocks));
     const hipError_t e = by_two(delta_whole(r, r.dy, r.dy), [&](auto whole) {
-      delta_back_chain_kernel<T, KEYS, decltype(whole)::value != 0><<<grid, kChainThreads, 0, s>>>(r, w);
+      constexpr bool WHOLE = decltype(whole)::value != 0;
+      const unsigned chains = static_cast<unsigned>(sequences * w.cuts.parts), columns = static_cast<unsigned>(blocks);
+      if (w.cuts.parts > 1) {
+        const dim3 all(chains, static_cast<unsigned>(blocks + units));
+        delta_back_chain_kernel<T, KEYS, WHOLE, true><<<all, kChainThreads, 0, s>>>(r, w);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        delta_join_kernel<T, KEYS, true>
+            <<<dim3(static_cast<unsigned>(sequences), static_cast<unsigned>((r.values + 15) / 16)), KEYS / 16 * kWave, 0, s>>>(r, w);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+      }
+      delta_back_chain_kernel<T, KEYS, WHOLE, false><<<dim3(chains, columns), kChainThreads, 0, s>>>(r, w);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;

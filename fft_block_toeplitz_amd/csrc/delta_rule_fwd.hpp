@@ -16,7 +16,10 @@ struct ForwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
   alignas(16) f32x4 u[kFrontWaves][kTiles][kWave];  // U
 };
 
-template <typename T, int KEYS, bool WHOLE, bool SAVE>
+// What a chain is for: the outputs, also with the states kept for the backward pass, or the maps of parts.
+enum ChainUse { kOutputs, kCarries, kMaps };
+
+template <typename T, int KEYS, bool WHOLE, int USE>
 __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Tri = Triangles<T, false>;
   constexpr int FRAGS = kFrags * kFull, S = KEYS / 32;
@@ -31,12 +34,17 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
   auto again = [&]() __attribute__((always_inline)) {
     thread = afresh(thread), lane = thread % kWave, x = lane % 16, g = lane / 16;
   };
-  const int64_t head = blockIdx.x % r.heads, b = blockIdx.x / r.heads;
+  const int64_t sequence = blockIdx.x / w.cuts.parts, head = sequence % r.heads, b = sequence / r.heads;
   const int64_t key_head = head / (r.heads / r.key_heads);
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
-  const int first_col = blockIdx.y * kValues, col = first_col + wave * 16 + x;
-  const bool inside = col < values;
+  // maps: blocks of value columns, then blocks of unit states without values
+  const int value_blocks = (values + kValues - 1) / kValues;
+  const bool units = USE == kMaps && static_cast<int>(blockIdx.y) >= value_blocks;
+  const int first_col = (blockIdx.y - (units ? value_blocks : 0)) * kValues, col = first_col + wave * 16 + x;
+  const bool inside = col < (units ? keys : values);
   const Span span = span_of(r, b);
+  const Part part(w.cuts, blockIdx.x, span.len);
+  if (USE == kMaps ? part.end >= span.len : part.part > 0 && part.begin >= span.len) return;
   const int64_t states = r.keys * r.values;
 
   if (side == 0) {
@@ -46,31 +54,36 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int key = key_of(t, g, i);
-        state[t][i] = r.h0 && inside && key < keys
-                          ? r.h0[(b * r.heads + head) * states + static_cast<int64_t>(key) * values + col]
-                          : 0.0f;
+        state[t][i] = 0.0f;
+        if constexpr (USE == kMaps) {
+          state[t][i] = units && key == col ? 1.0f : 0.0f;
+        } else {
+          const float *from = part.part ? w.starts + blockIdx.x * states : r.h0 ? r.h0 + sequence * states : nullptr;
+          if (from && inside && key < keys) state[t][i] = from[static_cast<int64_t>(key) * values + col];
+        }
       }
-    auto keep = [&](float *to) __attribute__((always_inline)) {
+    auto keep = [&](float *to, int width) __attribute__((always_inline)) {
 #pragma unroll
       for (int t = 0; t < KEYS / 16; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int key = key_of(t, g, i);
-          if (inside && key < keys) to[static_cast<int64_t>(key) * values + col] = state[t][i];
+          if (inside && key < keys) to[static_cast<int64_t>(key) * width + col] = state[t][i];
         }
     };
-    Cut<kFull> part[S];
+    Cut<kFull> cuts[S];
     auto leave_state = [&]() __attribute__((always_inline)) {
 #pragma unroll
       for (int s = 0; s < S; ++s) {
-        part[s] = cut_tiles<kFull>(state[2 * s], state[2 * s + 1]);
+        cuts[s] = cut_tiles<kFull>(state[2 * s], state[2 * s + 1]);
 #pragma unroll
-        for (int p = 0; p < NO; ++p) lds.s[wave][s][p][lane] = part[s].p[p];
+        for (int p = 0; p < NO; ++p)
+          if constexpr (USE != kMaps) lds.s[wave][s][p][lane] = cuts[s].p[p];
       }
     };
     leave_state();
     __syncthreads();
-    for (int first = 0, buffer = 0; first < span.len; first += kRun, buffer = (buffer + 1) % BUFFERS) {
+    for (int first = part.begin, buffer = 0; first < part.end; first += kRun, buffer = (buffer + 1) % BUFFERS) {
       const uint16_t *k = lds.k[buffer];
       again();
       f32x4 u[kTiles];
@@ -80,7 +93,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
       for (int s = 0; s < S; ++s) {
         Cut<NP> rows[kTiles];
         tile_rows<KEYS>(rows, k, s, lane);
-        multiply_rows<kFull>(u, rows, part[s]);
+        multiply_rows<kFull>(u, rows, cuts[s]);
       }
 #pragma unroll
       for (int m = 0; m < kTiles; ++m)
@@ -91,12 +104,14 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
         for (int m = 0; m < kTiles; ++m) u[m] = f32x4{0, 0, 0, 0};
         multiply_triangle<kFull, kFull, kFull, false>(u, lds.frags, a, c, lane);
       }
+      if constexpr (USE != kMaps) {
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) lds.u[wave][m][lane] = u[m];
+        for (int m = 0; m < kTiles; ++m) lds.u[wave][m][lane] = u[m];
+      }
 #pragma unroll
       for (int m = 0; m < kTiles; ++m) u[m] *= *reinterpret_cast<const f32x4 *>(lds.out + 16 * m + 4 * g);
       const float whole = lds.into[kRun - 1];
-      if constexpr (SAVE) keep(r.carries + ((span.run + first / kRun) * r.heads + head) * states);
+      if constexpr (USE == kCarries) keep(r.carries + ((span.run + first / kRun) * r.heads + head) * states, values);
       __syncthreads();
       const Cut<kFull> a = cut_tiles<kFull>(u[0], u[1]), c = cut_tiles<kFull>(u[2], u[3]);
 #pragma unroll
@@ -106,7 +121,10 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
       leave_state();
       __syncthreads();
     }
-    if (r.h_last) keep(r.h_last + (b * r.heads + head) * states);
+    if constexpr (USE == kMaps)
+      keep(w.maps + static_cast<int64_t>(blockIdx.x) * keys * (keys + values) + (units ? values : 0), keys + values);
+    else if (r.h_last && part.end >= span.len)
+      keep(r.h_last + sequence * states, values);
   } else {
     Fetched<T, KEYS, FRAGS, WHOLE> next;
     Raw8<T> own[KEYS / 32];       // queries, with a tile
@@ -116,18 +134,24 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
     auto at = [&](int first) __attribute__((always_inline)) { return (span.run + first / kRun) * r.heads + head; };
     auto steps = [&](int first) __attribute__((always_inline)) { return min(kRun, span.len - first); };
     // behind the last run that one again: loads stand in no branch
-    const int last = (span.len - 1) / kRun * kRun;
+    const int last = (part.end - 1) / kRun * kRun;
     auto fetch = [&](int first) __attribute__((always_inline)) {
       next.fetch_keys(thread, r.k, keys, span.batch, span.row + first, steps(first), key_head);
       next.fetch_values(thread, r.v, values, span.batch, span.row + first, steps(first), head, first_col);
       next.fetch_factors(thread, w.triangles + at(first) * Tri::kAll * kWave, w.factors[at(first)]);
-      if constexpr (TILE)
+      if constexpr (TILE && USE != kMaps)
         fetch_rows<T, KEYS, WHOLE>(own, thread, r.q, keys, span.batch, span.row + first, steps(first), key_head);
     };
     auto put = [&](int first) __attribute__((always_inline)) {
+      if (units) {
+#pragma unroll
+        for (auto &v : next.v)
+#pragma unroll
+          for (auto &word : v.w) word = u32x4{0, 0, 0, 0};
+      }
       next.put_values(thread, lds, values, steps(first), first_col);
       next.put_factors(thread, lds);
-      if constexpr (TILE) put_rows<T, KEYS, WHOLE>(own, thread, lds.q, keys, steps(first));
+      if constexpr (TILE && USE != kMaps) put_rows<T, KEYS, WHOLE>(own, thread, lds.q, keys, steps(first));
     };
     auto fetch_triangle = [&](int first) __attribute__((always_inline)) {
 #pragma unroll
@@ -138,61 +162,65 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
       q.template fetch<decltype(s)::value>(r.q, keys, span.batch, span.row + first, steps(first), key_head, lane);
     };
     auto fetch_first_queries = [&](int first) __attribute__((always_inline)) { unrolled<0, HOLD>([&](auto s) __attribute__((always_inline)) { fetch_queries(first, s); }); };
-    if (span.len > 0) {
-      fetch(0);
-      if constexpr (sizeof(T) == 2) fetch_triangle(0);
-      if constexpr (!TILE) fetch_first_queries(0);
-      next.put_keys(thread, lds.k[0], keys, steps(0));
-      put(0);
+    if (part.end > part.begin) {
+      fetch(part.begin);
+      if constexpr (sizeof(T) == 2 && USE != kMaps) fetch_triangle(part.begin);
+      if constexpr (!TILE && USE != kMaps) fetch_first_queries(part.begin);
+      next.put_keys(thread, lds.k[0], keys, steps(part.begin));
+      put(part.begin);
     }
     __syncthreads();
-    for (int first = 0, buffer = 0; first < span.len; first += kRun, buffer = (buffer + 1) % BUFFERS) {
+    for (int first = part.begin, buffer = 0; first < part.end; first += kRun, buffer = (buffer + 1) % BUFFERS) {
       again();
       const int n = steps(first), then = min(first + kRun, last);
       fetch(then);
       f32x4 y[kTiles];
 #pragma unroll
       for (int m = 0; m < kTiles; ++m) y[m] = f32x4{0, 0, 0, 0};
-      unrolled<0, S>([&](auto i) __attribute__((always_inline)) {
-        constexpr int s = decltype(i)::value;
-        Cut<NO> part;
+      if constexpr (USE != kMaps) {
+        unrolled<0, S>([&](auto i) __attribute__((always_inline)) {
+          constexpr int s = decltype(i)::value;
+          Cut<NO> part;
 #pragma unroll
-        for (int p = 0; p < NO; ++p) part.p[p] = lds.s[wave][s][p][lane];
-        Cut<NP> rows[kTiles];
-        if constexpr (TILE) {
-          tile_rows<KEYS>(rows, lds.q, s, lane);
-        } else {
+          for (int p = 0; p < NO; ++p) part.p[p] = lds.s[wave][s][p][lane];
+          Cut<NP> rows[kTiles];
+          if constexpr (TILE) {
+            tile_rows<KEYS>(rows, lds.q, s, lane);
+          } else {
 #pragma unroll
-          for (int m = 0; m < kTiles; ++m) rows[m] = q.template operand<s>(m, keys, n, lane);
-          if constexpr (s + HOLD < S) fetch_queries(first, Const<s + HOLD>{});
-        }
-        multiply_rows_t<NO>(y, rows, part);  // steps along the lanes
-        if constexpr (!TILE) part_done();
-      });
-      if constexpr (sizeof(T) == 4) fetch_triangle(first);  // only now: registers
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) y[m] *= r.scale * lds.into[16 * m + x];
-      __syncthreads();
-      f32x4 u[kTiles];
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) u[m] = lds.u[wave][m][lane];
-      multiply_triangle<NO, false, true>(y, p, cut_tiles<NO>(u[0], u[1]), cut_tiles<NO>(u[2], u[3]));
-      if constexpr (sizeof(T) == 2) fetch_triangle(then);
-      if constexpr (!TILE) fetch_first_queries(then);
-      const int c = first_col + 16 * wave + 4 * g;
-      T *to = head_row<T>(r.y, span.batch, span.row + first, head);
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        const int t = 16 * m + x;
-        if constexpr (WHOLE) {
-          if (t < n && c < values) {
-            const float e[4] = {y[m][0], y[m][1], y[m][2], y[m][3]};
-            store_vec(&at_lane_of(to, t * static_cast<uint32_t>(r.y.step) + c), e, false);
+            for (int m = 0; m < kTiles; ++m) rows[m] = q.template operand<s>(m, keys, n, lane);
+            if constexpr (s + HOLD < S) fetch_queries(first, Const<s + HOLD>{});
           }
-        } else {
+          multiply_rows_t<NO>(y, rows, part);  // steps along the lanes
+          if constexpr (!TILE) part_done();
+        });
+        if constexpr (sizeof(T) == 4) fetch_triangle(first);  // only now: registers
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (t < n && c + i < values) to[t * r.y.step + c + i] = static_cast<T>(y[m][i]);
+        for (int m = 0; m < kTiles; ++m) y[m] *= r.scale * lds.into[16 * m + x];
+      }
+      __syncthreads();
+      if constexpr (USE != kMaps) {
+        f32x4 u[kTiles];
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) u[m] = lds.u[wave][m][lane];
+        multiply_triangle<NO, false, true>(y, p, cut_tiles<NO>(u[0], u[1]), cut_tiles<NO>(u[2], u[3]));
+        if constexpr (sizeof(T) == 2) fetch_triangle(then);
+        if constexpr (!TILE) fetch_first_queries(then);
+        const int c = first_col + 16 * wave + 4 * g;
+        T *to = head_row<T>(r.y, span.batch, span.row + first, head);
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m) {
+          const int t = 16 * m + x;
+          if constexpr (WHOLE) {
+            if (t < n && c < values) {
+              const float e[4] = {y[m][0], y[m][1], y[m][2], y[m][3]};
+              store_vec(&at_lane_of(to, t * static_cast<uint32_t>(r.y.step) + c), e, false);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (t < n && c + i < values) to[t * r.y.step + c + i] = static_cast<T>(y[m][i]);
+          }
         }
       }
       again();
@@ -210,11 +238,11 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
 
 template <typename T>
 hipError_t launch_delta_forward(const fftmv_delta_rule_t &r, hipStream_t s) {
-  const int64_t runs = delta_runs(r.batch, r.steps, r.offsets != nullptr);
+  const int64_t runs = delta_runs(r.batch, r.steps, r.offsets != nullptr), sequences = r.batch * r.heads;
   DeltaWorkspace w;
-  delta_workspace(runs, r.heads, r.keys, r.values, r.dtype, false, r.workspace, &w);
-  const int64_t blocks = (r.values + kValues - 1) / kValues;
-  if (!grid_fits(runs * r.heads, kWave) || !grid_fits(r.batch * r.heads * blocks, kChainThreads))
+  delta_workspace(r.batch, r.steps, r.heads, r.keys, r.values, r.dtype, r.offsets != nullptr, false, r.workspace, &w);
+  const int64_t blocks = (r.values + kValues - 1) / kValues, units = (r.keys + kValues - 1) / kValues;
+  if (!grid_fits(runs * r.heads, kWave) || !grid_fits(sequences * ((r.values + 15) / 16), 512) || !grid_fits(sequences * w.cuts.parts * (blocks + units), kChainThreads))
     return hipErrorInvalidConfiguration;
   return by_keys(r.keys, [&](auto k) {
     constexpr int KEYS = decltype(k)::value;
@@ -222,12 +250,23 @@ hipError_t launch_delta_forward(const fftmv_delta_rule_t &r, hipStream_t s) {
       delta_factors_kernel<T, KEYS, false><<<static_cast<unsigned>(runs * r.heads), kWave, 0, s>>>(r, w);
       if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    const dim3 grid(static_cast<unsigned>(r.batch * r.heads), static_cast<unsigned>(blocks));
-    auto launch = [&](auto whole, auto save) {
-      delta_chain_kernel<T, KEYS, decltype(whole)::value != 0, decltype(save)::value != 0><<<grid, kChainThreads, 0, s>>>(r, w);
+    return by_two(delta_whole(r, r.v, r.y), [&](auto whole) {
+      constexpr bool WHOLE = decltype(whole)::value != 0;
+      const unsigned chains = static_cast<unsigned>(sequences * w.cuts.parts), columns = static_cast<unsigned>(blocks);
+      if (w.cuts.parts > 1) {
+        const dim3 all(chains, static_cast<unsigned>(blocks + units));
+        delta_chain_kernel<T, KEYS, WHOLE, kMaps><<<all, kChainThreads, 0, s>>>(r, w);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        delta_join_kernel<T, KEYS, false>
+            <<<dim3(static_cast<unsigned>(sequences), static_cast<unsigned>((r.values + 15) / 16)), KEYS / 16 * kWave, 0, s>>>(r, w);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+      }
+      if (r.carries)
+        delta_chain_kernel<T, KEYS, WHOLE, kCarries><<<dim3(chains, columns), kChainThreads, 0, s>>>(r, w);
+      else
+        delta_chain_kernel<T, KEYS, WHOLE, kOutputs><<<dim3(chains, columns), kChainThreads, 0, s>>>(r, w);
       return hipGetLastError();
-    };
-    return by_two(delta_whole(r, r.v, r.y), [&](auto whole) { return by_two(r.carries != nullptr, [&](auto save) { return launch(whole, save); }); });
+    });
   });
 }
 

@@ -138,6 +138,26 @@ def test_delta_packed(fm, dtype, V, cuts, T):
     check_delta(fm, 8, len(cuts) - 1, T, 1, 2, 32, V, dtype, spans=list(zip(cuts[:-1], cuts[1:])), packed=True)
 
 
+@pytest.mark.parametrize("dtype,B,T,Hk,H,K,V,lengths", [
+    ("bf16", 1, 2100, 1, 1, 128, 64, None), ("fp32", 1, 1300, 1, 2, 40, 72, None), ("fp16", 1, 1700, 2, 2, 64, 128, None),
+    ("bf16", 3, 1999, 1, 1, 75, 41, None), ("fp32", 4, 1500, 1, 1, 64, 33, [1500, 0, 449, 700]),
+    ("bf16", 5, 1536, 1, 1, 32, 16, [1, 1536, 1535, 512, 64]), ("fp32", 1, 1100, 1, 1, 128, 130, None)])
+def test_delta_long_sequences_in_parts(fm, dtype, B, T, Hk, H, K, V, lengths):
+    """Few heads and many steps: sequences cut into parts, ends inside, at the edges of and in front of parts."""
+    check_delta(fm, 13, B, T, Hk, H, K, V, dtype, spans=None if lengths is None else [(0, n) for n in lengths])
+
+
+def test_delta_parts_keep_what_the_beginning_left(fm):
+    """Decays of one: the first part's state reaches the last output."""
+    def change(q, k, v, gate, beta):
+        gate.fill_(40.0)
+        v[:, 64:] = 0.0
+        k[:, 64:] = 0.0
+        k[:, 64:, :, 0] = 1.0
+
+    check_delta(fm, 14, 1, 1400, 1, 1, 64, 64, "fp32", change=change)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_delta_gates_at_their_ends(fm, dtype):
     """A decay of zero clears the state, one of one keeps it; rates of zero write nothing, of one replace."""
