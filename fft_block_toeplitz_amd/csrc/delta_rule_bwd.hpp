@@ -277,9 +277,8 @@ struct GradsLds {
   alignas(16) uint16_t q[QUERIES ? NP * kRun * kTileRow<KEYS> : 8];
   alignas(16) u32x4 frags[FRAGS ? 3 * kFrags * NO * kWave : 1];
   union {
-    // U and Z first as they are, then with dY as they stand in the gradients' rows; u holds V's rows before U's
     struct {
-      alignas(16) uint16_t u[NO * kRun * VR], z[NO * kRun * VR], dy[NO * kRun * VR];
+      alignas(16) uint16_t u[NO * kRun * VR], z[NO * kRun * VR], dy[NP * kRun * VR];  // u holds V's rows before U's
     } one;
     struct {
       alignas(16) uint16_t f[NO * kRun * VR], h[NO * kRun * VR];
@@ -288,37 +287,42 @@ struct GradsLds {
   alignas(16) Factors f;
   float sums[kGradWaves][kRun];    // what of dG goes through the states by the keys, of each wave's values
   float rates[kFrontWaves][kRun];  // z . x, of each wave's values
+  double turned[kRun];             // q . dq over the heads that dq holds
   float turns[KEYS / 16][kRun];    // q . dq, of each 16 keys
   float lasts[kGradWaves];         // what the last step's G has beside
   float gram_rows[2 * kGrams][16], gram_cols[2 * kGrams][16], gram_rates[kGrams][16];
 };
 
-// One column of four result tiles as parts, for all waves to read by rows.
+// Four transposed result tiles (step 16 m + x, four columns) as parts, for all waves to read by rows.
 template <int N, int ROW>
-__device__ __forceinline__ void put_column(uint16_t *tile, const f32x4 (&v)[kTiles], int col, int lane) {
+__device__ __forceinline__ void put_transposed(uint16_t *tile, const f32x4 (&v)[kTiles], int col, int lane) {
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-  for (int m = 0; m < kTiles; ++m)
+  for (int m = 0; m < kTiles; ++m) {
+    f32x4 rest = v[m];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float rest = v[m][i];
+    for (int p = 0; p < N; ++p) {
+      bf16x4 part;
 #pragma unroll
-      for (int p = 0; p < N; ++p) {
-        const __bf16 part = static_cast<__bf16>(rest);
-        tile[(p * kRun + 16 * m + 4 * (lane / 16) + i) * ROW + col + lane % 16] = __builtin_bit_cast(uint16_t, part);
-        rest -= static_cast<float>(part);
+      for (int i = 0; i < 4; ++i) {
+        part[i] = static_cast<__bf16>(rest[i]);
+        rest[i] -= static_cast<float>(part[i]);
       }
+      *reinterpret_cast<bf16x4 *>(tile + (p * kRun + 16 * m + lane % 16) * ROW + col + 4 * (lane / 16)) = part;
     }
+  }
 }
 __device__ __forceinline__ f32x4 factor4(const float *f, int m, int lane) {
   return *reinterpret_cast<const f32x4 *>(f + 16 * m + 4 * (lane / 16));
 }
 
-template <typename T, int KEYS, bool WHOLE>
+// SHARED: several heads have the same queries and keys.
+template <typename T, int KEYS, bool WHOLE, bool SHARED>
 __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Tri = Triangles<T, true>;
-  constexpr bool QUERIES = sizeof(GradsLds<T, KEYS, true, false>) <= kLdsBytes;
-  constexpr bool FRAGS = sizeof(GradsLds<T, KEYS, QUERIES, true>) <= kLdsBytes;
+  constexpr bool FRAGS = sizeof(GradsLds<T, KEYS, false, true>) <= kLdsBytes;
+  constexpr bool QUERIES = sizeof(GradsLds<T, KEYS, true, FRAGS>) <= kLdsBytes;
   using Lds = GradsLds<T, KEYS, QUERIES, FRAGS>;
   constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32, VR = Lds::VR, KR = kTileRow<KEYS>;
   constexpr int KT = KEYS / 16, MT = kTiles * KT / kGradWaves;  // tiles of keys, and of steps for one of them a wave
@@ -355,19 +359,53 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     }
   };
 
+  // FP32 gradients of shared queries and keys add up in the outputs, others, which would round there, in registers
+  constexpr bool KEEP = SHARED && sizeof(T) == 2;
   f32x4 dq[MT], dk[MT];
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) dq[m] = dk[m] = f32x4{0, 0, 0, 0};
-  double turned = 0.0;  // wave 0, lane i: q_i . dq_i over the heads so far
+    for (int m = 0; m < MT; ++m) dq[m] = dk[m] = f32x4{0, 0, 0, 0};
+  };
+  clear();
+  if (thread < kRun) lds.turned[thread] = 0.0;
+  auto store_gradients = [&](bool add) __attribute__((always_inline)) {
+    again();
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int t = 16 * (tile_m + m) + x, key = 16 * tile_k + 4 * g;
+      if (t >= n) continue;
+      T *q = head_row<T>(r.dq, span.batch, row + t, key_head) + key, *k = head_row<T>(r.dk, span.batch, row + t, key_head) + key;
+      if (key + 4 <= keys) {
+        float a[4] = {dq[m][0], dq[m][1], dq[m][2], dq[m][3]}, b[4] = {dk[m][0], dk[m][1], dk[m][2], dk[m][3]};
+        if (SHARED && !KEEP && add) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] += static_cast<float>(q[i]), b[i] += static_cast<float>(k[i]);
+        }
+        store_vec(q, a, false);
+        store_vec(k, b, false);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (key + i < keys) {
+            const bool more = SHARED && !KEEP && add;
+            q[i] = static_cast<T>(more ? dq[m][i] + static_cast<float>(q[i]) : dq[m][i]);
+            k[i] = static_cast<T>(more ? dk[m][i] + static_cast<float>(k[i]) : dk[m][i]);
+          }
+      }
+    }
+  };
 
-  for (int64_t head = key_head * share; head < (key_head + 1) * share; ++head) {
+  int64_t head = key_head * share;
+  do {
     again();
     const int64_t at = slot * r.heads + head;
     const u32x4 *tri = w.triangles + at * Tri::kAll * kWave;
     // states and their gradients: rows behind the last read as zeros
     const auto state = __builtin_amdgcn_make_buffer_rsrc(r.carries + at * states, 0, static_cast<int>(states * 4), kBufferFlags);
     const auto grad = __builtin_amdgcn_make_buffer_rsrc(w.grads + at * states, 0, static_cast<int>(states * 4), kBufferFlags);
-    f32x4 gram[kGradJobs];
+    f32x4 gram[kGradJobs], yq[MT], zs[MT], ud[MT];  // the triangles' tiles; dY S^T, Z S^T and U D^T, transposed
+#pragma unroll
+    for (int m = 0; m < MT; ++m) yq[m] = zs[m] = ud[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int q = 0; q < kGradJobs; ++q) gram[q] = f32x4{0, 0, 0, 0};
     float last = 0.0f;  // of this wave's values: e^{G_last} <state, its gradient> and the sum of k . o
@@ -376,6 +414,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     if (thread < static_cast<int>(sizeof(Factors) / 16))
       reinterpret_cast<u32x4 *>(&lds.f)[thread] = at_lane(reinterpret_cast<const u32x4 *>(w.factors + at), thread);
     if (QUERIES && head % share == 0) fill(lds.q, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.q, span.batch, row, key_head, n, keys), 0);
+    again();
     if constexpr (FRAGS) {  // T diag(b), P^T and T^T, NO parts of each
       constexpr int N = kFrags * NO * kWave;
 #pragma unroll
@@ -389,13 +428,28 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     f32x4 by_row[2][kTiles];  // over this wave's values: z . x and b z . K S on U's side, u . K D on Z's
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) by_row[0][m] = by_row[1][m] = f32x4{0, 0, 0, 0};
+    // T diag(b), P^T and T^T; U and Z transposed: a lane has four neighbouring columns of a step
     auto triangle = [&](f32x4 (&c)[kTiles], auto which, const auto &lo, const auto &hi) __attribute__((always_inline)) {
       constexpr int W = decltype(which)::value;
-      if constexpr (FRAGS)
-        multiply_triangle<NO, NO, NO, W != 0>(c, lds.frags + W * kFrags * NO * kWave, lo, hi, lane);
-      else
-        multiply_triangle<NO, NO, W == 0 ? Tri::kTParts : kFull, W != 0>(
-            c, tri + (W == 0 ? Tri::kT : W == 1 ? Tri::kP : Tri::kTt) * kWave, lo, hi, lane);
+      constexpr bool UPPER = W != 0, TRANSPOSED = W != 1;
+      unrolled<0, 2>([&](auto half) __attribute__((always_inline)) {
+        constexpr int h = decltype(half)::value;
+        constexpr int first = UPPER || h == 0 ? 0 : 2, count = (UPPER ? in_upper(2, h) : in_lower(0, h)) ? 4 : 2;
+        Cut<NO> f[count];
+#pragma unroll
+        for (int m = 0; m < count; ++m) {
+          const int frag = UPPER ? upper_frag(first + m, h) : lower_frag(first + m, h);
+          if constexpr (FRAGS)
+            f[m] = load_frag<NO>(lds.frags + W * kFrags * NO * kWave, frag, NO, lane);
+          else
+            f[m] = load_frag<NO>(tri + (W == 0 ? Tri::kT : W == 1 ? Tri::kP : Tri::kTt) * kWave, frag, W == 0 ? Tri::kTParts : kFull, lane);
+        }
+        if constexpr (TRANSPOSED)
+          multiply_rows_t<NO>(c + first, f, h ? hi : lo);
+        else
+          multiply_rows<NO>(c + first, f, h ? hi : lo);
+        if constexpr (!FRAGS || KEYS == 128) part_done();
+      });
     };
 
     for (int from = 0; from < values; from += kValues) {
@@ -432,20 +486,22 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         Cut<NP> k[kTiles];
         tile_rows<KEYS>(k, lds.k, s, lane);
         multiply_rows<NO>(p, k, cut<NO>(a[s]));
+        if constexpr (KEYS == 128 && (SHARED || sizeof(T) == 4)) part_done();
       }
       // rows of the state and its gradient, for the products at the end
       u32x4 rows[kValues / 32][2][2];
-      auto fetch_rows_of_states = [&]() __attribute__((always_inline)) {
+      auto fetch_rows_of_states = [&](auto part) __attribute__((always_inline)) {
+        constexpr int s = decltype(part)::value;
 #pragma unroll
-        for (int s = 0; s < kValues / 32; ++s)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int byte = ((16 * tile_k + x) * values + from + 32 * s + 8 * g + 4 * h) * 4;
-            rows[s][0][h] = __builtin_amdgcn_raw_buffer_load_b128(state, byte, 0, 0);
-            rows[s][1][h] = __builtin_amdgcn_raw_buffer_load_b128(grad, byte, 0, 0);
-          }
+        for (int h = 0; h < 2; ++h) {
+          const int byte = ((16 * tile_k + x) * values + from + 32 * s + 8 * g + 4 * h) * 4;
+          rows[s][0][h] = __builtin_amdgcn_raw_buffer_load_b128(state, byte, 0, 0);
+          rows[s][1][h] = __builtin_amdgcn_raw_buffer_load_b128(grad, byte, 0, 0);
+        }
       };
-      if constexpr (sizeof(T) == 2) fetch_rows_of_states();  // FP32 has no registers for them
+      // where registers are left
+      constexpr bool EARLY = sizeof(T) == 2 && !(SHARED && KEYS == 128);
+      if constexpr (EARLY) unrolled<0, kValues / 32>(fetch_rows_of_states);
       part_done();
       if (first_side) {
 #pragma unroll
@@ -461,7 +517,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         }
         part_done();
         triangle(o, Const<0>{}, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]));
-        put_column<NO, VR>(lds.one.u, o, 16 * column, lane);
+        put_transposed<NO, VR>(lds.one.u, o, 16 * column, lane);
       } else {
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) {
@@ -474,7 +530,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
                  plain_columns<VR, NP, 16>(lds.one.dy, 32, 16 * column, lane));
         part_done();
         triangle(o, Const<2>{}, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]));
-        put_column<NO, VR>(lds.one.z, o, 16 * column, lane);
+        put_transposed<NO, VR>(lds.one.z, o, 16 * column, lane);
       }
       __syncthreads();
       again();
@@ -489,6 +545,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
             multiply<NO>(gram[q], tile_rows<kValues, NP>(lds.one.dy, gram_row(tile), s, lane), u);
           else
             multiply<NO>(gram[q], tile_rows<kValues, NO>(lds.one.z, gram_row(tile), s, lane), u);
+          if constexpr (KEYS == 128 && SHARED) part_done();
         }
       }
       part_done();
@@ -523,34 +580,21 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
       }
       part_done();
       again();
-      if (first_side) {
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
+      for (int m = 0; m < kTiles; ++m) {
+        if (first_side) {
           const f32x4 z = tile_values<VR, NO>(lds.one.z, m, 16 * column, lane);
           by_row[0][m] += z * in[m];
           by_row[1][m] += factor4(lds.f.rate, m, lane) * z * p[m];
-          in[m] = tile_values<VR, NP>(lds.one.dy, m, 16 * column, lane) * (factor4(lds.f.into, m, lane) * r.scale);
-          o[m] *= factor4(lds.f.out, m, lane);
-          part_done();
-        }
-      }
-      __syncthreads();
-      if (first_side) {
-        put_column<NO, VR>(lds.one.dy, in, 16 * column, lane);
-      } else {
-#pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
+        } else {
           by_row[1][m] += tile_values<VR, NO>(lds.one.u, m, 16 * column, lane) * p[m];
-          o[m] *= -(factor4(lds.f.rate, m, lane) * factor4(lds.f.into, m, lane));
-          part_done();
         }
-        put_column<NO, VR>(lds.one.z, o, 16 * column, lane);
+        part_done();
       }
-      Cut<NO> sp[kValues / 32], dp[kValues / 32];
       again();
-      if constexpr (sizeof(T) == 4) fetch_rows_of_states();
-#pragma unroll
-      for (int s = 0; s < kValues / 32; ++s) {
+      unrolled<0, kValues / 32>([&](auto part) __attribute__((always_inline)) {
+        constexpr int s = decltype(part)::value;
+        if constexpr (!EARLY) fetch_rows_of_states(part);
         const int c = from + 32 * s + 8 * g;
         float b[2][8];
 #pragma unroll
@@ -571,20 +615,21 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 #pragma unroll
           for (int e = 0; e < 8; ++e) last = fmaf(b[0][e] * lds.f.into[kRun - 1], b[1][e], last);
         }
-        sp[s] = cut<NO>(b[0]);
-        dp[s] = cut<NO>(b[1]);
-      }
-      __syncthreads();
-      if (first_side) put_column<NO, VR>(lds.one.u, o, 16 * column, lane);
-      __syncthreads();
-#pragma unroll
-      for (int s = 0; s < kValues / 32; ++s)
+        const Cut<NO> sp = cut<NO>(b[0]), dp = cut<NO>(b[1]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          multiply<NO>(dq[m], sp[s], tile_rows<kValues, NO>(lds.one.dy, tile_m + m, s, lane));
-          multiply<NO>(dk[m], sp[s], tile_rows<kValues, NO>(lds.one.z, tile_m + m, s, lane));
-          multiply<NO>(dk[m], dp[s], tile_rows<kValues, NO>(lds.one.u, tile_m + m, s, lane));
+          multiply<NO>(yq[m], sp, tile_rows<kValues, NP>(lds.one.dy, tile_m + m, s, lane));
+          multiply<NO>(zs[m], sp, tile_rows<kValues, NO>(lds.one.z, tile_m + m, s, lane));
+          multiply<NO>(ud[m], dp, tile_rows<kValues, NO>(lds.one.u, tile_m + m, s, lane));
+          if constexpr (KEYS == 128 && (SHARED || sizeof(T) == 4)) part_done();
         }
+      });
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {  // a step's factors are a lane's here
+      const int t = 16 * (tile_m + m) + x;
+      dq[m] += yq[m] * (r.scale * lds.f.into[t]);
+      dk[m] += ud[m] * lds.f.out[t] - zs[m] * (lds.f.rate[t] * lds.f.into[t]);
     }
 #pragma unroll
     for (int m = 0; m < kTiles; ++m) {
@@ -641,7 +686,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
       for (int i = 0; i < 4; ++i) {
         const int t = 16 * m + 4 * g + i;
         const bool in = job < kGrams ? j <= t : j < t;
-        const float e = in ? expf(static_cast<float>(lds.f.sum[t] - sum_j)) : 0.0f;
+        const float e = in ? exp_of<T>(static_cast<float>(lds.f.sum[t] - sum_j)) : 0.0f;
         // dG_t: q . dq holds this row of P but for its diagonal, which e^{G_t - G_t} is no factor of
         float v = (job < kGrams ? r.scale : -lds.f.rate[t]) * e * gram[q][i], line, rate = 0.0f;
         if (!in) v = 0.0f;
@@ -712,18 +757,19 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
       if (g == 0) lds.turns[tile_k][t] = sum;
     }
     __syncthreads();
+    again();
     if (wave == 0) {  // the gates: lane i has step i
-      double own = -turned, rate = 0.0, end = 0.0;
-      turned = 0.0;
+      double turned = 0.0, rate = 0.0, end = 0.0;
 #pragma unroll
       for (int v = 0; v < KT; ++v) turned += lds.turns[v][lane];
+      double own = KEEP ? turned - lds.turned[lane] : turned;
+      if constexpr (KEEP) lds.turned[lane] = turned;
 #pragma unroll
       for (int v = 0; v < kGradWaves; ++v) {
         own -= lds.sums[v][lane];
         if (v < kFrontWaves) rate += lds.rates[v][lane];
         end += lds.lasts[v];
       }
-      own += turned;
 #pragma unroll
       for (int job = 0; job < 2 * kGrams; ++job) {
         const int tile = job % kGrams;
@@ -746,26 +792,12 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         *head_row<T>(r.dbeta, span.batch, row + lane, head) = static_cast<T>(static_cast<float>(rate) * turn);
       }
     }
-  }
-  again();
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = 16 * (tile_m + m) + x, key = 16 * tile_k + 4 * g;
-    if (t >= n) continue;
-    T *q = head_row<T>(r.dq, span.batch, row + t, key_head) + key, *k = head_row<T>(r.dk, span.batch, row + t, key_head) + key;
-    if (key + 4 <= keys) {
-      const float a[4] = {dq[m][0], dq[m][1], dq[m][2], dq[m][3]}, b[4] = {dk[m][0], dk[m][1], dk[m][2], dk[m][3]};
-      store_vec(q, a, false);
-      store_vec(k, b, false);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (key + i < keys) {
-          q[i] = static_cast<T>(dq[m][i]);
-          k[i] = static_cast<T>(dk[m][i]);
-        }
+    if constexpr (SHARED && !KEEP) {
+      store_gradients(head > key_head * share);
+      clear();
     }
-  }
+  } while (SHARED && ++head < (key_head + 1) * share);
+  if constexpr (!SHARED || KEEP) store_gradients(false);
 }
 
 template <typename T>
@@ -800,9 +832,11 @@ hipError_t launch_delta_backward(const fftmv_delta_rule_t &r, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (runs == 0) return hipSuccess;
     return by_two(delta_whole(r, r.dy, r.v), [&](auto whole) {
-      delta_grads_kernel<T, KEYS, decltype(whole)::value != 0>
-          <<<static_cast<unsigned>(runs * r.key_heads), kGradThreads, 0, s>>>(r, w);
-      return hipGetLastError();
+      return by_two(r.heads > r.key_heads, [&](auto shared) {
+        delta_grads_kernel<T, KEYS, decltype(whole)::value != 0, decltype(shared)::value != 0>
+            <<<static_cast<unsigned>(runs * r.key_heads), kGradThreads, 0, s>>>(r, w);
+        return hipGetLastError();
+      });
     });
   });
 }
