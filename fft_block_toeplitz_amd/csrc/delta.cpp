@@ -160,7 +160,7 @@ int fftmv_qk_norm_workspace(int64_t batch, int64_t steps, int64_t query_heads, i
   if (dim > FFTMV_QK_NORM_DIM || !sizes_fit(batch, steps, query_heads) || !sizes_fit(key_heads, 1, 1) ||
       !sizes_fit(batch * steps, 1, kNormRows * (query_heads + key_heads)))
     return FFTMV_ERR_UNSUPPORTED_SIZE;
-  *bytes = qk_norm_workspace(batch * steps, dim);
+  *bytes = qk_norm_workspace(batch * steps, query_heads, key_heads, dim);
   return FFTMV_SUCCESS;
 }
 

@@ -3,78 +3,118 @@
 namespace fftmv {
 namespace {
 
-// The elements of a lane's pairs 4 l..4 l + 3 of one head: two runs of four
-// (rotated halves), one run of eight (neighbours, and what is not rotated), or
-// whatever is left at borders, one by one.
+// Where a lane's elements are: slots 0..3 and 4..7 from `first` and `second`
+// on, or each by itself. Rotated halves: pair e in slots e and e + 4;
+// neighbours: in slots 2 e and 2 e + 1.
 struct Lane {
-  int first, second;  // element of pair 0's halves
-  int mode;           // 0: four and four, 1: eight, 2: one by one, 3: nothing
+  int first, second;
+  bool whole;      // by fours
+  uint32_t owned;  // slots that are this lane's alone, bit by bit
+  int turns;       // its cosines
 };
-__device__ __forceinline__ int pair_first(int p, int turned, bool halves) { return halves && p < turned ? p : 2 * p; }
-__device__ __forceinline__ int pair_second(int p, int turned, bool halves) {
-  return halves && p < turned ? p + turned : 2 * p + 1;
+// The element of a slot of a lane that takes them one by one, or -1.
+__device__ __forceinline__ int element_of(const NormPlan &s, bool halves, int l, int slot) {
+  const int p = kNormPairs * l + (halves ? slot % kNormPairs : slot / 2);
+  const bool odd = halves ? slot >= kNormPairs : slot % 2;
+  const int i = halves && p < s.turned ? p + (odd ? s.turned : 0) : 2 * p + odd;
+  return i < s.dim ? i : -1;
 }
-__device__ __forceinline__ Lane lane_of(int l, int turned, bool halves, int dim) {
-  const int p = kNormPairs * l, end = p + kNormPairs;
-  Lane r = {pair_first(p, turned, halves), pair_second(p, turned, halves), 2};
-  if (2 * p >= dim && (!halves || p >= turned))
-    r.mode = 3;
-  else if (halves && end <= turned)
-    r.mode = 0;
-  else if ((!halves || p >= turned) && 2 * end <= dim)
-    r.mode = 1;
+// The rotated pair of a lane's e-th.
+template <bool WHOLE>
+__device__ __forceinline__ int pair_of(const NormPlan &s, int l, int e) {
+  const int p = kNormPairs * l;
+  return (WHOLE ? min(p, s.turned - kNormPairs) : p) + e;
+}
+template <bool WHOLE>
+__device__ __forceinline__ Lane lane_of(const NormPlan &s, bool halves, int l) {
+  Lane r = {0, 4, true, 0, min(l, s.turned_lanes) * kNormPairs};
+  const int p = kNormPairs * l;
+  if constexpr (WHOLE) {
+    if (l < s.turned_lanes) {
+      const int from = pair_of<WHOLE>(s, l, 0), shared = p - from;
+      r.first = halves ? from : 2 * from;
+      r.second = halves ? from + s.turned : 2 * from + 4;
+      r.owned = halves ? (0xfu & (0xfu << shared)) * 0x11u : 0xffu & (0xffu << 2 * shared);
+    } else {
+      const int at = 2 * s.turned + kNormElements * (l - s.turned_lanes), from = min(at, s.dim - kNormElements);
+      r.first = from;
+      r.second = from + 4;
+      r.owned = at < s.dim ? 0xffu & (0xffu << (at - from)) : 0;
+    }
+  } else {
+    r.whole = halves && p < s.turned ? p + kNormPairs <= s.turned : 2 * p + kNormElements <= s.dim;
+    r.first = halves && p < s.turned ? p : 2 * p;
+    r.second = halves && p < s.turned ? p + s.turned : 2 * p + 4;
+#pragma unroll
+    for (int e = 0; e < kNormElements; ++e)
+      if (element_of(s, halves, l, e) >= 0) r.owned |= 1u << e;
+  }
   return r;
 }
 
+// A lane's elements as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load_pairs(const T *x, const Lane &at, int l, int turned, bool halves, int dim,
-                                           float (&a)[kNormPairs], float (&b)[kNormPairs]) {
-  if (at.mode == 0) {
-    const Vec<T, 4> u = load_vec<T, 4>(x + at.first), v = load_vec<T, 4>(x + at.second);
+struct Raw {
+  Vec<T, 4> part[2];
+  __device__ __forceinline__ float operator[](int e) const { return part[e / 4][e % 4]; }
+};
+// Lanes without elements read some of their neighbours' where all are taken by fours.
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void fetch(Raw<T> &r, const T *x, const Lane &at, const NormPlan &s, bool halves, int l) {
+  if (WHOLE || at.whole) {
+    r.part[0] = load_vec<T, 4>(x + at.first);
+    r.part[1] = load_vec<T, 4>(x + at.second);
+  } else if (at.owned) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a[e] = u[e], b[e] = v[e];
-  } else if (at.mode == 1) {
-    const Vec<T, 4> u = load_vec<T, 4>(x + at.first), v = load_vec<T, 4>(x + at.first + 4);
-    a[0] = u[0], b[0] = u[1], a[1] = u[2], b[1] = u[3];
-    a[2] = v[0], b[2] = v[1], a[3] = v[2], b[3] = v[3];
-  } else {
-#pragma unroll
-    for (int e = 0; e < kNormPairs; ++e) {
-      const int p = kNormPairs * l + e, i = pair_first(p, turned, halves), j = pair_second(p, turned, halves);
-      a[e] = at.mode == 2 && i < dim ? static_cast<float>(x[i]) : 0.0f;
-      b[e] = at.mode == 2 && j < dim ? static_cast<float>(x[j]) : 0.0f;
+    for (int e = 0; e < kNormElements; ++e) {
+      const int i = element_of(s, halves, l, e);
+      r.part[e / 4].v[e % 4] = i >= 0 ? x[i] : static_cast<T>(0.0f);
     }
   }
 }
-template <typename T>
-__device__ __forceinline__ void store_pairs(T *y, const Lane &at, int l, int turned, bool halves, int dim,
-                                            const float (&a)[kNormPairs], const float (&b)[kNormPairs]) {
-  if (at.mode == 0) {
-    store_vec(y + at.first, a);
-    store_vec(y + at.second, b);
-  } else if (at.mode == 1) {
-    const float u[8] = {a[0], b[0], a[1], b[1], a[2], b[2], a[3], b[3]};
-    if constexpr (sizeof(T) == 2) {
-      store_vec(y + at.first, u);
-    } else {
-      const float lo[4] = {u[0], u[1], u[2], u[3]}, hi[4] = {u[4], u[5], u[6], u[7]};
-      store_vec(y + at.first, lo);
-      store_vec(y + at.first + 4, hi);
-    }
-  } else if (at.mode == 2) {
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void put(T *y, const float (&v)[kNormElements], const Lane &at, const NormPlan &s, bool halves,
+                                    int l) {
+  if (!at.owned) return;
+  if (WHOLE || at.whole) {
+    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+    store_vec(y + at.first, lo);
+    store_vec(y + at.second, hi);
+  } else {
 #pragma unroll
-    for (int e = 0; e < kNormPairs; ++e) {
-      const int p = kNormPairs * l + e, i = pair_first(p, turned, halves), j = pair_second(p, turned, halves);
-      if (i < dim) y[i] = static_cast<T>(a[e]);
-      if (j < dim) y[j] = static_cast<T>(b[e]);
+    for (int e = 0; e < kNormElements; ++e) {
+      const int i = element_of(s, halves, l, e);
+      if (i >= 0) y[i] = static_cast<T>(v[e]);
     }
   }
 }
 
+// The pairs of a lane turned by their angles.
+__device__ __forceinline__ void turn(float (&v)[kNormElements], const float4 &cosines, const float4 &sines, bool halves) {
+  const float c[4] = {cosines.x, cosines.y, cosines.z, cosines.w}, s[4] = {sines.x, sines.y, sines.z, sines.w};
+  const auto pair = [&](int e, float &a, float &b) {
+    const float x = a, y = b;
+    a = fmaf(x, c[e], -(y * s[e]));
+    b = fmaf(y, c[e], x * s[e]);
+  };
+  if (halves) {
+#pragma unroll
+    for (int e = 0; e < kNormPairs; ++e) pair(e, v[e], v[e + 4]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kNormPairs; ++e) pair(e, v[2 * e], v[2 * e + 1]);
+  }
+}
+
+// The sum over the LANES lanes of a head, the same in each of them.
 template <int LANES>
 __device__ __forceinline__ float across(float v) {
-#pragma unroll
-  for (int d = 1; d < LANES; d *= 2) v += __shfl_xor(v, d);
+  v += dpp<kDppQuadXor1>(v);
+  v += dpp<kDppQuadXor2>(v);
+  v += dpp<kDppRowHalfMirror>(v);
+  if constexpr (LANES >= 16) v += dpp<kDppRowMirror>(v);
+  if constexpr (LANES >= 32) v += __shfl_xor(v, 16);
+  if constexpr (LANES >= 64) v += __shfl_xor(v, 32);
   return v;
 }
 
@@ -85,140 +125,181 @@ __device__ __forceinline__ float inverse_root(float v) {
   return __builtin_amdgcn_rsqf(v);
 }
 
-template <typename T>
-__device__ __forceinline__ T *row_of(const fftmv_heads_t &f, int64_t b, int64_t t, int64_t head) {
-  return static_cast<T *>(f.data) + b * f.batch + t * f.step + head * f.head;
-}
+// A row of a workgroup: where it begins in x, dy and y (dx), in elements, and
+// its position. Rows behind their sequence have nothing to read.
+struct NormRow {
+  int64_t x, dy, to;
+  double position;
+  int held;
+};
 
-template <typename T, int LANES, bool BACK>
-__global__ __launch_bounds__(kBlock) void qk_norm_kernel(fftmv_qk_norm_t n, NormPlan plan, float *partials) {
-  constexpr int GROUPS = kBlock / LANES;
-  __shared__ float2 turns[kNormTurns];
-  const int turned = static_cast<int>(n.frequencies), dim = static_cast<int>(n.dim);
-  const bool halves = n.pairs == FFTMV_PAIRS_HALVES;
+template <typename T, int LANES, bool WHOLE, bool BACK>
+__global__ __launch_bounds__(kBlock) void qk_norm_kernel(fftmv_qk_norm_t n, NormPlan s, float *partials) {
+  constexpr int GROUPS = kBlock / LANES, SLOTS = LANES * kNormElements;
+  __shared__ float4 turns[2][kNormTurns / 4];
+  __shared__ NormRow table[kNormRows];
+  const bool halves = n.pairs == FFTMV_PAIRS_HALVES, query = static_cast<int>(blockIdx.x) < s.blocks[0];
+  const int block = query ? blockIdx.x : blockIdx.x - s.blocks[0], blocks = s.blocks[query ? 0 : 1];
+  const int most = s.rows[query ? 0 : 1], heads = static_cast<int>(query ? n.query_heads : n.key_heads);
+  const fftmv_heads_t from = query ? n.q : n.k, grad = query ? n.dqy : n.dky;
+  const fftmv_heads_t to = BACK ? (query ? n.dq : n.dk) : (query ? n.qy : n.ky);
+  const float *weight = query ? n.q_weight : n.k_weight;
   const int l = threadIdx.x % LANES, group = threadIdx.x / LANES;
-  const Lane at = lane_of(l, turned, halves, dim);
-  const int64_t rows = n.batch * n.steps;
-  const int heads = static_cast<int>(n.query_heads + n.key_heads), queries = static_cast<int>(n.query_heads);
-  const float over = n.norm == FFTMV_NORM_RMS ? 1.0f / dim : 1.0f;
-  float wq[2][kNormPairs], wk[2][kNormPairs], gq[2][kNormPairs] = {}, gk[2][kNormPairs] = {};
+  const Lane at = lane_of<WHOLE>(s, halves, l);
+  const uint32_t rows = static_cast<uint32_t>(n.batch * n.steps), steps = static_cast<uint32_t>(n.steps);
+  const float over = n.norm == FFTMV_NORM_RMS ? 1.0f / s.dim : 1.0f;
+  float w[kNormElements], dw[kNormElements] = {};
+  Raw<float> weights;
 #pragma unroll
-  for (int e = 0; e < kNormPairs; ++e) {
-    const int p = kNormPairs * l + e, i = pair_first(p, turned, halves), j = pair_second(p, turned, halves);
-    wq[0][e] = n.q_weight && i < dim ? n.q_weight[i] : 1.0f;
-    wq[1][e] = n.q_weight && j < dim ? n.q_weight[j] : 1.0f;
-    wk[0][e] = n.k_weight && i < dim ? n.k_weight[i] : 1.0f;
-    wk[1][e] = n.k_weight && j < dim ? n.k_weight[j] : 1.0f;
-  }
-  for (int64_t first = static_cast<int64_t>(blockIdx.x) * plan.rows; first < rows;
-       first += static_cast<int64_t>(gridDim.x) * plan.rows) {
-    const int count = static_cast<int>(min(static_cast<int64_t>(plan.rows), rows - first));
-    if (turned) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < count * turned; i += kBlock) {
-        const int64_t row = first + i / turned, b = row / n.steps, t = row - b * n.steps;
-        const double position = n.positions ? n.positions[b * n.position_batch + t] : static_cast<double>(t);
-        double turn = position * n.frequency[i % turned] * 0.15915494309189533577;  // 1 / (2 pi)
-        turn -= rint(turn);
-        float sn, cs;
-        sincospif(2.0f * static_cast<float>(turn), &sn, &cs);
-        turns[i] = make_float2(cs, sn);
+  for (int e = 0; e < kNormElements; ++e) weights.part[e / 4].v[e % 4] = 1.0f;
+  if (weight) fetch<WHOLE>(weights, weight, at, s, halves, l);
+#pragma unroll
+  for (int e = 0; e < kNormElements; ++e) w[e] = weights[e];
+  // the next of a group's heads, `GROUPS` further along the rows
+  const int down = GROUPS / heads, along = GROUPS - down * heads;
+  for (uint32_t first = static_cast<uint32_t>(block) * most; first < rows; first += static_cast<uint32_t>(blocks) * most) {
+    const int count = static_cast<int>(min(static_cast<uint32_t>(most), rows - first));
+    int r = group / heads, h = group - r * heads;
+    Raw<T> x = {}, dy = {};
+    const auto take = [&](int64_t x0, int64_t dy0) {
+      fetch<WHOLE>(x, static_cast<const T *>(from.data) + x0 + h * from.head, at, s, halves, l);
+      if constexpr (BACK) fetch<WHOLE>(dy, static_cast<const T *>(grad.data) + dy0 + h * grad.head, at, s, halves, l);
+    };
+    if (r < count) {  // the first head needs no table, and is fetched held or not
+      const uint32_t b = (first + r) / steps, t = first + r - b * steps;
+      take(b * from.batch + t * from.step, b * grad.batch + t * grad.step);
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < count) {
+      const uint32_t row = first + threadIdx.x, b = row / steps, t = row - b * steps;
+      table[threadIdx.x] = {b * from.batch + t * from.step, b * grad.batch + t * grad.step, b * to.batch + t * to.step,
+                            n.positions ? static_cast<double>(n.positions[b * n.position_batch + t]) : static_cast<double>(t),
+                            !n.lengths || static_cast<int>(t) < n.lengths[b]};
+    }
+    __syncthreads();
+    if (s.turned) {
+      float *cosines = reinterpret_cast<float *>(turns[0]), *sines = reinterpret_cast<float *>(turns[1]);
+      for (int i = threadIdx.x; i < count * s.turns; i += kBlock) {
+        const int row = i / s.turns, slot = i - row * s.turns;
+        const int p = pair_of<WHOLE>(s, slot / kNormPairs, slot % kNormPairs);
+        float sn = 0.0f, cs = 1.0f;
+        if (slot < s.turns - kNormPairs && p < s.turned) {
+          double angle = table[row].position * n.frequency[p] * 0.15915494309189533577;  // 1 / (2 pi)
+          angle -= rint(angle);
+          sincospif(2.0f * static_cast<float>(angle), &sn, &cs);
+        }
+        cosines[i] = cs;
+        sines[i] = sn;
       }
       __syncthreads();
     }
-    for (int i = group; i < count * heads; i += GROUPS) {
-      const int r = i / heads, h = i - r * heads;
-      const int64_t row = first + r, b = row / n.steps, t = row - b * n.steps;
-      const bool query = h < queries;
-      const int64_t head = query ? h : h - queries;
-      const bool held = !n.lengths || t < n.lengths[b];
-      float a[kNormPairs] = {}, c[kNormPairs] = {};
-      if (held) load_pairs(row_of<const T>(query ? n.q : n.k, b, t, head), at, l, turned, halves, dim, a, c);
-      float dy[2][kNormPairs] = {};
-      if constexpr (BACK) {
-        if (held) load_pairs(row_of<const T>(query ? n.dqy : n.dky, b, t, head), at, l, turned, halves, dim, dy[0], dy[1]);
+    while (r < count) {
+      float v[kNormElements], g[kNormElements];
+#pragma unroll
+      for (int e = 0; e < kNormElements; ++e) v[e] = x[e], g[e] = dy[e];
+      const int row = r;
+      const bool held = table[row].held;
+      T *y = static_cast<T *>(to.data) + table[row].to + h * to.head;
+      r += down, h += along;
+      if (h >= heads) h -= heads, ++r;
+      if (r < count && table[r].held) take(table[r].x, table[r].dy);
+      if (!held) {
+#pragma unroll
+        for (int e = 0; e < kNormElements; ++e) v[e] = 0.0f;
+        put<WHOLE>(y, v, at, s, halves, l);
+        continue;
       }
       float sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < kNormPairs; ++e) sum = fmaf(a[e], a[e], fmaf(c[e], c[e], sum));
-      const float inverse = held ? inverse_root<T>(fmaf(across<LANES>(sum), over, n.eps)) : 0.0f;
+      for (int e = 0; e < kNormElements; ++e) {
+        const float u = at.owned >> e & 1 ? v[e] : 0.0f;
+        sum = fmaf(u, u, sum);
+      }
+      const float inverse = inverse_root<T>(fmaf(across<LANES>(sum), over, n.eps));
+      float4 cs = {}, sn = {};
+      if (s.turned) {
+        const int i = (row * s.turns + at.turns) / 4;
+        cs = turns[0][i], sn = turns[1][i];
+      }
       if constexpr (!BACK) {
 #pragma unroll
-        for (int e = 0; e < kNormPairs; ++e) {
-          const int p = kNormPairs * l + e;
-          const float u = a[e] * inverse * (query ? wq[0][e] : wk[0][e]), v = c[e] * inverse * (query ? wq[1][e] : wk[1][e]);
-          const float2 w = p < turned ? turns[r * turned + p] : make_float2(1.0f, 0.0f);
-          a[e] = held ? fmaf(u, w.x, -(v * w.y)) : 0.0f;
-          c[e] = held ? fmaf(v, w.x, u * w.y) : 0.0f;
-        }
-        store_pairs(row_of<T>(query ? n.qy : n.ky, b, t, head), at, l, turned, halves, dim, a, c);
+        for (int e = 0; e < kNormElements; ++e) v[e] *= inverse * w[e];
+        if (s.turned) turn(v, cs, sn, halves);
       } else {
+        if (s.turned) turn(g, cs, make_float4(-sn.x, -sn.y, -sn.z, -sn.w), halves);
         float inner = 0.0f;
 #pragma unroll
-        for (int e = 0; e < kNormPairs; ++e) {
-          const int p = kNormPairs * l + e;
-          const float2 w = p < turned ? turns[r * turned + p] : make_float2(1.0f, 0.0f);
-          const float u = fmaf(dy[0][e], w.x, dy[1][e] * w.y), v = fmaf(dy[1][e], w.x, -(dy[0][e] * w.y));
-          a[e] *= inverse;  // x / n
-          c[e] *= inverse;
-          (query ? gq[0][e] : gk[0][e]) += u * a[e];
-          (query ? gq[1][e] : gk[1][e]) += v * c[e];
-          dy[0][e] = u * (query ? wq[0][e] : wk[0][e]);
-          dy[1][e] = v * (query ? wq[1][e] : wk[1][e]);
-          inner = fmaf(dy[0][e], a[e], fmaf(dy[1][e], c[e], inner));
+        for (int e = 0; e < kNormElements; ++e) {
+          v[e] *= inverse;  // x / n
+          dw[e] = fmaf(g[e], v[e], dw[e]);
+          g[e] *= w[e];
+          inner = fmaf(at.owned >> e & 1 ? g[e] : 0.0f, v[e], inner);
         }
         inner = across<LANES>(inner) * over;
 #pragma unroll
-        for (int e = 0; e < kNormPairs; ++e) {
-          a[e] = held ? inverse * fmaf(-a[e], inner, dy[0][e]) : 0.0f;
-          c[e] = held ? inverse * fmaf(-c[e], inner, dy[1][e]) : 0.0f;
-        }
-        store_pairs(row_of<T>(query ? n.dq : n.dk, b, t, head), at, l, turned, halves, dim, a, c);
+        for (int e = 0; e < kNormElements; ++e) v[e] = inverse * fmaf(-v[e], inner, g[e]);
       }
+      put<WHOLE>(y, v, at, s, halves, l);
     }
   }
   if constexpr (BACK) {
     if (!partials) return;
-    // the groups' sums, joined in a fixed order: one weight and half of the pairs after the other
+    // the groups' sums, joined in a fixed order
     float *sums = reinterpret_cast<float *>(turns);
-    static_assert(sizeof(turns) >= kBlock * kNormPairs * sizeof(float), "one sum of each thread");
+    static_assert(sizeof(turns) >= kBlock * kNormElements * sizeof(float), "eight sums of each thread");
+    __syncthreads();
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < kNormPairs; ++e)
-        sums[group * (LANES * kNormPairs) + l * kNormPairs + e] = v < 2 ? gq[v][e] : gk[v - 2][e];
-      __syncthreads();
-      for (int p = threadIdx.x; p < LANES * kNormPairs; p += kBlock) {
-        const int i = v % 2 ? pair_second(p, turned, halves) : pair_first(p, turned, halves);
-        if (i >= dim) continue;
-        float s = 0.0f;
+    for (int e = 0; e < kNormElements; ++e) sums[group * SLOTS + e * LANES + l] = dw[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < SLOTS; i += kBlock) {
+      const int e = i / LANES;  // of this thread's own lane: LANES divides kBlock
+      if (!(at.owned >> e & 1)) continue;
+      const int j = !WHOLE && !at.whole ? element_of(s, halves, l, e) : e < 4 ? at.first + e : at.second + e - 4;
+      float sum = 0.0f;
 #pragma unroll 4
-        for (int q = 0; q < GROUPS; ++q) s += sums[q * (LANES * kNormPairs) + p];
-        partials[(static_cast<int64_t>(blockIdx.x) * 2 + v / 2) * dim + i] = s;
-      }
+      for (int q = 0; q < GROUPS; ++q) sum += sums[q * SLOTS + i];
+      partials[static_cast<int64_t>(blockIdx.x) * s.dim + j] = sum;
     }
   }
 }
 
 // The workgroups' sums for one element of one weight each: a wave's lanes take
 // every 64th, and add up across.
-__global__ __launch_bounds__(kWave) void qk_norm_sums_kernel(const float *partials, int blocks, int dim, float *dq, float *dk) {
-  const int i = blockIdx.x % dim, which = blockIdx.x / dim;
-  float *to = which ? dk : dq;
+__global__ __launch_bounds__(kWave) void qk_norm_sums_kernel(const float *partials, int queries, int keys, int dim, float *dq,
+                                                             float *dk) {
+  const bool query = static_cast<int>(blockIdx.x) < dim;
+  const int i = query ? blockIdx.x : blockIdx.x - dim, blocks = query ? queries : keys;
+  float *to = query ? dq : dk;
   if (!to) return;
-  float s = 0.0f;
-  for (int b = threadIdx.x; b < blocks; b += kWave) s += partials[(static_cast<int64_t>(b) * 2 + which) * dim + i];
-  s = across<kWave>(s);
-  if (threadIdx.x == 0) to[i] = s;
+  if (!query) partials += static_cast<int64_t>(queries) * dim;
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int b = threadIdx.x; b < blocks; b += kWave) sum += partials[static_cast<int64_t>(b) * dim + i];
+  sum = across<kWave>(sum);
+  if (threadIdx.x == 0) to[i] = sum;
 }
 
 template <typename F>
-hipError_t by_lanes(int64_t dim, F f) {
-  if (dim <= 64) return f(Const<8>{});
-  if (dim <= 128) return f(Const<16>{});
-  if (dim <= 256) return f(Const<32>{});
+hipError_t by_lanes(int lanes, F f) {
+  if (lanes <= 8) return f(Const<8>{});
+  if (lanes <= 16) return f(Const<16>{});
+  if (lanes <= 32) return f(Const<32>{});
   return f(Const<64>{});
+}
+
+template <bool BACK>
+hipError_t launch(const fftmv_qk_norm_t &n, const NormPlan &p, float *partials, hipStream_t s) {
+  return by_dtype(n.dtype, [&](auto t) {
+    return by_lanes(p.lanes, [&](auto lanes) {
+      constexpr int L = decltype(lanes)::value;
+      const int blocks = p.blocks[0] + p.blocks[1];
+      if (p.apart)
+        qk_norm_kernel<decltype(t), L, true, BACK><<<blocks, kBlock, 0, s>>>(n, p, partials);
+      else
+        qk_norm_kernel<decltype(t), L, false, BACK><<<blocks, kBlock, 0, s>>>(n, p, partials);
+      return hipGetLastError();
+    });
+  });
 }
 
 }  // namespace
@@ -226,31 +307,21 @@ hipError_t by_lanes(int64_t dim, F f) {
 hipError_t launch_qk_norm_forward(const fftmv_qk_norm_t &n, hipStream_t s) {
   const int64_t rows = n.batch * n.steps;
   if (rows == 0) return hipSuccess;
-  const NormPlan plan = qk_norm_plan(rows, n.frequencies, false);
-  return by_dtype(n.dtype, [&](auto t) {
-    return by_lanes(n.dim, [&](auto lanes) {
-      qk_norm_kernel<decltype(t), decltype(lanes)::value, false><<<plan.blocks, kBlock, 0, s>>>(n, plan, nullptr);
-      return hipGetLastError();
-    });
-  });
+  return launch<false>(n, qk_norm_plan(rows, n.query_heads, n.key_heads, n.dim, n.frequencies, false), nullptr, s);
 }
 
 hipError_t launch_qk_norm_backward(const fftmv_qk_norm_t &n, hipStream_t s) {
   const int64_t rows = n.batch * n.steps;
-  const NormPlan plan = qk_norm_plan(rows, n.frequencies, true);
+  NormPlan p = {};
   float *partials = n.dq_weight || n.dk_weight ? static_cast<float *>(n.workspace) : nullptr;
   if (rows > 0) {
-    const hipError_t e = by_dtype(n.dtype, [&](auto t) {
-      return by_lanes(n.dim, [&](auto lanes) {
-        qk_norm_kernel<decltype(t), decltype(lanes)::value, true><<<plan.blocks, kBlock, 0, s>>>(n, plan, partials);
-        return hipGetLastError();
-      });
-    });
+    p = qk_norm_plan(rows, n.query_heads, n.key_heads, n.dim, n.frequencies, true);
+    const hipError_t e = launch<true>(n, p, partials, s);
     if (e != hipSuccess) return e;
   }
   if (!n.dq_weight && !n.dk_weight) return hipSuccess;
-  const int blocks = rows ? plan.blocks : 0, dim = static_cast<int>(n.dim);
-  qk_norm_sums_kernel<<<2 * dim, kWave, 0, s>>>(partials, blocks, dim, n.dq_weight, n.dk_weight);
+  const int dim = static_cast<int>(n.dim);
+  qk_norm_sums_kernel<<<2 * dim, kWave, 0, s>>>(partials, p.blocks[0], p.blocks[1], dim, n.dq_weight, n.dk_weight);
   return hipGetLastError();
 }
 
