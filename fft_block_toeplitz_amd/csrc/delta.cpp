@@ -27,9 +27,9 @@ int delta_sizes_ok(int64_t batch, int64_t steps, int64_t key_heads, int64_t head
     return FFTMV_ERR_INVALID_ARG;
   if (!sizes_fit(batch, steps, heads) || keys > FFTMV_DELTA_KEYS || values > FFTMV_DELTA_VALUES)
     return FFTMV_ERR_UNSUPPORTED_SIZE;
-  // one wave for each run and head: what a grid takes, and far from where a product of sizes leaves 63 bits
+  // one workgroup for each run and head: what a grid takes, and far from where a product of sizes leaves 63 bits
   if (!grid_fits(batch, kWave) || !grid_fits(batch * heads, kWave) || !grid_fits(delta_runs(batch, steps, false), kWave) ||
-      !grid_fits(delta_runs(batch, steps, false) * heads, kWave))
+      !grid_fits(delta_runs(batch, steps, false) * heads, kBlock))
     return FFTMV_ERR_UNSUPPORTED_SIZE;
   return FFTMV_SUCCESS;
 }
@@ -109,7 +109,7 @@ int fftmv_delta_rule_sizes(int64_t batch, int64_t steps, int64_t key_heads, int6
   if (st != FFTMV_SUCCESS) return st;
   if (packed) {
     if (steps < 0) return FFTMV_ERR_INVALID_ARG;
-    if (!sizes_fit(1, steps, 1) || !grid_fits(delta_runs(batch, steps, true) * heads, kWave))
+    if (!sizes_fit(1, steps, 1) || !grid_fits(delta_runs(batch, steps, true) * heads, kBlock))
       return FFTMV_ERR_UNSUPPORTED_SIZE;
   }
   const int64_t n = delta_runs(batch, steps, packed != 0);

@@ -27,6 +27,8 @@
 // lies in the registers: slots 0..3 from one 16-row tile, 4..7 from the next.
 #pragma once
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "internal.hpp"
 #include "sequence.hpp"
@@ -47,6 +49,7 @@ static_assert(kRun == 64, "one lane for each step of a run");
 constexpr int kFrags = 6;  // operands of 16 rows x 32 slots that a triangle of kRun holds something in
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -190,30 +193,6 @@ __device__ __forceinline__ void load8(const T *p, int c, int n, float (&x)[8]) {
     for (int e = 0; e < 8; ++e) x[e] = c + e < n ? static_cast<float>(p[c + e]) : 0.0f;
   }
 }
-// The same as an operand; bf16 needs no conversion.
-template <typename T>
-__device__ __forceinline__ Cut<kParts<T>> load_cut(const T *p, int c, int n, bool held) {
-  if constexpr (kParts<T> == 1) {
-    Cut<1> r;
-    r.p[0] = u32x4{0, 0, 0, 0};
-    if (held) {
-      if (c + 8 <= n) {
-        const u32x4_any w = *reinterpret_cast<const u32x4_any *>(p + c);
-        r.p[0] = u32x4{w[0], w[1], w[2], w[3]};
-      } else {
-        float x[8];
-        load8(p, c, n, x);
-        r = cut<1>(x);
-      }
-    }
-    return r;
-  } else {
-    float x[8] = {};
-    if (held) load8(p, c, n, x);
-    return cut<kParts<T>>(x);
-  }
-}
-
 // Eight elements c.. of row t of n elements as they lie in memory: loaded now,
 // settled (what is behind the row's end, or in rows that are not there, cleared)
 // when they are needed. A run's rows are loaded a run ahead, so nothing here may
@@ -312,14 +291,6 @@ __device__ __forceinline__ Cut<kParts<T>> cut_raw(const Raw8<T> &r) {
     for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(e[i]);
     return cut<kParts<T>>(x);
   }
-}
-
-// Eight FP32 values as N parts.
-template <int N>
-__device__ __forceinline__ Cut<N> load_wide(const float *p, int c, int n, bool held) {
-  float x[8] = {};
-  if (held) load8(p, c, n, x);
-  return cut<N>(x);
 }
 
 // The steps of sequence b: flat rows (packed) or rows of its own, and the
@@ -505,7 +476,6 @@ inline size_t delta_workspace(int64_t batch, int64_t steps, int64_t heads, int64
 // ------------------------------------------------------ gates of 64 steps
 // log a, bounded below: e^-1e5 is zero, and a sum with it still tells the others
 // apart in 64 bits.
-template <int DUMMY = 0>
 __device__ __forceinline__ float log_decay(int decay, float g) {
   float l = g;
   if (decay == FFTMV_DECAY_SIGMOID) l = fminf(g, 0.0f) - log1pf(expf(-fabsf(g)));
@@ -524,11 +494,11 @@ __device__ __forceinline__ double lane_sums(double v, int lane) {
   return v;
 }
 
-// ------------------------------------------------------ T, P and the factors
-// One wave for each run slot and head. The inverse goes by blocks: a lane
-// solves one column of a diagonal block of 16 by substitution (products of
-// powers would lose what cancels where keys are alike), and the blocks below
-// are joined in FP32 products, T_21 = -T_22 A_21 T_11.
+// ------------------------------------------------------------ the inverse
+// By one wave, in blocks: a lane solves one column of a diagonal block of 16 by
+// substitution (products of powers would lose what cancels where keys are
+// alike), and the blocks below are joined in FP32 products,
+// T_21 = -T_22 A_21 T_11.
 constexpr int kTri = kRun + 4;  // floats between rows of the triangle in LDS
 
 template <bool TRANSPOSED>
@@ -552,6 +522,12 @@ __device__ __forceinline__ void block_store(float *a, int r, int c, f32x4 v, int
   for (int i = 0; i < 4; ++i) a[(r + 4 * (lane / 16) + i) * kTri + c + lane % 16] = v[i];
 }
 
+// What the wave's lanes have written to LDS is there for all of them: its accesses stay in order.
+__device__ __forceinline__ void wave_done() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // Turns the strictly lower A in LDS into (1 + A)^-1 (its upper blocks are not written).
 __device__ __forceinline__ void invert(float *a, int lane) {
   {  // the diagonal blocks: block lane / 16, column lane % 16
@@ -569,19 +545,19 @@ __device__ __forceinline__ void invert(float *a, int lane) {
       }
       x[r] = s;
     }
-    __syncthreads();
+    wave_done();
 #pragma unroll
     for (int r = 0; r < 16; ++r) a[(b + r) * kTri + b + col] = x[r];
-    __syncthreads();
+    wave_done();
   }
 #pragma unroll
   for (int b = 0; b < kRun; b += 32) {
     f32x4 y = {0, 0, 0, 0}, t = {0, 0, 0, 0};
     block_multiply(y, a, b + 16, b, block_load(a, b, b, lane), lane);
     block_multiply(t, a, b + 16, b + 16, -y, lane);
-    __syncthreads();
+    wave_done();
     block_store(a, b + 16, b, t, lane);
-    __syncthreads();
+    wave_done();
   }
   f32x4 y[2][2], t[2][2];
 #pragma unroll
@@ -600,207 +576,12 @@ __device__ __forceinline__ void invert(float *a, int lane) {
 #pragma unroll
       for (int k = 0; k <= r; ++k) block_multiply(t[r][c], a, 32 + 16 * r, 32 + 16 * k, -y[k][c], lane);
     }
-  __syncthreads();
+  wave_done();
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
     for (int c = 0; c < 2; ++c) block_store(a, 32 + 16 * r, 16 * c, t[r][c], lane);
-  __syncthreads();
-}
-
-// Zeros in the rows of `n` elements that belong to no sequence: those of a
-// padded run behind its length; of the packed axis, rows 64 i.. outside all.
-template <typename T>
-__device__ __forceinline__ void clear_rows(const fftmv_delta_rule_t &r, const fftmv_heads_t &f, int64_t slot,
-                                           int64_t b, int first, int64_t head, int n, int lane) {
-  if (!f.data) return;
-  const int steps = static_cast<int>(r.steps);
-  if (r.offsets) {
-    const int lo = clamp_to(r.offsets[0], steps), hi = clamp_to(r.offsets[r.batch], steps);
-    const int64_t at = slot * kRun;
-    for (int64_t t = at; t < at + kRun && t < steps; ++t) {
-      if (t >= lo && t < hi) continue;
-      T *row = head_row<T>(f, 0, t, head);
-      for (int c = lane; c < n; c += kWave) row[c] = static_cast<T>(0.0f);
-    }
-  } else if (r.lengths) {
-    const int len = clamp_to(r.lengths[b], steps);
-    for (int t = max(first, len); t < min(first + kRun, steps); ++t) {
-      T *row = head_row<T>(f, b, t, head);
-      for (int c = lane; c < n; c += kWave) row[c] = static_cast<T>(0.0f);
-    }
-  }
-}
-
-template <typename T, int KEYS, bool BACK>
-__global__ __launch_bounds__(kWave) void delta_factors_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
-  __shared__ __align__(16) float tri[kRun * kTri];
-  __shared__ double total[kRun];
-  __shared__ float rates[kRun];
-  using Tri = Triangles<T, BACK>;
-  const int lane = threadIdx.x, x = lane % 16, g = lane / 16;
-  const int64_t slot = blockIdx.x / r.heads, head = blockIdx.x % r.heads, at = slot * r.heads + head;
-  const int64_t key_head = head / (r.heads / r.key_heads);
-  const Slot where = slot_of(r, slot);
-  if constexpr (BACK) {
-    clear_rows<T>(r, r.dv, slot, where.b, where.first, head, static_cast<int>(r.values), lane);
-    clear_rows<T>(r, r.dgate, slot, where.b, where.first, head, 1, lane);
-    clear_rows<T>(r, r.dbeta, slot, where.b, where.first, head, 1, lane);
-    if (head % (r.heads / r.key_heads) == 0) {
-      clear_rows<T>(r, r.dq, slot, where.b, where.first, key_head, static_cast<int>(r.keys), lane);
-      clear_rows<T>(r, r.dk, slot, where.b, where.first, key_head, static_cast<int>(r.keys), lane);
-    }
-  } else {
-    clear_rows<T>(r, r.y, slot, where.b, where.first, head, static_cast<int>(r.values), lane);
-  }
-  if (where.first < 0) return;
-  const Span span = span_of(r, where.b);
-  const int n = min(kRun, span.len - where.first);  // steps of this run
-  if (n <= 0) return;
-  const int64_t row = span.row + where.first;
-
-  // gates: lane i has step i; steps behind the last leave the state as it is
-  {
-    const bool held = lane < n;
-    const float gate = held ? static_cast<float>(*head_row<T>(r.gate, span.batch, row + lane, head)) : 0.0f;
-    const float beta = held ? static_cast<float>(*head_row<T>(r.beta, span.batch, row + lane, head)) : 0.0f;
-    const double sum = lane_sums(held ? static_cast<double>(log_decay(r.decay, gate)) : 0.0, lane);
-    const double last = __shfl(sum, kRun - 1);
-    Factors &f = w.factors[at];
-    f.into[lane] = expf(static_cast<float>(sum));
-    f.out[lane] = expf(static_cast<float>(last - sum));
-    f.sum[lane] = sum;
-    f.rate[lane] = rates[lane] = held ? rate_of(r.rate, beta) : 0.0f;
-    total[lane] = sum;
-  }
-
-  // rows of keys, as both operands of K K^T and K Q^T
-  constexpr int S = KEYS / 32, NP = kParts<T>;
-  const int keys = static_cast<int>(r.keys);
-  Cut<NP> k[kTiles][S];
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-      k[m][s] = load_cut(head_row<T>(r.k, span.batch, row + min(16 * m + x, n - 1), key_head), 32 * s + 8 * g, keys,
-                         16 * m + x < n);
-  __syncthreads();
-  auto decay = [&](int i, int j) { return expf(static_cast<float>(total[i] - total[j])); };
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int c = 0; c <= m; ++c) {
-      f32x4 p = {0, 0, 0, 0};
-#pragma unroll
-      for (int s = 0; s < S; ++s) multiply<kFull>(p, k[m][s], k[c][s]);
-      const int j = 16 * c + x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * m + 4 * g + i;
-        tri[t * kTri + j] = j < t ? rates[t] * decay(t, j) * p[i] : 0.0f;
-      }
-    }
-  __syncthreads();
-  invert(tri, lane);
-
-  u32x4 *out = w.triangles + at * Tri::kAll * kWave;
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (in_lower(m, s)) {  // T diag(b): row 16 m + x, slots of the columns
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = 16 * m + x, j = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
-          v[e] = j <= i ? tri[i * kTri + j] * rates[j] : 0.0f;
-        }
-        const auto c = cut<Tri::kTParts>(v);
-#pragma unroll
-        for (int q = 0; q < Tri::kTParts; ++q) out[(Tri::kT + lower_frag(m, s) * Tri::kTParts + q) * kWave + lane] = c.p[q];
-      }
-      if constexpr (BACK) {
-        if (in_upper(m, s)) {  // T^T
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int j = 16 * m + x, i = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
-            v[e] = j <= i ? tri[i * kTri + j] : 0.0f;
-          }
-          const auto c = cut<Tri::kTtParts>(v);
-#pragma unroll
-          for (int q = 0; q < Tri::kTtParts; ++q) out[(Tri::kTt + upper_frag(m, s) * Tri::kTtParts + q) * kWave + lane] = c.p[q];
-        }
-      }
-    }
-
-  // P as the operand that it becomes: forward its rows at lane % 16 and columns
-  // as slots, so the tile is computed as K Q^T; backward P^T, as Q K^T
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m) {
-    Cut<NP> q[S];
-#pragma unroll
-    for (int s = 0; s < S; ++s)
-      q[s] = load_cut(head_row<T>(r.q, span.batch, row + min(16 * m + x, n - 1), key_head), 32 * s + 8 * g, keys,
-                      16 * m + x < n);
-    if constexpr (!BACK) {
-      f32x4 p[kTiles];
-#pragma unroll
-      for (int c = 0; c < kTiles; ++c) {
-        p[c] = f32x4{0, 0, 0, 0};
-        if (c > m) continue;
-#pragma unroll
-        for (int s = 0; s < S; ++s) multiply<kOut<T>>(p[c], k[c][s], q[s]);
-        const int i = 16 * m + x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 16 * c + 4 * g + e;
-          p[c][e] = j <= i ? r.scale * decay(i, j) * p[c][e] : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (in_lower(m, s)) {
-          const auto c = cut_tiles<Tri::kPParts>(p[2 * s], p[2 * s + 1]);
-#pragma unroll
-          for (int a = 0; a < Tri::kPParts; ++a) out[(Tri::kP + lower_frag(m, s) * Tri::kPParts + a) * kWave + lane] = c.p[a];
-        }
-    } else {
-      // row tile m of Q gives slots tile m of P^T for all columns c <= m: kept in LDS until both tiles of a slot are there
-#pragma unroll
-      for (int c = 0; c <= m; ++c) {
-        f32x4 p = {0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < S; ++s) multiply<kFull>(p, q[s], k[c][s]);
-        const int j = 16 * c + x;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 16 * m + 4 * g + e;
-          p[e] = j <= i ? r.scale * decay(i, j) * p[e] : 0.0f;
-        }
-        if (c == 0 && m == 0) __syncthreads();
-        block_store(tri, 16 * m, 16 * c, p, lane);
-      }
-    }
-  }
-  if constexpr (BACK) {
-    __syncthreads();
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m)
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (in_upper(m, s)) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int j = 16 * m + x, i = 32 * s + 16 * (e / 4) + 4 * g + e % 4;
-            v[e] = j <= i ? tri[i * kTri + j] : 0.0f;
-          }
-          const auto c = cut<Tri::kPParts>(v);
-#pragma unroll
-          for (int q = 0; q < Tri::kPParts; ++q) out[(Tri::kP + upper_frag(m, s) * Tri::kPParts + q) * kWave + lane] = c.p[q];
-        }
-  }
+  wave_done();
 }
 
 // ------------------------------------------------------ tiles of keys in LDS
@@ -809,19 +590,6 @@ __global__ __launch_bounds__(kWave) void delta_factors_kernel(fftmv_delta_rule_t
 template <int KEYS>
 constexpr int kTileRow = KEYS + 8;
 
-template <typename T, int KEYS, int THREADS>
-__device__ __forceinline__ void fill_tile(uint16_t *tile, const fftmv_heads_t &f, int64_t b, int64_t row, int n,
-                                          int64_t head, int width, int from = 0) {
-  constexpr int G = KEYS / 8, NP = kParts<T>;
-#pragma unroll
-  for (int u = threadIdx.x; u < kRun * G; u += THREADS) {
-    const int t = u / G, c = u % G * 8;
-    const Cut<NP> v = load_cut(head_row<T>(f, b, row + min(t, n - 1), head), from + c, width, t < n);
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-      *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * kTileRow<KEYS> + c) = v.p[p];
-  }
-}
 // Operand with index row 16 m + lane % 16 and slots of elements 32 s + 8 g ...
 template <int KEYS, int NP>
 __device__ __forceinline__ Cut<NP> tile_rows(const uint16_t *tile, int m, int s, int lane) {
@@ -982,6 +750,237 @@ __device__ __forceinline__ void put_rows(Raw8<T> (&k)[KEYS / 32], int thread, ui
   }
 }
 
+// ------------------------------------------------------ T, P and the factors
+// Zeros in the rows of `n` elements that belong to no sequence: those of a
+// padded run behind its length; of the packed axis, rows 64 i.. outside all.
+template <typename T>
+__device__ __forceinline__ void clear_rows(const fftmv_delta_rule_t &r, const fftmv_heads_t &f, int64_t slot,
+                                           int64_t b, int first, int64_t head, int n) {
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+  constexpr int WAVES = kFrontWaves;
+  if (!f.data) return;
+  const int steps = static_cast<int>(r.steps);
+  if (r.offsets) {
+    const int lo = clamp_to(r.offsets[0], steps), hi = clamp_to(r.offsets[r.batch], steps);
+    const int64_t at = slot * kRun;
+    for (int64_t t = at + wave; t < at + kRun && t < steps; t += WAVES) {
+      if (t >= lo && t < hi) continue;
+      T *row = head_row<T>(f, 0, t, head);
+      for (int c = lane; c < n; c += kWave) row[c] = static_cast<T>(0.0f);
+    }
+  } else if (r.lengths) {
+    const int len = clamp_to(r.lengths[b], steps);
+    for (int t = max(first, len) + wave; t < min(first + kRun, steps); t += WAVES) {
+      T *row = head_row<T>(f, b, t, head);
+      for (int c = lane; c < n; c += kWave) row[c] = static_cast<T>(0.0f);
+    }
+  }
+}
+
+// The kernel of a run's factors, for each run slot and head. Only the inverse is
+// in line; products, decays and outputs go by fragments, the pieces that the
+// chains load, two of P's tiles and the same two of the triangle each, so that a
+// decay is computed once for both: four waves have three or two tiles each. Rows
+// lie in LDS as they are in memory: products of 16-bit elements are exact in
+// FP32, FP32 ones are cut where they are read.
+template <typename T, int KEYS>
+struct FactorLds {
+  static constexpr int ROW = KEYS + 16 / sizeof(T);
+  alignas(16) T k[kRun * ROW];
+  union {
+    alignas(16) T q[kRun * ROW];
+    alignas(16) float tri[kRun * kTri];  // once the products are there
+  };
+  double total[kRun];
+  float rates[kRun];
+};
+
+// Fragment i of a wave: three of six tiles' worth to the first two waves, two to the others.
+template <bool UPPER>
+__device__ __forceinline__ int fragment_of(int wave, int i) {
+  return UPPER ? (wave == 0 ? 1 + i : wave == 1 ? 4 + i : wave == 2 ? 0 : 3) : (wave < 2 ? 2 * wave + i : wave + 2);
+}
+__device__ __forceinline__ int fragments_of(int wave) { return wave < 2 ? 2 : 1; }
+// The rows' tile and the slots' half of a fragment.
+template <bool UPPER>
+__device__ __forceinline__ int fragment_tile(int f) {
+  return UPPER ? (f < 4 ? f / 2 : f - 2) : (f < 2 ? f : f / 2 + 1);
+}
+template <bool UPPER>
+__device__ __forceinline__ int fragment_half(int f) {
+  return UPPER ? (f < 4 ? f % 2 : 1) : (f < 2 ? 0 : f % 2);
+}
+
+// c += (rows of tile a of one) (rows of tile b of the other)^T, 32 elements.
+template <typename T, int ROW>
+struct RowOperand {
+  using Raw = std::conditional_t<sizeof(T) == 4, Cut<kFull>, Cut<1>>;
+  static __device__ __forceinline__ Raw load(const T *rows, int tile, int s, int lane) {
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(rows + (16 * tile + lane % 16) * ROW + 32 * s + 8 * (lane / 16));
+    if constexpr (sizeof(T) == 4)
+      return cut_raw<T>(Raw8<T>{{p[0], p[1]}});
+    else
+      return Raw{{p[0]}};
+  }
+  static __device__ __forceinline__ void multiply_into(f32x4 &c, const Raw &a, const Raw &b) {
+    if constexpr (std::is_same_v<T, f16>)
+      c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a.p[0]), __builtin_bit_cast(f16x8, b.p[0]), c, 0, 0, 0);
+    else
+      multiply<kFull>(c, a, b);
+  }
+};
+
+template <typename T, int KEYS, bool WHOLE, bool BACK>
+__global__ __launch_bounds__(kFrontThreads) void delta_factors_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
+  using Lds = FactorLds<T, KEYS>;
+  using Tri = Triangles<T, BACK>;
+  __shared__ Lds lds;
+  const int thread = threadIdx.x, lane = thread % kWave, wave = thread / kWave, x = lane % 16, g = lane / 16;
+  const int64_t slot = blockIdx.x / r.heads, head = blockIdx.x % r.heads, at = slot * r.heads + head;
+  const int64_t key_head = head / (r.heads / r.key_heads);
+  const Slot where = slot_of(r, slot);
+  if constexpr (BACK) {
+    clear_rows<T>(r, r.dv, slot, where.b, where.first, head, static_cast<int>(r.values));
+    clear_rows<T>(r, r.dgate, slot, where.b, where.first, head, 1);
+    clear_rows<T>(r, r.dbeta, slot, where.b, where.first, head, 1);
+    if (head % (r.heads / r.key_heads) == 0) {
+      clear_rows<T>(r, r.dq, slot, where.b, where.first, key_head, static_cast<int>(r.keys));
+      clear_rows<T>(r, r.dk, slot, where.b, where.first, key_head, static_cast<int>(r.keys));
+    }
+  } else {
+    clear_rows<T>(r, r.y, slot, where.b, where.first, head, static_cast<int>(r.values));
+  }
+  if (where.first < 0) return;
+  const Span span = span_of(r, where.b);
+  const int n = min(kRun, span.len - where.first);  // steps of this run
+  if (n <= 0) return;
+  const int64_t row = span.row + where.first;
+  const int keys = static_cast<int>(r.keys);
+
+  float gate = 0.0f, beta = 0.0f;
+  if (wave == 0 && lane < n) {
+    gate = static_cast<float>(*head_row<T>(r.gate, span.batch, row + lane, head));
+    beta = static_cast<float>(*head_row<T>(r.beta, span.batch, row + lane, head));
+  }
+  Raw8<T> rows[2][KEYS / 32];
+  fetch_rows<T, KEYS, WHOLE>(rows[0], thread, r.k, keys, span.batch, row, n, key_head);
+  fetch_rows<T, KEYS, WHOLE>(rows[1], thread, r.q, keys, span.batch, row, n, key_head);
+  if (wave == 0) {  // gates: lane i has step i; steps behind the last leave the state as it is
+    const bool held = lane < n;
+    const double sum = lane_sums(held ? static_cast<double>(log_decay(r.decay, gate)) : 0.0, lane);
+    const double last = __shfl(sum, kRun - 1);
+    const float rate = held ? rate_of(r.rate, beta) : 0.0f;
+    Factors &f = w.factors[at];
+    f.into[lane] = expf(static_cast<float>(sum));
+    f.out[lane] = expf(static_cast<float>(last - sum));
+    f.sum[lane] = sum;
+    f.rate[lane] = lds.rates[lane] = rate;
+    lds.total[lane] = sum;
+  }
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int i = 0; i < KEYS / 32; ++i) {
+      const int u = thread + i * kFrontThreads, t = u / (KEYS / 8), c = u % (KEYS / 8) * 8;
+      if (!WHOLE || keys < KEYS) settle<WHOLE>(rows[which][i], c, keys, t < n);
+      u32x4 *to = reinterpret_cast<u32x4 *>((which ? lds.q : lds.k) + t * Lds::ROW + c);
+#pragma unroll
+      for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h) to[h] = rows[which][i].w[h];
+    }
+  __syncthreads();
+
+  // products and decays: rows of tile `own` at lane % 16, two tiles of slots. Forward
+  // rows are those of T and P, backward those of their transposes
+  using Op = RowOperand<T, Lds::ROW>;
+  u32x4 *out = w.triangles + at * Tri::kAll * kWave;
+  const int count = fragments_of(wave);
+  f32x4 below[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i >= count) break;
+    const int f = fragment_of<BACK>(wave, i), own = fragment_tile<BACK>(f), half = fragment_half<BACK>(f);
+    f32x4 p[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int other = 2 * half + h;
+      p[h] = below[i][h] = f32x4{0, 0, 0, 0};
+      if (BACK ? other < own : other > own) continue;
+#pragma unroll
+      for (int s = 0; s < KEYS / 32; ++s) {
+        const auto a = Op::load(lds.k, other, s, lane), b = Op::load(lds.k, own, s, lane);
+        Op::multiply_into(below[i][h], a, b);
+        if constexpr (BACK)
+          Op::multiply_into(p[h], Op::load(lds.q, other, s, lane), b);
+        else
+          Op::multiply_into(p[h], a, Op::load(lds.q, own, s, lane));
+      }
+      const int one = 16 * own + x, first = 16 * other + 4 * g;
+      const double mine = lds.total[one];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int step = BACK ? first + e : one, past = BACK ? one : first + e;
+        const double between = BACK ? lds.total[step] - mine : mine - lds.total[past];
+        const float decay = past <= step ? exp_of<T>(static_cast<float>(between)) : 0.0f;
+        p[h][e] = past <= step ? r.scale * decay * p[h][e] : 0.0f;
+        below[i][h][e] = past < step ? lds.rates[step] * decay * below[i][h][e] : 0.0f;
+      }
+    }
+    const auto c = cut_tiles<Tri::kPParts>(p[0], p[1]);
+#pragma unroll
+    for (int a = 0; a < Tri::kPParts; ++a) out[(Tri::kP + f * Tri::kPParts + a) * kWave + lane] = c.p[a];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i >= count) break;
+    const int f = fragment_of<BACK>(wave, i), own = fragment_tile<BACK>(f), half = fragment_half<BACK>(f);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int other = 2 * half + h;
+      if (BACK ? other < own : other > own) continue;
+      if constexpr (BACK)
+        block_store(lds.tri, 16 * other, 16 * own, below[i][h], lane);
+      else
+        *reinterpret_cast<f32x4 *>(lds.tri + (16 * own + x) * kTri + 16 * other + 4 * g) = below[i][h];
+    }
+  }
+  __syncthreads();
+  if (wave == 0) invert(lds.tri, lane);
+  __syncthreads();
+
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // T diag(b)
+    if (i >= count) break;
+    const int f = fragment_of<false>(wave, i), t = 16 * fragment_tile<false>(f) + x, first = 32 * fragment_half<false>(f) + 4 * g;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = first + 16 * (e / 4) + e % 4;
+      v[e] = j <= t ? lds.tri[t * kTri + j] * lds.rates[j] : 0.0f;
+    }
+    const auto c = cut<Tri::kTParts>(v);
+#pragma unroll
+    for (int q = 0; q < Tri::kTParts; ++q) out[(Tri::kT + f * Tri::kTParts + q) * kWave + lane] = c.p[q];
+  }
+  if constexpr (BACK) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // T^T, more of it for the waves that had less of T
+      const int f = wave < 2 ? wave : 2 * wave - 2 + i;
+      if (i >= (wave < 2 ? 1 : 2)) break;
+      const int j = 16 * fragment_tile<true>(f) + x, first = 32 * fragment_half<true>(f) + 4 * g;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int t = first + 16 * (e / 4) + e % 4;
+        v[e] = j <= t ? lds.tri[t * kTri + j] : 0.0f;
+      }
+      const auto c = cut<Tri::kTtParts>(v);
+#pragma unroll
+      for (int q = 0; q < Tri::kTtParts; ++q) out[(Tri::kTt + f * Tri::kTtParts + q) * kWave + lane] = c.p[q];
+    }
+  }
+}
+
 // The same for all that a run needs: keys, values, a triangle's fragments, factors.
 template <typename T, int KEYS, int FRAGS, bool WHOLE>
 struct Fetched {
@@ -1075,9 +1074,11 @@ inline bool delta_whole(const fftmv_heads_t &f, int64_t width, int dtype) {
   return width % 8 == 0 && f.step >= width && f.step <= (1 << 22) && f.batch * es % 4 == 0 && f.step * es % 4 == 0 &&
          f.head * es % 4 == 0 && reinterpret_cast<uintptr_t>(f.data) % 4 == 0;
 }
+inline bool delta_whole_rows(const fftmv_delta_rule_t &r) {
+  return delta_whole(r.q, r.keys, r.dtype) && delta_whole(r.k, r.keys, r.dtype);
+}
 inline bool delta_whole(const fftmv_delta_rule_t &r, const fftmv_heads_t &valued, const fftmv_heads_t &other) {
-  return delta_whole(r.q, r.keys, r.dtype) && delta_whole(r.k, r.keys, r.dtype) && delta_whole(valued, r.values, r.dtype) &&
-         delta_whole(other, r.values, r.dtype);
+  return delta_whole_rows(r) && delta_whole(valued, r.values, r.dtype) && delta_whole(other, r.values, r.dtype);
 }
 // A part of a sequence, in its steps.
 struct Part {

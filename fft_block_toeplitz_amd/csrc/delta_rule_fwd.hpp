@@ -242,13 +242,17 @@ hipError_t launch_delta_forward(const fftmv_delta_rule_t &r, hipStream_t s) {
   DeltaWorkspace w;
   delta_workspace(r.batch, r.steps, r.heads, r.keys, r.values, r.dtype, r.offsets != nullptr, false, r.workspace, &w);
   const int64_t blocks = (r.values + kValues - 1) / kValues, units = (r.keys + kValues - 1) / kValues;
-  if (!grid_fits(runs * r.heads, kWave) || !grid_fits(sequences * ((r.values + 15) / 16), 512) || !grid_fits(sequences * w.cuts.parts * (blocks + units), kChainThreads))
+  if (!grid_fits(runs * r.heads, kFrontThreads) || !grid_fits(sequences * ((r.values + 15) / 16), 512) || !grid_fits(sequences * w.cuts.parts * (blocks + units), kChainThreads))
     return hipErrorInvalidConfiguration;
   return by_keys(r.keys, [&](auto k) {
     constexpr int KEYS = decltype(k)::value;
     if (runs > 0) {
-      delta_factors_kernel<T, KEYS, false><<<static_cast<unsigned>(runs * r.heads), kWave, 0, s>>>(r, w);
-      if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+      const hipError_t e = by_two(delta_whole_rows(r), [&](auto whole) {
+        delta_factors_kernel<T, KEYS, decltype(whole)::value != 0, false>
+            <<<static_cast<unsigned>(runs * r.heads), kFrontThreads, 0, s>>>(r, w);
+        return hipGetLastError();
+      });
+      if (e != hipSuccess) return e;
     }
     return by_two(delta_whole(r, r.v, r.y), [&](auto whole) {
       constexpr bool WHOLE = decltype(whole)::value != 0;
