@@ -3,14 +3,15 @@
 // Within a run that the state S enters, with G_i the sum of log a up to step i,
 // E_ij = exp(G_i - G_j) and
 //   B_ij = E_ij k_i.k_j  (j < i),      P_ij = scale E_ij q_i.k_j  (j <= i),
-//   T    = (1 + diag(b) B)^-1          (unit lower triangular),
-// the corrections U (row i is what step i writes under its key) are
-//   U  = T diag(b) (V - diag(e^G) K S)
-//   Y  = scale diag(e^G) Q S + P U
-//   S' = e^{G_last} S + (diag(e^{G_last - G}) K)^T U
-// so that a run is products of matrices, and only K S, T (..) and K^T U wait for
-// the run before. T, P and the factors need no state: a kernel of their own
-// computes them for all runs at once.
+//   T    = (1 + B diag(b))^-1          (unit lower triangular),
+// the errors X (row i is what step i finds wrong under its key: it writes U =
+// diag(b) X there) are
+//   X  = T (V - diag(e^G) K S)
+//   Y  = scale diag(e^G) Q S + P diag(b) X
+//   S' = e^{G_last} S + K^T diag(b e^{G_last - G}) X
+// so that a run is products of matrices, and only K S, T (..) and K^T (..) X wait
+// for the run before. T, P diag(b) and the factors need no state: a kernel of
+// their own computes them for all runs at once.
 //
 // Products go to the bf16 matrix instructions with FP32 sums. An FP32 operand
 // is cut into bf16 parts, the leading 8 bits, the next 8, the last 8: three parts
@@ -340,17 +341,17 @@ __device__ __forceinline__ Slot slot_of(const fftmv_delta_rule_t &r, int64_t i) 
 // What the first kernel leaves for each run slot and head.
 struct Factors {
   double sum[kRun];  // G_i
-  float into[kRun], out[kRun], rate[kRun];  // e^{G_i}, e^{G_last - G_i}, b_i; into[kRun - 1] is the whole run's decay
+  // e^{G_i}, e^{G_last - G_i} (forward times b_i), b_i; into[kRun - 1] is the whole run's decay
+  float into[kRun], out[kRun], rate[kRun];
 };
-// Fragments (one part of an operand, 64 lanes x 16 bytes) of: T diag(b) and P
-// forward; T diag(b), T^T and P^T backward.
+// Fragments (one part of an operand, 64 lanes x 16 bytes) of T and P diag(b)
+// forward, of P^T and (1 + diag(b) B)^-T backward.
 template <typename T, bool BACK>
 struct Triangles {
-  static constexpr int kT = 0, kTParts = BACK ? kOut<T> : kFull;
+  static constexpr int kT = 0, kTParts = BACK ? 0 : kFull;
   static constexpr int kP = kT + kFrags * kTParts, kPParts = BACK ? kFull : kOut<T>;
   static constexpr int kTt = kP + kFrags * kPParts, kTtParts = BACK ? kFull : 0;
   static constexpr int kAll = kTt + kFrags * kTtParts;
-  static constexpr size_t kBytes = size_t{kAll} * kWave * sizeof(u32x4);
 };
 // Fragment of rows tile m and slots 32 s.. of a lower or upper triangle.
 __host__ __device__ constexpr int lower_frag(int m, int s) { return m < 2 ? m : 2 * m - 2 + s; }
@@ -441,7 +442,7 @@ inline DeltaCuts delta_cuts(int64_t batch, int64_t steps, int64_t heads, int64_t
 struct DeltaWorkspace {
   Factors *factors;
   u32x4 *triangles;
-  float *grads;  // backward: the gradients of the states behind each run, [runs][heads][keys][values]
+  float *grads;  // backward: the gradients of the states behind each run and Z, [runs][heads][keys + kRun][values]
   // of each part of a sequence: (N, M) [keys][values + keys], and the state in front of it (backward: behind it)
   float *maps, *starts;
   DeltaCuts cuts;
@@ -449,7 +450,7 @@ struct DeltaWorkspace {
 inline size_t delta_triangle_bytes(int dtype, bool back) {
   const size_t per_part = size_t{kFrags} * kWave * sizeof(u32x4);
   const size_t out = dtype == FFTMV_F32 ? 3 : 2;
-  return per_part * (back ? out + 2 * kFull : kFull + out);
+  return per_part * (kFull + (back ? kFull : out));
 }
 inline size_t delta_workspace(int64_t batch, int64_t steps, int64_t heads, int64_t keys, int64_t values, int dtype,
                               bool packed, bool back, void *at = nullptr, DeltaWorkspace *w = nullptr) {
@@ -457,7 +458,7 @@ inline size_t delta_workspace(int64_t batch, int64_t steps, int64_t heads, int64
   const DeltaCuts cuts = delta_cuts(batch, steps, heads, keys, values, packed);
   const size_t parts = cuts.parts > 1 ? static_cast<size_t>(batch) * heads * cuts.parts : 0;
   const size_t factors = n * sizeof(Factors), triangles = n * delta_triangle_bytes(dtype, back);
-  const size_t grads = (back ? n * keys * values * sizeof(float) + 15 : 0) & ~size_t{15};
+  const size_t grads = (back ? n * (keys + kRun) * values * sizeof(float) + 15 : 0) & ~size_t{15};
   const size_t maps = (parts * keys * (keys + values) * sizeof(float) + 15) & ~size_t{15};
   const size_t starts = parts * keys * values * sizeof(float);
   static_assert(sizeof(Factors) % 16 == 0, "fragments are 16-byte aligned");
@@ -649,32 +650,19 @@ __device__ __forceinline__ void multiply_columns(f32x4 (&state)[KEYS / 16], cons
     multiply_rows<kFull>(state + t, k[1], hi);
   }
 }
-// Operand with index columns col.. (lane % 16) and slots of rows row + 8 g + 0..7 (GAP 4), or as results hold them (GAP 16).
-template <int ROW, int NP, int GAP>
+// Operand with index columns col.. (lane % 16) and slots of rows row + 8 g + 0..7.
+template <int ROW, int NP>
 __device__ __forceinline__ Cut<NP> plain_columns(const uint16_t *tile, int row, int col, int lane) {
   Cut<NP> c;
   const int l = lane % 16;
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    const uint16_t *q = tile + (p * kRun + row + (GAP == 4 ? 8 : 4) * (lane / 16) + l / 4) * ROW + col + 4 * (l % 4);
-    c.p[p] = join8(transposed4(q), transposed4(q + GAP * ROW));
+    const uint16_t *q = tile + (p * kRun + row + 8 * (lane / 16) + l / 4) * ROW + col + 4 * (l % 4);
+    c.p[p] = join8(transposed4(q), transposed4(q + 4 * ROW));
   }
   return c;
 }
 
-// Rows 16 m + 4 g + 0..3 of column col + lane % 16, as results hold them.
-template <int ROW, int NP>
-__device__ __forceinline__ f32x4 tile_values(const uint16_t *tile, int m, int col, int lane) {
-  f32x4 v = {0, 0, 0, 0};
-  const int l = lane % 16;
-#pragma unroll
-  for (int p = NP - 1; p >= 0; --p) {
-    const s16x4 q = transposed4(tile + (p * kRun + 16 * m + 4 * (lane / 16) + l / 4) * ROW + col + 4 * (l % 4));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += __uint_as_float(static_cast<uint32_t>(static_cast<uint16_t>(q[i])) << 16);
-  }
-  return v;
-}
 // Keeps the scheduler from moving work across: it would start on later loads and products and spill.
 __device__ __forceinline__ void part_done() { __builtin_amdgcn_sched_barrier(0); }
 
@@ -872,7 +860,7 @@ __global__ __launch_bounds__(kFrontThreads) void delta_factors_kernel(fftmv_delt
     const float rate = held ? rate_of(r.rate, beta) : 0.0f;
     Factors &f = w.factors[at];
     f.into[lane] = expf(static_cast<float>(sum));
-    f.out[lane] = expf(static_cast<float>(last - sum));
+    f.out[lane] = expf(static_cast<float>(last - sum)) * (BACK ? 1.0f : rate);
     f.sum[lane] = sum;
     f.rate[lane] = lds.rates[lane] = rate;
     lds.total[lane] = sum;
@@ -921,8 +909,9 @@ __global__ __launch_bounds__(kFrontThreads) void delta_factors_kernel(fftmv_delt
         const int step = BACK ? first + e : one, past = BACK ? one : first + e;
         const double between = BACK ? lds.total[step] - mine : mine - lds.total[past];
         const float decay = past <= step ? exp_of<T>(static_cast<float>(between)) : 0.0f;
-        p[h][e] = past <= step ? r.scale * decay * p[h][e] : 0.0f;
-        below[i][h][e] = past < step ? lds.rates[step] * decay * below[i][h][e] : 0.0f;
+        // A = B diag(b) forward, diag(b) B backward
+        p[h][e] = past <= step ? r.scale * (BACK ? 1.0f : lds.rates[past]) * decay * p[h][e] : 0.0f;
+        below[i][h][e] = past < step ? lds.rates[BACK ? step : past] * decay * below[i][h][e] : 0.0f;
       }
     }
     const auto c = cut_tiles<Tri::kPParts>(p[0], p[1]);
@@ -949,35 +938,18 @@ __global__ __launch_bounds__(kFrontThreads) void delta_factors_kernel(fftmv_delt
   __syncthreads();
 
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {  // T diag(b)
+  for (int i = 0; i < 2; ++i) {
     if (i >= count) break;
-    const int f = fragment_of<false>(wave, i), t = 16 * fragment_tile<false>(f) + x, first = 32 * fragment_half<false>(f) + 4 * g;
+    const int f = fragment_of<BACK>(wave, i), own = 16 * fragment_tile<BACK>(f) + x, first = 32 * fragment_half<BACK>(f) + 4 * g;
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int j = first + 16 * (e / 4) + e % 4;
-      v[e] = j <= t ? lds.tri[t * kTri + j] * lds.rates[j] : 0.0f;
+      const int other = first + 16 * (e / 4) + e % 4, t = BACK ? other : own, j = BACK ? own : other;
+      v[e] = j <= t ? lds.tri[t * kTri + j] : 0.0f;
     }
-    const auto c = cut<Tri::kTParts>(v);
+    const auto c = cut<kFull>(v);
 #pragma unroll
-    for (int q = 0; q < Tri::kTParts; ++q) out[(Tri::kT + f * Tri::kTParts + q) * kWave + lane] = c.p[q];
-  }
-  if constexpr (BACK) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {  // T^T, more of it for the waves that had less of T
-      const int f = wave < 2 ? wave : 2 * wave - 2 + i;
-      if (i >= (wave < 2 ? 1 : 2)) break;
-      const int j = 16 * fragment_tile<true>(f) + x, first = 32 * fragment_half<true>(f) + 4 * g;
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int t = first + 16 * (e / 4) + e % 4;
-        v[e] = j <= t ? lds.tri[t * kTri + j] : 0.0f;
-      }
-      const auto c = cut<Tri::kTtParts>(v);
-#pragma unroll
-      for (int q = 0; q < Tri::kTtParts; ++q) out[(Tri::kTt + f * Tri::kTtParts + q) * kWave + lane] = c.p[q];
-    }
+    for (int q = 0; q < kFull; ++q) out[((BACK ? Tri::kTt : Tri::kT) + f * kFull + q) * kWave + lane] = c.p[q];
   }
 }
 

@@ -1,6 +1,6 @@
 // Backward pass of the gated delta rule. With D the gradient of the state behind
 // a run and dY that of its outputs,
-//   Z   = T^T (P^T dY + diag(e^{G_last - G}) K D)      the gradient of U
+//   Z   = (1 + diag(b) B)^-T (P^T dY + diag(e^{G_last - G}) K D)   the gradient of U = diag(b) X
 //   D'  = e^{G_last} D + (scale diag(e^G) Q)^T dY - (diag(b e^G) K)^T Z
 // goes from run to run, from the last to the first, as the state does forward;
 // everything else belongs to one run:
@@ -8,12 +8,15 @@
 //   dP  = dY U^T,  N = Z U^T, both lower triangles;  F = scale E o dP,  H = -diag(b) E o N
 //   dQ  = scale diag(e^G) dY S^T + F K
 //   dK  = F^T Q + (H + H^T) K + diag(e^{G_last - G}) U D^T - diag(b e^G) Z S^T
-//   db_j = z_j . x_j - sum_i E_ji k_j.k_i N_ji   with X = V - diag(e^G) K S
+//   db_j = z_j . x_j
 //   dG_i collects, with its sign, every product that e^{G_i} is a factor of; the
 //   gradient of log a_t is the sum of dG_i over i >= t.
 // So three kernels: the factors, the chain of D, and the gradients of all runs
-// at once, which compute U and Z again from the states that the passes kept:
-// that costs a tenth of a run's products, and reading them back half of its bytes.
+// at once, from the states and X that the forward pass kept and the gradients and
+// Z that the chain left. (Computing X and Z again from the states saves half of the
+// bytes, 64 KB of a run of 128 values, and takes three triangles and K S, K D: 8 x 2048
+// steps of 16 heads of 128 x 128 bf16 in 576 us instead of 437, with the chains 43
+// faster. Without them a run needs half of a CU's LDS, and two go side by side: 323.)
 #pragma once
 
 #include "delta_rule.hpp"
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
     for (int first = last, buffer = 0; first >= part.begin; first -= kRun, buffer = (buffer + 1) % BUFFERS) {
       again();
       const uint16_t *k = lds.k[buffer];
-      if constexpr (!MAPS) keep(w.grads + at(first) * states, values);
+      if constexpr (!MAPS) keep(w.grads + at(first) * (states + kRun * r.values), values);
       const float whole = lds.into[kRun - 1];
       f32x4 z[kTiles];
 #pragma unroll
@@ -110,6 +113,14 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) z[m] = f32x4{0, 0, 0, 0};
         multiply_triangle<kFull, kFull, kFull, true>(z, lds.frags, a, c, lane);
+      }
+      if constexpr (!MAPS) {
+        float *to = w.grads + at(first) * (states + kRun * r.values) + states;
+#pragma unroll
+        for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (inside) to[static_cast<int64_t>(16 * m + 4 * g + i) * values + col] = z[m][i];
       }
 #pragma unroll
       for (int m = 0; m < kTiles; ++m)
@@ -269,66 +280,53 @@ __device__ __forceinline__ float across_groups(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// QUERIES, FRAGS: tiles of their own for the queries and the triangles, where they fit.
-template <typename T, int KEYS, bool QUERIES, bool FRAGS>
+// QUERIES: a tile of their own for the queries, where it fits.
+template <typename T, int KEYS, bool QUERIES>
 struct GradsLds {
   static constexpr int NP = kParts<T>, NO = kOut<T>, VR = kTileRow<kValues>;
   alignas(16) uint16_t k[NP * kRun * kTileRow<KEYS>];  // keys, and without a tile of their own at the end queries
   alignas(16) uint16_t q[QUERIES ? NP * kRun * kTileRow<KEYS> : 8];
-  alignas(16) u32x4 frags[FRAGS ? 3 * kFrags * NO * kWave : 1];
   union {
     struct {
-      alignas(16) uint16_t u[NO * kRun * VR], z[NO * kRun * VR], dy[NP * kRun * VR];  // u holds V's rows before U's
+      alignas(16) uint16_t u[NO * kRun * VR], z[NO * kRun * VR], dy[NP * kRun * VR];
     } one;
     struct {
       alignas(16) uint16_t f[NO * kRun * VR], h[NO * kRun * VR];
     } two;
   };
   alignas(16) Factors f;
-  float sums[kGradWaves][kRun];    // what of dG goes through the states by the keys, of each wave's values
-  float rates[kFrontWaves][kRun];  // z . x, of each wave's values
-  double turned[kRun];             // q . dq over the heads that dq holds
-  float turns[KEYS / 16][kRun];    // q . dq, of each 16 keys
-  float lasts[kGradWaves];         // what the last step's G has beside
-  float gram_rows[2 * kGrams][16], gram_cols[2 * kGrams][16], gram_rates[kGrams][16];
+  float sums[KEYS / 16][kRun];  // what of dG goes through the states, of each 16 keys
+  float rates[kRun];            // z . x
+  double turned[kRun];          // q . dq over the heads that dq holds
+  float turns[KEYS / 16][kRun]; // q . dq, of each 16 keys
+  float lasts[kGradWaves];      // what the last step's G has beside
+  float gram_rows[2 * kGrams][16], gram_cols[2 * kGrams][16];
 };
 
-// Four transposed result tiles (step 16 m + x, four columns) as parts, for all waves to read by rows.
-template <int N, int ROW>
-__device__ __forceinline__ void put_transposed(uint16_t *tile, const f32x4 (&v)[kTiles], int col, int lane) {
-  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-  for (int m = 0; m < kTiles; ++m) {
-    f32x4 rest = v[m];
-#pragma unroll
-    for (int p = 0; p < N; ++p) {
-      bf16x4 part;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        part[i] = static_cast<__bf16>(rest[i]);
-        rest[i] -= static_cast<float>(part[i]);
-      }
-      *reinterpret_cast<bf16x4 *>(tile + (p * kRun + 16 * m + lane % 16) * ROW + col + 4 * (lane / 16)) = part;
-    }
-  }
+// Two workgroups on a CU where LDS and registers hold them: one loads while the
+// other computes. (8 x 2048 steps, 16 heads of 128 x 128 bf16: one 437 us, two
+// 323; 32 heads of 64 x 64 with 8 of queries and keys: 439 and 300. Shared heads'
+// gradients take the registers of 128 keys.)
+template <typename T, int KEYS, bool SHARED>
+constexpr bool grads_twice() {
+  return (!SHARED || KEYS <= 64) && 2 * sizeof(GradsLds<T, KEYS, false>) <= kLdsBytes;
 }
-__device__ __forceinline__ f32x4 factor4(const float *f, int m, int lane) {
-  return *reinterpret_cast<const f32x4 *>(f + 16 * m + 4 * (lane / 16));
+template <typename T, int KEYS, bool SHARED>
+constexpr bool grads_queries() {
+  return (grads_twice<T, KEYS, SHARED>() ? 2 : 1) * sizeof(GradsLds<T, KEYS, true>) <= kLdsBytes;
 }
 
 // SHARED: several heads have the same queries and keys.
 template <typename T, int KEYS, bool WHOLE, bool SHARED>
-__global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
+__global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 : 2)) void delta_grads_kernel(
     fftmv_delta_rule_t r, DeltaWorkspace w) {
-  using Tri = Triangles<T, true>;
-  constexpr bool FRAGS = sizeof(GradsLds<T, KEYS, false, true>) <= kLdsBytes;
-  constexpr bool QUERIES = sizeof(GradsLds<T, KEYS, true, FRAGS>) <= kLdsBytes;
-  using Lds = GradsLds<T, KEYS, QUERIES, FRAGS>;
+  constexpr bool QUERIES = grads_queries<T, KEYS, SHARED>();
+  using Lds = GradsLds<T, KEYS, QUERIES>;
   constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32, VR = Lds::VR, KR = kTileRow<KEYS>;
+  constexpr bool LATE = grads_twice<T, KEYS, SHARED>() && (KEYS == 128 || SHARED);  // what the other workgroup hides need not be held
   constexpr int KT = KEYS / 16, MT = kTiles * KT / kGradWaves;  // tiles of keys, and of steps for one of them a wave
   __shared__ Lds lds;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), column = wave % kFrontWaves;
-  const bool first_side = wave < kFrontWaves;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int tile_k = wave % KT, tile_m = wave / KT * MT;  // this wave's keys and steps
   int thread = threadIdx.x, lane = thread % kWave, x = lane % 16, g = lane / 16;
   auto again = [&]() __attribute__((always_inline)) {
@@ -399,10 +397,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
   do {
     again();
     const int64_t at = slot * r.heads + head;
-    const u32x4 *tri = w.triangles + at * Tri::kAll * kWave;
-    // states and their gradients: rows behind the last read as zeros
-    const auto state = __builtin_amdgcn_make_buffer_rsrc(r.carries + at * states, 0, static_cast<int>(states * 4), kBufferFlags);
-    const auto grad = __builtin_amdgcn_make_buffer_rsrc(w.grads + at * states, 0, static_cast<int>(states * 4), kBufferFlags);
+    // states with X behind them, their gradients with Z: what is behind the last reads as zeros
+    const int64_t each = states + kRun * r.values;
+    const auto state = __builtin_amdgcn_make_buffer_rsrc(r.carries + at * each, 0, static_cast<int>(each * 4), kBufferFlags);
+    const auto grad = __builtin_amdgcn_make_buffer_rsrc(w.grads + at * each, 0, static_cast<int>(each * 4), kBufferFlags);
     f32x4 gram[kGradJobs], yq[MT], zs[MT], ud[MT];  // the triangles' tiles; dY S^T, Z S^T and U D^T, transposed
 #pragma unroll
     for (int m = 0; m < MT; ++m) yq[m] = zs[m] = ud[m] = f32x4{0, 0, 0, 0};
@@ -415,122 +413,70 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
       reinterpret_cast<u32x4 *>(&lds.f)[thread] = at_lane(reinterpret_cast<const u32x4 *>(w.factors + at), thread);
     if (QUERIES && head % share == 0) fill(lds.q, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.q, span.batch, row, key_head, n, keys), 0);
     again();
-    if constexpr (FRAGS) {  // T diag(b), P^T and T^T, NO parts of each
-      constexpr int N = kFrags * NO * kWave;
-#pragma unroll
-      for (int i = 0; i < (3 * N + kGradThreads - 1) / kGradThreads; ++i) {
-        const int u = thread + i * kGradThreads, which = u / N, frag = u % N / kWave;
-        if (u >= 3 * N) break;
-        const int parts = which == 0 ? Tri::kTParts : kFull, start = which == 0 ? Tri::kT : which == 1 ? Tri::kP : Tri::kTt;
-        lds.frags[u] = at_lane(tri, (start + frag / NO * parts + frag % NO) * kWave + u % kWave);
-      }
-    }
-    f32x4 by_row[2][kTiles];  // over this wave's values: z . x and b z . K S on U's side, u . K D on Z's
-#pragma unroll
-    for (int m = 0; m < kTiles; ++m) by_row[0][m] = by_row[1][m] = f32x4{0, 0, 0, 0};
-    // T diag(b), P^T and T^T; U and Z transposed: a lane has four neighbouring columns of a step
-    auto triangle = [&](f32x4 (&c)[kTiles], auto which, const auto &lo, const auto &hi) __attribute__((always_inline)) {
-      constexpr int W = decltype(which)::value;
-      constexpr bool UPPER = W != 0, TRANSPOSED = W != 1;
-      unrolled<0, 2>([&](auto half) __attribute__((always_inline)) {
-        constexpr int h = decltype(half)::value;
-        constexpr int first = UPPER || h == 0 ? 0 : 2, count = (UPPER ? in_upper(2, h) : in_lower(0, h)) ? 4 : 2;
-        Cut<NO> f[count];
-#pragma unroll
-        for (int m = 0; m < count; ++m) {
-          const int frag = UPPER ? upper_frag(first + m, h) : lower_frag(first + m, h);
-          if constexpr (FRAGS)
-            f[m] = load_frag<NO>(lds.frags + W * kFrags * NO * kWave, frag, NO, lane);
-          else
-            f[m] = load_frag<NO>(tri + (W == 0 ? Tri::kT : W == 1 ? Tri::kP : Tri::kTt) * kWave, frag, W == 0 ? Tri::kTParts : kFull, lane);
-        }
-        if constexpr (TRANSPOSED)
-          multiply_rows_t<NO>(c + first, f, h ? hi : lo);
-        else
-          multiply_rows<NO>(c + first, f, h ? hi : lo);
-        if constexpr (!FRAGS || KEYS == 128) part_done();
-      });
-    };
-
+    const float own_rate = w.factors[at].rate[thread / (kValues / 8)];
+    float rate_sum = 0.0f;  // z . x of this thread's step and columns
     for (int from = 0; from < values; from += kValues) {
       if (from) __syncthreads();
       again();
-      const int col = from + 16 * column + x;
-      const bool inside = col < values;
-      // one side's columns of the state, the other's of its gradient
-      float a[S][8];
-#pragma unroll
-      for (int s = 0; s < S; ++s)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          a[s][e] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(first_side ? state : grad, ((32 * s + e + 8 * g) * values + col) * 4, 0, 0));
-      fill(lds.one.dy, Const<kValues / 8>{}, Rows<T, WHOLE>(r.dy, span.batch, row, head, n, values), from);
-      if constexpr (sizeof(T) == 2) {
-        const int t = thread / (kValues / 8), c = thread % (kValues / 8) * 8;
-        Raw8<T> v = Rows<T, WHOLE>(r.v, span.batch, row, head, n, values).load(t, from + c);
-        if (!WHOLE || from + kValues > values) settle<WHOLE>(v, from + c, values, t < n);
-        *reinterpret_cast<u32x4 *>(lds.one.u + t * VR + c) = v.w[0];
-      }
-      __syncthreads();
-      if (from + kValues > values) {
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) a[s][e] = inside ? a[s][e] : 0.0f;
-      }
-      f32x4 o[kTiles], p[kTiles], in[kTiles];  // U's side: U, K S and X; Z's: Z, its part through K
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) p[m] = f32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        Cut<NP> k[kTiles];
-        tile_rows<KEYS>(k, lds.k, s, lane);
-        multiply_rows<NO>(p, k, cut<NO>(a[s]));
-        if constexpr (KEYS == 128 && (SHARED || sizeof(T) == 4)) part_done();
-      }
-      // rows of the state and its gradient, for the products at the end
+      // rows of the state and its gradient, for the products with the values; behind the last key zeros
       u32x4 rows[kValues / 32][2][2];
       auto fetch_rows_of_states = [&](auto part) __attribute__((always_inline)) {
         constexpr int s = decltype(part)::value;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int byte = ((16 * tile_k + x) * values + from + 32 * s + 8 * g + 4 * h) * 4;
+          const int key = 16 * tile_k + x;
+          const int byte = (key < keys ? key * values + from + 32 * s + 8 * g + 4 * h : static_cast<int>(each)) * 4;
           rows[s][0][h] = __builtin_amdgcn_raw_buffer_load_b128(state, byte, 0, 0);
           rows[s][1][h] = __builtin_amdgcn_raw_buffer_load_b128(grad, byte, 0, 0);
         }
       };
-      // where registers are left
-      constexpr bool EARLY = sizeof(T) == 2 && !(SHARED && KEYS == 128);
-      if constexpr (EARLY) unrolled<0, kValues / 32>(fetch_rows_of_states);
-      part_done();
-      if (first_side) {
+      {  // a thread has eight columns of one step: U, Z and dY into LDS, dV out
+        const int t = thread / (kValues / 8), at_c = thread % (kValues / 8) * 8, c = from + at_c;
+        const int byte = static_cast<int>(states + t * values + c) * 4;
+        u32x4 errors[2], zs_of[2];
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          f32x4 v;
-          if constexpr (sizeof(T) == 2)
-            v = value_column(reinterpret_cast<const T *>(lds.one.u), m, 16 * column, lane);
-          else
-            v = load_column<T>(r.v, span.batch, row, n, head, m, g, col, inside);
-          p[m] *= factor4(lds.f.into, m, lane);
-          in[m] = v - p[m];
-          o[m] = f32x4{0, 0, 0, 0};
+        for (int h = 0; h < 2; ++h) {
+          errors[h] = __builtin_amdgcn_raw_buffer_load_b128(state, byte + 16 * h, 0, 0);
+          zs_of[h] = __builtin_amdgcn_raw_buffer_load_b128(grad, byte + 16 * h, 0, 0);
         }
-        part_done();
-        triangle(o, Const<0>{}, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]));
-        put_transposed<NO, VR>(lds.one.u, o, 16 * column, lane);
-      } else {
+        Raw8<T> dy = Rows<T, WHOLE>(r.dy, span.batch, row, head, n, values).load(t, c);
+        if constexpr (!LATE) unrolled<0, kValues / 32>(fetch_rows_of_states);
+        float u[8], z[8];
 #pragma unroll
-        for (int m = 0; m < kTiles; ++m) {
-          p[m] *= factor4(lds.f.out, m, lane);
-          in[m] = p[m];
-          o[m] = f32x4{0, 0, 0, 0};
+        for (int e = 0; e < 8; ++e) {
+          const bool in = c + e < values;
+          u[e] = in ? __uint_as_float(errors[e / 4][e % 4]) : 0.0f;
+          z[e] = in ? __uint_as_float(zs_of[e / 4][e % 4]) : 0.0f;
+          rate_sum = fmaf(z[e], u[e], rate_sum);
+          u[e] *= own_rate;
         }
-        part_done();
-        triangle(in, Const<1>{}, plain_columns<VR, NP, 16>(lds.one.dy, 0, 16 * column, lane),
-                 plain_columns<VR, NP, 16>(lds.one.dy, 32, 16 * column, lane));
-        part_done();
-        triangle(o, Const<2>{}, cut_tiles<NO>(in[0], in[1]), cut_tiles<NO>(in[2], in[3]));
-        put_transposed<NO, VR>(lds.one.z, o, 16 * column, lane);
+        const auto u_parts = cut<NO>(u), z_parts = cut<NO>(z);
+        if (!WHOLE || from + kValues > values) settle<WHOLE>(dy, c, values, t < n);
+        const auto dy_parts = cut_raw<T>(dy);
+#pragma unroll
+        for (int p = 0; p < NO; ++p) {
+          *reinterpret_cast<u32x4 *>(lds.one.u + (p * kRun + t) * VR + at_c) = u_parts.p[p];
+          *reinterpret_cast<u32x4 *>(lds.one.z + (p * kRun + t) * VR + at_c) = z_parts.p[p];
+          if (p < NP) *reinterpret_cast<u32x4 *>(lds.one.dy + (p * kRun + t) * VR + at_c) = dy_parts.p[p < NP ? p : 0];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] *= own_rate;
+        if (t < n) {
+          T *to = head_row<T>(r.dv, span.batch, row + t, head) + c;
+          if (c + 8 <= values) {
+            if constexpr (sizeof(T) == 2) {
+              store_vec(to, z, false);
+            } else {
+              const float lo[4] = {z[0], z[1], z[2], z[3]}, hi[4] = {z[4], z[5], z[6], z[7]};
+              store_vec(to, lo, false);
+              store_vec(to + 4, hi, false);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (c + e < values) to[e] = static_cast<T>(z[e]);
+          }
+        }
       }
       __syncthreads();
       again();
@@ -549,52 +495,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         }
       }
       part_done();
-      {  // dV by rows, eight columns a thread
-        const int t = thread / (kValues / 8), c = from + thread % (kValues / 8) * 8;
-        float v[8] = {};
-#pragma unroll
-        for (int part = NO - 1; part >= 0; --part) {
-          const bf16x8 b = *reinterpret_cast<const bf16x8 *>(lds.one.z + (part * kRun + t) * VR + c - from);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += static_cast<float>(b[e]);
-        }
-        const float rate = lds.f.rate[t];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= rate;
-        if (t < n) {
-          T *to = head_row<T>(r.dv, span.batch, row + t, head) + c;
-          if (c + 8 <= values) {
-            if constexpr (sizeof(T) == 2) {
-              store_vec(to, v, false);
-            } else {
-              const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-              store_vec(to, lo, false);
-              store_vec(to + 4, hi, false);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (c + e < values) to[e] = static_cast<T>(v[e]);
-          }
-        }
-      }
-      part_done();
-      again();
-#pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        if (first_side) {
-          const f32x4 z = tile_values<VR, NO>(lds.one.z, m, 16 * column, lane);
-          by_row[0][m] += z * in[m];
-          by_row[1][m] += factor4(lds.f.rate, m, lane) * z * p[m];
-        } else {
-          by_row[1][m] += tile_values<VR, NO>(lds.one.u, m, 16 * column, lane) * p[m];
-        }
-        part_done();
-      }
       again();
       unrolled<0, kValues / 32>([&](auto part) __attribute__((always_inline)) {
         constexpr int s = decltype(part)::value;
-        if constexpr (!EARLY) fetch_rows_of_states(part);
+        if constexpr (LATE) fetch_rows_of_states(part);
         const int c = from + 32 * s + 8 * g;
         float b[2][8];
 #pragma unroll
@@ -615,39 +519,49 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
 #pragma unroll
           for (int e = 0; e < 8; ++e) last = fmaf(b[0][e] * lds.f.into[kRun - 1], b[1][e], last);
         }
-        const Cut<NO> sp = cut<NO>(b[0]), dp = cut<NO>(b[1]);
+        constexpr bool TIGHT = KEYS == 128 && (SHARED || sizeof(T) == 4);  // registers
+        if constexpr (TIGHT) part_done();
+        const Cut<NO> sp = cut<NO>(b[0]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           multiply<NO>(yq[m], sp, tile_rows<kValues, NP>(lds.one.dy, tile_m + m, s, lane));
           multiply<NO>(zs[m], sp, tile_rows<kValues, NO>(lds.one.z, tile_m + m, s, lane));
+          if constexpr (TIGHT) part_done();
+        }
+        const Cut<NO> dp = cut<NO>(b[1]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
           multiply<NO>(ud[m], dp, tile_rows<kValues, NO>(lds.one.u, tile_m + m, s, lane));
-          if constexpr (KEYS == 128 && (SHARED || sizeof(T) == 4)) part_done();
+          if constexpr (TIGHT) part_done();
         }
       });
     }
+    again();
 #pragma unroll
     for (int m = 0; m < MT; ++m) {  // a step's factors are a lane's here
       const int t = 16 * (tile_m + m) + x;
+      const f32x4 o = ud[m] * lds.f.out[t], i = zs[m] * (lds.f.rate[t] * lds.f.into[t]);
       dq[m] += yq[m] * (r.scale * lds.f.into[t]);
-      dk[m] += ud[m] * lds.f.out[t] - zs[m] * (lds.f.rate[t] * lds.f.into[t]);
-    }
+      dk[m] += o - i;
+      float ends = 0.0f, sum = 0.0f;  // k . o, k . i
 #pragma unroll
-    for (int m = 0; m < kTiles; ++m) {
-      float sums[2][4];
+      for (int part = 0; part < NP; ++part) {
+        const uint16_t *k = lds.k + (part * kRun + t) * KR + 16 * tile_k + 4 * g;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sums[0][i] = across16(by_row[0][m][i]);
-        sums[1][i] = across16(by_row[1][m][i]);
-        if (!first_side && x == 0) last += sums[1][i];  // k . o
+        for (int e = 0; e < 4; ++e) {
+          const float key = __uint_as_float(static_cast<uint32_t>(k[e]) << 16);
+          ends = fmaf(key, o[e], ends);
+          sum = fmaf(key, i[e], sum);
+        }
       }
-      if (x < 4) {
-        const auto of = [&](const float (&v)[4]) __attribute__((always_inline)) {
-          return x == 0 ? v[0] : x == 1 ? v[1] : x == 2 ? v[2] : v[3];
-        };
-        lds.sums[wave][16 * m + 4 * g + x] = of(sums[1]);
-        if (first_side) lds.rates[wave][16 * m + 4 * g + x] = of(sums[0]);
-      }
+      last += ends;
+      sum = across_groups(sum + ends);
+      if (g == 0) lds.sums[tile_k][t] = sum;
     }
+    rate_sum += dpp<kDppQuadXor1>(rate_sum);
+    rate_sum += dpp<kDppQuadXor2>(rate_sum);
+    rate_sum += dpp<kDppRowHalfMirror>(rate_sum);
+    if (thread % (kValues / 8) == 0) lds.rates[thread / (kValues / 8)] = rate_sum;
     last = across_groups(across16(last));
     if (lane == 0) lds.lasts[wave] = last;
     __syncthreads();  // u, z and dy are done with
@@ -688,7 +602,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         const bool in = job < kGrams ? j <= t : j < t;
         const float e = in ? exp_of<T>(static_cast<float>(lds.f.sum[t] - sum_j)) : 0.0f;
         // dG_t: q . dq holds this row of P but for its diagonal, which e^{G_t - G_t} is no factor of
-        float v = (job < kGrams ? r.scale : -lds.f.rate[t]) * e * gram[q][i], line, rate = 0.0f;
+        float v = (job < kGrams ? r.scale : -lds.f.rate[t]) * e * gram[q][i], line;
         if (!in) v = 0.0f;
         const float p = in ? v * raw[i] : 0.0f;
         if (job < kGrams) {
@@ -696,13 +610,9 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
           down += j < t ? p : 0.0f;
         } else {
           line = across16(p);
-          rate = across16(in ? -e * raw[i] * gram[q][i] : 0.0f);
           down += p;
         }
-        if (x == 0) {
-          lds.gram_rows[job][4 * g + i] = line;
-          if (job >= kGrams) lds.gram_rates[tile][4 * g + i] = rate;
-        }
+        if (x == 0) lds.gram_rows[job][4 * g + i] = line;
 #pragma unroll
         for (int a = 0; a < NO; ++a) {
           const __bf16 vb = static_cast<__bf16>(v);
@@ -720,14 +630,14 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     again();
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const Cut<NP> k = plain_columns<KR, NP, 4>(lds.k, 32 * s, 16 * tile_k, lane);
+      const Cut<NP> k = plain_columns<KR, NP>(lds.k, 32 * s, 16 * tile_k, lane);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (in_lower(tile_m + m, s)) {
           multiply<NO>(dq[m], k, tile_rows<kValues, NO>(lds.two.f, tile_m + m, s, lane));
           multiply<NO>(dk[m], k, tile_rows<kValues, NO>(lds.two.h, tile_m + m, s, lane));
         }
-        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], k, plain_columns<VR, NO, 4>(lds.two.h, 32 * s, 16 * (tile_m + m), lane));
+        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], k, plain_columns<VR, NO>(lds.two.h, 32 * s, 16 * (tile_m + m), lane));
       }
     }
     if constexpr (!QUERIES) {
@@ -738,10 +648,10 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     const uint16_t *queries = QUERIES ? lds.q : lds.k;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const Cut<NP> q = plain_columns<KR, NP, 4>(queries, 32 * s, 16 * tile_k, lane);
+      const Cut<NP> q = plain_columns<KR, NP>(queries, 32 * s, 16 * tile_k, lane);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], q, plain_columns<VR, NO, 4>(lds.two.f, 32 * s, 16 * (tile_m + m), lane));
+        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], q, plain_columns<VR, NO>(lds.two.f, 32 * s, 16 * (tile_m + m), lane));
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {  // q . dq: step 16 m + x, four keys
@@ -759,24 +669,19 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
     __syncthreads();
     again();
     if (wave == 0) {  // the gates: lane i has step i
-      double turned = 0.0, rate = 0.0, end = 0.0;
+      double turned = 0.0, end = 0.0;
 #pragma unroll
       for (int v = 0; v < KT; ++v) turned += lds.turns[v][lane];
       double own = KEEP ? turned - lds.turned[lane] : turned;
       if constexpr (KEEP) lds.turned[lane] = turned;
 #pragma unroll
-      for (int v = 0; v < kGradWaves; ++v) {
-        own -= lds.sums[v][lane];
-        if (v < kFrontWaves) rate += lds.rates[v][lane];
-        end += lds.lasts[v];
-      }
+      for (int v = 0; v < KT; ++v) own -= lds.sums[v][lane];
+#pragma unroll
+      for (int v = 0; v < kGradWaves; ++v) end += lds.lasts[v];
 #pragma unroll
       for (int job = 0; job < 2 * kGrams; ++job) {
         const int tile = job % kGrams;
-        if (gram_row(tile) == g) {
-          own += lds.gram_rows[job][x];
-          if (job >= kGrams) rate += lds.gram_rates[tile][x];
-        }
+        if (gram_row(tile) == g) own += lds.gram_rows[job][x];
         if (gram_col(tile) == g) own -= lds.gram_cols[job][x];
       }
       // sum over this step and those behind it
@@ -789,7 +694,7 @@ __global__ __launch_bounds__(kGradThreads, 2) void delta_grads_kernel(
         const float b = rate_of(r.rate, beta);
         const float turn = r.rate == FFTMV_RATE_SIGMOID ? b / (1.0f + expf(beta)) : 1.0f;
         *head_row<T>(r.dgate, span.batch, row + lane, head) = static_cast<T>(static_cast<float>(grad_log) * slope);
-        *head_row<T>(r.dbeta, span.batch, row + lane, head) = static_cast<T>(static_cast<float>(rate) * turn);
+        *head_row<T>(r.dbeta, span.batch, row + lane, head) = static_cast<T>(lds.rates[lane] * turn);
       }
     }
     if constexpr (SHARED && !KEEP) {

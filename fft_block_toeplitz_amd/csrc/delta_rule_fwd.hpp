@@ -13,7 +13,7 @@ struct ForwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
   alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS> : 8];
   static constexpr int NO = kOut<T>, S = KEYS / 32;
   alignas(16) u32x4 s[kFrontWaves][S][NO][kWave];  // the state at the run's start, cut
-  alignas(16) f32x4 u[kFrontWaves][kTiles][kWave];  // U
+  alignas(16) f32x4 u[kFrontWaves][kTiles][kWave];  // X
 };
 
 // What a chain is for: the outputs, also with the states kept for the backward pass, or the maps of parts.
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
 #pragma unroll
       for (int m = 0; m < kTiles; ++m) u[m] *= *reinterpret_cast<const f32x4 *>(lds.out + 16 * m + 4 * g);
       const float whole = lds.into[kRun - 1];
-      if constexpr (USE == kCarries) keep(r.carries + ((span.run + first / kRun) * r.heads + head) * states, values);
+      if constexpr (USE == kCarries) keep(r.carries + ((span.run + first / kRun) * r.heads + head) * (states + kRun * r.values), values);
       __syncthreads();
       const Cut<kFull> a = cut_tiles<kFull>(u[0], u[1]), c = cut_tiles<kFull>(u[2], u[3]);
 #pragma unroll
@@ -203,6 +203,14 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
         f32x4 u[kTiles];
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) u[m] = lds.u[wave][m][lane];
+        if constexpr (USE == kCarries) {
+          float *to = r.carries + at(first) * (states + kRun * r.values) + states;
+#pragma unroll
+          for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (inside) to[static_cast<int64_t>(16 * m + 4 * g + i) * values + col] = u[m][i];
+        }
         multiply_triangle<NO, false, true>(y, p, cut_tiles<NO>(u[0], u[1]), cut_tiles<NO>(u[2], u[3]));
         if constexpr (sizeof(T) == 2) fetch_triangle(then);
         if constexpr (!TILE) fetch_first_queries(then);

@@ -214,9 +214,9 @@ def delta_rule(q, k, v, gate, beta, h0=None, *, decay="sigmoid", rate="sigmoid",
     last = v.new_empty((B, H, K, V), dtype=_sq._torch.float32)
     if B == 0:
         y.zero_()
-        return (y, last, last) if save else (y, last)
+        return (y, last, last.new_empty((0, H, K + FFTMV_DELTA_RUN, V))) if save else (y, last)
     runs, need = _sizes(B, T, Hk, H, K, V, dtype, offsets is not None, False)
-    carries = v.new_empty((runs, H, K, V), dtype=_sq._torch.float32) if save else None
+    carries = v.new_empty((runs, H, K + FFTMV_DELTA_RUN, V), dtype=_sq._torch.float32) if save else None
     ws = v.new_empty(need, dtype=_sq._torch.uint8)
     r = _DELTA.pack(B, T, Hk, H, K, V, dtype, *kinds, _scale(scale, K), lens, offs, *fields, h0p,
                     carries.data_ptr() if save else 0, ws.data_ptr(), need, *_fresh(y), last.data_ptr(), *_NONE, 0,
@@ -244,7 +244,7 @@ def delta_rule_backward(dy, q, k, v, gate, beta, carries, h0=None, dh_last=None,
     runs, need = _sizes(B, T, Hk, H, K, V, dtype, offsets is not None, True) if B else (0, 0)
     if carries is None:
         raise ValueError("carries must be what delta_rule(..., save=True) returned")
-    cp = _floats(carries, (runs, H, K, V), v, "carries")
+    cp = _floats(carries, (runs, H, K + FFTMV_DELTA_RUN, V), v, "carries")
     lens, offs = _ints(lengths, B, v, "lengths"), _ints(offsets, B + 1, v, "offsets")
     dq, dk, dv, dg, db = (_empty(t) for t in (q, k, v, gate, beta))
     dh0 = v.new_empty((B, H, K, V), dtype=torch.float32)

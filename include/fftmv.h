@@ -511,8 +511,9 @@ typedef struct fftmv_heads_s {
  * (rounded once to the element type) and, where not NULL,
  *   h_last   [batch][heads][keys][values] the states after the last steps (h0
  *            of an empty sequence)
- *   carries  [runs][heads][keys][values] (runs: fftmv_delta_rule_sizes) the
- *            states that enter the runs: what the backward pass starts from
+ *   carries  [runs][heads][keys + FFTMV_DELTA_RUN][values] (runs:
+ *            fftmv_delta_rule_sizes): the states that enter the runs and, for
+ *            each of their steps, v - a S^T k: what the backward pass starts from
  * Backward takes the inputs, h0 and carries as the forward had and left them,
  * dy (the gradient of y) and, where not NULL, dh_last (that of h_last), and
  * writes the gradients dq, dk (summed over the heads that share them), dv,
