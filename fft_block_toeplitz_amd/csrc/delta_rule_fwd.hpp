@@ -8,8 +8,8 @@
 
 namespace fftmv {
 
-template <typename T, int KEYS, int BUFFERS, bool TILE>
-struct ForwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
+template <typename T, int KEYS, int FRAGS, int BUFFERS, bool TILE>
+struct ForwardLds : ChainLds<T, KEYS, FRAGS, BUFFERS> {
   alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS> : 8];
   static constexpr int NO = kOut<T>, S = KEYS / 32;
   alignas(16) u32x4 s[kFrontWaves][S][NO][kWave];  // the state at the run's start, cut
@@ -22,11 +22,14 @@ enum ChainUse { kOutputs, kCarries, kMaps };
 template <typename T, int KEYS, bool WHOLE, int USE>
 __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Tri = Triangles<T, false>;
-  constexpr int FRAGS = kFrags * kFull, S = KEYS / 32;
-  constexpr bool TILE = sizeof(ForwardLds<T, KEYS, 1, true>) <= kLdsBytes;  // else queries go from memory to registers
-  constexpr int BUFFERS = sizeof(ForwardLds<T, KEYS, 2, TILE>) <= kLdsBytes ? 2 : 1;
-  using Lds = ForwardLds<T, KEYS, BUFFERS, TILE>;
-  constexpr int NP = kParts<T>, NO = kOut<T>;
+  constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32;
+  // P of 16-bit elements goes through LDS as T does: each wave for itself from memory, four times the loads, made one
+  // sequence of 65536 steps (8 heads of 128 x 128 bf16) 276 us instead of 262. The parts of FP32 ones do not fit
+  constexpr bool PTILE = USE != kMaps && sizeof(T) == 2;
+  constexpr int FRAGS = kFrags * (PTILE ? kFull + NO : kFull);
+  constexpr bool TILE = sizeof(ForwardLds<T, KEYS, FRAGS, 1, true>) <= kLdsBytes;  // else queries go from memory to registers
+  constexpr int BUFFERS = sizeof(ForwardLds<T, KEYS, FRAGS, 2, TILE>) <= kLdsBytes ? 2 : 1;
+  using Lds = ForwardLds<T, KEYS, FRAGS, BUFFERS, TILE>;
   __shared__ Lds lds;
   const int side = __builtin_amdgcn_readfirstlane(threadIdx.x / kFrontThreads);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % kFrontWaves;
@@ -155,8 +158,12 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
     };
     auto fetch_triangle = [&](int first) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < kFrags; ++i)
-        p[i] = load_frag<NO>(w.triangles + (at(first) * Tri::kAll + Tri::kP) * kWave, i, Tri::kPParts, lane);
+      for (int i = 0; i < kFrags; ++i) {
+        if constexpr (PTILE)
+          p[i] = load_frag<NO>(lds.frags + Tri::kP * kWave, i, Tri::kPParts, lane);
+        else
+          p[i] = load_frag<NO>(w.triangles + (at(first) * Tri::kAll + Tri::kP) * kWave, i, Tri::kPParts, lane);
+      }
     };
     auto fetch_queries = [&](int first, auto s) __attribute__((always_inline)) {
       q.template fetch<decltype(s)::value>(r.q, keys, span.batch, span.row + first, steps(first), key_head, lane);
@@ -164,7 +171,6 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
     auto fetch_first_queries = [&](int first) __attribute__((always_inline)) { unrolled<0, HOLD>([&](auto s) __attribute__((always_inline)) { fetch_queries(first, s); }); };
     if (part.end > part.begin) {
       fetch(part.begin);
-      if constexpr (sizeof(T) == 2 && USE != kMaps) fetch_triangle(part.begin);
       if constexpr (!TILE && USE != kMaps) fetch_first_queries(part.begin);
       next.put_keys(thread, lds.k[0], keys, steps(part.begin));
       put(part.begin);
@@ -194,7 +200,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
           multiply_rows_t<NO>(y, rows, part);  // steps along the lanes
           if constexpr (!TILE) part_done();
         });
-        if constexpr (sizeof(T) == 4) fetch_triangle(first);  // only now: registers
+        fetch_triangle(first);  // only now: registers
 #pragma unroll
         for (int m = 0; m < kTiles; ++m) y[m] *= r.scale * lds.into[16 * m + x];
       }
@@ -212,7 +218,6 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
               if (inside) to[static_cast<int64_t>(16 * m + 4 * g + i) * values + col] = u[m][i];
         }
         multiply_triangle<NO, false, true>(y, p, cut_tiles<NO>(u[0], u[1]), cut_tiles<NO>(u[2], u[3]));
-        if constexpr (sizeof(T) == 2) fetch_triangle(then);
         if constexpr (!TILE) fetch_first_queries(then);
         const int c = first_col + 16 * wave + 4 * g;
         T *to = head_row<T>(r.y, span.batch, span.row + first, head);
