@@ -204,6 +204,8 @@ __device__ __forceinline__ void load8(const T *p, int c, int n, float (&x)[8]) {
 //          Addresses take one instruction, and no branch stands between loads
 //   else   where the row ends inside, the load is moved back to end with the row,
 //          and shifted afterwards
+// (45 packed sequences of 30011 steps, 16 heads of 64 x 128 fp16: 490 us whole, 650 by
+// the other way; 8 x 2048 steps of 16 heads of 128 x 128 bf16 with gradients 1120 and 1194.)
 template <typename T>
 struct Raw8 {
   u32x4 w[sizeof(T) / 2];
@@ -418,8 +420,10 @@ struct DeltaCuts {
   int runs;   // of a part
 };
 // Times in tenths of a run of the chain, on 256 CUs: a map's run takes 0.8 of one, a joint 1.2, the
-// two more launches 4. (One sequence of 65536 steps, 8 heads of 128 x 128: whole
-// 3430 us, in 16 parts 560.) Packed sequences' lengths are on the device: they stay whole.
+// two more launches 4. (bf16, whole and in parts: one sequence of 65536 steps, 8 heads of
+// 128 x 128 3637 and 747 us; 5 of 1999 steps, 7 heads of 75 x 41 168 and 121; FP32 with gradients,
+// 6 of up to 1000 steps, 4 heads of 64 x 64 255 and 202.) Packed sequences' lengths are on the
+// device: they stay whole.
 inline DeltaCuts delta_cuts(int64_t batch, int64_t steps, int64_t heads, int64_t keys, int64_t values, bool packed) {
   const int64_t runs = (steps + kRun - 1) / kRun, chains = batch * heads;
   DeltaCuts best = {1, static_cast<int>(runs > 0 ? runs : 1)};
@@ -697,8 +701,10 @@ __device__ __forceinline__ f32x4 load_column(const fftmv_heads_t &f, int64_t b, 
 // run has two halves between barriers:
 //   front  R = V - e^G K S, U = T R     | S' = e^{G_last} S + K^T (..) U
 //   back   Q S; the next run's loads    | Y = .. + P U; the next run into LDS
-// (8 x 2048 x 16 heads of 128 x 128 in bf16 took 235 us with all of it in one
-// wave a SIMD.)
+// The back waves' half with the loads' way to LDS bounds a run (4.1 us at 128 keys, of which
+// the front's products in line take 2.9), where states are kept also memory. (8 x 2048
+// steps of 16 heads of 128 x 128 in bf16, 210 us with the states and errors kept, took 235
+// without the errors and all of it in one wave a SIMD. Loads two runs ahead were slower.)
 constexpr int kFrontWaves = 4;
 constexpr int kFrontThreads = kFrontWaves * kWave;
 constexpr int kChainThreads = 2 * kFrontThreads;
@@ -770,7 +776,10 @@ __device__ __forceinline__ void clear_rows(const fftmv_delta_rule_t &r, const ff
 // chains load, two of P's tiles and the same two of the triangle each, so that a
 // decay is computed once for both: four waves have three or two tiles each. Rows
 // lie in LDS as they are in memory: products of 16-bit elements are exact in
-// FP32, FP32 ones are cut where they are read.
+// FP32, FP32 ones are cut where they are read. Memory bounds it: a run of 128 keys
+// in 16 bits reads 32 KB and leaves 31 to 37 (8 x 2048 steps of 16 heads: 67 us forward, 73
+// backward, 3.9 TB/s; one wave a run, with the rows in registers, took 72 and 80, and
+// 20 instead of 12 for 4 runs of 20 heads in FP32, where the latency of one counts).
 template <typename T, int KEYS>
 struct FactorLds {
   static constexpr int ROW = KEYS + 16 / sizeof(T);
@@ -1067,7 +1076,7 @@ struct Part {
 // The states in front of the parts (backward: the gradients of those behind
 // them) one after another. A workgroup has 16 value columns and a wave 16 keys of
 // them; the waves pass each other the state through LDS, and load the next map
-// while they wait. (One wave for all keys took 18 us a joint at 128 x 128.)
+// while they wait: 3.1 us a joint at 128 x 128 (one wave for all keys: 18).
 // (T keeps the instances of one element type's source apart from the others'.)
 template <typename T, int KEYS, bool BACK>
 __global__ __launch_bounds__(KEYS / 16 * kWave) void delta_join_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {

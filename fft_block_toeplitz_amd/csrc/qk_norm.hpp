@@ -10,6 +10,11 @@
 // cosines are the same for all heads of a row: a workgroup computes them once
 // for its rows, in LDS. Angles are reduced to a turn in FP64: half a million
 // positions along, FP32 would leave two digits of them.
+// 16384 rows of 40 heads of 128 bf16: 55 us, 6.1 TB/s (out of memory 71, a copy's
+// rate); with results through the caches 90. Gradients of as many rows of 32
+// heads: 78 us. 9995 rows of 10 heads of 75 FP32 take 25 us either way, for 12 and
+// 19 of bytes: rows that are not aligned, a third of the lanes idle, and the
+// card filled once.
 #pragma once
 
 #include <algorithm>
@@ -28,14 +33,18 @@ constexpr int kNormPairs = 4;              // pairs of elements a lane
 constexpr int kNormTurns = 2048;           // cosines a workgroup keeps, and as many sines: 16 KB of LDS
 constexpr int kNormRows = 32;              // rows a workgroup takes at once, at most
 constexpr int kNormUnits = 256;            // heads of rows that it takes at once, about
-constexpr int kNormWide = 1024;            // workgroups that fill the card: eight on each CU
+// Workgroups that fill the card, four on each CU. (Gradients of 8 x 2048 rows of
+// 32 heads of 128 bf16: 1024 88 us, 2048 96, 512 122.)
+constexpr int kNormWide = 1024;
 
 // How the elements of a head lie on the lanes. Apart: first the rotated pairs,
 // four a lane, then the rest, eight a lane; the last lane of either goes back
 // until it has four or eight, and what it shares with the lane before counts
 // for sums there alone. Where a part is shorter than a lane, or the lanes do
 // not suffice, pairs follow each other through all of the head, and lanes with
-// an end in them take their elements one by one.
+// an end in them take their elements one by one. (All heads that way: 9995 rows
+// of 10 heads of 75 FP32 with gradients 73 us instead of 54, 16384 rows of 40 heads
+// of 128 bf16 63 instead of 57.)
 struct NormPlan {
   int turned, dim;    // pairs that are rotated, elements
   int apart;          // 0: pairs follow each other
@@ -62,7 +71,8 @@ inline NormPlan qk_norm_plan(int64_t rows, int64_t query_heads, int64_t key_head
   p.turns = (p.turned_lanes + 1) * kNormPairs;
   const int64_t heads[2] = {query_heads, key_heads};
   for (int i = 0; i < 2; ++i) {
-    // few rows: so few at a time that all of the card takes part
+    // few rows: so few at a time that all of the card takes part (64 rows of 40 heads of 128: 4.2 us, six at a
+    // time 12.9; 2048 rows 10 and 16)
     const int64_t each = std::max<int64_t>(heads[i], 1), spread = rows * (query_heads + key_heads) / (kNormWide * each);
     const int64_t fit = p.turned ? kNormTurns / p.turns : kNormRows;
     const int64_t r = std::min({kNormUnits / each, spread, fit, int64_t{kNormRows}});
