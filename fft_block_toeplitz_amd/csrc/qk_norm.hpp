@@ -12,7 +12,7 @@
 // positions along, FP32 would leave two digits of them.
 // 16384 rows of 40 heads of 128 bf16: 55 us, 6.1 TB/s (out of memory 71, a copy's
 // rate); with results through the caches 90. Gradients of as many rows of 32
-// heads: 78 us. 9995 rows of 10 heads of 75 FP32 take 25 us either way, for 12 and
+// heads: 71 us. 9995 rows of 10 heads of 75 FP32 take 25 us either way, for 12 and
 // 19 of bytes: rows that are not aligned, a third of the lanes idle, and the
 // card filled once.
 #pragma once
