@@ -9,6 +9,7 @@ namespace {
 struct Lane {
   int first, second;
   bool whole;      // by fours
+  bool joined;     // all eight in a row
   uint32_t owned;  // slots that are this lane's alone, bit by bit
   int turns;       // its cosines
 };
@@ -27,7 +28,7 @@ __device__ __forceinline__ int pair_of(const NormPlan &s, int l, int e) {
 }
 template <bool WHOLE>
 __device__ __forceinline__ Lane lane_of(const NormPlan &s, bool halves, int l) {
-  Lane r = {0, 4, true, 0, min(l, s.turned_lanes) * kNormPairs};
+  Lane r = {0, 4, true, false, 0, min(l, s.turned_lanes) * kNormPairs};
   const int p = kNormPairs * l;
   if constexpr (WHOLE) {
     if (l < s.turned_lanes) {
@@ -49,48 +50,55 @@ __device__ __forceinline__ Lane lane_of(const NormPlan &s, bool halves, int l) {
     for (int e = 0; e < kNormElements; ++e)
       if (element_of(s, halves, l, e) >= 0) r.owned |= 1u << e;
   }
+  r.joined = r.whole && r.second == r.first + 4;
   return r;
 }
 
-// A lane's elements as they lie in memory.
+// A lane's elements as they lie in memory, in words: as elements of 16 bits the
+// compiler takes them apart where they are loaded, and waits there (8 x 2048 rows
+// of 32 heads of 128 bf16, gradients: 83 us, so 72).
 template <typename T>
 struct Raw {
-  Vec<T, 4> part[2];
-  __device__ __forceinline__ float operator[](int e) const { return part[e / 4][e % 4]; }
+  uint32_t w[2 * sizeof(T)];
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(w[e]);
+    else
+      return static_cast<float>(__builtin_bit_cast(T, static_cast<uint16_t>(w[e / 2] >> e % 2 * 16)));
+  }
 };
 // Lanes without elements read some of their neighbours' where all are taken by fours.
 template <bool WHOLE, typename T>
 __device__ __forceinline__ void fetch(Raw<T> &r, const T *x, const Lane &at, const NormPlan &s, bool halves, int l) {
-  if constexpr (sizeof(T) == 2) {
-    if ((WHOLE || at.whole) && at.second == at.first + 4) {
-      r = __builtin_bit_cast(Raw<T>, load_vec<T, 8>(x + at.first));
-      return;
-    }
-  }
-  if (WHOLE || at.whole) {
-    r.part[0] = load_vec<T, 4>(x + at.first);
-    r.part[1] = load_vec<T, 4>(x + at.second);
+  using W = typename Words<4 * sizeof(T)>::type;
+  constexpr int N = sizeof(T);  // words of four elements
+  if (at.joined && sizeof(T) == 2) {
+    const u32x4_any v = *reinterpret_cast<const u32x4_any *>(x + at.first);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = v[i];
+  } else if (WHOLE || at.whole) {
+    const W u = *reinterpret_cast<const W *>(x + at.first), v = *reinterpret_cast<const W *>(x + at.second);
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.w[i] = u[i], r.w[N + i] = v[i];
   } else if (at.owned) {
+    T each[kNormElements];
 #pragma unroll
     for (int e = 0; e < kNormElements; ++e) {
       const int i = element_of(s, halves, l, e);
-      r.part[e / 4].v[e % 4] = i >= 0 ? x[i] : static_cast<T>(0.0f);
+      each[e] = i >= 0 ? x[i] : static_cast<T>(0.0f);
     }
+    __builtin_memcpy(&r, each, sizeof(r));
   }
 }
 template <bool WHOLE, typename T>
 __device__ __forceinline__ void put(T *y, const float (&v)[kNormElements], const Lane &at, const NormPlan &s, bool halves,
                                     int l) {
   if (!at.owned) return;
-  if constexpr (sizeof(T) == 2) {
+  if (at.joined && sizeof(T) == 2) {
     // in one: lines streamed by halves partly leave twice (neighbours, 128 MB of results: 150 MB written, 52 us instead
-    // of 47; gradients 80 instead of 71)
-    if ((WHOLE || at.whole) && at.second == at.first + 4) {
-      store_vec(y + at.first, v);
-      return;
-    }
-  }
-  if (WHOLE || at.whole) {
+    // of 47; gradients 80 instead of 72)
+    if constexpr (sizeof(T) == 2) store_vec(y + at.first, v);
+  } else if (WHOLE || at.whole) {
     const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
     store_vec(y + at.first, lo);
     store_vec(y + at.second, hi);
@@ -165,7 +173,7 @@ __global__ __launch_bounds__(kBlock) void qk_norm_kernel(fftmv_qk_norm_t n, Norm
   float w[kNormElements], dw[kNormElements] = {};
   Raw<float> weights;
 #pragma unroll
-  for (int e = 0; e < kNormElements; ++e) weights.part[e / 4].v[e % 4] = 1.0f;
+  for (int e = 0; e < kNormElements; ++e) weights.w[e] = __float_as_uint(1.0f);
   if (weight) fetch<WHOLE>(weights, weight, at, s, halves, l);
 #pragma unroll
   for (int e = 0; e < kNormElements; ++e) w[e] = weights[e];

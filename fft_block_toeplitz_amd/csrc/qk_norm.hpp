@@ -12,7 +12,7 @@
 // positions along, FP32 would leave two digits of them.
 // 16384 rows of 40 heads of 128 bf16: 55 us, 6.1 TB/s (out of memory 71, a copy's
 // rate); with results through the caches 90. Gradients of as many rows of 32
-// heads: 71 us. 9995 rows of 10 heads of 75 FP32 take 25 us either way, for 12 and
+// heads: 72 us. 9995 rows of 10 heads of 75 FP32 take 25 us either way, for 12 and
 // 19 of bytes: rows that are not aligned, a third of the lanes idle, and the
 // card filled once.
 #pragma once
@@ -34,7 +34,7 @@ constexpr int kNormTurns = 2048;           // cosines a workgroup keeps, and as 
 constexpr int kNormRows = 32;              // rows a workgroup takes at once, at most
 constexpr int kNormUnits = 256;            // heads of rows that it takes at once, about
 // Workgroups that fill the card, four on each CU. (Gradients of 8 x 2048 rows of
-// 32 heads of 128 bf16: 1024 88 us, 2048 96, 512 122.)
+// 32 heads of 128 bf16, before later steps: 1024 88 us, 2048 96, 512 122.)
 constexpr int kNormWide = 1024;
 
 // How the elements of a head lie on the lanes. Apart: first the rotated pairs,
