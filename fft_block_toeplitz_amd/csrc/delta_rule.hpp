@@ -693,14 +693,14 @@ __device__ __forceinline__ f32x4 load_column(const fftmv_heads_t &f, int64_t b, 
 
 // ------------------------------------------------------- runs one after another
 // The chains (of states, and of their gradients) go through a sequence's runs.
-// Only K S, T (..) and K^T U of a run wait for the run before: four waves, the
+// Only K S, T (..) and K^T (..) X of a run wait for the run before: four waves, the
 // front, do those, 16 value columns each with the state in registers; four more,
 // one on each SIMD beside a front wave, do all else: they bring the next run's
 // rows and triangles from memory to LDS and make the outputs from what the front
-// leaves there, operands of the state at a run's start and of U in its middle. A
+// leaves there, operands of the state at a run's start and of X in its middle. A
 // run has two halves between barriers:
-//   front  R = V - e^G K S, U = T R     | S' = e^{G_last} S + K^T (..) U
-//   back   Q S; the next run's loads    | Y = .. + P U; the next run into LDS
+//   front  R = V - e^G K S, X = T R     | S' = e^{G_last} S + K^T (..) X
+//   back   Q S; the next run's loads    | Y = .. + P diag(b) X; the next run into LDS
 // The back waves' half with the loads' way to LDS bounds a run (4.1 us at 128 keys, of which
 // the front's products in line take 2.9), where states are kept also memory. (8 x 2048
 // steps of 16 heads of 128 x 128 in bf16, 210 us with the states and errors kept, took 235

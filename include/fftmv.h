@@ -522,8 +522,9 @@ typedef struct fftmv_heads_s {
  * workspace: fftmv_delta_rule_sizes bytes, 16-byte aligned, any contents; calls
  * that may run at the same time need their own. States and sums are FP32. A
  * value that is not finite makes results of its head not finite from the first
- * step of its run on until the sequence ends; it reaches no other sequence and no
- * head with other queries and keys.
+ * step of its run on until the sequence ends, and gradients through all of the
+ * sequence; it reaches no other sequence, and other heads by the gradients of
+ * queries and keys that they share alone.
  * Errors: FFTMV_ERR_INVALID_ARG (a null or misaligned pointer, a size < 1 --
  * steps may be 0 --, an unknown type/decay/rate, key_heads that do not divide
  * heads, both lengths and offsets, a workspace that is too small);
