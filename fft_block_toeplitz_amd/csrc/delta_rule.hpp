@@ -590,10 +590,13 @@ __device__ __forceinline__ void invert(float *a, int lane) {
 }
 
 // ------------------------------------------------------ tiles of keys in LDS
-// Rows of kRun steps, KEYS elements from `from` on (zeros behind the last), parts
-// one behind the other; 16 bytes between rows keep them off each other's banks.
-template <int KEYS>
-constexpr int kTileRow = KEYS + 8;
+// Rows of kRun steps, KEYS elements each, parts one behind the other. The bytes
+// between rows keep off each other's banks both eight rows read by 16 bytes
+// (tile_rows) and four by 8 (tile_columns): 16 of them do the former alone at 128 keys,
+// 48 all but in pairs; more parts leave no room for that. (The maps of 65536 steps of 8
+// heads of 128 x 128 bf16 381 and 366 us, outputs 262 either way.)
+template <int KEYS, int NP>
+constexpr int kTileRow = KEYS + (KEYS == 128 && NP == 1 ? 24 : 8);
 
 // Operand with index row 16 m + lane % 16 and slots of elements 32 s + 8 g ...
 template <int KEYS, int NP>
@@ -601,7 +604,7 @@ __device__ __forceinline__ Cut<NP> tile_rows(const uint16_t *tile, int m, int s,
   Cut<NP> c;
 #pragma unroll
   for (int p = 0; p < NP; ++p)
-    c.p[p] = *reinterpret_cast<const u32x4 *>(tile + (p * kRun + 16 * m + lane % 16) * kTileRow<KEYS> + 32 * s + 8 * (lane / 16));
+    c.p[p] = *reinterpret_cast<const u32x4 *>(tile + (p * kRun + 16 * m + lane % 16) * kTileRow<KEYS, NP> + 32 * s + 8 * (lane / 16));
   return c;
 }
 template <int KEYS, int NP>
@@ -631,8 +634,8 @@ __device__ __forceinline__ Cut<NP> tile_columns(const uint16_t *tile, int t, int
   const int l = lane % 16, row = 32 * s + 4 * (lane / 16) + l / 4, col = key_of(t, l % 4, 0);
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
-    const uint16_t *q = tile + (p * kRun + row) * kTileRow<KEYS> + col;
-    c.p[p] = join8(transposed4(q), transposed4(q + 16 * kTileRow<KEYS>));
+    const uint16_t *q = tile + (p * kRun + row) * kTileRow<KEYS, NP> + col;
+    c.p[p] = join8(transposed4(q), transposed4(q + 16 * kTileRow<KEYS, NP>));
   }
   return c;
 }
@@ -718,7 +721,7 @@ constexpr int kValueRow = kValues + 16 / sizeof(T);
 template <typename T, int KEYS, int FRAGS, int BUFFERS>
 struct ChainLds {
   static constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32;
-  alignas(16) uint16_t k[BUFFERS][NP * kRun * kTileRow<KEYS>];
+  alignas(16) uint16_t k[BUFFERS][NP * kRun * kTileRow<KEYS, NP>];
   alignas(16) T v[kRun * kValueRow<T>];
   alignas(16) u32x4 frags[FRAGS * kWave];
   alignas(16) float into[kRun], out[kRun], rate[kRun];
@@ -741,7 +744,7 @@ __device__ __forceinline__ void put_rows(Raw8<T> (&k)[KEYS / 32], int thread, ui
     const auto parts = cut_raw<T>(k[i]);
 #pragma unroll
     for (int p = 0; p < kParts<T>; ++p)
-      *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * kTileRow<KEYS> + c) = parts.p[p];
+      *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * kTileRow<KEYS, kParts<T>> + c) = parts.p[p];
   }
 }
 

@@ -29,7 +29,7 @@ namespace fftmv {
 // 0.8 GB, half of them the gradients and Z that it leaves.)
 template <typename T, int KEYS, int BUFFERS, bool TILE>
 struct BackwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
-  alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS> : 8];  // queries of the back waves' run
+  alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS, kParts<T>> : 8];  // queries of the back waves' run
   alignas(16) f32x4 z[kFrontWaves][kTiles][kWave];                       // P^T dY of the front's
   alignas(16) f32x4 d[kFrontWaves][KEYS / 16][kWave];                    // Q^T (..) dY
 };
@@ -287,9 +287,9 @@ __device__ __forceinline__ float across_groups(float v) {
 // QUERIES: a tile of their own for the queries, where it fits.
 template <typename T, int KEYS, bool QUERIES>
 struct GradsLds {
-  static constexpr int NP = kParts<T>, NO = kOut<T>, VR = kTileRow<kValues>;
-  alignas(16) uint16_t k[NP * kRun * kTileRow<KEYS>];  // keys, and without a tile of their own at the end queries
-  alignas(16) uint16_t q[QUERIES ? NP * kRun * kTileRow<KEYS> : 8];
+  static constexpr int NP = kParts<T>, NO = kOut<T>, VR = kTileRow<kValues, kParts<T>>;
+  alignas(16) uint16_t k[NP * kRun * kTileRow<KEYS, NP>];  // keys, and without a tile of their own at the end queries
+  alignas(16) uint16_t q[QUERIES ? NP * kRun * kTileRow<KEYS, NP> : 8];
   union {
     struct {
       alignas(16) uint16_t u[NO * kRun * VR], z[NO * kRun * VR], dy[NP * kRun * VR];
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
     fftmv_delta_rule_t r, DeltaWorkspace w) {
   constexpr bool QUERIES = grads_queries<T, KEYS, SHARED>();
   using Lds = GradsLds<T, KEYS, QUERIES>;
-  constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32, VR = Lds::VR, KR = kTileRow<KEYS>;
+  constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32, VR = Lds::VR, KR = kTileRow<KEYS, NP>;
   constexpr bool LATE = grads_twice<T, KEYS, SHARED>() && (KEYS == 128 || SHARED);  // what the other workgroup hides need not be held
   constexpr int KT = KEYS / 16, MT = kTiles * KT / kGradWaves;  // tiles of keys, and of steps for one of them a wave
   __shared__ Lds lds;
@@ -357,7 +357,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
       if (!WHOLE || from + 8 * C > rows.width) settle<WHOLE>(v, from + c, rows.width, t < n);
       const auto parts = cut_raw<T>(v);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * (8 * C + 8) + c) = parts.p[p];
+      for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * kTileRow<8 * C, NP> + c) = parts.p[p];
     }
   };
 

@@ -10,7 +10,7 @@ namespace fftmv {
 
 template <typename T, int KEYS, int FRAGS, int BUFFERS, bool TILE>
 struct ForwardLds : ChainLds<T, KEYS, FRAGS, BUFFERS> {
-  alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS> : 8];
+  alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS, kParts<T>> : 8];
   static constexpr int NO = kOut<T>, S = KEYS / 32;
   alignas(16) u32x4 s[kFrontWaves][S][NO][kWave];  // the state at the run's start, cut
   alignas(16) f32x4 u[kFrontWaves][kTiles][kWave];  // X
