@@ -714,6 +714,7 @@ constexpr int kFrontThreads = kFrontWaves * kWave;
 constexpr int kChainThreads = 2 * kFrontThreads;
 constexpr int kValues = 16 * kFrontWaves;  // value columns of a workgroup
 constexpr int kLdsBytes = 160 << 10;
+constexpr int kCus = 256;
 
 template <typename T>
 constexpr int kValueRow = kValues + 16 / sizeof(T);
@@ -1067,15 +1068,50 @@ inline bool delta_whole(const fftmv_delta_rule_t &r, const fftmv_heads_t &valued
 }
 // A part of a sequence, in its steps.
 struct Part {
-  int64_t sequence;  // sequence and head
   int part, begin, end;
   __device__ __forceinline__ Part(const DeltaCuts &cuts, int64_t index, int len)
-      : sequence(index / cuts.parts), part(static_cast<int>(index % cuts.parts)) {
+      : part(static_cast<int>(index % cuts.parts)) {
     const int64_t each = static_cast<int64_t>(cuts.runs) * kRun;
     begin = static_cast<int>(min(part * each, static_cast<int64_t>(len)));
     end = static_cast<int>(part == cuts.parts - 1 ? len : min((part + 1) * each, static_cast<int64_t>(len)));
   }
 };
+
+// Which chain (a part of a sequence, one head) and block of columns a workgroup has,
+// from a grid of all of them in one row. Blocks of a chain share its rows of keys and
+// triangles: they follow each other on one XCD (workgroup i runs on XCD i % 8).
+struct ChainPlace {
+  int64_t chain;
+  int block;
+  __device__ __forceinline__ ChainPlace(int64_t count, int columns) {  // a grid's workgroups are counted in 32 bits
+    const uint32_t chains = static_cast<uint32_t>(count), blocks = static_cast<uint32_t>(columns), i = blockIdx.x;
+    const uint32_t whole = chains / kXcds * kXcds, width = i < whole * blocks ? kXcds : chains % kXcds;  // the last few chains
+    const uint32_t j = i < whole * blocks ? i : i - whole * blocks, row = j / width;
+    chain = (i < whole * blocks ? row / blocks * kXcds : whole) + (j - row * width);
+    block = static_cast<int>(row % blocks);
+  }
+};
+// The sequence of a place, longest first, so that none of the long ones begins when
+// the others end. `lens`: kChainThreads + 1 words of LDS. More sequences than threads,
+// sequences in parts and those that all run at once keep their order. (45 packed
+// sequences of 30011 steps, 16 heads of 64 x 128 fp16: 260 us, in their order 350, with a
+// chain's blocks far apart too 385.)
+__device__ __forceinline__ int64_t longest_first(const fftmv_delta_rule_t &r, const DeltaCuts &cuts, int64_t place, int *lens) {
+  if (!(r.offsets || r.lengths) || r.batch > kChainThreads || cuts.parts > 1 || gridDim.x <= kCus) return place;
+  const int me = threadIdx.x, n = static_cast<int>(r.batch);
+  if (me < n) lens[me] = span_of(r, me).len;
+  __syncthreads();
+  if (me < n) {
+    const int mine = lens[me];
+    int rank = 0;
+    for (int i = 0; i < n; ++i) rank += lens[i] > mine || (lens[i] == mine && i < me);
+    if (rank == place) lens[kChainThreads] = me;
+  }
+  __syncthreads();
+  const int b = __builtin_amdgcn_readfirstlane(lens[kChainThreads]);
+  __syncthreads();
+  return b;
+}
 
 // The states in front of the parts (backward: the gradients of those behind
 // them) one after another. A workgroup has 16 value columns and a wave 16 keys of

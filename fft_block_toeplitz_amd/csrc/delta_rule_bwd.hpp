@@ -48,16 +48,18 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
   auto again = [&]() __attribute__((always_inline)) {
     thread = afresh(thread), lane = thread % kWave, x = lane % 16, g = lane / 16;
   };
-  const int64_t sequence = blockIdx.x / w.cuts.parts, head = sequence % r.heads, b = sequence / r.heads;
-  const int64_t key_head = head / (r.heads / r.key_heads);
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
   // maps: blocks of value columns, then blocks of unit gradients without dY
-  const int value_blocks = (values + kValues - 1) / kValues;
-  const bool units = MAPS && static_cast<int>(blockIdx.y) >= value_blocks;
-  const int first_col = (blockIdx.y - (units ? value_blocks : 0)) * kValues, col = first_col + wave * 16 + x;
+  const int value_blocks = (values + kValues - 1) / kValues, unit_blocks = MAPS ? (keys + kValues - 1) / kValues : 0;
+  const ChainPlace place(r.batch * r.heads * w.cuts.parts, value_blocks + unit_blocks);
+  const uint32_t heads = static_cast<uint32_t>(r.heads), of_all = static_cast<uint32_t>(place.chain) / w.cuts.parts;
+  const int64_t head = of_all % heads, b = longest_first(r, w.cuts, of_all / heads, reinterpret_cast<int *>(&lds));
+  const int64_t sequence = b * r.heads + head, key_head = head / (heads / static_cast<uint32_t>(r.key_heads));
+  const bool units = MAPS && place.block >= value_blocks;
+  const int first_col = (place.block - (units ? value_blocks : 0)) * kValues, col = first_col + wave * 16 + x;
   const bool inside = col < (units ? keys : values);
   const Span span = span_of(r, b);
-  const Part part(w.cuts, blockIdx.x, span.len);
+  const Part part(w.cuts, place.chain, span.len);
   if (MAPS ? part.part == 0 || part.begin >= span.len : part.part > 0 && part.begin >= span.len) return;
   const int64_t states = r.keys * r.values;
   const int last = part.end > part.begin ? (part.end - 1) / kRun * kRun : part.begin - kRun;
@@ -74,7 +76,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
         if constexpr (MAPS) {
           grad[t][i] = units && key == col ? 1.0f : 0.0f;
         } else {
-          const float *from = part.end < span.len ? w.starts + blockIdx.x * states : r.dh_last ? r.dh_last + sequence * states : nullptr;
+          const float *from = part.end < span.len ? w.starts + place.chain * states : r.dh_last ? r.dh_last + sequence * states : nullptr;
           if (from && inside && key < keys) grad[t][i] = from[static_cast<int64_t>(key) * values + col];
         }
       }
@@ -133,7 +135,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
       __syncthreads();
     }
     if constexpr (MAPS)
-      keep(w.maps + static_cast<int64_t>(blockIdx.x) * keys * (keys + values) + (units ? values : 0), keys + values);
+      keep(w.maps + place.chain * keys * (keys + values) + (units ? values : 0), keys + values);
     else if (r.dh0 && part.part == 0)
       keep(r.dh0 + sequence * states, values);
   } else {
@@ -732,14 +734,14 @@ hipError_t launch_delta_backward(const fftmv_delta_rule_t &r, hipStream_t s) {
       constexpr bool WHOLE = decltype(whole)::value != 0;
       const unsigned chains = static_cast<unsigned>(sequences * w.cuts.parts), columns = static_cast<unsigned>(blocks);
       if (w.cuts.parts > 1) {
-        const dim3 all(chains, static_cast<unsigned>(blocks + units));
+        const unsigned all = chains * static_cast<unsigned>(blocks + units);
         delta_back_chain_kernel<T, KEYS, WHOLE, true><<<all, kChainThreads, 0, s>>>(r, w);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
         delta_join_kernel<T, KEYS, true>
             <<<dim3(static_cast<unsigned>(sequences), static_cast<unsigned>((r.values + 15) / 16)), KEYS / 16 * kWave, 0, s>>>(r, w);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
       }
-      delta_back_chain_kernel<T, KEYS, WHOLE, false><<<dim3(chains, columns), kChainThreads, 0, s>>>(r, w);
+      delta_back_chain_kernel<T, KEYS, WHOLE, false><<<chains * columns, kChainThreads, 0, s>>>(r, w);
       return hipGetLastError();
     });
     if (e != hipSuccess) return e;

@@ -221,3 +221,36 @@ def test_queries_and_keys_of_one_memory(fm):
     same = fm.delta_rule(x[1], x[1], x[1], *x[3:])
     copies = fm.delta_rule(x[1].clone(), x[1].clone(), x[1].clone(), *x[3:])
     assert torch.equal(same[0], copies[0]) and torch.equal(same[1], copies[1])
+
+
+@pytest.mark.parametrize("B,packed", [(130, False), (129, True), (600, False), (530, True)])
+def test_many_ragged_sequences(fm, B, packed):
+    """More chains than run at once, lengths of all kinds: each sequence as in a call of a few, whatever its place."""
+    gen = generator(B)
+    lengths = torch.randint(0, 200, (B,), generator=gen, device="cuda", dtype=torch.int32)
+    lengths[:4] = torch.tensor([0, 200, 1, 64], dtype=torch.int32)
+    lengths[7] = lengths[8]
+    x = fields(14, (B, 200), 1, 2, 16, 72, "bf16")
+    dy = torch.randn((B, 200, 2, 72), generator=gen, device="cuda").bfloat16()
+    h0, dl = (torch.randn((B, 2, 16, 72), generator=gen, device="cuda") for _ in range(2))
+    hold = torch.arange(200, device="cuda")[None] < lengths[:, None]
+
+    def run(pick):
+        n = lengths[pick].contiguous()
+        if packed:
+            how = {"offsets": torch.cat([n[:1] * 0, n.cumsum(0).to(torch.int32)])}
+            a = [t[pick][hold[pick]] for t in (*x, dy)]
+        else:
+            how, a = {"lengths": n}, [t[pick].contiguous() for t in (*x, dy)]
+        y, last, carries = fm.delta_rule(*a[:5], h0[pick].contiguous(), save=True, **how)
+        *grads, dh0 = fm.delta_rule_backward(a[5], *a[:5], carries, h0[pick].contiguous(), dl[pick].contiguous(), **how)
+        rows = [y, *grads] if packed else [t[hold[pick]] for t in (y, *grads)]
+        ends = n.cumsum(0).tolist()
+        return [[t[e - int(m):e] for e, m in zip(ends, n)] for t in rows] + [list(last), list(dh0)]
+
+    everything = run(torch.arange(B, device="cuda"))
+    backwards = run(torch.arange(B - 1, -1, -1, device="cuda"))
+    few = run(torch.arange(9, device="cuda"))
+    for a, b, c in zip(everything, backwards, few):
+        assert all(torch.equal(s, t) for s, t in zip(a, reversed(b)))
+        assert all(torch.equal(s, t) for s, t in zip(a[:9], c))
