@@ -782,9 +782,11 @@ __device__ __forceinline__ void clear_rows(const fftmv_delta_rule_t &r, const ff
 // decay is computed once for both: four waves have three or two tiles each. Rows
 // lie in LDS as they are in memory: products of 16-bit elements are exact in
 // FP32, FP32 ones are cut where they are read. Memory bounds it: a run of 128 keys
-// in 16 bits reads 32 KB and leaves 31 to 37 (8 x 2048 steps of 16 heads: 67 us forward, 73
-// backward, 3.9 TB/s; one wave a run, with the rows in registers, took 72 and 80, and
-// 20 instead of 12 for 4 runs of 20 heads in FP32, where the latency of one counts).
+// in 16 bits reads 32 KB and leaves 31 to 37 (8 x 2048 steps of 16 heads: 67 us
+// forward, 73 backward, 3.9 TB/s). One wave a run, with the rows in registers, took 72
+// and 80, and 20 instead of 12 for 4 runs of 20 heads in FP32, where the latency of one
+// counts. Heads that share keys follow each other: 30011 packed fp16 steps of 16 heads, 8
+// of keys, 91 us instead of 96.
 template <typename T, int KEYS>
 struct FactorLds {
   static constexpr int ROW = KEYS + 16 / sizeof(T);
@@ -795,6 +797,20 @@ struct FactorLds {
   };
   double total[kRun];
   float rates[kRun];
+};
+
+// Workgroups that read the same rows follow each other on one XCD (workgroup i runs on
+// XCD i % 8), which has them in its cache: `sharing` of them for each of `count` units,
+// from a grid of all of them in one row.
+struct Place {
+  uint32_t unit, which;
+  __device__ __forceinline__ Place(int64_t units, int sharing) {  // a grid's workgroups are counted in 32 bits
+    const uint32_t count = static_cast<uint32_t>(units), each = static_cast<uint32_t>(sharing), i = blockIdx.x;
+    const uint32_t whole = count / kXcds * kXcds, width = i < whole * each ? kXcds : count % kXcds;  // the last few units
+    const uint32_t j = i < whole * each ? i : i - whole * each, row = j / width;
+    unit = (i < whole * each ? row / each * kXcds : whole) + (j - row * width);
+    which = row % each;
+  }
 };
 
 // Fragment i of a wave: three of six tiles' worth to the first two waves, two to the others.
@@ -838,14 +854,16 @@ __global__ __launch_bounds__(kFrontThreads) void delta_factors_kernel(fftmv_delt
   using Tri = Triangles<T, BACK>;
   __shared__ Lds lds;
   const int thread = threadIdx.x, lane = thread % kWave, wave = thread / kWave, x = lane % 16, g = lane / 16;
-  const int64_t slot = blockIdx.x / r.heads, head = blockIdx.x % r.heads, at = slot * r.heads + head;
-  const int64_t key_head = head / (r.heads / r.key_heads);
+  const uint32_t key_heads = static_cast<uint32_t>(r.key_heads), share = static_cast<uint32_t>(r.heads) / key_heads;
+  const Place place(gridDim.x / share, share);
+  const int64_t slot = place.unit / key_heads, key_head = place.unit % key_heads, head = key_head * share + place.which;
+  const int64_t at = slot * r.heads + head;
   const Slot where = slot_of(r, slot);
   if constexpr (BACK) {
     clear_rows<T>(r, r.dv, slot, where.b, where.first, head, static_cast<int>(r.values));
     clear_rows<T>(r, r.dgate, slot, where.b, where.first, head, 1);
     clear_rows<T>(r, r.dbeta, slot, where.b, where.first, head, 1);
-    if (head % (r.heads / r.key_heads) == 0) {
+    if (place.which == 0) {
       clear_rows<T>(r, r.dq, slot, where.b, where.first, key_head, static_cast<int>(r.keys));
       clear_rows<T>(r, r.dk, slot, where.b, where.first, key_head, static_cast<int>(r.keys));
     }
@@ -1077,20 +1095,6 @@ struct Part {
   }
 };
 
-// Which chain (a part of a sequence, one head) and block of columns a workgroup has,
-// from a grid of all of them in one row. Blocks of a chain share its rows of keys and
-// triangles: they follow each other on one XCD (workgroup i runs on XCD i % 8).
-struct ChainPlace {
-  int64_t chain;
-  int block;
-  __device__ __forceinline__ ChainPlace(int64_t count, int columns) {  // a grid's workgroups are counted in 32 bits
-    const uint32_t chains = static_cast<uint32_t>(count), blocks = static_cast<uint32_t>(columns), i = blockIdx.x;
-    const uint32_t whole = chains / kXcds * kXcds, width = i < whole * blocks ? kXcds : chains % kXcds;  // the last few chains
-    const uint32_t j = i < whole * blocks ? i : i - whole * blocks, row = j / width;
-    chain = (i < whole * blocks ? row / blocks * kXcds : whole) + (j - row * width);
-    block = static_cast<int>(row % blocks);
-  }
-};
 // The sequence of a place, longest first, so that none of the long ones begins when
 // the others end. `lens`: kChainThreads + 1 words of LDS. More sequences than threads,
 // sequences in parts and those that all run at once keep their order. (45 packed

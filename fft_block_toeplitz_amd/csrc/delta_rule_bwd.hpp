@@ -51,15 +51,15 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
   // maps: blocks of value columns, then blocks of unit gradients without dY
   const int value_blocks = (values + kValues - 1) / kValues, unit_blocks = MAPS ? (keys + kValues - 1) / kValues : 0;
-  const ChainPlace place(r.batch * r.heads * w.cuts.parts, value_blocks + unit_blocks);
-  const uint32_t heads = static_cast<uint32_t>(r.heads), of_all = static_cast<uint32_t>(place.chain) / w.cuts.parts;
+  const Place place(r.batch * r.heads * w.cuts.parts, value_blocks + unit_blocks);
+  const uint32_t heads = static_cast<uint32_t>(r.heads), of_all = place.unit / w.cuts.parts;
   const int64_t head = of_all % heads, b = longest_first(r, w.cuts, of_all / heads, reinterpret_cast<int *>(&lds));
   const int64_t sequence = b * r.heads + head, key_head = head / (heads / static_cast<uint32_t>(r.key_heads));
-  const bool units = MAPS && place.block >= value_blocks;
-  const int first_col = (place.block - (units ? value_blocks : 0)) * kValues, col = first_col + wave * 16 + x;
+  const bool units = MAPS && static_cast<int>(place.which) >= value_blocks;
+  const int first_col = (static_cast<int>(place.which) - (units ? value_blocks : 0)) * kValues, col = first_col + wave * 16 + x;
   const bool inside = col < (units ? keys : values);
   const Span span = span_of(r, b);
-  const Part part(w.cuts, place.chain, span.len);
+  const Part part(w.cuts, place.unit, span.len);
   if (MAPS ? part.part == 0 || part.begin >= span.len : part.part > 0 && part.begin >= span.len) return;
   const int64_t states = r.keys * r.values;
   const int last = part.end > part.begin ? (part.end - 1) / kRun * kRun : part.begin - kRun;
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
         if constexpr (MAPS) {
           grad[t][i] = units && key == col ? 1.0f : 0.0f;
         } else {
-          const float *from = part.end < span.len ? w.starts + place.chain * states : r.dh_last ? r.dh_last + sequence * states : nullptr;
+          const float *from = part.end < span.len ? w.starts + place.unit * states : r.dh_last ? r.dh_last + sequence * states : nullptr;
           if (from && inside && key < keys) grad[t][i] = from[static_cast<int64_t>(key) * values + col];
         }
       }
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
       __syncthreads();
     }
     if constexpr (MAPS)
-      keep(w.maps + place.chain * keys * (keys + values) + (units ? values : 0), keys + values);
+      keep(w.maps + static_cast<int64_t>(place.unit) * keys * (keys + values) + (units ? values : 0), keys + values);
     else if (r.dh0 && part.part == 0)
       keep(r.dh0 + sequence * states, values);
   } else {

@@ -41,15 +41,15 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
   // maps: blocks of value columns, then blocks of unit states without values
   const int value_blocks = (values + kValues - 1) / kValues, unit_blocks = USE == kMaps ? (keys + kValues - 1) / kValues : 0;
-  const ChainPlace place(r.batch * r.heads * w.cuts.parts, value_blocks + unit_blocks);
-  const uint32_t heads = static_cast<uint32_t>(r.heads), of_all = static_cast<uint32_t>(place.chain) / w.cuts.parts;
+  const Place place(r.batch * r.heads * w.cuts.parts, value_blocks + unit_blocks);
+  const uint32_t heads = static_cast<uint32_t>(r.heads), of_all = place.unit / w.cuts.parts;
   const int64_t head = of_all % heads, b = longest_first(r, w.cuts, of_all / heads, reinterpret_cast<int *>(&lds));
   const int64_t sequence = b * r.heads + head, key_head = head / (heads / static_cast<uint32_t>(r.key_heads));
-  const bool units = USE == kMaps && place.block >= value_blocks;
-  const int first_col = (place.block - (units ? value_blocks : 0)) * kValues, col = first_col + wave * 16 + x;
+  const bool units = USE == kMaps && static_cast<int>(place.which) >= value_blocks;
+  const int first_col = (static_cast<int>(place.which) - (units ? value_blocks : 0)) * kValues, col = first_col + wave * 16 + x;
   const bool inside = col < (units ? keys : values);
   const Span span = span_of(r, b);
-  const Part part(w.cuts, place.chain, span.len);
+  const Part part(w.cuts, place.unit, span.len);
   if (USE == kMaps ? part.end >= span.len : part.part > 0 && part.begin >= span.len) return;
   const int64_t states = r.keys * r.values;
 
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
         if constexpr (USE == kMaps) {
           state[t][i] = units && key == col ? 1.0f : 0.0f;
         } else {
-          const float *from = part.part ? w.starts + place.chain * states : r.h0 ? r.h0 + sequence * states : nullptr;
+          const float *from = part.part ? w.starts + place.unit * states : r.h0 ? r.h0 + sequence * states : nullptr;
           if (from && inside && key < keys) state[t][i] = from[static_cast<int64_t>(key) * values + col];
         }
       }
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
       __syncthreads();
     }
     if constexpr (USE == kMaps)
-      keep(w.maps + place.chain * keys * (keys + values) + (units ? values : 0), keys + values);
+      keep(w.maps + static_cast<int64_t>(place.unit) * keys * (keys + values) + (units ? values : 0), keys + values);
     else if (r.h_last && part.end >= span.len)
       keep(r.h_last + sequence * states, values);
   } else {
