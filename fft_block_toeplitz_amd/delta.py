@@ -305,16 +305,19 @@ def delta_rule_step(q, k, v, gate, beta, state, slots=None, *, decay="sigmoid", 
 # ---- norms of queries and keys
 def _norm_call(q, k, q_weight, k_weight, norm, eps, frequencies, positions, pairs, lengths):
     """The head of the structure, up to the weights, and the sizes."""
-    torch = _sq._torch
-    if q.dim() not in (3, 4):
-        raise ValueError(f"q must be [batch, steps, heads, elements] or [rows, heads, elements], got {tuple(q.shape)}")
-    Hq, D = q.shape[-2:]
-    B, T = (q.shape[0], q.shape[1]) if q.dim() == 4 else (1, q.shape[0])
-    Hk = 0
+    torch, shape, device = _sq._torch, tuple(q.shape), q.get_device()
+    if len(shape) == 4:
+        B, T, Hq, D = shape
+    elif len(shape) == 3:
+        B, (T, Hq, D) = 1, shape
+    else:
+        raise ValueError(f"q must be [batch, steps, heads, elements] or [rows, heads, elements], got {shape}")
+    rows, Hk = shape[:-2], 0
     if k is not None:
-        if k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != D:
-            raise ValueError(f"q and k must have the same rows and elements: got {tuple(q.shape)} and {tuple(k.shape)}")
-        Hk = k.shape[-2]
+        keyed = tuple(k.shape)
+        if len(keyed) != len(shape) or keyed[:-2] != rows or keyed[-1] != D:
+            raise ValueError(f"q and k must have the same rows and elements: got {shape} and {keyed}")
+        Hk = keyed[-2]
     elif k_weight is not None:
         raise ValueError("k_weight belongs to keys: k is None")
     kinds = _choice(norm, NORMS, "norm"), _choice(pairs, PAIRS, "pairs")
@@ -323,13 +326,13 @@ def _norm_call(q, k, q_weight, k_weight, norm, eps, frequencies, positions, pair
     n = 0
     if frequencies is not None:
         if (frequencies.dtype != torch.float64 or frequencies.dim() != 1 or not frequencies.is_contiguous()
-                or frequencies.get_device() != q.get_device() or frequencies.shape[0] > D // 2):
+                or frequencies.get_device() != device or frequencies.shape[0] > D // 2):
             raise ValueError(f"frequencies must be a contiguous float64 tensor of at most {D // 2} on {q.device}, got "
                              f"{tuple(frequencies.shape)} {frequencies.dtype} on {frequencies.device}")
         n = frequencies.shape[0]
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != q.shape[:-2]
-                                  or not positions.is_contiguous() or positions.get_device() != q.get_device()):
-        raise ValueError(f"positions must be a contiguous int32 tensor {tuple(q.shape[:-2])} on {q.device}, got "
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != rows
+                                  or not positions.is_contiguous() or positions.get_device() != device):
+        raise ValueError(f"positions must be a contiguous int32 tensor {rows} on {q.device}, got "
                          f"{tuple(positions.shape)} {positions.dtype} on {positions.device}")
     lens = _ints(lengths, B, q, "lengths")
     sizes = B, T, Hq, Hk, D, n
