@@ -324,8 +324,8 @@ struct Slot {
 __device__ __forceinline__ Slot slot_of(const fftmv_delta_rule_t &r, int64_t i) {
   const int steps = static_cast<int>(r.steps);
   if (!r.offsets) {
-    const int64_t n = runs_of(steps), b = i / n;
-    return {b, static_cast<int>(i - b * n) * kRun};
+    const uint32_t n = static_cast<uint32_t>(runs_of(steps)), b = static_cast<uint32_t>(i) / n;  // a grid's workgroups
+    return {b, static_cast<int>(i - static_cast<int64_t>(b) * n) * kRun};
   }
   int64_t lo = 0, hi = r.batch - 1;
   while (lo < hi) {

@@ -338,7 +338,8 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
   auto again = [&]() __attribute__((always_inline)) {
     thread = afresh(thread), lane = thread % kWave, x = lane % 16, g = lane / 16;
   };
-  const int64_t slot = blockIdx.x / r.key_heads, key_head = blockIdx.x % r.key_heads;
+  const uint32_t key_heads = static_cast<uint32_t>(r.key_heads);
+  const int64_t slot = blockIdx.x / key_heads, key_head = blockIdx.x % key_heads;
   const Slot where = slot_of(r, slot);
   if (where.first < 0) return;
   const Span span = span_of(r, where.b);
@@ -346,7 +347,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
   if (n <= 0) return;
   const int64_t row = span.row + where.first, states = r.keys * r.values;
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
-  const int share = static_cast<int>(r.heads / r.key_heads);
+  const int share = static_cast<int>(static_cast<uint32_t>(r.heads) / key_heads);
 
   // rows of 8 * CHUNKS elements into a tile
   auto fill = [&](uint16_t *tile, auto chunks, const Rows<T, WHOLE> &rows, int from) __attribute__((always_inline)) {

@@ -23,7 +23,8 @@ __global__ __launch_bounds__(kBlock) void delta_step_kernel(fftmv_delta_rule_ste
   __shared__ float keys_of[KEYS], queries[KEYS];
   __shared__ __align__(16) f32x4 sums[2][WAVES][LANES];
   const int thread = threadIdx.x, lane = thread % kWave, wave = thread / kWave;
-  const int64_t b = blockIdx.x / r.heads, head = blockIdx.x % r.heads, key_head = head / (r.heads / r.key_heads);
+  const uint32_t heads = static_cast<uint32_t>(r.heads), share = heads / static_cast<uint32_t>(r.key_heads);
+  const int64_t b = blockIdx.x / heads, head = blockIdx.x % heads, key_head = blockIdx.x % heads / share;
   const int keys = static_cast<int>(r.keys), values = static_cast<int>(r.values);
   const int col = (blockIdx.y * LANES + thread % LANES) * 4, group = thread / LANES;
   const int most = min(4, values - col);
