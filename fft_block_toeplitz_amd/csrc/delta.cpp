@@ -114,7 +114,7 @@ int fftmv_delta_rule_sizes(int64_t batch, int64_t steps, int64_t key_heads, int6
   }
   const int64_t n = delta_runs(batch, steps, packed != 0);
   if (runs) *runs = n;
-  if (workspace_bytes) *workspace_bytes = delta_workspace(batch, steps, heads, keys, values, dtype, packed != 0, backward != 0);
+  if (workspace_bytes) *workspace_bytes = delta_workspace(batch, steps, heads, keys, values, packed != 0, backward != 0);
   return FFTMV_SUCCESS;
 }
 

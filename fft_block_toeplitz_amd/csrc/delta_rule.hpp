@@ -15,11 +15,15 @@
 //
 // Products go to the bf16 matrix instructions with FP32 sums. An FP32 operand
 // is cut into bf16 parts, the leading 8 bits, the next 8, the last 8: three parts
-// hold all 24 bits. bf16 inputs are one part, fp16 inputs two, both exact. What
-// becomes an FP32 output (the states, gradients of h0) takes all products of
-// parts down to 2^-24; what becomes a 16-bit output, products down to 2^-16,
-// far under that rounding. (An FP32 matrix instruction has a sixteenth of the rate:
-// three parts against one exact operand are 5.3 times as fast, six products 2.7.)
+// hold all 24 bits. bf16 inputs are one part, fp16 inputs two, both exact. All
+// products of parts down to 2^-24 are taken, whatever the outputs' type: a result
+// of 16 bits is then the 32-bit one rounded once, and the gates' gradients, which
+// are differences of sums, have 32-bit sums' digits. (An FP32 matrix instruction has
+// a sixteenth of the rate: three parts against one exact operand are 5.3 times as
+// fast, six products 2.7. Two parts for what becomes 16 bits, three products instead
+// of six, put one value in 135 of bf16 results and one in 20 of fp16 ones on the other
+// side of a rounding, for 744 us instead of 764 at 65536 steps of 8 heads of 128 x 128
+// bf16 and 882 instead of 958 at 8 x 2048 steps of 16 such heads with gradients.)
 //
 // Layouts of a 16x16x32 product in a wave: operands have index lane % 16 and 8
 // slots of the contracted axis, the result column lane % 16 and rows 4 (lane /
@@ -55,15 +59,12 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// bf16 parts of an element, exact; and of an FP32 value next to it: kept down
-// to 2^-24 (kFull) or, for results of 16 bits, 2^-16
+// bf16 parts of an element, exact; and of an FP32 value next to it
 template <typename T>
 constexpr int kParts = sizeof(T) == 4 ? 3 : 1;
 template <>
 inline constexpr int kParts<f16> = 2;
 constexpr int kFull = 3;
-template <typename T>
-constexpr int kOut = sizeof(T) == 4 ? 3 : 2;
 
 // f(Const<0>), ..., f(Const<N - 1>): loops whose numbers choose registers.
 template <int I, int N, typename F>
@@ -348,11 +349,11 @@ struct Factors {
 };
 // Fragments (one part of an operand, 64 lanes x 16 bytes) of T and P diag(b)
 // forward, of P^T and (1 + diag(b) B)^-T backward.
-template <typename T, bool BACK>
+template <bool BACK>
 struct Triangles {
   static constexpr int kT = 0, kTParts = BACK ? 0 : kFull;
-  static constexpr int kP = kT + kFrags * kTParts, kPParts = BACK ? kFull : kOut<T>;
-  static constexpr int kTt = kP + kFrags * kPParts, kTtParts = BACK ? kFull : 0;
+  static constexpr int kP = kT + kFrags * kTParts;  // backward a fragment's parts side by side, forward those of one rank
+  static constexpr int kTt = kP + kFrags * kFull, kTtParts = BACK ? kFull : 0;
   static constexpr int kAll = kTt + kFrags * kTtParts;
 };
 // Fragment of rows tile m and slots 32 s.. of a lower or upper triangle.
@@ -451,17 +452,12 @@ struct DeltaWorkspace {
   float *maps, *starts;
   DeltaCuts cuts;
 };
-inline size_t delta_triangle_bytes(int dtype, bool back) {
-  const size_t per_part = size_t{kFrags} * kWave * sizeof(u32x4);
-  const size_t out = dtype == FFTMV_F32 ? 3 : 2;
-  return per_part * (kFull + (back ? kFull : out));
-}
-inline size_t delta_workspace(int64_t batch, int64_t steps, int64_t heads, int64_t keys, int64_t values, int dtype,
-                              bool packed, bool back, void *at = nullptr, DeltaWorkspace *w = nullptr) {
+inline size_t delta_workspace(int64_t batch, int64_t steps, int64_t heads, int64_t keys, int64_t values, bool packed,
+                              bool back, void *at = nullptr, DeltaWorkspace *w = nullptr) {
   const size_t n = static_cast<size_t>(delta_runs(batch, steps, packed)) * heads;
   const DeltaCuts cuts = delta_cuts(batch, steps, heads, keys, values, packed);
   const size_t parts = cuts.parts > 1 ? static_cast<size_t>(batch) * heads * cuts.parts : 0;
-  const size_t factors = n * sizeof(Factors), triangles = n * delta_triangle_bytes(dtype, back);
+  const size_t factors = n * sizeof(Factors), triangles = n * 2 * kFull * kFrags * kWave * sizeof(u32x4);
   const size_t grads = (back ? n * (keys + kRun) * values * sizeof(float) + 15 : 0) & ~size_t{15};
   const size_t maps = (parts * keys * (keys + values) * sizeof(float) + 15) & ~size_t{15};
   const size_t starts = parts * keys * values * sizeof(float);
@@ -599,13 +595,17 @@ template <int KEYS, int NP>
 constexpr int kTileRow = KEYS + (KEYS == 128 && NP == 1 ? 24 : 8);
 
 // Operand with index row 16 m + lane % 16 and slots of elements 32 s + 8 g ...
-template <int KEYS, int NP>
-__device__ __forceinline__ Cut<NP> tile_rows(const uint16_t *tile, int m, int s, int lane) {
+template <int ROW, int NP>
+__device__ __forceinline__ Cut<NP> plain_rows(const uint16_t *tile, int m, int s, int lane) {
   Cut<NP> c;
 #pragma unroll
   for (int p = 0; p < NP; ++p)
-    c.p[p] = *reinterpret_cast<const u32x4 *>(tile + (p * kRun + 16 * m + lane % 16) * kTileRow<KEYS, NP> + 32 * s + 8 * (lane / 16));
+    c.p[p] = *reinterpret_cast<const u32x4 *>(tile + (p * kRun + 16 * m + lane % 16) * ROW + 32 * s + 8 * (lane / 16));
   return c;
+}
+template <int KEYS, int NP>
+__device__ __forceinline__ Cut<NP> tile_rows(const uint16_t *tile, int m, int s, int lane) {
+  return plain_rows<kTileRow<KEYS, NP>, NP>(tile, m, s, lane);
 }
 template <int KEYS, int NP>
 __device__ __forceinline__ void tile_rows(Cut<NP> (&c)[kTiles], const uint16_t *tile, int s, int lane) {
@@ -721,7 +721,7 @@ constexpr int kValueRow = kValues + 16 / sizeof(T);
 
 template <typename T, int KEYS, int FRAGS, int BUFFERS>
 struct ChainLds {
-  static constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32;
+  static constexpr int NP = kParts<T>, S = KEYS / 32;
   alignas(16) uint16_t k[BUFFERS][NP * kRun * kTileRow<KEYS, NP>];
   alignas(16) T v[kRun * kValueRow<T>];
   alignas(16) u32x4 frags[FRAGS * kWave];
@@ -851,7 +851,7 @@ struct RowOperand {
 template <typename T, int KEYS, bool WHOLE, bool BACK>
 __global__ __launch_bounds__(kFrontThreads) void delta_factors_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
   using Lds = FactorLds<T, KEYS>;
-  using Tri = Triangles<T, BACK>;
+  using Tri = Triangles<BACK>;
   __shared__ Lds lds;
   const int thread = threadIdx.x, lane = thread % kWave, wave = thread / kWave, x = lane % 16, g = lane / 16;
   const uint32_t key_heads = static_cast<uint32_t>(r.key_heads), share = static_cast<uint32_t>(r.heads) / key_heads;
@@ -940,15 +940,15 @@ __global__ __launch_bounds__(kFrontThreads) void delta_factors_kernel(fftmv_delt
       for (int e = 0; e < 4; ++e) {
         const int step = BACK ? first + e : one, past = BACK ? one : first + e;
         const double between = BACK ? lds.total[step] - mine : mine - lds.total[past];
-        const float decay = past <= step ? exp_of<T>(static_cast<float>(between)) : 0.0f;
+        const float decay = past <= step ? expf(static_cast<float>(between)) : 0.0f;
         // A = B diag(b) forward, diag(b) B backward
         p[h][e] = past <= step ? r.scale * (BACK ? 1.0f : lds.rates[past]) * decay * p[h][e] : 0.0f;
         below[i][h][e] = past < step ? lds.rates[BACK ? step : past] * decay * below[i][h][e] : 0.0f;
       }
     }
-    const auto c = cut_tiles<Tri::kPParts>(p[0], p[1]);
+    const auto c = cut_tiles<kFull>(p[0], p[1]);
 #pragma unroll
-    for (int a = 0; a < Tri::kPParts; ++a) out[(Tri::kP + f * Tri::kPParts + a) * kWave + lane] = c.p[a];
+    for (int a = 0; a < kFull; ++a) out[(Tri::kP + (BACK ? f * kFull + a : a * kFrags + f)) * kWave + lane] = c.p[a];
   }
   __syncthreads();
 #pragma unroll

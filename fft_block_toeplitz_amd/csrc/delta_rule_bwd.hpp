@@ -36,7 +36,7 @@ struct BackwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
 
 template <typename T, int KEYS, bool WHOLE, bool MAPS>
 __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
-  using Tri = Triangles<T, true>;
+  using Tri = Triangles<true>;
   constexpr int FRAGS = kFrags * kFull, NP = kParts<T>, S = KEYS / 32;
   constexpr bool TILE = sizeof(BackwardLds<T, KEYS, 1, true>) <= kLdsBytes;
   constexpr int BUFFERS = sizeof(BackwardLds<T, KEYS, 2, TILE>) <= kLdsBytes ? 2 : 1;
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
     auto fetch_own = [&](int first) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < kFrags; ++i)
-        p[i] = load_frag<kFull>(w.triangles + (at(first) * Tri::kAll + Tri::kP) * kWave, i, Tri::kPParts, lane);
+        p[i] = load_frag<kFull>(w.triangles + (at(first) * Tri::kAll + Tri::kP) * kWave, i, kFull, lane);
 #pragma unroll
       for (int m = 0; m < kTiles; ++m) into[m] = *reinterpret_cast<const f32x4 *>(w.factors[at(first)].into + 16 * m + 4 * g);
     };
@@ -257,8 +257,8 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
 // ------------------------------------------------------------ one run's gradients
 // A workgroup has one run of one head of queries and keys, and goes through the
 // heads that share it, so that their gradients add up in registers. Values are
-// taken kValues columns at a time: threads bring eight of a step of U, Z and dY each
-// to LDS, then the waves take products over the values, each for keys (and steps)
+// taken 64 or 32 columns at a time: threads bring eight or four of a step of U, Z and dY
+// each to LDS, then the waves take products over the values, each for keys (and steps)
 // of its own, transposed, so that a lane has four neighbouring keys. What K S
 // and K D would be needed for, the sums over a step's values, comes from Z S^T and U D^T
 // by the step's key: z . S^T k = k . S z. Memory bounds it: states, X, Z and fields of a
@@ -287,17 +287,17 @@ __device__ __forceinline__ float across_groups(float v) {
 }
 
 // QUERIES: a tile of their own for the queries, where it fits.
-template <typename T, int KEYS, bool QUERIES>
+template <typename T, int KEYS, int COLS, bool QUERIES>
 struct GradsLds {
-  static constexpr int NP = kParts<T>, NO = kOut<T>, VR = kTileRow<kValues, kParts<T>>;
-  alignas(16) uint16_t k[NP * kRun * kTileRow<KEYS, NP>];  // keys, and without a tile of their own at the end queries
-  alignas(16) uint16_t q[QUERIES ? NP * kRun * kTileRow<KEYS, NP> : 8];
+  static constexpr int NP = kParts<T>, KR = KEYS + 8, VR = COLS + 8, FR = kRun + 8;  // elements between rows
+  alignas(16) uint16_t k[NP * kRun * KR];  // keys, and without a tile of their own at the end queries
+  alignas(16) uint16_t q[QUERIES ? NP * kRun * KR : 8];
   union {
     struct {
-      alignas(16) uint16_t u[NO * kRun * VR], z[NO * kRun * VR], dy[NP * kRun * VR];
+      alignas(16) uint16_t u[kFull * kRun * VR], z[kFull * kRun * VR], dy[NP * kRun * VR];
     } one;
     struct {
-      alignas(16) uint16_t f[NO * kRun * VR], h[NO * kRun * VR];
+      alignas(16) uint16_t f[kFull * kRun * FR], h[kFull * kRun * FR];
     } two;
   };
   alignas(16) Factors f;
@@ -315,11 +315,16 @@ struct GradsLds {
 // gradients take the registers of 128 keys.)
 template <typename T, int KEYS, bool SHARED>
 constexpr bool grads_twice() {
-  return (!SHARED || KEYS <= 64) && 2 * sizeof(GradsLds<T, KEYS, false>) <= kLdsBytes;
+  return (!SHARED || KEYS <= 64) && 2 * sizeof(GradsLds<T, KEYS, 32, false>) <= kLdsBytes;
+}
+// Value columns at a time: half as many where only that leaves room for a second workgroup.
+template <typename T, int KEYS, bool SHARED>
+constexpr int grads_cols() {
+  return grads_twice<T, KEYS, SHARED>() && 2 * sizeof(GradsLds<T, KEYS, 64, false>) > kLdsBytes ? 32 : 64;
 }
 template <typename T, int KEYS, bool SHARED>
 constexpr bool grads_queries() {
-  return (grads_twice<T, KEYS, SHARED>() ? 2 : 1) * sizeof(GradsLds<T, KEYS, true>) <= kLdsBytes;
+  return (grads_twice<T, KEYS, SHARED>() ? 2 : 1) * sizeof(GradsLds<T, KEYS, grads_cols<T, KEYS, SHARED>(), true>) <= kLdsBytes;
 }
 
 // SHARED: several heads have the same queries and keys.
@@ -327,9 +332,10 @@ template <typename T, int KEYS, bool WHOLE, bool SHARED>
 __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 : 2)) void delta_grads_kernel(
     fftmv_delta_rule_t r, DeltaWorkspace w) {
   constexpr bool QUERIES = grads_queries<T, KEYS, SHARED>();
-  using Lds = GradsLds<T, KEYS, QUERIES>;
-  constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32, VR = Lds::VR, KR = kTileRow<KEYS, NP>;
-  constexpr bool LATE = grads_twice<T, KEYS, SHARED>() && (KEYS == 128 || SHARED);  // what the other workgroup hides need not be held
+  constexpr int COLS = grads_cols<T, KEYS, SHARED>(), PER = COLS / 8;  // of them a thread's
+  using Lds = GradsLds<T, KEYS, COLS, QUERIES>;
+  constexpr int NP = kParts<T>, NO = kFull, S = KEYS / 32, VR = Lds::VR, KR = Lds::KR, FR = Lds::FR;
+  constexpr bool LATE = grads_twice<T, KEYS, SHARED>() && (KEYS == 128 || SHARED || (KEYS == 64 && COLS == 64 && !WHOLE));  // what the other workgroup hides need not be held
   constexpr int KT = KEYS / 16, MT = kTiles * KT / kGradWaves;  // tiles of keys, and of steps for one of them a wave
   __shared__ Lds lds;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -360,7 +366,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
       if (!WHOLE || from + 8 * C > rows.width) settle<WHOLE>(v, from + c, rows.width, t < n);
       const auto parts = cut_raw<T>(v);
 #pragma unroll
-      for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * kTileRow<8 * C, NP> + c) = parts.p[p];
+      for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4 *>(tile + (p * kRun + t) * KR + c) = parts.p[p];
     }
   };
 
@@ -420,13 +426,13 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
       reinterpret_cast<u32x4 *>(&lds.f)[thread] = at_lane(reinterpret_cast<const u32x4 *>(w.factors + at), thread);
     if (QUERIES && head % share == 0) fill(lds.q, Const<KEYS / 8>{}, Rows<T, WHOLE>(r.q, span.batch, row, key_head, n, keys), 0);
     again();
-    const float own_rate = w.factors[at].rate[thread / (kValues / 8)];
+    const float own_rate = w.factors[at].rate[thread / 8];
     float rate_sum = 0.0f;  // z . x of this thread's step and columns
-    for (int from = 0; from < values; from += kValues) {
+    for (int from = 0; from < values; from += COLS) {
       if (from) __syncthreads();
       again();
       // rows of the state and its gradient, for the products with the values; behind the last key zeros
-      u32x4 rows[kValues / 32][2][2];
+      u32x4 rows[COLS / 32][2][2];
       auto fetch_rows_of_states = [&](auto part) __attribute__((always_inline)) {
         constexpr int s = decltype(part)::value;
 #pragma unroll
@@ -437,20 +443,20 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
           rows[s][1][h] = __builtin_amdgcn_raw_buffer_load_b128(grad, byte, 0, 0);
         }
       };
-      {  // a thread has eight columns of one step: U, Z and dY into LDS, dV out
-        const int t = thread / (kValues / 8), at_c = thread % (kValues / 8) * 8, c = from + at_c;
+      {  // a thread has PER columns of one step: U, Z and dY into LDS, dV out; dY by eights
+        const int t = thread / 8, at_c = thread % 8 * PER, c = from + at_c, at_dy = at_c / 8 * 8;
         const int byte = static_cast<int>(states + t * values + c) * 4;
-        u32x4 errors[2], zs_of[2];
+        u32x4 errors[PER / 4], zs_of[PER / 4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < PER / 4; ++h) {
           errors[h] = __builtin_amdgcn_raw_buffer_load_b128(state, byte + 16 * h, 0, 0);
           zs_of[h] = __builtin_amdgcn_raw_buffer_load_b128(grad, byte + 16 * h, 0, 0);
         }
-        Raw8<T> dy = Rows<T, WHOLE>(r.dy, span.batch, row, head, n, values).load(t, c);
-        if constexpr (!LATE) unrolled<0, kValues / 32>(fetch_rows_of_states);
-        float u[8], z[8];
+        Raw8<T> dy = Rows<T, WHOLE>(r.dy, span.batch, row, head, n, values).load(t, from + at_dy);
+        if constexpr (!LATE) unrolled<0, COLS / 32>(fetch_rows_of_states);
+        float u[8] = {}, z[8] = {};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < PER; ++e) {
           const bool in = c + e < values;
           u[e] = in ? __uint_as_float(errors[e / 4][e % 4]) : 0.0f;
           z[e] = in ? __uint_as_float(zs_of[e / 4][e % 4]) : 0.0f;
@@ -458,29 +464,41 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
           u[e] *= own_rate;
         }
         const auto u_parts = cut<NO>(u), z_parts = cut<NO>(z);
-        if (!WHOLE || from + kValues > values) settle<WHOLE>(dy, c, values, t < n);
+        if (!WHOLE || from + COLS > values) settle<WHOLE>(dy, from + at_dy, values, t < n);
         const auto dy_parts = cut_raw<T>(dy);
+        auto put = [&](uint16_t *tile, const u32x4 &part, int p) __attribute__((always_inline)) {
+          uint16_t *to = tile + (p * kRun + t) * VR + at_c;
+          if constexpr (PER == 8) {
+            *reinterpret_cast<u32x4 *>(to) = part;
+          } else {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            *reinterpret_cast<u32x2 *>(to) = u32x2{part[0], part[1]};
+          }
+        };
 #pragma unroll
         for (int p = 0; p < NO; ++p) {
-          *reinterpret_cast<u32x4 *>(lds.one.u + (p * kRun + t) * VR + at_c) = u_parts.p[p];
-          *reinterpret_cast<u32x4 *>(lds.one.z + (p * kRun + t) * VR + at_c) = z_parts.p[p];
-          if (p < NP) *reinterpret_cast<u32x4 *>(lds.one.dy + (p * kRun + t) * VR + at_c) = dy_parts.p[p < NP ? p : 0];
+          put(lds.one.u, u_parts.p[p], p);
+          put(lds.one.z, z_parts.p[p], p);
+        }
+        if (PER == 8 || thread % 2 == 0) {
+#pragma unroll
+          for (int p = 0; p < NP; ++p) *reinterpret_cast<u32x4 *>(lds.one.dy + (p * kRun + t) * VR + at_dy) = dy_parts.p[p];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] *= own_rate;
+        for (int e = 0; e < PER; ++e) z[e] *= own_rate;
         if (t < n) {
           T *to = head_row<T>(r.dv, span.batch, row + t, head) + c;
-          if (c + 8 <= values) {
-            if constexpr (sizeof(T) == 2) {
+          if (c + PER <= values) {
+            if constexpr (sizeof(T) == 2 && PER == 8) {
               store_vec(to, z, false);
             } else {
               const float lo[4] = {z[0], z[1], z[2], z[3]}, hi[4] = {z[4], z[5], z[6], z[7]};
               store_vec(to, lo, false);
-              store_vec(to + 4, hi, false);
+              if constexpr (PER == 8) store_vec(to + 4, hi, false);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < PER; ++e)
               if (c + e < values) to[e] = static_cast<T>(z[e]);
           }
         }
@@ -492,18 +510,18 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
         const int job = wave + kGradWaves * q, tile = job < kGrams ? job : job - kGrams;
         if (job >= 2 * kGrams) break;
 #pragma unroll
-        for (int s = 0; s < kValues / 32; ++s) {
-          const Cut<NO> u = tile_rows<kValues, NO>(lds.one.u, gram_col(tile), s, lane);
+        for (int s = 0; s < COLS / 32; ++s) {
+          const Cut<NO> u = plain_rows<VR, NO>(lds.one.u, gram_col(tile), s, lane);
           if (job < kGrams)
-            multiply<NO>(gram[q], tile_rows<kValues, NP>(lds.one.dy, gram_row(tile), s, lane), u);
+            multiply<NO>(gram[q], plain_rows<VR, NP>(lds.one.dy, gram_row(tile), s, lane), u);
           else
-            multiply<NO>(gram[q], tile_rows<kValues, NO>(lds.one.z, gram_row(tile), s, lane), u);
+            multiply<NO>(gram[q], plain_rows<VR, NO>(lds.one.z, gram_row(tile), s, lane), u);
           if constexpr (KEYS == 128 && SHARED) part_done();
         }
       }
       part_done();
       again();
-      unrolled<0, kValues / 32>([&](auto part) __attribute__((always_inline)) {
+      unrolled<0, COLS / 32>([&](auto part) __attribute__((always_inline)) {
         constexpr int s = decltype(part)::value;
         if constexpr (LATE) fetch_rows_of_states(part);
         const int c = from + 32 * s + 8 * g;
@@ -515,7 +533,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
             b[0][4 * h + e] = __uint_as_float(rows[s][0][h][e]);
             b[1][4 * h + e] = __uint_as_float(rows[s][1][h][e]);
           }
-        if (from + kValues > values) {
+        if (from + COLS > values) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             b[0][e] = c + e < values ? b[0][e] : 0.0f;
@@ -531,14 +549,14 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
         const Cut<NO> sp = cut<NO>(b[0]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          multiply<NO>(yq[m], sp, tile_rows<kValues, NP>(lds.one.dy, tile_m + m, s, lane));
-          multiply<NO>(zs[m], sp, tile_rows<kValues, NO>(lds.one.z, tile_m + m, s, lane));
+          multiply<NO>(yq[m], sp, plain_rows<VR, NP>(lds.one.dy, tile_m + m, s, lane));
+          multiply<NO>(zs[m], sp, plain_rows<VR, NO>(lds.one.z, tile_m + m, s, lane));
           if constexpr (TIGHT) part_done();
         }
         const Cut<NO> dp = cut<NO>(b[1]);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-          multiply<NO>(ud[m], dp, tile_rows<kValues, NO>(lds.one.u, tile_m + m, s, lane));
+          multiply<NO>(ud[m], dp, plain_rows<VR, NO>(lds.one.u, tile_m + m, s, lane));
           if constexpr (TIGHT) part_done();
         }
       });
@@ -568,7 +586,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
     rate_sum += dpp<kDppQuadXor1>(rate_sum);
     rate_sum += dpp<kDppQuadXor2>(rate_sum);
     rate_sum += dpp<kDppRowHalfMirror>(rate_sum);
-    if (thread % (kValues / 8) == 0) lds.rates[thread / (kValues / 8)] = rate_sum;
+    if (thread % 8 == 0) lds.rates[thread / 8] = rate_sum;
     last = across_groups(across16(last));
     if (lane == 0) lds.lasts[wave] = last;
     __syncthreads();  // u, z and dy are done with
@@ -584,7 +602,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
       if (job < kGrams) {
         if constexpr (QUERIES) {
 #pragma unroll
-          for (int s = 0; s < S; ++s) multiply<NO>(raw, tile_rows<KEYS, NP>(lds.q, m, s, lane), tile_rows<KEYS, NP>(lds.k, c, s, lane));
+          for (int s = 0; s < S; ++s) multiply<NO>(raw, plain_rows<KR, NP>(lds.q, m, s, lane), plain_rows<KR, NP>(lds.k, c, s, lane));
         } else {
           const Rows<T, WHOLE> rows(r.q, span.batch, row, key_head, n, keys);
           Raw8<T> own[S];
@@ -593,12 +611,12 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
 #pragma unroll
           for (int s = 0; s < S; ++s) {
             if (!WHOLE || keys < KEYS) settle<WHOLE>(own[s], 32 * s + 8 * g, keys, 16 * m + x < n);
-            multiply<NO>(raw, cut_raw<T>(own[s]), tile_rows<KEYS, NP>(lds.k, c, s, lane));
+            multiply<NO>(raw, cut_raw<T>(own[s]), plain_rows<KR, NP>(lds.k, c, s, lane));
           }
         }
       } else {
 #pragma unroll
-        for (int s = 0; s < S; ++s) multiply<NO>(raw, tile_rows<KEYS, NP>(lds.k, m, s, lane), tile_rows<KEYS, NP>(lds.k, c, s, lane));
+        for (int s = 0; s < S; ++s) multiply<NO>(raw, plain_rows<KR, NP>(lds.k, m, s, lane), plain_rows<KR, NP>(lds.k, c, s, lane));
       }
       uint16_t *to = job < kGrams ? lds.two.f : lds.two.h;
       const double sum_j = lds.f.sum[j];
@@ -607,7 +625,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
       for (int i = 0; i < 4; ++i) {
         const int t = 16 * m + 4 * g + i;
         const bool in = job < kGrams ? j <= t : j < t;
-        const float e = in ? exp_of<T>(static_cast<float>(lds.f.sum[t] - sum_j)) : 0.0f;
+        const float e = in ? expf(static_cast<float>(lds.f.sum[t] - sum_j)) : 0.0f;
         // dG_t: q . dq holds this row of P but for its diagonal, which e^{G_t - G_t} is no factor of
         float v = (job < kGrams ? r.scale : -lds.f.rate[t]) * e * gram[q][i], line;
         if (!in) v = 0.0f;
@@ -623,8 +641,8 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
 #pragma unroll
         for (int a = 0; a < NO; ++a) {
           const __bf16 vb = static_cast<__bf16>(v);
-          to[(a * kRun + t) * VR + j] = __builtin_bit_cast(uint16_t, vb);
-          if (m % 2 == 0 && m == c) to[(a * kRun + t) * VR + j + 16] = 0;  // the tile right of it shares its slots
+          to[(a * kRun + t) * FR + j] = __builtin_bit_cast(uint16_t, vb);
+          if (m % 2 == 0 && m == c) to[(a * kRun + t) * FR + j + 16] = 0;  // the tile right of it shares its slots
           v -= static_cast<float>(vb);
         }
       }
@@ -641,10 +659,10 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (in_lower(tile_m + m, s)) {
-          multiply<NO>(dq[m], k, tile_rows<kValues, NO>(lds.two.f, tile_m + m, s, lane));
-          multiply<NO>(dk[m], k, tile_rows<kValues, NO>(lds.two.h, tile_m + m, s, lane));
+          multiply<NO>(dq[m], k, plain_rows<FR, NO>(lds.two.f, tile_m + m, s, lane));
+          multiply<NO>(dk[m], k, plain_rows<FR, NO>(lds.two.h, tile_m + m, s, lane));
         }
-        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], k, plain_columns<VR, NO>(lds.two.h, 32 * s, 16 * (tile_m + m), lane));
+        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], k, plain_columns<FR, NO>(lds.two.h, 32 * s, 16 * (tile_m + m), lane));
       }
     }
     if constexpr (!QUERIES) {
@@ -658,7 +676,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
       const Cut<NP> q = plain_columns<KR, NP>(queries, 32 * s, 16 * tile_k, lane);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
-        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], q, plain_columns<VR, NO>(lds.two.f, 32 * s, 16 * (tile_m + m), lane));
+        if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], q, plain_columns<FR, NO>(lds.two.f, 32 * s, 16 * (tile_m + m), lane));
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {  // q . dq: step 16 m + x, four keys
@@ -716,7 +734,7 @@ template <typename T>
 hipError_t launch_delta_backward(const fftmv_delta_rule_t &r, hipStream_t s) {
   const int64_t runs = delta_runs(r.batch, r.steps, r.offsets != nullptr), sequences = r.batch * r.heads;
   DeltaWorkspace w;
-  delta_workspace(r.batch, r.steps, r.heads, r.keys, r.values, r.dtype, r.offsets != nullptr, true, r.workspace, &w);
+  delta_workspace(r.batch, r.steps, r.heads, r.keys, r.values, r.offsets != nullptr, true, r.workspace, &w);
   const int64_t blocks = (r.values + kValues - 1) / kValues, units = (r.keys + kValues - 1) / kValues;
   if (!grid_fits(runs * r.heads, kFrontThreads) || !grid_fits(sequences * ((r.values + 15) / 16), 512) || !grid_fits(runs * r.key_heads, kGradThreads) ||
       !grid_fits(sequences * w.cuts.parts * (blocks + units), kChainThreads))

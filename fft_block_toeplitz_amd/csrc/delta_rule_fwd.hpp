@@ -8,12 +8,31 @@
 
 namespace fftmv {
 
-template <typename T, int KEYS, int FRAGS, int BUFFERS, bool TILE>
+// The state at a run's start goes to the back waves in parts, as the front waves need
+// it, or (!PARTS) in FP32, two thirds of the bytes, to be cut there again.
+template <typename T, int KEYS, int FRAGS, int BUFFERS, bool TILE, bool PARTS>
 struct ForwardLds : ChainLds<T, KEYS, FRAGS, BUFFERS> {
   alignas(16) uint16_t q[TILE ? kParts<T> * kRun * kTileRow<KEYS, kParts<T>> : 8];
-  static constexpr int NO = kOut<T>, S = KEYS / 32;
-  alignas(16) u32x4 s[kFrontWaves][S][NO][kWave];  // the state at the run's start, cut
+  static constexpr int S = KEYS / 32;
+  alignas(16) u32x4 s[kFrontWaves][S][PARTS ? kFull : 2][kWave];
   alignas(16) f32x4 u[kFrontWaves][kTiles][kWave];  // X
+};
+
+// What a chain has in LDS, the first that fits: queries (not in three parts), P's
+// parts as T's (of 16-bit elements; two of three where the third does not fit), two
+// buffers of keys, the state in parts.
+template <typename T, int KEYS, bool MAPS>
+struct ForwardPlan {
+  template <int P, int BUFFERS, bool TILE, bool PARTS>
+  static constexpr bool fits() {
+    return sizeof(ForwardLds<T, KEYS, kFrags * (kFull + P), BUFFERS, TILE, PARTS>) <= kLdsBytes;
+  }
+  static constexpr bool HALF = sizeof(T) == 2;
+  static constexpr int P = MAPS || !HALF ? 0 : fits<kFull, 1, true, false>() ? kFull : kFull - 1;
+  static constexpr bool TILE = fits<P, 1, true, false>();
+  static constexpr int BUFFERS = fits<P, 2, TILE, false>() ? 2 : 1;
+  static constexpr bool PARTS = fits<P, BUFFERS, TILE, true>();
+  using Lds = ForwardLds<T, KEYS, kFrags * (kFull + P), BUFFERS, TILE, PARTS>;
 };
 
 // What a chain is for: the outputs, also with the states kept for the backward pass, or the maps of parts.
@@ -21,17 +40,11 @@ enum ChainUse { kOutputs, kCarries, kMaps };
 
 template <typename T, int KEYS, bool WHOLE, int USE>
 __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_rule_t r, DeltaWorkspace w) {
-  using Tri = Triangles<T, false>;
-  constexpr int NP = kParts<T>, NO = kOut<T>, S = KEYS / 32;
-  // P of 16-bit elements goes through LDS as T does: each wave for itself from memory, four times the loads, made one
-  // sequence of 65536 steps (8 heads of 128 x 128 bf16) 276 us instead of 262. The parts of FP32 ones do not fit
-  constexpr bool PTILE = USE != kMaps && sizeof(T) == 2;
-  constexpr int FRAGS = kFrags * (PTILE ? kFull + NO : kFull);
-  // else queries go from memory to registers (the same sequence 329 us, packed FP16 ones 461 instead of 385)
-  constexpr bool TILE = sizeof(ForwardLds<T, KEYS, FRAGS, 1, true>) <= kLdsBytes;
-  constexpr int BUFFERS = sizeof(ForwardLds<T, KEYS, FRAGS, 2, TILE>) <= kLdsBytes ? 2 : 1;
-  using Lds = ForwardLds<T, KEYS, FRAGS, BUFFERS, TILE>;
-  __shared__ Lds lds;
+  using Tri = Triangles<false>;
+  using Plan = ForwardPlan<T, KEYS, USE == kMaps>;
+  constexpr int NP = kParts<T>, S = KEYS / 32, P = Plan::P, FRAGS = kFrags * (kFull + P), BUFFERS = Plan::BUFFERS;
+  constexpr bool TILE = Plan::TILE;
+  __shared__ typename Plan::Lds lds;
   const int side = __builtin_amdgcn_readfirstlane(threadIdx.x / kFrontThreads);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % kFrontWaves;
   int thread = threadIdx.x % kFrontThreads, lane = threadIdx.x % kWave, x = lane % 16, g = lane / 16;
@@ -82,9 +95,14 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
 #pragma unroll
       for (int s = 0; s < S; ++s) {
         cuts[s] = cut_tiles<kFull>(state[2 * s], state[2 * s + 1]);
+        if constexpr (USE == kMaps) continue;
+        if constexpr (Plan::PARTS) {
 #pragma unroll
-        for (int p = 0; p < NO; ++p)
-          if constexpr (USE != kMaps) lds.s[wave][s][p][lane] = cuts[s].p[p];
+          for (int p = 0; p < kFull; ++p) lds.s[wave][s][p][lane] = cuts[s].p[p];
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) lds.s[wave][s][h][lane] = __builtin_bit_cast(u32x4, state[2 * s + h]);
+        }
       }
     };
     leave_state();
@@ -134,8 +152,9 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
   } else {
     Fetched<T, KEYS, FRAGS, WHOLE> next;
     Raw8<T> own[KEYS / 32];       // queries, with a tile
-    QueryRows<T, KEYS, WHOLE> q;  // without a tile
-    Cut<NO> p[kFrags];
+    // without a tile (65536 steps of 8 heads of 128 x 128 bf16 that way 329 us instead of 262, packed FP16 ones 461 and 385)
+    QueryRows<T, KEYS, WHOLE> q;
+    Cut<kFull> p[kFrags];
     constexpr int HOLD = QueryRows<T, KEYS, WHOLE>::HOLD;
     auto at = [&](int first) __attribute__((always_inline)) { return (span.run + first / kRun) * r.heads + head; };
     auto steps = [&](int first) __attribute__((always_inline)) { return min(kRun, span.len - first); };
@@ -160,13 +179,13 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
       if constexpr (TILE && USE != kMaps) put_rows<T, KEYS, WHOLE>(own, thread, lds.q, keys, steps(first));
     };
     auto fetch_triangle = [&](int first) __attribute__((always_inline)) {
+      // from LDS as far as P is there. Each wave for itself from memory, four times the loads, made one sequence of
+      // 65536 steps (8 heads of 128 x 128 bf16) 276 us instead of 262; FP32 elements leave no room
+      const u32x4 *far = w.triangles + at(first) * Tri::kAll * kWave;
 #pragma unroll
-      for (int i = 0; i < kFrags; ++i) {
-        if constexpr (PTILE)
-          p[i] = load_frag<NO>(lds.frags + Tri::kP * kWave, i, Tri::kPParts, lane);
-        else
-          p[i] = load_frag<NO>(w.triangles + (at(first) * Tri::kAll + Tri::kP) * kWave, i, Tri::kPParts, lane);
-      }
+      for (int a = 0; a < kFull; ++a)
+#pragma unroll
+        for (int i = 0; i < kFrags; ++i) p[i].p[a] = at_lane((a < P ? lds.frags : far) + (Tri::kP + a * kFrags + i) * kWave, lane);
     };
     auto fetch_queries = [&](int first, auto s) __attribute__((always_inline)) {
       q.template fetch<decltype(s)::value>(r.q, keys, span.batch, span.row + first, steps(first), key_head, lane);
@@ -189,9 +208,13 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
       if constexpr (USE != kMaps) {
         unrolled<0, S>([&](auto i) __attribute__((always_inline)) {
           constexpr int s = decltype(i)::value;
-          Cut<NO> part;
+          Cut<kFull> part;
+          if constexpr (Plan::PARTS) {
 #pragma unroll
-          for (int p = 0; p < NO; ++p) part.p[p] = lds.s[wave][s][p][lane];
+            for (int p = 0; p < kFull; ++p) part.p[p] = lds.s[wave][s][p][lane];
+          } else {
+            part = cut_tiles<kFull>(__builtin_bit_cast(f32x4, lds.s[wave][s][0][lane]), __builtin_bit_cast(f32x4, lds.s[wave][s][1][lane]));
+          }
           Cut<NP> rows[kTiles];
           if constexpr (TILE) {
             tile_rows<KEYS>(rows, lds.q, s, lane);
@@ -200,7 +223,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
             for (int m = 0; m < kTiles; ++m) rows[m] = q.template operand<s>(m, keys, n, lane);
             if constexpr (s + HOLD < S) fetch_queries(first, Const<s + HOLD>{});
           }
-          multiply_rows_t<NO>(y, rows, part);  // steps along the lanes
+          multiply_rows_t<kFull>(y, rows, part);  // steps along the lanes
           if constexpr (!TILE) part_done();
         });
         fetch_triangle(first);  // only now: registers
@@ -220,7 +243,7 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
             for (int i = 0; i < 4; ++i)
               if (inside) to[static_cast<int64_t>(16 * m + 4 * g + i) * values + col] = u[m][i];
         }
-        multiply_triangle<NO, false, true>(y, p, cut_tiles<NO>(u[0], u[1]), cut_tiles<NO>(u[2], u[3]));
+        multiply_triangle<kFull, false, true>(y, p, cut_tiles<kFull>(u[0], u[1]), cut_tiles<kFull>(u[2], u[3]));
         if constexpr (!TILE) fetch_first_queries(then);
         const int c = first_col + 16 * wave + 4 * g;
         T *to = head_row<T>(r.y, span.batch, span.row + first, head);
@@ -256,7 +279,7 @@ template <typename T>
 hipError_t launch_delta_forward(const fftmv_delta_rule_t &r, hipStream_t s) {
   const int64_t runs = delta_runs(r.batch, r.steps, r.offsets != nullptr), sequences = r.batch * r.heads;
   DeltaWorkspace w;
-  delta_workspace(r.batch, r.steps, r.heads, r.keys, r.values, r.dtype, r.offsets != nullptr, false, r.workspace, &w);
+  delta_workspace(r.batch, r.steps, r.heads, r.keys, r.values, r.offsets != nullptr, false, r.workspace, &w);
   const int64_t blocks = (r.values + kValues - 1) / kValues, units = (r.keys + kValues - 1) / kValues;
   if (!grid_fits(runs * r.heads, kFrontThreads) || !grid_fits(sequences * ((r.values + 15) / 16), 512) || !grid_fits(sequences * w.cuts.parts * (blocks + units), kChainThreads))
     return hipErrorInvalidConfiguration;
