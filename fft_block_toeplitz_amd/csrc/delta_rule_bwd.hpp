@@ -303,8 +303,7 @@ struct GradsLds {
   alignas(16) Factors f;
   float sums[KEYS / 16][kRun];  // what of dG goes through the states, of each 16 keys
   float rates[kRun];            // z . x
-  double turned[kRun];          // q . dq over the heads that dq holds
-  float turns[KEYS / 16][kRun]; // q . dq, of each 16 keys
+  float turns[KEYS / 16][kRun]; // q . dq of this head, of each 16 keys
   float lasts[kGradWaves];      // what the last step's G has beside
   float gram_rows[2 * kGrams][16], gram_cols[2 * kGrams][16];
 };
@@ -370,7 +369,8 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
     }
   };
 
-  // FP32 gradients of shared queries and keys add up in the outputs, others, which would round there, in registers
+  // FP32 gradients of shared queries and keys add up in the outputs, others, which would round there, in registers. A
+  // head's part of dq is whole before it joins them: its q . dq goes into this head's gates alone
   constexpr bool KEEP = SHARED && sizeof(T) == 2;
   f32x4 dq[MT], dk[MT];
   auto clear = [&]() __attribute__((always_inline)) {
@@ -378,7 +378,6 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
     for (int m = 0; m < MT; ++m) dq[m] = dk[m] = f32x4{0, 0, 0, 0};
   };
   clear();
-  if (thread < kRun) lds.turned[thread] = 0.0;
   auto store_gradients = [&](bool add) __attribute__((always_inline)) {
     again();
 #pragma unroll
@@ -414,7 +413,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
     const int64_t each = states + kRun * r.values;
     const auto state = __builtin_amdgcn_make_buffer_rsrc(r.carries + at * each, 0, static_cast<int>(each * 4), kBufferFlags);
     const auto grad = __builtin_amdgcn_make_buffer_rsrc(w.grads + at * each, 0, static_cast<int>(each * 4), kBufferFlags);
-    f32x4 gram[kGradJobs], yq[MT], zs[MT], ud[MT];  // the triangles' tiles; dY S^T, Z S^T and U D^T, transposed
+    f32x4 gram[kGradJobs], yq[MT], zs[MT], ud[MT];  // the triangles' tiles; dY S^T (then dQ), Z S^T and U D^T, transposed
 #pragma unroll
     for (int m = 0; m < MT; ++m) yq[m] = zs[m] = ud[m] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -566,7 +565,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
     for (int m = 0; m < MT; ++m) {  // a step's factors are a lane's here
       const int t = 16 * (tile_m + m) + x;
       const f32x4 o = ud[m] * lds.f.out[t], i = zs[m] * (lds.f.rate[t] * lds.f.into[t]);
-      dq[m] += yq[m] * (r.scale * lds.f.into[t]);
+      yq[m] *= r.scale * lds.f.into[t];
       dk[m] += o - i;
       float ends = 0.0f, sum = 0.0f;  // k . o, k . i
 #pragma unroll
@@ -659,7 +658,7 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (in_lower(tile_m + m, s)) {
-          multiply<NO>(dq[m], k, plain_rows<FR, NO>(lds.two.f, tile_m + m, s, lane));
+          multiply<NO>(yq[m], k, plain_rows<FR, NO>(lds.two.f, tile_m + m, s, lane));
           multiply<NO>(dk[m], k, plain_rows<FR, NO>(lds.two.h, tile_m + m, s, lane));
         }
         if (in_upper(tile_m + m, s)) multiply<NO>(dk[m], k, plain_columns<FR, NO>(lds.two.h, 32 * s, 16 * (tile_m + m), lane));
@@ -686,21 +685,18 @@ __global__ __launch_bounds__(kGradThreads, (grads_twice<T, KEYS, SHARED>() ? 4 :
       for (int part = 0; part < NP; ++part) {
         const uint16_t *q = queries + (part * kRun + t) * KR + 16 * tile_k + 4 * g;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum = fmaf(dq[m][i], __uint_as_float(static_cast<uint32_t>(q[i]) << 16), sum);
+        for (int i = 0; i < 4; ++i) sum = fmaf(yq[m][i], __uint_as_float(static_cast<uint32_t>(q[i]) << 16), sum);
       }
+      dq[m] += yq[m];
       sum = across_groups(sum);
       if (g == 0) lds.turns[tile_k][t] = sum;
     }
     __syncthreads();
     again();
     if (wave == 0) {  // the gates: lane i has step i
-      double turned = 0.0, end = 0.0;
+      double own = 0.0, end = 0.0;
 #pragma unroll
-      for (int v = 0; v < KT; ++v) turned += lds.turns[v][lane];
-      double own = KEEP ? turned - lds.turned[lane] : turned;
-      if constexpr (KEEP) lds.turned[lane] = turned;
-#pragma unroll
-      for (int v = 0; v < KT; ++v) own -= lds.sums[v][lane];
+      for (int v = 0; v < KT; ++v) own += static_cast<double>(lds.turns[v][lane]) - lds.sums[v][lane];
 #pragma unroll
       for (int v = 0; v < kGradWaves; ++v) end += lds.lasts[v];
 #pragma unroll

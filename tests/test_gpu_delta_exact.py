@@ -85,3 +85,49 @@ def test_gradients_of_gates_far_apart(fm, dtype, Hk, H, K, V):
         for h in range(H):
             wrong = E.gates_off(got["dgate"][b, :, h], want[b]["dgate"][:, h], want[b]["size"][:, h], DT[dtype])
             assert not wrong, f"sequence {b}, head {h}: {wrong}"
+
+
+@pytest.mark.parametrize("dtype,small", [("bf16", -20), ("fp16", -10), ("fp32", -20)])
+@pytest.mark.parametrize("K,V", [(24, 40), (64, 64), (128, 72)])
+def test_gradients_of_gates_beside_a_larger_head(fm, dtype, small, K, V):
+    """A head whose outputs count far less than those of the head in front of it, with the same queries and keys: the
+    larger one's roundings stay out of its gates' gradients, in either order."""
+    for first in (True, False):
+        def change(q, k, v, gate, beta, dy, dlast):
+            one, rest = (slice(0, 1), slice(1, 3)) if first else (slice(2, 3), slice(0, 2))
+            for t, heads in ((dy, 2), (dlast, 1)):
+                t.movedim(heads, 0)[rest] *= 2.0 ** small
+                t.movedim(heads, 0)[one] *= 8.0
+
+        got, want = call(fm, 34, 1, 150, 1, 3, K, V, dtype, change=change)
+        for h in range(3):
+            wrong = E.gates_off(got["dgate"][0, :, h], want[0]["dgate"][:, h], want[0]["size"][:, h], DT[dtype])
+            assert not wrong, f"head {h}: {wrong}"
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("K,V", [(32, 72), (64, 64), (128, 40)])
+def test_not_finite_in_any_head_of_a_group(fm, bad, dtype, K, V):
+    """One value that is not finite, in each head of a group in turn: the others' values, gates and rates keep their
+    gradients' bits."""
+    x = fields(35, (2, 200), 2, 6, K, V, dtype)
+    dy = torch.randn((2, 200, 6, V), generator=generator(36), device="cuda").to(DT[dtype])
+    y, last, carries = fm.delta_rule(*x, save=True)
+    grads = fm.delta_rule_backward(dy, *x, carries)
+    for head in (0, 1, 2, 4):
+        for t in (x[2], dy):
+            kept = t[1, 130, head, 5].clone()
+            t[1, 130, head, 5] = bad
+            y2, last2, carries2 = fm.delta_rule(*x, save=True)
+            grads2 = fm.delta_rule_backward(dy, *x, carries2)
+            t[1, 130, head, 5] = kept
+            rest = [h for h in range(6) if h != head]
+            assert not torch.isfinite(grads2[3][1, :, head]).all()
+            for a, b in ((y2, y), *zip(grads2[2:5], grads[2:5])):
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1, :, rest], b[1, :, rest])
+            for a, b in ((last2, last), (grads2[5], grads[5])):
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1, rest], b[1, rest])
+            for a, b in zip(grads2[:2], grads[:2]):
+                group = head // 3
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1, :, 1 - group], b[1, :, 1 - group])
