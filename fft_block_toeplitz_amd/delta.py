@@ -23,8 +23,8 @@ import struct
 
 from . import lib
 from . import sequence as _sq
-from .sequence import _check, _choice, _current_stream, _dtype_of, _elsewhere, _floats, _ints, _no_out, _output, \
-    _wants_grad, _wrote
+from .sequence import _check, _choice, _current_stream, _dtype_of, _elsewhere, _floats, _ints, _no_out, _no_tangents, \
+    _output, _wants_grad, _wrote
 
 FFTMV_DELTA_RUN = 64
 FFTMV_DELTA_KEYS, FFTMV_DELTA_VALUES, FFTMV_QK_NORM_DIM = 128, 1024, 512
@@ -199,6 +199,7 @@ def delta_rule(q, k, v, gate, beta, h0=None, *, decay="sigmoid", rate="sigmoid",
         return _elsewhere(stream, delta_rule, q, k, v, gate, beta, h0, decay=decay, rate=rate, scale=scale,
                           lengths=lengths, offsets=offsets, save=save, out=out)
     dtype = _dtype_of(v, "v")
+    _no_tangents(q, k, v, gate, beta, h0, out)
     if not save and _wants_grad(q, k, v, gate, beta, h0, out):
         from . import layers
 
@@ -236,6 +237,7 @@ def delta_rule_backward(dy, q, k, v, gate, beta, carries, h0=None, dh_last=None,
         return _elsewhere(stream, delta_rule_backward, dy, q, k, v, gate, beta, carries, h0, dh_last, decay=decay,
                           rate=rate, scale=scale, lengths=lengths, offsets=offsets)
     dtype = _dtype_of(v, "v")
+    _no_tangents(dy, q, k, v, gate, beta, carries, h0, dh_last)
     torch = _sq._torch
     B, T, Hk, H, K, V = _shapes(q, k, v, gate, beta, offsets, lengths)
     kinds = _choice(decay, DECAYS, "decay"), _choice(rate, RATES, "rate")
@@ -271,6 +273,7 @@ def delta_rule_step(q, k, v, gate, beta, state, slots=None, *, decay="sigmoid", 
         return _elsewhere(stream, delta_rule_step, q, k, v, gate, beta, state, slots, decay=decay, rate=rate,
                           scale=scale, out=out)
     dtype = _dtype_of(v, "v")
+    _no_tangents(q, k, v, gate, beta, state, out)
     if _wants_grad(q, k, v, gate, beta, state, out):
         raise ValueError("a step in place has no gradient: call it under torch.no_grad(), or delta_rule on whole series")
     B, _, Hk, H, K, V = _shapes(q, k, v, gate, beta, None, None, step=True)
@@ -373,6 +376,7 @@ def qk_norm(q, k=None, q_weight=None, k_weight=None, *, norm="rms", eps=1e-6, fr
                           positions=positions, pairs=pairs, lengths=lengths)
     _dtype_of(q, "q")
     _same_type(q, k)
+    _no_tangents(q, k, q_weight, k_weight)
     if _wants_grad(q, k, q_weight, k_weight):
         from . import layers
 
@@ -397,6 +401,7 @@ def qk_norm_backward(dqy, dky, q, k=None, q_weight=None, k_weight=None, *, norm=
                           frequencies=frequencies, positions=positions, pairs=pairs, lengths=lengths)
     _dtype_of(q, "q")
     _same_type(q, k)
+    _no_tangents(dqy, dky, q, k, q_weight, k_weight)
     torch = _sq._torch
     head, sizes = _norm_call(q, k, q_weight, k_weight, norm, eps, frequencies, positions, pairs, lengths)
     dqf = _elements(dqy, q.shape, q, "dqy")

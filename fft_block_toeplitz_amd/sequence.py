@@ -14,8 +14,8 @@ memory and streams. Elements are float32, bfloat16 or float16; states,
 statistics and parameters are float32. ``recurrence`` and ``group_norm`` of
 tensors that require a gradient go through the differentiable forms in
 ``layers``; with ``save=True`` they are the first half of a gradient taken by
-hand, and their results carry none. There is no fallback: without the built
-library every call raises.
+hand, and their results carry none. Forward-mode derivatives are refused.
+There is no fallback: without the built library every call raises.
 """
 
 from __future__ import annotations
@@ -214,6 +214,15 @@ def _wants_grad(*tensors):
     return False
 
 
+def _no_tangents(*tensors):
+    """Forward-mode derivatives are refused: a kernel takes a dual tensor by its address, and would drop its tangent."""
+    forward = _torch.autograd.forward_ad
+    if forward._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward.unpack_dual(t).tangent is not None:
+                raise ValueError("there is no forward-mode derivative: take a backward one, or forward_ad.unpack_dual(x).primal")
+
+
 def _no_out(out):
     if out is not None:
         raise ValueError("out= takes results without a gradient: call under torch.no_grad() or detach the inputs")
@@ -352,6 +361,7 @@ def recurrence(x, gate, h0=None, *, decay="sigmoid", drive="complement", lengths
         return _elsewhere(stream, recurrence, x, gate, h0, decay=decay, drive=drive, lengths=lengths, offsets=offsets,
                           save=save, out=out)
     dtype = _dtype_of(x, "x")
+    _no_tangents(x, gate, h0, out)
     if not save and _wants_grad(x, gate, h0, out):
         from . import layers
 
@@ -392,6 +402,7 @@ def recurrence_backward(dh, x, gate, carries, h0=None, dh_last=None, *, decay="s
         return _elsewhere(stream, recurrence_backward, dh, x, gate, carries, h0, dh_last, decay=decay, drive=drive,
                           lengths=lengths, offsets=offsets)
     dtype = _dtype_of(x, "x")
+    _no_tangents(dh, x, gate, carries, h0, dh_last)
     B, T, C = _sequences(x, lengths, offsets)
     kinds = _choice(decay, DECAYS, "decay"), _choice(drive, DRIVES, "drive")
     shape = x.shape
@@ -428,6 +439,7 @@ def recurrence_step(x, gate, state, slots=None, *, decay="sigmoid", drive="compl
     if stream is not None:
         return _elsewhere(stream, recurrence_step, x, gate, state, slots, decay=decay, drive=drive, out=out)
     dtype = _dtype_of(x, "x")
+    _no_tangents(x, gate, state, out)
     if _wants_grad(x, gate, state, out):
         raise ValueError("a step in place has no gradient: call it under torch.no_grad(), or recurrence on whole series")
     shape = x.shape
@@ -500,6 +512,7 @@ def group_norm(x, groups, weight=None, bias=None, *, eps=1e-5, activation=None, 
         return _elsewhere(stream, group_norm, x, groups, weight, bias, eps=eps, activation=activation, lengths=lengths,
                           save=save, out=out)
     dtype = _dtype_of(x, "x")
+    _no_tangents(x, weight, bias, out)
     if not save and _wants_grad(x, weight, bias, out):
         from . import layers
 
@@ -536,6 +549,7 @@ def group_norm_backward(dy, x, stats, groups, weight=None, bias=None, *, activat
         return _elsewhere(stream, group_norm_backward, dy, x, stats, groups, weight, bias, activation=activation,
                           lengths=lengths)
     dtype = _dtype_of(x, "x")
+    _no_tangents(dy, x, stats, weight, bias)
     v = _samples(x)
     N, S, C = shape = v.shape
     if not isinstance(groups, int) or groups < 1 or C < 1 or C % groups:

@@ -1,0 +1,58 @@
+"""Calls of the sequence operators' torch forms that are refused, or answered, whatever the sizes: tangents of
+forward-mode differentiation."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from torch.autograd import forward_ad  # noqa: E402
+
+from test_gpu_delta import fields  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fm():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import fft_block_toeplitz_amd as fm
+
+    fm.lib()
+    return fm
+
+
+def calls(fm):
+    """(call, its arguments) of every entry point, small."""
+    q, k, v, gate, beta = fields(1, (2, 10), 2, 4, 16, 8, "fp32")
+    state, w = torch.zeros((2, 4, 16, 8), device="cuda"), torch.ones(16, device="cuda")
+    y, _, carries = fm.delta_rule(q, k, v, gate, beta, state, save=True)
+    x, g, h = v.flatten(2), v.flatten(2) + 1.0, torch.zeros((2, 32), device="cuda")
+    hy, _, kept = fm.recurrence(x, g, h, save=True)
+    z, stats = fm.group_norm(x, 4, save=True)
+    one = torch.ones(32, device="cuda")
+    return [
+        (fm.delta_rule, dict(q=q, k=k, v=v, gate=gate, beta=beta, h0=state)),
+        (lambda **a: fm.delta_rule(save=True, **a), dict(q=q, k=k, v=v, gate=gate, beta=beta, h0=state)),
+        (fm.delta_rule_backward, dict(dy=y, q=q, k=k, v=v, gate=gate, beta=beta, carries=carries, h0=state, dh_last=state)),
+        (fm.delta_rule_step, dict(q=q[:, 0], k=k[:, 0], v=v[:, 0], gate=gate[:, 0], beta=beta[:, 0], state=state.clone())),
+        (fm.qk_norm, dict(q=q, k=k, q_weight=w, k_weight=w)),
+        (fm.qk_norm_backward, dict(dqy=q, dky=k, q=q, k=k, q_weight=w, k_weight=w)),
+        (fm.recurrence, dict(x=x, gate=g, h0=h)),
+        (fm.recurrence_backward, dict(dh=hy, x=x, gate=g, carries=kept, h0=h, dh_last=h)),
+        (fm.recurrence_step, dict(x=x[:, 0], gate=g[:, 0], state=h.clone())),
+        (lambda **a: fm.group_norm(groups=4, **a), dict(x=x, weight=one, bias=one)),
+        (lambda **a: fm.group_norm_backward(groups=4, **a), dict(dy=z, x=x, stats=stats, weight=one, bias=one)),
+    ]
+
+
+def test_tangents_are_refused(fm):
+    """Each tensor of each call as a dual one, under no_grad too; without one, a level changes nothing."""
+    for call, args in calls(fm):
+        with forward_ad.dual_level():
+            call(**args)
+            for name, t in args.items():
+                dual = forward_ad.make_dual(t, torch.ones_like(t))
+                with pytest.raises(ValueError, match="forward-mode"):
+                    call(**{**args, name: dual})
+                with torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):
+                    call(**{**args, name: dual})
