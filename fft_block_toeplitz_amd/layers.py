@@ -195,11 +195,24 @@ class DeltaLayer(nn.Module):
         self.skip = nn.Linear(inputs, outputs, bias=False, device=device)
         self.weight = nn.Parameter(torch.ones(heads * values, device=device))
         self.bias = nn.Parameter(torch.zeros(heads * values, device=device))
-        # a plain attribute: moving the layer to another type leaves the frequencies as they are
-        self.frequencies = None if base is None else base ** (
-            -2.0 / keys * torch.arange(keys // 2, dtype=torch.float64, device=device))
+        self.base = base
+        self.frequencies = self._frequencies(device)
         with torch.no_grad():  # memories from a few steps to a few hundred
             self.into.bias[sum(self.parts[:3]):sum(self.parts[:4])] = torch.linspace(1.0, 6.0, heads, device=device)
+
+    def _frequencies(self, device):
+        if self.base is None:
+            return None
+        return self.base ** (-2.0 / self.keys * torch.arange(self.keys // 2, dtype=torch.float64, device=device))
+
+    def _apply(self, fn, recurse=True):
+        """Moves the layer. The frequencies are no buffer, which another type or ``to_empty`` would spoil: they are
+        made again on the device that the parameters came to."""
+        super()._apply(fn, recurse)
+        device = self.into.weight.device
+        if self.base is not None and self.frequencies.device != device:
+            self.frequencies = self._frequencies(device)
+        return self
 
     def _fields(self, x, positions, lengths=None):
         q, k, v, gate, beta = self.into(x).split(self.parts, -1)

@@ -1,5 +1,5 @@
-"""Calls of the sequence operators' torch forms that are refused, or answered, whatever the sizes: tangents of
-forward-mode differentiation."""
+"""Calls of the sequence operators' torch forms and layers that are refused, or answered, whatever the sizes: tangents of
+forward-mode differentiation, layers moved between devices."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -56,3 +56,19 @@ def test_tangents_are_refused(fm):
                     call(**{**args, name: dual})
                 with torch.no_grad(), pytest.raises(ValueError, match="forward-mode"):
                     call(**{**args, name: dual})
+
+
+def test_layer_moved_to_the_gpu(fm):
+    """Made on the CPU, moved, and moved to another type: what a layer made there gives."""
+    from fft_block_toeplitz_amd.layers import DeltaLayer
+
+    for dtype in (torch.float32, torch.bfloat16):
+        here = DeltaLayer(10, 4, 16, 24, 6, key_heads=2, base=100.0).to(dtype)
+        moved = DeltaLayer(10, 4, 16, 24, 6, key_heads=2, base=100.0, device="cpu").cuda().to(dtype)
+        moved.load_state_dict(here.state_dict())
+        x = torch.randn((3, 20, 10), device="cuda", dtype=dtype)
+        at = torch.full((3,), 5, dtype=torch.int32, device="cuda")
+        with torch.no_grad():
+            (y, last), (y2, last2) = here(x), moved(x)
+            assert torch.equal(last, last2) and torch.equal(y, y2)
+            assert torch.equal(here.step(x[:, 0], last, None, at), moved.step(x[:, 0], last2, None, at))
