@@ -404,6 +404,8 @@ def qk_norm_backward(dqy, dky, q, k=None, q_weight=None, k_weight=None, *, norm=
     _no_tangents(dqy, dky, q, k, q_weight, k_weight)
     torch = _sq._torch
     head, sizes = _norm_call(q, k, q_weight, k_weight, norm, eps, frequencies, positions, pairs, lengths)
+    if dqy is None or (dky is None) != (k is None):
+        raise ValueError("dqy and, with keys, dky must be the gradients of the results: one is missing, or keys are")
     dqf = _elements(dqy, q.shape, q, "dqy")
     dkf = _NONE if k is None else _elements(dky, k.shape, q, "dky")
     dq = _empty(q)

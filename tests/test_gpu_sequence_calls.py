@@ -72,3 +72,11 @@ def test_layer_moved_to_the_gpu(fm):
             (y, last), (y2, last2) = here(x), moved(x)
             assert torch.equal(last, last2) and torch.equal(y, y2)
             assert torch.equal(here.step(x[:, 0], last, None, at), moved.step(x[:, 0], last2, None, at))
+
+
+def test_gradients_of_norms_that_are_missing(fm):
+    q, k = fields(2, (2, 10), 2, 4, 16, 8, "bf16")[:2]
+    for args in ((q, None, q, k), (None, k, q, k), (q, k, q, None), (None, None, q, None)):
+        with pytest.raises(ValueError):
+            fm.qk_norm_backward(*args)
+    assert fm.qk_norm_backward(q, None, q)[1] is None
