@@ -333,14 +333,18 @@ def _norm_call(q, k, q_weight, k_weight, norm, eps, frequencies, positions, pair
             raise ValueError(f"frequencies must be a contiguous float64 tensor of at most {D // 2} on {q.device}, got "
                              f"{tuple(frequencies.shape)} {frequencies.dtype} on {frequencies.device}")
         n = frequencies.shape[0]
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != rows
-                                  or not positions.is_contiguous() or positions.get_device() != device):
-        raise ValueError(f"positions must be a contiguous int32 tensor {rows} on {q.device}, got "
-                         f"{tuple(positions.shape)} {positions.dtype} on {positions.device}")
+    apart = 0  # elements between two sequences' positions
+    if positions is not None:
+        st = positions.stride()
+        if (positions.dtype != torch.int32 or positions.shape != rows or positions.get_device() != device
+                or (st[-1] != 1 and T > 1)):
+            raise ValueError(f"positions must be an int32 tensor {rows} on {q.device} with contiguous steps, got "
+                             f"{tuple(positions.shape)} {positions.dtype}, strides {st}, on {positions.device}")
+        apart = st[0] if len(st) == 2 else 0
     lens = _ints(lengths, B, q, "lengths")
     sizes = B, T, Hq, Hk, D, n
     head = (*sizes, _sq._types[q.dtype], *kinds, eps, lens, frequencies.data_ptr() if n else 0,
-            positions.data_ptr() if positions is not None else 0, T, *_elements(q, q.shape, q, "q"),
+            positions.data_ptr() if positions is not None else 0, apart, *_elements(q, q.shape, q, "q"),
             *(_elements(k, k.shape, q, "k") if k is not None else _NONE), _floats(q_weight, (D,), q, "q_weight"),
             _floats(k_weight, (D,), q, "k_weight"))
     return head, sizes
@@ -365,8 +369,8 @@ def qk_norm(q, k=None, q_weight=None, k_weight=None, *, norm="rms", eps=1e-6, fr
     [elements] or None. ``frequencies``: float64 [n], radians a position, n at
     most half the elements: the first 2 n elements are turned, in ``pairs``
     "halves" (p, p + n) or "neighbours" (2 p, 2 p + 1); None: no rotation.
-    ``positions``: int32 [batch, steps] (or [rows]); None: 0, 1, 2, ... along
-    the steps. ``lengths`` (int32 [batch]): rows from lengths[b] on enter no
+    ``positions``: int32 [batch, steps] (or [rows]) with contiguous steps, as
+    one row expanded over the batch has; None: 0, 1, 2, ... along the steps. ``lengths`` (int32 [batch]): rows from lengths[b] on enter no
     sum whatever they hold, and come back zero.
 
     Returns the normalised q and k (None without), differentiable where an

@@ -80,3 +80,21 @@ def test_gradients_of_norms_that_are_missing(fm):
         with pytest.raises(ValueError):
             fm.qk_norm_backward(*args)
     assert fm.qk_norm_backward(q, None, q)[1] is None
+
+
+def test_positions_of_any_distance(fm):
+    """One row of positions for all sequences, rows apart, a column's single steps: what a contiguous copy gives."""
+    freq = 10.0 ** -torch.arange(4, dtype=torch.float64, device="cuda")
+    pos = torch.randint(0, 1000, (40, 30), dtype=torch.int32, device="cuda")
+    for rows, at in (((3, 10), pos[0, :10].expand(3, 10)), ((3, 10), pos[:3, 5:15]), ((3, 1), pos[:3, 7:8]),
+                     ((1, 10), pos[4:5, :10]), ((10,), pos[4, :10]), ((3, 10), pos[::2][:3, :10])):
+        q, k = fields(3, rows, 2, 2, 16, 8, "fp32")[:2]
+        how, copy = {"frequencies": freq, "positions": at}, {"frequencies": freq, "positions": at.contiguous()}
+        for a, b in zip(fm.qk_norm(q, k, **how), fm.qk_norm(q, k, **copy)):
+            assert torch.equal(a, b)
+        for a, b in zip(fm.qk_norm_backward(q, k, q, k, **how)[:2], fm.qk_norm_backward(q, k, q, k, **copy)[:2]):
+            assert torch.equal(a, b)
+    q = fields(3, (3, 10), 2, 2, 16, 8, "fp32")[0]
+    for at in (pos[:10, :3].T, pos[:3, :20:2], pos[0, :1].expand(3, 10)):
+        with pytest.raises(ValueError):
+            fm.qk_norm(q, frequencies=freq, positions=at)
