@@ -140,13 +140,6 @@ __device__ __forceinline__ float across(float v) {
   return v;
 }
 
-// 1 / sqrt(v): 16-bit elements take the hardware's (1 ulp), FP32 ones two roundings.
-template <typename T>
-__device__ __forceinline__ float inverse_root(float v) {
-  if constexpr (sizeof(T) == 4) return 1.0f / sqrtf(v);
-  return __builtin_amdgcn_rsqf(v);
-}
-
 // A row of a workgroup: where it begins in x, dy and y (dx), in elements, and
 // its position. Rows behind their sequence have nothing to read.
 struct NormRow {
@@ -237,7 +230,7 @@ __global__ __launch_bounds__(kBlock) void qk_norm_kernel(fftmv_qk_norm_t n, Norm
         const float u = at.owned >> e & 1 ? v[e] : 0.0f;
         sum = fmaf(u, u, sum);
       }
-      const float inverse = inverse_root<T>(fmaf(across<LANES>(sum), over, n.eps));
+      const float inverse = 1.0f / sqrtf(fmaf(across<LANES>(sum), over, n.eps));
       float4 cs = {}, sn = {};
       if (s.turned) {
         const int i = (row * s.turns + at.turns) / 4;

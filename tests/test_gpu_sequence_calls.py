@@ -1,5 +1,5 @@
 """Calls of the sequence operators' torch forms and layers that are refused, or answered, whatever the sizes: tangents of
-forward-mode differentiation, layers moved between devices."""
+forward-mode differentiation, layers moved between devices, positions of any distance, tiny rows."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -98,3 +98,19 @@ def test_positions_of_any_distance(fm):
     for at in (pos[:10, :3].T, pos[:3, :20:2], pos[0, :1].expand(3, 10)):
         with pytest.raises(ValueError):
             fm.qk_norm(q, frequencies=freq, positions=at)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+def test_norms_of_tiny_rows(fm, dtype, norm):
+    """Rows whose squares add up to a subnormal number, without an eps: as long as any others. The sum is a multiple of
+    2^-149 and off by 64 halves of it at most, a relative 64 * 2^-150 / 2^-128 at the least sum of them, 2^-16."""
+    x = fields(4, (3, 10), 2, 2, 64, 8, dtype)[0]
+    x = (x.float() * 2.0 ** -63).to(x.dtype)  # rows of 2^-63, squares 2^-126 together and less
+    x[1] *= 0.5
+    x[2] = (x[2].float() * 0.6).to(x.dtype)
+    y = fm.qk_norm(x, norm=norm, eps=0.0)[0].double()
+    wide = x.double()
+    want = wide / (wide.square().mean(-1, keepdim=True) if norm == "rms" else wide.square().sum(-1, keepdim=True)).sqrt()
+    off = float(((y - want).norm(dim=-1) / want.norm(dim=-1)).nan_to_num(float("inf")).max())
+    assert off <= 2.0 ** -16 + (2.0 ** -8 if dtype == "bf16" else 2.0 ** -22)
