@@ -423,8 +423,9 @@ struct DeltaCuts {
 // Times in tenths of a run of the chain, on 256 CUs: a map's run takes 0.8 of one, a joint 1.2, the
 // two more launches 4. (bf16, whole and in parts: one sequence of 65536 steps, 8 heads of
 // 128 x 128 3637 and 747 us; 5 of 1999 steps, 7 heads of 75 x 41 168 and 121; FP32 with gradients,
-// 6 of up to 1000 steps, 4 heads of 64 x 64 255 and 202.) Packed sequences' lengths are on the
-// device: they stay whole.
+// 6 of up to 1000 steps, 4 heads of 64 x 64 255 and 202.) Packed sequences stay whole: places
+// of parts by what the host knows, as runs have them (slot_of), have not been built, and one
+// packed sequence of 65536 steps takes the 3.6 ms.
 inline DeltaCuts delta_cuts(int64_t batch, int64_t steps, int64_t heads, int64_t keys, int64_t values, bool packed) {
   const int64_t runs = (steps + kRun - 1) / kRun, chains = batch * heads;
   DeltaCuts best = {1, static_cast<int>(runs > 0 ? runs : 1)};
@@ -704,11 +705,15 @@ __device__ __forceinline__ f32x4 load_column(const fftmv_heads_t &f, int64_t b, 
 // run has two halves between barriers:
 //   front  R = V - e^G K S, X = T R     | S' = e^{G_last} S + K^T (..) X
 //   back   Q S; the next run's loads    | Y = .. + P diag(b) X; the next run into LDS
-// LDS bounds a run: about 490 KB go through it at 128 keys in 4.1 us, 64 bytes a clock,
-// most of them the rows of keys and the triangles that each wave reads whole (the
-// front's products in line take 2.9 us); where states are kept also memory. (8 x 2048
-// steps of 16 heads of 128 x 128 in bf16, 210 us with the states and errors kept, took 235
-// without the errors and all of it in one wave a SIMD. Loads two runs ahead were slower.)
+// The back waves set the pace of outputs: at 128 bf16 keys, nothing kept, a run takes 4.6
+// us, 8.9 k clocks, of which the front works 5.1 (2.8 and 2.3 in its halves) and waits
+// for the back's 4.7 (the next loads 1.7, Q S 3.0) and 4.3 (P diag(b) X and stores 2.5, the
+// next run into LDS 1.8). The matrix units are busy 38 % of the time and 516 KB go through
+// LDS, 58 bytes a clock of the 107 to 114 that a kernel of reads alone reaches. Maps, which
+// have no outputs, take 2.7 us a run by the front's products in line; where states are kept,
+// memory counts too. (8 x 2048 steps of 16 heads of 128 x 128 in bf16, 210 us with the
+// states and errors kept, took 235 without the errors and all of it in one wave a SIMD,
+// both before third parts: 225 with them. Loads two runs ahead were slower.)
 constexpr int kFrontWaves = 4;
 constexpr int kFrontThreads = kFrontWaves * kWave;
 constexpr int kChainThreads = 2 * kFrontThreads;
@@ -782,11 +787,11 @@ __device__ __forceinline__ void clear_rows(const fftmv_delta_rule_t &r, const ff
 // decay is computed once for both: four waves have three or two tiles each. Rows
 // lie in LDS as they are in memory: products of 16-bit elements are exact in
 // FP32, FP32 ones are cut where they are read. Memory bounds it: a run of 128 keys
-// in 16 bits reads 32 KB and leaves 31 to 37 (8 x 2048 steps of 16 heads: 67 us
-// forward, 73 backward, 3.9 TB/s). One wave a run, with the rows in registers, took 72
-// and 80, and 20 instead of 12 for 4 runs of 20 heads in FP32, where the latency of one
+// in 16 bits reads 32 KB and leaves 37 (8 x 2048 steps of 16 heads: 71 us forward, 74
+// backward, 4.3 TB/s). One wave a run, with the rows in registers, took 8 % longer,
+// and 20 us instead of 12 for 4 runs of 20 heads in FP32, where the latency of one
 // counts. Heads that share keys follow each other: 30011 packed fp16 steps of 16 heads, 8
-// of keys, 91 us instead of 96.
+// of keys, 91 us instead of 96 (107 with P's third parts).
 template <typename T, int KEYS>
 struct FactorLds {
   static constexpr int ROW = KEYS + 16 / sizeof(T);
@@ -1098,8 +1103,8 @@ struct Part {
 // The sequence of a place, longest first, so that none of the long ones begins when
 // the others end. `lens`: kChainThreads + 1 words of LDS. More sequences than threads,
 // sequences in parts and those that all run at once keep their order. (45 packed
-// sequences of 30011 steps, 16 heads of 64 x 128 fp16: 260 us, in their order 350, with a
-// chain's blocks far apart too 385.)
+// sequences of 30011 steps, 16 heads of 64 x 128 fp16: 288 us, in their order 350, with a
+// chain's blocks far apart too 385; 310 with third parts.)
 __device__ __forceinline__ int64_t longest_first(const fftmv_delta_rule_t &r, const DeltaCuts &cuts, int64_t place, int *lens) {
   if (!(r.offsets || r.lengths) || r.batch > kChainThreads || cuts.parts > 1 || gridDim.x <= kCus) return place;
   const int me = threadIdx.x, n = static_cast<int>(r.batch);

@@ -16,7 +16,8 @@
 // Z that the chain left. (Computing X and Z again from the states saves half of the
 // bytes, 64 KB of a run of 128 values, and takes three triangles and K S, K D: 8 x 2048
 // steps of 16 heads of 128 x 128 bf16 in 576 us instead of 437, with the chains 43
-// faster. Without them a run needs half of a CU's LDS, and two go side by side: 323.)
+// faster, all in two parts an operand. Without them a run needs half of a CU's LDS, and
+// two go side by side: 377 us in three parts.)
 #pragma once
 
 #include "delta_rule.hpp"
@@ -25,7 +26,7 @@ namespace fftmv {
 
 // The chain of the states' gradients. P^T dY and (scale diag(e^G) Q)^T dY wait
 // for no other run: the back waves compute them a run ahead of the front, which
-// does K D, T^T (..) and K^T Z. (8 x 2048 steps of 16 heads of 128 x 128 bf16: 260 us, for
+// does K D, T^T (..) and K^T Z. (8 x 2048 steps of 16 heads of 128 x 128 bf16: 258 us, for
 // 0.8 GB, half of them the gradients and Z that it leaves.)
 template <typename T, int KEYS, int BUFFERS, bool TILE>
 struct BackwardLds : ChainLds<T, KEYS, kFrags * kFull, BUFFERS> {
@@ -261,8 +262,9 @@ __global__ __launch_bounds__(kChainThreads) void delta_back_chain_kernel(fftmv_d
 // each to LDS, then the waves take products over the values, each for keys (and steps)
 // of its own, transposed, so that a lane has four neighbouring keys. What K S
 // and K D would be needed for, the sums over a step's values, comes from Z S^T and U D^T
-// by the step's key: z . S^T k = k . S z. Memory bounds it: states, X, Z and fields of a
-// run of 128 x 128 are 290 KB, 1.2 GB for 8 x 2048 steps of 16 heads in 323 us.
+// by the step's key: z . S^T k = k . S z. States, X, Z and fields of a run of 128 x 128 are
+// 290 KB, 1.3 GB for 8 x 2048 steps of 16 heads in 377 us: 3.5 TB/s, with the matrix units
+// busy 24 % of the time and LDS conflicts 18 % (two parts an operand: 321 us).
 constexpr int kGradWaves = 8;
 constexpr int kGradThreads = kGradWaves * kWave;
 constexpr int kGrams = 10;  // 16x16 tiles of a lower triangle of kRun
@@ -309,9 +311,10 @@ struct GradsLds {
 };
 
 // Two workgroups on a CU where LDS and registers hold them: one loads while the
-// other computes. (8 x 2048 steps, 16 heads of 128 x 128 bf16: one 437 us, two
-// 323; 32 heads of 64 x 64 with 8 of queries and keys: 439 and 300. Shared heads'
-// gradients take the registers of 128 keys.)
+// other computes. (8 x 2048 steps, 16 heads of 128 x 128 bf16: one, 64 columns at a time,
+// 488 us, two by 32 columns 407 on the same card; 32 heads of 64 x 64 with 8 of queries
+// and keys: bf16, 64 columns either way, 547 and 358, fp16, two by 32, 546 and 444. Shared
+// heads' gradients take the registers of 128 keys.)
 template <typename T, int KEYS, bool SHARED>
 constexpr bool grads_twice() {
   return (!SHARED || KEYS <= 64) && 2 * sizeof(GradsLds<T, KEYS, 32, false>) <= kLdsBytes;

@@ -18,9 +18,10 @@ struct ForwardLds : ChainLds<T, KEYS, FRAGS, BUFFERS> {
   alignas(16) f32x4 u[kFrontWaves][kTiles][kWave];  // X
 };
 
-// What a chain has in LDS, the first that fits: queries (not in three parts), P's
-// parts as T's (of 16-bit elements; two of three where the third does not fit), two
-// buffers of keys, the state in parts.
+// What a chain has in LDS, in this order as far as it fits: P's parts as T's (of 16-bit
+// elements; two of three where only that leaves room for the queries), queries, two
+// buffers of keys, the state in parts. (65536 steps of 8 heads of 128 x 128 bf16, two buffers
+// and the state in FP32: 767 us, one and the state in parts 790.)
 template <typename T, int KEYS, bool MAPS>
 struct ForwardPlan {
   template <int P, int BUFFERS, bool TILE, bool PARTS>
@@ -152,7 +153,8 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
   } else {
     Fetched<T, KEYS, FRAGS, WHOLE> next;
     Raw8<T> own[KEYS / 32];       // queries, with a tile
-    // without a tile (65536 steps of 8 heads of 128 x 128 bf16 that way 329 us instead of 262, packed FP16 ones 461 and 385)
+    // without a tile (outputs of 65536 steps of 8 heads of 128 x 128 bf16 that way 329 us instead of 262, packed FP16 ones
+    // 461 and 385, before third parts)
     QueryRows<T, KEYS, WHOLE> q;
     Cut<kFull> p[kFrags];
     constexpr int HOLD = QueryRows<T, KEYS, WHOLE>::HOLD;
@@ -179,8 +181,8 @@ __global__ __launch_bounds__(kChainThreads) void delta_chain_kernel(fftmv_delta_
       if constexpr (TILE && USE != kMaps) put_rows<T, KEYS, WHOLE>(own, thread, lds.q, keys, steps(first));
     };
     auto fetch_triangle = [&](int first) __attribute__((always_inline)) {
-      // from LDS as far as P is there. Each wave for itself from memory, four times the loads, made one sequence of
-      // 65536 steps (8 heads of 128 x 128 bf16) 276 us instead of 262; FP32 elements leave no room
+      // from LDS as far as P is there. Each wave for itself from memory, four times the loads, made the outputs of 65536
+      // steps (8 heads of 128 x 128 bf16) 276 us instead of 262, before third parts; FP32 elements leave no room
       const u32x4 *far = w.triangles + at(first) * Tri::kAll * kWave;
 #pragma unroll
       for (int a = 0; a < kFull; ++a)

@@ -10,9 +10,9 @@
 // cosines are the same for all heads of a row: a workgroup computes them once
 // for its rows, in LDS. Angles are reduced to a turn in FP64: half a million
 // positions along, FP32 would leave two digits of them.
-// 16384 rows of 40 heads of 128 bf16: 55 us, 6.1 TB/s (out of memory 71, a copy's
+// 16384 rows of 40 heads of 128 bf16: 58 us, 5.8 TB/s (out of memory 73, a copy's
 // rate); with results through the caches 90. Gradients of as many rows of 32
-// heads: 72 us. 9995 rows of 10 heads of 75 FP32 take 25 us either way, for 12 and
+// heads: 78 us. 9995 rows of 10 heads of 75 FP32 take 29 and 24 us, for 12 and
 // 19 of bytes: rows that are not aligned, a third of the lanes idle, and the
 // card filled once.
 #pragma once

@@ -182,7 +182,8 @@ def delta_rule(q, k, v, gate, beta, h0=None, *, decay="sigmoid", rate="sigmoid",
         y_t = scale S_t^T q_t
 
     ``decay``: a = sigmoid(gate) ("sigmoid") or exp(gate) ("exp"; minus
-    infinity clears the state); ``rate``: b = sigmoid(beta) ("sigmoid") or
+    infinity clears the state, and decays are meant to be at most one: results
+    are not finite where the gates of 64 steps add up to more than 88); ``rate``: b = sigmoid(beta) ("sigmoid") or
     beta ("value"); ``scale``: keys ** -0.5 when None. q, k: [batch, steps,
     key heads, keys] (or one sequence [steps, key heads, keys]), v: [batch,
     steps, heads, values], gate, beta: [batch, steps, heads], with contiguous

@@ -497,10 +497,11 @@ typedef struct fftmv_heads_s {
  *
  * The state is asked for what it holds under k_t and corrected towards v_t.
  * a = 1 / (1 + exp(-gate)) or exp(gate) (FFTMV_DECAY_SIGMOID, _EXP; a gate of
- * minus infinity clears the state), b = 1 / (1 + exp(-beta)) or beta
- * (FFTMV_RATE_*). Head n takes the queries and keys of head n / (heads /
- * key_heads); key_heads divides heads. Keys are meant to have norms near or
- * below one (fftmv_qk_norm_forward).
+ * minus infinity clears the state; decays are meant to be at most one: where the
+ * gates of a run of steps add up to more than 88, its results are not finite),
+ * b = 1 / (1 + exp(-beta)) or beta (FFTMV_RATE_*). Head n takes the queries and
+ * keys of head n / (heads / key_heads); key_heads divides heads. Keys are meant
+ * to have norms near or below one (fftmv_qk_norm_forward).
  *
  * q, k: [keys] elements a head; v, y: [values]; gate, beta: one (their `head`
  * is the stride between heads). Batch, padded and packed forms, lengths and
